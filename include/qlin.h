@@ -102,6 +102,54 @@ typedef enum {
   QLIN_MX_FP4_E2M1 = 1   /* MXFP4: E2M1 elements, two per byte (element 2i in the low nibble) */
 } qlin_mx_fmt;
 
+/* Codes of a quantized key / value cache (qlin_kv_cache). */
+typedef enum {
+  QLIN_KV_INT8 = 0,  /* int8 in [-127, 127], float32 scale */
+  QLIN_KV_E4M3 = 1,  /* E4M3-FN, float32 scale */
+  QLIN_KV_U4 = 2     /* unsigned 4-bit, two per byte (element 2i in the low nibble), fp16 scale and fp16 zero-point */
+} qlin_kv_fmt;
+
+/* A strided [T][heads][D] array of 16-bit elements: element (t, h, i) lies at
+   data + 2 (t token_stride + h head_stride + i) bytes.  Strides are in
+   elements and multiples of 8; data is 16-byte aligned. */
+typedef struct {
+  void* data;
+  int64_t heads;
+  int64_t token_stride;
+  int64_t head_stride;
+} qlin_heads;
+
+/* The position rotation of qlin_qk_norm_rope, with the optional head norms. */
+typedef struct {
+  const int64_t* positions;  /* [T] */
+  const double* inv_freq;    /* [rot / 2]: radians per position */
+  int64_t rot;               /* channels that are rotated (0 = none), a multiple of 16, <= D */
+  int interleaved;           /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1) */
+  const void* q_gamma;       /* [D] of the array's dtype, or NULL: no norm of q */
+  const void* k_gamma;       /* [D], or NULL: no norm of k */
+  float eps;
+} qlin_rope;
+
+/* A paged, quantized key / value cache (all pointers device pointers).
+   Place s = page * page_size + offset holds one token; its key of head h is
+   the head_dim codes at k + page * page_stride + (h * page_size + offset) *
+   row bytes (head_dim, or head_dim / 2 for U4), its scale the 4 bytes at
+   k_scale + page * scale_page_stride + 4 (h * page_size + offset): a float32,
+   or for U4 an fp16 scale and then an fp16 zero-point.  Values likewise. */
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  int64_t pages;
+  int64_t heads;
+  int64_t page_size;          /* 16, 32, 64, 128 or 256 tokens */
+  int64_t head_dim;           /* 64, 128 or 256 */
+  int64_t page_stride;        /* bytes, a multiple of 16 */
+  int64_t scale_page_stride;  /* bytes, a multiple of 16 */
+  int fmt;                    /* qlin_kv_fmt */
+} qlin_kv_cache;
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* qlin_status_string(qlin_status status);
 
@@ -726,6 +774,93 @@ qlin_status qlin_hadamard(const void* x, qlin_dtype dtype, int64_t rows, int64_t
 qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t rows, int64_t K, const void* gamma,
                                      float eps, const int32_t* perm, int64_t S, qlin_nvfp4_mode mode, const float* g,
                                      uint8_t* q, uint8_t* sf, qlin_sf_layout sf_layout, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Between a decoder block's q/k/v linear and its o linear: head norms with
+ * the position rotation, the quantized cache, and attention over it
+ *
+ * Heads are of D = 64, 128 or 256 elements of F16 or BF16.  Every entry point
+ * here only reads lengths, page numbers and places on the device, so all of
+ * them can be captured into a graph and replayed while those change.  An
+ * index on the device that is out of range (a place, a page number, a
+ * sequence's bounds) is not used: the kernel skips it, records an error in
+ * the device error word (qlin_get_device_error) and goes on.
+ *
+ * qlin_qk_norm_rope: for every token t and head of q and of k
+ *   y = x / sqrt(mean(x^2) + eps) * gamma      (y = x when gamma is NULL)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)   with the angle
+ *   positions[t] * inv_freq[i] for pair i < rot / 2 (channels from rot on
+ *   keep y), in float32 (the angle modulo a full turn exactly, in 64-bit
+ *   fixed point), rounded once to dtype.  k (and k_out) may be NULL.  An
+ *   output may be its input (same data and strides); other overlaps are not
+ *   allowed.
+ *
+ * qlin_qk_norm_rope_cache: the same pass, with k and v quantized into the
+ * cache at slots[t] (page * page_size + offset; a negative place skips the
+ * token's k and v): k from its rotated float32 values, v as it comes.  Per
+ * token and head, one float32 operation at a time, ties to even:
+ *   INT8  s = max(max|x| / 127, 2^-64), n = rint(x / s)
+ *   E4M3  s = max(max|x| / 448, 2^-64), n = e4m3(x / s), saturating
+ *         (a row of zeros: s = 1)
+ *   U4    lo = min(x, 0), hi = max(x, 0) over the row,
+ *         s = fp16(min(max(hi - lo, 1e-5) / 15, 65504)),
+ *         z = clamp(rint(-lo / s), 0, 15), n = clamp(rint(x / s) + z, 0, 15)
+ * A row that holds a NaN or an infinity gets a NaN scale and zero codes (it
+ * reads back as NaN); the codes themselves never are NaN.  Two tokens of one
+ * call must not have the same place.  q_out and k_out may be NULL where the
+ * rotated rows are not wanted (q NULL as well then).
+ *
+ * qlin_kv_cache_write: the quantization alone, of k and v as they come.
+ *
+ * qlin_kv_cache_read: the tokens starts[b] .. of sequence b, as many as
+ * indptr[b + 1] - indptr[b], to rows indptr[b] .. of k_out and v_out:
+ * s n (U4: s (n - z)) rounded once to dtype.  Token j of sequence b lies on
+ * page block_table[b][j / page_size].
+ *   block_table int32 [B][max_pages]; starts int32 [B]; indptr int32 [B + 1],
+ *   from 0 to `rows` without going down
+ *
+ * qlin_tree_attention: sequence b has ctx_lens[b] tokens in the cache, and
+ * after them, at places ctx_lens[b] + i, its nodes i (the new tokens: one, a
+ * chain, or a tree of drafts), whose queries are the rows q_indptr[b] + i of
+ * q, i < q_indptr[b + 1] - q_indptr[b] <= max_nodes.  Node i sees every
+ * cached token, and node j when bit j % 64 of mask[q_indptr[b] + i][j / 64]
+ * is set (mask NULL: when j <= i).  Head h of q reads head h / (Hq / Hk) of
+ * the cache.
+ *   out = sum_j p_ij v_j, p = softmax over what node i sees of
+ *   scale (q_i . k_j); lse = ln sum_j exp(scale (q_i . k_j))
+ * A node that sees nothing gets out = 0 and lse = -infinity.  What a node
+ * does not see does not reach its output, whatever its scales hold.  Codes
+ * enter the products exactly; sums are in float32, and the probabilities are
+ * rounded to fp16 before they meet the codes of v.  The result depends on the
+ * sequences' lengths and the GPU's number of SMs, not on timing.
+ *   q, out      [Tq][Hq][D] of dtype; Hq a multiple of the cache's heads
+ *   mask        int64 [Tq][mask_words], mask_words = ceil(max_nodes / 64), or NULL
+ *   lse         out, float32 [Tq][Hq], or NULL
+ *   max_nodes   1 .. 256 (mask NULL or not)
+ *   workspace   qlin_tree_attention_workspace_bytes(...) bytes, 256-byte
+ *               aligned, contents arbitrary; one call at a time may use it
+ * ---------------------------------------------------------------------- */
+qlin_status qlin_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* q_out,
+                              const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D, const qlin_rope* rope,
+                              cudaStream_t stream);
+qlin_status qlin_qk_norm_rope_cache(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v,
+                                    const qlin_heads* q_out, const qlin_heads* k_out, qlin_dtype dtype, int64_t T,
+                                    const qlin_rope* rope, const int64_t* slots, const qlin_kv_cache* cache,
+                                    cudaStream_t stream);
+qlin_status qlin_kv_cache_write(const qlin_heads* k, const qlin_heads* v, qlin_dtype dtype, int64_t T,
+                                const int64_t* slots, const qlin_kv_cache* cache, cudaStream_t stream);
+qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                               const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows,
+                               const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype,
+                               cudaStream_t stream);
+/* -1 when an argument is out of range.  Hq query heads over `cache`, at most
+   max_nodes nodes a sequence and B sequences. */
+int64_t qlin_tree_attention_workspace_bytes(const qlin_kv_cache* cache, int64_t Hq, int64_t max_nodes, int64_t B);
+qlin_status qlin_tree_attention(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
+                                const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B, const int64_t* mask,
+                                int64_t mask_words, int64_t max_nodes, float scale, float* lse, void* workspace,
+                                int64_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

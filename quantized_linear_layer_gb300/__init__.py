@@ -31,6 +31,10 @@ __all__ = [
     "qlin_rmsnorm_quant_nvfp4", "QLIN_MX_FP8_E4M3", "QLIN_MX_FP4_E2M1", "qlin_mx_sf_bytes", "qlin_quant_mx",
     "qlin_mx_gemm", "QLIN_HADAMARD_SYLVESTER", "QLIN_HADAMARD_REGULAR", "qlin_hadamard",
     "qlin_w4a16_act_order_prepare", "qlin_w4a16_gemm_act_order",
+    "QLIN_KV_INT8", "QLIN_KV_E4M3", "QLIN_KV_U4", "qlin_kv_cache", "QlinCall",
+    "qlin_qk_norm_rope", "qlin_qk_norm_rope_prepare", "qlin_qk_norm_rope_cache", "qlin_qk_norm_rope_cache_prepare",
+    "qlin_kv_cache_write", "qlin_kv_cache_write_prepare", "qlin_kv_cache_read", "qlin_kv_cache_read_prepare",
+    "qlin_tree_attention_workspace_bytes", "qlin_tree_attention", "qlin_tree_attention_prepare",
 ]
 
 QLIN_F16, QLIN_BF16, QLIN_F32, QLIN_I32 = 0, 1, 2, 3
@@ -39,6 +43,7 @@ QLIN_SF_ROWS, QLIN_SF_MMA = 0, 1
 QLIN_QFMT_INT8, QLIN_QFMT_FP8_E4M3 = 0, 1
 QLIN_MX_FP8_E4M3, QLIN_MX_FP4_E2M1 = 0, 1
 QLIN_HADAMARD_SYLVESTER, QLIN_HADAMARD_REGULAR = 0, 1
+QLIN_KV_INT8, QLIN_KV_E4M3, QLIN_KV_U4 = 0, 1, 2
 
 _STATUS = {0: "QLIN_OK", 1: "QLIN_ERR_INVALID_ARG", 2: "QLIN_ERR_ALIGNMENT", 3: "QLIN_ERR_UNSUPPORTED",
            4: "QLIN_ERR_CUDA", 5: "QLIN_ERR_TIMEOUT"}
@@ -93,6 +98,13 @@ _SIGS = {
     "qlin_rmsnorm_quant": ([_P, _I32, _I64, _I64, _P, ctypes.c_float, _I32, _P, _P, _P], _I32),
     "qlin_rmsnorm_quant_nvfp4": ([_P, _I32, _I64, _I64, _P, ctypes.c_float, _P, _I64, _I32, _P, _P, _P, _I32, _P],
                                  _I32),
+    "qlin_qk_norm_rope": ([_P, _P, _P, _P, _I32, _I64, _I64, _P, _P], _I32),
+    "qlin_qk_norm_rope_cache": ([_P, _P, _P, _P, _P, _I32, _I64, _P, _P, _P, _P], _I32),
+    "qlin_kv_cache_write": ([_P, _P, _I32, _I64, _P, _P, _P], _I32),
+    "qlin_kv_cache_read": ([_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I32, _P], _I32),
+    "qlin_tree_attention_workspace_bytes": ([_P, _I64, _I64, _I64], _I64),
+    "qlin_tree_attention": ([_P, _P, _I32, _I64, _P, _P, _I64, _P, _P, _I64, _P, _I64, _I64, ctypes.c_float, _P, _P,
+                             _I64, _P], _I32),
 }
 
 _lib = None
@@ -648,3 +660,266 @@ def qlin_hadamard(x, n, y=None, kind=QLIN_HADAMARD_SYLVESTER, signs=None, stream
     _check("qlin_hadamard", lib().qlin_hadamard(_ptr(x), _dtype_code(x), rows, k, kind, n, _ptr(signs), _ptr(y),
                                                _stream(stream)))
     return y
+
+
+# ---- head norms, rotation, quantized cache, tree attention -----------------
+
+
+class _Heads(ctypes.Structure):
+    """The C struct qlin_heads: a strided [T][heads][D] array."""
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):
+    """The C struct qlin_rope."""
+    _fields_ = [("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("rot", ctypes.c_int64),
+                ("interleaved", ctypes.c_int), ("q_gamma", ctypes.c_void_p), ("k_gamma", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class _KvCache(ctypes.Structure):
+    """The C struct qlin_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("scale_page_stride", ctypes.c_int64), ("fmt", ctypes.c_int)]
+
+
+class QlinCall:
+    """One call of a C entry point with its arguments checked and marshalled
+    once: run() makes the call on the current (or the given) stream.  It holds
+    the tensors' device pointers, so it is valid while they are, and keeps the
+    tensors referenced; lengths, page numbers and places are read on the
+    device at every run."""
+
+    def __init__(self, name, args, keep):
+        self._name, self._fn, self._args, self._keep = name, getattr(lib(), name), args, keep
+
+    def run(self, stream=None):
+        status = self._fn(*self._args, _stream(stream))
+        if status != 0:
+            _check(self._name, status)
+
+
+class qlin_kv_cache:
+    """A paged, quantized key / value cache over caller-allocated tensors (the C struct of the same name).
+
+    k, v: [pages][heads][page_size][head_dim] int8 (INT8), float8_e4m3fn or uint8 (E4M3), or
+    [..][head_dim / 2] uint8 (U4); k_scale, v_scale: float32 [pages][heads][page_size], or for U4
+    float16 [pages][heads][page_size][2] (scale, zero-point).  Each page is contiguous; the pages of k and
+    v may be any (equal) distance apart, and so may those of the scales."""
+
+    def __init__(self, k, v, k_scale, v_scale, fmt):
+        torch = _torch()
+        if fmt not in (QLIN_KV_INT8, QLIN_KV_E4M3, QLIN_KV_U4):
+            raise ValueError("unknown cache format %r" % (fmt,))
+        kinds = {QLIN_KV_INT8: (torch.int8,), QLIN_KV_E4M3: (torch.float8_e4m3fn, torch.uint8),
+                 QLIN_KV_U4: (torch.uint8,)}[fmt]
+        u4 = fmt == QLIN_KV_U4
+        for name, t in (("k", k), ("v", v)):
+            _need(t, *kinds, contiguous=False, name=name)
+            if t.dim() != 4 or t.shape != k.shape:
+                raise ValueError("%s must be [pages][heads][page_size][row bytes], the same for k and v" % name)
+            self._check_page(name, t)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _need(t, torch.float16 if u4 else torch.float32, contiguous=False, name=name)
+            if tuple(t.shape) != tuple(k.shape[:3]) + ((2,) if u4 else ()):
+                raise ValueError("%s has shape %s, one entry per token and head of k expected" % (name, tuple(t.shape)))
+            self._check_page(name, t)
+        if k.stride(0) != v.stride(0) or k_scale.stride(0) != v_scale.stride(0):
+            raise ValueError("k and v (and their scales) must have equal page strides")
+        pages, heads, page_size, width = k.shape
+        self.fmt, self.heads, self.page_size, self.head_dim = fmt, heads, page_size, 2 * width if u4 else width
+        self.device = k.device
+        self._keep = (k, v, k_scale, v_scale)
+        many = pages > 1
+        self._c = _KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, page_size,
+                           self.head_dim, k.stride(0) if many else heads * page_size * width,
+                           k_scale.stride(0) * k_scale.element_size() if many else heads * page_size * 4, fmt)
+
+    @staticmethod
+    def _check_page(name, t):
+        want = 1
+        for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+            if size != 1 and stride != want:
+                raise ValueError("each page of %s must be contiguous" % name)
+            want *= size
+
+
+def _heads(t, dtype, d, name, tokens=None, device=None):
+    """The C struct of a [T][heads][D] tensor whose last dimension is contiguous."""
+    _need(t, dtype, contiguous=False, name=name)
+    if t.dim() != 3 or t.shape[2] != d:
+        raise ValueError("%s has shape %s, [T][heads][%d] expected" % (name, tuple(t.shape), d))
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+    if tokens is not None and t.shape[0] != tokens:
+        raise ValueError("%s has %d tokens, %d expected" % (name, t.shape[0], tokens))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    # the stride of a dimension of one element says nothing: any valid one will do
+    return _Heads(t.data_ptr(), t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1] * d,
+                  t.stride(1) if t.shape[1] > 1 else d)
+
+
+def _vector(t, dtype, name, numel=None, device=None):
+    _need(t, dtype, name=name)
+    if numel is not None and t.numel() != numel:
+        raise ValueError("%s has %d elements, %d expected" % (name, t.numel(), numel))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    return _ptr(t)
+
+
+def _half_dtype(t, name):
+    torch = _torch()
+    _need(t, torch.float16, torch.bfloat16, contiguous=False, name=name)
+    return t.dtype, _dtype_code(t)
+
+
+def _rope(positions, inv_freq, q_gamma, k_gamma, eps, interleaved, dtype, d, tokens, device):
+    torch = _torch()
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if rot:
+        _vector(positions, torch.int64, "positions", tokens, device)
+        _vector(inv_freq, torch.float64, "inv_freq", device=device)
+    for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+        if g is not None:
+            _vector(g, dtype, name, d, device)
+    return _Rope(positions.data_ptr() if rot else None, inv_freq.data_ptr() if rot else None, rot, int(bool(interleaved)),
+                 None if q_gamma is None else q_gamma.data_ptr(), None if k_gamma is None else k_gamma.data_ptr(), eps)
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.cast(ctypes.pointer(struct), ctypes.c_void_p)
+
+
+def qlin_qk_norm_rope_prepare(q, k, q_out, k_out, positions, inv_freq, q_gamma=None, k_gamma=None, eps=1e-6,
+                              interleaved=False):
+    """qlin_qk_norm_rope's arguments checked and marshalled once (QlinCall.run)."""
+    dtype, code = _half_dtype(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [T][heads][D]")
+    t, _, d = q.shape
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    parts = [_heads(x, dtype, d, n, t, q.device) if x is not None else None
+             for n, x in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))]
+    rope = _rope(positions, inv_freq, q_gamma, k_gamma, eps, interleaved, dtype, d, t, q.device)
+    return QlinCall("qlin_qk_norm_rope", (*map(_ref, parts), code, t, d, _ref(rope)),
+                    (parts, rope, q, k, q_out, k_out, positions, inv_freq, q_gamma, k_gamma))
+
+
+def qlin_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_gamma=None, k_gamma=None, eps=1e-6,
+                      interleaved=False, stream=None):
+    """RMSNorm of every head of q and k (where its gamma is given) and the position rotation, in one pass.
+
+    q, q_out [T][Hq][D], k, k_out [T][Hk][D] (None to leave k out) fp16 / bf16 with any token and head strides;
+    positions int64 [T]; inv_freq float64 [rot / 2] radians per position (None: no rotation); gammas [D]."""
+    qlin_qk_norm_rope_prepare(q, k, q_out, k_out, positions, inv_freq, q_gamma, k_gamma, eps, interleaved).run(stream)
+
+
+def qlin_qk_norm_rope_cache_prepare(q, k, v, q_out, positions, inv_freq, slots, cache, q_gamma=None, k_gamma=None,
+                                    eps=1e-6, interleaved=False, k_out=None):
+    """qlin_qk_norm_rope_cache's arguments checked and marshalled once (QlinCall.run)."""
+    torch = _torch()
+    dtype, code = _half_dtype(k, "k")
+    t, d = k.shape[0], cache.head_dim
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    parts = [_heads(x, dtype, d, n, t, cache.device) if x is not None else None
+             for n, x in (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out))]
+    rope = _rope(positions, inv_freq, q_gamma, k_gamma, eps, interleaved, dtype, d, t, cache.device)
+    at = _vector(slots, torch.int64, "slots", t, cache.device)
+    return QlinCall("qlin_qk_norm_rope_cache", (*map(_ref, parts), code, t, _ref(rope), at, _ref(cache._c)),
+                    (parts, rope, q, k, v, q_out, k_out, positions, inv_freq, q_gamma, k_gamma, slots, cache))
+
+
+def qlin_qk_norm_rope_cache(q, k, v, q_out, positions, inv_freq, slots, cache, q_gamma=None, k_gamma=None, eps=1e-6,
+                            interleaved=False, k_out=None, stream=None):
+    """qlin_qk_norm_rope with k and v quantized into `cache` at slots int64 [T] in the same pass (negative: the
+    token's k and v are not stored).  q and q_out may be None; k_out [T][Hk][D] gets the rotated keys as well."""
+    qlin_qk_norm_rope_cache_prepare(q, k, v, q_out, positions, inv_freq, slots, cache, q_gamma, k_gamma, eps,
+                                    interleaved, k_out).run(stream)
+
+
+def qlin_kv_cache_write_prepare(k, v, slots, cache):
+    """qlin_kv_cache_write's arguments checked and marshalled once (QlinCall.run)."""
+    torch = _torch()
+    dtype, code = _half_dtype(k, "k")
+    t = k.shape[0]
+    parts = [_heads(x, dtype, cache.head_dim, n, t, cache.device) for n, x in (("k", k), ("v", v))]
+    at = _vector(slots, torch.int64, "slots", t, cache.device)
+    return QlinCall("qlin_kv_cache_write", (*map(_ref, parts), code, t, at, _ref(cache._c)), (parts, k, v, slots, cache))
+
+
+def qlin_kv_cache_write(k, v, slots, cache, stream=None):
+    """k, v [T][heads][D] fp16 / bf16 quantized into `cache` at slots int64 [T] (negative: skipped)."""
+    qlin_kv_cache_write_prepare(k, v, slots, cache).run(stream)
+
+
+def qlin_kv_cache_read_prepare(cache, block_table, starts, indptr, k_out, v_out):
+    """qlin_kv_cache_read's arguments checked and marshalled once (QlinCall.run)."""
+    torch = _torch()
+    dtype, code = _half_dtype(k_out, "k_out")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B][max_pages]")
+    b, max_pages = block_table.shape
+    rows = k_out.shape[0]
+    parts = [_heads(x, dtype, cache.head_dim, n, rows, cache.device) for n, x in (("k_out", k_out), ("v_out", v_out))]
+    tp = _vector(block_table, torch.int32, "block_table", device=cache.device)
+    sp = _vector(starts, torch.int32, "starts", b, cache.device)
+    ip = _vector(indptr, torch.int32, "indptr", b + 1, cache.device)
+    return QlinCall("qlin_kv_cache_read", (_ref(cache._c), tp, max_pages, sp, ip, b, rows, *map(_ref, parts), code),
+                    (parts, cache, block_table, starts, indptr, k_out, v_out))
+
+
+def qlin_kv_cache_read(cache, block_table, starts, indptr, k_out, v_out, stream=None):
+    """Tokens starts[b] .. of sequence b (pages block_table[b]) dequantized to rows indptr[b] .. indptr[b + 1] of
+    k_out, v_out [rows][heads][D] fp16 / bf16.  block_table int32 [B][max_pages], starts int32 [B], indptr int32 [B + 1]."""
+    qlin_kv_cache_read_prepare(cache, block_table, starts, indptr, k_out, v_out).run(stream)
+
+
+def qlin_tree_attention_workspace_bytes(cache, heads, max_nodes, seqs):
+    """Workspace of qlin_tree_attention for `heads` query heads, at most max_nodes nodes per sequence, `seqs` sequences."""
+    n = lib().qlin_tree_attention_workspace_bytes(_ref(cache._c), heads, max_nodes, seqs)
+    if n < 0:
+        raise ValueError("no tree attention for %d heads over %d, %d nodes, %d sequences" % (heads, cache.heads, max_nodes, seqs))
+    return n
+
+
+def qlin_tree_attention_prepare(q, cache, block_table, q_indptr, ctx_lens, mask, out, workspace, max_nodes, scale=None,
+                                lse=None):
+    """qlin_tree_attention's arguments checked and marshalled once (QlinCall.run)."""
+    torch = _torch()
+    dtype, code = _half_dtype(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [Tq][heads][D]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B][max_pages]")
+    tq, hq, d = q.shape
+    b, max_pages = block_table.shape
+    parts = [_heads(x, dtype, cache.head_dim, n, tq, cache.device) for n, x in (("q", q), ("out", out))]
+    tp = _vector(block_table, torch.int32, "block_table", device=cache.device)
+    ip = _vector(q_indptr, torch.int32, "q_indptr", b + 1, cache.device)
+    cp = _vector(ctx_lens, torch.int32, "ctx_lens", b, cache.device)
+    words = (max_nodes + 63) // 64
+    mp = _vector(mask, torch.int64, "mask", tq * words, cache.device) if mask is not None else None
+    lp = _vector(lse, torch.float32, "lse", tq * hq, cache.device) if lse is not None else None
+    wp = _vector(workspace, torch.uint8, "workspace", device=cache.device)
+    return QlinCall("qlin_tree_attention",
+                    (*map(_ref, parts), code, tq, _ref(cache._c), tp, max_pages, ip, cp, b, mp, words if mask is not None else 0,
+                     max_nodes, d ** -0.5 if scale is None else scale, lp, wp, workspace.numel()),
+                    (parts, q, cache, block_table, q_indptr, ctx_lens, mask, out, workspace, lse))
+
+
+def qlin_tree_attention(q, cache, block_table, q_indptr, ctx_lens, mask, out, workspace, max_nodes, scale=None, lse=None,
+                        stream=None):
+    """Attention of every sequence's new tokens over its cached ones and, as `mask` says, over each other.
+
+    q, out [Tq][Hq][D]; sequence b has ctx_lens[b] cached tokens and the nodes q_indptr[b] .. q_indptr[b + 1], stored
+    in the cache right behind them; bit j of mask[i] (int64 [Tq][ceil(max_nodes / 64)]): node j is seen by row i (None:
+    a chain); scale defaults to D ** -0.5; lse float32 [Tq][Hq] (optional) gets ln sum exp of the scores."""
+    qlin_tree_attention_prepare(q, cache, block_table, q_indptr, ctx_lens, mask, out, workspace, max_nodes, scale,
+                                lse).run(stream)

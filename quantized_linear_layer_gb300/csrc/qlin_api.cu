@@ -781,3 +781,214 @@ qlin_status qlin_rmsnorm_quant(const void* x, qlin_dtype x_dtype, int64_t rows, 
 }
 
 }  // extern "C"
+
+// ---- head norms, rotation, quantized cache, tree attention ------------------
+
+namespace {
+
+bool is_half_dtype(qlin_dtype d) { return d == QLIN_F16 || d == QLIN_BF16; }
+
+// A strided [T][heads][D] array.
+qlin_status check_heads(const char* what, const qlin_heads* a, int64_t T, int64_t D) {
+  QLIN_REQUIRE(a != nullptr, QLIN_ERR_INVALID_ARG, "%s: null descriptor", what);
+  QLIN_REQUIRE(a->heads >= 1 && a->heads <= 65535, QLIN_ERR_INVALID_ARG, "%s: heads=%lld outside [1, 65535]", what,
+               (long long)a->heads);
+  QLIN_REQUIRE(a->data != nullptr || T == 0, QLIN_ERR_INVALID_ARG, "%s: null pointer", what);
+  QLIN_REQUIRE(aligned16(a->data), QLIN_ERR_ALIGNMENT, "%s: data must be 16-byte aligned", what);
+  QLIN_REQUIRE(a->token_stride % 8 == 0 && a->head_stride % 8 == 0, QLIN_ERR_ALIGNMENT,
+               "%s: strides must be multiples of 8 elements", what);
+  QLIN_REQUIRE(a->heads == 1 || a->head_stride >= D, QLIN_ERR_INVALID_ARG, "%s: head_stride=%lld below the head size %lld",
+               what, (long long)a->head_stride, (long long)D);
+  QLIN_REQUIRE(T <= 1 || a->token_stride >= D, QLIN_ERR_INVALID_ARG, "%s: token_stride=%lld below the head size %lld", what,
+               (long long)a->token_stride, (long long)D);
+  QLIN_REQUIRE(a->token_stride <= (int64_t(1) << 40) && a->head_stride <= (int64_t(1) << 40), QLIN_ERR_INVALID_ARG,
+               "%s: stride too large", what);
+  return QLIN_OK;
+}
+
+bool is_head_dim(int64_t d) { return d == 64 || d == 128 || d == 256; }
+
+qlin_status check_cache(const qlin_kv_cache* c) {
+  QLIN_REQUIRE(c != nullptr, QLIN_ERR_INVALID_ARG, "null cache");
+  QLIN_REQUIRE(c->fmt >= QLIN_KV_INT8 && c->fmt <= QLIN_KV_U4, QLIN_ERR_INVALID_ARG, "cache: unknown format %d", c->fmt);
+  QLIN_REQUIRE(is_head_dim(c->head_dim), QLIN_ERR_UNSUPPORTED, "cache: head_dim=%lld (64, 128 and 256 are built)",
+               (long long)c->head_dim);
+  QLIN_REQUIRE(c->page_size == 16 || c->page_size == 32 || c->page_size == 64 || c->page_size == 128 ||
+                   c->page_size == 256,
+               QLIN_ERR_UNSUPPORTED, "cache: page_size=%lld (16, 32, 64, 128 and 256 are built)", (long long)c->page_size);
+  QLIN_REQUIRE(c->heads >= 1 && c->heads <= 65535, QLIN_ERR_INVALID_ARG, "cache: heads=%lld outside [1, 65535]",
+               (long long)c->heads);
+  QLIN_REQUIRE(c->pages >= 1 && c->pages <= kMaxDim, QLIN_ERR_INVALID_ARG, "cache: pages=%lld out of range",
+               (long long)c->pages);
+  QLIN_REQUIRE(c->k && c->v && c->k_scale && c->v_scale, QLIN_ERR_INVALID_ARG, "cache: null pointer");
+  QLIN_REQUIRE(aligned16(c->k) && aligned16(c->v) && aligned16(c->k_scale) && aligned16(c->v_scale), QLIN_ERR_ALIGNMENT,
+               "cache: k, v and their scales must be 16-byte aligned");
+  const int64_t rows = c->heads * c->page_size;
+  const int64_t row_bytes = c->fmt == QLIN_KV_U4 ? c->head_dim / 2 : c->head_dim;
+  QLIN_REQUIRE(c->page_stride % 16 == 0 && c->scale_page_stride % 16 == 0, QLIN_ERR_ALIGNMENT,
+               "cache: page strides must be multiples of 16 bytes");
+  QLIN_REQUIRE(c->page_stride >= rows * row_bytes && c->scale_page_stride >= rows * 4 &&
+                   c->page_stride <= (int64_t(1) << 38) && c->scale_page_stride <= (int64_t(1) << 38),
+               QLIN_ERR_INVALID_ARG, "cache: page stride out of range");
+  return QLIN_OK;
+}
+
+qlin_status check_rope(const qlin_rope* r, int64_t D, int64_t T) {
+  QLIN_REQUIRE(r != nullptr, QLIN_ERR_INVALID_ARG, "null rope");
+  QLIN_REQUIRE(r->rot >= 0 && r->rot <= D && r->rot % 16 == 0, QLIN_ERR_INVALID_ARG,
+               "rot=%lld must be a multiple of 16 and at most the head size", (long long)r->rot);
+  QLIN_REQUIRE(r->interleaved == 0 || r->interleaved == 1, QLIN_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  QLIN_REQUIRE(r->rot == 0 || T == 0 || (r->positions && r->inv_freq), QLIN_ERR_INVALID_ARG, "null positions or inv_freq");
+  QLIN_REQUIRE((reinterpret_cast<uintptr_t>(r->positions) & 7u) == 0 && (reinterpret_cast<uintptr_t>(r->inv_freq) & 7u) == 0,
+               QLIN_ERR_ALIGNMENT, "positions and inv_freq must be 8-byte aligned");
+  QLIN_REQUIRE(aligned16(r->q_gamma) && aligned16(r->k_gamma), QLIN_ERR_ALIGNMENT, "gamma must be 16-byte aligned");
+  QLIN_REQUIRE(r->eps >= 0.0f && r->eps <= 3.0e38f, QLIN_ERR_INVALID_ARG, "eps must be finite and not negative");
+  return QLIN_OK;
+}
+
+qlin_status check_same_heads(const char* what, const qlin_heads* a, int64_t heads) {
+  QLIN_REQUIRE(a->heads == heads, QLIN_ERR_INVALID_ARG, "%s: %lld heads, %lld expected", what, (long long)a->heads,
+               (long long)heads);
+  return QLIN_OK;
+}
+
+}  // namespace
+
+#define QLIN_CHECK(expr)                   \
+  do {                                     \
+    const qlin_status st_ = (expr);        \
+    if (st_ != QLIN_OK) return st_;        \
+  } while (0)
+
+extern "C" {
+
+qlin_status qlin_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* q_out,
+                              const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D, const qlin_rope* rope,
+                              cudaStream_t stream) {
+  QLIN_REQUIRE(is_half_dtype(dtype), QLIN_ERR_INVALID_ARG, "dtype must be F16 or BF16");
+  QLIN_REQUIRE(T >= 0 && T <= kMaxDim, QLIN_ERR_INVALID_ARG, "T=%lld out of range", (long long)T);
+  QLIN_REQUIRE(is_head_dim(D), QLIN_ERR_UNSUPPORTED, "D=%lld (64, 128 and 256 are built)", (long long)D);
+  QLIN_CHECK(check_rope(rope, D, T));
+  QLIN_CHECK(check_heads("q", q, T, D));
+  QLIN_CHECK(check_heads("q_out", q_out, T, D));
+  QLIN_CHECK(check_same_heads("q_out", q_out, q->heads));
+  QLIN_REQUIRE((k == nullptr) == (k_out == nullptr), QLIN_ERR_INVALID_ARG, "k and k_out go together");
+  if (k != nullptr) {
+    QLIN_CHECK(check_heads("k", k, T, D));
+    QLIN_CHECK(check_heads("k_out", k_out, T, D));
+    QLIN_CHECK(check_same_heads("k_out", k_out, k->heads));
+  }
+  if (T == 0) return ok();
+  QLIN_DEVICE();
+  QLIN_LAUNCH(launch_qk_norm_rope(q, k, nullptr, q_out, k_out, dtype, T, D, rope, nullptr, nullptr, stream),
+              "qk_norm_rope launch");
+}
+
+qlin_status qlin_qk_norm_rope_cache(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v,
+                                    const qlin_heads* q_out, const qlin_heads* k_out, qlin_dtype dtype, int64_t T,
+                                    const qlin_rope* rope, const int64_t* slots, const qlin_kv_cache* cache,
+                                    cudaStream_t stream) {
+  QLIN_REQUIRE(is_half_dtype(dtype), QLIN_ERR_INVALID_ARG, "dtype must be F16 or BF16");
+  QLIN_REQUIRE(T >= 0 && T <= kMaxDim, QLIN_ERR_INVALID_ARG, "T=%lld out of range", (long long)T);
+  QLIN_CHECK(check_cache(cache));
+  const int64_t D = cache->head_dim;
+  QLIN_CHECK(check_rope(rope, D, T));
+  QLIN_REQUIRE((q == nullptr) == (q_out == nullptr), QLIN_ERR_INVALID_ARG, "q and q_out go together");
+  if (q != nullptr) {
+    QLIN_CHECK(check_heads("q", q, T, D));
+    QLIN_CHECK(check_heads("q_out", q_out, T, D));
+    QLIN_CHECK(check_same_heads("q_out", q_out, q->heads));
+  }
+  QLIN_CHECK(check_heads("k", k, T, D));
+  QLIN_CHECK(check_heads("v", v, T, D));
+  QLIN_CHECK(check_same_heads("k", k, cache->heads));
+  QLIN_CHECK(check_same_heads("v", v, cache->heads));
+  if (k_out != nullptr) {
+    QLIN_CHECK(check_heads("k_out", k_out, T, D));
+    QLIN_CHECK(check_same_heads("k_out", k_out, k->heads));
+  }
+  if (T == 0) return ok();
+  QLIN_REQUIRE(slots != nullptr, QLIN_ERR_INVALID_ARG, "null slots");
+  QLIN_REQUIRE((reinterpret_cast<uintptr_t>(slots) & 7u) == 0, QLIN_ERR_ALIGNMENT, "slots must be 8-byte aligned");
+  QLIN_DEVICE();
+  QLIN_LAUNCH(launch_qk_norm_rope(q, k, v, q_out, k_out, dtype, T, D, rope, slots, cache, stream),
+              "qk_norm_rope_cache launch");
+}
+
+qlin_status qlin_kv_cache_write(const qlin_heads* k, const qlin_heads* v, qlin_dtype dtype, int64_t T,
+                                const int64_t* slots, const qlin_kv_cache* cache, cudaStream_t stream) {
+  const qlin_rope plain = {nullptr, nullptr, 0, 0, nullptr, nullptr, 0.0f};
+  return qlin_qk_norm_rope_cache(nullptr, k, v, nullptr, nullptr, dtype, T, &plain, slots, cache, stream);
+}
+
+qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                               const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows,
+                               const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype,
+                               cudaStream_t stream) {
+  QLIN_REQUIRE(is_half_dtype(dtype), QLIN_ERR_INVALID_ARG, "dtype must be F16 or BF16");
+  QLIN_REQUIRE(B >= 0 && B <= kMaxDim && rows >= 0 && rows <= kMaxDim, QLIN_ERR_INVALID_ARG,
+               "bad sizes B=%lld rows=%lld", (long long)B, (long long)rows);
+  QLIN_REQUIRE(max_pages >= 0 && max_pages <= kMaxDim, QLIN_ERR_INVALID_ARG, "max_pages=%lld out of range",
+               (long long)max_pages);
+  QLIN_CHECK(check_cache(cache));
+  QLIN_CHECK(check_heads("k_out", k_out, rows, cache->head_dim));
+  QLIN_CHECK(check_heads("v_out", v_out, rows, cache->head_dim));
+  QLIN_CHECK(check_same_heads("k_out", k_out, cache->heads));
+  QLIN_CHECK(check_same_heads("v_out", v_out, cache->heads));
+  if (rows == 0 || B == 0) return ok();
+  QLIN_REQUIRE(block_table && starts && indptr, QLIN_ERR_INVALID_ARG, "null pointer");
+  QLIN_REQUIRE(((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(starts) |
+                 reinterpret_cast<uintptr_t>(indptr)) & 3u) == 0,
+               QLIN_ERR_ALIGNMENT, "block_table, starts and indptr must be 4-byte aligned");
+  QLIN_DEVICE();
+  QLIN_LAUNCH(launch_kv_cache_read(cache, block_table, max_pages, starts, indptr, B, rows, k_out, v_out, dtype, stream),
+              "kv_cache_read launch");
+}
+
+int64_t qlin_tree_attention_workspace_bytes(const qlin_kv_cache* cache, int64_t Hq, int64_t max_nodes, int64_t B) {
+  if (check_cache(cache) != QLIN_OK) return -1;
+  DeviceInfo* info = nullptr;
+  (void)probe_current_device(&info);  // the number of SMs; without a GPU the default is used
+  if (Hq < 1 || Hq > 65535 || Hq % cache->heads != 0 || max_nodes < 1 || max_nodes > 256 || B < 0 || B > 65535) return -1;
+  return tree_attention_workspace_bytes(*cache, Hq, max_nodes, B);
+}
+
+qlin_status qlin_tree_attention(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
+                                const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B, const int64_t* mask,
+                                int64_t mask_words, int64_t max_nodes, float scale, float* lse, void* workspace,
+                                int64_t workspace_bytes, cudaStream_t stream) {
+  QLIN_REQUIRE(is_half_dtype(dtype), QLIN_ERR_INVALID_ARG, "dtype must be F16 or BF16");
+  QLIN_REQUIRE(Tq >= 0 && Tq <= kMaxDim && B >= 0 && B <= 65535, QLIN_ERR_INVALID_ARG, "bad sizes Tq=%lld B=%lld",
+               (long long)Tq, (long long)B);
+  QLIN_REQUIRE(max_pages >= 0 && max_pages <= kMaxDim, QLIN_ERR_INVALID_ARG, "max_pages=%lld out of range",
+               (long long)max_pages);
+  QLIN_REQUIRE(max_nodes >= 1 && max_nodes <= 256, QLIN_ERR_UNSUPPORTED, "max_nodes=%lld (1 .. 256 are built)",
+               (long long)max_nodes);
+  QLIN_REQUIRE(scale == scale && scale - scale == 0.0f, QLIN_ERR_INVALID_ARG, "scale must be finite");
+  QLIN_CHECK(check_cache(cache));
+  QLIN_CHECK(check_heads("q", q, Tq, cache->head_dim));
+  QLIN_CHECK(check_heads("out", out, Tq, cache->head_dim));
+  QLIN_CHECK(check_same_heads("out", out, q->heads));
+  QLIN_REQUIRE(q->heads % cache->heads == 0, QLIN_ERR_INVALID_ARG, "%lld query heads over %lld cached heads",
+               (long long)q->heads, (long long)cache->heads);
+  QLIN_REQUIRE(mask == nullptr || mask_words == (max_nodes + 63) / 64, QLIN_ERR_INVALID_ARG,
+               "mask_words=%lld, %lld expected", (long long)mask_words, (long long)((max_nodes + 63) / 64));
+  if (Tq == 0 || B == 0) return ok();
+  QLIN_REQUIRE(block_table && q_indptr && ctx_lens && workspace, QLIN_ERR_INVALID_ARG, "null pointer");
+  QLIN_REQUIRE(((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(q_indptr) |
+                 reinterpret_cast<uintptr_t>(ctx_lens) | reinterpret_cast<uintptr_t>(lse)) & 3u) == 0 &&
+                   (reinterpret_cast<uintptr_t>(mask) & 7u) == 0,
+               QLIN_ERR_ALIGNMENT, "int32 and float arrays must be 4-byte aligned, mask 8-byte");
+  QLIN_REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, QLIN_ERR_ALIGNMENT,
+               "workspace must be 256-byte aligned");
+  QLIN_DEVICE();
+  const int64_t need = tree_attention_workspace_bytes(*cache, q->heads, max_nodes, B);
+  QLIN_REQUIRE(workspace_bytes >= need, QLIN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed",
+               (long long)workspace_bytes, (long long)need);
+  const TreeAttentionArgs a = {*q, *out, dtype, Tq, *cache, block_table, max_pages, q_indptr, ctx_lens, B, mask,
+                               mask ? mask_words : 0, max_nodes, scale, lse, workspace};
+  QLIN_LAUNCH(launch_tree_attention(a, stream), "tree_attention launch");
+}
+
+}  // extern "C"

@@ -146,4 +146,34 @@ cudaError_t launch_fp8_gemm(const uint8_t* a, const uint8_t* b, int64_t T, int64
                             const float* scale_b, const void* bias, qlin_dtype bias_dtype, void* out,
                             qlin_dtype out_dtype, cudaStream_t stream);
 
+// Head norms, position rotation and the quantized cache.  `cache` null: the
+// rotation alone (v unused); rope null: the write alone (q, q_out, k_out unused).
+cudaError_t launch_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v, const qlin_heads* q_out,
+                                const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D, const qlin_rope* rope,
+                                const int64_t* slots, const qlin_kv_cache* cache, cudaStream_t stream);
+cudaError_t launch_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                 const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows,
+                                 const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype,
+                                 cudaStream_t stream);
+
+struct TreeAttentionArgs {
+  qlin_heads q, out;
+  qlin_dtype dtype;
+  int64_t Tq;
+  qlin_kv_cache cache;
+  const int32_t* block_table;
+  int64_t max_pages;
+  const int32_t* q_indptr;
+  const int32_t* ctx_lens;
+  int64_t B;
+  const int64_t* mask;
+  int64_t mask_words;
+  int64_t max_nodes;
+  float scale;
+  float* lse;
+  void* workspace;
+};
+int64_t tree_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t Hq, int64_t max_nodes, int64_t B);
+cudaError_t launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t stream);
+
 }  // namespace qlin
