@@ -1,26 +1,88 @@
 // Attention of the new tokens of each sequence (one, a chain or a tree of
-// drafts) over a paged, quantized key / value cache.
+// drafts) over a paged, quantized key / value cache, on the warp-level tensor
+// cores, split over the cached tokens.
 //
-// The plain kernel: a block per query row and head, four warps that take the
-// cached tokens in turn.  Scores, the running maximum, the sum and the output
-// are float32.
+// Mathematics.  With k_j = sk_j n_j and v_j = sv_j u_j (n, u the codes, small
+// integers or E4M3 numbers, exact in fp16):
+//   t_ij = log2(e) scale sk_j (q_i . n_j) + log2(sv_j)
+//   o_i  = sum_j 2^(t_ij - m_i) u_j / sum_j 2^(t_ij - m_i) / sv_j
+// for any reference m_i, so the codes go to the tensor cores as they are and
+// neither product rounds an operand except the probabilities 2^(t - m) (to
+// fp16).  q rows are scaled by a power of two to below 2^15 before they become
+// fp16: exact for fp16, and for bf16 down to 2^-39 of the row's largest.  The
+// reference m_i follows the running maximum of t lazily: it moves when t
+// exceeds it by more than 2, and the exponent carries an offset of 13, so that
+// the probabilities lie below 2^15 and those down to 2^-27 of the reference are
+// normal fp16 numbers.  Smaller ones matter where the large ones meet codes of
+// 0: when 16 x 16 of them hold any, these go through a second product, times
+// 2^24 against codes times 2^-24 (2^15 for E4M3), both exact in fp16, so that
+// every probability keeps 11 bits down to 2^-51 (2^-42) of the largest.
+//
+// Work.  The rows of one key head (node, query head of the group) are cut
+// into tiles of kRows = 16, the tokens into tiles of kTile = 64.  All (sequence,
+// key head, row tile, token tile) units in this order are dealt out evenly to
+// a grid that just fills the GPU: a block takes a run of units, which touches
+// as many segments (sequence, head, row tile) as it happens to.  The division
+// is worked out on the device from the lengths, so ragged batches and one long
+// sequence load the GPU alike, and a captured call stays right when lengths
+// change.  A segment cut by a block's border leaves float32 partial results
+// (o, m, l), which a second kernel joins in the order of the blocks; a
+// sequence's result depends on the lengths, not on timing.
+//
+// A block has four compute warps and one that loads.  The loading warp keeps a
+// ring of stages filled by TMA: 64 tokens' codes of K and V (one box per page
+// that the tile touches, 128-, 64- or 32-byte swizzled rows) and their scales.
+// Each compute warp takes 16 of the stage's tokens for all rows, with its own
+// running maximum, sums and output, so that no barrier lies between warps
+// until the segment ends.  Codes are widened to fp16 in registers, straight
+// into the operand layout of mma.m16n8k16: the order of channels in q . n and
+// of output channels is permuted such that a lane's operands are contiguous
+// bytes of a row, read without bank conflicts through the swizzle.
+//
+// Bound: HBM for one to about eight rows per key head; at 16 rows (8-bit
+// codes) the widening instructions take about as long as the loads.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv_common.cuh"
 #include "qlin_internal.h"
+#include "tc_common.cuh"
+#include "tmap.h"
 
 namespace qlin {
 namespace {
 
+constexpr int kTile = 64;
 constexpr int kWarps = 4;
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kRows = 16;
+constexpr float kOffset = 13.0f;
+constexpr float kSlack = 2.0f;
+constexpr float kHalfNormal = 6.103515625e-5f;  // 2^-14, the smallest normal fp16
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kMaxBlocks = 1024;
+
+// What a block leaves for the joining kernel when a segment begins in it and
+// ends in a later one.
+struct Record {
+  int32_t last;  // the block where the segment ends, or -1: nothing to join
+  int32_t head, row_tile, nodes;
+  int64_t q_row;
+};
 
 struct Params {
+  CUtensorMap k_map, v_map;
   const uint8_t* q;
   uint8_t* out;
   int64_t qt, qh, ot, oh;  // strides in bytes
-  int32_t hq, group;
+  int32_t hq, hk, group, dtype;
   int64_t Tq;
-  kv::CacheView cache;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  int64_t scale_page_stride;
+  int32_t pages, page_shift;
   const int32_t* table;
   int64_t max_pages;
   const int32_t* q_indptr;
@@ -30,124 +92,766 @@ struct Params {
   int32_t mask_words, max_nodes;
   float scale;
   float* lse;
+  Record* records;   // [blocks]
+  float* part_o;     // [2 blocks][kRows][D]
+  float2* part_ml;   // [2 blocks][kRows]
   int32_t* err;
 };
 
-template <int FMT, int PER>
-__device__ __forceinline__ void load_codes(const uint8_t* row, int lane, uint32_t scale_word, float* x) {
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int c = lane * PER + i;
-    if constexpr (FMT == QLIN_KV_U4) {
-      const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(scale_word & 0xffffu)));
-      const float z = __half2float(__ushort_as_half(static_cast<unsigned short>(scale_word >> 16)));
-      x[i] = (static_cast<float>((row[c / 2] >> (4 * (c & 1))) & 15) - z) * s;
-    } else if constexpr (FMT == QLIN_KV_INT8) {
-      x[i] = static_cast<float>(static_cast<int8_t>(row[c])) * __uint_as_float(scale_word);
-    } else {
-      x[i] = kv::unpack2<0>(kv::e4m3x2_to_half2(row[c])).x * __uint_as_float(scale_word);
+// A sequence's bounds as far as they can be used: nodes = 0 when they cannot.
+struct Sequence {
+  int64_t q_row;
+  int32_t nodes, ctx, len;
+  int32_t row_tiles, token_tiles;
+};
+
+__device__ __forceinline__ Sequence sequence(const Params& p, int b) {
+  Sequence s;
+  const int32_t q0 = p.q_indptr[b], q1 = p.q_indptr[b + 1];
+  s.q_row = q0;
+  s.nodes = q1 - q0;
+  s.ctx = p.ctx_lens[b];
+  const int64_t len = static_cast<int64_t>(s.ctx) + s.nodes;
+  const bool fits = q0 >= 0 && q1 >= q0 && q1 <= p.Tq && s.nodes <= p.max_nodes && s.ctx >= 0 &&
+                    len <= (p.max_pages << p.page_shift) && len <= 0x7fffff00;
+  if (!fits) {
+    record_device_error(p.err, kDevErrBadIndex);
+    s.nodes = 0;
+  }
+  s.len = static_cast<int32_t>(len);
+  s.row_tiles = (s.nodes * p.group + kRows - 1) / kRows;
+  s.token_tiles = (s.len + kTile - 1) / kTile;
+  if (s.nodes == 0) s.row_tiles = 0;
+  return s;
+}
+
+__device__ __forceinline__ int64_t units(const Params& p, const Sequence& s) {
+  return s.row_tiles == 0 ? 0 : static_cast<int64_t>(p.hk) * s.row_tiles * s.token_tiles;
+}
+
+// Walks a block's run of units, one segment at a time.
+struct Walk {
+  int32_t b;
+  int64_t at, end;     // next unit, end of the run
+  int64_t first;       // first unit of sequence b
+  Sequence s;
+  // the segment's part that is this block's
+  int32_t head, row_tile, tile, tiles;
+
+  __device__ __forceinline__ bool next(const Params& p) {
+    if (at >= end) return false;
+    int64_t n = units(p, s);
+    while (at - first >= n) {
+      first += n;
+      if (++b >= p.B) return false;  // not reached while the lengths stay as they were counted
+      s = sequence(p, b);
+      n = units(p, s);
     }
+    const int64_t i = at - first;
+    const int32_t seg = static_cast<int32_t>(i / s.token_tiles);
+    tile = static_cast<int32_t>(i - static_cast<int64_t>(seg) * s.token_tiles);
+    head = seg / s.row_tiles;
+    row_tile = seg - head * s.row_tiles;
+    tiles = static_cast<int32_t>(min(static_cast<int64_t>(s.token_tiles - tile), end - at));
+    at += tiles;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+constexpr uint32_t kMagic = 0x64006400u;      // 1024 in both halves: 1024 + n is 0x6400 | n
+constexpr uint32_t kInt8Bias = 0x64806480u;   // 1024 + 128
+
+// Four 8-bit codes of one row as two fp16 pairs (codes 0, 1 and 2, 3).
+template <int FMT>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == QLIN_KV_INT8) {
+    w ^= 0x80808080u;
+    lo = hsub2(__byte_perm(w, kMagic, 0x7170), kInt8Bias);
+    hi = hsub2(__byte_perm(w, kMagic, 0x7372), kInt8Bias);
+  } else {
+    lo = kv::e4m3x2_to_half2(static_cast<uint16_t>(w));
+    hi = kv::e4m3x2_to_half2(static_cast<uint16_t>(w >> 16));
   }
 }
 
-template <int DT, int D, int FMT>
-__global__ void __launch_bounds__(32 * kWarps) tree_attention_plain_kernel(const __grid_constant__ Params p) {
-  constexpr int PER = D / 32;
-  __shared__ float part[kWarps][D + 2];
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y;
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else if constexpr (BYTES == 8)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+
+// The geometry of one (format, head size).
+template <int FMT, int D>
+struct Geo {
+  static constexpr bool kU4 = FMT == QLIN_KV_U4;
+  static constexpr int kRowBytes = kU4 ? D / 2 : D;
+  static constexpr int kSub = kRowBytes > 128 ? 2 : 1;      // 128-byte column blocks of a row
+  static constexpr int kW = kRowBytes / kSub;               // bytes of a row in one of them
+  static constexpr int kSubBytes = kTile * kW;
+  static constexpr int kCodeBytes = kTile * kRowBytes;      // K or V of a stage
+  static constexpr int kScaleBytes = kTile * 4;
+  static constexpr int kStage = 2 * kCodeBytes;
+  static constexpr int kPerSub = kU4 ? 2 * kW : kW;         // channels of a column block
+  static constexpr int kKLane = kW / 4;                     // bytes of a row a lane takes for q . k
+  static constexpr int kVLane = kW / 8;                     // and for p . v
+  static constexpr int kNPerSub = kPerSub / 8;              // output tiles of a column block
+  static constexpr int kStages = kRowBytes >= 256 ? 3 : kRowBytes == 128 ? 4 : 6;
+  static constexpr int kBlocksPerSm = D == 256 ? 1 : 2;
+  // 2^24 (2^15 for E4M3): codes times 2^-kShift are fp16 numbers, exactly
+  static constexpr float kShiftUp = FMT == QLIN_KV_E4M3 ? 32768.0f : 16777216.0f;
+  static constexpr uint32_t kShiftDown = FMT == QLIN_KV_E4M3 ? 0x02000200u : 0x00010001u;
+  // shared memory: stages, scales, merge area, q_max etc.
+  static constexpr int kOffScale = kStages * kStage;
+  static constexpr int kOffMerge = kOffScale + kStages * 2 * kScaleBytes;
+  static constexpr int kMergeRow = D + 4;
+  static constexpr int kOffMl = kOffMerge + kWarps * kRows * kMergeRow * 4;
+  static constexpr int kOffBar = kOffMl + kWarps * kRows * 8;
+  static constexpr int kOffScan = kOffBar + 2 * kStages * 8;
+  static constexpr int kSmem = kOffScan + (kThreads + 1) * 8 + 1024;  // + alignment of the base
+
+  // where 16-byte chunk c of row r of a column block lies
+  static __device__ __forceinline__ uint32_t chunk(int r, int c) {
+    const int s = kW == 128 ? (r & 7) : kW == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+    return static_cast<uint32_t>(r * kW + ((c ^ s) << 4));
+  }
+};
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
+    tree_attention_kernel(const __grid_constant__ Params p) {
+  using G = Geo<FMT, D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - tc::smem_u32(smem_raw));
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int hk = h / p.group;
+  const uint32_t bar_full = base + G::kOffBar, bar_free = bar_full + G::kStages * 8;
+  int64_t* scan = reinterpret_cast<int64_t*>(smem + G::kOffScan);  // [kThreads + 1]
 
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (p.q_indptr[mid] <= t) lo = mid; else hi = mid;
-  }
-  if (t < p.q_indptr[lo] || t >= p.q_indptr[lo + 1]) return;
-  const int node = static_cast<int>(t - p.q_indptr[lo]);
-  const int nodes = p.q_indptr[lo + 1] - p.q_indptr[lo];
-  const int64_t ctx = p.ctx_lens[lo];
-  const int64_t len = ctx + nodes;
-
-  float q[PER], o[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const uint32_t u = reinterpret_cast<const uint16_t*>(p.q + t * p.qt + h * p.qh)[lane * PER + i];
-    q[i] = kv::unpack2<DT>(u).x * p.scale;
-    o[i] = 0.0f;
-  }
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t j = warp; j < len; j += kWarps) {
-    if (j >= ctx) {
-      const int b = static_cast<int>(j - ctx);
-      const bool seen = p.mask == nullptr ? b <= node : (p.mask[t * p.mask_words + b / 64] >> (b & 63)) & 1;
-      if (!seen) continue;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < G::kStages; ++i) {
+      tc::mbar_init(bar_full + 8 * i, 1);
+      tc::mbar_init(bar_free + 8 * i, kWarps);
     }
-    const int64_t n = j >> p.cache.page_shift;
-    const int32_t page = n < p.max_pages ? p.table[lo * p.max_pages + n] : -1;
-    if (page < 0 || page >= p.cache.pages) {
-      record_device_error(p.err, kDevErrBadIndex);
-      continue;
-    }
-    const int64_t row = (static_cast<int64_t>(hk) << p.cache.page_shift) + (j - (n << p.cache.page_shift));
-    const int64_t c = page * p.cache.page_stride + row * kv::row_bytes(FMT, D);
-    const int64_t s = page * p.cache.scale_page_stride + row * 4;
-    float x[PER];
-    load_codes<FMT, PER>(p.cache.k + c, lane, *reinterpret_cast<const uint32_t*>(p.cache.k_scale + s), x);
-    float score = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) score = fmaf(q[i], x[i], score);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) score += __shfl_xor_sync(0xffffffffu, score, w);
-    load_codes<FMT, PER>(p.cache.v + c, lane, *reinterpret_cast<const uint32_t*>(p.cache.v_scale + s), x);
-    const float m_new = fmaxf(m, score);
-    const float keep = m == -INFINITY ? 0.0f : __expf(m - m_new);
-    const float w = __expf(score - m_new);
-    l = l * keep + w;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = o[i] * keep + w * x[i];
-    m = m_new;
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&p.k_map);
+    tc::prefetch_tmap(&p.v_map);
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) part[warp][lane * PER + i] = o[i];
-  if (lane == 0) {
-    part[warp][D] = m;
-    part[warp][D + 1] = l;
+  // the units before each thread's share of the sequences
+  const int share = (p.B + kThreads - 1) / kThreads;
+  {
+    int64_t sum = 0;
+    for (int b = threadIdx.x * share; b < min(p.B, static_cast<int>(threadIdx.x + 1) * share); ++b)
+      sum += units(p, sequence(p, b));
+    scan[threadIdx.x + 1] = sum;
+    if (threadIdx.x == 0) scan[0] = 0;
   }
   __syncthreads();
-  if (warp != 0) return;
-  float top = -INFINITY, total = 0.0f, acc[PER] = {};
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part[w][D]);
-  for (int w = 0; w < kWarps; ++w) {
-    const float keep = part[w][D] == -INFINITY ? 0.0f : __expf(part[w][D] - top);
-    total += part[w][D + 1] * keep;
+  if (warp == 0) {
+    int64_t carry = 0;
+    for (int i = 0; i < kThreads; i += 32) {
+      int64_t v = scan[1 + i + lane];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] += part[w][lane * PER + i] * keep;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      v += carry;
+      scan[1 + i + lane] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
   }
-  const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+  __syncthreads();
+  const int64_t total = scan[kThreads];
+  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);  // each of these has a unit or more
+  if (threadIdx.x == 0) p.records[blockIdx.x].last = -1;
+  if (blockIdx.x >= blocks) {
+    pdl_launch_dependents();
+    return;
+  }
+
+  Walk w;
+  w.at = total * blockIdx.x / blocks;
+  w.end = total * (blockIdx.x + 1) / blocks;
+  {
+    int lo = 0, hi = kThreads;  // the last share that begins at or before the run
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (scan[mid] <= w.at) lo = mid; else hi = mid;
+    }
+    w.b = lo * share;
+    w.first = scan[lo];
+    w.s = sequence(p, w.b);
+  }
+
+  if (warp == kWarps) {  // ---- the loading warp
+    int stage = 0;
+    uint32_t phase = 1;  // the first round finds every stage free
+    bool dead = false;
+    const int page = 1 << p.page_shift;
+    const int box = min(page, kTile);
+    const uint64_t policy = tc::l2_policy_evict_first();
+    while (!dead && w.next(p)) {
+      const int32_t* table = p.table + w.b * p.max_pages;
+      for (int t = w.tile; t < w.tile + w.tiles; ++t) {
+        const int j0 = t * kTile;
+        const int boxes = (min(kTile, w.s.len - j0) + box - 1) / box;  // pages (or the part of one) to load
+        int32_t pg = -1;
+        if (lane < boxes) {
+          pg = table[(j0 + lane * box) >> p.page_shift];
+          if (pg < 0 || pg >= p.pages) {
+            record_device_error(p.err, kDevErrBadIndex);
+            pg = -1;
+          }
+        }
+        const int good = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+        if (!tc::mbar_wait(bar_free + 8 * stage, phase, p.err, 0x50)) dead = true;
+        if (__any_sync(0xffffffffu, dead)) {
+          dead = true;
+          break;
+        }
+        const uint32_t bar = bar_full + 8 * stage;
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, good * box * (2 * G::kRowBytes + 8));
+        __syncwarp();
+        if (pg >= 0) {
+          const int off = (j0 + lane * box) & (page - 1);
+          const int row = w.head * page + off;
+          const uint32_t kd = base + stage * G::kStage + lane * box * G::kW;
 #pragma unroll
-  for (int i = 0; i < PER; ++i)
-    reinterpret_cast<uint16_t*>(p.out + t * p.ot + h * p.oh)[lane * PER + i] =
-        static_cast<uint16_t>(kv::pack2<DT>(acc[i] * inv, 0.0f));
-  if (p.lse != nullptr && lane == 0) p.lse[t * p.hq + h] = top + logf(total);
+          for (int h = 0; h < G::kSub; ++h) {
+            tc::tma_load_3d(kd + h * G::kSubBytes, &p.k_map, h * G::kW, row, pg, bar);
+            tc::tma_load_3d(kd + G::kCodeBytes + h * G::kSubBytes, &p.v_map, h * G::kW, row, pg, bar);
+          }
+          const int64_t so = pg * p.scale_page_stride + static_cast<int64_t>(row) * 4;
+          const uint32_t sd = base + G::kOffScale + stage * 2 * G::kScaleBytes + lane * box * 4;
+          tc::bulk_load_policy(sd, p.k_scale + so, box * 4, bar, policy);
+          tc::bulk_load_policy(sd + G::kScaleBytes, p.v_scale + so, box * 4, bar, policy);
+        }
+        if (++stage == G::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    pdl_launch_dependents();
+    return;
+  }
+
+  // ---- the compute warps
+  const int g = lane >> 2, r = lane & 3;
+  int stage = 0;
+  uint32_t phase = 0;
+  bool dead = false;  // a wait ran out: go on without waiting, so that every barrier is met
+  while (w.next(p)) {
+    // q of this lane's rows g and g + 8, as fp16 operands scaled by a power of two
+    uint32_t qa[D / 16][4];
+    float row_scale[2];
+    int32_t row_node[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = w.row_tile * kRows + g + 8 * i;
+      const int node = row / p.group;
+      const bool live = node < w.s.nodes;
+      row_node[i] = live ? node : -1;
+      const uint8_t* src = p.q + (w.s.q_row + node) * p.qt + (w.head * p.group + row - node * p.group) * p.qh;
+      uint32_t raw[D / 8];  // this lane's D / 4 channels: kPerSub / 4 contiguous ones of each column block
+      uint32_t top = 0;
+#pragma unroll
+      for (int h = 0; h < G::kSub; ++h) {
+#pragma unroll
+        for (int c = 0; c < G::kPerSub / 32; ++c) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (live) v = ldg_v4(src + 2 * (h * G::kPerSub + r * (G::kPerSub / 4) + 8 * c));
+          uint32_t* to = raw + h * (G::kPerSub / 8) + 4 * c;
+          to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+        }
+      }
+      const bool bf16 = p.dtype == QLIN_BF16;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const float2 f = bf16 ? kv::unpack2<1>(raw[c]) : kv::unpack2<0>(raw[c]);
+        top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the largest magnitude to [2^14, 2^15); rows of zeros, infinities or NaN as they are
+      int e = 0;
+      if (top > 0 && top < 0x7f800000u) e = ilogbf(__uint_as_float(top)) - 14;
+      row_scale[i] = ldexpf(p.scale * kLog2e, e);
+      // 2^-e in two factors, each a normal float for every e of a 16-bit row
+      const float s1 = ldexpf(1.0f, -(e / 2)), s2 = ldexpf(1.0f, -(e - e / 2));
+      uint16_t q16[D / 4];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const float2 f = bf16 ? kv::unpack2<1>(raw[c]) : kv::unpack2<0>(raw[c]);
+        const uint32_t u = kv::pack2<0>(f.x * s1 * s2, f.y * s1 * s2);
+        q16[2 * c] = static_cast<uint16_t>(u);
+        q16[2 * c + 1] = static_cast<uint16_t>(u >> 16);
+      }
+      // the order in which the widened codes of a lane's bytes meet the k index
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int x = G::kU4 ? 8 * (ks / 2) + 2 * (ks % 2) + h : 4 * ks + 2 * h;
+          const int y = G::kU4 ? x + 4 : x + 1;
+          qa[ks][i + 2 * h] = static_cast<uint32_t>(q16[x]) | (static_cast<uint32_t>(q16[y]) << 16);
+        }
+      }
+    }
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    for (int t = w.tile; t < w.tile + w.tiles; ++t) {
+      if (!dead) dead = !tc::mbar_wait(bar_full + 8 * stage, phase, p.err, 0x51);
+      dead = __any_sync(0xffffffffu, dead);
+      const int j0 = t * kTile + warp * 16;  // this warp's first token
+      if (j0 < w.s.len) {
+        const uint32_t ks_at = base + stage * G::kStage;
+        const uint32_t vs_at = ks_at + G::kCodeBytes;
+        const uint8_t* sc = smem + G::kOffScale + stage * 2 * G::kScaleBytes;
+
+        // the scales of the four tokens whose scores this lane holds: 8 n + 2 r + {0, 1}
+        float sk[4], lsv[4], rsv[4];
+        uint32_t vz[2];  // U4: 1024 + the zero-points of the tokens, per pair
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int tok = warp * 16 + 8 * n + 2 * r;
+          const uint2 kw = *reinterpret_cast<const uint2*>(sc + tok * 4);
+          const uint2 vw = *reinterpret_cast<const uint2*>(sc + G::kScaleBytes + tok * 4);
+          const uint32_t kws[2] = {kw.x, kw.y}, vws[2] = {vw.x, vw.y};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float sv;
+            if constexpr (G::kU4) {
+              sk[2 * n + i] = __half2float(__ushort_as_half(static_cast<unsigned short>(kws[i] & 0xffffu)));
+              sv = __half2float(__ushort_as_half(static_cast<unsigned short>(vws[i] & 0xffffu)));
+            } else {
+              sk[2 * n + i] = __uint_as_float(kws[i]);
+              sv = __uint_as_float(vws[i]);
+            }
+            lsv[2 * n + i] = lg2(sv);
+            rsv[2 * n + i] = __frcp_rn(sv);
+          }
+          if constexpr (G::kU4) {
+            // a zero-point that is not one (its token is not seen) becomes 0: what is not seen has to stay finite
+            const uint32_t z = __byte_perm(vw.x, vw.y, 0x7632);
+            const __half2 zz = __hmin2(__hmax2(*reinterpret_cast<const __half2*>(&z), __float2half2_rn(0.0f)),
+                                       __float2half2_rn(15.0f));
+            const __half2 b = __hadd2(zz, __float2half2_rn(1024.0f));
+            vz[n] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+        }
+
+        // scores of 16 rows x 16 tokens
+        float s[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+          const int tok = warp * 16 + 8 * n + g;
+          uint32_t kz = 0;
+          if constexpr (G::kU4) {
+            const uint32_t kw = *reinterpret_cast<const uint32_t*>(sc + tok * 4);
+            const __half2 b = __hadd2(__half2half2(__ushort_as_half(static_cast<unsigned short>(kw >> 16))),
+                                      __float2half2_rn(1024.0f));
+            kz = *reinterpret_cast<const uint32_t*>(&b);
+          }
+#pragma unroll
+          for (int h = 0; h < G::kSub; ++h) {
+            constexpr int kLoad = G::kKLane < 16 ? G::kKLane : 16;
+#pragma unroll
+            for (int c = 0; c < G::kKLane / kLoad; ++c) {
+              uint32_t wd[4];
+              const int byte = r * G::kKLane + c * 16;
+              lds<kLoad>(ks_at + h * G::kSubBytes + G::chunk(tok, byte / 16) + byte % 16, wd);
+#pragma unroll
+              for (int i = 0; i < kLoad / 4; ++i) {
+                if constexpr (G::kU4) {
+                  const int ks = h * (G::kPerSub / 16) + (c * (kLoad / 4) + i) * 2;
+                  const uint32_t x0 = hsub2((wd[i] & 0x000f000fu) | kMagic, kz);
+                  const uint32_t x1 = hsub2(((wd[i] >> 4) & 0x000f000fu) | kMagic, kz);
+                  const uint32_t x2 = hsub2(((wd[i] >> 8) & 0x000f000fu) | kMagic, kz);
+                  const uint32_t x3 = hsub2(((wd[i] >> 12) & 0x000f000fu) | kMagic, kz);
+                  mma16816(s[n], qa[ks], x0, x1);
+                  mma16816(s[n], qa[ks + 1], x2, x3);
+                } else {
+                  const int ks = h * (G::kPerSub / 16) + c * (kLoad / 4) + i;
+                  uint32_t lo, hi;
+                  widen4<FMT>(wd[i], lo, hi);
+                  mma16816(s[n], qa[ks], lo, hi);
+                }
+              }
+            }
+          }
+        }
+
+        // t, hiding what a row does not see
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s[n][i] = fmaf(s[n][i] * row_scale[i >> 1], sk[2 * n + (i & 1)], lsv[2 * n + (i & 1)]);
+        if (j0 + 16 > w.s.ctx) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = j0 + 8 * n + 2 * r + (i & 1) - w.s.ctx;  // the node that the token is
+              const int node = row_node[i >> 1];
+              bool seen = j < 0;
+              if (!seen && j < w.s.nodes && node >= 0)
+                seen = p.mask == nullptr
+                           ? j <= node
+                           : ((p.mask[(w.s.q_row + node) * p.mask_words + (j >> 6)] >> (j & 63)) & 1) != 0;
+              if (!seen) s[n][i] = -INFINITY;
+            }
+        }
+
+        // move the reference where t leaves it behind
+        const float top0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        const float top1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        if (__any_sync(0xffffffffu, top0 > m[0] + kSlack || top1 > m[1] + kSlack)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = i == 0 ? top0 : top1;
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float to = fmaxf(m[i], top);
+            const float keep = m[i] == -INFINITY ? 0.0f : ex2(m[i] - to);
+            m[i] = to;
+            l[i] *= keep;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              o[c][2 * i] *= keep;
+              o[c][2 * i + 1] *= keep;
+            }
+          }
+        }
+        const float ref0 = m[0] == -INFINITY ? 0.0f : m[0] - kOffset;
+        const float ref1 = m[1] == -INFINITY ? 0.0f : m[1] - kOffset;
+        uint32_t pa[4], pb[4];
+        bool small = false;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            e[i] = ex2(s[n][i] - (i < 2 ? ref0 : ref1));
+            // a hidden token adds nothing, whatever its scale is
+            l[i >> 1] += e[i] == 0.0f ? 0.0f : e[i] * rsv[2 * n + (i & 1)];
+            small = small || (e[i] > 0.0f && e[i] < kHalfNormal);
+          }
+          pa[2 * n] = kv::pack2<0>(e[0], e[1]);
+          pa[2 * n + 1] = kv::pack2<0>(e[2], e[3]);
+          s[n][0] = e[0], s[n][1] = e[1], s[n][2] = e[2], s[n][3] = e[3];
+        }
+        small = __any_sync(0xffffffffu, small);
+        if (small) {  // those below fp16's normal range apart, times 2^kShift
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float x = s[n][2 * h], y = s[n][2 * h + 1];
+              const bool u = x < kHalfNormal, v = y < kHalfNormal;
+              pa[2 * n + h] = kv::pack2<0>(u ? 0.0f : x, v ? 0.0f : y);
+              pb[2 * n + h] = kv::pack2<0>(u ? x * G::kShiftUp : 0.0f, v ? y * G::kShiftUp : 0.0f);
+            }
+        }
+
+        // p . v: the lane's four tokens 2 r + {0, 1, 8, 9}, contiguous channels of each
+        const bool tail = j0 + 16 > w.s.len;
+        auto accumulate = [&](const uint32_t* pr, auto shifted) {
+          constexpr bool kShifted = decltype(shifted)::value;
+          auto product = [&](float* acc, uint32_t b0, uint32_t b1) {
+            if constexpr (kShifted) {
+              b0 = hmul2(b0, G::kShiftDown);
+              b1 = hmul2(b1, G::kShiftDown);
+            }
+            mma16816(acc, pr, b0, b1);
+          };
+#pragma unroll
+          for (int h = 0; h < G::kSub; ++h) {
+            constexpr int kLoad = G::kVLane;  // 16, 8 or 4 bytes
+            uint32_t wd[4][kLoad / 4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = warp * 16 + 2 * r + (i & 1) + 8 * (i >> 1);
+              const int byte = g * kLoad;
+              lds<kLoad>(vs_at + h * G::kSubBytes + G::chunk(tok, byte / 16) + byte % 16, wd[i]);
+              if constexpr (FMT == QLIN_KV_E4M3) {
+                // beyond the sequence's end lies anything, E4M3 NaN among it
+                if (tail && t * kTile + tok >= w.s.len) {
+#pragma unroll
+                  for (int c = 0; c < kLoad / 4; ++c) wd[i][c] = 0u;
+                }
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < kLoad / 4; ++c) {
+              if constexpr (G::kU4) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const uint32_t sel = half ? 0x7632u : 0x5410u;
+                  const uint32_t a = __byte_perm(wd[0][c], wd[1][c], sel), b = __byte_perm(wd[2][c], wd[3][c], sel);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    product(o[h * G::kNPerSub + 8 * c + 4 * half + i], hsub2(((a >> (4 * i)) & 0x000f000fu) | kMagic, vz[0]),
+                            hsub2(((b >> (4 * i)) & 0x000f000fu) | kMagic, vz[1]));
+                }
+              } else {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const uint32_t sel = half ? 0x7362u : 0x5140u;
+                  uint32_t a0, a1, b0, b1;
+                  widen4<FMT>(__byte_perm(wd[0][c], wd[1][c], sel), a0, a1);
+                  widen4<FMT>(__byte_perm(wd[2][c], wd[3][c], sel), b0, b1);
+                  const int n = h * G::kNPerSub + 4 * c + 2 * half;
+                  product(o[n], a0, b0);
+                  product(o[n + 1], a1, b1);
+                }
+              }
+            }
+          }
+        };
+        accumulate(pa, std::false_type{});
+        if (small) accumulate(pb, std::true_type{});
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar_free + 8 * stage);
+      if (++stage == G::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+
+    // join the warps: each scaled to the common reference
+    float* area = reinterpret_cast<float*>(smem + G::kOffMerge);
+    float2* ml = reinterpret_cast<float2*>(smem + G::kOffMl);  // [warp][row]
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (r == 0) ml[warp * kRows + g + 8 * i] = make_float2(m[i], l[i]);
+      float* to = area + (warp * kRows + g + 8 * i) * G::kMergeRow;
+#pragma unroll
+      for (int h = 0; h < G::kSub; ++h)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int c = 0; c < G::kNPerSub; c += 4) {
+            const int n = h * G::kNPerSub + c;
+            *reinterpret_cast<float4*>(to + h * G::kPerSub + (2 * r + y) * G::kNPerSub + c) =
+                make_float4(o[n][2 * i + y], o[n + 1][2 * i + y], o[n + 2][2 * i + y], o[n + 3][2 * i + y]);
+          }
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    const bool begins = w.tile == 0, ends = w.tile + w.tiles == w.s.token_tiles;
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (begins ? 1 : 0);
+    constexpr int kPer = D / 4;  // threads a row
+    for (int row = threadIdx.x / kPer; row < kRows; row += 32 * kWarps / kPer) {
+      const int c = threadIdx.x % kPer * 4;
+      const int at = w.row_tile * kRows + row;
+      const int node = at / p.group;
+      if (node >= w.s.nodes) break;
+      float2 e[kWarps];
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        e[i] = ml[i * kRows + row];
+        top = fmaxf(top, e[i].x);
+      }
+      float sum = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        // a warp that saw nothing has o = l = 0, or NaN from a query that is NaN: pass that on
+        const float f = e[i].x == -INFINITY ? 1.0f : ex2(e[i].x - top);
+        const float4 v = *reinterpret_cast<const float4*>(area + (i * kRows + row) * G::kMergeRow + c);
+        sum += f * e[i].y;
+        acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+      }
+      if (begins && ends) {
+        const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+        const int head = w.head * p.group + at - node * p.group;
+        const int64_t tok = w.s.q_row + node;
+        const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+        const uint2 u = p.dtype == QLIN_BF16 ? make_uint2(kv::pack2<1>(v[0], v[1]), kv::pack2<1>(v[2], v[3]))
+                                              : make_uint2(kv::pack2<0>(v[0], v[1]), kv::pack2<0>(v[2], v[3]));
+        *reinterpret_cast<uint2*>(p.out + tok * p.ot + head * p.oh + c * 2) = u;
+        if (p.lse != nullptr && c == 0) p.lse[tok * p.hq + head] = (lg2(sum) + (top - kOffset)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (slot * kRows + row) * D + c) = acc;
+        if (c == 0) p.part_ml[slot * kRows + row] = make_float2(top, sum);
+      }
+    }
+    if (begins && !ends && threadIdx.x == 0) {
+      const int64_t end = w.at - w.tiles + w.s.token_tiles;  // the segment's end, in units
+      Record rec;
+      rec.last = static_cast<int32_t>((end * blocks - 1) / total);
+      rec.head = w.head;
+      rec.row_tile = w.row_tile;
+      rec.nodes = w.s.nodes;
+      rec.q_row = w.s.q_row;
+      p.records[blockIdx.x] = rec;
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");  // the merge area is free again
+  }
+  pdl_launch_dependents();
 }
 
-template <int DT, int D>
-cudaError_t launch(const Params& p, int fmt, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.Tq), static_cast<unsigned>(p.hq));
-  if (fmt == QLIN_KV_INT8) tree_attention_plain_kernel<DT, D, QLIN_KV_INT8><<<grid, 32 * kWarps, 0, stream>>>(p);
-  else if (fmt == QLIN_KV_E4M3) tree_attention_plain_kernel<DT, D, QLIN_KV_E4M3><<<grid, 32 * kWarps, 0, stream>>>(p);
-  else tree_attention_plain_kernel<DT, D, QLIN_KV_U4><<<grid, 32 * kWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+// Joins the parts of a segment that begins in block `blockIdx.x` of the first
+// kernel and ends in a later one: one row per block, its parts dealt to the
+// warps, D / 4 lanes' worth of float4 each.
+template <int D>
+__global__ void __launch_bounds__(128) tree_attention_join_kernel(const __grid_constant__ Params p) {
+  constexpr int kLanes = D / 4 < 32 ? D / 4 : 32;  // lanes that cover a row once
+  constexpr int kWide = D / 4 / kLanes;            // float4 a lane
+  constexpr int kTeams = 128 / kLanes;
+  __shared__ float4 part[kTeams][D / 4];
+  __shared__ float2 part_ml[kTeams];
+  pdl_wait();
+  const Record rec = p.records[blockIdx.x];
+  if (rec.last < 0) return;
+  const int row = blockIdx.y;
+  const int at = rec.row_tile * kRows + row;
+  const int node = at / p.group;
+  if (node >= rec.nodes) return;
+  const int team = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const int count = rec.last - static_cast<int>(blockIdx.x) + 1;
+
+  float m = -INFINITY, l = 0.0f;
+  float4 o[kWide];
+#pragma unroll
+  for (int i = 0; i < kWide; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = team; i < count; i += kTeams) {
+    const int64_t slot = 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0);
+    const float2 e = p.part_ml[slot * kRows + row];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot * kRows + row) * D) + lane;
+    float4 v[kWide];
+#pragma unroll
+    for (int x = 0; x < kWide; ++x) v[x] = src[x * kLanes];
+    const float to = fmaxf(m, e.x);
+    const float fa = m == -INFINITY ? 1.0f : ex2(m - to), fb = e.x == -INFINITY ? 1.0f : ex2(e.x - to);
+    m = to;
+    l = l * fa + e.y * fb;
+#pragma unroll
+    for (int x = 0; x < kWide; ++x) {
+      o[x].x = o[x].x * fa + v[x].x * fb;
+      o[x].y = o[x].y * fa + v[x].y * fb;
+      o[x].z = o[x].z * fa + v[x].z * fb;
+      o[x].w = o[x].w * fa + v[x].w * fb;
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < kWide; ++x) part[team][lane + x * kLanes] = o[x];
+  if (lane == 0) part_ml[team] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x >= D / 4) return;
+  float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kTeams; ++i) top = fmaxf(top, part_ml[i].x);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < kTeams; ++i) {
+    const float f = part_ml[i].x == -INFINITY ? 1.0f : ex2(part_ml[i].x - top);
+    const float4 v = part[i][threadIdx.x];
+    sum += f * part_ml[i].y;
+    acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+  }
+  const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+  const int head = rec.head * p.group + at - node * p.group;
+  const int64_t tok = rec.q_row + node;
+  const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  const uint2 u = p.dtype == QLIN_BF16 ? make_uint2(kv::pack2<1>(v[0], v[1]), kv::pack2<1>(v[2], v[3]))
+                                        : make_uint2(kv::pack2<0>(v[0], v[1]), kv::pack2<0>(v[2], v[3]));
+  *reinterpret_cast<uint2*>(p.out + tok * p.ot + head * p.oh + threadIdx.x * 8) = u;
+  if (p.lse != nullptr && threadIdx.x == 0) p.lse[tok * p.hq + head] = (lg2(sum) + (top - kOffset)) * kLn2;
+}
+
+int grid_blocks(int64_t head_dim) { return std::min(kMaxBlocks, sm_count() * (head_dim == 256 ? 1 : 2)); }
+
+template <int FMT, int D>
+cudaError_t launch(const Params& p, cudaStream_t stream) {
+  using G = Geo<FMT, D>;
+  const void* fn = reinterpret_cast<const void*>(tree_attention_kernel<FMT, D>);
+  cudaError_t e = ensure_max_dynamic_smem(fn);
+  if (e != cudaSuccess) return e;
+  const unsigned blocks = static_cast<unsigned>(grid_blocks(D));
+  tree_attention_kernel<FMT, D><<<blocks, kThreads, G::kSmem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, kRows);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<D>, p);
+}
+
+template <int FMT>
+cudaError_t launch(const Params& p, int64_t d, cudaStream_t stream) {
+  if (d == 64) return launch<FMT, 64>(p, stream);
+  if (d == 128) return launch<FMT, 128>(p, stream);
+  return launch<FMT, 256>(p, stream);
 }
 
 }  // namespace
 
-int64_t tree_attention_workspace_bytes(const qlin_kv_cache&, int64_t, int64_t, int64_t) { return 256; }
+int64_t tree_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t, int64_t, int64_t) {
+  const int64_t blocks = grid_blocks(cache.head_dim);
+  return blocks * static_cast<int64_t>(sizeof(Record)) + 256 +
+         2 * blocks * kRows * (cache.head_dim * 4 + static_cast<int64_t>(sizeof(float2)));
+}
 
 cudaError_t launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t stream) {
   Params p = {};
+  const qlin_kv_cache& c = a.cache;
+  const int64_t row_bytes = kv::row_bytes(c.fmt, static_cast<int>(c.head_dim));
+  const uint32_t box_cols = static_cast<uint32_t>(std::min<int64_t>(row_bytes, 128));
+  const uint32_t box_rows = static_cast<uint32_t>(std::min<int64_t>(c.page_size, kTile));
+  cudaError_t e = make_tmap_3d_u8(&p.k_map, c.k, row_bytes, c.heads * c.page_size, c.pages, c.page_stride, box_cols, box_rows);
+  if (e == cudaSuccess)
+    e = make_tmap_3d_u8(&p.v_map, c.v, row_bytes, c.heads * c.page_size, c.pages, c.page_stride, box_cols, box_rows);
+  if (e != cudaSuccess) return e;
   p.q = static_cast<const uint8_t*>(a.q.data);
   p.out = static_cast<uint8_t*>(a.out.data);
   p.qt = 2 * a.q.token_stride;
@@ -155,9 +859,16 @@ cudaError_t launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t strea
   p.ot = 2 * a.out.token_stride;
   p.oh = 2 * a.out.head_stride;
   p.hq = static_cast<int32_t>(a.q.heads);
-  p.group = static_cast<int32_t>(a.q.heads / a.cache.heads);
+  p.hk = static_cast<int32_t>(c.heads);
+  p.group = p.hq / p.hk;
+  p.dtype = a.dtype;
   p.Tq = a.Tq;
-  p.cache = kv::view_of(a.cache);
+  p.k_scale = static_cast<const uint8_t*>(c.k_scale);
+  p.v_scale = static_cast<const uint8_t*>(c.v_scale);
+  p.scale_page_stride = c.scale_page_stride;
+  const kv::CacheView view = kv::view_of(c);
+  p.pages = view.pages;
+  p.page_shift = view.page_shift;
   p.table = a.block_table;
   p.max_pages = a.max_pages;
   p.q_indptr = a.q_indptr;
@@ -168,17 +879,17 @@ cudaError_t launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t strea
   p.max_nodes = static_cast<int32_t>(a.max_nodes);
   p.scale = a.scale;
   p.lse = a.lse;
+  const int64_t blocks = grid_blocks(c.head_dim);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  ws += 2 * blocks * kRows * c.head_dim * 4;
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  ws += 2 * blocks * kRows * static_cast<int64_t>(sizeof(float2));
+  p.records = reinterpret_cast<Record*>(ws);
   p.err = device_error_word();
-  const int fmt = a.cache.fmt;
-  const int64_t d = a.cache.head_dim;
-  if (a.dtype == QLIN_F16) {
-    if (d == 64) return launch<0, 64>(p, fmt, stream);
-    if (d == 128) return launch<0, 128>(p, fmt, stream);
-    return launch<0, 256>(p, fmt, stream);
-  }
-  if (d == 64) return launch<1, 64>(p, fmt, stream);
-  if (d == 128) return launch<1, 128>(p, fmt, stream);
-  return launch<1, 256>(p, fmt, stream);
+  if (c.fmt == QLIN_KV_INT8) return launch<QLIN_KV_INT8>(p, c.head_dim, stream);
+  if (c.fmt == QLIN_KV_E4M3) return launch<QLIN_KV_E4M3>(p, c.head_dim, stream);
+  return launch<QLIN_KV_U4>(p, c.head_dim, stream);
 }
 
 }  // namespace qlin
