@@ -29,15 +29,16 @@
 // (o, m, l), which a second kernel joins in the order of the blocks; a
 // sequence's result depends on the lengths, not on timing.
 //
-// A block has four compute warps and one that loads.  The loading warp keeps a
-// ring of stages filled by TMA: 64 tokens' codes of K and V (one box per page
-// that the tile touches, 128-, 64- or 32-byte swizzled rows) and their scales.
-// Each compute warp takes 16 of the stage's tokens for all rows, with its own
-// running maximum, sums and output, so that no barrier lies between warps
-// until the segment ends.  Codes are widened to fp16 in registers, straight
-// into the operand layout of mma.m16n8k16: the order of channels in q . n and
-// of output channels is permuted such that a lane's operands are contiguous
-// bytes of a row, read without bank conflicts through the swizzle.
+// A block has five compute warps (seven where registers allow) and one that
+// loads.  The loading warp keeps a ring of stages filled by TMA: one unit's
+// codes of K and V (one box per page that the tile touches, 128-, 64- or
+// 32-byte swizzled rows) and their scales.  Units go to the compute warps in
+// turn; a warp takes all rows of its unit, with its own running maximum, sums
+// and output, so that nothing but the ring lies between warps until a segment
+// ends.  Codes are widened to fp16 in registers, straight into the operand
+// layout of mma.m16n8k16: the order of channels in q . n and of output channels
+// is permuted such that a lane's operands are contiguous bytes of a row, read
+// without bank conflicts through the swizzle.
 //
 // Bound: HBM for one to about eight rows per key head; at 16 rows (8-bit
 // codes) the widening instructions take about as long as the loads.
@@ -53,12 +54,12 @@
 namespace qlin {
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kTile = 32;
 constexpr int kRows = 16;
 constexpr float kOffset = 13.0f;
 constexpr float kSlack = 2.0f;
+constexpr float kNoRef = -1e30f;  // before a row has seen anything
+constexpr float kHalfExp = -14.0f;
 constexpr float kHalfNormal = 6.103515625e-5f;  // 2^-14, the smallest normal fp16
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
@@ -165,7 +166,13 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float lg2(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -227,19 +234,23 @@ struct Geo {
   static constexpr int kKLane = kW / 4;                     // bytes of a row a lane takes for q . k
   static constexpr int kVLane = kW / 8;                     // and for p . v
   static constexpr int kNPerSub = kPerSub / 8;              // output tiles of a column block
-  static constexpr int kStages = kRowBytes >= 256 ? 3 : kRowBytes == 128 ? 4 : 6;
+  // 168 registers a thread (D = 128) let 12 warps live on an SM, 128 (D = 64) 16, 255 (D = 256) 8
   static constexpr int kBlocksPerSm = D == 256 ? 1 : 2;
+  static constexpr int kWarps = D == 128 ? 5 : 7;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kStages = kRowBytes >= 256 ? 6 : kRowBytes == 128 ? 8 : kRowBytes == 64 ? 12 : 16;
   // 2^24 (2^15 for E4M3): codes times 2^-kShift are fp16 numbers, exactly
   static constexpr float kShiftUp = FMT == QLIN_KV_E4M3 ? 32768.0f : 16777216.0f;
   static constexpr uint32_t kShiftDown = FMT == QLIN_KV_E4M3 ? 0x02000200u : 0x00010001u;
   // shared memory: stages, scales, merge area, q_max etc.
   static constexpr int kOffScale = kStages * kStage;
   static constexpr int kOffMerge = kOffScale + kStages * 2 * kScaleBytes;
-  static constexpr int kMergeRow = D + 4;
+  static constexpr int kMergeRow = D + 4;  // floats
   static constexpr int kOffMl = kOffMerge + kWarps * kRows * kMergeRow * 4;
   static constexpr int kOffBar = kOffMl + kWarps * kRows * 8;
   static constexpr int kOffScan = kOffBar + 2 * kStages * 8;
-  static constexpr int kSmem = kOffScan + (kThreads + 1) * 8 + 1024;  // + alignment of the base
+  static constexpr int kOffWalk = (kOffScan + (kThreads + 1) * 8 + 15) / 16 * 16;
+  static constexpr int kSmem = kOffWalk + kWarps * static_cast<int>(sizeof(Walk)) + 1024;  // + alignment of the base
 
   // where 16-byte chunk c of row r of a column block lies
   static __device__ __forceinline__ uint32_t chunk(int r, int c) {
@@ -249,9 +260,10 @@ struct Geo {
 };
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
+__global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPerSm)
     tree_attention_kernel(const __grid_constant__ Params p) {
   using G = Geo<FMT, D>;
+  constexpr int kWarps = G::kWarps, kThreads = G::kThreads;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - tc::smem_u32(smem_raw));
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kStages; ++i) {
       tc::mbar_init(bar_full + 8 * i, 1);
-      tc::mbar_init(bar_free + 8 * i, kWarps);
+      tc::mbar_init(bar_free + 8 * i, 1);
     }
     tc::fence_mbar_init();
     tc::prefetch_tmap(&p.k_map);
@@ -301,41 +313,50 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
     return;
   }
 
-  Walk w;
-  w.at = total * blockIdx.x / blocks;
-  w.end = total * (blockIdx.x + 1) / blocks;
+  Walk run;
+  run.at = total * blockIdx.x / blocks;
+  run.end = total * (blockIdx.x + 1) / blocks;
   {
     int lo = 0, hi = kThreads;  // the last share that begins at or before the run
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (scan[mid] <= w.at) lo = mid; else hi = mid;
+      if (scan[mid] <= run.at) lo = mid; else hi = mid;
     }
-    w.b = lo * share;
-    w.first = scan[lo];
-    w.s = sequence(p, w.b);
+    run.b = lo * share;
+    run.first = scan[lo];
+    run.s = sequence(p, run.b);
   }
 
   if (warp == kWarps) {  // ---- the loading warp
+    Walk& w = run;
     int stage = 0;
     uint32_t phase = 1;  // the first round finds every stage free
     bool dead = false;
     const int page = 1 << p.page_shift;
     const int box = min(page, kTile);
+    const int boxes = kTile / box;  // of a unit
     const uint64_t policy = tc::l2_policy_evict_first();
     while (!dead && w.next(p)) {
       const int32_t* table = p.table + w.b * p.max_pages;
+      int32_t ahead = -1;  // the page of box `lane` of the 32 boxes from unit `from` on
+      int from = 0;
       for (int t = w.tile; t < w.tile + w.tiles; ++t) {
-        const int j0 = t * kTile;
-        const int boxes = (min(kTile, w.s.len - j0) + box - 1) / box;  // pages (or the part of one) to load
-        int32_t pg = -1;
-        if (lane < boxes) {
-          pg = table[(j0 + lane * box) >> p.page_shift];
-          if (pg < 0 || pg >= p.pages) {
-            record_device_error(p.err, kDevErrBadIndex);
-            pg = -1;
+        if (t == w.tile || (t - from) * boxes == 32) {
+          from = t;
+          const int j = t * kTile + lane * box;
+          ahead = -1;
+          if (j < min(w.s.len, (w.tile + w.tiles) * kTile)) {
+            ahead = table[j >> p.page_shift];
+            if (ahead < 0 || ahead >= p.pages) {
+              record_device_error(p.err, kDevErrBadIndex);
+              ahead = -1;
+            }
           }
         }
-        const int good = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+        const int at = (t - from) * boxes;  // this unit's boxes; those past the end have no page
+        const int32_t pg = __shfl_sync(0xffffffffu, ahead, (at + lane) & 31);
+        const bool load = lane < boxes && pg >= 0;
+        const int good = __popc(__ballot_sync(0xffffffffu, load));
         if (!tc::mbar_wait(bar_free + 8 * stage, phase, p.err, 0x50)) dead = true;
         if (__any_sync(0xffffffffu, dead)) {
           dead = true;
@@ -344,19 +365,19 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
         const uint32_t bar = bar_full + 8 * stage;
         if (lane == 0) tc::mbar_arrive_expect_tx(bar, good * box * (2 * G::kRowBytes + 8));
         __syncwarp();
-        if (pg >= 0) {
-          const int off = (j0 + lane * box) & (page - 1);
+        if (load) {
+          const int off = (t * kTile + lane * box) & (page - 1);
           const int row = w.head * page + off;
           const uint32_t kd = base + stage * G::kStage + lane * box * G::kW;
-#pragma unroll
-          for (int h = 0; h < G::kSub; ++h) {
-            tc::tma_load_3d(kd + h * G::kSubBytes, &p.k_map, h * G::kW, row, pg, bar);
-            tc::tma_load_3d(kd + G::kCodeBytes + h * G::kSubBytes, &p.v_map, h * G::kW, row, pg, bar);
-          }
           const int64_t so = pg * p.scale_page_stride + static_cast<int64_t>(row) * 4;
           const uint32_t sd = base + G::kOffScale + stage * 2 * G::kScaleBytes + lane * box * 4;
+#pragma unroll
+          for (int h = 0; h < G::kSub; ++h) tc::tma_load_3d(kd + h * G::kSubBytes, &p.k_map, h * G::kW, row, pg, bar);
           tc::bulk_load_policy(sd, p.k_scale + so, box * 4, bar, policy);
           tc::bulk_load_policy(sd + G::kScaleBytes, p.v_scale + so, box * 4, bar, policy);
+#pragma unroll
+          for (int h = 0; h < G::kSub; ++h)
+            tc::tma_load_3d(kd + G::kCodeBytes + h * G::kSubBytes, &p.v_map, h * G::kW, row, pg, bar);
         }
         if (++stage == G::kStages) {
           stage = 0;
@@ -370,10 +391,17 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
 
   // ---- the compute warps
   const int g = lane >> 2, r = lane & 3;
-  int stage = 0;
-  uint32_t phase = 0;
+  uint32_t unit0 = 0;  // units of the run before this segment
   bool dead = false;  // a wait ran out: go on without waiting, so that every barrier is met
-  while (w.next(p)) {
+  // the walk stays in shared memory, out of the registers of the loop below
+  Walk& w = reinterpret_cast<Walk*>(smem + G::kOffWalk)[warp];
+  if (lane == 0) w = run;
+  while (true) {
+    bool more = false;
+    __syncwarp();
+    if (lane == 0) more = w.next(p);
+    __syncwarp();
+    if (!__shfl_sync(0xffffffffu, more, 0)) break;
     // q of this lane's rows g and g + 8, as fp16 operands scaled by a power of two
     uint32_t qa[D / 16][4];
     float row_scale[2];
@@ -434,168 +462,166 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float ref[2] = {kNoRef, kNoRef}, l[2] = {0.0f, 0.0f};
 
-    for (int t = w.tile; t < w.tile + w.tiles; ++t) {
-      if (!dead) dead = !tc::mbar_wait(bar_full + 8 * stage, phase, p.err, 0x51);
+    // this warp's units of the segment
+    uint32_t u = unit0 + (warp + kWarps - unit0 % kWarps) % kWarps;
+    const bool took = u < unit0 + w.tiles;
+    for (; u < unit0 + w.tiles; u += kWarps) {
+      const uint32_t stage = u % G::kStages;
+      if (!dead) dead = !tc::mbar_wait(bar_full + 8 * stage, (u / G::kStages) & 1, p.err, 0x51);
       dead = __any_sync(0xffffffffu, dead);
-      const int j0 = t * kTile + warp * 16;  // this warp's first token
-      if (j0 < w.s.len) {
-        const uint32_t ks_at = base + stage * G::kStage;
-        const uint32_t vs_at = ks_at + G::kCodeBytes;
-        const uint8_t* sc = smem + G::kOffScale + stage * 2 * G::kScaleBytes;
+      const int j0 = (w.tile + static_cast<int>(u - unit0)) * kTile;  // the unit's first token
+      const uint32_t ks_at = base + stage * G::kStage;
+      const uint32_t vs_at = ks_at + G::kCodeBytes;
+      const uint8_t* sc = smem + G::kOffScale + stage * 2 * G::kScaleBytes;
+      const bool masked = j0 + kTile > w.s.ctx;
 
-        // the scales of the four tokens whose scores this lane holds: 8 n + 2 r + {0, 1}
-        float sk[4], lsv[4], rsv[4];
-        uint32_t vz[2];  // U4: 1024 + the zero-points of the tokens, per pair
+      // scores of 16 rows x 32 tokens; this lane's: rows g, g + 8, tokens 8 n + 2 r + {0, 1}
+      float s[4][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int tok = warp * 16 + 8 * n + 2 * r;
-          const uint2 kw = *reinterpret_cast<const uint2*>(sc + tok * 4);
-          const uint2 vw = *reinterpret_cast<const uint2*>(sc + G::kScaleBytes + tok * 4);
-          const uint32_t kws[2] = {kw.x, kw.y}, vws[2] = {vw.x, vw.y};
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float sv;
-            if constexpr (G::kU4) {
-              sk[2 * n + i] = __half2float(__ushort_as_half(static_cast<unsigned short>(kws[i] & 0xffffu)));
-              sv = __half2float(__ushort_as_half(static_cast<unsigned short>(vws[i] & 0xffffu)));
-            } else {
-              sk[2 * n + i] = __uint_as_float(kws[i]);
-              sv = __uint_as_float(vws[i]);
-            }
-            lsv[2 * n + i] = lg2(sv);
-            rsv[2 * n + i] = __frcp_rn(sv);
-          }
-          if constexpr (G::kU4) {
-            // a zero-point that is not one (its token is not seen) becomes 0: what is not seen has to stay finite
-            const uint32_t z = __byte_perm(vw.x, vw.y, 0x7632);
-            const __half2 zz = __hmin2(__hmax2(*reinterpret_cast<const __half2*>(&z), __float2half2_rn(0.0f)),
-                                       __float2half2_rn(15.0f));
-            const __half2 b = __hadd2(zz, __float2half2_rn(1024.0f));
-            vz[n] = *reinterpret_cast<const uint32_t*>(&b);
-          }
+      for (int n = 0; n < 4; ++n) {
+        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+        const int tok = 8 * n + g;
+        uint32_t kz = 0;
+        if constexpr (G::kU4) {
+          const uint32_t kw = *reinterpret_cast<const uint32_t*>(sc + tok * 4);
+          const __half2 b = __hadd2(__half2half2(__ushort_as_half(static_cast<unsigned short>(kw >> 16))),
+                                    __float2half2_rn(1024.0f));
+          kz = *reinterpret_cast<const uint32_t*>(&b);
         }
-
-        // scores of 16 rows x 16 tokens
-        float s[2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-          const int tok = warp * 16 + 8 * n + g;
-          uint32_t kz = 0;
-          if constexpr (G::kU4) {
-            const uint32_t kw = *reinterpret_cast<const uint32_t*>(sc + tok * 4);
-            const __half2 b = __hadd2(__half2half2(__ushort_as_half(static_cast<unsigned short>(kw >> 16))),
-                                      __float2half2_rn(1024.0f));
-            kz = *reinterpret_cast<const uint32_t*>(&b);
-          }
+        for (int h = 0; h < G::kSub; ++h) {
+          constexpr int kLoad = G::kKLane < 16 ? G::kKLane : 16;
 #pragma unroll
-          for (int h = 0; h < G::kSub; ++h) {
-            constexpr int kLoad = G::kKLane < 16 ? G::kKLane : 16;
+          for (int c = 0; c < G::kKLane / kLoad; ++c) {
+            uint32_t wd[4];
+            const int byte = r * G::kKLane + c * 16;
+            lds<kLoad>(ks_at + h * G::kSubBytes + G::chunk(tok, byte / 16) + byte % 16, wd);
 #pragma unroll
-            for (int c = 0; c < G::kKLane / kLoad; ++c) {
-              uint32_t wd[4];
-              const int byte = r * G::kKLane + c * 16;
-              lds<kLoad>(ks_at + h * G::kSubBytes + G::chunk(tok, byte / 16) + byte % 16, wd);
-#pragma unroll
-              for (int i = 0; i < kLoad / 4; ++i) {
-                if constexpr (G::kU4) {
-                  const int ks = h * (G::kPerSub / 16) + (c * (kLoad / 4) + i) * 2;
-                  const uint32_t x0 = hsub2((wd[i] & 0x000f000fu) | kMagic, kz);
-                  const uint32_t x1 = hsub2(((wd[i] >> 4) & 0x000f000fu) | kMagic, kz);
-                  const uint32_t x2 = hsub2(((wd[i] >> 8) & 0x000f000fu) | kMagic, kz);
-                  const uint32_t x3 = hsub2(((wd[i] >> 12) & 0x000f000fu) | kMagic, kz);
-                  mma16816(s[n], qa[ks], x0, x1);
-                  mma16816(s[n], qa[ks + 1], x2, x3);
-                } else {
-                  const int ks = h * (G::kPerSub / 16) + c * (kLoad / 4) + i;
-                  uint32_t lo, hi;
-                  widen4<FMT>(wd[i], lo, hi);
-                  mma16816(s[n], qa[ks], lo, hi);
-                }
+            for (int i = 0; i < kLoad / 4; ++i) {
+              if constexpr (G::kU4) {
+                const int ks = h * (G::kPerSub / 16) + (c * (kLoad / 4) + i) * 2;
+                const uint32_t x0 = hsub2((wd[i] & 0x000f000fu) | kMagic, kz);
+                const uint32_t x1 = hsub2(((wd[i] >> 4) & 0x000f000fu) | kMagic, kz);
+                const uint32_t x2 = hsub2(((wd[i] >> 8) & 0x000f000fu) | kMagic, kz);
+                const uint32_t x3 = hsub2(((wd[i] >> 12) & 0x000f000fu) | kMagic, kz);
+                mma16816(s[n], qa[ks], x0, x1);
+                mma16816(s[n], qa[ks + 1], x2, x3);
+              } else {
+                const int ks = h * (G::kPerSub / 16) + c * (kLoad / 4) + i;
+                uint32_t lo, hi;
+                widen4<FMT>(wd[i], lo, hi);
+                mma16816(s[n], qa[ks], lo, hi);
               }
             }
           }
         }
+      }
 
-        // t, hiding what a row does not see
+      // t, hiding what a row does not see
+      float rsv[8];
+      uint32_t vz[4];  // U4: 1024 + the zero-points of the tokens, per pair
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 4; ++n) {
+        const int tok = 8 * n + 2 * r;
+        const uint2 kw = *reinterpret_cast<const uint2*>(sc + tok * 4);
+        const uint2 vw = *reinterpret_cast<const uint2*>(sc + G::kScaleBytes + tok * 4);
+        const uint32_t kws[2] = {kw.x, kw.y}, vws[2] = {vw.x, vw.y};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s[n][i] = fmaf(s[n][i] * row_scale[i >> 1], sk[2 * n + (i & 1)], lsv[2 * n + (i & 1)]);
-        if (j0 + 16 > w.s.ctx) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int j = j0 + 8 * n + 2 * r + (i & 1) - w.s.ctx;  // the node that the token is
-              const int node = row_node[i >> 1];
-              bool seen = j < 0;
-              if (!seen && j < w.s.nodes && node >= 0)
-                seen = p.mask == nullptr
-                           ? j <= node
-                           : ((p.mask[(w.s.q_row + node) * p.mask_words + (j >> 6)] >> (j & 63)) & 1) != 0;
-              if (!seen) s[n][i] = -INFINITY;
-            }
-        }
-
-        // move the reference where t leaves it behind
-        const float top0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        const float top1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-        if (__any_sync(0xffffffffu, top0 > m[0] + kSlack || top1 > m[1] + kSlack)) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float top = i == 0 ? top0 : top1;
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float to = fmaxf(m[i], top);
-            const float keep = m[i] == -INFINITY ? 0.0f : ex2(m[i] - to);
-            m[i] = to;
-            l[i] *= keep;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              o[c][2 * i] *= keep;
-              o[c][2 * i + 1] *= keep;
-            }
+        for (int i = 0; i < 2; ++i) {
+          float sk, sv;
+          if constexpr (G::kU4) {
+            sk = __half2float(__ushort_as_half(static_cast<unsigned short>(kws[i] & 0xffffu)));
+            sv = __half2float(__ushort_as_half(static_cast<unsigned short>(vws[i] & 0xffffu)));
+          } else {
+            sk = __uint_as_float(kws[i]);
+            sv = __uint_as_float(vws[i]);
           }
+          const float lsv = lg2(sv);
+          rsv[2 * n + i] = rcp(sv);
+          s[n][i] = fmaf(s[n][i] * row_scale[0], sk, lsv);
+          s[n][2 + i] = fmaf(s[n][2 + i] * row_scale[1], sk, lsv);
         }
-        const float ref0 = m[0] == -INFINITY ? 0.0f : m[0] - kOffset;
-        const float ref1 = m[1] == -INFINITY ? 0.0f : m[1] - kOffset;
-        uint32_t pa[4], pb[4];
-        bool small = false;
+        if constexpr (G::kU4) {
+          const uint32_t z = __byte_perm(vw.x, vw.y, 0x7632);
+          // a zero-point that is not one (its token is not seen) becomes 0: what is not seen has to stay finite
+          const __half2 zz = __hmin2(__hmax2(*reinterpret_cast<const __half2*>(&z), __float2half2_rn(0.0f)),
+                                     __float2half2_rn(15.0f));
+          const __half2 b = __hadd2(zz, __float2half2_rn(1024.0f));
+          vz[n] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+      }
+      if (masked) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float e[4];
+        for (int n = 0; n < 4; ++n) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            e[i] = ex2(s[n][i] - (i < 2 ? ref0 : ref1));
-            // a hidden token adds nothing, whatever its scale is
-            l[i >> 1] += e[i] == 0.0f ? 0.0f : e[i] * rsv[2 * n + (i & 1)];
-            small = small || (e[i] > 0.0f && e[i] < kHalfNormal);
+            const int j = j0 + 8 * n + 2 * r + (i & 1) - w.s.ctx;  // the node that the token is
+            const int node = row_node[i >> 1];
+            bool seen = j < 0;
+            if (!seen && j < w.s.nodes && node >= 0)
+              seen = p.mask == nullptr
+                         ? j <= node
+                         : ((p.mask[(w.s.q_row + node) * p.mask_words + (j >> 6)] >> (j & 63)) & 1) != 0;
+            if (!seen) s[n][i] = -INFINITY;
           }
-          pa[2 * n] = kv::pack2<0>(e[0], e[1]);
-          pa[2 * n + 1] = kv::pack2<0>(e[2], e[3]);
-          s[n][0] = e[0], s[n][1] = e[1], s[n][2] = e[2], s[n][3] = e[3];
-        }
-        small = __any_sync(0xffffffffu, small);
-        if (small) {  // those below fp16's normal range apart, times 2^kShift
+          // a hidden token adds nothing to l, whatever its scale is; one that is seen makes t a NaN with it
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float x = s[n][2 * h], y = s[n][2 * h + 1];
-              const bool u = x < kHalfNormal, v = y < kHalfNormal;
-              pa[2 * n + h] = kv::pack2<0>(u ? 0.0f : x, v ? 0.0f : y);
-              pb[2 * n + h] = kv::pack2<0>(u ? x * G::kShiftUp : 0.0f, v ? y * G::kShiftUp : 0.0f);
-            }
+          for (int i = 0; i < 2; ++i)
+            if (!(rsv[2 * n + i] < INFINITY)) rsv[2 * n + i] = 0.0f;
         }
+      }
 
-        // p . v: the lane's four tokens 2 r + {0, 1, 8, 9}, contiguous channels of each
-        const bool tail = j0 + 16 > w.s.len;
-        auto accumulate = [&](const uint32_t* pr, auto shifted) {
-          constexpr bool kShifted = decltype(shifted)::value;
+      // move the reference where t leaves it behind
+      float hi[2], lo[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        hi[i] = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
+        lo[i] = fminf(s[0][2 * i], s[0][2 * i + 1]);
+#pragma unroll
+        for (int n = 1; n < 4; ++n) {
+          hi[i] = fmaxf(hi[i], fmaxf(s[n][2 * i], s[n][2 * i + 1]));
+          lo[i] = fminf(lo[i], fminf(s[n][2 * i], s[n][2 * i + 1]));
+        }
+      }
+      if (__any_sync(0xffffffffu, fmaxf(hi[0] - ref[0], hi[1] - ref[1]) > kOffset + kSlack)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float top = hi[i];
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float to = fmaxf(ref[i], top - kOffset);
+          const float keep = ex2(ref[i] - to);
+          ref[i] = to;
+          l[i] *= keep;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            o[c][2 * i] *= keep;
+            o[c][2 * i + 1] *= keep;
+          }
+        }
+      }
+      const bool small = __any_sync(0xffffffffu, fminf(lo[0] - ref[0], lo[1] - ref[1]) < kHalfExp);
+      uint32_t pa[4][2];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[n][i] = ex2(s[n][i] - ref[i >> 1]);
+          l[i >> 1] = fmaf(s[n][i], rsv[2 * n + (i & 1)], l[i >> 1]);
+        }
+        pa[n][0] = kv::pack2<0>(s[n][0], s[n][1]);
+        pa[n][1] = kv::pack2<0>(s[n][2], s[n][3]);
+      }
+
+      // p . v: the lane's tokens 16 k + 2 r + {0, 1, 8, 9}, contiguous channels of each
+      const bool tail = j0 + kTile > w.s.len;
+      auto accumulate = [&](auto shifted) {
+        constexpr bool kShifted = decltype(shifted)::value;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t pr[4] = {pa[2 * k][0], pa[2 * k][1], pa[2 * k + 1][0], pa[2 * k + 1][1]};
           auto product = [&](float* acc, uint32_t b0, uint32_t b1) {
             if constexpr (kShifted) {
               b0 = hmul2(b0, G::kShiftDown);
@@ -609,12 +635,12 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
             uint32_t wd[4][kLoad / 4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int tok = warp * 16 + 2 * r + (i & 1) + 8 * (i >> 1);
+              const int tok = 16 * k + 2 * r + (i & 1) + 8 * (i >> 1);
               const int byte = g * kLoad;
               lds<kLoad>(vs_at + h * G::kSubBytes + G::chunk(tok, byte / 16) + byte % 16, wd[i]);
               if constexpr (FMT == QLIN_KV_E4M3) {
                 // beyond the sequence's end lies anything, E4M3 NaN among it
-                if (tail && t * kTile + tok >= w.s.len) {
+                if (tail && j0 + tok >= w.s.len) {
 #pragma unroll
                   for (int c = 0; c < kLoad / 4; ++c) wd[i][c] = 0u;
                 }
@@ -629,8 +655,9 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
                   const uint32_t a = __byte_perm(wd[0][c], wd[1][c], sel), b = __byte_perm(wd[2][c], wd[3][c], sel);
 #pragma unroll
                   for (int i = 0; i < 4; ++i)
-                    product(o[h * G::kNPerSub + 8 * c + 4 * half + i], hsub2(((a >> (4 * i)) & 0x000f000fu) | kMagic, vz[0]),
-                            hsub2(((b >> (4 * i)) & 0x000f000fu) | kMagic, vz[1]));
+                    product(o[h * G::kNPerSub + 8 * c + 4 * half + i],
+                            hsub2(((a >> (4 * i)) & 0x000f000fu) | kMagic, vz[2 * k]),
+                            hsub2(((b >> (4 * i)) & 0x000f000fu) | kMagic, vz[2 * k + 1]));
                 }
               } else {
 #pragma unroll
@@ -646,17 +673,28 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
               }
             }
           }
-        };
-        accumulate(pa, std::false_type{});
-        if (small) accumulate(pb, std::true_type{});
+        }
+      };
+      if (small) {
+        // some lie below fp16's normal range: these times 2^kShift first, then the others
+        uint32_t rest[4][2];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float a = s[n][2 * h], b = s[n][2 * h + 1];
+            rest[n][h] = kv::pack2<0>(a < kHalfNormal ? 0.0f : a, b < kHalfNormal ? 0.0f : b);
+            pa[n][h] = kv::pack2<0>(a < kHalfNormal ? a * G::kShiftUp : 0.0f, b < kHalfNormal ? b * G::kShiftUp : 0.0f);
+          }
+        accumulate(std::true_type{});
+#pragma unroll
+        for (int n = 0; n < 4; ++n) pa[n][0] = rest[n][0], pa[n][1] = rest[n][1];
       }
+      accumulate(std::false_type{});
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar_free + 8 * stage);
-      if (++stage == G::kStages) {
-        stage = 0;
-        phase ^= 1;
-      }
     }
+    unit0 += w.tiles;
 
     // join the warps: each scaled to the common reference
     float* area = reinterpret_cast<float*>(smem + G::kOffMerge);
@@ -665,7 +703,8 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (r == 0) ml[warp * kRows + g + 8 * i] = make_float2(m[i], l[i]);
+      if (r == 0) ml[warp * kRows + g + 8 * i] = make_float2(ref[i] == kNoRef ? -INFINITY : ref[i] + kOffset, l[i]);
+      if (!took) continue;
       float* to = area + (warp * kRows + g + 8 * i) * G::kMergeRow;
 #pragma unroll
       for (int h = 0; h < G::kSub; ++h)
@@ -698,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, Geo<FMT, D>::kBlocksPerSm)
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        // a warp that saw nothing has o = l = 0, or NaN from a query that is NaN: pass that on
+        // a warp that saw nothing has o = l = 0 (and may not have written o), or NaN where the query is NaN
+        if (e[i].x == -INFINITY && e[i].y == 0.0f) continue;
         const float f = e[i].x == -INFINITY ? 1.0f : ex2(e[i].x - top);
         const float4 v = *reinterpret_cast<const float4*>(area + (i * kRows + row) * G::kMergeRow + c);
         sum += f * e[i].y;
@@ -812,7 +852,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   cudaError_t e = ensure_max_dynamic_smem(fn);
   if (e != cudaSuccess) return e;
   const unsigned blocks = static_cast<unsigned>(grid_blocks(D));
-  tree_attention_kernel<FMT, D><<<blocks, kThreads, G::kSmem, stream>>>(p);
+  tree_attention_kernel<FMT, D><<<blocks, G::kThreads, G::kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
