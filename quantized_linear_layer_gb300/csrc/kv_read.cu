@@ -1,14 +1,14 @@
 // Reads tokens of a paged, quantized cache back as 16-bit rows: a gather with
 // dequantization, bound by HBM (codes and scales in, 16-bit rows out).
 //
-// A block takes kTokens output rows: its first threads resolve each to its
-// place in the cache (a binary search of the row's sequence, then the page
-// number), once for all heads; then groups of D / 8 lanes walk the heads,
-// eight elements per lane, so that a lane's code load is 8 bytes (4 for U4)
-// and its store 16, and kUnroll rows of keys and values are in flight per
-// thread.  Consecutive groups take consecutive tokens of one head: the codes
-// of a page are contiguous per head, the outputs are whole 128-byte lines or
-// more either way.
+// A block takes kTokens output rows x the heads that make one pass of its
+// threads: groups of D / 8 lanes take a (token, head) each, eight elements per
+// lane, so that a lane's code load is 8 bytes (4 for U4) and its store 16, with
+// kUnroll rows of keys and values in flight per thread.  A warp per token first
+// finds the row's sequence (32 bounds per probe) and its place in the cache.
+// Consecutive groups take consecutive tokens of one head: the codes of a page
+// are contiguous per head, the outputs are whole 128-byte lines or more either
+// way.  Small blocks of one pass fill the GPU from a few hundred rows on.
 #include "kv_common.cuh"
 #include "qlin_internal.h"
 
@@ -16,7 +16,7 @@ namespace qlin {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 32;
+constexpr int kTokens = 8;  // one per warp
 constexpr int kUnroll = 4;
 
 struct Params {
@@ -73,32 +73,43 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kTokens;
   const int count = static_cast<int>(min(static_cast<int64_t>(kTokens), p.rows - row0));
 
-  if (threadIdx.x < count) {
-    const int64_t row = row0 + threadIdx.x;
-    int lo = 0, hi = p.B;  // the last sequence that starts at or before `row`
+  const int warp = threadIdx.x / 32;
+  if (warp < count) {
+    const int l = threadIdx.x % 32;
+    const int64_t row = row0 + warp;
+    int lo = 0, hi = p.B;  // the last sequence that begins at or before `row` is in [lo, hi)
     while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (p.indptr[mid] <= row) lo = mid; else hi = mid;
+      const int step = (hi - lo + 31) / 32;
+      const int b = lo + l * step;
+      const unsigned before = __ballot_sync(0xffffffffu, b < hi && p.indptr[b] <= row);
+      const int n = before == 0 ? 0 : 31 - __clz(before);
+      lo += n * step;
+      hi = min(hi, lo + step);
     }
-    int64_t at = -1;
-    if (p.indptr[lo] <= row && row < p.indptr[lo + 1]) {
-      const int64_t pos = static_cast<int64_t>(p.starts[lo]) + (row - p.indptr[lo]);
-      const int64_t n = pos >> p.cache.page_shift;
-      if (pos >= 0 && n < p.max_pages) {
-        const int32_t page = p.table[lo * p.max_pages + n];
-        if (page >= 0 && page < p.cache.pages)
-          at = (static_cast<int64_t>(page) << p.cache.page_shift) | (pos & ((int64_t(1) << p.cache.page_shift) - 1));
+    if (l == 0) {
+      int64_t at = -1;
+      if (p.indptr[lo] <= row && row < p.indptr[lo + 1]) {
+        const int64_t pos = static_cast<int64_t>(p.starts[lo]) + (row - p.indptr[lo]);
+        const int64_t n = pos >> p.cache.page_shift;
+        if (pos >= 0 && n < p.max_pages) {
+          const int32_t page = p.table[lo * p.max_pages + n];
+          if (page >= 0 && page < p.cache.pages)
+            at = (static_cast<int64_t>(page) << p.cache.page_shift) | (pos & ((int64_t(1) << p.cache.page_shift) - 1));
+        }
       }
+      if (at < 0) record_device_error(p.err, kDevErrBadIndex);
+      place[warp] = at;
     }
-    if (at < 0) record_device_error(p.err, kDevErrBadIndex);
-    place[threadIdx.x] = at;
   }
   __syncthreads();
 
   const int lane = threadIdx.x % LANES;
   const int group = threadIdx.x / LANES;
-  const int items = count * p.cache.heads;
-  for (int i0 = group; i0 < items; i0 += kGroups * kUnroll) {
+  constexpr int kHeads = kGroups * kUnroll / kTokens;  // heads of a block
+  const int head0 = blockIdx.y * kHeads;
+  const int items = count * min(kHeads, p.cache.heads - head0);
+  {
+    const int i0 = group;
     uint2 kc[kUnroll], vc[kUnroll];
     uint32_t ks[kUnroll], vs[kUnroll];
     int tok[kUnroll], head[kUnroll];
@@ -107,6 +118,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
       const int i = i0 + u * kGroups;
       head[u] = i / count;
       tok[u] = i - head[u] * count;
+      head[u] += head0;
       kc[u] = vc[u] = make_uint2(0u, 0u);
       ks[u] = vs[u] = 0u;
       if (i >= items) continue;
@@ -139,7 +151,9 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
 
 template <int DT, int D>
 cudaError_t launch(const Params& p, int fmt, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((p.rows + kTokens - 1) / kTokens));
+  constexpr int kHeads = kThreads / (D / 8) * kUnroll / kTokens;
+  const dim3 grid(static_cast<unsigned>((p.rows + kTokens - 1) / kTokens),
+                  static_cast<unsigned>((p.cache.heads + kHeads - 1) / kHeads));
   if (fmt == QLIN_KV_INT8) kv_read_kernel<DT, D, QLIN_KV_INT8><<<grid, kThreads, 0, stream>>>(p);
   else if (fmt == QLIN_KV_E4M3) kv_read_kernel<DT, D, QLIN_KV_E4M3><<<grid, kThreads, 0, stream>>>(p);
   else kv_read_kernel<DT, D, QLIN_KV_U4><<<grid, kThreads, 0, stream>>>(p);

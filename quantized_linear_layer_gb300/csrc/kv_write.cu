@@ -4,9 +4,9 @@
 // A row is one head of one token, D 16-bit elements, held by D / 8 lanes of
 // eight elements (one 16-byte load each).  A block takes kRows consecutive
 // rows of the flat (token, head) order per step: D / 8 lanes x kUnroll rows
-// per lane group, whose loads are all issued before the block works out the
-// angles of the tokens they belong to, so that the angles (a few dozen
-// integer and special-function instructions) hide under the loads.
+// per lane group.  A step issues its loads, then works out the angles of the
+// next step's tokens into the other of two buffers while they are under way,
+// then finishes its rows; one barrier a step.
 //
 // Angles: a position times inv_freq, modulo a full turn.  The frequency in
 // turns is kept as a 64-bit fraction (worked out once per block in float64);
@@ -17,8 +17,12 @@
 // small fraction of the float32 rate here).
 //
 // The mean of squares, the norm, the rotation and the scales are float32; a
-// row is rounded once, to its 16-bit output or to its codes.  The kernel is
-// bound by HBM from about a thousand tokens on, by launch latency below.
+// row is rounded once, to its 16-bit output or to its codes.  Integer codes
+// are rounded by adding 1.5 x 2^23 (nearest even, the code in the low bits),
+// which is the float-to-integer conversion at the rate of an addition.  The
+// kernel is bound by HBM from about a thousand tokens on, by launch latency
+// below.
+#include <algorithm>
 #include <cmath>
 
 #include "kv_common.cuh"
@@ -29,6 +33,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // rows per lane group and step: 64 bytes in flight per thread
+constexpr float kRoundMagic = 12582912.0f;  // 1.5 x 2^23
 constexpr float kScaleFloor = 5.42101086e-20f;  // 2^-64
 
 struct Params {
@@ -39,12 +44,15 @@ struct Params {
   uint8_t* k_out;
   int64_t qt, qh, kt, kh, vt, vh, qot, qoh, kot, koh;  // strides in bytes
   int32_t hq, hk, hv;  // heads of q, k and v (0: absent)
+  int32_t heads;       // their sum
+  uint32_t magic;      // ceil(2^32 / heads) where at x magic / 2^32 is exact for every `at` of a step, or 0
   int64_t T;
   const int64_t* positions;
   const double* inv_freq;
   const void* q_gamma;
   const void* k_gamma;
   int32_t half_rot, interleaved;
+  int32_t step_tokens;  // tokens that one step of a block can touch
   float eps;
   const int64_t* slots;
   kv::CacheView cache;
@@ -57,6 +65,13 @@ __device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
+}
+
+// x / d rounded to nearest even from r = __frcp_rn(d), as div_by_rcp, but for
+// the sign of a quotient of zero.
+__device__ __forceinline__ float divide(float x, float d, float r) {
+  const float q = __fmul_rn(x, r);
+  return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
 }
 
 // Quantizes the row held by this group of lanes (eight values each) and
@@ -85,12 +100,13 @@ __device__ __forceinline__ void quantize_row(const float* y, int lane, bool writ
     const __half s16 = __float2half_rn(fminf(__fdiv_rn(span, 15.0f), 65504.0f));
     const float s = __half2float(s16);  // at least the fp16 nearest 1e-5 / 15, a normal float32
     const float r = __frcp_rn(s);
-    const float z = fminf(fmaxf(rintf(div_by_rcp(-lo, s, r)), 0.0f), 15.0f);
+    const float z = fminf(fmaxf(rintf(divide(-lo, s, r)), 0.0f), 15.0f);
+    // rint(y / s) + z in [0, 15]: the clamp first (z is an integer), the rounding and + z in the magic sum
     uint32_t packed = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float n = fminf(fmaxf(rintf(div_by_rcp(y[i], s, r)) + z, 0.0f), 15.0f);
-      packed |= static_cast<uint32_t>(static_cast<int>(n)) << (4 * i);
+      const float n = fminf(fmaxf(divide(y[i], s, r), -z), 15.0f - z);
+      packed |= (__float_as_uint((n + kRoundMagic) + z) & 15u) << (4 * i);
     }
     if (write) {
       *reinterpret_cast<uint32_t*>(codes + 4 * lane) = finite ? packed : 0u;
@@ -110,12 +126,16 @@ __device__ __forceinline__ void quantize_row(const float* y, int lane, bool writ
     for (int h = 0; h < 2; ++h) {
       float n[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n[i] = div_by_rcp(y[4 * h + i], s, r);
+      for (int i = 0; i < 4; ++i) n[i] = divide(y[4 * h + i], s, r);
       if constexpr (FMT == QLIN_KV_INT8) {
-        w[h] = 0;
+        uint32_t u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[h] |= (static_cast<uint32_t>(__float2int_rn(n[i])) & 0xffu) << (8 * i);
+        for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(n[i] + kRoundMagic);
+        w[h] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
       } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // a quotient that is zero keeps the sign of y
+          n[i] = __uint_as_float((__float_as_uint(n[i]) & 0x7fffffffu) | (__float_as_uint(y[4 * h + i]) & 0x80000000u));
         w[h] = kv::floats_to_e4m3x2(n[0], n[1]) | (kv::floats_to_e4m3x2(n[2], n[3]) << 16);
       }
     }
@@ -132,24 +152,59 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_
   constexpr int LANES = D / 8;
   constexpr int kGroups = kThreads / LANES;
   constexpr int kRows = kGroups * kUnroll;
+  // [D / 2 fractions of a turn][gammas of q and k as float, D each][two buffers of angles]
   extern __shared__ __align__(16) uint8_t smem[];
-  uint64_t* freq = reinterpret_cast<uint64_t*>(smem);                 // [half_rot] fractions of a turn
-  float2* trig = reinterpret_cast<float2*>(freq + p.half_rot);        // [tokens of a step][half_rot] (cos, sin)
+  uint64_t* freq = reinterpret_cast<uint64_t*>(smem);
+  float* gammas = reinterpret_cast<float*>(freq + D / 2);
+  float* trig = gammas + 2 * D;
+  const int per_token = 2 * p.half_rot;  // cosines, then sines; see trig_at
+  const int per_buffer = per_token * p.step_tokens;
 
   const int lane = threadIdx.x % LANES;
   const int group = threadIdx.x / LANES;
-  const int heads = p.hq + p.hk + p.hv;
-  const int64_t rows = p.T * heads;
+  const int64_t rows = p.T * p.heads;
+  const bool normed = p.q_gamma != nullptr || p.k_gamma != nullptr;
 
   for (int i = threadIdx.x; i < p.half_rot; i += kThreads) {
     const double turns = p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
     freq[i] = static_cast<uint64_t>((turns - floor(turns)) * 18446744073709551616.0);
   }
+  if (normed) {
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+      const void* from = i < D ? p.q_gamma : p.k_gamma;
+      if (from != nullptr) gammas[i] = load_elem<DT>(from, i < D ? i : i - D);
+    }
+  }
+  // Where the cosine of frequency i lies in a token's block (its sine half_rot behind).  Halves: the four
+  // that a lane reads at once are together, lanes 16 bytes apart, free of bank conflicts.
+  auto trig_at = [&](int i) {
+    return p.interleaved ? i : ((i >> 2) & 1) * (p.half_rot / 2) + (i >> 3) * 4 + (i & 3);
+  };
+  auto angles = [&](int64_t row0, float* to) {
+    const int64_t t0 = row0 / p.heads;
+    const int64_t last = min(rows - 1, row0 + kRows - 1) / p.heads;
+    const int count = static_cast<int>(last - t0 + 1) * p.half_rot;
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+      const int j = i / p.half_rot, f = i - j * p.half_rot;
+      const uint64_t turn = static_cast<uint64_t>(p.positions[t0 + j]) * freq[f];
+      float s, c;  // the fraction of a turn, as a signed number of half turns
+      sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 1.08420217e-19f, &s, &c);  // 2^-63
+      float* at = to + j * per_token + trig_at(f);
+      at[0] = c;
+      at[p.half_rot] = s;
+    }
+  };
 
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < rows;
-       row0 += static_cast<int64_t>(gridDim.x) * kRows) {
-    const int64_t t0 = row0 / heads;
-    const int32_t h0 = static_cast<int32_t>(row0 - t0 * heads);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  if (p.half_rot > 0 || normed) __syncthreads();  // freq and gammas are there
+  if (p.half_rot > 0) {
+    angles(row0, trig);
+    __syncthreads();
+  }
+  for (int buffer = 0; row0 < rows; row0 += stride, buffer ^= 1) {
+    const int64_t t0 = row0 / p.heads;
+    const int32_t h0 = static_cast<int32_t>(row0 - t0 * p.heads);
 
     int32_t tok[kUnroll], head[kUnroll];  // token after t0; head in the order q, k, v (-1: no row)
     uint4 raw[kUnroll];
@@ -157,8 +212,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int32_t at = h0 + group + u * kGroups;
-      tok[u] = at / heads;
-      head[u] = at - tok[u] * heads;
+      tok[u] = p.magic == 0 ? at / p.heads : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(at), p.magic));
+      head[u] = at - tok[u] * p.heads;
       slot[u] = -1;
       raw[u] = make_uint4(0u, 0u, 0u, 0u);
       const int64_t t = t0 + tok[u];
@@ -177,19 +232,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_
       }
     }
 
-    if (p.half_rot > 0) {
-      __syncthreads();  // freq written; the last step's angles are no longer read
-      const int64_t last = min(rows - 1, row0 + kRows - 1) / heads;
-      const int count = static_cast<int>(last - t0 + 1) * p.half_rot;
-      for (int i = threadIdx.x; i < count; i += kThreads) {
-        const int j = i / p.half_rot;
-        const uint64_t turn = static_cast<uint64_t>(p.positions[t0 + j]) * freq[i - j * p.half_rot];
-        float s, c;  // the fraction of a turn, as a signed number of half turns
-        sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 1.08420217e-19f, &s, &c);  // 2^-63
-        trig[i] = make_float2(c, s);
-      }
-      __syncthreads();
-    }
+    if (p.half_rot > 0 && row0 + stride < rows) angles(row0 + stride, trig + (buffer ^ 1) * per_buffer);
 
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -199,33 +242,35 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_
       float y[8];
       kv::unpack8<DT>(raw[u], y);
 
-      const void* gamma = is_q ? p.q_gamma : is_k ? p.k_gamma : nullptr;
-      if (p.q_gamma != nullptr || p.k_gamma != nullptr) {  // uniform: the shuffles below need every lane
+      if (normed) {  // uniform: the shuffles below need every lane
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (gamma != nullptr) {
-          const float inv = __frcp_rn(__fsqrt_rn(ss * (1.0f / D) + p.eps));
-          float g[8];
-          kv::unpack8<DT>(ldg_v4(static_cast<const uint8_t*>(gamma) + lane * 16), g);
+        if ((is_q && p.q_gamma != nullptr) || (is_k && p.k_gamma != nullptr)) {
+          const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
+          const float4* g4 = reinterpret_cast<const float4*>(gammas + (is_q ? 0 : D) + lane * 8);
+          const float4 ga = g4[0], gb = g4[1];
+          const float g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * g[i];
         }
       }
 
       if (p.half_rot > 0) {
-        const float2* cs = trig + tok[u] * p.half_rot;
-        const int c0 = lane * 8;  // this lane's first channel
+        const float* cs = trig + buffer * per_buffer + tok[u] * per_token;
         if (p.interleaved) {
-          if ((is_q || is_k) && c0 < 2 * p.half_rot) {
+          const int c0 = lane * 4;  // this lane's first frequency
+          if ((is_q || is_k) && c0 < p.half_rot) {
+            const float4 c = *reinterpret_cast<const float4*>(cs + c0);
+            const float4 s = *reinterpret_cast<const float4*>(cs + p.half_rot + c0);
+            const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 f = cs[c0 / 2 + i];
               const float a = y[2 * i], b = y[2 * i + 1];
-              y[2 * i] = a * f.x - b * f.y;
-              y[2 * i + 1] = b * f.x + a * f.y;
+              y[2 * i] = a * cc[i] - b * sn[i];
+              y[2 * i + 1] = b * cc[i] + a * sn[i];
             }
           }
         } else {
@@ -236,9 +281,16 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, y[i], from);
           if ((is_q || is_k) && (first || second)) {
-            const float2* f = cs + (first ? c0 : c0 - p.half_rot);
+            const float* at = cs + 4 * (first ? lane : lane - step);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = y[i] * f[i].x + (first ? -o[i] : o[i]) * f[i].y;
+            for (int h = 0; h < 2; ++h) {
+              const float4 c = *reinterpret_cast<const float4*>(at + h * (p.half_rot / 2));
+              const float4 s = *reinterpret_cast<const float4*>(at + h * (p.half_rot / 2) + p.half_rot);
+              const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[4 * h + i] = y[4 * h + i] * cc[i] + (first ? -o[4 * h + i] : o[4 * h + i]) * sn[i];
+            }
           }
         }
       }
@@ -265,18 +317,21 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_
         }
       }
     }
+    if (p.half_rot > 0) __syncthreads();
   }
 }
 
 template <int DT, int D>
-cudaError_t launch(const Params& p, int fmt, cudaStream_t stream) {
+cudaError_t launch(Params p, int fmt, cudaStream_t stream) {
   constexpr int kRows = kThreads / (D / 8) * kUnroll;
-  const int64_t heads = p.hq + p.hk + p.hv;
-  const int64_t steps = (p.T * heads + kRows - 1) / kRows;
+  p.heads = p.hq + p.hk + p.hv;
+  p.magic = p.heads > 1 && p.heads <= 16384 ? static_cast<uint32_t>(((uint64_t(1) << 32) + p.heads - 1) / p.heads) : 0;
+  const int64_t steps = (p.T * p.heads + kRows - 1) / kRows;
   // tokens that one step can touch
-  const int64_t tokens = heads >= kRows ? 2 : (kRows + heads - 2) / heads + 1;
-  const size_t smem = p.half_rot * (8 + 8 * static_cast<size_t>(tokens));
-  const int64_t grid = steps < sm_count() * 6 ? steps : sm_count() * 6;
+  p.step_tokens = p.heads >= kRows ? 2 : (kRows + p.heads - 2) / p.heads + 1;
+  const int64_t grid = std::min<int64_t>(steps, sm_count() * 6);
+  const int buffers = steps > grid ? 2 : 1;
+  const size_t smem = D / 2 * 8 + 2 * D * 4 + 8 * static_cast<size_t>(p.half_rot) * p.step_tokens * buffers;
   const void* fn = fmt < 0                ? reinterpret_cast<const void*>(norm_rope_write_kernel<DT, D, -1>)
                    : fmt == QLIN_KV_INT8 ? reinterpret_cast<const void*>(norm_rope_write_kernel<DT, D, QLIN_KV_INT8>)
                    : fmt == QLIN_KV_E4M3 ? reinterpret_cast<const void*>(norm_rope_write_kernel<DT, D, QLIN_KV_E4M3>)
@@ -285,7 +340,7 @@ cudaError_t launch(const Params& p, int fmt, cudaStream_t stream) {
     const cudaError_t e = ensure_max_dynamic_smem(fn);
     if (e != cudaSuccess) return e;
   }
-  void* args[] = {const_cast<Params*>(&p)};
+  void* args[] = {&p};
   return cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kThreads), args, smem, stream);
 }
 

@@ -856,7 +856,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, kRows);
+  cfg.gridDim = dim3(blocks, static_cast<unsigned>(std::min<int64_t>(kRows, static_cast<int64_t>(p.max_nodes) * p.group)));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
