@@ -150,6 +150,14 @@ typedef struct {
   int fmt;                    /* qlin_kv_fmt */
 } qlin_kv_cache;
 
+/* A checked call of one of the entry points below that have a _prepare form,
+   kept by the caller in host memory: qlin_call_run makes the call as often as
+   wanted.  It holds the device pointers and sizes it was given (and a plan of
+   the launches), no data.  Contents are private. */
+typedef struct {
+  uint64_t data[112];
+} qlin_call;
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* qlin_status_string(qlin_status status);
 
@@ -839,6 +847,12 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  *   max_nodes   1 .. 256 (mask NULL or not)
  *   workspace   qlin_tree_attention_workspace_bytes(...) bytes, 256-byte
  *               aligned, contents arbitrary; one call at a time may use it
+ *
+ * Each call has a _prepare form with the same arguments, which checks them
+ * and plans the launches into *call (host memory) without launching anything;
+ * qlin_call_run(call, stream) then launches, for decode loops whose buffers
+ * stay where they are.  The current device has to be the one of the
+ * preparation.
  * ---------------------------------------------------------------------- */
 qlin_status qlin_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* q_out,
                               const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D, const qlin_rope* rope,
@@ -861,6 +875,26 @@ qlin_status qlin_tree_attention(const qlin_heads* q, const qlin_heads* out, qlin
                                 const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B, const int64_t* mask,
                                 int64_t mask_words, int64_t max_nodes, float scale, float* lse, void* workspace,
                                 int64_t workspace_bytes, cudaStream_t stream);
+
+qlin_status qlin_qk_norm_rope_prepare(const qlin_heads* q, const qlin_heads* k, const qlin_heads* q_out,
+                                      const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D,
+                                      const qlin_rope* rope, qlin_call* call);
+qlin_status qlin_qk_norm_rope_cache_prepare(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v,
+                                            const qlin_heads* q_out, const qlin_heads* k_out, qlin_dtype dtype,
+                                            int64_t T, const qlin_rope* rope, const int64_t* slots,
+                                            const qlin_kv_cache* cache, qlin_call* call);
+qlin_status qlin_kv_cache_write_prepare(const qlin_heads* k, const qlin_heads* v, qlin_dtype dtype, int64_t T,
+                                        const int64_t* slots, const qlin_kv_cache* cache, qlin_call* call);
+qlin_status qlin_kv_cache_read_prepare(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                       const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows,
+                                       const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype,
+                                       qlin_call* call);
+qlin_status qlin_tree_attention_prepare(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
+                                        const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                        const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B,
+                                        const int64_t* mask, int64_t mask_words, int64_t max_nodes, float scale,
+                                        float* lse, void* workspace, int64_t workspace_bytes, qlin_call* call);
+qlin_status qlin_call_run(const qlin_call* call, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

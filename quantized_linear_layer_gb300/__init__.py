@@ -99,12 +99,19 @@ _SIGS = {
     "qlin_rmsnorm_quant_nvfp4": ([_P, _I32, _I64, _I64, _P, ctypes.c_float, _P, _I64, _I32, _P, _P, _P, _I32, _P],
                                  _I32),
     "qlin_qk_norm_rope": ([_P, _P, _P, _P, _I32, _I64, _I64, _P, _P], _I32),
+    "qlin_qk_norm_rope_prepare": ([_P, _P, _P, _P, _I32, _I64, _I64, _P, _P], _I32),
     "qlin_qk_norm_rope_cache": ([_P, _P, _P, _P, _P, _I32, _I64, _P, _P, _P, _P], _I32),
+    "qlin_qk_norm_rope_cache_prepare": ([_P, _P, _P, _P, _P, _I32, _I64, _P, _P, _P, _P], _I32),
     "qlin_kv_cache_write": ([_P, _P, _I32, _I64, _P, _P, _P], _I32),
+    "qlin_kv_cache_write_prepare": ([_P, _P, _I32, _I64, _P, _P, _P], _I32),
     "qlin_kv_cache_read": ([_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I32, _P], _I32),
+    "qlin_kv_cache_read_prepare": ([_P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _I32, _P], _I32),
     "qlin_tree_attention_workspace_bytes": ([_P, _I64, _I64, _I64], _I64),
     "qlin_tree_attention": ([_P, _P, _I32, _I64, _P, _P, _I64, _P, _P, _I64, _P, _I64, _I64, ctypes.c_float, _P, _P,
                              _I64, _P], _I32),
+    "qlin_tree_attention_prepare": ([_P, _P, _I32, _I64, _P, _P, _I64, _P, _P, _I64, _P, _I64, _I64, ctypes.c_float, _P,
+                                     _P, _I64, _P], _I32),
+    "qlin_call_run": ([_P, _P], _I32),
 }
 
 _lib = None
@@ -687,17 +694,22 @@ class _KvCache(ctypes.Structure):
 
 
 class QlinCall:
-    """One call of a C entry point with its arguments checked and marshalled
-    once: run() makes the call on the current (or the given) stream.  It holds
-    the tensors' device pointers, so it is valid while they are, and keeps the
-    tensors referenced; lengths, page numbers and places are read on the
-    device at every run."""
+    """One call of a C entry point, checked and planned once (the C struct qlin_call, made by the entry point's
+    _prepare form): run() launches it on the current (or the given) stream.  It holds the tensors' device pointers,
+    so it is valid while they are, and keeps the tensors referenced; lengths, page numbers and places are read on
+    the device at every run."""
 
-    def __init__(self, name, args, keep):
-        self._name, self._fn, self._args, self._keep = name, getattr(lib(), name), args, keep
+    def __init__(self, name, args, keep, device):
+        self._name, self._keep = name, keep
+        self._device = device.index if device.index is not None else _torch().cuda.current_device()
+        self._call = (ctypes.c_uint64 * 112)()
+        self._at = ctypes.cast(self._call, ctypes.c_void_p)
+        self._run = lib().qlin_call_run
+        self._stream = _torch()._C._cuda_getCurrentRawStream
+        _check(name, getattr(lib(), name + "_prepare")(*args, self._at))
 
     def run(self, stream=None):
-        status = self._fn(*self._args, _stream(stream))
+        status = self._run(self._at, self._stream(self._device) if stream is None else stream.cuda_stream)
         if status != 0:
             _check(self._name, status)
 
@@ -797,7 +809,7 @@ def _ref(struct):
 
 def qlin_qk_norm_rope_prepare(q, k, q_out, k_out, positions, inv_freq, q_gamma=None, k_gamma=None, eps=1e-6,
                               interleaved=False):
-    """qlin_qk_norm_rope's arguments checked and marshalled once (QlinCall.run)."""
+    """qlin_qk_norm_rope's arguments checked and its launches planned once (QlinCall.run)."""
     dtype, code = _half_dtype(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [T][heads][D]")
@@ -808,7 +820,7 @@ def qlin_qk_norm_rope_prepare(q, k, q_out, k_out, positions, inv_freq, q_gamma=N
              for n, x in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out))]
     rope = _rope(positions, inv_freq, q_gamma, k_gamma, eps, interleaved, dtype, d, t, q.device)
     return QlinCall("qlin_qk_norm_rope", (*map(_ref, parts), code, t, d, _ref(rope)),
-                    (parts, rope, q, k, q_out, k_out, positions, inv_freq, q_gamma, k_gamma))
+                    (parts, rope, q, k, q_out, k_out, positions, inv_freq, q_gamma, k_gamma), q.device)
 
 
 def qlin_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_gamma=None, k_gamma=None, eps=1e-6,
@@ -822,7 +834,7 @@ def qlin_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, q_gamma=None, k_g
 
 def qlin_qk_norm_rope_cache_prepare(q, k, v, q_out, positions, inv_freq, slots, cache, q_gamma=None, k_gamma=None,
                                     eps=1e-6, interleaved=False, k_out=None):
-    """qlin_qk_norm_rope_cache's arguments checked and marshalled once (QlinCall.run)."""
+    """qlin_qk_norm_rope_cache's arguments checked and its launches planned once (QlinCall.run)."""
     torch = _torch()
     dtype, code = _half_dtype(k, "k")
     t, d = k.shape[0], cache.head_dim
@@ -833,7 +845,7 @@ def qlin_qk_norm_rope_cache_prepare(q, k, v, q_out, positions, inv_freq, slots, 
     rope = _rope(positions, inv_freq, q_gamma, k_gamma, eps, interleaved, dtype, d, t, cache.device)
     at = _vector(slots, torch.int64, "slots", t, cache.device)
     return QlinCall("qlin_qk_norm_rope_cache", (*map(_ref, parts), code, t, _ref(rope), at, _ref(cache._c)),
-                    (parts, rope, q, k, v, q_out, k_out, positions, inv_freq, q_gamma, k_gamma, slots, cache))
+                    (parts, rope, q, k, v, q_out, k_out, positions, inv_freq, q_gamma, k_gamma, slots, cache), cache.device)
 
 
 def qlin_qk_norm_rope_cache(q, k, v, q_out, positions, inv_freq, slots, cache, q_gamma=None, k_gamma=None, eps=1e-6,
@@ -845,13 +857,14 @@ def qlin_qk_norm_rope_cache(q, k, v, q_out, positions, inv_freq, slots, cache, q
 
 
 def qlin_kv_cache_write_prepare(k, v, slots, cache):
-    """qlin_kv_cache_write's arguments checked and marshalled once (QlinCall.run)."""
+    """qlin_kv_cache_write's arguments checked and its launches planned once (QlinCall.run)."""
     torch = _torch()
     dtype, code = _half_dtype(k, "k")
     t = k.shape[0]
     parts = [_heads(x, dtype, cache.head_dim, n, t, cache.device) for n, x in (("k", k), ("v", v))]
     at = _vector(slots, torch.int64, "slots", t, cache.device)
-    return QlinCall("qlin_kv_cache_write", (*map(_ref, parts), code, t, at, _ref(cache._c)), (parts, k, v, slots, cache))
+    return QlinCall("qlin_kv_cache_write", (*map(_ref, parts), code, t, at, _ref(cache._c)), (parts, k, v, slots, cache),
+                    cache.device)
 
 
 def qlin_kv_cache_write(k, v, slots, cache, stream=None):
@@ -860,7 +873,7 @@ def qlin_kv_cache_write(k, v, slots, cache, stream=None):
 
 
 def qlin_kv_cache_read_prepare(cache, block_table, starts, indptr, k_out, v_out):
-    """qlin_kv_cache_read's arguments checked and marshalled once (QlinCall.run)."""
+    """qlin_kv_cache_read's arguments checked and its launches planned once (QlinCall.run)."""
     torch = _torch()
     dtype, code = _half_dtype(k_out, "k_out")
     if block_table.dim() != 2:
@@ -872,7 +885,7 @@ def qlin_kv_cache_read_prepare(cache, block_table, starts, indptr, k_out, v_out)
     sp = _vector(starts, torch.int32, "starts", b, cache.device)
     ip = _vector(indptr, torch.int32, "indptr", b + 1, cache.device)
     return QlinCall("qlin_kv_cache_read", (_ref(cache._c), tp, max_pages, sp, ip, b, rows, *map(_ref, parts), code),
-                    (parts, cache, block_table, starts, indptr, k_out, v_out))
+                    (parts, cache, block_table, starts, indptr, k_out, v_out), cache.device)
 
 
 def qlin_kv_cache_read(cache, block_table, starts, indptr, k_out, v_out, stream=None):
@@ -891,7 +904,7 @@ def qlin_tree_attention_workspace_bytes(cache, heads, max_nodes, seqs):
 
 def qlin_tree_attention_prepare(q, cache, block_table, q_indptr, ctx_lens, mask, out, workspace, max_nodes, scale=None,
                                 lse=None):
-    """qlin_tree_attention's arguments checked and marshalled once (QlinCall.run)."""
+    """qlin_tree_attention's arguments checked and its launches planned once (QlinCall.run)."""
     torch = _torch()
     dtype, code = _half_dtype(q, "q")
     if q.dim() != 3:
@@ -911,7 +924,7 @@ def qlin_tree_attention_prepare(q, cache, block_table, q_indptr, ctx_lens, mask,
     return QlinCall("qlin_tree_attention",
                     (*map(_ref, parts), code, tq, _ref(cache._c), tp, max_pages, ip, cp, b, mp, words if mask is not None else 0,
                      max_nodes, d ** -0.5 if scale is None else scale, lp, wp, workspace.numel()),
-                    (parts, q, cache, block_table, q_indptr, ctx_lens, mask, out, workspace, lse))
+                    (parts, q, cache, block_table, q_indptr, ctx_lens, mask, out, workspace, lse), cache.device)
 
 
 def qlin_tree_attention(q, cache, block_table, q_indptr, ctx_lens, mask, out, workspace, max_nodes, scale=None, lse=None,

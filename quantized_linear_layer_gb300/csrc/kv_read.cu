@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kTokens;
   const int count = static_cast<int>(min(static_cast<int64_t>(kTokens), p.rows - row0));
 
+  pdl_launch_dependents();
+  pdl_wait();
   const int warp = threadIdx.x / 32;
   if (warp < count) {
     const int l = threadIdx.x % 32;
@@ -150,22 +152,23 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
 }
 
 template <int DT, int D>
-cudaError_t launch(const Params& p, int fmt, cudaStream_t stream) {
+cudaError_t plan(const Params& p, int fmt, Prepared* out) {
   constexpr int kHeads = kThreads / (D / 8) * kUnroll / kTokens;
-  const dim3 grid(static_cast<unsigned>((p.rows + kTokens - 1) / kTokens),
-                  static_cast<unsigned>((p.cache.heads + kHeads - 1) / kHeads));
-  if (fmt == QLIN_KV_INT8) kv_read_kernel<DT, D, QLIN_KV_INT8><<<grid, kThreads, 0, stream>>>(p);
-  else if (fmt == QLIN_KV_E4M3) kv_read_kernel<DT, D, QLIN_KV_E4M3><<<grid, kThreads, 0, stream>>>(p);
-  else kv_read_kernel<DT, D, QLIN_KV_U4><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const void* fn = fmt == QLIN_KV_INT8   ? reinterpret_cast<const void*>(kv_read_kernel<DT, D, QLIN_KV_INT8>)
+                   : fmt == QLIN_KV_E4M3 ? reinterpret_cast<const void*>(kv_read_kernel<DT, D, QLIN_KV_E4M3>)
+                                         : reinterpret_cast<const void*>(kv_read_kernel<DT, D, QLIN_KV_U4>);
+  out->count = 1;
+  out->launch[0] = {fn, static_cast<uint32_t>((p.rows + kTokens - 1) / kTokens),
+                    static_cast<uint32_t>((p.cache.heads + kHeads - 1) / kHeads), kThreads, 0};
+  out->set(p);
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+cudaError_t plan_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
                                  const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows,
-                                 const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype,
-                                 cudaStream_t stream) {
+                                 const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype, Prepared* out) {
   Params p = {};
   p.cache = kv::view_of(*cache);
   p.table = block_table;
@@ -183,13 +186,13 @@ cudaError_t launch_kv_cache_read(const qlin_kv_cache* cache, const int32_t* bloc
   p.err = device_error_word();
   const int64_t d = cache->head_dim;
   if (dtype == QLIN_F16) {
-    if (d == 64) return launch<0, 64>(p, cache->fmt, stream);
-    if (d == 128) return launch<0, 128>(p, cache->fmt, stream);
-    return launch<0, 256>(p, cache->fmt, stream);
+    if (d == 64) return plan<0, 64>(p, cache->fmt, out);
+    if (d == 128) return plan<0, 128>(p, cache->fmt, out);
+    return plan<0, 256>(p, cache->fmt, out);
   }
-  if (d == 64) return launch<1, 64>(p, cache->fmt, stream);
-  if (d == 128) return launch<1, 128>(p, cache->fmt, stream);
-  return launch<1, 256>(p, cache->fmt, stream);
+  if (d == 64) return plan<1, 64>(p, cache->fmt, out);
+  if (d == 128) return plan<1, 128>(p, cache->fmt, out);
+  return plan<1, 256>(p, cache->fmt, out);
 }
 
 }  // namespace qlin

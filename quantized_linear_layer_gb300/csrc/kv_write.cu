@@ -4,9 +4,9 @@
 // A row is one head of one token, D 16-bit elements, held by D / 8 lanes of
 // eight elements (one 16-byte load each).  A block takes kRows consecutive
 // rows of the flat (token, head) order per step: D / 8 lanes x kUnroll rows
-// per lane group.  A step issues its loads, then works out the angles of the
-// next step's tokens into the other of two buffers while they are under way,
-// then finishes its rows; one barrier a step.
+// per lane group.  While a step's loads are under way the block works out the
+// angles of the next step's tokens into the other of two buffers; then it
+// finishes the step's rows and issues the next loads; one barrier a step.
 //
 // Angles: a position times inv_freq, modulo a full turn.  The frequency in
 // turns is kept as a 64-bit fraction (worked out once per block in float64);
@@ -165,6 +165,42 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_
   const int64_t rows = p.T * p.heads;
   const bool normed = p.q_gamma != nullptr || p.k_gamma != nullptr;
 
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  int64_t t0 = 0;                        // the first row's token
+  int32_t tok[kUnroll], head[kUnroll];   // token after t0; head in the order q, k, v (-1: no row)
+  uint4 raw[kUnroll];
+  int64_t slot[kUnroll];
+  auto load_rows = [&]() {
+    t0 = row0 / p.heads;
+    const int32_t h0 = static_cast<int32_t>(row0 - t0 * p.heads);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int32_t at = h0 + group + u * kGroups;
+      tok[u] = p.magic == 0 ? at / p.heads : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(at), p.magic));
+      head[u] = at - tok[u] * p.heads;
+      slot[u] = -1;
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      const int64_t t = t0 + tok[u];
+      if (t >= p.T) {
+        head[u] = -1;
+      } else {
+        const uint8_t* src;
+        if (head[u] < p.hq) {
+          src = p.q + t * p.qt + head[u] * p.qh;
+        } else {
+          const int32_t h = head[u] - p.hq;
+          src = h < p.hk ? p.k + t * p.kt + h * p.kh : p.v + t * p.vt + (h - p.hk) * p.vh;
+          if constexpr (FMT >= 0) slot[u] = p.slots[t];
+        }
+        raw[u] = *reinterpret_cast<const uint4*>(src + lane * 16);
+      }
+    }
+  };
+  load_rows();
+
   for (int i = threadIdx.x; i < p.half_rot; i += kThreads) {
     const double turns = p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
     freq[i] = static_cast<uint64_t>((turns - floor(turns)) * 18446744073709551616.0);
@@ -195,43 +231,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_
     }
   };
 
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
-  int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
   if (p.half_rot > 0 || normed) __syncthreads();  // freq and gammas are there
   if (p.half_rot > 0) {
     angles(row0, trig);
     __syncthreads();
   }
-  for (int buffer = 0; row0 < rows; row0 += stride, buffer ^= 1) {
-    const int64_t t0 = row0 / p.heads;
-    const int32_t h0 = static_cast<int32_t>(row0 - t0 * p.heads);
-
-    int32_t tok[kUnroll], head[kUnroll];  // token after t0; head in the order q, k, v (-1: no row)
-    uint4 raw[kUnroll];
-    int64_t slot[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int32_t at = h0 + group + u * kGroups;
-      tok[u] = p.magic == 0 ? at / p.heads : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(at), p.magic));
-      head[u] = at - tok[u] * p.heads;
-      slot[u] = -1;
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      const int64_t t = t0 + tok[u];
-      if (t >= p.T) {
-        head[u] = -1;
-      } else {
-        const uint8_t* src;
-        if (head[u] < p.hq) {
-          src = p.q + t * p.qt + head[u] * p.qh;
-        } else {
-          const int32_t h = head[u] - p.hq;
-          src = h < p.hk ? p.k + t * p.kt + h * p.kh : p.v + t * p.vt + (h - p.hk) * p.vh;
-          if constexpr (FMT >= 0) slot[u] = p.slots[t];
-        }
-        raw[u] = *reinterpret_cast<const uint4*>(src + lane * 16);
-      }
-    }
-
+  for (int buffer = 0;; buffer ^= 1) {
     if (p.half_rot > 0 && row0 + stride < rows) angles(row0 + stride, trig + (buffer ^ 1) * per_buffer);
 
 #pragma unroll
@@ -317,12 +322,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_
         }
       }
     }
+    row0 += stride;
+    if (row0 >= rows) break;
+    load_rows();
     if (p.half_rot > 0) __syncthreads();
   }
 }
 
 template <int DT, int D>
-cudaError_t launch(Params p, int fmt, cudaStream_t stream) {
+cudaError_t plan(Params p, int fmt, Prepared* out) {
   constexpr int kRows = kThreads / (D / 8) * kUnroll;
   p.heads = p.hq + p.hk + p.hv;
   p.magic = p.heads > 1 && p.heads <= 16384 ? static_cast<uint32_t>(((uint64_t(1) << 32) + p.heads - 1) / p.heads) : 0;
@@ -340,15 +348,17 @@ cudaError_t launch(Params p, int fmt, cudaStream_t stream) {
     const cudaError_t e = ensure_max_dynamic_smem(fn);
     if (e != cudaSuccess) return e;
   }
-  void* args[] = {&p};
-  return cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(kThreads), args, smem, stream);
+  out->count = 1;
+  out->launch[0] = {fn, static_cast<uint32_t>(grid), 1, kThreads, static_cast<uint32_t>(smem)};
+  out->set(p);
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v, const qlin_heads* q_out,
+cudaError_t plan_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v, const qlin_heads* q_out,
                                 const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D, const qlin_rope* rope,
-                                const int64_t* slots, const qlin_kv_cache* cache, cudaStream_t stream) {
+                                const int64_t* slots, const qlin_kv_cache* cache, Prepared* out) {
   Params p = {};
   p.T = T;
   if (q != nullptr) {
@@ -392,13 +402,13 @@ cudaError_t launch_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const 
   }
   p.err = device_error_word();
   if (dtype == QLIN_F16) {
-    if (D == 64) return launch<0, 64>(p, fmt, stream);
-    if (D == 128) return launch<0, 128>(p, fmt, stream);
-    return launch<0, 256>(p, fmt, stream);
+    if (D == 64) return plan<0, 64>(p, fmt, out);
+    if (D == 128) return plan<0, 128>(p, fmt, out);
+    return plan<0, 256>(p, fmt, out);
   }
-  if (D == 64) return launch<1, 64>(p, fmt, stream);
-  if (D == 128) return launch<1, 128>(p, fmt, stream);
-  return launch<1, 256>(p, fmt, stream);
+  if (D == 64) return plan<1, 64>(p, fmt, out);
+  if (D == 128) return plan<1, 128>(p, fmt, out);
+  return plan<1, 256>(p, fmt, out);
 }
 
 }  // namespace qlin

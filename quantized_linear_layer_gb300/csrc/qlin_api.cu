@@ -854,6 +854,59 @@ qlin_status check_same_heads(const char* what, const qlin_heads* a, int64_t head
 
 }  // namespace
 
+namespace {
+
+constexpr uint64_t kPreparedMagic = 0x716c696e63616c6cull;
+
+// An empty plan in *call.
+qlin_status begin_call(qlin_call* call, Prepared** out) {
+  QLIN_REQUIRE(call != nullptr, QLIN_ERR_INVALID_ARG, "null call");
+  Prepared* c = reinterpret_cast<Prepared*>(call);
+  c->magic = 0;
+  c->count = 0;
+  c->device = -1;
+  *out = c;
+  return QLIN_OK;
+}
+
+qlin_status empty_call(Prepared* c) {
+  c->magic = kPreparedMagic;
+  return ok();
+}
+
+qlin_status planned(Prepared* c, cudaError_t e, const char* what) {
+  if (e == cudaSuccess) e = cudaGetDevice(&c->device);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  c->magic = kPreparedMagic;
+  return ok();
+}
+
+}  // namespace
+
+namespace qlin {
+
+cudaError_t run_prepared(const Prepared& c, cudaStream_t stream) {
+  void* args[] = {const_cast<uint64_t*>(c.params)};
+  for (int i = 0; i < c.count; ++i) {
+    const Launch& l = c.launch[i];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(l.grid_x, l.grid_y);
+    cfg.blockDim = dim3(l.threads);
+    cfg.dynamicSmemBytes = l.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, l.kernel, args);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace qlin
+
 #define QLIN_CHECK(expr)                   \
   do {                                     \
     const qlin_status st_ = (expr);        \
@@ -862,9 +915,11 @@ qlin_status check_same_heads(const char* what, const qlin_heads* a, int64_t head
 
 extern "C" {
 
-qlin_status qlin_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* q_out,
-                              const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D, const qlin_rope* rope,
-                              cudaStream_t stream) {
+qlin_status qlin_qk_norm_rope_prepare(const qlin_heads* q, const qlin_heads* k, const qlin_heads* q_out,
+                                      const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D,
+                                      const qlin_rope* rope, qlin_call* call) {
+  Prepared* plan = nullptr;
+  QLIN_CHECK(begin_call(call, &plan));
   QLIN_REQUIRE(is_half_dtype(dtype), QLIN_ERR_INVALID_ARG, "dtype must be F16 or BF16");
   QLIN_REQUIRE(T >= 0 && T <= kMaxDim, QLIN_ERR_INVALID_ARG, "T=%lld out of range", (long long)T);
   QLIN_REQUIRE(is_head_dim(D), QLIN_ERR_UNSUPPORTED, "D=%lld (64, 128 and 256 are built)", (long long)D);
@@ -878,16 +933,17 @@ qlin_status qlin_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const ql
     QLIN_CHECK(check_heads("k_out", k_out, T, D));
     QLIN_CHECK(check_same_heads("k_out", k_out, k->heads));
   }
-  if (T == 0) return ok();
+  if (T == 0) return empty_call(plan);
   QLIN_DEVICE();
-  QLIN_LAUNCH(launch_qk_norm_rope(q, k, nullptr, q_out, k_out, dtype, T, D, rope, nullptr, nullptr, stream),
-              "qk_norm_rope launch");
+  return planned(plan, plan_qk_norm_rope(q, k, nullptr, q_out, k_out, dtype, T, D, rope, nullptr, nullptr, plan), "qk_norm_rope");
 }
 
-qlin_status qlin_qk_norm_rope_cache(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v,
-                                    const qlin_heads* q_out, const qlin_heads* k_out, qlin_dtype dtype, int64_t T,
-                                    const qlin_rope* rope, const int64_t* slots, const qlin_kv_cache* cache,
-                                    cudaStream_t stream) {
+qlin_status qlin_qk_norm_rope_cache_prepare(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v,
+                                            const qlin_heads* q_out, const qlin_heads* k_out, qlin_dtype dtype,
+                                            int64_t T, const qlin_rope* rope, const int64_t* slots,
+                                            const qlin_kv_cache* cache, qlin_call* call) {
+  Prepared* plan = nullptr;
+  QLIN_CHECK(begin_call(call, &plan));
   QLIN_REQUIRE(is_half_dtype(dtype), QLIN_ERR_INVALID_ARG, "dtype must be F16 or BF16");
   QLIN_REQUIRE(T >= 0 && T <= kMaxDim, QLIN_ERR_INVALID_ARG, "T=%lld out of range", (long long)T);
   QLIN_CHECK(check_cache(cache));
@@ -907,24 +963,25 @@ qlin_status qlin_qk_norm_rope_cache(const qlin_heads* q, const qlin_heads* k, co
     QLIN_CHECK(check_heads("k_out", k_out, T, D));
     QLIN_CHECK(check_same_heads("k_out", k_out, k->heads));
   }
-  if (T == 0) return ok();
+  if (T == 0) return empty_call(plan);
   QLIN_REQUIRE(slots != nullptr, QLIN_ERR_INVALID_ARG, "null slots");
   QLIN_REQUIRE((reinterpret_cast<uintptr_t>(slots) & 7u) == 0, QLIN_ERR_ALIGNMENT, "slots must be 8-byte aligned");
   QLIN_DEVICE();
-  QLIN_LAUNCH(launch_qk_norm_rope(q, k, v, q_out, k_out, dtype, T, D, rope, slots, cache, stream),
-              "qk_norm_rope_cache launch");
+  return planned(plan, plan_qk_norm_rope(q, k, v, q_out, k_out, dtype, T, D, rope, slots, cache, plan), "qk_norm_rope_cache");
 }
 
-qlin_status qlin_kv_cache_write(const qlin_heads* k, const qlin_heads* v, qlin_dtype dtype, int64_t T,
-                                const int64_t* slots, const qlin_kv_cache* cache, cudaStream_t stream) {
+qlin_status qlin_kv_cache_write_prepare(const qlin_heads* k, const qlin_heads* v, qlin_dtype dtype, int64_t T,
+                                        const int64_t* slots, const qlin_kv_cache* cache, qlin_call* call) {
   const qlin_rope plain = {nullptr, nullptr, 0, 0, nullptr, nullptr, 0.0f};
-  return qlin_qk_norm_rope_cache(nullptr, k, v, nullptr, nullptr, dtype, T, &plain, slots, cache, stream);
+  return qlin_qk_norm_rope_cache_prepare(nullptr, k, v, nullptr, nullptr, dtype, T, &plain, slots, cache, call);
 }
 
-qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
-                               const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows,
-                               const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype,
-                               cudaStream_t stream) {
+qlin_status qlin_kv_cache_read_prepare(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                       const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows, const
+                                       qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype, qlin_call* call)
+                                       {
+  Prepared* plan = nullptr;
+  QLIN_CHECK(begin_call(call, &plan));
   QLIN_REQUIRE(is_half_dtype(dtype), QLIN_ERR_INVALID_ARG, "dtype must be F16 or BF16");
   QLIN_REQUIRE(B >= 0 && B <= kMaxDim && rows >= 0 && rows <= kMaxDim, QLIN_ERR_INVALID_ARG,
                "bad sizes B=%lld rows=%lld", (long long)B, (long long)rows);
@@ -935,14 +992,13 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_
   QLIN_CHECK(check_heads("v_out", v_out, rows, cache->head_dim));
   QLIN_CHECK(check_same_heads("k_out", k_out, cache->heads));
   QLIN_CHECK(check_same_heads("v_out", v_out, cache->heads));
-  if (rows == 0 || B == 0) return ok();
+  if (rows == 0 || B == 0) return empty_call(plan);
   QLIN_REQUIRE(block_table && starts && indptr, QLIN_ERR_INVALID_ARG, "null pointer");
   QLIN_REQUIRE(((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(starts) |
                  reinterpret_cast<uintptr_t>(indptr)) & 3u) == 0,
                QLIN_ERR_ALIGNMENT, "block_table, starts and indptr must be 4-byte aligned");
   QLIN_DEVICE();
-  QLIN_LAUNCH(launch_kv_cache_read(cache, block_table, max_pages, starts, indptr, B, rows, k_out, v_out, dtype, stream),
-              "kv_cache_read launch");
+  return planned(plan, plan_kv_cache_read(cache, block_table, max_pages, starts, indptr, B, rows, k_out, v_out, dtype, plan), "kv_cache_read");
 }
 
 int64_t qlin_tree_attention_workspace_bytes(const qlin_kv_cache* cache, int64_t Hq, int64_t max_nodes, int64_t B) {
@@ -953,11 +1009,13 @@ int64_t qlin_tree_attention_workspace_bytes(const qlin_kv_cache* cache, int64_t 
   return tree_attention_workspace_bytes(*cache, Hq, max_nodes, B);
 }
 
-qlin_status qlin_tree_attention(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
-                                const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
-                                const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B, const int64_t* mask,
-                                int64_t mask_words, int64_t max_nodes, float scale, float* lse, void* workspace,
-                                int64_t workspace_bytes, cudaStream_t stream) {
+qlin_status qlin_tree_attention_prepare(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
+                                        const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                        const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B,
+                                        const int64_t* mask, int64_t mask_words, int64_t max_nodes, float scale,
+                                        float* lse, void* workspace, int64_t workspace_bytes, qlin_call* call) {
+  Prepared* plan = nullptr;
+  QLIN_CHECK(begin_call(call, &plan));
   QLIN_REQUIRE(is_half_dtype(dtype), QLIN_ERR_INVALID_ARG, "dtype must be F16 or BF16");
   QLIN_REQUIRE(Tq >= 0 && Tq <= kMaxDim && B >= 0 && B <= 65535, QLIN_ERR_INVALID_ARG, "bad sizes Tq=%lld B=%lld",
                (long long)Tq, (long long)B);
@@ -974,7 +1032,7 @@ qlin_status qlin_tree_attention(const qlin_heads* q, const qlin_heads* out, qlin
                (long long)q->heads, (long long)cache->heads);
   QLIN_REQUIRE(mask == nullptr || mask_words == (max_nodes + 63) / 64, QLIN_ERR_INVALID_ARG,
                "mask_words=%lld, %lld expected", (long long)mask_words, (long long)((max_nodes + 63) / 64));
-  if (Tq == 0 || B == 0) return ok();
+  if (Tq == 0 || B == 0) return empty_call(plan);
   QLIN_REQUIRE(block_table && q_indptr && ctx_lens && workspace, QLIN_ERR_INVALID_ARG, "null pointer");
   QLIN_REQUIRE(((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(q_indptr) |
                  reinterpret_cast<uintptr_t>(ctx_lens) | reinterpret_cast<uintptr_t>(lse)) & 3u) == 0 &&
@@ -988,7 +1046,67 @@ qlin_status qlin_tree_attention(const qlin_heads* q, const qlin_heads* out, qlin
                (long long)workspace_bytes, (long long)need);
   const TreeAttentionArgs a = {*q, *out, dtype, Tq, *cache, block_table, max_pages, q_indptr, ctx_lens, B, mask,
                                mask ? mask_words : 0, max_nodes, scale, lse, workspace};
-  QLIN_LAUNCH(launch_tree_attention(a, stream), "tree_attention launch");
+  return planned(plan, plan_tree_attention(a, plan), "tree_attention");
+}
+
+qlin_status qlin_call_run(const qlin_call* call, cudaStream_t stream) {
+  QLIN_REQUIRE(call != nullptr, QLIN_ERR_INVALID_ARG, "null call");
+  const Prepared& c = *reinterpret_cast<const Prepared*>(call);
+  QLIN_REQUIRE(c.magic == kPreparedMagic, QLIN_ERR_INVALID_ARG, "not a prepared call");
+  if (c.count == 0) return ok();
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  QLIN_REQUIRE(dev == c.device, QLIN_ERR_INVALID_ARG, "prepared on device %d, run on device %d", c.device, dev);
+  e = run_prepared(c, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "launch of a prepared call");
+  return ok();
+}
+
+qlin_status qlin_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* q_out,
+                              const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D, const qlin_rope* rope,
+                              cudaStream_t stream) {
+  qlin_call call;
+  QLIN_CHECK(qlin_qk_norm_rope_prepare(q, k, q_out, k_out, dtype, T, D, rope, &call));
+  return qlin_call_run(&call, stream);
+}
+
+qlin_status qlin_qk_norm_rope_cache(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v,
+                                    const qlin_heads* q_out, const qlin_heads* k_out, qlin_dtype dtype, int64_t T,
+                                    const qlin_rope* rope, const int64_t* slots, const qlin_kv_cache* cache,
+                                    cudaStream_t stream) {
+  qlin_call call;
+  QLIN_CHECK(qlin_qk_norm_rope_cache_prepare(q, k, v, q_out, k_out, dtype, T, rope, slots, cache, &call));
+  return qlin_call_run(&call, stream);
+}
+
+qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                               const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows,
+                               const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype,
+                               cudaStream_t stream) {
+  qlin_call call;
+  QLIN_CHECK(
+      qlin_kv_cache_read_prepare(cache, block_table, max_pages, starts, indptr, B, rows, k_out, v_out, dtype, &call));
+  return qlin_call_run(&call, stream);
+}
+
+qlin_status qlin_tree_attention(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
+                                const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B, const int64_t* mask,
+                                int64_t mask_words, int64_t max_nodes, float scale, float* lse, void* workspace,
+                                int64_t workspace_bytes, cudaStream_t stream) {
+  qlin_call call;
+  QLIN_CHECK(
+      qlin_tree_attention_prepare(q, out, dtype, Tq, cache, block_table, max_pages, q_indptr, ctx_lens, B, mask, mask_words,
+                                  max_nodes, scale, lse, workspace, workspace_bytes, &call));
+  return qlin_call_run(&call, stream);
+}
+
+qlin_status qlin_kv_cache_write(const qlin_heads* k, const qlin_heads* v, qlin_dtype dtype, int64_t T,
+                                const int64_t* slots, const qlin_kv_cache* cache, cudaStream_t stream) {
+  qlin_call call;
+  QLIN_CHECK(qlin_kv_cache_write_prepare(k, v, dtype, T, slots, cache, &call));
+  return qlin_call_run(&call, stream);
 }
 
 }  // extern "C"

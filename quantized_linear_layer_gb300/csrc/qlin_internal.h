@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cstring>
 #include <cuda_runtime.h>
 
 #include "qlin.h"
@@ -146,15 +147,39 @@ cudaError_t launch_fp8_gemm(const uint8_t* a, const uint8_t* b, int64_t T, int64
                             const float* scale_b, const void* bias, qlin_dtype bias_dtype, void* out,
                             qlin_dtype out_dtype, cudaStream_t stream);
 
+// A planned call (what a qlin_call holds): its launches, which share one block
+// of kernel parameters.
+struct Launch {
+  const void* kernel;
+  uint32_t grid_x, grid_y, threads, smem;
+};
+struct Prepared {
+  uint64_t magic;
+  int32_t device;
+  int32_t count;  // launches; 0: an empty problem
+  Launch launch[2];
+  uint64_t params[96];
+
+  template <class P>
+  void set(const P& p) {
+    static_assert(sizeof(P) <= sizeof(params), "kernel parameters too large");
+    memcpy(params, &p, sizeof(P));
+  }
+};
+static_assert(sizeof(Prepared) <= sizeof(qlin_call), "qlin_call too small");
+// Enqueues a planned call.  Every kernel of it is launched with programmatic
+// stream serialization: it waits for the work before it (griddepcontrol.wait,
+// in every block) before it reads or writes global memory.
+cudaError_t run_prepared(const Prepared& c, cudaStream_t stream);
+
 // Head norms, position rotation and the quantized cache.  `cache` null: the
-// rotation alone (v unused); rope null: the write alone (q, q_out, k_out unused).
-cudaError_t launch_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v, const qlin_heads* q_out,
-                                const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D, const qlin_rope* rope,
-                                const int64_t* slots, const qlin_kv_cache* cache, cudaStream_t stream);
-cudaError_t launch_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
-                                 const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows,
-                                 const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype,
-                                 cudaStream_t stream);
+// rotation alone (v unused).
+cudaError_t plan_qk_norm_rope(const qlin_heads* q, const qlin_heads* k, const qlin_heads* v, const qlin_heads* q_out,
+                              const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D, const qlin_rope* rope,
+                              const int64_t* slots, const qlin_kv_cache* cache, Prepared* out);
+cudaError_t plan_kv_cache_read(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                               const int32_t* starts, const int32_t* indptr, int64_t B, int64_t rows,
+                               const qlin_heads* k_out, const qlin_heads* v_out, qlin_dtype dtype, Prepared* out);
 
 struct TreeAttentionArgs {
   qlin_heads q, out;
@@ -174,6 +199,6 @@ struct TreeAttentionArgs {
   void* workspace;
 };
 int64_t tree_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t Hq, int64_t max_nodes, int64_t B);
-cudaError_t launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t stream);
+cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out);
 
 }  // namespace qlin

@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
     tc::prefetch_tmap(&p.k_map);
     tc::prefetch_tmap(&p.v_map);
   }
+  pdl_wait();
   // the units before each thread's share of the sequences
   const int share = (p.B + kThreads - 1) / kThreads;
   {
@@ -783,6 +784,7 @@ __global__ void __launch_bounds__(128) tree_attention_join_kernel(const __grid_c
   constexpr int kTeams = 128 / kLanes;
   __shared__ float4 part[kTeams][D / 4];
   __shared__ float2 part_ml[kTeams];
+  pdl_launch_dependents();
   pdl_wait();
   const Record rec = p.records[blockIdx.x];
   if (rec.last < 0) return;
@@ -846,32 +848,25 @@ __global__ void __launch_bounds__(128) tree_attention_join_kernel(const __grid_c
 int grid_blocks(int64_t head_dim) { return std::min(kMaxBlocks, sm_count() * (head_dim == 256 ? 1 : 2)); }
 
 template <int FMT, int D>
-cudaError_t launch(const Params& p, cudaStream_t stream) {
+cudaError_t plan(const Params& p, Prepared* out) {
   using G = Geo<FMT, D>;
   const void* fn = reinterpret_cast<const void*>(tree_attention_kernel<FMT, D>);
-  cudaError_t e = ensure_max_dynamic_smem(fn);
+  const cudaError_t e = ensure_max_dynamic_smem(fn);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>(grid_blocks(D));
-  tree_attention_kernel<FMT, D><<<blocks, G::kThreads, G::kSmem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, static_cast<unsigned>(std::min<int64_t>(kRows, static_cast<int64_t>(p.max_nodes) * p.group)));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<D>, p);
+  const uint32_t blocks = static_cast<uint32_t>(grid_blocks(D));
+  const uint32_t rows = static_cast<uint32_t>(std::min<int64_t>(kRows, static_cast<int64_t>(p.max_nodes) * p.group));
+  out->count = 2;
+  out->launch[0] = {fn, blocks, 1, G::kThreads, G::kSmem};
+  out->launch[1] = {reinterpret_cast<const void*>(tree_attention_join_kernel<D>), blocks, rows, 128, 0};
+  out->set(p);
+  return cudaSuccess;
 }
 
 template <int FMT>
-cudaError_t launch(const Params& p, int64_t d, cudaStream_t stream) {
-  if (d == 64) return launch<FMT, 64>(p, stream);
-  if (d == 128) return launch<FMT, 128>(p, stream);
-  return launch<FMT, 256>(p, stream);
+cudaError_t plan(const Params& p, int64_t d, Prepared* out) {
+  if (d == 64) return plan<FMT, 64>(p, out);
+  if (d == 128) return plan<FMT, 128>(p, out);
+  return plan<FMT, 256>(p, out);
 }
 
 }  // namespace
@@ -882,7 +877,7 @@ int64_t tree_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t, int6
          2 * blocks * kRows * (cache.head_dim * 4 + static_cast<int64_t>(sizeof(float2)));
 }
 
-cudaError_t launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t stream) {
+cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out) {
   Params p = {};
   const qlin_kv_cache& c = a.cache;
   const int64_t row_bytes = kv::row_bytes(c.fmt, static_cast<int>(c.head_dim));
@@ -927,9 +922,9 @@ cudaError_t launch_tree_attention(const TreeAttentionArgs& a, cudaStream_t strea
   ws += 2 * blocks * kRows * static_cast<int64_t>(sizeof(float2));
   p.records = reinterpret_cast<Record*>(ws);
   p.err = device_error_word();
-  if (c.fmt == QLIN_KV_INT8) return launch<QLIN_KV_INT8>(p, c.head_dim, stream);
-  if (c.fmt == QLIN_KV_E4M3) return launch<QLIN_KV_E4M3>(p, c.head_dim, stream);
-  return launch<QLIN_KV_U4>(p, c.head_dim, stream);
+  if (c.fmt == QLIN_KV_INT8) return plan<QLIN_KV_INT8>(p, c.head_dim, out);
+  if (c.fmt == QLIN_KV_E4M3) return plan<QLIN_KV_E4M3>(p, c.head_dim, out);
+  return plan<QLIN_KV_U4>(p, c.head_dim, out);
 }
 
 }  // namespace qlin
