@@ -1,0 +1,321 @@
+// What the two tree attention kernels share: their parameters, the division of
+// the work among blocks, the widening of codes, and the kernel that joins the
+// parts of a segment.  The mathematics and the division of the work are
+// described in tree_attention.cu.
+#pragma once
+
+#include <cmath>
+
+#include "kv_common.cuh"
+#include "qlin_internal.h"
+#include "tc_common.cuh"
+
+namespace qlin {
+namespace tree {
+
+constexpr float kOffset = 13.0f;
+constexpr float kSlack = 2.0f;
+constexpr float kNoRef = -1e30f;  // before a row has seen anything
+constexpr float kHalfExp = -14.0f;
+constexpr float kHalfNormal = 6.103515625e-5f;  // 2^-14, the smallest normal fp16
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+
+// What a block leaves for the joining kernel when a segment begins in it and
+// ends in a later one.
+struct Record {
+  int32_t last;  // the block where the segment ends, or -1: nothing to join
+  int32_t head, row_tile, nodes;
+  int64_t q_row;
+};
+
+struct Params {
+  CUtensorMap k_map, v_map;
+  const uint8_t* q;
+  uint8_t* out;
+  int64_t qt, qh, ot, oh;  // strides in bytes
+  int32_t hq, hk, group, dtype;
+  int64_t Tq;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  int64_t scale_page_stride;
+  int32_t pages, page_shift;
+  const int32_t* table;
+  int64_t max_pages;
+  const int32_t* q_indptr;
+  const int32_t* ctx_lens;
+  int32_t B;
+  const int64_t* mask;
+  int32_t mask_words, max_nodes;
+  float scale;
+  float* lse;
+  Record* records;   // [blocks]
+  float* part_o;      // [2 blocks][tile_rows][D]
+  float2* part_ml;    // [2 blocks][tile_rows]
+  int32_t tile_rows;  // rows of a row tile
+  int32_t* err;
+};
+
+// A sequence's bounds as far as they can be used: nodes = 0 when they cannot.
+struct Sequence {
+  int64_t q_row;
+  int32_t nodes, ctx, len;
+  int32_t row_tiles, token_tiles;
+};
+
+// In row tiles of ROWS and token tiles of TILE.
+template <int ROWS, int TILE>
+__device__ __forceinline__ Sequence sequence(const Params& p, int b) {
+  Sequence s;
+  const int32_t q0 = p.q_indptr[b], q1 = p.q_indptr[b + 1];
+  s.q_row = q0;
+  s.nodes = q1 - q0;
+  s.ctx = p.ctx_lens[b];
+  const int64_t len = static_cast<int64_t>(s.ctx) + s.nodes;
+  const bool fits = q0 >= 0 && q1 >= q0 && q1 <= p.Tq && s.nodes <= p.max_nodes && s.ctx >= 0 &&
+                    len <= (p.max_pages << p.page_shift) && len <= 0x7fffff00;
+  if (!fits) {
+    record_device_error(p.err, kDevErrBadIndex);
+    s.nodes = 0;
+  }
+  s.len = static_cast<int32_t>(len);
+  s.row_tiles = (s.nodes * p.group + ROWS - 1) / ROWS;
+  s.token_tiles = (s.len + TILE - 1) / TILE;
+  if (s.nodes == 0) s.row_tiles = 0;
+  return s;
+}
+
+__device__ __forceinline__ int64_t units(const Params& p, const Sequence& s) {
+  return s.row_tiles == 0 ? 0 : static_cast<int64_t>(p.hk) * s.row_tiles * s.token_tiles;
+}
+
+// Walks a block's run of units, one segment at a time.
+template <int ROWS, int TILE>
+struct Walk {
+  int32_t b;
+  int64_t at, end;     // next unit, end of the run
+  int64_t first;       // first unit of sequence b
+  Sequence s;
+  // the segment's part that is this block's
+  int32_t head, row_tile, tile, tiles;
+
+  __device__ __forceinline__ bool next(const Params& p) {
+    if (at >= end) return false;
+    int64_t n = units(p, s);
+    while (at - first >= n) {
+      first += n;
+      if (++b >= p.B) return false;  // not reached while the lengths stay as they were counted
+      s = sequence<ROWS, TILE>(p, b);
+      n = units(p, s);
+    }
+    const int64_t i = at - first;
+    const int32_t seg = static_cast<int32_t>(i / s.token_tiles);
+    tile = static_cast<int32_t>(i - static_cast<int64_t>(seg) * s.token_tiles);
+    head = seg / s.row_tiles;
+    row_tile = seg - head * s.row_tiles;
+    tiles = static_cast<int32_t>(min(static_cast<int64_t>(s.token_tiles - tile), end - at));
+    at += tiles;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+constexpr uint32_t kMagic = 0x64006400u;      // 1024 in both halves: 1024 + n is 0x6400 | n
+constexpr uint32_t kInt8Bias = 0x64806480u;   // 1024 + 128
+
+// Four 8-bit codes of one row as two fp16 pairs (codes 0, 1 and 2, 3).
+template <int FMT>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == QLIN_KV_INT8) {
+    w ^= 0x80808080u;
+    lo = hsub2(__byte_perm(w, kMagic, 0x7170), kInt8Bias);
+    hi = hsub2(__byte_perm(w, kMagic, 0x7372), kInt8Bias);
+  } else {
+    lo = kv::e4m3x2_to_half2(static_cast<uint16_t>(w));
+    hi = kv::e4m3x2_to_half2(static_cast<uint16_t>(w >> 16));
+  }
+}
+
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else if constexpr (BYTES == 8)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+
+// The units before each thread's share of the sequences, into scan[THREADS + 1]
+// (share b .. b + share - 1 of thread b / share), by all threads of the block.
+template <int ROWS, int TILE, int THREADS>
+__device__ __forceinline__ void scan_units(const Params& p, int share, int64_t* scan) {
+  int64_t sum = 0;
+  for (int b = threadIdx.x * share; b < min(p.B, static_cast<int>(threadIdx.x + 1) * share); ++b)
+    sum += units(p, sequence<ROWS, TILE>(p, b));
+  scan[threadIdx.x + 1] = sum;
+  if (threadIdx.x == 0) scan[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int64_t carry = 0;
+    for (int i = 0; i < THREADS; i += 32) {
+      int64_t v = scan[1 + i + lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      v += carry;
+      scan[1 + i + lane] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// The run of units of block `block` of `blocks`.
+template <int ROWS, int TILE, int THREADS>
+__device__ __forceinline__ Walk<ROWS, TILE> begin_run(const Params& p, int share, const int64_t* scan, int64_t block,
+                                                      int64_t blocks) {
+  Walk<ROWS, TILE> run;
+  const int64_t total = scan[THREADS];
+  run.at = total * block / blocks;
+  run.end = total * (block + 1) / blocks;
+  int lo = 0, hi = THREADS;  // the last share that begins at or before the run
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (scan[mid] <= run.at) lo = mid; else hi = mid;
+  }
+  run.b = lo * share;
+  run.first = scan[lo];
+  run.s = sequence<ROWS, TILE>(p, run.b);
+  return run;
+}
+
+// What the joining kernel needs of the segment that the walk stands at, which
+// begins in this block and ends in a later one.
+template <int ROWS, int TILE>
+__device__ __forceinline__ Record record_of(const Walk<ROWS, TILE>& w, int64_t blocks, int64_t total) {
+  const int64_t end = w.at - w.tiles + w.s.token_tiles;  // the segment's end, in units
+  Record rec;
+  rec.last = static_cast<int32_t>((end * blocks - 1) / total);
+  rec.head = w.head;
+  rec.row_tile = w.row_tile;
+  rec.nodes = w.s.nodes;
+  rec.q_row = w.s.q_row;
+  return rec;
+}
+
+// Joins the parts of a segment that begins in block `blockIdx.x` of the first
+// kernel and ends in a later one: one row per block, its parts dealt to the
+// warps, D / 4 lanes' worth of float4 each.
+template <int D>
+static __global__ void __launch_bounds__(128) tree_attention_join_kernel(const __grid_constant__ Params p) {
+  constexpr int kLanes = D / 4 < 32 ? D / 4 : 32;  // lanes that cover a row once
+  constexpr int kWide = D / 4 / kLanes;            // float4 a lane
+  constexpr int kTeams = 128 / kLanes;
+  __shared__ float4 part[kTeams][D / 4];
+  __shared__ float2 part_ml[kTeams];
+  pdl_launch_dependents();
+  pdl_wait();
+  const Record rec = p.records[blockIdx.x];
+  if (rec.last < 0) return;
+  const int row = blockIdx.y;
+  const int at = rec.row_tile * p.tile_rows + row;
+  const int node = at / p.group;
+  if (node >= rec.nodes) return;
+  const int team = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const int count = rec.last - static_cast<int>(blockIdx.x) + 1;
+
+  float m = -INFINITY, l = 0.0f;
+  float4 o[kWide];
+#pragma unroll
+  for (int i = 0; i < kWide; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int i = team; i < count; i += kTeams) {
+    const int64_t slot = 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0);
+    const float2 e = p.part_ml[slot * p.tile_rows + row];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot * p.tile_rows + row) * D) + lane;
+    float4 v[kWide];
+#pragma unroll
+    for (int x = 0; x < kWide; ++x) v[x] = src[x * kLanes];
+    const float to = fmaxf(m, e.x);
+    const float fa = m == -INFINITY ? 1.0f : ex2(m - to), fb = e.x == -INFINITY ? 1.0f : ex2(e.x - to);
+    m = to;
+    l = l * fa + e.y * fb;
+#pragma unroll
+    for (int x = 0; x < kWide; ++x) {
+      o[x].x = o[x].x * fa + v[x].x * fb;
+      o[x].y = o[x].y * fa + v[x].y * fb;
+      o[x].z = o[x].z * fa + v[x].z * fb;
+      o[x].w = o[x].w * fa + v[x].w * fb;
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < kWide; ++x) part[team][lane + x * kLanes] = o[x];
+  if (lane == 0) part_ml[team] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x >= D / 4) return;
+  float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kTeams; ++i) top = fmaxf(top, part_ml[i].x);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < kTeams; ++i) {
+    const float f = part_ml[i].x == -INFINITY ? 1.0f : ex2(part_ml[i].x - top);
+    const float4 v = part[i][threadIdx.x];
+    sum += f * part_ml[i].y;
+    acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+  }
+  const float inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
+  const int head = rec.head * p.group + at - node * p.group;
+  const int64_t tok = rec.q_row + node;
+  const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  const uint2 u = p.dtype == QLIN_BF16 ? make_uint2(kv::pack2<1>(v[0], v[1]), kv::pack2<1>(v[2], v[3]))
+                                        : make_uint2(kv::pack2<0>(v[0], v[1]), kv::pack2<0>(v[2], v[3]));
+  *reinterpret_cast<uint2*>(p.out + tok * p.ot + head * p.oh + threadIdx.x * 8) = u;
+  if (p.lse != nullptr && threadIdx.x == 0) p.lse[tok * p.hq + head] = (lg2(sum) + (top - kOffset)) * kLn2;
+}
+
+
+// Which of the two kernels takes a call (tree_attention.cu).
+bool use_wide(int64_t head_dim, int64_t rows);
+int wide_blocks();
+cudaError_t plan_wide(const Params& p, int fmt, int64_t head_dim, Prepared* out);
+
+}  // namespace tree
+}  // namespace qlin

@@ -1,0 +1,773 @@
+// Tree attention for many rows per key head (nodes x query heads of a group),
+// on the tcgen05 tensor cores.  The mathematics, the division of the work and
+// the joining kernel are those of tree_attention.cu; here a row tile has 128
+// rows and a token tile 128 tokens, so that one widening of the codes serves
+// 128 rows and the products run at the full tensor rate.
+//
+// A block (one per SM) has 14 warps:
+//   0-7    softmax: two threads per row (tokens 0-63 and 64-127 of a tile)
+//   8-11   widen codes to fp16 in shared memory, in the tensor core's layout
+//   12     loads codes and scales by TMA into a ring of half tiles
+//   13     issues the products (one thread)
+// Per token tile: S = q n^T (128 x 128, operands from shared memory) into one of
+// two tensor-memory buffers; the softmax threads read their 64 columns of it,
+// turn them into probabilities and write these as fp16 over the same buffer;
+// O += P u takes P from tensor memory and the codes of v from shared memory as
+// they lie (tokens x channels, the operand's other major order), so neither K
+// nor V is transposed.  S of the next tile is issued before P u of this one,
+// so the tensor cores work while the softmax of a tile runs.
+//
+// The two threads of a row agree on the reference through shared memory; when
+// it moves, each rescales half of the row of O in tensor memory.  Probabilities
+// below fp16's normal range are written apart, times 2^29, into the buffer's
+// other half, and go to a second accumulator O2 (o = O + 2^-29 O2) in the tiles
+// that hold any.
+//
+// Tensor memory, all 512 columns: S/P 2 x 128, O 128, O2 128.
+//
+// Bound: for 128 live rows the tensor products (2 x 128 x 128 x D per tile) and
+// the softmax instructions take about as long as each other, and longer than
+// the codes take to come from HBM.
+#include <algorithm>
+#include <cmath>
+
+#include "tmap.h"
+#include "tree_common.cuh"
+
+namespace qlin {
+namespace tree {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kTile = 128;
+constexpr int kHalf = 64;  // tokens of a stage of the ring
+constexpr int kSoftmaxWarps = 8;
+constexpr int kWidenWarps = 4;
+constexpr int kLoadWarp = kSoftmaxWarps + kWidenWarps;
+constexpr int kMmaWarp = kLoadWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kStages = 4;
+constexpr int kCols = 4;  // buffers of the tokens' scales: see the widening warps
+constexpr float kShiftUp = 536870912.0f;              // 2^29: the small probabilities lie below 2^15
+constexpr float kShiftDown = 1.862645149230957e-9f;  // 2^-29
+using W = Walk<kRows, kTile>;
+
+// tensor memory columns
+constexpr uint32_t kTmemO = 256, kTmemO2 = 384;
+
+template <int FMT, int D>
+struct Geo {
+  static constexpr bool kU4 = FMT == QLIN_KV_U4;
+  static constexpr int kRowBytes = kU4 ? D / 2 : D;
+  static constexpr int kBlocks = D / 64;                // 64-channel blocks of 128 rows x 128 bytes
+  static constexpr int kOperand = kBlocks * 16384;      // q, K or V of a tile in fp16
+  static constexpr int kRawCode = kHalf * kRowBytes;    // K or V codes of a stage
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kOperand;
+  static constexpr int kOffV = kOffK + kOperand;        // two buffers
+  static constexpr int kOffRaw = kOffV + 2 * kOperand;
+  static constexpr int kOffScale = kOffRaw + kStages * 2 * kRawCode;
+  static constexpr int kOffCol = kOffScale + kStages * 2 * kHalf * 4;  // [kCols][sk, log2 sv, 1 / sv][128]
+  static constexpr int kOffPair = kOffCol + kCols * 3 * kTile * 4;     // [tile parity][half][row]
+  static constexpr int kOffQmax = kOffPair + 2 * 2 * kRows * 4;        // [half][row]
+  static constexpr int kOffEnd = kOffQmax + 2 * kRows * 4;             // [half][row] (l, small)
+  static constexpr int kOffBar = kOffEnd + 2 * kRows * 8;
+  static constexpr int kBars = 2 * kStages + 1 + 1 + 2 + 2 + 2 + 2 + 1 + kCols;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;  // tensor memory address, flags
+  static constexpr int kOffScan = kOffMisc + 16;
+  static constexpr int kOffWalk = (kOffScan + (kThreads + 1) * 8 + 15) / 16 * 16;
+  static constexpr int kSmem = kOffWalk + (kSoftmaxWarps + kWidenWarps) * static_cast<int>(sizeof(W)) + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+
+  // where 16-byte chunk c of row r of a stage's codes lies
+  static __device__ __forceinline__ uint32_t raw_chunk(int r, int c) {
+    const int s = kRowBytes == 128 ? (r & 7) : kRowBytes == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+    return static_cast<uint32_t>(r * kRowBytes + ((c ^ s) << 4));
+  }
+};
+
+// Where 16-byte chunk c (eight channels) of row r of a 64-channel fp16 block lies (128-byte swizzle).
+__device__ __forceinline__ uint32_t half_chunk(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Pairs of float32 in one 64-bit register: two operations per instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Shared-memory descriptor of an operand stored k x n with n contiguous, in
+// 128-byte swizzled atoms of 8 k x 64 n: atoms of the next 8 k follow (1024
+// bytes), the next 64 n lie `n_stride` bytes on.
+__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr, uint32_t n_stride) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(n_stride >> 4) << 16;   // leading byte offset
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;      // stride byte offset
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Which of the 64 tokens from node `first` on (negative: cached tokens) node
+// `node` sees, one bit each.
+__device__ __forceinline__ uint64_t seen_bits(const Params& p, const Sequence& s, int node, int first) {
+  if (first <= -64) return ~0ull;
+  uint64_t v = 0;
+  const int from = max(first, 0), n = min(s.nodes - from, 64);  // nodes from .. from + n - 1
+  if (node >= 0 && node < s.nodes && n > 0) {
+    if (p.mask == nullptr) {
+      const int m = node + 1 - from;
+      v = m <= 0 ? 0 : m >= 64 ? ~0ull : (1ull << m) - 1;
+    } else {
+      const int64_t* words = p.mask + (s.q_row + node) * p.mask_words;
+      const int w = from >> 6, sh = from & 63;
+      v = static_cast<uint64_t>(words[w]) >> sh;
+      if (sh != 0 && w + 1 < p.mask_words) v |= static_cast<uint64_t>(words[w + 1]) << (64 - sh);
+    }
+    if (n < 64) v &= (1ull << n) - 1;
+  }
+  if (first < 0) v = (v << -first) | ((1ull << -first) - 1);
+  return v;
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const __grid_constant__ Params p) {
+  using G = Geo<FMT, D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - tc::smem_u32(smem_raw));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  const uint32_t bars = base + G::kOffBar;
+  const uint32_t raw_full = bars, raw_free = raw_full + 8 * kStages;  // [kStages]
+  const uint32_t k_full = raw_free + 8 * kStages, k_free = k_full + 8;
+  const uint32_t v_full = k_free + 8;       // [2]
+  const uint32_t s_full = v_full + 16;      // [2]
+  const uint32_t p_full = s_full + 16;      // [2]
+  const uint32_t pv_done = p_full + 16;     // [2]
+  const uint32_t q_full = pv_done + 16;
+  const uint32_t col_full = q_full + 8;     // [kCols]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
+  volatile uint32_t* small_tile = reinterpret_cast<volatile uint32_t*>(smem + G::kOffMisc + 8);  // [2]: 1 + the last tile with any
+  int64_t* scan = reinterpret_cast<int64_t*>(smem + G::kOffScan);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(raw_full + 8 * i, 1);
+      tc::mbar_init(raw_free + 8 * i, kWidenWarps);
+    }
+    tc::mbar_init(k_full, kWidenWarps);
+    tc::mbar_init(k_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(v_full + 8 * i, kWidenWarps);
+      tc::mbar_init(s_full + 8 * i, 1);
+      tc::mbar_init(p_full + 8 * i, kSoftmaxWarps);
+      tc::mbar_init(pv_done + 8 * i, 1);
+      small_tile[i] = 0;
+    }
+    tc::mbar_init(q_full, kSoftmaxWarps);
+    for (int i = 0; i < kCols; ++i) tc::mbar_init(col_full + 8 * i, kWidenWarps);
+    tc::fence_mbar_init();
+    tc::prefetch_tmap(&p.k_map);
+    tc::prefetch_tmap(&p.v_map);
+  }
+  pdl_wait();
+  const int share = (p.B + kThreads - 1) / kThreads;
+  scan_units<kRows, kTile, kThreads>(p, share, scan);
+  const int64_t total = scan[kThreads];
+  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);  // each of these has a unit or more
+  if (threadIdx.x == 0) p.records[blockIdx.x].last = -1;
+  if (blockIdx.x >= blocks) {
+    pdl_launch_dependents();
+    return;
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  W run = begin_run<kRows, kTile, kThreads>(p, share, scan, blockIdx.x, blocks);
+
+  // In every role a wait that runs out makes it go on without waiting, so that
+  // all loops end and every barrier among threads is met.
+  bool dead = false;
+  auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+    if (!dead) dead = !tc::mbar_wait(bar, parity & 1, p.err, site);
+  };
+
+  if (warp == kLoadWarp) {
+    // ---------------- loads ----------------
+    uint32_t n = 0;  // half tiles
+    const int page = 1 << p.page_shift;
+    const int box = min(page, kHalf);
+    const int boxes = kHalf / box;
+    const uint64_t policy = tc::l2_policy_evict_first();
+    while (run.next(p)) {
+      const int32_t* table = p.table + run.b * p.max_pages;
+      const int end = min(run.s.len, (run.tile + run.tiles) * kTile);
+      int32_t ahead = -1;  // the page of box `lane` of the 32 boxes from half tile `from` on
+      int from = 0;
+      for (int t = 2 * run.tile; t < 2 * (run.tile + run.tiles); ++t, ++n) {
+        if (t == 2 * run.tile || (t - from) * boxes == 32) {
+          from = t;
+          const int j = t * kHalf + lane * box;
+          ahead = -1;
+          if (j < end) {
+            ahead = table[j >> p.page_shift];
+            if (ahead < 0 || ahead >= p.pages) {
+              record_device_error(p.err, kDevErrBadIndex);
+              ahead = -1;
+            }
+          }
+        }
+        const int32_t pg = __shfl_sync(0xffffffffu, ahead, ((t - from) * boxes + lane) & 31);
+        const bool load = lane < boxes && pg >= 0;
+        const int good = __popc(__ballot_sync(0xffffffffu, load));
+        const uint32_t stage = n % kStages;
+        if (n >= kStages) wait(raw_free + 8 * stage, n / kStages - 1, 0x60);
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) continue;
+        const uint32_t bar = raw_full + 8 * stage;
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, good * box * (2 * G::kRowBytes + 8));
+        __syncwarp();
+        if (load) {
+          const int row = run.head * page + ((t * kHalf + lane * box) & (page - 1));
+          const uint32_t kd = base + G::kOffRaw + stage * 2 * G::kRawCode + lane * box * G::kRowBytes;
+          const int64_t so = pg * p.scale_page_stride + static_cast<int64_t>(row) * 4;
+          const uint32_t sd = base + G::kOffScale + stage * 2 * kHalf * 4 + lane * box * 4;
+          tc::tma_load_3d(kd, &p.k_map, 0, row, pg, bar);
+          tc::bulk_load_policy(sd, p.k_scale + so, box * 4, bar, policy);
+          tc::bulk_load_policy(sd + kHalf * 4, p.v_scale + so, box * 4, bar, policy);
+          tc::tma_load_3d(kd + G::kRawCode, &p.v_map, 0, row, pg, bar);
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------- products ----------------
+    if (lane == 0) {
+      const uint32_t idesc_s = tc::idesc_f16(kRows, kTile, 0);
+      const uint32_t idesc_o = tc::idesc_f16(kRows, D, 0) | (1u << 16);  // B with n contiguous
+      uint32_t t = 0, seg = 0;
+      bool o2_begun = false;
+      auto second = [&](uint32_t x, bool first) {  // O += P u of tile x, the first of its segment or not
+        const uint32_t buf = x & 1;
+        wait(p_full + 8 * buf, x >> 1, 0x61);
+        wait(v_full + 8 * buf, x >> 1, 0x62);
+        tc::tc_fence_after();
+        if (first) o2_begun = false;
+        const uint32_t vb = base + G::kOffV + buf * G::kOperand;
+        const bool small = small_tile[buf] == x + 1;
+        if (!dead) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            tc::mma_f16_ta(tmem + kTmemO, tmem + buf * 128 + 8 * k, sw128_nmajor_desc(vb + k * 2048, 16384), idesc_o,
+                           !first || k > 0 ? 1u : 0u);
+          if (small) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              tc::mma_f16_ta(tmem + kTmemO2, tmem + buf * 128 + 64 + 8 * k, sw128_nmajor_desc(vb + k * 2048, 16384),
+                             idesc_o, o2_begun || k > 0 ? 1u : 0u);
+            o2_begun = true;
+          }
+        }
+        tc::mma_commit(pv_done + 8 * buf);
+      };
+      bool pending_first = false;
+      while (run.next(p)) {
+        for (int i = 0; i < run.tiles; ++i, ++t) {
+          const uint32_t buf = t & 1;
+          if (i == 0) wait(q_full, seg, 0x63);
+          wait(k_full, t, 0x64);
+          if (t >= 2) wait(pv_done + 8 * buf, (t - 2) >> 1, 0x65);
+          tc::tc_fence_after();
+          if (!dead) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+              tc::mma_f16(tmem + buf * 128, tc::sw128_kmajor_desc(base + G::kOffQ + off),
+                          tc::sw128_kmajor_desc(base + G::kOffK + off), idesc_s, k > 0 ? 1u : 0u);
+            }
+          }
+          tc::mma_commit(s_full + 8 * buf);
+          tc::mma_commit(k_free);
+          if (t > 0) second(t - 1, pending_first);
+          pending_first = i == 0;
+        }
+        ++seg;
+      }
+      second(t - 1, pending_first);
+      // every product is done before the tensor memory is given back
+      wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x66);
+    }
+    __syncwarp();
+  } else if (warp >= kSoftmaxWarps) {
+    // ---------------- widening ----------------
+    const int wid = threadIdx.x - 32 * kSoftmaxWarps;  // 0 .. 127: the token whose scales this thread prepares
+    W& w = reinterpret_cast<W*>(smem + G::kOffWalk)[warp];
+    if (lane == 0) w = run;
+    uint32_t t = 0;
+    constexpr int kLanes = G::kRowBytes / 16;      // lanes a row, 16 bytes of codes each
+    constexpr int kStep = 32 / kLanes;             // rows a warp takes at once
+    constexpr int kPieces = G::kU4 ? 4 : 2;        // 16-byte fp16 chunks a lane makes of them
+    const int c = lane % kLanes;
+    // the order in which a lane stores its chunks, so that the eight lanes of a quarter warp hit eight bank groups
+    const int flip = (G::kBlocks == 2 && c >= kLanes / 2) ? 1 : 0;
+    while (true) {
+      bool more = false;
+      __syncwarp();
+      if (lane == 0) more = w.next(p);
+      __syncwarp();
+      if (!__shfl_sync(0xffffffffu, more, 0)) break;
+      const int len = w.s.len;
+      for (int i = 0; i < w.tiles; ++i, ++t) {
+        const int j0 = (w.tile + i) * kTile;
+        // K or V (v) of both halves of the tile into `to`
+        auto widen = [&](bool v, uint32_t to) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t n = 2 * t + h, stage = n % kStages;
+            if (!v) wait(raw_full + 8 * stage, n / kStages, 0x67);
+            const uint32_t from = base + G::kOffRaw + stage * 2 * G::kRawCode + (v ? G::kRawCode : 0);
+            const uint8_t* sc = smem + G::kOffScale + stage * 2 * kHalf * 4 + (v ? kHalf * 4 : 0);
+#pragma unroll
+            for (int x = 0; x < kHalf / kWidenWarps; x += kStep) {
+              const int row = (warp - kSoftmaxWarps) * (kHalf / kWidenWarps) + x + lane / kLanes;
+              const uint4 u = tc::lds128(from + G::raw_chunk(row, c));
+              uint32_t wd[4] = {u.x, u.y, u.z, u.w};
+              // beyond the sequence's end lies anything: zeros for the second product
+              const bool out = v && j0 + h * kHalf + row >= len;
+              const uint32_t at = to + (h * kHalf + row) * 128;
+              const int sw = row & 7;
+              if constexpr (G::kU4) {
+                const uint32_t word = *reinterpret_cast<const uint32_t*>(sc + row * 4);
+                // a zero-point that is not one (its token is not seen) becomes 0: what is not seen has to stay finite
+                const __half z = __hmin(__hmax(__ushort_as_half(static_cast<unsigned short>(word >> 16)), __float2half(0.0f)),
+                                        __float2half(15.0f));
+                const __half2 zz = __half2half2(__hadd(z, __float2half(1024.0f)));
+                const uint32_t bias = *reinterpret_cast<const uint32_t*>(&zz);
+                if (flip) {
+                  uint32_t s = wd[0]; wd[0] = wd[1]; wd[1] = s;
+                  s = wd[2]; wd[2] = wd[3]; wd[3] = s;
+                }
+                const int first = c * 4;  // this lane's first chunk of eight channels
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) {
+                  uint32_t o[4];
+#pragma unroll
+                  for (int m = 0; m < 4; ++m) {
+                    o[m] = hsub2(((wd[k] >> (4 * m)) & 0x000f000fu) | kMagic, bias);
+                    if (out) o[m] = 0u;
+                  }
+                  const int chunk = first + (k ^ flip);
+                  sts128(at + (chunk >> 3) * 16384 + (((chunk & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                }
+              } else {
+                if (flip) {
+                  uint32_t s = wd[0]; wd[0] = wd[2]; wd[2] = s;
+                  s = wd[1]; wd[1] = wd[3]; wd[3] = s;
+                }
+                const int first = c * 2;
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) {
+                  uint32_t o[4];
+                  widen4<FMT>(wd[2 * k], o[0], o[1]);
+                  widen4<FMT>(wd[2 * k + 1], o[2], o[3]);
+                  if (out) o[0] = o[1] = o[2] = o[3] = 0u;
+                  const int chunk = first + (k ^ flip);
+                  sts128(at + (chunk >> 3) * 16384 + (((chunk & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+                }
+              }
+            }
+          }
+          tc::fence_proxy_async_smem();
+        };
+
+        // K, once S of the tile before is done
+        if (t >= 1) wait(k_free, t - 1, 0x68);
+        dead = __any_sync(0xffffffffu, dead);
+        widen(false, base + G::kOffK);
+        dead = __any_sync(0xffffffffu, dead);
+        // The tokens' scales.  Their buffer was last read for tile t - kCols; K of this tile could be written
+        // only after S of tile t - 1, which needed p of tile t - 3.
+        {
+          const uint32_t stage = (2 * t + (wid >> 6)) % kStages;
+          const uint8_t* sc = smem + G::kOffScale + stage * 2 * kHalf * 4 + (wid & 63) * 4;
+          const uint32_t kw = *reinterpret_cast<const uint32_t*>(sc);
+          const uint32_t vw = *reinterpret_cast<const uint32_t*>(sc + kHalf * 4);
+          float sk, sv;
+          if constexpr (G::kU4) {
+            sk = __half2float(__ushort_as_half(static_cast<unsigned short>(kw & 0xffffu)));
+            sv = __half2float(__ushort_as_half(static_cast<unsigned short>(vw & 0xffffu)));
+          } else {
+            sk = __uint_as_float(kw);
+            sv = __uint_as_float(vw);
+          }
+          const float rsv = rcp(sv);
+          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + wid;
+          col[0] = sk;
+          col[kTile] = lg2(sv);
+          // a hidden token adds nothing to l, whatever its scale is; one that is seen makes t a NaN with it
+          col[2 * kTile] = rsv < INFINITY ? rsv : 0.0f;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(k_full);
+          tc::mbar_arrive(col_full + 8 * (t % kCols));
+        }
+        // V, once P u of the tile before the last is done
+        if (t >= 2) wait(pv_done + 8 * (t & 1), (t - 2) >> 1, 0x69);
+        dead = __any_sync(0xffffffffu, dead);
+        widen(true, base + G::kOffV + (t & 1) * G::kOperand);
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(v_full + 8 * (t & 1));
+          tc::mbar_arrive(raw_free + 8 * ((2 * t) % kStages));
+          tc::mbar_arrive(raw_free + 8 * ((2 * t + 1) % kStages));
+        }
+      }
+    }
+  } else {
+    // ---------------- softmax ----------------
+    const int quad = warp & 3, half = warp >> 2;
+    const int row = quad * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    constexpr int kMine = D / 2;  // channels of q and o that this thread takes
+    float* pair_max = reinterpret_cast<float*>(smem + G::kOffPair);
+    uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + G::kOffQmax);
+    float2* ends = reinterpret_cast<float2*>(smem + G::kOffEnd);
+    W& w = reinterpret_cast<W*>(smem + G::kOffWalk)[warp];
+    auto sync_pair = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };  // the two warps of these rows
+
+    // What is left to do for a segment once its last product is issued, and what its rows are.
+    struct Segment {
+      Sequence s;
+      int32_t head, row_tile, node;
+      bool begins, ends;
+    };
+
+    // q of this thread's half row, scaled by a power of two, into shared memory; the factor to undo it
+    auto stage_q = [&](const Segment& g, float& row_scale) {
+      const int at = g.row_tile * kRows + row;
+      const bool live = g.node < g.s.nodes;
+      uint4 raw[kMine / 8];
+      uint32_t top = 0;
+      const bool bf16 = p.dtype == QLIN_BF16;
+      const uint8_t* src = p.q + (g.s.q_row + g.node) * p.qt + (g.head * p.group + at - g.node * p.group) * p.qh + half * kMine * 2;
+#pragma unroll
+      for (int i = 0; i < kMine / 8; ++i) {
+        raw[i] = live ? ldg_v4(src + i * 16) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = bf16 ? kv::unpack2<1>(u[k]) : kv::unpack2<0>(u[k]);
+          top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+        }
+      }
+      q_max[half * kRows + row] = top;
+      sync_pair();
+      top = max(top, q_max[(half ^ 1) * kRows + row]);
+      int e = 0;
+      if (top > 0 && top < 0x7f800000u) e = ilogbf(__uint_as_float(top)) - 14;
+      row_scale = ldexpf(p.scale * kLog2e, e);
+      const float s1 = ldexpf(1.0f, -(e / 2)), s2 = ldexpf(1.0f, -(e - e / 2));
+#pragma unroll
+      for (int i = 0; i < kMine / 8; ++i) {
+        const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = bf16 ? kv::unpack2<1>(u[k]) : kv::unpack2<0>(u[k]);
+          f[2 * k] = v.x * s1 * s2;
+          f[2 * k + 1] = v.y * s1 * s2;
+        }
+        const int chunk = half * (kMine / 8) + i;
+        const uint32_t to = base + G::kOffQ + (chunk >> 3) * 16384 + half_chunk(row, chunk & 7);
+        if constexpr (G::kU4)  // the order in which 4-bit codes are widened
+          sts128(to, kv::pack2<0>(f[0], f[4]), kv::pack2<0>(f[1], f[5]), kv::pack2<0>(f[2], f[6]), kv::pack2<0>(f[3], f[7]));
+        else
+          sts128(to, kv::pack2<0>(f[0], f[1]), kv::pack2<0>(f[2], f[3]), kv::pack2<0>(f[4], f[5]), kv::pack2<0>(f[6], f[7]));
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(q_full);
+    };
+
+    auto segment = [&]() {
+      Segment g;
+      g.s = w.s;
+      g.head = w.head;
+      g.row_tile = w.row_tile;
+      g.node = (w.row_tile * kRows + row) / p.group;
+      g.begins = w.tile == 0;
+      g.ends = w.tile + w.tiles == w.s.token_tiles;
+      if (threadIdx.x == 0 && g.begins && !g.ends) p.records[blockIdx.x] = record_of(w, blocks, total);
+      return g;
+    };
+    auto next = [&]() {
+      bool more = false;
+      __syncwarp();
+      if (lane == 0) more = w.next(p);
+      __syncwarp();
+      return __shfl_sync(0xffffffffu, more, 0) != 0;
+    };
+
+    if (lane == 0) w = run;
+    uint32_t t = 0;
+    bool more = next();
+    Segment g = segment();
+    float row_scale;
+    stage_q(g, row_scale);
+    while (more) {
+      float ref = kNoRef;
+      uint64_t l2 = pair(0.0f, 0.0f);
+      bool had_small = false;
+      const int tiles = w.tiles, tile0 = w.tile;
+      for (int i = 0; i < tiles; ++i, ++t) {
+        const uint32_t buf = t & 1;
+        wait(s_full + 8 * buf, t >> 1, 0x6a);
+        wait(col_full + 8 * (t % kCols), t / kCols, 0x6b);
+        dead = __any_sync(0xffffffffu, dead);
+        tc::tc_fence_after();
+        const uint32_t s_at = lanes + buf * 128;
+        uint32_t v[64];
+        tc::tmem_ld_32x32b_x32(s_at + half * 64, v);
+        tc::tmem_ld_32x32b_x32(s_at + half * 64 + 32, v + 32);
+        tc::tmem_wait_ld();
+        const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + half * 64;
+        const uint64_t rs = pair(row_scale, row_scale);
+        float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+          const float4 sk = *reinterpret_cast<const float4*>(col + k);
+          const float4 ls = *reinterpret_cast<const float4*>(col + kTile + k);
+          const float2 a = unpair(fma2(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rs), pair(sk.x, sk.y),
+                                       pair(ls.x, ls.y)));
+          const float2 b = unpair(fma2(mul2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), rs),
+                                       pair(sk.z, sk.w), pair(ls.z, ls.w)));
+          v[k] = __float_as_uint(a.x);
+          v[k + 1] = __float_as_uint(a.y);
+          v[k + 2] = __float_as_uint(b.x);
+          v[k + 3] = __float_as_uint(b.y);
+        }
+        const int first = (tile0 + i) * kTile + half * 64 - g.s.ctx;  // the node that column 0 is
+        if (first > -64) {
+          const uint64_t seen = seen_bits(p, g.s, g.node, first);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (!((static_cast<uint32_t>(seen) >> k) & 1u)) v[k] = 0xff800000u;
+            if (!((static_cast<uint32_t>(seen >> 32) >> k) & 1u)) v[32 + k] = 0xff800000u;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          hi = fmaxf(hi, __uint_as_float(v[k]));
+          lo = fminf(lo, __uint_as_float(v[k]));
+        }
+        pair_max[buf * 2 * kRows + half * kRows + row] = hi;
+        sync_pair();
+        hi = fmaxf(hi, pair_max[buf * 2 * kRows + (half ^ 1) * kRows + row]);
+        const bool move = hi > ref + (kOffset + kSlack);
+        if (__any_sync(0xffffffffu, move)) {  // the same in both warps of these rows
+          const float to = move ? hi - kOffset : ref;
+          const float keep = ex2(ref - to);
+          ref = to;
+          l2 = mul2(l2, pair(keep, keep));
+          if (i > 0) {
+            wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x6c);
+            dead = __any_sync(0xffffffffu, dead);
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll 1
+              for (int cc = 0; cc < kMine; cc += 16) {
+                const uint32_t at = lanes + (x == 0 ? kTmemO : kTmemO2) + half * kMine + cc;
+                uint32_t o[16];
+                tc::tmem_ld_32x32b_x16(at, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                tc::tmem_st_32x32b_x16(at, o);
+              }
+            }
+          }
+        }
+        const uint64_t nref = pair(-ref, -ref);
+        const bool mine = lo - ref < kHalfExp;
+        had_small = had_small || mine;
+        auto four = [&](int k, float* e) {  // the probabilities of columns k .. k + 3, added to l
+          const float4 rv = *reinterpret_cast<const float4*>(col + 2 * kTile + k);
+          const float2 a = unpair(add2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), nref));
+          const float2 b = unpair(add2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), nref));
+          e[0] = ex2(a.x), e[1] = ex2(a.y), e[2] = ex2(b.x), e[3] = ex2(b.y);
+          l2 = fma2(pair(e[0], e[1]), pair(rv.x, rv.y), l2);
+          l2 = fma2(pair(e[2], e[3]), pair(rv.z, rv.w), l2);
+        };
+        if (__any_sync(0xffffffffu, mine)) {
+          // the ones below fp16's normal range apart
+#pragma unroll
+          for (int h = 0; h < 64; h += 32) {
+            uint32_t pk[16], ps[16];
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              float e[4];
+              four(h + k, e);
+#pragma unroll
+              for (int x = 0; x < 4; x += 2) {
+                const bool s0 = e[x] < kHalfNormal, s1 = e[x + 1] < kHalfNormal;
+                pk[(k + x) / 2] = kv::pack2<0>(s0 ? 0.0f : e[x], s1 ? 0.0f : e[x + 1]);
+                ps[(k + x) / 2] = kv::pack2<0>(s0 ? e[x] * kShiftUp : 0.0f, s1 ? e[x + 1] * kShiftUp : 0.0f);
+              }
+            }
+            tc::tmem_st_32x32b_x16(s_at + half * 32 + h / 2, pk);
+            tc::tmem_st_32x32b_x16(s_at + 64 + half * 32 + h / 2, ps);
+          }
+          if (lane == 0) small_tile[buf] = t + 1;
+        } else {
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 64; k += 4) {
+            float e[4];
+            four(k, e);
+            pk[k / 2] = kv::pack2<0>(e[0], e[1]);
+            pk[k / 2 + 1] = kv::pack2<0>(e[2], e[3]);
+          }
+          tc::tmem_st_32x32b_x32(s_at + half * 32, pk);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) pk[k] = 0u;  // another warp's rows may have some
+          tc::tmem_st_32x32b_x16(s_at + 64 + half * 32, pk);
+          tc::tmem_st_32x32b_x16(s_at + 64 + half * 32 + 16, pk);
+        }
+        __syncwarp();
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + 8 * buf);
+      }
+
+      // the next segment's q, then this one's output
+      const Segment done = g;
+      const float2 lp = unpair(l2);
+      float l = lp.x + lp.y;
+      ends[half * kRows + row] = make_float2(l, had_small ? 1.0f : 0.0f);
+      more = next();
+      if (more) {
+        g = segment();
+        stage_q(g, row_scale);
+      }
+      sync_pair();
+      const float2 other = ends[(half ^ 1) * kRows + row];
+      l += other.x;
+      had_small = had_small || other.y != 0.0f;
+      wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x6d);
+      dead = __any_sync(0xffffffffu, dead);
+      tc::tc_fence_after();
+      const bool live = done.node < done.s.nodes;
+      const bool whole = done.begins && done.ends;
+      const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : __frcp_rn(l);
+      const float m = ref == kNoRef ? -INFINITY : ref + kOffset;
+      const int head = done.head * p.group + done.row_tile * kRows + row - done.node * p.group;
+      const int64_t tok = done.s.q_row + done.node;
+      const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (done.begins ? 1 : 0)) * kRows + row;
+#pragma unroll 1
+      for (int cc = 0; cc < kMine; cc += 16) {
+        uint32_t o[16], s[16];
+        __syncwarp();
+        tc::tmem_ld_32x32b_x16(lanes + kTmemO + half * kMine + cc, o);
+        tc::tmem_ld_32x32b_x16(lanes + kTmemO2 + half * kMine + cc, s);
+        tc::tmem_wait_ld();
+        float f[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          // 4-bit codes: column k of eight is channel k / 2 + 4 (k % 2)
+          const int to = G::kU4 ? (k & 8) + ((k & 7) >> 1) + 4 * (k & 1) : k;
+          // O2 holds anything until a tile with small ones
+          f[to] = (__uint_as_float(o[k]) + (had_small ? __uint_as_float(s[k]) * kShiftDown : 0.0f)) * inv;
+        }
+        if (!live) continue;
+        const int ch = half * kMine + cc;
+        if (whole) {
+          uint8_t* to = p.out + tok * p.ot + head * p.oh + ch * 2;
+#pragma unroll
+          for (int k = 0; k < 16; k += 8)
+            *reinterpret_cast<uint4*>(to + k * 2) = p.dtype == QLIN_BF16 ? kv::pack8<1>(f + k) : kv::pack8<0>(f + k);
+        } else {
+          float* to = p.part_o + slot * D + ch;
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(to + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+        }
+      }
+      if (live && half == 0) {
+        if (!whole) p.part_ml[slot] = make_float2(m, l);
+        else if (p.lse != nullptr) p.lse[tok * p.hq + head] = (lg2(l) + (m - kOffset)) * kLn2;
+      }
+      tc::tc_fence_before();
+    }
+  }
+  pdl_launch_dependents();
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int FMT, int D>
+cudaError_t plan(const Params& p, Prepared* out) {
+  const void* fn = reinterpret_cast<const void*>(tree_attention_wide_kernel<FMT, D>);
+  const cudaError_t e = ensure_max_dynamic_smem(fn);
+  if (e != cudaSuccess) return e;
+  const uint32_t blocks = static_cast<uint32_t>(wide_blocks());
+  const uint32_t rows = static_cast<uint32_t>(std::min<int64_t>(kRows, static_cast<int64_t>(p.max_nodes) * p.group));
+  out->count = 2;
+  out->launch[0] = {fn, blocks, 1, kThreads, Geo<FMT, D>::kSmem};
+  out->launch[1] = {reinterpret_cast<const void*>(tree_attention_join_kernel<D>), blocks, rows, 128, 0};
+  out->set(p);
+  return cudaSuccess;
+}
+
+}  // namespace
+
+int wide_blocks() { return sm_count(); }
+
+cudaError_t plan_wide(const Params& p, int fmt, int64_t head_dim, Prepared* out) {
+  if (head_dim == 64) {
+    if (fmt == QLIN_KV_INT8) return plan<QLIN_KV_INT8, 64>(p, out);
+    if (fmt == QLIN_KV_E4M3) return plan<QLIN_KV_E4M3, 64>(p, out);
+    return plan<QLIN_KV_U4, 64>(p, out);
+  }
+  if (fmt == QLIN_KV_INT8) return plan<QLIN_KV_INT8, 128>(p, out);
+  if (fmt == QLIN_KV_E4M3) return plan<QLIN_KV_E4M3, 128>(p, out);
+  return plan<QLIN_KV_U4, 128>(p, out);
+}
+
+}  // namespace tree
+}  // namespace qlin
