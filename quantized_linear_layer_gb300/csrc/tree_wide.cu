@@ -4,11 +4,11 @@
 // rows and a token tile 128 tokens, so that one widening of the codes serves
 // 128 rows and the products run at the full tensor rate.
 //
-// A block (one per SM) has 14 warps:
+// A block (one per SM) has 20 warps, whose registers are dealt out anew by role:
 //   0-7    softmax: two threads per row (tokens 0-63 and 64-127 of a tile)
-//   8-11   widen codes to fp16 in shared memory, in the tensor core's layout
-//   12     loads codes and scales by TMA into a ring of half tiles
-//   13     issues the products (one thread)
+//   8-15   widen codes to fp16 in shared memory, in the tensor core's layout
+//   16     loads codes and scales by TMA into a ring of half tiles
+//   17     issues the products (one thread)
 // Per token tile: S = q n^T (128 x 128, operands from shared memory) into one of
 // two tensor-memory buffers; the softmax threads read their 64 columns of it,
 // turn them into probabilities and write these as fp16 over the same buffer;
@@ -18,10 +18,11 @@
 // so the tensor cores work while the softmax of a tile runs.
 //
 // The two threads of a row agree on the reference through shared memory; when
-// it moves, each rescales half of the row of O in tensor memory.  Probabilities
-// below fp16's normal range are written apart, times 2^29, into the buffer's
-// other half, and go to a second accumulator O2 (o = O + 2^-29 O2) in the tiles
-// that hold any.
+// it moves, each rescales half of the row of O in tensor memory, after its
+// probabilities are written, when P u of the tile before is done.
+// Probabilities below fp16's normal range are written apart, times 2^29, into
+// the buffer's other half, and go to a second accumulator O2 (o = O + 2^-29 O2)
+// in the tiles that hold any.
 //
 // Tensor memory, all 512 columns: S/P 2 x 128, O 128, O2 128.
 //
@@ -42,10 +43,12 @@ constexpr int kRows = 128;
 constexpr int kTile = 128;
 constexpr int kHalf = 64;  // tokens of a stage of the ring
 constexpr int kSoftmaxWarps = 8;
-constexpr int kWidenWarps = 4;
+constexpr int kWidenWarps = 8;
 constexpr int kLoadWarp = kSoftmaxWarps + kWidenWarps;
 constexpr int kMmaWarp = kLoadWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kThreads = 32 * 20;  // whole groups of four warps
+// Registers: 640 threads are launched with 96 each, 61440 in all; 256 x 144 + 256 x 72 + 128 x 40 = 60416.
+constexpr int kSoftmaxRegs = 144, kWidenRegs = 72, kOtherRegs = 40;
 constexpr int kStages = 4;
 constexpr int kCols = 4;  // buffers of the tokens' scales: see the widening warps
 constexpr float kShiftUp = 536870912.0f;              // 2^29: the small probabilities lie below 2^15
@@ -120,6 +123,13 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+// Halves below fp16's normal range become 0.
+__device__ __forceinline__ __half2 flush(uint32_t v) {
+  uint32_t r;
+  asm("mul.rn.ftz.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x3c003c00u));
+  return *reinterpret_cast<const __half2*>(&r);
+}
+
 // Shared-memory descriptor of an operand stored k x n with n contiguous, in
 // 128-byte swizzled atoms of 8 k x 64 n: atoms of the next 8 k follow (1024
 // bytes), the next 64 n lie `n_stride` bytes on.
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(raw_full + 8 * i, 1);
-      tc::mbar_init(raw_free + 8 * i, kWidenWarps);
+      tc::mbar_init(raw_free + 8 * i, kWidenWarps / 2);
     }
     tc::mbar_init(k_full, kWidenWarps);
     tc::mbar_init(k_free, 1);
@@ -223,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
     if (!dead) dead = !tc::mbar_wait(bar, parity & 1, p.err, site);
   };
 
+  if (warp >= kLoadWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kLoadWarp) {
     // ---------------- loads ----------------
     uint32_t n = 0;  // half tiles
@@ -328,9 +339,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x66);
     }
     __syncwarp();
+  } else if (warp > kMmaWarp) {
+    // (fills up the group)
   } else if (warp >= kSoftmaxWarps) {
     // ---------------- widening ----------------
-    const int wid = threadIdx.x - 32 * kSoftmaxWarps;  // 0 .. 127: the token whose scales this thread prepares
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWidenRegs));
+    const int part = warp - kSoftmaxWarps;  // this warp's 16 tokens of a tile
+    const int h = part / 4;                 // the half tile they lie in
     W& w = reinterpret_cast<W*>(smem + G::kOffWalk)[warp];
     if (lane == 0) w = run;
     uint32_t t = 0;
@@ -349,79 +364,73 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       const int len = w.s.len;
       for (int i = 0; i < w.tiles; ++i, ++t) {
         const int j0 = (w.tile + i) * kTile;
-        // K or V (v) of both halves of the tile into `to`
+        const uint32_t stage = (2 * t + h) % kStages;
+        const uint32_t raw = base + G::kOffRaw + stage * 2 * G::kRawCode;
+        const uint8_t* scales = smem + G::kOffScale + stage * 2 * kHalf * 4;
+        // K or V (v) of this warp's tokens into `to`
         auto widen = [&](bool v, uint32_t to) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t n = 2 * t + h, stage = n % kStages;
-            if (!v) wait(raw_full + 8 * stage, n / kStages, 0x67);
-            const uint32_t from = base + G::kOffRaw + stage * 2 * G::kRawCode + (v ? G::kRawCode : 0);
-            const uint8_t* sc = smem + G::kOffScale + stage * 2 * kHalf * 4 + (v ? kHalf * 4 : 0);
+          const uint32_t from = raw + (v ? G::kRawCode : 0);
+          const uint8_t* sc = scales + (v ? kHalf * 4 : 0);
+          const bool tail = v && j0 + kTile > len;
 #pragma unroll
-            for (int x = 0; x < kHalf / kWidenWarps; x += kStep) {
-              const int row = (warp - kSoftmaxWarps) * (kHalf / kWidenWarps) + x + lane / kLanes;
-              const uint4 u = tc::lds128(from + G::raw_chunk(row, c));
-              uint32_t wd[4] = {u.x, u.y, u.z, u.w};
-              // beyond the sequence's end lies anything: zeros for the second product
-              const bool out = v && j0 + h * kHalf + row >= len;
-              const uint32_t at = to + (h * kHalf + row) * 128;
-              const int sw = row & 7;
-              if constexpr (G::kU4) {
-                const uint32_t word = *reinterpret_cast<const uint32_t*>(sc + row * 4);
-                // a zero-point that is not one (its token is not seen) becomes 0: what is not seen has to stay finite
-                const __half z = __hmin(__hmax(__ushort_as_half(static_cast<unsigned short>(word >> 16)), __float2half(0.0f)),
-                                        __float2half(15.0f));
-                const __half2 zz = __half2half2(__hadd(z, __float2half(1024.0f)));
-                const uint32_t bias = *reinterpret_cast<const uint32_t*>(&zz);
-                if (flip) {
-                  uint32_t s = wd[0]; wd[0] = wd[1]; wd[1] = s;
-                  s = wd[2]; wd[2] = wd[3]; wd[3] = s;
-                }
-                const int first = c * 4;  // this lane's first chunk of eight channels
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k) {
-                  uint32_t o[4];
-#pragma unroll
-                  for (int m = 0; m < 4; ++m) {
-                    o[m] = hsub2(((wd[k] >> (4 * m)) & 0x000f000fu) | kMagic, bias);
-                    if (out) o[m] = 0u;
-                  }
-                  const int chunk = first + (k ^ flip);
-                  sts128(at + (chunk >> 3) * 16384 + (((chunk & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
-                }
-              } else {
-                if (flip) {
-                  uint32_t s = wd[0]; wd[0] = wd[2]; wd[2] = s;
-                  s = wd[1]; wd[1] = wd[3]; wd[3] = s;
-                }
-                const int first = c * 2;
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k) {
-                  uint32_t o[4];
-                  widen4<FMT>(wd[2 * k], o[0], o[1]);
-                  widen4<FMT>(wd[2 * k + 1], o[2], o[3]);
-                  if (out) o[0] = o[1] = o[2] = o[3] = 0u;
-                  const int chunk = first + (k ^ flip);
-                  sts128(at + (chunk >> 3) * 16384 + (((chunk & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
-                }
+          for (int x = 0; x < 16; x += kStep) {
+            const int row = (part & 3) * 16 + x + lane / kLanes;  // of the half tile
+            const uint4 u = tc::lds128(from + G::raw_chunk(row, c));
+            uint32_t wd[4] = {u.x, u.y, u.z, u.w};
+            // beyond the sequence's end lies anything: zeros for the second product
+            const bool out = tail && j0 + h * kHalf + row >= len;
+            const uint32_t at = to + (h * kHalf + row) * 128;
+            const int sw = row & 7;
+            uint32_t bias = 0;
+            if constexpr (G::kU4) {
+              const uint32_t word = *reinterpret_cast<const uint32_t*>(sc + row * 4);
+              // a zero-point that is not one (its token is not seen) becomes 0: what is not seen has to stay finite
+              const __half z = __hmin(__hmax(__ushort_as_half(static_cast<unsigned short>(word >> 16)), __float2half(0.0f)),
+                                      __float2half(15.0f));
+              const __half2 zz = __half2half2(__hadd(z, __float2half(1024.0f)));
+              bias = *reinterpret_cast<const uint32_t*>(&zz);
+              if (flip) {
+                uint32_t s = wd[0]; wd[0] = wd[1]; wd[1] = s;
+                s = wd[2]; wd[2] = wd[3]; wd[3] = s;
               }
+            } else {
+              if (flip) {
+                uint32_t s = wd[0]; wd[0] = wd[2]; wd[2] = s;
+                s = wd[1]; wd[1] = wd[3]; wd[3] = s;
+              }
+            }
+            const int first = c * kPieces;  // this lane's first chunk of eight channels
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+              uint32_t o[4];
+              if constexpr (G::kU4) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) o[m] = hsub2(((wd[k] >> (4 * m)) & 0x000f000fu) | kMagic, bias);
+              } else {
+                widen4<FMT>(wd[2 * k], o[0], o[1]);
+                widen4<FMT>(wd[2 * k + 1], o[2], o[3]);
+              }
+              if (tail) {
+                if (out) o[0] = o[1] = o[2] = o[3] = 0u;
+              }
+              const int chunk = first + (k ^ flip);
+              sts128(at + (chunk >> 3) * 16384 + (((chunk & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
             }
           }
           tc::fence_proxy_async_smem();
         };
 
         // K, once S of the tile before is done
+        wait(raw_full + 8 * stage, (2 * t + h) / kStages, 0x67);
         if (t >= 1) wait(k_free, t - 1, 0x68);
         dead = __any_sync(0xffffffffu, dead);
         widen(false, base + G::kOffK);
-        dead = __any_sync(0xffffffffu, dead);
         // The tokens' scales.  Their buffer was last read for tile t - kCols; K of this tile could be written
         // only after S of tile t - 1, which needed p of tile t - 3.
-        {
-          const uint32_t stage = (2 * t + (wid >> 6)) % kStages;
-          const uint8_t* sc = smem + G::kOffScale + stage * 2 * kHalf * 4 + (wid & 63) * 4;
-          const uint32_t kw = *reinterpret_cast<const uint32_t*>(sc);
-          const uint32_t vw = *reinterpret_cast<const uint32_t*>(sc + kHalf * 4);
+        if (lane < 16) {
+          const int token = (part & 3) * 16 + lane;  // of the half tile
+          const uint32_t kw = *reinterpret_cast<const uint32_t*>(scales + token * 4);
+          const uint32_t vw = *reinterpret_cast<const uint32_t*>(scales + (kHalf + token) * 4);
           float sk, sv;
           if constexpr (G::kU4) {
             sk = __half2float(__ushort_as_half(static_cast<unsigned short>(kw & 0xffffu)));
@@ -431,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
             sv = __uint_as_float(vw);
           }
           const float rsv = rcp(sv);
-          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + wid;
+          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + part * 16 + lane;
           col[0] = sk;
           col[kTile] = lg2(sv);
           // a hidden token adds nothing to l, whatever its scale is; one that is seen makes t a NaN with it
@@ -449,13 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         __syncwarp();
         if (lane == 0) {
           tc::mbar_arrive(v_full + 8 * (t & 1));
-          tc::mbar_arrive(raw_free + 8 * ((2 * t) % kStages));
-          tc::mbar_arrive(raw_free + 8 * ((2 * t + 1) % kStages));
+          tc::mbar_arrive(raw_free + 8 * stage);
         }
       }
     }
   } else {
     // ---------------- softmax ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int quad = warp & 3, half = warp >> 2;
     const int row = quad * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -563,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         tc::tmem_wait_ld();
         const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + half * 64;
         const uint64_t rs = pair(row_scale, row_scale);
-        float hi = -INFINITY, lo = INFINITY;
+        float hi = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 64; k += 4) {
           const float4 sk = *reinterpret_cast<const float4*>(col + k);
@@ -587,83 +596,65 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           }
         }
 #pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          hi = fmaxf(hi, __uint_as_float(v[k]));
-          lo = fminf(lo, __uint_as_float(v[k]));
-        }
+        for (int k = 0; k < 64; ++k) hi = fmaxf(hi, __uint_as_float(v[k]));
         pair_max[buf * 2 * kRows + half * kRows + row] = hi;
         sync_pair();
         hi = fmaxf(hi, pair_max[buf * 2 * kRows + (half ^ 1) * kRows + row]);
         const bool move = hi > ref + (kOffset + kSlack);
-        if (__any_sync(0xffffffffu, move)) {  // the same in both warps of these rows
-          const float to = move ? hi - kOffset : ref;
-          const float keep = ex2(ref - to);
-          ref = to;
-          l2 = mul2(l2, pair(keep, keep));
-          if (i > 0) {
-            wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x6c);
-            dead = __any_sync(0xffffffffu, dead);
-            tc::tc_fence_after();
-#pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
-#pragma unroll 1
-              for (int cc = 0; cc < kMine; cc += 16) {
-                const uint32_t at = lanes + (x == 0 ? kTmemO : kTmemO2) + half * kMine + cc;
-                uint32_t o[16];
-                tc::tmem_ld_32x32b_x16(at, o);
-                tc::tmem_wait_ld();
+        const float to = move ? hi - kOffset : ref;
+        const float keep = ex2(ref - to);
+        ref = to;
+        l2 = mul2(l2, pair(keep, keep));
+
+        const uint64_t nref = pair(-ref, -ref), up = pair(kShiftUp, kShiftUp);
+        uint32_t any_small = 0;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-                tc::tmem_st_32x32b_x16(at, o);
-              }
+        for (int h = 0; h < 64; h += 32) {
+          uint32_t pk[16], ps[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 rv = *reinterpret_cast<const float4*>(col + 2 * kTile + h + k);
+            const float rr[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+            for (int x = 0; x < 4; x += 2) {
+              const int i0 = h + k + x;
+              const float2 a = unpair(add2(pair(__uint_as_float(v[i0]), __uint_as_float(v[i0 + 1])), nref));
+              const uint64_t e = pair(ex2(a.x), ex2(a.y));
+              l2 = fma2(e, pair(rr[x], rr[x + 1]), l2);
+              const float2 f = unpair(e), s = unpair(mul2(e, up));
+              // what fp16 cannot hold as a normal number is 0 here and, times 2^29, in the other part
+              const __half2 p16 = flush(kv::pack2<0>(f.x, f.y));
+              pk[(k + x) / 2] = *reinterpret_cast<const uint32_t*>(&p16);
+              ps[(k + x) / 2] = kv::pack2<0>(s.x, s.y) & __heq2_mask(p16, __float2half2_rn(0.0f));
+              any_small |= ps[(k + x) / 2];
             }
           }
+          tc::tmem_st_32x32b_x16(s_at + half * 32 + h / 2, pk);
+          tc::tmem_st_32x32b_x16(s_at + 64 + half * 32 + h / 2, ps);
         }
-        const uint64_t nref = pair(-ref, -ref);
-        const bool mine = lo - ref < kHalfExp;
-        had_small = had_small || mine;
-        auto four = [&](int k, float* e) {  // the probabilities of columns k .. k + 3, added to l
-          const float4 rv = *reinterpret_cast<const float4*>(col + 2 * kTile + k);
-          const float2 a = unpair(add2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), nref));
-          const float2 b = unpair(add2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), nref));
-          e[0] = ex2(a.x), e[1] = ex2(a.y), e[2] = ex2(b.x), e[3] = ex2(b.y);
-          l2 = fma2(pair(e[0], e[1]), pair(rv.x, rv.y), l2);
-          l2 = fma2(pair(e[2], e[3]), pair(rv.z, rv.w), l2);
-        };
-        if (__any_sync(0xffffffffu, mine)) {
-          // the ones below fp16's normal range apart
+        had_small = had_small || any_small != 0;
+        if (__any_sync(0xffffffffu, any_small != 0) && lane == 0) small_tile[buf] = t + 1;
+        if (__any_sync(0xffffffffu, move) && i > 0) {  // the same in both warps of these rows
+          wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x6c);
+          dead = __any_sync(0xffffffffu, dead);
+          tc::tc_fence_after();
 #pragma unroll
-          for (int h = 0; h < 64; h += 32) {
-            uint32_t pk[16], ps[16];
+          for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              float e[4];
-              four(h + k, e);
+            for (int cc = 0; cc < kMine; cc += 32) {
+              const uint32_t at = lanes + (x == 0 ? kTmemO : kTmemO2) + half * kMine + cc;
+              uint32_t o[32];
+              tc::tmem_ld_32x32b_x32(at, o);
+              tc::tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 4; x += 2) {
-                const bool s0 = e[x] < kHalfNormal, s1 = e[x + 1] < kHalfNormal;
-                pk[(k + x) / 2] = kv::pack2<0>(s0 ? 0.0f : e[x], s1 ? 0.0f : e[x + 1]);
-                ps[(k + x) / 2] = kv::pack2<0>(s0 ? e[x] * kShiftUp : 0.0f, s1 ? e[x + 1] * kShiftUp : 0.0f);
+              for (int k = 0; k < 32; k += 2) {
+                const float2 f = unpair(mul2(pair(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), pair(keep, keep)));
+                o[k] = __float_as_uint(f.x);
+                o[k + 1] = __float_as_uint(f.y);
               }
+              tc::tmem_st_32x32b_x32(at, o);
             }
-            tc::tmem_st_32x32b_x16(s_at + half * 32 + h / 2, pk);
-            tc::tmem_st_32x32b_x16(s_at + 64 + half * 32 + h / 2, ps);
           }
-          if (lane == 0) small_tile[buf] = t + 1;
-        } else {
-          uint32_t pk[32];
-#pragma unroll
-          for (int k = 0; k < 64; k += 4) {
-            float e[4];
-            four(k, e);
-            pk[k / 2] = kv::pack2<0>(e[0], e[1]);
-            pk[k / 2 + 1] = kv::pack2<0>(e[2], e[3]);
-          }
-          tc::tmem_st_32x32b_x32(s_at + half * 32, pk);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) pk[k] = 0u;  // another warp's rows may have some
-          tc::tmem_st_32x32b_x16(s_at + 64 + half * 32, pk);
-          tc::tmem_st_32x32b_x16(s_at + 64 + half * 32 + 16, pk);
         }
         __syncwarp();
         tc::tmem_wait_st();
