@@ -123,6 +123,13 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+
 // Halves below fp16's normal range become 0.
 __device__ __forceinline__ __half2 flush(uint32_t v) {
   uint32_t r;
@@ -283,61 +290,70 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
     }
   } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
-    if (lane == 0) {
-      const uint32_t idesc_s = tc::idesc_f16(kRows, kTile, 0);
-      const uint32_t idesc_o = tc::idesc_f16(kRows, D, 0) | (1u << 16);  // B with n contiguous
-      uint32_t t = 0, seg = 0;
-      bool o2_begun = false;
-      auto second = [&](uint32_t x, bool first) {  // O += P u of tile x, the first of its segment or not
-        const uint32_t buf = x & 1;
-        wait(p_full + 8 * buf, x >> 1, 0x61);
-        wait(v_full + 8 * buf, x >> 1, 0x62);
-        tc::tc_fence_after();
-        if (first) o2_begun = false;
-        const uint32_t vb = base + G::kOffV + buf * G::kOperand;
-        const bool small = small_tile[buf] == x + 1;
-        if (!dead) {
+    // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one thread issues.
+    const bool leader = elect_one();
+    const uint32_t idesc_s = tc::idesc_f16(kRows, kTile, 0);
+    const uint32_t idesc_o = tc::idesc_f16(kRows, D, 0) | (1u << 16);  // B with n contiguous
+    // a descriptor's address field counts 16 bytes and does not overflow below 256 KB: advancing is an addition
+    const uint64_t q_desc = tc::sw128_kmajor_desc(base + G::kOffQ), k_desc = tc::sw128_kmajor_desc(base + G::kOffK);
+    const uint64_t v_desc = sw128_nmajor_desc(base + G::kOffV, 16384);
+    uint32_t t = 0, seg = 0;
+    bool o2_begun = false;
+    auto second = [&](uint32_t x, bool first) {  // O += P u of tile x, the first of its segment or not
+      const uint32_t buf = x & 1;
+      wait(p_full + 8 * buf, x >> 1, 0x61);
+      wait(v_full + 8 * buf, x >> 1, 0x62);
+      dead = __any_sync(0xffffffffu, dead);
+      tc::tc_fence_after();
+      if (first) o2_begun = false;
+      const uint64_t vd = v_desc + buf * (G::kOperand >> 4);
+      const uint32_t pt = tmem + buf * 128;
+      const bool small = __any_sync(0xffffffffu, small_tile[buf] == x + 1);
+      if (!dead) {
+        if (leader) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
-            tc::mma_f16_ta(tmem + kTmemO, tmem + buf * 128 + 8 * k, sw128_nmajor_desc(vb + k * 2048, 16384), idesc_o,
-                           !first || k > 0 ? 1u : 0u);
+            tc::mma_f16_ta(tmem + kTmemO, pt + 8 * k, vd + k * 128, idesc_o, !first || k > 0 ? 1u : 0u);
           if (small) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-              tc::mma_f16_ta(tmem + kTmemO2, tmem + buf * 128 + 64 + 8 * k, sw128_nmajor_desc(vb + k * 2048, 16384),
-                             idesc_o, o2_begun || k > 0 ? 1u : 0u);
-            o2_begun = true;
+              tc::mma_f16_ta(tmem + kTmemO2, pt + 64 + 8 * k, vd + k * 128, idesc_o, o2_begun || k > 0 ? 1u : 0u);
           }
         }
-        tc::mma_commit(pv_done + 8 * buf);
-      };
-      bool pending_first = false;
-      while (run.next(p)) {
-        for (int i = 0; i < run.tiles; ++i, ++t) {
-          const uint32_t buf = t & 1;
-          if (i == 0) wait(q_full, seg, 0x63);
-          wait(k_full, t, 0x64);
-          if (t >= 2) wait(pv_done + 8 * buf, (t - 2) >> 1, 0x65);
-          tc::tc_fence_after();
+        o2_begun = o2_begun || small;
+      }
+      if (leader) tc::mma_commit(pv_done + 8 * buf);
+      __syncwarp();
+    };
+    bool pending_first = false;
+    while (run.next(p)) {
+      for (int i = 0; i < run.tiles; ++i, ++t) {
+        const uint32_t buf = t & 1;
+        if (i == 0) wait(q_full, seg, 0x63);
+        wait(k_full, t, 0x64);
+        if (t >= 2) wait(pv_done + 8 * buf, (t - 2) >> 1, 0x65);
+        dead = __any_sync(0xffffffffu, dead);
+        tc::tc_fence_after();
+        if (leader) {
           if (!dead) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-              tc::mma_f16(tmem + buf * 128, tc::sw128_kmajor_desc(base + G::kOffQ + off),
-                          tc::sw128_kmajor_desc(base + G::kOffK + off), idesc_s, k > 0 ? 1u : 0u);
+              const uint32_t off = (k >> 2) * 1024 + (k & 3) * 2;
+              tc::mma_f16(tmem + buf * 128, q_desc + off, k_desc + off, idesc_s, k > 0 ? 1u : 0u);
             }
           }
           tc::mma_commit(s_full + 8 * buf);
           tc::mma_commit(k_free);
-          if (t > 0) second(t - 1, pending_first);
-          pending_first = i == 0;
         }
-        ++seg;
+        __syncwarp();
+        if (t > 0) second(t - 1, pending_first);
+        pending_first = i == 0;
       }
-      second(t - 1, pending_first);
-      // every product is done before the tensor memory is given back
-      wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x66);
+      ++seg;
     }
+    second(t - 1, pending_first);
+    // every product is done before the tensor memory is given back
+    wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x66);
     __syncwarp();
   } else if (warp > kMmaWarp) {
     // (fills up the group)
