@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
         const int32_t pg = __shfl_sync(0xffffffffu, ahead, (at + lane) & 31);
         const bool load = lane < boxes && pg >= 0;
         const int good = __popc(__ballot_sync(0xffffffffu, load));
-        if (!tc::mbar_wait(bar_free + 8 * stage, phase, p.err, 0x50)) dead = true;
+        if (!tc::mbar_wait_quiet(bar_free + 8 * stage, phase, p.err, 0x50)) dead = true;
         if (__any_sync(0xffffffffu, dead)) {
           dead = true;
           break;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
     const bool took = u < unit0 + w.tiles;
     for (; u < unit0 + w.tiles; u += kWarps) {
       const uint32_t stage = u % G::kStages;
-      if (!dead) dead = !tc::mbar_wait(bar_full + 8 * stage, (u / G::kStages) & 1, p.err, 0x51);
+      if (!dead) dead = !tc::mbar_wait_quiet(bar_full + 8 * stage, (u / G::kStages) & 1, p.err, 0x51);
       dead = __any_sync(0xffffffffu, dead);
       const int j0 = (w.tile + static_cast<int>(u - unit0)) * kTile;  // the unit's first token
       const uint32_t ks_at = base + stage * G::kStage;

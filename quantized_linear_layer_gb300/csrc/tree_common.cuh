@@ -160,7 +160,7 @@ constexpr uint32_t kInt8Bias = 0x64806480u;   // 1024 + 128
 template <int FMT>
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == QLIN_KV_INT8) {
-    w ^= 0x80808080u;
+    w ^= 0x80808080u;  // n + 128, unsigned
     lo = hsub2(__byte_perm(w, kMagic, 0x7170), kInt8Bias);
     hi = hsub2(__byte_perm(w, kMagic, 0x7372), kInt8Bias);
   } else {

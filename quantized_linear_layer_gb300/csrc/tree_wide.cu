@@ -70,7 +70,7 @@ struct Geo {
   static constexpr int kOffV = kOffK + kOperand;        // two buffers
   static constexpr int kOffRaw = kOffV + 2 * kOperand;
   static constexpr int kOffScale = kOffRaw + kStages * 2 * kRawCode;
-  static constexpr int kOffCol = kOffScale + kStages * 2 * kHalf * 4;  // [kCols][sk, log2 sv, 1 / sv][128]
+  static constexpr int kOffCol = kOffScale + kStages * 2 * kHalf * 4;  // [kCols][scale log2(e) sk, log2 sv, 1 / sv][128]
   static constexpr int kOffPair = kOffCol + kCols * 3 * kTile * 4;     // [tile parity][half][row]
   static constexpr int kOffQmax = kOffPair + 2 * 2 * kRows * 4;        // [half][row]
   static constexpr int kOffEnd = kOffQmax + 2 * kRows * 4;             // [half][row] (l, small)
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
   // all loops end and every barrier among threads is met.
   bool dead = false;
   auto wait = [&](uint32_t bar, uint32_t parity, int site) {
-    if (!dead) dead = !tc::mbar_wait(bar, parity & 1, p.err, site);
+    if (!dead) dead = !tc::mbar_wait_quiet(bar, parity & 1, p.err, site);
   };
 
   if (warp >= kLoadWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -365,12 +365,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
     W& w = reinterpret_cast<W*>(smem + G::kOffWalk)[warp];
     if (lane == 0) w = run;
     uint32_t t = 0;
-    constexpr int kLanes = G::kRowBytes / 16;      // lanes a row, 16 bytes of codes each
-    constexpr int kStep = 32 / kLanes;             // rows a warp takes at once
-    constexpr int kPieces = G::kU4 ? 4 : 2;        // 16-byte fp16 chunks a lane makes of them
-    const int c = lane % kLanes;
-    // the order in which a lane stores its chunks, so that the eight lanes of a quarter warp hit eight bank groups
-    const int flip = (G::kBlocks == 2 && c >= kLanes / 2) ? 1 : 0;
+    // A lane takes 16 bytes of codes of one row at a time and makes kPieces 16-byte chunks of fp16 of them.  Rows and
+    // chunks are dealt to lanes such that the eight lanes of a quarter warp read from, and for each piece write to,
+    // eight different bank groups through the two swizzles, and a lane's row is the same modulo 8 throughout, so
+    // that its addresses differ by constants:
+    //   rows of 128 bytes: rows r, r ^ 5 x four chunks (one 64-channel block); two blocks, then eight rows on
+    //   rows of 64 bytes, two blocks (U4): rows 0 1 6 7 or 2 3 4 5 x two chunks; 16 rows, two blocks
+    //   rows of 64 or 32 bytes, one block: consecutive rows
+    constexpr int kPieces = G::kU4 ? 4 : 2;
+    constexpr bool kPairs = G::kRowBytes == 128, kFours = G::kU4 && G::kBlocks == 2;
+    constexpr int kRowsAtOnce = G::kRowBytes == 32 || kFours ? 16 : 8;
+    int row, c;  // of the 16 rows, and the 16-byte chunk of the row (of the block)
+    if constexpr (kPairs) {
+      row = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+      c = lane & 3;
+    } else if constexpr (kFours) {
+      const int i = (lane >> 1) & 3;
+      row = 8 * (lane >> 4) + ((lane & 8) ? 2 + i : i + (i & 2) * 2);
+      c = lane & 1;
+    } else {
+      row = lane / (G::kRowBytes / 16);
+      c = lane % (G::kRowBytes / 16);
+    }
+    constexpr int kBlockBytes = G::kRowBytes / G::kBlocks;  // of a row's codes in one 64-channel block
+    const uint32_t raw_at = G::raw_chunk(row, c);
+    const uint32_t out_at = static_cast<uint32_t>(row * 128 + (((c * kPieces) ^ (row & 7)) << 4));
     while (true) {
       bool more = false;
       __syncwarp();
@@ -385,52 +404,48 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         const uint8_t* scales = smem + G::kOffScale + stage * 2 * kHalf * 4;
         // K or V (v) of this warp's tokens into `to`
         auto widen = [&](bool v, uint32_t to) {
-          const uint32_t from = raw + (v ? G::kRawCode : 0);
-          const uint8_t* sc = scales + (v ? kHalf * 4 : 0);
+          const uint32_t from = raw + (v ? G::kRawCode : 0) + (part & 3) * 16 * G::kRowBytes + raw_at;
+          const uint8_t* sc = scales + (v ? kHalf * 4 : 0) + ((part & 3) * 16 + row) * 4;
+          const uint32_t out = to + part * 16 * 128 + out_at;
+          // beyond the sequence's end lies anything: zeros for the second product
+          const int alive = v ? len - (j0 + part * 16 + row) : 16;  // of this lane's rows, those below it
           const bool tail = v && j0 + kTile > len;
+          uint4 u[G::kBlocks * 16 / kRowsAtOnce];
 #pragma unroll
-          for (int x = 0; x < 16; x += kStep) {
-            const int row = (part & 3) * 16 + x + lane / kLanes;  // of the half tile
-            const uint4 u = tc::lds128(from + G::raw_chunk(row, c));
-            uint32_t wd[4] = {u.x, u.y, u.z, u.w};
-            // beyond the sequence's end lies anything: zeros for the second product
-            const bool out = tail && j0 + h * kHalf + row >= len;
-            const uint32_t at = to + (h * kHalf + row) * 128;
-            const int sw = row & 7;
+          for (int x = 0; x < 16 / kRowsAtOnce; ++x)
+#pragma unroll
+            for (int b = 0; b < G::kBlocks; ++b)
+              u[x * G::kBlocks + b] = tc::lds128((from + x * kRowsAtOnce * G::kRowBytes) ^ (b * kBlockBytes));
+#pragma unroll
+          for (int x = 0; x < 16 / kRowsAtOnce; ++x) {
             uint32_t bias = 0;
             if constexpr (G::kU4) {
-              const uint32_t word = *reinterpret_cast<const uint32_t*>(sc + row * 4);
+              const uint32_t word = *reinterpret_cast<const uint32_t*>(sc + x * kRowsAtOnce * 4);
               // a zero-point that is not one (its token is not seen) becomes 0: what is not seen has to stay finite
               const __half z = __hmin(__hmax(__ushort_as_half(static_cast<unsigned short>(word >> 16)), __float2half(0.0f)),
                                       __float2half(15.0f));
               const __half2 zz = __half2half2(__hadd(z, __float2half(1024.0f)));
               bias = *reinterpret_cast<const uint32_t*>(&zz);
-              if (flip) {
-                uint32_t s = wd[0]; wd[0] = wd[1]; wd[1] = s;
-                s = wd[2]; wd[2] = wd[3]; wd[3] = s;
-              }
-            } else {
-              if (flip) {
-                uint32_t s = wd[0]; wd[0] = wd[2]; wd[2] = s;
-                s = wd[1]; wd[1] = wd[3]; wd[3] = s;
-              }
             }
-            const int first = c * kPieces;  // this lane's first chunk of eight channels
 #pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-              uint32_t o[4];
-              if constexpr (G::kU4) {
+            for (int b = 0; b < G::kBlocks; ++b) {
+              const uint4& r4 = u[x * G::kBlocks + b];
+              const uint32_t wd[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
-                for (int m = 0; m < 4; ++m) o[m] = hsub2(((wd[k] >> (4 * m)) & 0x000f000fu) | kMagic, bias);
-              } else {
-                widen4<FMT>(wd[2 * k], o[0], o[1]);
-                widen4<FMT>(wd[2 * k + 1], o[2], o[3]);
+              for (int k = 0; k < kPieces; ++k) {
+                uint32_t o[4];
+                if constexpr (G::kU4) {
+#pragma unroll
+                  for (int m = 0; m < 4; ++m) o[m] = hsub2(((wd[k] >> (4 * m)) & 0x000f000fu) | kMagic, bias);
+                } else {
+                  widen4<FMT>(wd[2 * k], o[0], o[1]);
+                  widen4<FMT>(wd[2 * k + 1], o[2], o[3]);
+                }
+                if (tail) {
+                  if (alive <= x * kRowsAtOnce) o[0] = o[1] = o[2] = o[3] = 0u;
+                }
+                sts128((out ^ (k << 4)) + x * kRowsAtOnce * 128 + b * 16384, o[0], o[1], o[2], o[3]);
               }
-              if (tail) {
-                if (out) o[0] = o[1] = o[2] = o[3] = 0u;
-              }
-              const int chunk = first + (k ^ flip);
-              sts128(at + (chunk >> 3) * 16384 + (((chunk & 7) ^ sw) << 4), o[0], o[1], o[2], o[3]);
             }
           }
           tc::fence_proxy_async_smem();
@@ -457,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           }
           const float rsv = rcp(sv);
           float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + part * 16 + lane;
-          col[0] = sk;
+          col[0] = sk * (p.scale * kLog2e);
           col[kTile] = lg2(sv);
           // a hidden token adds nothing to l, whatever its scale is; one that is seen makes t a NaN with it
           col[2 * kTile] = rsv < INFINITY ? rsv : 0.0f;
@@ -519,9 +534,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       q_max[half * kRows + row] = top;
       sync_pair();
       top = max(top, q_max[(half ^ 1) * kRows + row]);
+      // fp16 rows go as they are, and bf16 rows whose largest lies in [2^-4, 2^15): what fp16 drops of those is below
+      // 2^-20 of it; others by a power of two that puts the largest into [2^14, 2^15)
       int e = 0;
-      if (top > 0 && top < 0x7f800000u) e = ilogbf(__uint_as_float(top)) - 14;
-      row_scale = ldexpf(p.scale * kLog2e, e);
+      if (bf16 && top > 0 && top < 0x7f800000u) {
+        const int x = ilogbf(__uint_as_float(top));
+        if (x < -4 || x > 14) e = x - 14;
+      }
+      row_scale = ldexpf(1.0f, e);
       const float s1 = ldexpf(1.0f, -(e / 2)), s2 = ldexpf(1.0f, -(e - e / 2));
 #pragma unroll
       for (int i = 0; i < kMine / 8; ++i) {
@@ -575,6 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       uint64_t l2 = pair(0.0f, 0.0f);
       bool had_small = false;
       const int tiles = w.tiles, tile0 = w.tile;
+      // where a moved reference puts the row's largest probability: with more tiles to come, six bits below the
+      // top of fp16, which it may grow by before the row has to be rescaled
+      const float put = tiles > 1 ? 9.0f : kOffset;
       for (int i = 0; i < tiles; ++i, ++t) {
         const uint32_t buf = t & 1;
         wait(s_full + 8 * buf, t >> 1, 0x6a);
@@ -587,16 +610,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         tc::tmem_ld_32x32b_x32(s_at + half * 64 + 32, v + 32);
         tc::tmem_wait_ld();
         const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + half * 64;
-        const uint64_t rs = pair(row_scale, row_scale);
+        if (!__all_sync(0xffffffffu, row_scale == 1.0f)) {
+          const uint64_t rs = pair(row_scale, row_scale);
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) {
+            const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rs));
+            v[k] = __float_as_uint(a.x);
+            v[k + 1] = __float_as_uint(a.y);
+          }
+        }
         float hi = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 64; k += 4) {
           const float4 sk = *reinterpret_cast<const float4*>(col + k);
           const float4 ls = *reinterpret_cast<const float4*>(col + kTile + k);
-          const float2 a = unpair(fma2(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rs), pair(sk.x, sk.y),
-                                       pair(ls.x, ls.y)));
-          const float2 b = unpair(fma2(mul2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), rs),
-                                       pair(sk.z, sk.w), pair(ls.z, ls.w)));
+          const float2 a = unpair(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y), pair(ls.x, ls.y)));
+          const float2 b =
+              unpair(fma2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), pair(sk.z, sk.w), pair(ls.z, ls.w)));
           v[k] = __float_as_uint(a.x);
           v[k + 1] = __float_as_uint(a.y);
           v[k + 2] = __float_as_uint(b.x);
@@ -617,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         sync_pair();
         hi = fmaxf(hi, pair_max[buf * 2 * kRows + (half ^ 1) * kRows + row]);
         const bool move = hi > ref + (kOffset + kSlack);
-        const float to = move ? hi - kOffset : ref;
+        const float to = move ? hi - put : ref;
         const float keep = ex2(ref - to);
         ref = to;
         l2 = mul2(l2, pair(keep, keep));
@@ -642,8 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
               const __half2 p16 = flush(kv::pack2<0>(f.x, f.y));
               pk[(k + x) / 2] = *reinterpret_cast<const uint32_t*>(&p16);
               ps[(k + x) / 2] = kv::pack2<0>(s.x, s.y) & __heq2_mask(p16, __float2half2_rn(0.0f));
-              any_small |= ps[(k + x) / 2];
             }
+            any_small |= ps[k / 2] | ps[k / 2 + 1];
           }
           tc::tmem_st_32x32b_x16(s_at + half * 32 + h / 2, pk);
           tc::tmem_st_32x32b_x16(s_at + 64 + half * 32 + h / 2, ps);
