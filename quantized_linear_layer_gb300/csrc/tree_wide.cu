@@ -4,21 +4,21 @@
 // rows and a token tile 128 tokens, so that one widening of the codes serves
 // 128 rows and the products run at the full tensor rate.
 //
-// A block (one per SM) has 20 warps, whose registers are dealt out anew by role:
-//   0-7    softmax: two threads per row (tokens 0-63 and 64-127 of a tile)
-//   8-15   widen codes to fp16 in shared memory, in the tensor core's layout
-//   16     loads codes and scales by TMA into a ring of half tiles
-//   17     issues the products (one thread)
+// A block (one per SM) has 28 warps, whose registers are dealt out anew by role:
+//   0-15   softmax: four threads per row, 32 of a tile's tokens each
+//   16-23  widen codes to fp16 in shared memory, in the tensor core's layout
+//   24     loads codes and scales by TMA into a ring of half tiles
+//   25     issues the products (one thread)
 // Per token tile: S = q n^T (128 x 128, operands from shared memory) into one of
-// two tensor-memory buffers; the softmax threads read their 64 columns of it,
+// two tensor-memory buffers; the softmax threads read their 32 columns of it,
 // turn them into probabilities and write these as fp16 over the same buffer;
 // O += P u takes P from tensor memory and the codes of v from shared memory as
 // they lie (tokens x channels, the operand's other major order), so neither K
 // nor V is transposed.  S of the next tile is issued before P u of this one,
 // so the tensor cores work while the softmax of a tile runs.
 //
-// The two threads of a row agree on the reference through shared memory; when
-// it moves, each rescales half of the row of O in tensor memory, after its
+// The four threads of a row agree on the reference through shared memory; when
+// it moves, each rescales a quarter of the row of O in tensor memory, after its
 // probabilities are written, when P u of the tile before is done.
 // Probabilities below fp16's normal range are written apart, times 2^29, into
 // the buffer's other half, and go to a second accumulator O2 (o = O + 2^-29 O2)
@@ -42,13 +42,15 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kTile = 128;
 constexpr int kHalf = 64;  // tokens of a stage of the ring
-constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kSubs = kSoftmaxWarps / 4;  // threads of a row
+constexpr int kSpan = kTile / kSubs;      // tokens of each
 constexpr int kWidenWarps = 8;
 constexpr int kLoadWarp = kSoftmaxWarps + kWidenWarps;
 constexpr int kMmaWarp = kLoadWarp + 1;
-constexpr int kThreads = 32 * 20;  // whole groups of four warps
-// Registers: 640 threads are launched with 96 each, 61440 in all; 256 x 144 + 256 x 72 + 128 x 40 = 60416.
-constexpr int kSoftmaxRegs = 144, kWidenRegs = 72, kOtherRegs = 40;
+constexpr int kThreads = 32 * 28;  // whole groups of four warps
+// Registers: 896 threads are launched with 72 each, 64512 in all; 512 x 88 + 256 x 56 + 128 x 40 = 64512.
+constexpr int kSoftmaxRegs = 88, kWidenRegs = 56, kOtherRegs = 40;
 constexpr int kStages = 4;
 constexpr int kCols = 4;  // buffers of the tokens' scales: see the widening warps
 constexpr float kShiftUp = 536870912.0f;              // 2^29: the small probabilities lie below 2^15
@@ -71,10 +73,10 @@ struct Geo {
   static constexpr int kOffRaw = kOffV + 2 * kOperand;
   static constexpr int kOffScale = kOffRaw + kStages * 2 * kRawCode;
   static constexpr int kOffCol = kOffScale + kStages * 2 * kHalf * 4;  // [kCols][scale log2(e) sk, log2 sv, 1 / sv][128]
-  static constexpr int kOffPair = kOffCol + kCols * 3 * kTile * 4;     // [tile parity][half][row]
-  static constexpr int kOffQmax = kOffPair + 2 * 2 * kRows * 4;        // [half][row]
-  static constexpr int kOffEnd = kOffQmax + 2 * kRows * 4;             // [half][row] (l, small)
-  static constexpr int kOffBar = kOffEnd + 2 * kRows * 8;
+  static constexpr int kOffPair = kOffCol + kCols * 3 * kTile * 4;     // [tile parity][thread of the row][row]
+  static constexpr int kOffQmax = kOffPair + 2 * kSubs * kRows * 4;    // [thread of the row][row]
+  static constexpr int kOffEnd = kOffQmax + kSubs * kRows * 4;         // [thread of the row][row] (l, small)
+  static constexpr int kOffBar = kOffEnd + kSubs * kRows * 8;
   static constexpr int kBars = 2 * kStages + 1 + 1 + 2 + 2 + 2 + 2 + 1 + kCols;
   static constexpr int kOffMisc = kOffBar + kBars * 8;  // tensor memory address, flags
   static constexpr int kOffScan = kOffMisc + 16;
@@ -496,15 +498,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
   } else {
     // ---------------- softmax ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int quad = warp & 3, half = warp >> 2;
+    const int quad = warp & 3, sub = warp >> 2;
     const int row = quad * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    constexpr int kMine = D / 2;  // channels of q and o that this thread takes
-    float* pair_max = reinterpret_cast<float*>(smem + G::kOffPair);
+    constexpr int kMine = D / kSubs;  // channels of q and o that this thread takes
+    float* row_max = reinterpret_cast<float*>(smem + G::kOffPair);
     uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + G::kOffQmax);
     float2* ends = reinterpret_cast<float2*>(smem + G::kOffEnd);
     W& w = reinterpret_cast<W*>(smem + G::kOffWalk)[warp];
-    auto sync_pair = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };  // the two warps of these rows
+    auto sync_rows = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + quad), "n"(32 * kSubs) : "memory"); };  // the warps of these rows
 
     // What is left to do for a segment once its last product is issued, and what its rows are.
     struct Segment {
@@ -513,14 +515,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       bool begins, ends;
     };
 
-    // q of this thread's half row, scaled by a power of two, into shared memory; the factor to undo it
+    // q of this thread's part of the row, scaled by a power of two, into shared memory; the factor to undo it
     auto stage_q = [&](const Segment& g, float& row_scale) {
       const int at = g.row_tile * kRows + row;
       const bool live = g.node < g.s.nodes;
       uint4 raw[kMine / 8];
       uint32_t top = 0;
       const bool bf16 = p.dtype == QLIN_BF16;
-      const uint8_t* src = p.q + (g.s.q_row + g.node) * p.qt + (g.head * p.group + at - g.node * p.group) * p.qh + half * kMine * 2;
+      const uint8_t* src = p.q + (g.s.q_row + g.node) * p.qt + (g.head * p.group + at - g.node * p.group) * p.qh + sub * kMine * 2;
 #pragma unroll
       for (int i = 0; i < kMine / 8; ++i) {
         raw[i] = live ? ldg_v4(src + i * 16) : make_uint4(0u, 0u, 0u, 0u);
@@ -531,9 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
         }
       }
-      q_max[half * kRows + row] = top;
-      sync_pair();
-      top = max(top, q_max[(half ^ 1) * kRows + row]);
+      q_max[sub * kRows + row] = top;
+      sync_rows();
+#pragma unroll
+      for (int x = 1; x < kSubs; ++x) top = max(top, q_max[(sub ^ x) * kRows + row]);
       // fp16 rows go as they are, and bf16 rows whose largest lies in [2^-4, 2^15): what fp16 drops of those is below
       // 2^-20 of it; others by a power of two that puts the largest into [2^14, 2^15)
       int e = 0;
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           f[2 * k] = v.x * s1 * s2;
           f[2 * k + 1] = v.y * s1 * s2;
         }
-        const int chunk = half * (kMine / 8) + i;
+        const int chunk = sub * (kMine / 8) + i;
         const uint32_t to = base + G::kOffQ + (chunk >> 3) * 16384 + half_chunk(row, chunk & 7);
         if constexpr (G::kU4)  // the order in which 4-bit codes are widened
           sts128(to, kv::pack2<0>(f[0], f[4]), kv::pack2<0>(f[1], f[5]), kv::pack2<0>(f[2], f[6]), kv::pack2<0>(f[3], f[7]));
@@ -605,15 +608,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         dead = __any_sync(0xffffffffu, dead);
         tc::tc_fence_after();
         const uint32_t s_at = lanes + buf * 128;
-        uint32_t v[64];
-        tc::tmem_ld_32x32b_x32(s_at + half * 64, v);
-        tc::tmem_ld_32x32b_x32(s_at + half * 64 + 32, v + 32);
+        uint32_t v[kSpan];
+        tc::tmem_ld_32x32b_x32(s_at + sub * kSpan, v);
         tc::tmem_wait_ld();
-        const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + half * 64;
+        const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + sub * kSpan;
         if (!__all_sync(0xffffffffu, row_scale == 1.0f)) {
           const uint64_t rs = pair(row_scale, row_scale);
 #pragma unroll
-          for (int k = 0; k < 64; k += 2) {
+          for (int k = 0; k < kSpan; k += 2) {
             const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rs));
             v[k] = __float_as_uint(a.x);
             v[k + 1] = __float_as_uint(a.y);
@@ -621,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         }
         float hi = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 64; k += 4) {
+        for (int k = 0; k < kSpan; k += 4) {
           const float4 sk = *reinterpret_cast<const float4*>(col + k);
           const float4 ls = *reinterpret_cast<const float4*>(col + kTile + k);
           const float2 a = unpair(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y), pair(ls.x, ls.y)));
@@ -632,20 +634,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           v[k + 2] = __float_as_uint(b.x);
           v[k + 3] = __float_as_uint(b.y);
         }
-        const int first = (tile0 + i) * kTile + half * 64 - g.s.ctx;  // the node that column 0 is
-        if (first > -64) {
-          const uint64_t seen = seen_bits(p, g.s, g.node, first);
+        const int first = (tile0 + i) * kTile + sub * kSpan - g.s.ctx;  // the node that column 0 is
+        if (first > -kSpan) {
+          const uint32_t seen = static_cast<uint32_t>(seen_bits(p, g.s, g.node, first));
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (!((static_cast<uint32_t>(seen) >> k) & 1u)) v[k] = 0xff800000u;
-            if (!((static_cast<uint32_t>(seen >> 32) >> k) & 1u)) v[32 + k] = 0xff800000u;
-          }
+          for (int k = 0; k < kSpan; ++k)
+            if (!((seen >> k) & 1u)) v[k] = 0xff800000u;
         }
 #pragma unroll
-        for (int k = 0; k < 64; ++k) hi = fmaxf(hi, __uint_as_float(v[k]));
-        pair_max[buf * 2 * kRows + half * kRows + row] = hi;
-        sync_pair();
-        hi = fmaxf(hi, pair_max[buf * 2 * kRows + (half ^ 1) * kRows + row]);
+        for (int k = 0; k < kSpan; ++k) hi = fmaxf(hi, __uint_as_float(v[k]));
+        float* maxima = row_max + buf * kSubs * kRows + row;
+        maxima[sub * kRows] = hi;
+        sync_rows();
+#pragma unroll
+        for (int x = 1; x < kSubs; ++x) hi = fmaxf(hi, maxima[(sub ^ x) * kRows]);
         const bool move = hi > ref + (kOffset + kSlack);
         const float to = move ? hi - put : ref;
         const float keep = ex2(ref - to);
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         const uint64_t nref = pair(-ref, -ref), up = pair(kShiftUp, kShiftUp);
         uint32_t any_small = 0;
 #pragma unroll
-        for (int h = 0; h < 64; h += 32) {
+        for (int h = 0; h < kSpan; h += 32) {
           uint32_t pk[16], ps[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
@@ -675,30 +677,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
             }
             any_small |= ps[k / 2] | ps[k / 2 + 1];
           }
-          tc::tmem_st_32x32b_x16(s_at + half * 32 + h / 2, pk);
-          tc::tmem_st_32x32b_x16(s_at + 64 + half * 32 + h / 2, ps);
+          tc::tmem_st_32x32b_x16(s_at + (sub * kSpan + h) / 2, pk);
+          tc::tmem_st_32x32b_x16(s_at + 64 + (sub * kSpan + h) / 2, ps);
         }
         had_small = had_small || any_small != 0;
         if (__any_sync(0xffffffffu, any_small != 0) && lane == 0) small_tile[buf] = t + 1;
-        if (__any_sync(0xffffffffu, move) && i > 0) {  // the same in both warps of these rows
+        if (__any_sync(0xffffffffu, move) && i > 0) {  // the same in all warps of these rows
           wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x6c);
           dead = __any_sync(0xffffffffu, dead);
           tc::tc_fence_after();
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int cc = 0; cc < kMine; cc += 32) {
-              const uint32_t at = lanes + (x == 0 ? kTmemO : kTmemO2) + half * kMine + cc;
-              uint32_t o[32];
-              tc::tmem_ld_32x32b_x32(at, o);
+            for (int cc = 0; cc < kMine; cc += 16) {
+              const uint32_t at = lanes + (x == 0 ? kTmemO : kTmemO2) + sub * kMine + cc;
+              uint32_t o[16];
+              tc::tmem_ld_32x32b_x16(at, o);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; k += 2) {
+              for (int k = 0; k < 16; k += 2) {
                 const float2 f = unpair(mul2(pair(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), pair(keep, keep)));
                 o[k] = __float_as_uint(f.x);
                 o[k + 1] = __float_as_uint(f.y);
               }
-              tc::tmem_st_32x32b_x32(at, o);
+              tc::tmem_st_32x32b_x16(at, o);
             }
           }
         }
@@ -713,16 +715,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       const Segment done = g;
       const float2 lp = unpair(l2);
       float l = lp.x + lp.y;
-      ends[half * kRows + row] = make_float2(l, had_small ? 1.0f : 0.0f);
+      ends[sub * kRows + row] = make_float2(l, had_small ? 1.0f : 0.0f);
       more = next();
       if (more) {
         g = segment();
         stage_q(g, row_scale);
       }
-      sync_pair();
-      const float2 other = ends[(half ^ 1) * kRows + row];
-      l += other.x;
-      had_small = had_small || other.y != 0.0f;
+      sync_rows();
+      l = 0.0f;  // in one order for all four
+#pragma unroll
+      for (int x = 0; x < kSubs; ++x) {
+        const float2 e = ends[x * kRows + row];
+        l += e.x;
+        had_small = had_small || e.y != 0.0f;
+      }
       wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x6d);
       dead = __any_sync(0xffffffffu, dead);
       tc::tc_fence_after();
@@ -737,8 +743,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       for (int cc = 0; cc < kMine; cc += 16) {
         uint32_t o[16], s[16];
         __syncwarp();
-        tc::tmem_ld_32x32b_x16(lanes + kTmemO + half * kMine + cc, o);
-        tc::tmem_ld_32x32b_x16(lanes + kTmemO2 + half * kMine + cc, s);
+        tc::tmem_ld_32x32b_x16(lanes + kTmemO + sub * kMine + cc, o);
+        tc::tmem_ld_32x32b_x16(lanes + kTmemO2 + sub * kMine + cc, s);
         tc::tmem_wait_ld();
         float f[16];
 #pragma unroll
@@ -749,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           f[to] = (__uint_as_float(o[k]) + (had_small ? __uint_as_float(s[k]) * kShiftDown : 0.0f)) * inv;
         }
         if (!live) continue;
-        const int ch = half * kMine + cc;
+        const int ch = sub * kMine + cc;
         if (whole) {
           uint8_t* to = p.out + tok * p.ot + head * p.oh + ch * 2;
 #pragma unroll
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(to + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
         }
       }
-      if (live && half == 0) {
+      if (live && sub == 0) {
         if (!whole) p.part_ml[slot] = make_float2(m, l);
         else if (p.lse != nullptr) p.lse[tok * p.hq + head] = (lg2(l) + (m - kOffset)) * kLn2;
       }
