@@ -79,12 +79,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t
   return true;
 }
 
-// mbar_wait for many waiting warps beside busy ones: the wait itself suspends
-// the warp for as long as the hardware sees fit, and the clock is read only
-// every 64 tries, so that waiting takes few issue slots.
+// mbar_wait in few instructions, for kernels whose roles wait in many places
+// and share the SM's instruction cache: bounded by the number of tries (each
+// suspends the warp for as long as the hardware sees fit), tens of
+// milliseconds at the least.
 __device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity, int32_t* err, int site) {
-  long long t0 = 0;
-  for (uint32_t tries = 0;; ++tries) {
+#pragma unroll 1
+  for (int tries = 0; tries < (1 << 20); ++tries) {
     uint32_t ok;
     asm volatile(
         "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
@@ -92,15 +93,9 @@ __device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity, i
         : "r"(bar), "r"(parity)
         : "memory");
     if (ok) return true;
-    if ((tries & 63u) == 0) {
-      if (tries == 0) {
-        t0 = clock64();
-      } else if (clock64() - t0 > kWaitTimeoutCycles) {
-        record_device_error(err, kDevErrTimeoutBase + site);
-        return false;
-      }
-    }
   }
+  record_device_error(err, kDevErrTimeoutBase + site);
+  return false;
 }
 
 // Bounded wait that sleeps `ns` nanoseconds between polls: for threads with

@@ -237,17 +237,14 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // the largest magnitude to [2^14, 2^15); rows of zeros, infinities or NaN as they are
-      int e = 0;
-      if (top > 0 && top < 0x7f800000u) e = ilogbf(__uint_as_float(top)) - 14;
-      row_scale[i] = ldexpf(p.scale * kLog2e, e);
-      // 2^-e in two factors, each a normal float for every e of a 16-bit row
-      const float s1 = ldexpf(1.0f, -(e / 2)), s2 = ldexpf(1.0f, -(e - e / 2));
+      const int e = row_exponent(top);
+      row_scale[i] = p.scale * kLog2e * power_of_two(e);
+      const float down = power_of_two(-e);
       uint16_t q16[D / 4];
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         const float2 f = bf16 ? kv::unpack2<1>(raw[c]) : kv::unpack2<0>(raw[c]);
-        const uint32_t u = kv::pack2<0>(f.x * s1 * s2, f.y * s1 * s2);
+        const uint32_t u = kv::pack2<0>(f.x * down, f.y * down);
         q16[2 * c] = static_cast<uint16_t>(u);
         q16[2 * c + 1] = static_cast<uint16_t>(u >> 16);
       }

@@ -153,6 +153,17 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// The exponent e, in [-126, 113], for which 2^-e puts the largest magnitude of a
+// row of 16-bit numbers (`top`, the bits of a float32) into [2^14, 2^15), or
+// below it for rows of less than 2^-112; 0 for rows of zeros and rows that hold
+// an infinity or a NaN.
+__device__ __forceinline__ int row_exponent(uint32_t top) {
+  if (top == 0 || top >= 0x7f800000u) return 0;
+  return max(static_cast<int>(top >> 23) - 127 - 14, -126);
+}
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 constexpr uint32_t kMagic = 0x64006400u;      // 1024 in both halves: 1024 + n is 0x6400 | n
 constexpr uint32_t kInt8Bias = 0x64806480u;   // 1024 + 128
 
