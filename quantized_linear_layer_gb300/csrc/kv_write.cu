@@ -1,12 +1,15 @@
 // Head norms and the position rotation of q and k in one pass, with k and v
 // quantized into the paged cache in the same pass when there is one.
 //
-// A row is one head of one token, D 16-bit elements, held by D / 8 lanes of
-// eight elements (one 16-byte load each).  A block takes kRows consecutive
-// rows of the flat (token, head) order per step: D / 8 lanes x kUnroll rows
-// per lane group.  While a step's loads are under way the block works out the
-// angles of the next step's tokens into the other of two buffers; then it
-// finishes the step's rows and issues the next loads; one barrier a step.
+// A row is one head of one token, D 16-bit elements, held by a group of D / 8
+// lanes, eight elements each, as two pieces of four: a lane's pieces are the two
+// sides of four rotated pairs (halves: channels 4 l .. and rot / 2 + 4 l ..;
+// interleaved: eight consecutive channels), so that the rotation exchanges
+// nothing between lanes, and a lane needs four angles whatever the head.  A
+// group takes one token's heads `parts` apart (all of them, or a share where
+// there are few tokens): it works out its lanes' four sines and cosines once per
+// token and keeps them and the gammas in registers over the heads, the next rows
+// loaded ahead.
 //
 // Angles: a position times inv_freq, modulo a full turn.  The frequency in
 // turns is kept as a 64-bit fraction (worked out once per block in float64);
@@ -32,7 +35,13 @@ namespace qlin {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // rows per lane group and step: 64 bytes in flight per thread
+// Rows a group takes at once, and blocks that share an SM.  Rotation alone does little per row, so two rows at once and
+// 80 registers; quantizing fills a warp's issue slots by itself, and the shorter code and a fourth block count for
+// more.  Rotation of 8192 tokens x 40 heads of 128: 39.3 us at two rows and three blocks, 45.5 at one and four.
+// Appending 6835 tokens x 96 heads: 92.5 and 90.4 us; 64 tokens x 48 heads: 8.5 and 7.1 us.
+__host__ __device__ constexpr int unroll_of(int fmt) { return fmt < 0 ? 2 : 1; }
+__host__ __device__ constexpr int blocks_of(int fmt) { return fmt < 0 ? 3 : 4; }
+constexpr int kFlat = 2;  // rows a group of the plain write takes at once
 constexpr float kRoundMagic = 12582912.0f;  // 1.5 x 2^23
 constexpr float kScaleFloor = 5.42101086e-20f;  // 2^-64
 
@@ -45,14 +54,13 @@ struct Params {
   int64_t qt, qh, kt, kh, vt, vh, qot, qoh, kot, koh;  // strides in bytes
   int32_t hq, hk, hv;  // heads of q, k and v (0: absent)
   int32_t heads;       // their sum
-  uint32_t magic;      // ceil(2^32 / heads) where at x magic / 2^32 is exact for every `at` of a step, or 0
+  int32_t parts;       // groups that share a token's heads
   int64_t T;
   const int64_t* positions;
   const double* inv_freq;
   const void* q_gamma;
   const void* k_gamma;
   int32_t half_rot, interleaved;
-  int32_t step_tokens;  // tokens that one step of a block can touch
   float eps;
   const int64_t* slots;
   kv::CacheView cache;
@@ -74,11 +82,12 @@ __device__ __forceinline__ float divide(float x, float d, float r) {
   return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
 }
 
-// Quantizes the row held by this group of lanes (eight values each) and
-// writes its codes and scale.  All lanes of the warp call it (shuffles);
-// `write` says whether this group's row is stored.
-template <int FMT, int LANES>
-__device__ __forceinline__ void quantize_row(const float* y, int lane, bool write, uint8_t* codes, uint8_t* scale_at) {
+// Quantizes the row held by this group of lanes (four values from channel ca
+// on, four from cb on each; JOINED: cb = ca + 4) and writes its codes and scale.  All lanes of the
+// warp call it (shuffles); `write` says whether this group's row is stored.
+template <int FMT, int LANES, bool JOINED>
+__device__ __forceinline__ void quantize_row(const float* y, int lane, int ca, int cb, bool write, uint8_t* codes,
+                                             uint8_t* scale_at) {
   uint32_t amax_bits = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax_bits = max(amax_bits, __float_as_uint(y[i]) & 0x7fffffffu);
@@ -109,7 +118,13 @@ __device__ __forceinline__ void quantize_row(const float* y, int lane, bool writ
       packed |= (__float_as_uint((n + kRoundMagic) + z) & 15u) << (4 * i);
     }
     if (write) {
-      *reinterpret_cast<uint32_t*>(codes + 4 * lane) = finite ? packed : 0u;
+      if (!finite) packed = 0;
+      if constexpr (JOINED) {
+        *reinterpret_cast<uint32_t*>(codes + ca / 2) = packed;
+      } else {
+        *reinterpret_cast<uint16_t*>(codes + ca / 2) = static_cast<uint16_t>(packed);
+        *reinterpret_cast<uint16_t*>(codes + cb / 2) = static_cast<uint16_t>(packed >> 16);
+      }
       if (lane == 0) {
         const uint32_t word = static_cast<uint32_t>(__half_as_ushort(s16)) |
                               (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(z))) << 16);
@@ -140,7 +155,13 @@ __device__ __forceinline__ void quantize_row(const float* y, int lane, bool writ
       }
     }
     if (write) {
-      *reinterpret_cast<uint2*>(codes + 8 * lane) = finite ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
+      if (!finite) w[0] = w[1] = 0;
+      if constexpr (JOINED) {
+        *reinterpret_cast<uint2*>(codes + ca) = make_uint2(w[0], w[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(codes + ca) = w[0];
+        *reinterpret_cast<uint32_t*>(codes + cb) = w[1];
+      }
       if (lane == 0) *reinterpret_cast<float*>(scale_at) = finite ? s : __uint_as_float(0x7fc00000u);
     }
   }
@@ -148,208 +169,264 @@ __device__ __forceinline__ void quantize_row(const float* y, int lane, bool writ
 
 // DT: 0 fp16, 1 bf16.  FMT: the cache's format, or -1 without a cache.
 template <int DT, int D, int FMT>
-__global__ void __launch_bounds__(kThreads) norm_rope_write_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, blocks_of(FMT)) norm_rope_write_kernel(const __grid_constant__ Params p) {
   constexpr int LANES = D / 8;
   constexpr int kGroups = kThreads / LANES;
-  constexpr int kRows = kGroups * kUnroll;
-  // [D / 2 fractions of a turn][gammas of q and k as float, D each][two buffers of angles]
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint64_t* freq = reinterpret_cast<uint64_t*>(smem);
-  float* gammas = reinterpret_cast<float*>(freq + D / 2);
-  float* trig = gammas + 2 * D;
-  const int per_token = 2 * p.half_rot;  // cosines, then sines; see trig_at
-  const int per_buffer = per_token * p.step_tokens;
-
+  constexpr int kUnroll = unroll_of(FMT);
+  __shared__ __align__(16) uint64_t freq[D / 2];  // fractions of a turn
   const int lane = threadIdx.x % LANES;
-  const int group = threadIdx.x / LANES;
-  const int64_t rows = p.T * p.heads;
-  const bool normed = p.q_gamma != nullptr || p.k_gamma != nullptr;
+  const int hqk = p.hq + p.hk;
+
+  // this lane's channels: ca .. ca + 3 and cb .. cb + 3
+  const bool turns = 4 * lane < p.half_rot;
+  int ca = 8 * lane, cb = ca + 4;
+  if (turns && !p.interleaved) {
+    ca = 4 * lane;
+    cb = p.half_rot + 4 * lane;
+  }
 
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
-  int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows;
-  int64_t t0 = 0;                        // the first row's token
-  int32_t tok[kUnroll], head[kUnroll];   // token after t0; head in the order q, k, v (-1: no row)
-  uint4 raw[kUnroll];
-  int64_t slot[kUnroll];
-  auto load_rows = [&]() {
-    t0 = row0 / p.heads;
-    const int32_t h0 = static_cast<int32_t>(row0 - t0 * p.heads);
+  const int64_t tasks = p.T * p.parts;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kGroups;
+  int64_t task = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / LANES;
+  int64_t t;
+  int part;
+  auto locate = [&]() {  // the task's token and share of its heads
+    t = tasks <= 0xffffffffll ? static_cast<uint32_t>(task) / static_cast<uint32_t>(p.parts) : task / p.parts;
+    part = static_cast<int>(task - t * p.parts);
+  };
+  locate();
+  int64_t pos = 0;
+  if (p.half_rot > 0 && t < p.T) pos = p.positions[t];
+
+  // the gammas of this lane's channels
+  float gq[8], gk[8];
+  {
+    const int c[2] = {ca, cb};
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int32_t at = h0 + group + u * kGroups;
-      tok[u] = p.magic == 0 ? at / p.heads : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(at), p.magic));
-      head[u] = at - tok[u] * p.heads;
-      slot[u] = -1;
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      const int64_t t = t0 + tok[u];
-      if (t >= p.T) {
-        head[u] = -1;
-      } else {
-        const uint8_t* src;
-        if (head[u] < p.hq) {
-          src = p.q + t * p.qt + head[u] * p.qh;
-        } else {
-          const int32_t h = head[u] - p.hq;
-          src = h < p.hk ? p.k + t * p.kt + h * p.kh : p.v + t * p.vt + (h - p.hk) * p.vh;
-          if constexpr (FMT >= 0) slot[u] = p.slots[t];
-        }
-        raw[u] = *reinterpret_cast<const uint4*>(src + lane * 16);
-      }
-    }
-  };
-  load_rows();
-
-  for (int i = threadIdx.x; i < p.half_rot; i += kThreads) {
-    const double turns = p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    freq[i] = static_cast<uint64_t>((turns - floor(turns)) * 18446744073709551616.0);
-  }
-  if (normed) {
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-      const void* from = i < D ? p.q_gamma : p.k_gamma;
-      if (from != nullptr) gammas[i] = load_elem<DT>(from, i < D ? i : i - D);
+    for (int i = 0; i < 8; ++i) {
+      gq[i] = p.q_gamma != nullptr ? load_elem<DT>(p.q_gamma, c[i / 4] + i % 4) : 1.0f;
+      gk[i] = p.k_gamma != nullptr ? load_elem<DT>(p.k_gamma, c[i / 4] + i % 4) : 1.0f;
     }
   }
-  // Where the cosine of frequency i lies in a token's block (its sine half_rot behind).  Halves: the four
-  // that a lane reads at once are together, lanes 16 bytes apart, free of bank conflicts.
-  auto trig_at = [&](int i) {
-    return p.interleaved ? i : ((i >> 2) & 1) * (p.half_rot / 2) + (i >> 3) * 4 + (i & 3);
-  };
-  auto angles = [&](int64_t row0, float* to) {
-    const int64_t t0 = row0 / p.heads;
-    const int64_t last = min(rows - 1, row0 + kRows - 1) / p.heads;
-    const int count = static_cast<int>(last - t0 + 1) * p.half_rot;
-    for (int i = threadIdx.x; i < count; i += kThreads) {
-      const int j = i / p.half_rot, f = i - j * p.half_rot;
-      const uint64_t turn = static_cast<uint64_t>(p.positions[t0 + j]) * freq[f];
-      float s, c;  // the fraction of a turn, as a signed number of half turns
-      sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 1.08420217e-19f, &s, &c);  // 2^-63
-      float* at = to + j * per_token + trig_at(f);
-      at[0] = c;
-      at[p.half_rot] = s;
-    }
-  };
-
-  if (p.half_rot > 0 || normed) __syncthreads();  // freq and gammas are there
   if (p.half_rot > 0) {
-    angles(row0, trig);
+    for (int i = threadIdx.x; i < p.half_rot; i += kThreads) {
+      const double x = p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+      freq[i] = static_cast<uint64_t>((x - floor(x)) * 18446744073709551616.0);
+    }
     __syncthreads();
   }
-  for (int buffer = 0;; buffer ^= 1) {
-    if (p.half_rot > 0 && row0 + stride < rows) angles(row0 + stride, trig + (buffer ^ 1) * per_buffer);
 
+  // The rows of one kind, from head `h` of the task on, kUnroll at once and as many loaded ahead; `finish(row, head,
+  // live)` takes each.  All groups of the warp go round together (the shuffles need every lane).
+  auto rows = [&](int& h, int count, bool live, const uint8_t* base, int64_t pitch, auto finish) {
+    uint4 next[kUnroll];
+    auto load = [&](int at) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t t = t0 + tok[u];
-      const bool is_q = head[u] >= 0 && head[u] < p.hq;
-      const bool is_k = head[u] >= p.hq && head[u] < p.hq + p.hk;
-      float y[8];
-      kv::unpack8<DT>(raw[u], y);
-
-      if (normed) {  // uniform: the shuffles below need every lane
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if ((is_q && p.q_gamma != nullptr) || (is_k && p.k_gamma != nullptr)) {
-          const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
-          const float4* g4 = reinterpret_cast<const float4*>(gammas + (is_q ? 0 : D) + lane * 8);
-          const float4 ga = g4[0], gb = g4[1];
-          const float g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * g[i];
+      for (int u = 0; u < kUnroll; ++u) {
+        const int head = at + u * p.parts;
+        uint2 a = make_uint2(0u, 0u), b = a;
+        if (live && head < count) {
+          const uint8_t* src = base + head * pitch;
+          a = *reinterpret_cast<const uint2*>(src + 2 * ca);
+          b = *reinterpret_cast<const uint2*>(src + 2 * cb);
         }
+        next[u] = make_uint4(a.x, a.y, b.x, b.y);
       }
-
-      if (p.half_rot > 0) {
-        const float* cs = trig + buffer * per_buffer + tok[u] * per_token;
-        if (p.interleaved) {
-          const int c0 = lane * 4;  // this lane's first frequency
-          if ((is_q || is_k) && c0 < p.half_rot) {
-            const float4 c = *reinterpret_cast<const float4*>(cs + c0);
-            const float4 s = *reinterpret_cast<const float4*>(cs + p.half_rot + c0);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+    };
+    load(h);
+    while (__any_sync(0xffffffffu, live && h < count)) {
+      uint4 raw[kUnroll];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = y[2 * i], b = y[2 * i + 1];
-              y[2 * i] = a * cc[i] - b * sn[i];
-              y[2 * i + 1] = b * cc[i] + a * sn[i];
-            }
-          }
-        } else {
-          const int step = p.half_rot / 8;  // lanes between the two of a pair
-          const bool first = lane < step, second = lane >= step && lane < 2 * step;
-          const int from = (threadIdx.x & 31) + (first ? step : second ? -step : 0);
-          float o[8];
+      for (int u = 0; u < kUnroll; ++u) raw[u] = next[u];
+      load(h + kUnroll * p.parts);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, y[i], from);
-          if ((is_q || is_k) && (first || second)) {
-            const float* at = cs + 4 * (first ? lane : lane - step);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 c = *reinterpret_cast<const float4*>(at + h * (p.half_rot / 2));
-              const float4 s = *reinterpret_cast<const float4*>(at + h * (p.half_rot / 2) + p.half_rot);
-              const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                y[4 * h + i] = y[4 * h + i] * cc[i] + (first ? -o[4 * h + i] : o[4 * h + i]) * sn[i];
-            }
-          }
-        }
+      for (int u = 0; u < kUnroll; ++u) {
+        float y[8];
+        kv::unpack8<DT>(raw[u], y);
+        const int head = h + u * p.parts;
+        finish(y, head, live && head < count);
       }
-
-      if (is_q && p.q_out != nullptr)
-        *reinterpret_cast<uint4*>(p.q_out + t * p.qot + head[u] * p.qoh + lane * 16) = kv::pack8<DT>(y);
-      if (is_k && p.k_out != nullptr)
-        *reinterpret_cast<uint4*>(p.k_out + t * p.kot + (head[u] - p.hq) * p.koh + lane * 16) = kv::pack8<DT>(y);
-
-      if constexpr (FMT >= 0) {
-        bool write = head[u] >= p.hq && slot[u] >= 0;
-        const int64_t page = slot[u] >> p.cache.page_shift;
-        if (write && page >= p.cache.pages) {
-          record_device_error(p.err, kDevErrBadIndex);
-          write = false;
-        }
-        if (__any_sync(0xffffffffu, write)) {
-          const int32_t h = is_k ? head[u] - p.hq : head[u] - p.hq - p.hk;
-          const int64_t row = (static_cast<int64_t>(h) << p.cache.page_shift) +
-                              (slot[u] & ((int64_t(1) << p.cache.page_shift) - 1));
-          uint8_t* codes = (is_k ? p.cache.k : p.cache.v) + page * p.cache.page_stride + row * kv::row_bytes(FMT, D);
-          uint8_t* scale = (is_k ? p.cache.k_scale : p.cache.v_scale) + page * p.cache.scale_page_stride + row * 4;
-          quantize_row<FMT, LANES>(y, lane, write, codes, scale);
-        }
+      h += kUnroll * p.parts;
+    }
+    // the first of this task's heads past the kind's last
+    if (h >= count) h -= (h - count) / p.parts * p.parts;
+    h -= count;
+  };
+  // Norm and rotation of a row, with the factors of the token: (a, b) -> (a fac[0..3] - b fac[4..7],
+  // b fac[8..11] + a fac[12..15]) for a lane that turns, channel by channel times fac[0..3] and fac[8..11] else.
+  auto norm_turn = [&](float* y, bool norm, const float* fac) {
+    if (norm) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= inv;
+    }
+    if (!turns) {  // not a turn by zero: its b x 0 would make NaN of an infinity, and lose a zero's sign
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] *= p.interleaved ? (i & 1 ? fac[8 + i / 2] : fac[i / 2]) : fac[i];
+        y[4 + i] *= p.interleaved ? (i & 1 ? fac[10 + i / 2] : fac[2 + i / 2]) : fac[8 + i];
+      }
+    } else if (p.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = y[2 * i], b = y[2 * i + 1];
+        y[2 * i] = fmaf(a, fac[i], -(b * fac[4 + i]));
+        y[2 * i + 1] = fmaf(b, fac[8 + i], a * fac[12 + i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = y[i], b = y[4 + i];
+        y[i] = fmaf(a, fac[i], -(b * fac[4 + i]));
+        y[4 + i] = fmaf(b, fac[8 + i], a * fac[12 + i]);
       }
     }
-    row0 += stride;
-    if (row0 >= rows) break;
-    load_rows();
-    if (p.half_rot > 0) __syncthreads();
+  };
+
+  while (__any_sync(0xffffffffu, task < tasks)) {
+    const bool live = task < tasks;
+    int64_t slot = -1;
+    if constexpr (FMT >= 0) {
+      if (live) slot = p.slots[t];
+    }
+    float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {};
+    if (turns && live && part < hqk) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t turn = static_cast<uint64_t>(pos) * freq[4 * lane + i];
+        // the fraction of a turn, as a signed number of half turns
+        sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 1.08420217e-19f, &sn[i], &cs[i]);  // 2^-63
+      }
+    }
+    auto factors = [&](const float* g, float* fac) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ga = p.interleaved ? g[2 * i] : g[i], gb = p.interleaved ? g[2 * i + 1] : g[4 + i];
+        fac[i] = ga * cs[i];
+        fac[4 + i] = gb * sn[i];
+        fac[8 + i] = gb * cs[i];
+        fac[12 + i] = ga * sn[i];
+      }
+    };
+    auto store_row = [&](uint8_t* to, const float* y) {
+      const uint4 o = kv::pack8<DT>(y);
+      *reinterpret_cast<uint2*>(to + 2 * ca) = make_uint2(o.x, o.y);
+      *reinterpret_cast<uint2*>(to + 2 * cb) = make_uint2(o.z, o.w);
+    };
+    // this token's place in the cache
+    const int64_t page = slot >> p.cache.page_shift;
+    const bool stored = slot >= 0 && page < p.cache.pages;
+    if (FMT >= 0 && slot >= 0 && !stored) record_device_error(p.err, kDevErrBadIndex);
+    auto quantize = [&](const float* y, int head, bool there, uint8_t* codes, uint8_t* scale) {
+      if constexpr (FMT >= 0) {
+        const int64_t row = (static_cast<int64_t>(head) << p.cache.page_shift) +
+                            (slot & ((int64_t(1) << p.cache.page_shift) - 1));
+        quantize_row<FMT, LANES, false>(y, lane, ca, cb, there && stored,
+                                 codes + page * p.cache.page_stride + row * kv::row_bytes(FMT, D),
+                                 scale + page * p.cache.scale_page_stride + row * 4);
+      }
+    };
+
+    int h = part;
+    float fac[16];
+    factors(gq, fac);
+    rows(h, p.hq, live, p.q + t * p.qt, p.qh, [&](float* y, int head, bool there) {
+      norm_turn(y, p.q_gamma != nullptr, fac);
+      if (there && p.q_out != nullptr) store_row(p.q_out + t * p.qot + head * p.qoh, y);
+    });
+    factors(gk, fac);
+    rows(h, p.hk, live, p.k + t * p.kt, p.kh, [&](float* y, int head, bool there) {
+      norm_turn(y, p.k_gamma != nullptr, fac);
+      if (there && p.k_out != nullptr) store_row(p.k_out + t * p.kot + head * p.koh, y);
+      quantize(y, head, there, p.cache.k, p.cache.k_scale);
+    });
+    if constexpr (FMT >= 0) {
+      rows(h, p.hv, live, p.v + t * p.vt, p.vh,
+           [&](float* y, int head, bool there) { quantize(y, head, there, p.cache.v, p.cache.v_scale); });
+    }
+    task += stride;
+    locate();
+    if (p.half_rot > 0 && task < tasks) pos = p.positions[t];
+  }
+}
+
+// k and v as they are: the rows of all tokens in one flat (token, head) order, kFlat rows a group at once.
+template <int DT, int D, int FMT>
+__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ Params p) {
+  constexpr int LANES = D / 8;
+  constexpr int kGroups = kThreads / LANES;
+  const int lane = threadIdx.x % LANES;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t count = p.T * p.heads;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kGroups * kFlat;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kGroups * kFlat; row0 < count; row0 += stride) {
+    uint4 raw[kFlat];
+    int64_t slot[kFlat];
+    int head[kFlat];
+#pragma unroll
+    for (int u = 0; u < kFlat; ++u) {
+      const int64_t at = row0 + u * kGroups + threadIdx.x / LANES;
+      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      slot[u] = -1;
+      head[u] = 0;
+      if (at < count) {
+        const int64_t t = count <= 0xffffffffll ? static_cast<uint32_t>(at) / static_cast<uint32_t>(p.heads) : at / p.heads;
+        head[u] = static_cast<int>(at - t * p.heads);
+        const uint8_t* src = head[u] < p.hk ? p.k + t * p.kt + head[u] * p.kh : p.v + t * p.vt + (head[u] - p.hk) * p.vh;
+        raw[u] = *reinterpret_cast<const uint4*>(src + lane * 16);
+        slot[u] = p.slots[t];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFlat; ++u) {
+      const int64_t page = slot[u] >> p.cache.page_shift;
+      const bool stored = slot[u] >= 0 && page < p.cache.pages;
+      if (slot[u] >= 0 && !stored) record_device_error(p.err, kDevErrBadIndex);
+      float y[8];
+      kv::unpack8<DT>(raw[u], y);
+      const bool is_k = head[u] < p.hk;
+      const int64_t row = (static_cast<int64_t>(is_k ? head[u] : head[u] - p.hk) << p.cache.page_shift) +
+                          (slot[u] & ((int64_t(1) << p.cache.page_shift) - 1));
+      quantize_row<FMT, LANES, true>(y, lane, 8 * lane, 8 * lane + 4, stored,
+                                     (is_k ? p.cache.k : p.cache.v) + page * p.cache.page_stride + row * kv::row_bytes(FMT, D),
+                                     (is_k ? p.cache.k_scale : p.cache.v_scale) + page * p.cache.scale_page_stride + row * 4);
+    }
   }
 }
 
 template <int DT, int D>
 cudaError_t plan(Params p, int fmt, Prepared* out) {
-  constexpr int kRows = kThreads / (D / 8) * kUnroll;
+  constexpr int kGroups = kThreads / (D / 8);
   p.heads = p.hq + p.hk + p.hv;
-  p.magic = p.heads > 1 && p.heads <= 16384 ? static_cast<uint32_t>(((uint64_t(1) << 32) + p.heads - 1) / p.heads) : 0;
-  const int64_t steps = (p.T * p.heads + kRows - 1) / kRows;
-  // tokens that one step can touch
-  p.step_tokens = p.heads >= kRows ? 2 : (kRows + p.heads - 2) / p.heads + 1;
-  const int64_t grid = std::min<int64_t>(steps, sm_count() * 6);
-  const int buffers = steps > grid ? 2 : 1;
-  const size_t smem = D / 2 * 8 + 2 * D * 4 + 8 * static_cast<size_t>(p.half_rot) * p.step_tokens * buffers;
+  out->count = 1;
+  if (p.hq == 0 && p.half_rot == 0 && p.k_gamma == nullptr && p.k_out == nullptr && fmt >= 0) {
+    const void* fn = fmt == QLIN_KV_INT8   ? reinterpret_cast<const void*>(write_kernel<DT, D, QLIN_KV_INT8>)
+                     : fmt == QLIN_KV_E4M3 ? reinterpret_cast<const void*>(write_kernel<DT, D, QLIN_KV_E4M3>)
+                                           : reinterpret_cast<const void*>(write_kernel<DT, D, QLIN_KV_U4>);
+    const int64_t blocks = (p.T * p.heads + kGroups * kFlat - 1) / (kGroups * kFlat);
+    out->launch[0] = {fn, static_cast<uint32_t>(std::min<int64_t>(blocks, sm_count() * 8)), 1, kThreads, 0};
+    out->set(p);
+    return cudaSuccess;
+  }
+  // four tasks for every group that fits on the GPU at once, as far as there are heads to share: the angles cost
+  // about one row's work per task
+  const int64_t resident = static_cast<int64_t>(sm_count()) * blocks_of(fmt);
+  p.parts = static_cast<int32_t>(std::min<int64_t>(p.heads, (4 * resident * kGroups + p.T - 1) / p.T));
+  const int64_t blocks = (p.T * p.parts + kGroups - 1) / kGroups;
+  const int64_t grid = std::min<int64_t>(blocks, resident);
   const void* fn = fmt < 0                ? reinterpret_cast<const void*>(norm_rope_write_kernel<DT, D, -1>)
                    : fmt == QLIN_KV_INT8 ? reinterpret_cast<const void*>(norm_rope_write_kernel<DT, D, QLIN_KV_INT8>)
                    : fmt == QLIN_KV_E4M3 ? reinterpret_cast<const void*>(norm_rope_write_kernel<DT, D, QLIN_KV_E4M3>)
                                          : reinterpret_cast<const void*>(norm_rope_write_kernel<DT, D, QLIN_KV_U4>);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = ensure_max_dynamic_smem(fn);
-    if (e != cudaSuccess) return e;
-  }
-  out->count = 1;
-  out->launch[0] = {fn, static_cast<uint32_t>(grid), 1, kThreads, static_cast<uint32_t>(smem)};
+  out->launch[0] = {fn, static_cast<uint32_t>(grid), 1, kThreads, 0};
   out->set(p);
   return cudaSuccess;
 }
