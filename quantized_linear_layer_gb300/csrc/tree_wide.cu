@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         const uint32_t s_at = lanes + buf * 128;
         uint32_t v[kSpan];
         tc::tmem_ld_32x32b_x32(s_at + sub * kSpan, v);
-        tc::tmem_wait_ld();
+        tc::tmem_wait_ld(v);
         const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + sub * kSpan;
         if (!__all_sync(0xffffffffu, row_scale == 1.0f)) {
           const uint64_t rs = pair(row_scale, row_scale);
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
               const uint32_t at = lanes + (x == 0 ? kTmemO : kTmemO2) + sub * kMine + cc;
               uint32_t o[16];
               tc::tmem_ld_32x32b_x16(at, o);
-              tc::tmem_wait_ld();
+              tc::tmem_wait_ld(o);
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
                 const float2 f = unpair(mul2(pair(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), pair(keep, keep)));
@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         __syncwarp();
         tc::tmem_ld_32x32b_x16(lanes + kTmemO + sub * kMine + cc, o);
         tc::tmem_ld_32x32b_x16(lanes + kTmemO2 + sub * kMine + cc, s);
-        tc::tmem_wait_ld();
+        tc::tmem_wait_ld(o);
+        tc::tmem_wait_ld(s);
         float f[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
