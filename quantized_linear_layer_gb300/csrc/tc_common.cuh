@@ -79,21 +79,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t
   return true;
 }
 
-// mbar_wait in few instructions, for kernels whose roles wait in many places
-// and share the SM's instruction cache: bounded by the number of tries (each
-// suspends the warp for as long as the hardware sees fit), tens of
-// milliseconds at the least.
+// mbar_wait for kernels whose roles wait in many places: the clock is read once
+// in 256 tries.  The limit is one of time all the same: a try takes some tens
+// of cycles, and the device can stand still for longer than a million of those
+// (memory mapped while a kernel runs, for one).
 __device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity, int32_t* err, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
 #pragma unroll 1
-  for (int tries = 0; tries < (1 << 20); ++tries) {
-    uint32_t ok;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
+  do {
+#pragma unroll 1
+    for (int tries = 0; tries < 256; ++tries)
+      if (mbar_try_wait(bar, parity)) return true;
+  } while (clock64() - t0 <= kWaitTimeoutCycles);
   record_device_error(err, kDevErrTimeoutBase + site);
   return false;
 }
@@ -120,15 +118,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
-// 3-D TMA tile load into shared memory, completing its bytes on the mbarrier.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 

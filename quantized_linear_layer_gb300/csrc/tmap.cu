@@ -54,21 +54,4 @@ cudaError_t make_tmap_2d_u64(CUtensorMap* map, const void* base, uint64_t cols8,
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t planes,
-                            uint64_t plane_stride, uint32_t box_cols, uint32_t box_rows) {
-  std::call_once(g_encode_once, resolve_encode);
-  if (g_encode == nullptr) return g_encode_status != cudaSuccess ? g_encode_status : cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {cols, rows, planes};
-  const cuuint64_t strides[2] = {cols, plane_stride};  // bytes between rows and planes
-  const cuuint32_t box[3] = {box_cols, box_rows, 1};
-  const cuuint32_t elem_strides[3] = {1, 1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
-                        elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        box_cols == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                        : box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                         : CU_TENSOR_MAP_SWIZZLE_32B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace qlin

@@ -26,12 +26,4 @@ cudaError_t make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t cols, u
 cudaError_t make_tmap_2d_u64(CUtensorMap* map, const void* base, uint64_t cols8, uint64_t rows, uint32_t box_cols8,
                              uint32_t box_rows);
 
-// Tiled tensor map over `planes` row-major uint8 matrices of `rows` x `cols`
-// bytes (dense rows), plane_stride bytes apart (a multiple of 16), loading
-// boxes of box_rows x box_cols bytes of one plane, box_cols 32, 64 or 128:
-// 16-byte chunk c of row r is stored at chunk c ^ ((r / 4) % 2), c ^ ((r / 2)
-// % 4) or c ^ (r % 8) of the row (destination 256-, 512- or 1024-byte aligned).
-cudaError_t make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t planes,
-                            uint64_t plane_stride, uint32_t box_cols, uint32_t box_rows);
-
 }  // namespace qlin

@@ -30,9 +30,9 @@
 // sequence's result depends on the lengths, not on timing.
 //
 // A block has five compute warps (seven where registers allow) and one that
-// loads.  The loading warp keeps a ring of stages filled by TMA: one unit's
-// codes of K and V (one box per page that the tile touches, 128-, 64- or
-// 32-byte swizzled rows) and their scales.  Units go to the compute warps in
+// loads.  The loading warp keeps a ring of stages filled by asynchronous
+// copies: one unit's codes of K and V (rows of 128, 64 or 32 bytes, their
+// 16-byte chunks swizzled) and their scales.  Units go to the compute warps in
 // turn; a warp takes all rows of its unit, with its own running maximum, sums
 // and output, so that nothing but the ring lies between warps until a segment
 // ends.  Codes are widened to fp16 in registers, straight into the operand
@@ -46,7 +46,6 @@
 #include <cmath>
 #include <type_traits>
 
-#include "tmap.h"
 #include "tree_common.cuh"
 
 namespace qlin {
@@ -111,23 +110,17 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < G::kStages; ++i) {
-      tc::mbar_init(bar_full + 8 * i, 1);
+      tc::mbar_init(bar_full + 8 * i, 32);
       tc::mbar_init(bar_free + 8 * i, 1);
     }
     tc::fence_mbar_init();
-    tc::prefetch_tmap(&p.k_map);
-    tc::prefetch_tmap(&p.v_map);
   }
-  pdl_wait();
   const int share = (p.B + kThreads - 1) / kThreads;
   scan_units<kRows, kTile, kThreads>(p, share, scan);
   const int64_t total = scan[kThreads];
   const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);  // each of these has a unit or more
   if (threadIdx.x == 0) p.records[blockIdx.x].last = -1;
-  if (blockIdx.x >= blocks) {
-    pdl_launch_dependents();
-    return;
-  }
+  if (blockIdx.x >= blocks) return;
 
   auto run = begin_run<kRows, kTile, kThreads>(p, share, scan, blockIdx.x, blocks);
 
@@ -157,39 +150,25 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
             }
           }
         }
-        const int at = (t - from) * boxes;  // this unit's boxes; those past the end have no page
-        const int32_t pg = __shfl_sync(0xffffffffu, ahead, (at + lane) & 31);
-        const bool load = lane < boxes && pg >= 0;
-        const int good = __popc(__ballot_sync(0xffffffffu, load));
         if (!tc::mbar_wait_quiet(bar_free + 8 * stage, phase, p.err, 0x50)) dead = true;
         if (__any_sync(0xffffffffu, dead)) {
           dead = true;
           break;
         }
-        const uint32_t bar = bar_full + 8 * stage;
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar, good * box * (2 * G::kRowBytes + 8));
-        __syncwarp();
-        if (load) {
-          const int off = (t * kTile + lane * box) & (page - 1);
-          const int row = w.head * page + off;
-          const uint32_t kd = base + stage * G::kStage + lane * box * G::kW;
-          const int64_t so = pg * p.scale_page_stride + static_cast<int64_t>(row) * 4;
-          const uint32_t sd = base + G::kOffScale + stage * 2 * G::kScaleBytes + lane * box * 4;
-#pragma unroll
-          for (int h = 0; h < G::kSub; ++h) tc::tma_load_3d(kd + h * G::kSubBytes, &p.k_map, h * G::kW, row, pg, bar);
-          tc::bulk_load_policy(sd, p.k_scale + so, box * 4, bar, policy);
-          tc::bulk_load_policy(sd + G::kScaleBytes, p.v_scale + so, box * 4, bar, policy);
-#pragma unroll
-          for (int h = 0; h < G::kSub; ++h)
-            tc::tma_load_3d(kd + G::kCodeBytes + h * G::kSubBytes, &p.v_map, h * G::kW, row, pg, bar);
-        }
+        // this unit's boxes; those past the end have no page
+        const uint32_t codes = base + stage * G::kStage, scales = base + G::kOffScale + stage * 2 * G::kScaleBytes;
+        copy_tokens<kTile, G::kRowBytes>(p, w.head, t * kTile, box, ahead, (t - from) * boxes, codes, codes + G::kCodeBytes,
+                                         scales, scales + G::kScaleBytes, policy, [](int r, int c) {
+                                           return c / (G::kW / 16) * G::kSubBytes + G::chunk(r, c % (G::kW / 16));
+                                         });
+        copies_arrive(bar_full + 8 * stage);
         if (++stage == G::kStages) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
-    pdl_launch_dependents();
+    copies_wait();  // none outlives the block, also where a wait ran out
     return;
   }
 
@@ -562,7 +541,6 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
     if (begins && !ends && threadIdx.x == 0) p.records[blockIdx.x] = record_of(w, blocks, total);
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");  // the merge area is free again
   }
-  pdl_launch_dependents();
 }
 
 int grid_blocks(int64_t head_dim) { return sm_count() * (head_dim == 256 ? 1 : 2); }
@@ -626,13 +604,6 @@ cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out) {
   Params p = {};
   const qlin_kv_cache& c = a.cache;
   const Shape shape = shape_of(c, a.q.heads, a.max_nodes);
-  const int64_t row_bytes = kv::row_bytes(c.fmt, static_cast<int>(c.head_dim));
-  const uint32_t box_cols = static_cast<uint32_t>(std::min<int64_t>(row_bytes, 128));
-  const uint32_t box_rows = static_cast<uint32_t>(std::min<int64_t>(c.page_size, shape.wide ? 64 : kTile));
-  cudaError_t e = make_tmap_3d_u8(&p.k_map, c.k, row_bytes, c.heads * c.page_size, c.pages, c.page_stride, box_cols, box_rows);
-  if (e == cudaSuccess)
-    e = make_tmap_3d_u8(&p.v_map, c.v, row_bytes, c.heads * c.page_size, c.pages, c.page_stride, box_cols, box_rows);
-  if (e != cudaSuccess) return e;
   p.q = static_cast<const uint8_t*>(a.q.data);
   p.out = static_cast<uint8_t*>(a.out.data);
   p.qt = 2 * a.q.token_stride;
@@ -644,6 +615,9 @@ cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out) {
   p.group = p.hq / p.hk;
   p.dtype = a.dtype;
   p.Tq = a.Tq;
+  p.k = static_cast<const uint8_t*>(c.k);
+  p.v = static_cast<const uint8_t*>(c.v);
+  p.page_stride = c.page_stride;
   p.k_scale = static_cast<const uint8_t*>(c.k_scale);
   p.v_scale = static_cast<const uint8_t*>(c.v_scale);
   p.scale_page_stride = c.scale_page_stride;

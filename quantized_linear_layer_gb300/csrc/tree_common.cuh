@@ -30,15 +30,16 @@ struct Record {
 };
 
 struct Params {
-  CUtensorMap k_map, v_map;
   const uint8_t* q;
   uint8_t* out;
   int64_t qt, qh, ot, oh;  // strides in bytes
   int32_t hq, hk, group, dtype;
   int64_t Tq;
+  const uint8_t* k;
+  const uint8_t* v;
   const uint8_t* k_scale;
   const uint8_t* v_scale;
-  int64_t scale_page_stride;
+  int64_t page_stride, scale_page_stride;
   int32_t pages, page_shift;
   const int32_t* table;
   int64_t max_pages;
@@ -190,6 +191,52 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
 }
 
+// 16 bytes from global to shared memory, asynchronously; streamed codes leave L2 first.
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy)
+               : "memory");
+}
+// Arrives on `bar` (one of its expected arrivals) once this thread's copies so far are there.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// One warp's copies of TOKENS tokens, from `first` on, into a stage of a ring: K and V codes and their scales, page by
+// page.  `ahead` is the page (or -1) of box `lane` of the 32 boxes of `box` tokens that hold the stage's boxes `at` ..;
+// row_at(r, c) says where 16-byte chunk c of row r lies.  The rows of a box are contiguous in its page, so a lane's
+// chunks are 512 bytes apart.  Plain asynchronous copies: with tensor-map copies of these boxes (the same time) calls
+// failed when other memory was mapped while they ran.
+template <int TOKENS, int ROW_BYTES, class RowAt>
+__device__ __forceinline__ void copy_tokens(const Params& p, int head, int first, int box, int32_t ahead, int at,
+                                            uint32_t k_to, uint32_t v_to, uint32_t ks_to, uint32_t vs_to, uint64_t policy,
+                                            RowAt row_at) {
+  constexpr int kChunks = ROW_BYTES / 16;      // of a row
+  constexpr int kRowsAtOnce = 32 / kChunks;
+  const int lane = threadIdx.x % 32;
+  const int page = 1 << p.page_shift;
+  for (int b = 0; b * box < TOKENS; ++b) {
+    const int32_t pg = __shfl_sync(0xffffffffu, ahead, (at + b) & 31);
+    if (pg < 0) continue;
+    const int64_t row = static_cast<int64_t>(head) * page + ((first + b * box) & (page - 1));
+    const int64_t codes = pg * p.page_stride + row * ROW_BYTES + lane * 16;
+    const uint8_t* k = p.k + codes;
+    const uint8_t* v = p.v + codes;
+#pragma unroll 4
+    for (int r = 0; r < box; r += kRowsAtOnce) {
+      const uint32_t to = row_at(b * box + r + lane / kChunks, lane % kChunks);
+      copy16(k_to + to, k + r * ROW_BYTES, policy);
+      copy16(v_to + to, v + r * ROW_BYTES, policy);
+    }
+    const int at16 = lane * 16;
+    if (at16 < box * 4) {
+      const int64_t scales = pg * p.scale_page_stride + row * 4 + at16;
+      copy16(ks_to + b * box * 4 + at16, p.k_scale + scales, policy);
+      copy16(vs_to + b * box * 4 + at16, p.v_scale + scales, policy);
+    }
+  }
+}
+
 // The units before each thread's share of the sequences, into scan[THREADS + 1]
 // (share b .. b + share - 1 of thread b / share), by all threads of the block.
 template <int ROWS, int TILE, int THREADS>
@@ -261,8 +308,6 @@ static __global__ void __launch_bounds__(128) tree_attention_join_kernel(const _
   constexpr int kTeams = 128 / kLanes;
   __shared__ float4 part[kTeams][D / 4];
   __shared__ float2 part_ml[kTeams];
-  pdl_wait();
-  pdl_launch_dependents();  // not before: what comes next then starts when the attention kernel is through
   const Record rec = p.records[blockIdx.x];
   if (rec.last < 0) return;
   const int row = blockIdx.y;

@@ -7,7 +7,7 @@
 // A block (one per SM) has 28 warps, whose registers are dealt out anew by role:
 //   0-15   softmax: four threads per row, 32 of a tile's tokens each
 //   16-23  widen codes to fp16 in shared memory, in the tensor core's layout
-//   24     loads codes and scales by TMA into a ring of half tiles
+//   24     copies codes and scales into a ring of half tiles
 //   25     issues the products (one thread)
 // Per token tile: S = q n^T (128 x 128, operands from shared memory) into one of
 // two tensor-memory buffers; the softmax threads read their 32 columns of it,
@@ -32,7 +32,6 @@
 #include <algorithm>
 #include <cmath>
 
-#include "tmap.h"
 #include "tree_common.cuh"
 
 namespace qlin {
@@ -49,8 +48,8 @@ constexpr int kWidenWarps = 8;
 constexpr int kLoadWarp = kSoftmaxWarps + kWidenWarps;
 constexpr int kMmaWarp = kLoadWarp + 1;
 constexpr int kThreads = 32 * 28;  // whole groups of four warps
-// Registers: 896 threads are launched with 72 each, 64512 in all; 512 x 88 + 256 x 56 + 128 x 40 = 64512.
-constexpr int kSoftmaxRegs = 88, kWidenRegs = 56, kOtherRegs = 40;
+// Registers: 896 threads are launched with 72 each, 64512 in all; 512 x 88 + 256 x 48 + 128 x 56 = 64512.
+constexpr int kSoftmaxRegs = 88, kWidenRegs = 48, kOtherRegs = 56;
 constexpr int kStages = 4;
 constexpr int kCols = 4;  // buffers of the tokens' scales: see the widening warps
 constexpr float kShiftUp = 536870912.0f;              // 2^29: the small probabilities lie below 2^15
@@ -77,7 +76,7 @@ struct Geo {
   static constexpr int kOffQmax = kOffPair + 2 * kSubs * kRows * 4;    // [thread of the row][row]
   static constexpr int kOffEnd = kOffQmax + kSubs * kRows * 4;         // [thread of the row][row] (l, small)
   static constexpr int kOffBar = kOffEnd + kSubs * kRows * 8;
-  static constexpr int kBars = 2 * kStages + 1 + 1 + 2 + 2 + 2 + 2 + 1 + kCols;
+  static constexpr int kBars = 2 * kStages + 1 + 1 + 2 + 2 + 2 + 2 + 1 + 1 + kCols;
   static constexpr int kOffMisc = kOffBar + kBars * 8;  // tensor memory address, flags
   static constexpr int kOffScan = kOffMisc + 16;
   static constexpr int kOffWalk = (kOffScan + (kThreads + 1) * 8 + 15) / 16 * 16;
@@ -190,14 +189,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
   const uint32_t p_full = s_full + 16;      // [2]
   const uint32_t pv_done = p_full + 16;     // [2]
   const uint32_t q_full = pv_done + 16;
-  const uint32_t col_full = q_full + 8;     // [kCols]
+  const uint32_t all_done = q_full + 8;
+  const uint32_t col_full = all_done + 8;   // [kCols]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
   volatile uint32_t* small_tile = reinterpret_cast<volatile uint32_t*>(smem + G::kOffMisc + 8);  // [2]: 1 + the last tile with any
   int64_t* scan = reinterpret_cast<int64_t*>(smem + G::kOffScan);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(raw_full + 8 * i, 1);
+      tc::mbar_init(raw_full + 8 * i, 32);
       tc::mbar_init(raw_free + 8 * i, kWidenWarps / 2);
     }
     tc::mbar_init(k_full, kWidenWarps);
@@ -210,21 +210,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       small_tile[i] = 0;
     }
     tc::mbar_init(q_full, kSoftmaxWarps);
+    tc::mbar_init(all_done, 1);
     for (int i = 0; i < kCols; ++i) tc::mbar_init(col_full + 8 * i, kWidenWarps);
     tc::fence_mbar_init();
-    tc::prefetch_tmap(&p.k_map);
-    tc::prefetch_tmap(&p.v_map);
   }
-  pdl_wait();
   const int share = (p.B + kThreads - 1) / kThreads;
   scan_units<kRows, kTile, kThreads>(p, share, scan);
   const int64_t total = scan[kThreads];
   const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);  // each of these has a unit or more
   if (threadIdx.x == 0) p.records[blockIdx.x].last = -1;
-  if (blockIdx.x >= blocks) {
-    pdl_launch_dependents();
-    return;
-  }
+  if (blockIdx.x >= blocks) return;
   if (warp == kMmaWarp) {
     tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
     tc::tmem_relinquish();
@@ -268,28 +263,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
             }
           }
         }
-        const int32_t pg = __shfl_sync(0xffffffffu, ahead, ((t - from) * boxes + lane) & 31);
-        const bool load = lane < boxes && pg >= 0;
-        const int good = __popc(__ballot_sync(0xffffffffu, load));
         const uint32_t stage = n % kStages;
         if (n >= kStages) wait(raw_free + 8 * stage, n / kStages - 1, 0x60);
         dead = __any_sync(0xffffffffu, dead);
         if (dead) continue;
-        const uint32_t bar = raw_full + 8 * stage;
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar, good * box * (2 * G::kRowBytes + 8));
-        __syncwarp();
-        if (load) {
-          const int row = run.head * page + ((t * kHalf + lane * box) & (page - 1));
-          const uint32_t kd = base + G::kOffRaw + stage * 2 * G::kRawCode + lane * box * G::kRowBytes;
-          const int64_t so = pg * p.scale_page_stride + static_cast<int64_t>(row) * 4;
-          const uint32_t sd = base + G::kOffScale + stage * 2 * kHalf * 4 + lane * box * 4;
-          tc::tma_load_3d(kd, &p.k_map, 0, row, pg, bar);
-          tc::bulk_load_policy(sd, p.k_scale + so, box * 4, bar, policy);
-          tc::bulk_load_policy(sd + kHalf * 4, p.v_scale + so, box * 4, bar, policy);
-          tc::tma_load_3d(kd + G::kRawCode, &p.v_map, 0, row, pg, bar);
-        }
+        const uint32_t codes = base + G::kOffRaw + stage * 2 * G::kRawCode;
+        const uint32_t scales = base + G::kOffScale + stage * 2 * kHalf * 4;
+        copy_tokens<kHalf, G::kRowBytes>(p, run.head, t * kHalf, box, ahead, (t - from) * boxes, codes, codes + G::kRawCode,
+                                         scales, scales + kHalf * 4, policy, [](int r, int c) { return G::raw_chunk(r, c); });
+        copies_arrive(raw_full + 8 * stage);
       }
     }
+    copies_wait();  // none outlives the block, also where a wait ran out
   } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
     // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one thread issues.
@@ -354,8 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       ++seg;
     }
     second(t - 1, pending_first);
-    // every product is done before the tensor memory is given back
-    wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x66);
+    // every product is done before the tensor memory is given back, whatever else ran out
+    if (leader) tc::mma_commit(all_done);
+    __syncwarp();
+    tc::mbar_wait_quiet(all_done, 0, p.err, 0x66);
     __syncwarp();
   } else if (warp > kMmaWarp) {
     // (fills up the group)
@@ -775,7 +762,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       tc::tc_fence_before();
     }
   }
-  pdl_launch_dependents();
   tc::tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
