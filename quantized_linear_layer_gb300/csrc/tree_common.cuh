@@ -202,6 +202,21 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// One warp's copies of the scales of TOKENS tokens, from `first` on; the arguments are those of copy_tokens.
+template <int TOKENS>
+__device__ __forceinline__ void copy_scales(const Params& p, int head, int first, int box, int32_t ahead, int at,
+                                            uint32_t ks_to, uint32_t vs_to, uint64_t policy) {
+  const int lane = threadIdx.x % 32;
+  const int page = 1 << p.page_shift;
+  const int token = lane % 16 * 4;  // lanes 0-15: scales of K, 16 bytes each, then of V
+  static_assert(TOKENS == 64, "four tokens a lane");
+  const int32_t pg = __shfl_sync(0xffffffffu, ahead, (at + token / box) & 31);
+  if (pg < 0) return;
+  const int64_t row = static_cast<int64_t>(head) * page + ((first + token) & (page - 1));
+  const int64_t scales = pg * p.scale_page_stride + row * 4;
+  copy16((lane < 16 ? ks_to : vs_to) + token * 4, (lane < 16 ? p.k_scale : p.v_scale) + scales, policy);
+}
+
 // One warp's copies of TOKENS tokens, from `first` on, into a stage of a ring: K and V codes and their scales, page by
 // page.  `ahead` is the page (or -1) of box `lane` of the 32 boxes of `box` tokens that hold the stage's boxes `at` ..;
 // row_at(r, c) says where 16-byte chunk c of row r lies.  The rows of a box are contiguous in its page, so a lane's

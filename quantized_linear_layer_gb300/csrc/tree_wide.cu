@@ -83,11 +83,6 @@ struct Geo {
   static constexpr int kSmem = kOffWalk + (kSoftmaxWarps + kWidenWarps) * static_cast<int>(sizeof(W)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 
-  // where 16-byte chunk c of row r of a stage's codes lies
-  static __device__ __forceinline__ uint32_t raw_chunk(int r, int c) {
-    const int s = kRowBytes == 128 ? (r & 7) : kRowBytes == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1);
-    return static_cast<uint32_t>(r * kRowBytes + ((c ^ s) << 4));
-  }
 };
 
 // Where 16-byte chunk c (eight channels) of row r of a 64-channel fp16 block lies (128-byte swizzle).
@@ -197,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(raw_full + 8 * i, 32);
+      tc::mbar_init(raw_full + 8 * i, 33);
       tc::mbar_init(raw_free + 8 * i, kWidenWarps / 2);
     }
     tc::mbar_init(k_full, kWidenWarps);
@@ -240,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
   if (warp >= kLoadWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kLoadWarp) {
     // ---------------- loads ----------------
-    uint32_t n = 0;  // half tiles
+    uint32_t n = 0;       // half tiles
+    uint32_t filled = 0;  // of them, those loaded
     const int page = 1 << p.page_shift;
     const int box = min(page, kHalf);
     const int boxes = kHalf / box;
@@ -267,14 +263,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         if (n >= kStages) wait(raw_free + 8 * stage, n / kStages - 1, 0x60);
         dead = __any_sync(0xffffffffu, dead);
         if (dead) continue;
-        const uint32_t codes = base + G::kOffRaw + stage * 2 * G::kRawCode;
+        // a box's codes are contiguous in its page: one bulk copy each of K and V; its scales go by small copies
+        const uint32_t bar = raw_full + 8 * stage;
+        const int32_t pg = __shfl_sync(0xffffffffu, ahead, ((t - from) * boxes + lane) & 31);
+        const bool load = lane < boxes && pg >= 0;
+        const int good = __popc(__ballot_sync(0xffffffffu, load));
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, good * box * 2 * G::kRowBytes);
+        __syncwarp();
+        if (load) {
+          const int64_t row = static_cast<int64_t>(run.head) * page + ((t * kHalf + lane * box) & (page - 1));
+          const int64_t codes = pg * p.page_stride + row * G::kRowBytes;
+          const uint32_t to = base + G::kOffRaw + stage * 2 * G::kRawCode + lane * box * G::kRowBytes;
+          tc::bulk_load_policy(to, p.k + codes, box * G::kRowBytes, bar, policy);
+          tc::bulk_load_policy(to + G::kRawCode, p.v + codes, box * G::kRowBytes, bar, policy);
+        }
         const uint32_t scales = base + G::kOffScale + stage * 2 * kHalf * 4;
-        copy_tokens<kHalf, G::kRowBytes>(p, run.head, t * kHalf, box, ahead, (t - from) * boxes, codes, codes + G::kRawCode,
-                                         scales, scales + kHalf * 4, policy, [](int r, int c) { return G::raw_chunk(r, c); });
-        copies_arrive(raw_full + 8 * stage);
+        copy_scales<kHalf>(p, run.head, t * kHalf, box, ahead, (t - from) * boxes, scales, scales + kHalf * 4, policy);
+        copies_arrive(bar);
+        filled = n + 1;
       }
     }
-    copies_wait();  // none outlives the block, also where a wait ran out
+    copies_wait();
+    // Where a wait ran out nobody may be waiting for the bulk copies that are under way, and they must not outlive the
+    // block.
+    if (dead) {
+      for (uint32_t i = filled < kStages ? 0 : filled - kStages; i < filled; ++i)
+        tc::mbar_wait_quiet(raw_full + 8 * (i % kStages), (i / kStages) & 1, p.err, 0x6f);
+    }
   } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
     // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one thread issues.
@@ -354,31 +369,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
     W& w = reinterpret_cast<W*>(smem + G::kOffWalk)[warp];
     if (lane == 0) w = run;
     uint32_t t = 0;
-    // A lane takes 16 bytes of codes of one row at a time and makes kPieces 16-byte chunks of fp16 of them.  Rows and
-    // chunks are dealt to lanes such that the eight lanes of a quarter warp read from, and for each piece write to,
-    // eight different bank groups through the two swizzles, and a lane's row is the same modulo 8 throughout, so
-    // that its addresses differ by constants:
-    //   rows of 128 bytes: rows r, r ^ 5 x four chunks (one 64-channel block); two blocks, then eight rows on
-    //   rows of 64 bytes, two blocks (U4): rows 0 1 6 7 or 2 3 4 5 x two chunks; 16 rows, two blocks
+    // A lane takes 16 bytes of codes of one row at a time and makes kPieces 16-byte chunks of fp16 of them.  The codes lie
+    // as they do in their pages; rows and chunks are dealt to lanes such that the eight lanes of a quarter warp read from,
+    // and for each piece write to, eight different bank groups, and a lane's row is the same modulo 8 throughout, so that
+    // its addresses differ by constants:
+    //   rows of 128 bytes: rows r, r ^ 5 x four chunks, one row's of one 64-channel block, the other's of the other
+    //   rows of 64 bytes, two blocks (U4): rows 0 1 | 6 7 or 2 3 | 4 5 x two chunks of one block | of the other
     //   rows of 64 or 32 bytes, one block: consecutive rows
     constexpr int kPieces = G::kU4 ? 4 : 2;
     constexpr bool kPairs = G::kRowBytes == 128, kFours = G::kU4 && G::kBlocks == 2;
     constexpr int kRowsAtOnce = G::kRowBytes == 32 || kFours ? 16 : 8;
-    int row, c;  // of the 16 rows, and the 16-byte chunk of the row (of the block)
+    int row, c;     // of the 16 rows, and the 16-byte chunk of the row (of the block)
+    int other = 0;  // the block this lane takes first
     if constexpr (kPairs) {
       row = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
       c = lane & 3;
+      other = (lane >> 2) & 1;
     } else if constexpr (kFours) {
       const int i = (lane >> 1) & 3;
       row = 8 * (lane >> 4) + ((lane & 8) ? 2 + i : i + (i & 2) * 2);
       c = lane & 1;
+      other = i >> 1;
     } else {
       row = lane / (G::kRowBytes / 16);
       c = lane % (G::kRowBytes / 16);
     }
     constexpr int kBlockBytes = G::kRowBytes / G::kBlocks;  // of a row's codes in one 64-channel block
-    const uint32_t raw_at = G::raw_chunk(row, c);
-    const uint32_t out_at = static_cast<uint32_t>(row * 128 + (((c * kPieces) ^ (row & 7)) << 4));
+    const uint32_t raw_at = static_cast<uint32_t>(row * G::kRowBytes + other * kBlockBytes + c * 16);
+    const uint32_t out_at = static_cast<uint32_t>(row * 128 + (((c * kPieces) ^ (row & 7)) << 4)) + other * 16384u;
+    const uint32_t second = other ? 0u - 16384u : 16384u;  // from the first block to the second
     while (true) {
       bool more = false;
       __syncwarp();
@@ -433,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
                 if (tail) {
                   if (alive <= x * kRowsAtOnce) o[0] = o[1] = o[2] = o[3] = 0u;
                 }
-                sts128((out ^ (k << 4)) + x * kRowsAtOnce * 128 + b * 16384, o[0], o[1], o[2], o[3]);
+                sts128((out ^ (k << 4)) + x * kRowsAtOnce * 128 + (b ? second : 0u), o[0], o[1], o[2], o[3]);
               }
             }
           }
