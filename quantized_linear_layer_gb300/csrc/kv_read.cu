@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kTokens;
   const int count = static_cast<int>(min(static_cast<int64_t>(kTokens), p.rows - row0));
 
+  pdl_wait();
+  pdl_launch_dependents();
   const int warp = threadIdx.x / 32;
   if (warp < count) {
     const int l = threadIdx.x % 32;

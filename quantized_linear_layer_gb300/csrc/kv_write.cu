@@ -185,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of(FMT)) norm_rope_write_kern
     cb = p.half_rot + 4 * lane;
   }
 
+  pdl_wait();
+  pdl_launch_dependents();
   const int64_t tasks = p.T * p.parts;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGroups;
   int64_t task = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / LANES;
@@ -361,6 +363,8 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
   constexpr int LANES = D / 8;
   constexpr int kGroups = kThreads / LANES;
   const int lane = threadIdx.x % LANES;
+  pdl_wait();
+  pdl_launch_dependents();
   const int64_t count = p.T * p.heads;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kGroups * kFlat;
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kGroups * kFlat; row0 < count; row0 += stride) {

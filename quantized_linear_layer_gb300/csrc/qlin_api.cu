@@ -889,7 +889,17 @@ cudaError_t run_prepared(const Prepared& c, cudaStream_t stream) {
   void* args[] = {const_cast<uint64_t*>(c.params)};
   for (int i = 0; i < c.count; ++i) {
     const Launch& l = c.launch[i];
-    const cudaError_t e = cudaLaunchKernel(l.kernel, dim3(l.grid_x, l.grid_y), dim3(l.threads), args, l.smem, stream);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(l.grid_x, l.grid_y);
+    cfg.blockDim = dim3(l.threads);
+    cfg.dynamicSmemBytes = l.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, l.kernel, args);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

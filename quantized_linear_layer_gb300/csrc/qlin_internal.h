@@ -167,8 +167,10 @@ struct Prepared {
   }
 };
 static_assert(sizeof(Prepared) <= sizeof(qlin_call), "qlin_call too small");
-// Enqueues a planned call: plain launches, each kernel after the one before it
-// has finished.
+// Enqueues a planned call.  Every kernel of it is launched with programmatic
+// stream serialization: it waits for the work before it (griddepcontrol.wait,
+// in every block) before it reads or writes global memory, and lets the next
+// one start only after that wait.
 cudaError_t run_prepared(const Prepared& c, cudaStream_t stream);
 
 // Head norms, position rotation and the quantized cache.  `cache` null: the

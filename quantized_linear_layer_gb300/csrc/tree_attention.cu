@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
     }
     tc::fence_mbar_init();
   }
+  pdl_wait();
+  pdl_launch_dependents();
   const int share = (p.B + kThreads - 1) / kThreads;
   scan_units<kRows, kTile, kThreads>(p, share, scan);
   const int64_t total = scan[kThreads];

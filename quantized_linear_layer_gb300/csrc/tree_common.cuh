@@ -323,6 +323,8 @@ static __global__ void __launch_bounds__(128) tree_attention_join_kernel(const _
   constexpr int kTeams = 128 / kLanes;
   __shared__ float4 part[kTeams][D / 4];
   __shared__ float2 part_ml[kTeams];
+  pdl_wait();
+  pdl_launch_dependents();
   const Record rec = p.records[blockIdx.x];
   if (rec.last < 0) return;
   const int row = blockIdx.y;

@@ -209,6 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
     for (int i = 0; i < kCols; ++i) tc::mbar_init(col_full + 8 * i, kWidenWarps);
     tc::fence_mbar_init();
   }
+  pdl_wait();
+  pdl_launch_dependents();
   const int share = (p.B + kThreads - 1) / kThreads;
   scan_units<kRows, kTile, kThreads>(p, share, scan);
   const int64_t total = scan[kThreads];
