@@ -22,9 +22,11 @@
 // The mean of squares, the norm, the rotation and the scales are float32; a
 // row is rounded once, to its 16-bit output or to its codes.  Integer codes
 // are rounded by adding 1.5 x 2^23 (nearest even, the code in the low bits),
-// which is the float-to-integer conversion at the rate of an addition.  The
-// kernel is bound by HBM from about a thousand tokens on, by launch latency
-// below.
+// which is the float-to-integer conversion at the rate of an addition.
+// Bound: below about a thousand tokens a launch's latency (64 tokens x 48 heads
+// into the cache: 7.5 us); above, HBM and the issue slots together: 8192 tokens x
+// 40 heads of 128 rotated in 39.3 us (4270 GB/s), 6835 x 96 rotated and quantized
+// in 90.5 us (3200 GB/s, 64 % of the issue slots).
 #include <algorithm>
 #include <cmath>
 

@@ -26,9 +26,13 @@
 //
 // Tensor memory, all 512 columns: S/P 2 x 128, O 128, O2 128.
 //
-// Bound: for 128 live rows the tensor products (2 x 128 x 128 x D per tile) and
-// the softmax instructions take about as long as each other, and longer than
-// the codes take to come from HBM.
+// Bound: a tile takes about 3900 cycles whatever its rows, of which 1024 to 1536
+// are products, 1024 exponentials, 2000 issue slots of each scheduler and 2300
+// shared-memory passes: the latency of the instructions of 26 warps, no single
+// unit.  One tree of 26 nodes (104 rows a key head) over 131000 tokens, U4: 140
+// us; 16 sequences x 64 nodes x 64 query heads over up to 8192 tokens, INT8: 340
+// us, 409 TFLOP/s; 32 sequences x 16 nodes over up to 32768, E4M3: 492 us, 2350
+// GB/s.
 #include <algorithm>
 #include <cmath>
 
