@@ -22,6 +22,9 @@ Operations (sizes as flags):
   w4a16_act_order  qlin_w4a16_gemm_act_order, X [T][K] fp16, act-order weights N x K (gather + GEMM)
   rmsnorm_nvfp4  qlin_rmsnorm_quant_nvfp4, X [T][K] fp16, gamma [K], S residual channels, MMA scale layout
   rmsnorm_int8   qlin_rmsnorm_quant, X [T][K] fp16, gamma [K], per-token int8
+  norm_rope_cache  qlin_qk_norm_rope_cache, T new tokens, heads --hq / --hk of 128, cache of --fmt
+  tree_attention   qlin_tree_attention, T sequences of --ctx cached tokens and --nodes new ones (a chain), heads
+               --hq / --hk of 128, cache of --fmt
   fp8_quant    qlin_quant_fp8, X [T][K] fp16, per-row E4M3
   fp8_gemm     qlin_fp8_gemm, A [T][K] and B [N][K] E4M3 (made by the quantizer), bias, bf16 out
 
@@ -216,6 +219,35 @@ def _setup(args, q, torch):
         out = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
         return lambda i: q.qlin_fp8_gemm(qa, ws[i % copies][0], sa, ws[i % copies][1], out, bias=bias)
 
+    if args.op in ("norm_rope_cache", "tree_attention"):
+        d, page, u4 = 128, 64, args.fmt == "u4"
+        fmt = {"int8": q.QLIN_KV_INT8, "e4m3": q.QLIN_KV_E4M3, "u4": q.QLIN_KV_U4}[args.fmt]
+        nodes, seqs = (1, 1) if args.op == "norm_rope_cache" else (args.nodes, T)
+        per = -(-(args.ctx + nodes) // page) if args.op == "tree_attention" else -(-T // page)
+        kv = [torch.empty((seqs * per, args.hk, page, d // 2 if u4 else d), dtype=torch.int8 if args.fmt == "int8" else torch.uint8,
+                          device="cuda").random_(0, 100, generator=g) for _ in range(2)]
+        scales = [torch.rand((seqs * per, args.hk, page), device="cuda", generator=g) * 0.02 + 0.01 for _ in range(2)]
+        if u4:
+            scales = [torch.stack([s, torch.full_like(s, 7)], -1).half() for s in scales]
+        cache = q.qlin_kv_cache(*kv, *scales, fmt)
+        tokens = T * nodes
+        x = randn((tokens, args.hq + 2 * args.hk, d), torch.bfloat16)
+        out = torch.empty((tokens, args.hq, d), dtype=torch.bfloat16, device="cuda")
+        if args.op == "norm_rope_cache":
+            at = torch.arange(tokens, device="cuda")
+            freq = 10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64, device="cuda") / d)
+            gamma = randn((d,), torch.bfloat16)
+            call = q.qlin_qk_norm_rope_cache_prepare(x[:, :args.hq], x[:, args.hq:args.hq + args.hk], x[:, args.hq + args.hk:],
+                                                     out, at, freq, at, cache, gamma, gamma)
+        else:
+            table = torch.randperm(seqs * per, device="cuda", generator=g).int().view(seqs, per)
+            starts = torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * nodes
+            work = torch.empty(q.qlin_tree_attention_workspace_bytes(cache, args.hq, nodes, seqs), dtype=torch.uint8, device="cuda")
+            call = q.qlin_tree_attention_prepare(x[:, :args.hq], cache, table, starts,
+                                                 torch.full((seqs,), args.ctx, dtype=torch.int32, device="cuda"), None, out,
+                                                 work, nodes)
+        return lambda i: call.run()
+
     raise ValueError(args.op)
 
 
@@ -224,7 +256,8 @@ def main(argv=None):
     ap.add_argument("op", choices=["w4a16", "w4a16_group", "w4a16_decode", "int8_quant", "w8a8", "w8a8_f16b", "w8a8_f16", "int8_quant_f16",
                                    "nvfp4_quant", "nvfp4_gemm",
                                    "fp8_quant", "fp8_gemm", "rmsnorm_nvfp4", "rmsnorm_int8", "mxfp8_quant",
-                                   "mxfp4_quant", "mxfp8_gemm", "mxfp4_gemm", "hadamard", "w4a16_act_order"])
+                                   "mxfp4_quant", "mxfp8_gemm", "mxfp4_gemm", "hadamard", "w4a16_act_order", "norm_rope_cache",
+                                   "tree_attention"])
     ap.add_argument("--n", type=int, default=256, help="Hadamard group size")
     ap.add_argument("--kind", type=int, default=0, help="Hadamard kind: 0 Sylvester, 1 regular")
     ap.add_argument("--T", type=int, default=1)
@@ -233,6 +266,11 @@ def main(argv=None):
     ap.add_argument("--S", type=int, default=128, help="NVFP4 residual channels (K includes them for nvfp4_gemm)")
     ap.add_argument("--groups", type=int, default=3, help="matrices per w4a16_group launch")
     ap.add_argument("--blocks", type=int, default=2, help="decoder blocks of a w4a16_decode plan")
+    ap.add_argument("--hq", type=int, default=32, help="query heads")
+    ap.add_argument("--hk", type=int, default=8, help="key heads")
+    ap.add_argument("--ctx", type=int, default=4096, help="cached tokens of a sequence")
+    ap.add_argument("--nodes", type=int, default=1, help="new tokens of a sequence")
+    ap.add_argument("--fmt", choices=("int8", "e4m3", "u4"), default="int8", help="cache format")
     ap.add_argument("--copies", type=int, default=4, help="weight copies rotated over the launches")
     ap.add_argument("--reps", type=int, default=4, help="launches")
     ap.add_argument("--seed", type=int, default=0)

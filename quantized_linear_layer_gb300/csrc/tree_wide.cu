@@ -31,7 +31,7 @@
 // shared-memory passes: the latency of the instructions of 26 warps, no single
 // unit.  One tree of 26 nodes (104 rows a key head) over 131000 tokens, U4: 140
 // us; 16 sequences x 64 nodes x 64 query heads over up to 8192 tokens, INT8: 340
-// us, 409 TFLOP/s; 32 sequences x 16 nodes over up to 32768, E4M3: 492 us, 2350
+// us, 411 TFLOP/s; 32 sequences x 16 nodes over up to 32768, E4M3: 492 us, 2350
 // GB/s.
 #include <algorithm>
 #include <cmath>
