@@ -42,7 +42,7 @@
 //
 // Bound: up to eight rows per key head, HBM and the latency of the loads: 64
 // ragged sequences of up to 8191 tokens, 8 key heads of 128, E4M3, one node of 32
-// query heads each: 150 us, 4260 GB/s (one copy would take 96 us).  At 16 rows the
+// query heads each: 149 us, 4300 GB/s (one copy would take 96 us).  At 16 rows the
 // widening instructions take as long as the loads.  One sequence of 500 tokens,
 // 32 heads: 11 us, two launches' latency.
 #include <algorithm>
@@ -162,10 +162,13 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
         }
         // this unit's boxes; those past the end have no page
         const uint32_t codes = base + stage * G::kStage, scales = base + G::kOffScale + stage * 2 * G::kScaleBytes;
-        copy_tokens<kTile, G::kRowBytes>(p, w.head, t * kTile, box, ahead, (t - from) * boxes, codes, codes + G::kCodeBytes,
-                                         scales, scales + G::kScaleBytes, policy, [](int r, int c) {
-                                           return c / (G::kW / 16) * G::kSubBytes + G::chunk(r, c % (G::kW / 16));
-                                         });
+        auto row_at = [](int r, int c) { return c / (G::kW / 16) * G::kSubBytes + G::chunk(r, c % (G::kW / 16)); };
+        const int at = (t - from) * boxes;
+        copy_scales<kTile>(p, w.head, t * kTile, box, ahead, at, scales, scales + G::kScaleBytes, policy);
+        if (box == kTile)
+          copy_codes<kTile, kTile, G::kRowBytes>(p, w.head, t * kTile, ahead, at, codes, codes + G::kCodeBytes, policy, row_at);
+        else
+          copy_codes<kTile, 16, G::kRowBytes>(p, w.head, t * kTile, ahead, at, codes, codes + G::kCodeBytes, policy, row_at);
         copies_arrive(bar_full + 8 * stage);
         if (++stage == G::kStages) {
           stage = 0;

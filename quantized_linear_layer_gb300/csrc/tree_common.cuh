@@ -202,52 +202,53 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// One warp's copies of the scales of TOKENS tokens, from `first` on; the arguments are those of copy_tokens.
+// One warp's copies of the scales of TOKENS tokens of a key head, from `first` on, into a stage of a ring.  `ahead` is
+// the page (or -1) of box `lane` of the 32 boxes of `box` tokens that hold the stage's boxes `at` ...
 template <int TOKENS>
 __device__ __forceinline__ void copy_scales(const Params& p, int head, int first, int box, int32_t ahead, int at,
                                             uint32_t ks_to, uint32_t vs_to, uint64_t policy) {
+  constexpr int kLanes = TOKENS / 4;  // four tokens each: the scales of K, then as many lanes for those of V
+  static_assert(2 * kLanes <= 32, "lanes");
   const int lane = threadIdx.x % 32;
-  const int page = 1 << p.page_shift;
-  const int token = lane % 16 * 4;  // lanes 0-15: scales of K, 16 bytes each, then of V
-  static_assert(TOKENS == 64, "four tokens a lane");
+  const int token = lane % kLanes * 4;
   const int32_t pg = __shfl_sync(0xffffffffu, ahead, (at + token / box) & 31);
-  if (pg < 0) return;
-  const int64_t row = static_cast<int64_t>(head) * page + ((first + token) & (page - 1));
-  const int64_t scales = pg * p.scale_page_stride + row * 4;
-  copy16((lane < 16 ? ks_to : vs_to) + token * 4, (lane < 16 ? p.k_scale : p.v_scale) + scales, policy);
+  if (pg < 0 || lane >= 2 * kLanes) return;
+  const bool k = lane < kLanes;
+  const int64_t row = (static_cast<int64_t>(head) << p.page_shift) + ((first + token) & ((1 << p.page_shift) - 1));
+  copy16((k ? ks_to : vs_to) + token * 4, (k ? p.k_scale : p.v_scale) + pg * p.scale_page_stride + row * 4, policy);
 }
 
-// One warp's copies of TOKENS tokens, from `first` on, into a stage of a ring: K and V codes and their scales, page by
-// page.  `ahead` is the page (or -1) of box `lane` of the 32 boxes of `box` tokens that hold the stage's boxes `at` ..;
-// row_at(r, c) says where 16-byte chunk c of row r lies.  The rows of a box are contiguous in its page, so a lane's
-// chunks are 512 bytes apart.  Plain asynchronous copies: with tensor-map copies of these boxes (the same time) calls
-// failed when other memory was mapped while they ran.
-template <int TOKENS, int ROW_BYTES, class RowAt>
-__device__ __forceinline__ void copy_tokens(const Params& p, int head, int first, int box, int32_t ahead, int at,
-                                            uint32_t k_to, uint32_t v_to, uint32_t ks_to, uint32_t vs_to, uint64_t policy,
-                                            RowAt row_at) {
-  constexpr int kChunks = ROW_BYTES / 16;      // of a row
+// One warp's copies of the codes of TOKENS tokens, page by page, box by box of BOX tokens; the other arguments are those
+// of copy_scales, and row_at(r, c) says where 16-byte chunk c of row r lies (its swizzle repeats after eight rows).  The
+// rows of a box are contiguous in its page, so a lane's chunks are 512 bytes apart and everything but the page's address
+// is known beforehand: the copies of a stage take the warp few instructions (with the box a variable and four copies at
+// once, a decode batch took 163 us instead of 149).  Plain asynchronous copies: with tensor-map copies of these
+// boxes, at the same speed, calls failed when other memory was mapped while they ran.
+template <int TOKENS, int BOX, int ROW_BYTES, class RowAt>
+__device__ __forceinline__ void copy_codes(const Params& p, int head, int first, int32_t ahead, int at, uint32_t k_to,
+                                           uint32_t v_to, uint64_t policy, RowAt row_at) {
+  constexpr int kChunks = ROW_BYTES / 16;  // of a row
   constexpr int kRowsAtOnce = 32 / kChunks;
+  constexpr int kPeriod = kRowsAtOnce < 8 ? 8 / kRowsAtOnce : 1;
   const int lane = threadIdx.x % 32;
-  const int page = 1 << p.page_shift;
-  for (int b = 0; b * box < TOKENS; ++b) {
+  uint32_t to[kPeriod];
+#pragma unroll
+  for (int i = 0; i < kPeriod; ++i) to[i] = row_at(i * kRowsAtOnce + lane / kChunks, lane % kChunks);
+  const uint32_t step = row_at(kPeriod * kRowsAtOnce, 0);
+#pragma unroll
+  for (int b = 0; b < TOKENS / BOX; ++b) {
     const int32_t pg = __shfl_sync(0xffffffffu, ahead, (at + b) & 31);
     if (pg < 0) continue;
-    const int64_t row = static_cast<int64_t>(head) * page + ((first + b * box) & (page - 1));
+    const int64_t row = (static_cast<int64_t>(head) << p.page_shift) + ((first + b * BOX) & ((1 << p.page_shift) - 1));
     const int64_t codes = pg * p.page_stride + row * ROW_BYTES + lane * 16;
     const uint8_t* k = p.k + codes;
     const uint8_t* v = p.v + codes;
-#pragma unroll 8  // (four: a decode batch takes 163 us instead of 153, as the loading warp falls behind)
-    for (int r = 0; r < box; r += kRowsAtOnce) {
-      const uint32_t to = row_at(b * box + r + lane / kChunks, lane % kChunks);
-      copy16(k_to + to, k + r * ROW_BYTES, policy);
-      copy16(v_to + to, v + r * ROW_BYTES, policy);
-    }
-    const int at16 = lane * 16;
-    if (at16 < box * 4) {
-      const int64_t scales = pg * p.scale_page_stride + row * 4 + at16;
-      copy16(ks_to + b * box * 4 + at16, p.k_scale + scales, policy);
-      copy16(vs_to + b * box * 4 + at16, p.v_scale + scales, policy);
+#pragma unroll
+    for (int x = 0; x < BOX / kRowsAtOnce; ++x) {
+      const int y = b * (BOX / kRowsAtOnce) + x;
+      const uint32_t at16 = to[y % kPeriod] + y / kPeriod * step;
+      copy16(k_to + at16, k + x * 512, policy);
+      copy16(v_to + at16, v + x * 512, policy);
     }
   }
 }
