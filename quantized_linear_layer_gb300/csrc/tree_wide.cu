@@ -26,10 +26,11 @@
 //
 // Tensor memory, all 512 columns: S/P 2 x 128, O 128, O2 128.
 //
-// Bound: a tile takes about 3900 cycles whatever its rows, of which 1024 to 1536
-// are products, 1024 exponentials, 2000 issue slots of each scheduler and 2300
-// shared-memory passes: the latency of the instructions of 26 warps, no single
-// unit.  One tree of 26 nodes (104 rows a key head) over 131000 tokens, U4: 140
+// Bound: a tile takes about 3900 cycles whatever its rows.  Shared memory is busy
+// for about 2900 of them: 768 to 1024 for the products' operands, 1000 for the
+// codes in and out of their widening, 900 for the tokens' scales, which every
+// warp of rows reads; issue slots take 2600 of each scheduler's, products 1024 to
+// 1536, exponentials 1024.  One tree of 26 nodes (104 rows a key head) over 131000 tokens, U4: 140
 // us; 16 sequences x 64 nodes x 64 query heads over up to 8192 tokens, INT8: 340
 // us, 411 TFLOP/s; 32 sequences x 16 nodes over up to 32768, E4M3: 492 us, 2350
 // GB/s.
