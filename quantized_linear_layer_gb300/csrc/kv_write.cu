@@ -26,7 +26,7 @@
 // Bound: below about a thousand tokens a launch's latency (64 tokens x 48 heads
 // into the cache: 7.5 us); above, HBM and the issue slots together: 8192 tokens x
 // 40 heads of 128 rotated in 39.3 us (4270 GB/s), 6835 x 96 rotated and quantized
-// in 90.5 us (3200 GB/s, 64 % of the issue slots).
+// in 87.4 us (3310 GB/s, about 64 % of the issue slots).
 #include <algorithm>
 #include <cmath>
 
@@ -69,16 +69,20 @@ struct Params {
   int32_t* err;
 };
 
-// The largest of the lanes' values in groups of LANES lanes.
-template <int LANES>
-__device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+// The largest and smallest of three, NaN if one is NaN (fmaxf and fminf drop it).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
-// x / d rounded to nearest even from r = __frcp_rn(d), as div_by_rcp, but for
-// the sign of a quotient of zero.
+// x / d rounded to nearest even from r = 1 / d rounded to nearest, as div_by_rcp,
+// but for the sign of a quotient of zero.
 __device__ __forceinline__ float divide(float x, float d, float r) {
   const float q = __fmul_rn(x, r);
   return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
@@ -90,25 +94,23 @@ __device__ __forceinline__ float divide(float x, float d, float r) {
 template <int FMT, int LANES, bool JOINED>
 __device__ __forceinline__ void quantize_row(const float* y, int lane, int ca, int cb, bool write, uint8_t* codes,
                                              uint8_t* scale_at) {
-  uint32_t amax_bits = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax_bits = max(amax_bits, __float_as_uint(y[i]) & 0x7fffffffu);
-  amax_bits = group_max_u32<LANES>(amax_bits);  // as integers a NaN or an infinity is above every finite value
-  const bool finite = amax_bits < 0x7f800000u;
   if constexpr (FMT == QLIN_KV_U4) {
     float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo = fminf(lo, y[i]);
-      hi = fmaxf(hi, y[i]);
+    for (int i = 0; i < 8; i += 2) {
+      lo = min3(lo, y[i], y[i + 1]);
+      hi = max3(hi, y[i], y[i + 1]);
     }
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      const float l = __shfl_xor_sync(0xffffffffu, lo, o), h = __shfl_xor_sync(0xffffffffu, hi, o);
+      lo = min3(lo, l, l);
+      hi = max3(hi, h, h);
     }
+    const bool finite = hi < INFINITY && lo > -INFINITY;
     const float span = fmaxf(__fsub_rn(hi, lo), 1e-5f);
-    const __half s16 = __float2half_rn(fminf(__fdiv_rn(span, 15.0f), 65504.0f));
+    // (a span that overflowed to infinity stays one)
+    const __half s16 = __float2half_rn(span < INFINITY ? fminf(divide(span, 15.0f, 1.0f / 15.0f), 65504.0f) : 65504.0f);
     const float s = __half2float(s16);  // at least the fp16 nearest 1e-5 / 15, a normal float32
     const float r = __frcp_rn(s);
     const float z = fminf(fmaxf(rintf(divide(-lo, s, r)), 0.0f), 15.0f);
@@ -134,9 +136,18 @@ __device__ __forceinline__ void quantize_row(const float* y, int lane, int ca, i
       }
     }
   } else {
-    const float amax = __uint_as_float(amax_bits);
-    float s = fmaxf(__fdiv_rn(amax, FMT == QLIN_KV_INT8 ? 127.0f : 448.0f), kScaleFloor);
-    if (amax_bits == 0) s = 1.0f;
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) amax = max3(amax, fabsf(y[i]), fabsf(y[i + 1]));
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      const float a = __shfl_xor_sync(0xffffffffu, amax, o);
+      amax = max3(amax, a, a);
+    }
+    const bool finite = amax < INFINITY;
+    constexpr float kTop = FMT == QLIN_KV_INT8 ? 127.0f : 448.0f;
+    float s = fmaxf(divide(amax, kTop, 1.0f / kTop), kScaleFloor);  // exact where it is above the floor
+    if (amax == 0.0f) s = 1.0f;
     const float r = __frcp_rn(s);  // s lies in [2^-64, 2^122]: normal, as is its reciprocal
     uint32_t w[2];
 #pragma unroll
