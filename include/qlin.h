@@ -833,7 +833,8 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * q, i < q_indptr[b + 1] - q_indptr[b] <= max_nodes.  Node i sees every
  * cached token, and node j when bit j % 64 of mask[q_indptr[b] + i][j / 64]
  * is set (mask NULL: when j <= i).  Head h of q reads head h / (Hq / Hk) of
- * the cache.
+ * the cache.  A sequence's ctx_lens[b] and nodes together are at most
+ * 2^31 - 65536.
  *   out = sum_j p_ij v_j, p = softmax over what node i sees of
  *   scale (q_i . k_j); lse = ln sum_j exp(scale (q_i . k_j))
  * A node that sees nothing gets out = 0 and lse = -infinity.  What a node

@@ -57,6 +57,10 @@ struct Params {
   int32_t* err;
 };
 
+// The longest sequence, nodes included: far enough below 2^31 that the token numbers the kernels form past a sequence's
+// end (whole tiles, and the loading warps' 32 boxes of up to 64 tokens) stay in an int32.
+constexpr int64_t kMaxLen = 0x7fff0000;
+
 // A sequence's bounds as far as they can be used: nodes = 0 when they cannot.
 struct Sequence {
   int64_t q_row;
@@ -74,7 +78,7 @@ __device__ __forceinline__ Sequence sequence(const Params& p, int b) {
   s.ctx = p.ctx_lens[b];
   const int64_t len = static_cast<int64_t>(s.ctx) + s.nodes;
   const bool fits = q0 >= 0 && q1 >= q0 && q1 <= p.Tq && s.nodes <= p.max_nodes && s.ctx >= 0 &&
-                    len <= (p.max_pages << p.page_shift) && len <= 0x7fffff00;
+                    len <= (p.max_pages << p.page_shift) && len <= kMaxLen;
   if (!fits) {
     record_device_error(p.err, kDevErrBadIndex);
     s.nodes = 0;
