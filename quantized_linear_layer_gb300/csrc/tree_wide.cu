@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "stage_ring.h"
 #include "tree_common.cuh"
 
 namespace qlin {
@@ -173,6 +174,25 @@ __device__ __forceinline__ uint64_t seen_bits(const Params& p, const Sequence& s
   return v;
 }
 
+// The ring of half tiles, for stage_ring.h.
+struct RingOps {
+  uint32_t full, free;  // barriers, [kStages]
+  volatile uint32_t* flag;
+  int32_t* err;
+  __device__ __forceinline__ bool wait_full(uint32_t stage, uint32_t parity) {
+    return tc::mbar_wait_quiet(full + 8 * stage, parity, err, 0x6f);
+  }
+  __device__ __forceinline__ bool wait_free(uint32_t stage, uint32_t parity) {
+    return tc::mbar_wait_quiet(free + 8 * stage, parity, err, 0x60);
+  }
+  __device__ __forceinline__ bool raised() { return *flag != 0; }
+  __device__ __forceinline__ void raise() {
+    *flag = 1;
+    __threadfence_block();
+  }
+  __device__ __forceinline__ bool any(bool b) { return __any_sync(0xffffffffu, b); }
+};
+
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const __grid_constant__ Params p) {
   using G = Geo<FMT, D>;
@@ -192,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
   const uint32_t all_done = q_full + 8;
   const uint32_t col_full = all_done + 8;   // [kCols]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
+  volatile uint32_t* ran_out = tmem_slot + 1;  // a wait of some role of the block ran out
   volatile uint32_t* small_tile = reinterpret_cast<volatile uint32_t*>(smem + G::kOffMisc + 8);  // [2]: 1 + the last tile with any
   int64_t* scan = reinterpret_cast<int64_t*>(smem + G::kOffScan);
 
@@ -212,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
     tc::mbar_init(q_full, kSoftmaxWarps);
     tc::mbar_init(all_done, 1);
     for (int i = 0; i < kCols; ++i) tc::mbar_init(col_full + 8 * i, kWidenWarps);
+    *ran_out = 0;
     tc::fence_mbar_init();
   }
   pdl_wait();
@@ -233,17 +255,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
   W run = begin_run<kRows, kTile, kThreads>(p, share, scan, blockIdx.x, blocks);
 
   // In every role a wait that runs out makes it go on without waiting, so that
-  // all loops end and every barrier among threads is met.
+  // all loops end and every barrier among threads is met; the block's flag tells
+  // the loading warp (stage_ring.h).
   bool dead = false;
+  RingOps ops = {raw_full, raw_free, ran_out, p.err};
   auto wait = [&](uint32_t bar, uint32_t parity, int site) {
-    if (!dead) dead = !tc::mbar_wait_quiet(bar, parity & 1, p.err, site);
+    ring::wait_or_raise(ops, dead, [&]() { return tc::mbar_wait_quiet(bar, parity & 1, p.err, site); });
   };
 
   if (warp >= kLoadWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kLoadWarp) {
     // ---------------- loads ----------------
-    uint32_t n = 0;       // half tiles
-    uint32_t filled = 0;  // of them, those loaded
+    ring::Filler<kStages> fill;
     const int page = 1 << p.page_shift;
     const int box = min(page, kHalf);
     const int boxes = kHalf / box;
@@ -253,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
       const int end = min(run.s.len, (run.tile + run.tiles) * kTile);
       int32_t ahead = -1;  // the page of box `lane` of the 32 boxes from half tile `from` on
       int from = 0;
-      for (int t = 2 * run.tile; t < 2 * (run.tile + run.tiles); ++t, ++n) {
+      for (int t = 2 * run.tile; t < 2 * (run.tile + run.tiles); ++t) {
         if (t == 2 * run.tile || (t - from) * boxes == 32) {
           from = t;
           const int j = t * kHalf + lane * box;
@@ -266,10 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
             }
           }
         }
-        const uint32_t stage = n % kStages;
-        if (n >= kStages) wait(raw_free + 8 * stage, n / kStages - 1, 0x60);
-        dead = __any_sync(0xffffffffu, dead);
-        if (dead) continue;
+        if (!fill.wait(ops)) continue;
+        const uint32_t stage = fill.stage();
         // a box's codes are contiguous in its page: one bulk copy each of K and V; its scales go by small copies
         const uint32_t bar = raw_full + 8 * stage;
         const int32_t pg = __shfl_sync(0xffffffffu, ahead, ((t - from) * boxes + lane) & 31);
@@ -287,16 +308,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         const uint32_t scales = base + G::kOffScale + stage * 2 * kHalf * 4;
         copy_scales<kHalf>(p, run.head, t * kHalf, box, ahead, (t - from) * boxes, scales, scales + kHalf * 4, policy);
         copies_arrive(bar);
-        filled = n + 1;
+        ++fill.filled;
       }
     }
     copies_wait();
-    // Where a wait ran out nobody may be waiting for the bulk copies that are under way, and they must not outlive the
-    // block.
-    if (dead) {
-      for (uint32_t i = filled < kStages ? 0 : filled - kStages; i < filled; ++i)
-        tc::mbar_wait_quiet(raw_full + 8 * (i % kStages), (i / kStages) & 1, p.err, 0x6f);
-    }
+    fill.drain(ops);
   } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
     // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one thread issues.
