@@ -29,6 +29,13 @@
 namespace qlin {
 namespace ring {
 
+// Whether `takers` readers may take the fills of a ring in turn (reader w the fills w, w + takers, ...), each waiting on
+// the full barrier of its fill alone, by parity.  A parity cannot tell a phase from the one two before it: a reader that
+// waits for fill u has to know that fill u - stages, the one before it in the same stage, has arrived, or it takes the
+// end of the phase before that for its own.  It has seen fill u - takers arrive; so fills must arrive in order (as a
+// thread's asynchronous copies do: each arrival follows all its earlier copies), and stages >= takers.
+constexpr bool turns_are_safe(int stages, int takers) { return stages >= takers; }
+
 // The filling role: STAGES stages in turn.
 template <int STAGES>
 struct Filler {

@@ -29,7 +29,7 @@
 // (o, m, l), which a second kernel joins in the order of the blocks; a
 // sequence's result depends on the lengths, not on timing.
 //
-// A block has five compute warps (seven where registers allow) and one that
+// A block has five compute warps (six or seven where registers allow) and one that
 // loads.  The loading warp keeps a ring of stages filled by asynchronous
 // copies: one unit's codes of K and V (rows of 128, 64 or 32 bytes, their
 // 16-byte chunks swizzled) and their scales.  Units go to the compute warps in
@@ -49,6 +49,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "stage_ring.h"
 #include "tree_common.cuh"
 
 namespace qlin {
@@ -76,9 +77,11 @@ struct Geo {
   static constexpr int kNPerSub = kPerSub / 8;              // output tiles of a column block
   // 168 registers a thread (D = 128) let 12 warps live on an SM, 128 (D = 64) 16, 255 (D = 256) 8
   static constexpr int kBlocksPerSm = D == 256 ? 1 : 2;
-  static constexpr int kWarps = D == 128 ? 5 : 7;
-  static constexpr int kThreads = 32 * (kWarps + 1);
+  // (six stages of rows of 256 bytes fit beside the merge area: no more than six warps may take turns at them)
   static constexpr int kStages = kRowBytes >= 256 ? 6 : kRowBytes == 128 ? 8 : kRowBytes == 64 ? 12 : 16;
+  static constexpr int kWarps = D == 128 ? 5 : kStages < 7 ? kStages : 7;
+  static_assert(ring::turns_are_safe(kStages, kWarps), "a warp's wait could be a whole round of the ring ahead");
+  static constexpr int kThreads = 32 * (kWarps + 1);
   // 2^24 (2^15 for E4M3): codes times 2^-kShift are fp16 numbers, exactly
   static constexpr float kShiftUp = FMT == QLIN_KV_E4M3 ? 32768.0f : 16777216.0f;
   static constexpr uint32_t kShiftDown = FMT == QLIN_KV_E4M3 ? 0x02000200u : 0x00010001u;

@@ -4,15 +4,22 @@
 // no barrier is armed in a phase that is not over, and no copy is under way when
 // the filling thread ends.
 //
-//   stage_ring <stages> <late> <delay ms> <reader limit ms> <filler limit ms>
+//   stage_ring <fills> <late> <delay ms> <reader limit ms> <filler limit ms>
 //
 // `late`: the fill whose copy takes `delay`; all others take none.
+//
+//   stage_ring turns <stages> <takers> <late> <delay ms>
+//
+// Readers that take the fills in turn, by parity, while copies arrive in order:
+// exits 0 when each found its fill's data, 1 when one was a round ahead; 4 when
+// turns_are_safe() says otherwise.
 #include <atomic>
 #include <chrono>
 #include <condition_variable>
 #include <cstdio>
 #include <cstdlib>
 #include <mutex>
+#include <string>
 #include <thread>
 #include <vector>
 
@@ -75,10 +82,45 @@ struct Ops {
   bool any(bool v) { return v; }
 };
 
+int turns(int stages, int takers, int late, milliseconds delay) {
+  const int fills = 12 * stages;
+  std::vector<Barrier> full(stages), free(stages);
+  std::vector<std::atomic<int>> data(stages);
+  for (int i = 0; i < stages; ++i) full[i].init(1), free[i].init(1), data[i] = -1;
+  std::atomic<bool> wrong{false};
+  std::thread filler([&] {
+    for (int i = 0; i < fills && !wrong; ++i) {
+      const int s = i % stages;
+      if (i >= stages) free[s].wait((i / stages - 1) & 1, seconds(10));
+      if (i == late) std::this_thread::sleep_for(delay);
+      data[s] = i;
+      full[s].arrive();
+    }
+  });
+  std::vector<std::thread> readers;
+  for (int w = 0; w < takers; ++w)
+    readers.emplace_back([&, w] {
+      for (int u = w; u < fills && !wrong; u += takers) {
+        const int s = u % stages;
+        full[s].wait((u / stages) & 1, milliseconds(500));
+        if (data[s] != u) wrong = true;
+        free[s].arrive();
+      }
+    });
+  filler.join();
+  for (auto& t : readers) t.join();
+  return wrong ? 1 : 0;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
   if (argc != 6) return 2;
+  if (std::string(argv[1]) == "turns") {
+    const int wrong = turns(atoi(argv[2]), atoi(argv[3]), atoi(argv[4]), milliseconds(atoi(argv[5])));
+    const bool safe = qlin::ring::turns_are_safe(atoi(argv[2]), atoi(argv[3]));
+    return wrong && safe ? 4 : wrong;
+  }
   const int fills = atoi(argv[1]), late = atoi(argv[2]);
   const milliseconds delay(atoi(argv[3])), reader_limit(atoi(argv[4])), filler_limit(atoi(argv[5]));
   Block b;

@@ -56,3 +56,19 @@ def test_longest_sequences(qlin_gpu, nodes, over):
     e, s = d * 2.0 ** -24 * spread, (at.size + 64) * 2.0 ** -24
     assert (np.abs(out.double().cpu().numpy() - o) <= (2.0 ** -11 + 2 * e + s)[..., None] * w + 2.0 ** -11 * np.abs(o) + 2.0 ** -24).all()
     assert (np.abs(lse.double().cpu().numpy() - l) <= e + s + 2.0 ** -22 * np.abs(l)).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+def test_heads_of_256_over_long_contexts(qlin_gpu, fmt):
+    """Each warp takes its turns at the ring for thousands of rounds, the codes from HBM: the same bits every time."""
+    q, d = qlin_gpu, 256
+    p = Problem(q, [(60000, 1), (30011, 3), (9000, 2)], 4, 2, d, 64, fmt, torch.bfloat16, "tree", 3)
+    first, lse = (x.clone() for x in p.run())
+    p.check()
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(20):
+        flush.fill_(i)                                # larger than L2
+        p.call.run()
+        torch.cuda.synchronize()
+        assert q.qlin_get_device_error() == 0
+        assert torch.equal(p.out, first) and torch.equal(p.lse, lse)

@@ -32,3 +32,17 @@ def program(tmp_path_factory):
 def test_waits_that_run_out(program, late, delay, reader, filler):
     r = subprocess.run([program, "40", str(late), str(delay), str(reader), str(filler)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, "%d: %s" % (r.returncode, r.stdout)
+
+
+@pytest.mark.parametrize("stages,takers", [(8, 5), (6, 6), (8, 7), (12, 7), (16, 7)])
+@pytest.mark.parametrize("late", [0, 1, 9])
+def test_taking_turns(program, stages, takers, late):
+    """Each reader finds its own fill, as many stages and readers as the kernels have."""
+    r = subprocess.run([program, "turns", str(stages), str(takers), str(late), "40"], timeout=60)
+    assert r.returncode == 0
+
+
+def test_more_readers_than_stages(program):
+    """Seven readers at six stages: one is a whole round ahead when a copy is late, which the kernels' geometry excludes."""
+    r = subprocess.run([program, "turns", "6", "7", "1", "40"], timeout=60)
+    assert r.returncode == 1
