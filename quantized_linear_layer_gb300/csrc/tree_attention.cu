@@ -357,10 +357,10 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
                          : ((p.mask[(w.s.q_row + node) * p.mask_words + (j >> 6)] >> (j & 63)) & 1) != 0;
             if (!seen) s[n][i] = -INFINITY;
           }
-          // a hidden token adds nothing to l, whatever its scale is; one that is seen makes t a NaN with it
+          // a hidden token adds nothing to l, whatever its scale is (1 / -0 is -infinity); one that is seen makes t a NaN with it
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (!(rsv[2 * n + i] < INFINITY)) rsv[2 * n + i] = 0.0f;
+            if (!(fabsf(rsv[2 * n + i]) < INFINITY)) rsv[2 * n + i] = 0.0f;
         }
       }
 

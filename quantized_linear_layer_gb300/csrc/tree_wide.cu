@@ -505,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + part * 16 + lane;
           col[0] = sk * (p.scale * kLog2e);
           col[kTile] = lg2(sv);
-          // a hidden token adds nothing to l, whatever its scale is; one that is seen makes t a NaN with it
-          col[2 * kTile] = rsv < INFINITY ? rsv : 0.0f;
+          // a hidden token adds nothing to l, whatever its scale is (1 / -0 is -infinity); one that is seen makes t a NaN with it
+          col[2 * kTile] = fabsf(rsv) < INFINITY ? rsv : 0.0f;
         }
         __syncwarp();
         if (lane == 0) {

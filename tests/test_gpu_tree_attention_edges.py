@@ -72,3 +72,81 @@ def test_heads_of_256_over_long_contexts(qlin_gpu, fmt):
         torch.cuda.synchronize()
         assert q.qlin_get_device_error() == 0
         assert torch.equal(p.out, first) and torch.equal(p.lse, lse)
+
+
+# One shape for each kernel and head size: few rows of queries per key head, and many.
+SIZES = [(64, 1), (128, 3), (256, 2), (64, 7), (128, 9)]
+FMTS = ["int8", "e4m3", "u4"]
+
+
+def _leave_behind(q, fmt, d):
+    """Fills the shared memory of every block with codes 0x80 (E4M3's -0) and scales of -0 before the next call."""
+    kind = torch.int8 if fmt == "int8" else torch.uint8
+    width = d // 2 if fmt == "u4" else d
+    codes = torch.full((64, 1, 256, width), 128, dtype=torch.uint8, device="cuda").view(kind)
+    scales = torch.full((64, 1, 256, 2) if fmt == "u4" else (64, 1, 256), -0.0, dtype=torch.float16 if fmt == "u4" else torch.float32,
+                        device="cuda")
+    cache = q.qlin_kv_cache(codes, codes, scales, scales, {"int8": q.QLIN_KV_INT8, "e4m3": q.QLIN_KV_E4M3, "u4": q.QLIN_KV_U4}[fmt])
+    for rows in (1, 20):
+        x = torch.zeros(4 * rows, 1, d, dtype=torch.float16, device="cuda")
+        ws = torch.empty(q.qlin_tree_attention_workspace_bytes(cache, 1, rows, 4), dtype=torch.uint8, device="cuda")
+        q.qlin_tree_attention(x, cache, torch.arange(64, dtype=torch.int32, device="cuda").view(1, 64).repeat(4, 16),
+                              rows * torch.arange(5, dtype=torch.int32, device="cuda"),
+                              torch.full((4,), 64 * 256 * 15, dtype=torch.int32, device="cuda"), None, torch.empty_like(x), ws, rows)
+
+
+def _put(p, where, words, which=(2, 3)):
+    """Scale words (numbers, or for "u4" pairs) of the given tensors at the places `where` (bool [pages][page])."""
+    for i in which:
+        dtype = p.t[i].dtype
+        at = where[:, None, :].expand(p.t[i].shape[:3]).cuda()
+        p.t[i][at] = torch.tensor(words, dtype=torch.float64).to(dtype).cuda()
+
+
+def _live(p):
+    where = torch.zeros(p.t[0].shape[0], p.page, dtype=torch.bool)
+    for b, (c, n) in enumerate(p.seqs):
+        j = torch.arange(c + n)
+        where[p.table[b, j // p.page].long(), j % p.page] = True
+    return where
+
+
+def _place(p, b, j):
+    where = torch.zeros(p.t[0].shape[0], p.page, dtype=torch.bool)
+    where[int(p.table[b, j // p.page]), j % p.page] = True
+    return where
+
+
+def _hide(p, node):
+    """No row of the first sequence sees node `node` of it."""
+    p.bits[:p.seqs[0][1], node] = False
+    p.mask = _bits(p.bits)
+
+
+FAR = 2.0 ** -149
+WORDS = [0.0, -0.0, -FAR, FAR, float("inf"), -float("inf"), -1.5, 3e38, float("nan")]
+PAIRS = [(0.0, 0.0), (-0.0, 3.0), (-2.0 ** -24, 15.0), (float("inf"), 0.0), (-1.0, -0.0), (65504.0, 7.5), (0.01, float("nan")),
+         (0.01, -300.0), (float("nan"), float("inf"))]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,nodes", SIZES)
+@pytest.mark.parametrize("ctx", [37, 160])
+def test_scales_that_nobody_sees(qlin_gpu, fmt, d, nodes, ctx):
+    """Whatever the scale words of places behind a sequence's end and of a node that no row sees hold, and whatever
+    lies in shared memory where a tile has no page: the same bits."""
+    q = qlin_gpu
+    p = Problem(q, [(ctx, nodes), (10, 2)], 8, 2, d, 16, fmt, torch.float16, "tree", nodes)
+    if nodes > 1:
+        _hide(p, 1)
+    gone = ~_live(p) | (_place(p, 0, ctx + 1) if nodes > 1 else False)
+    _put(p, gone, (1.0, 3.0) if fmt == "u4" else 1.0)
+    clean, lse = p.run()
+    p.check()
+    clean = clean.clone()
+    for word in PAIRS if fmt == "u4" else WORDS:
+        _put(p, gone, word)
+        _leave_behind(q, fmt, d)
+        out, l2 = p.run()
+        p.check()
+        assert torch.equal(out, clean) and torch.equal(l2, lse), word
