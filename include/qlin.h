@@ -838,7 +838,11 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  *   out = sum_j p_ij v_j, p = softmax over what node i sees of
  *   scale (q_i . k_j); lse = ln sum_j exp(scale (q_i . k_j))
  * A node that sees nothing gets out = 0 and lse = -infinity.  What a node
- * does not see does not reach its output, whatever its scales hold.  Codes
+ * does not see does not reach its output, whatever its scales hold.  Scales may
+ * be zero or negative; one that is not a number makes NaN (a value scale: of
+ * out, an infinite one infinities or NaN) in the rows that see its token.  The
+ * value scales of a row's tokens may lie 2^117 apart (smaller ones than 2^-91
+ * counted as that, zeros as 2^-64); beyond, the small one's weight is lost.  Codes
  * enter the products exactly; sums are in float32, and the probabilities are
  * rounded to fp16 before they meet the codes of v.  The result depends on the
  * sequences' lengths and the GPU's number of SMs, not on timing.

@@ -6,7 +6,8 @@
 // integers or E4M3 numbers, exact in fp16):
 //   t_ij = log2(e) scale sk_j (q_i . n_j) + log2(sv_j)
 //   o_i  = sum_j 2^(t_ij - m_i) u_j / sum_j 2^(t_ij - m_i) / sv_j
-// for any reference m_i, so the codes go to the tensor cores as they are and
+// for any reference m_i (scales that are zero, negative or out of range: usable_scale
+// in tree_common.cuh), so the codes go to the tensor cores as they are and
 // neither product rounds an operand except the probabilities 2^(t - m) (to
 // fp16).  q rows are scaled by a power of two to below 2^15 before they become
 // fp16: exact for fp16, and for bf16 down to 2^-39 of the row's largest.  The
@@ -90,10 +91,12 @@ struct Geo {
   static constexpr int kOffMerge = kOffScale + kStages * 2 * kScaleBytes;
   static constexpr int kMergeRow = D + 4;  // floats
   static constexpr int kOffMl = kOffMerge + kWarps * kRows * kMergeRow * 4;
-  static constexpr int kOffBar = kOffMl + kWarps * kRows * 8;
+  static constexpr int kOffFactor = kOffMl + kWarps * kRows * 8;  // [warp][token]: see usable_scale
+  static constexpr int kOffBar = kOffFactor + kWarps * kTile * 4;
   static constexpr int kOffScan = kOffBar + 2 * kStages * 8;
   static constexpr int kOffWalk = (kOffScan + (kThreads + 1) * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffWalk + kWarps * static_cast<int>(sizeof(Walk<kRows, kTile>)) + 1024;  // + alignment of the base
+  static_assert(kBlocksPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory of an SM");
 
   // where 16-byte chunk c of row r of a column block lies
   static __device__ __forceinline__ uint32_t chunk(int r, int c) {
@@ -268,6 +271,21 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
       const uint8_t* sc = smem + G::kOffScale + stage * 2 * G::kScaleBytes;
       const bool masked = j0 + kTile > w.s.ctx;
 
+      // odd value scales of the unit (it is this warp's alone until it is given free), those behind the end among them
+      float* factors = reinterpret_cast<float*>(smem + G::kOffFactor) + warp * kTile;
+      bool odd = false;  // a token of the sequence has one
+      {
+        uint32_t* word = reinterpret_cast<uint32_t*>(smem + G::kOffScale + stage * 2 * G::kScaleBytes + G::kScaleBytes) + lane;
+        const bool mine = odd_scale<FMT>(*word);
+        if (__any_sync(0xffffffffu, mine)) {
+          odd = __any_sync(0xffffffffu, mine && j0 + lane < w.s.len);
+          float factor = 1.0f;
+          if (mine) *word = usable_scale<FMT>(*word, factor);
+          factors[lane] = factor;
+          __syncwarp();
+        }
+      }
+
       // scores of 16 rows x 32 tokens; this lane's: rows g, g + 8, tokens 8 n + 2 r + {0, 1}
       float s[4][4];
 #pragma unroll
@@ -357,10 +375,6 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
                          : ((p.mask[(w.s.q_row + node) * p.mask_words + (j >> 6)] >> (j & 63)) & 1) != 0;
             if (!seen) s[n][i] = -INFINITY;
           }
-          // a hidden token adds nothing to l, whatever its scale is (1 / -0 is -infinity); one that is seen makes t a NaN with it
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (!(fabsf(rsv[2 * n + i]) < INFINITY)) rsv[2 * n + i] = 0.0f;
         }
       }
 
@@ -393,18 +407,25 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
           }
         }
       }
-      const bool small = __any_sync(0xffffffffu, fminf(lo[0] - ref[0], lo[1] - ref[1]) < kHalfExp);
+      const bool small = odd || __any_sync(0xffffffffu, fminf(lo[0] - ref[0], lo[1] - ref[1]) < kHalfExp);
       uint32_t pa[4][2];
+      auto weigh = [&](auto with_factors) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < 4; ++n) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[n][i] = ex2(s[n][i] - ref[i >> 1]);
-          l[i >> 1] = fmaf(s[n][i], rsv[2 * n + (i & 1)], l[i >> 1]);
+          for (int i = 0; i < 4; ++i) {
+            const float t = s[n][i];
+            s[n][i] = ex2(t - ref[i >> 1]);
+            l[i >> 1] = fmaf(s[n][i], rsv[2 * n + (i & 1)], l[i >> 1]);
+            if constexpr (decltype(with_factors)::value)  // (what is hidden has no product with a factor that is not a number)
+              s[n][i] = t == -INFINITY ? 0.0f : s[n][i] * factors[8 * n + 2 * r + (i & 1)];
+          }
+          pa[n][0] = kv::pack2<0>(s[n][0], s[n][1]);
+          pa[n][1] = kv::pack2<0>(s[n][2], s[n][3]);
         }
-        pa[n][0] = kv::pack2<0>(s[n][0], s[n][1]);
-        pa[n][1] = kv::pack2<0>(s[n][2], s[n][3]);
-      }
+      };
+      if (odd) weigh(std::true_type{});
+      else weigh(std::false_type{});
 
       // p . v: the lane's tokens 16 k + 2 r + {0, 1, 8, 9}, contiguous channels of each
       const bool tail = j0 + kTile > w.s.len;
@@ -474,8 +495,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float a = s[n][2 * h], b = s[n][2 * h + 1];
-            rest[n][h] = kv::pack2<0>(a < kHalfNormal ? 0.0f : a, b < kHalfNormal ? 0.0f : b);
-            pa[n][h] = kv::pack2<0>(a < kHalfNormal ? a * G::kShiftUp : 0.0f, b < kHalfNormal ? b * G::kShiftUp : 0.0f);
+            const bool sa = fabsf(a) < kHalfNormal, sb = fabsf(b) < kHalfNormal;
+            rest[n][h] = kv::pack2<0>(sa ? 0.0f : a, sb ? 0.0f : b);
+            pa[n][h] = kv::pack2<0>(sa ? a * G::kShiftUp : 0.0f, sb ? b * G::kShiftUp : 0.0f);
           }
         accumulate(std::true_type{});
 #pragma unroll

@@ -195,6 +195,38 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t* w) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
 }
 
+// The kernels fold log2(sv) of a value scale into the exponent, so they work with scales in [kLeastScale, kMostScale]
+// and a factor for each token: sv = usable scale x factor, t and l from the usable scale, P multiplied by the factor
+// before it is rounded.  The factor is 1 but for scales that are negative (-1), zero (0), outside the bounds (below: less
+// than 1, down to 2^-58 for the smallest subnormal) or not numbers; tiles without such a scale skip it.  A zero (or what
+// is not a number) stands at 2^-64, the smallest scale that the cache write gives.  With the lower bound l stays below
+// 2^127 for 2^21 tokens of such scales at equal weights, and P of a row of subnormal scales alone keeps its bits.  (A token's
+// share of l is lost when its usable scale lies 2^117 or more below that of the token that weighs most.)
+constexpr uint32_t kLeastScale = 0x12000000u, kMostScale = 0x7e800000u;  // 2^-91 and 2^126, as bits
+
+template <int FMT>
+__device__ __forceinline__ bool odd_scale(uint32_t word) {
+  if constexpr (FMT == QLIN_KV_U4) return (word & 0xffffu) - 1u > 0x7bffu - 1u;  // fp16: all positive numbers are usable
+  else return word - kLeastScale > kMostScale - kLeastScale;
+}
+
+// The scale word with a usable scale in place of an odd one; the factor goes to `factor`.
+template <int FMT>
+__device__ __forceinline__ uint32_t usable_scale(uint32_t word, float& factor) {
+  if constexpr (FMT == QLIN_KV_U4) {
+    const uint32_t a = word & 0x7fffu;
+    const uint32_t u = a == 0 || a >= 0x7c00u ? 1u : a;  // 2^-24 for what has no logarithm
+    factor = __half2float(__ushort_as_half(static_cast<unsigned short>(word))) /
+             __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+    return (word & 0xffff0000u) | u;
+  } else {
+    const uint32_t a = word & 0x7fffffffu;
+    const uint32_t u = a == 0 || a >= 0x7f800000u ? 0x1f800000u : min(max(a, kLeastScale), kMostScale);
+    factor = __uint_as_float(word) / __uint_as_float(u);
+    return u;
+  }
+}
+
 // 16 bytes from global to shared memory, asynchronously; streamed codes leave L2 first.
 __device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy)

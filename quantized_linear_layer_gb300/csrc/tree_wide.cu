@@ -36,6 +36,7 @@
 // GB/s.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "stage_ring.h"
 #include "tree_common.cuh"
@@ -77,14 +78,14 @@ struct Geo {
   static constexpr int kOffV = kOffK + kOperand;        // two buffers
   static constexpr int kOffRaw = kOffV + 2 * kOperand;
   static constexpr int kOffScale = kOffRaw + kStages * 2 * kRawCode;
-  static constexpr int kOffCol = kOffScale + kStages * 2 * kHalf * 4;  // [kCols][scale log2(e) sk, log2 sv, 1 / sv][128]
-  static constexpr int kOffPair = kOffCol + kCols * 3 * kTile * 4;     // [tile parity][thread of the row][row]
+  static constexpr int kOffCol = kOffScale + kStages * 2 * kHalf * 4;  // [kCols][scale log2(e) sk, log2 sv, 1 / sv, factor][128]
+  static constexpr int kOffPair = kOffCol + kCols * 4 * kTile * 4;     // [tile parity][thread of the row][row]
   static constexpr int kOffQmax = kOffPair + 2 * kSubs * kRows * 4;    // [thread of the row][row]
   static constexpr int kOffEnd = kOffQmax + kSubs * kRows * 4;         // [thread of the row][row] (l, small)
   static constexpr int kOffBar = kOffEnd + kSubs * kRows * 8;
   static constexpr int kBars = 2 * kStages + 1 + 1 + 2 + 2 + 2 + 2 + 1 + 1 + kCols;
   static constexpr int kOffMisc = kOffBar + kBars * 8;  // tensor memory address, flags
-  static constexpr int kOffScan = kOffMisc + 16;
+  static constexpr int kOffScan = kOffMisc + 32;
   static constexpr int kOffWalk = (kOffScan + (kThreads + 1) * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffWalk + (kSoftmaxWarps + kWidenWarps) * static_cast<int>(sizeof(W)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -137,6 +138,14 @@ __device__ __forceinline__ __half2 flush(uint32_t v) {
   uint32_t r;
   asm("mul.rn.ftz.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x3c003c00u));
   return *reinterpret_cast<const __half2*>(&r);
+}
+
+// Two probabilities as fp16: what fp16 cannot hold as a normal number is 0 in `large` and, times `up` (2^29), in `small`.
+__device__ __forceinline__ void split(uint64_t e, uint64_t up, uint32_t& large, uint32_t& small) {
+  const float2 f = unpair(e), s = unpair(mul2(e, up));
+  const __half2 p16 = flush(kv::pack2<0>(f.x, f.y));
+  large = *reinterpret_cast<const uint32_t*>(&p16);
+  small = kv::pack2<0>(s.x, s.y) & __heq2_mask(p16, __float2half2_rn(0.0f));
 }
 
 // Shared-memory descriptor of an operand stored k x n with n contiguous, in
@@ -214,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
   volatile uint32_t* ran_out = tmem_slot + 1;  // a wait of some role of the block ran out
   volatile uint32_t* small_tile = reinterpret_cast<volatile uint32_t*>(smem + G::kOffMisc + 8);  // [2]: 1 + the last tile with any
+  volatile uint32_t* odd_tile = small_tile + 2;  // [kCols]: 1 + the last tile with a factor (usable_scale) that is not 1
   int64_t* scan = reinterpret_cast<int64_t*>(smem + G::kOffScan);
 
   if (threadIdx.x == 0) {
@@ -232,7 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
     }
     tc::mbar_init(q_full, kSoftmaxWarps);
     tc::mbar_init(all_done, 1);
-    for (int i = 0; i < kCols; ++i) tc::mbar_init(col_full + 8 * i, kWidenWarps);
+    for (int i = 0; i < kCols; ++i) {
+      tc::mbar_init(col_full + 8 * i, kWidenWarps);
+      odd_tile[i] = 0;
+    }
     *ran_out = 0;
     tc::fence_mbar_init();
   }
@@ -492,7 +505,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         if (lane < 16) {
           const int token = (part & 3) * 16 + lane;  // of the half tile
           const uint32_t kw = *reinterpret_cast<const uint32_t*>(scales + token * 4);
-          const uint32_t vw = *reinterpret_cast<const uint32_t*>(scales + (kHalf + token) * 4);
+          uint32_t vw = *reinterpret_cast<const uint32_t*>(scales + (kHalf + token) * 4);
+          float factor = 1.0f;
+          if (odd_scale<FMT>(vw)) {
+            vw = usable_scale<FMT>(vw, factor);
+            if (j0 + part * 16 + lane < len) odd_tile[t % kCols] = t + 1;
+          }
           float sk, sv;
           if constexpr (G::kU4) {
             sk = __half2float(__ushort_as_half(static_cast<unsigned short>(kw & 0xffffu)));
@@ -501,12 +519,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
             sk = __uint_as_float(kw);
             sv = __uint_as_float(vw);
           }
-          const float rsv = rcp(sv);
-          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + part * 16 + lane;
+          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 4 * kTile + part * 16 + lane;
           col[0] = sk * (p.scale * kLog2e);
           col[kTile] = lg2(sv);
-          // a hidden token adds nothing to l, whatever its scale is (1 / -0 is -infinity); one that is seen makes t a NaN with it
-          col[2 * kTile] = fabsf(rsv) < INFINITY ? rsv : 0.0f;
+          col[2 * kTile] = rcp(sv);
+          col[3 * kTile] = factor;
         }
         __syncwarp();
         if (lane == 0) {
@@ -636,11 +653,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         wait(col_full + 8 * (t % kCols), t / kCols, 0x6b);
         dead = __any_sync(0xffffffffu, dead);
         tc::tc_fence_after();
+        const bool odd = odd_tile[t % kCols] == t + 1;  // read before it is needed: 40 cycles of a tile's 3900
         const uint32_t s_at = lanes + buf * 128;
         uint32_t v[kSpan];
         tc::tmem_ld_32x32b_x32(s_at + sub * kSpan, v);
         tc::tmem_wait_ld(v);
-        const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 3 * kTile + sub * kSpan;
+        const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 4 * kTile + sub * kSpan;
         if (!__all_sync(0xffffffffu, row_scale == 1.0f)) {
           const uint64_t rs = pair(row_scale, row_scale);
 #pragma unroll
@@ -685,30 +703,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
 
         const uint64_t nref = pair(-ref, -ref), up = pair(kShiftUp, kShiftUp);
         uint32_t any_small = 0;
-#pragma unroll
-        for (int h = 0; h < kSpan; h += 32) {
+        auto weigh = [&](auto with_factors) {
           uint32_t pk[16], ps[16];
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
-            const float4 rv = *reinterpret_cast<const float4*>(col + 2 * kTile + h + k);
+            const float4 rv = *reinterpret_cast<const float4*>(col + 2 * kTile + k);
             const float rr[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
             for (int x = 0; x < 4; x += 2) {
-              const int i0 = h + k + x;
+              const int i0 = k + x;
               const float2 a = unpair(add2(pair(__uint_as_float(v[i0]), __uint_as_float(v[i0 + 1])), nref));
-              const uint64_t e = pair(ex2(a.x), ex2(a.y));
+              uint64_t e = pair(ex2(a.x), ex2(a.y));
               l2 = fma2(e, pair(rr[x], rr[x + 1]), l2);
-              const float2 f = unpair(e), s = unpair(mul2(e, up));
-              // what fp16 cannot hold as a normal number is 0 here and, times 2^29, in the other part
-              const __half2 p16 = flush(kv::pack2<0>(f.x, f.y));
-              pk[(k + x) / 2] = *reinterpret_cast<const uint32_t*>(&p16);
-              ps[(k + x) / 2] = kv::pack2<0>(s.x, s.y) & __heq2_mask(p16, __float2half2_rn(0.0f));
+              if constexpr (decltype(with_factors)::value) {  // (what is hidden has no product with a factor that is not a number)
+                const float2 f = unpair(e);
+                e = pair(v[i0] == 0xff800000u ? 0.0f : f.x * col[3 * kTile + i0],
+                         v[i0 + 1] == 0xff800000u ? 0.0f : f.y * col[3 * kTile + i0 + 1]);
+              }
+              split(e, up, pk[i0 / 2], ps[i0 / 2]);
             }
             any_small |= ps[k / 2] | ps[k / 2 + 1];
           }
-          tc::tmem_st_32x32b_x16(s_at + (sub * kSpan + h) / 2, pk);
-          tc::tmem_st_32x32b_x16(s_at + 64 + (sub * kSpan + h) / 2, ps);
-        }
+          tc::tmem_st_32x32b_x16(s_at + sub * kSpan / 2, pk);
+          tc::tmem_st_32x32b_x16(s_at + 64 + sub * kSpan / 2, ps);
+        };
+        if (odd) weigh(std::true_type{});
+        else weigh(std::false_type{});
         had_small = had_small || any_small != 0;
         if (__any_sync(0xffffffffu, any_small != 0) && lane == 0) small_tile[buf] = t + 1;
         if (__any_sync(0xffffffffu, move) && i > 0) {  // the same in all warps of these rows

@@ -150,3 +150,85 @@ def test_scales_that_nobody_sees(qlin_gpu, fmt, d, nodes, ctx):
         out, l2 = p.run()
         p.check()
         assert torch.equal(out, clean) and torch.equal(l2, lse), word
+
+
+def _scale(p, i, b, j, word):
+    """The scale of the keys (i = 0) or values (i = 1) of token j of sequence b, on the host and the device."""
+    page, off = int(p.table[b, j // p.page]), j % p.page
+    if p.fmt == "u4":
+        p.scales[i][page, :, off, 0] = word
+        p.t[2 + i][page, :, off, 0] = float(np.float16(word))
+    else:
+        p.scales[i][page, :, off] = word
+        p.t[2 + i][page, :, off] = float(np.float32(word))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d,nodes", SIZES)
+def test_scales_of_zero_and_below_and_close_to_it(qlin_gpu, fmt, dtype, d, nodes):
+    """Rows of zeros by their scale, negative scales and subnormal ones count in the sum as they are, at any place of
+    a context and among the nodes."""
+    p = Problem(qlin_gpu, [(300, nodes), (40, nodes)], 8, 2, d, 32, fmt, dtype, "tree", nodes)
+    words = [0.0, -0.0, -0.01, 2.0 ** -24, -2.0 ** -20] if fmt == "u4" else [0.0, -0.0, -0.01, FAR, -2.0 ** -130, 2.0 ** -100, -2.0 ** -70]
+    r = np.random.default_rng(d)
+    for b, (c, n) in enumerate(p.seqs):
+        for i in range(2):
+            for j in r.permutation(c + n)[:(c + n) // 3]:
+                _scale(p, i, b, int(j), words[int(r.integers(len(words)))])
+    p.run()
+    p.check()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d,nodes", SIZES)
+def test_one_scale_for_all_values(qlin_gpu, fmt, dtype, d, nodes):
+    """All values zero; all near the smallest and the largest numbers of bf16; the lse is that of the keys throughout."""
+    p = Problem(qlin_gpu, [(300, nodes), (40, nodes)], 8, 2, d, 32, fmt, dtype, "tree", nodes, wide=0.0)
+    small = [0.0, -2.0 ** -24, 2.0 ** -16] if fmt == "u4" else [0.0, -0.0, 2.0 ** -126, -2.0 ** -131, 2.0 ** -92, -2.0 ** -64]
+    for word in small + ([] if fmt == "u4" or dtype == torch.float16 else [2.0 ** 100, -2.0 ** 110]):
+        for b, (c, n) in enumerate(p.seqs):
+            for j in range(c + n):
+                _scale(p, 1, b, j, word)
+        p.run()
+        p.check()
+        if word == 0:
+            assert not (p.out != 0).any()
+
+
+def _lse_bound(p):
+    """How far an lse may be off, [rows][heads]."""
+    out, row = [], 0
+    for b, (c, n) in enumerate(p.seqs):
+        j = np.arange(c + n)
+        pg = p.table[b, j // p.page].numpy()
+        k = ref.kv_values(p.codes[0][pg, :, j % p.page], p.scales[0][pg, :, j % p.page], p.fmt)
+        seen = np.ones((n, c + n), bool)
+        seen[:, c:] = np.tril(np.ones((n, n), bool)) if p.bits is None else p.bits[row:row + n, :n]
+        _, l, _, spread = ref.tree_attention(p.q[row:row + n].double().numpy(), k, k, seen, p.scale)
+        out.append(p.q.shape[2] * 2.0 ** -24 * spread + (c + n + 64) * 2.0 ** -24 + 2.0 ** -22 * np.abs(l))
+        row += n
+    return np.concatenate(out)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,nodes", SIZES)
+def test_values_that_are_not_numbers(qlin_gpu, fmt, d, nodes):
+    """A value row whose scale is NaN or infinite makes every row that sees it not a number, and no other; lse is of
+    the keys alone."""
+    p = Problem(qlin_gpu, [(100, nodes), (40, nodes)], 8, 2, d, 32, fmt, torch.bfloat16, "chain", nodes)
+    clean, lse = (x.clone() for x in p.run())
+    p.check()
+    keep = [x.clone() for x in p.t]
+    bound = torch.from_numpy(_lse_bound(p))
+    for word in (float("nan"), float("inf"), -float("inf")):
+        for j in (3, 100 + nodes - 1):
+            for x, y in zip(p.t, keep):
+                x.copy_(y)
+            _put(p, _place(p, 0, j), (word, 3.0) if fmt == "u4" else word, (3,))
+            out, l2 = p.run()
+            hit = torch.zeros(2 * nodes, dtype=torch.bool)
+            hit[0 if j < 100 else nodes - 1:nodes] = True
+            assert torch.equal(out[~hit], clean[~hit]) and not torch.isfinite(out[hit]).any()
+            assert ((l2 - lse).abs().double().cpu() <= 2 * bound).all()
