@@ -135,7 +135,8 @@ typedef struct {
    the head_dim codes at k + page * page_stride + (h * page_size + offset) *
    row bytes (head_dim, or head_dim / 2 for U4), its scale the 4 bytes at
    k_scale + page * scale_page_stride + 4 (h * page_size + offset): a float32,
-   or for U4 an fp16 scale and then an fp16 zero-point.  Values likewise. */
+   or for U4 an fp16 scale and then an fp16 zero-point, a whole number from 0 to
+   15.  Values likewise. */
 typedef struct {
   void* k;
   void* v;
@@ -840,7 +841,8 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * A node that sees nothing gets out = 0 and lse = -infinity.  What a node
  * does not see does not reach its output, whatever its scales hold.  Scales may
  * be zero or negative; one that is not a number makes NaN (a value scale: of
- * out, an infinite one infinities or NaN) in the rows that see its token.  The
+ * out, an infinite one infinities or NaN) in the rows that see its token, and so
+ * does a zero-point that is none (qlin_kv_cache_read takes any as it is).  The
  * value scales of a row's tokens may lie 2^117 apart (smaller ones than 2^-91
  * counted as that, zeros as 2^-64); beyond, the small one's weight is lost.  Codes
  * enter the products exactly; sums are in float32, and the probabilities are

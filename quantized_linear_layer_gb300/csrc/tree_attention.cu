@@ -275,12 +275,22 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
       float* factors = reinterpret_cast<float*>(smem + G::kOffFactor) + warp * kTile;
       bool odd = false;  // a token of the sequence has one
       {
-        uint32_t* word = reinterpret_cast<uint32_t*>(smem + G::kOffScale + stage * 2 * G::kScaleBytes + G::kScaleBytes) + lane;
-        const bool mine = odd_scale<FMT>(*word);
+        uint32_t* of_k = reinterpret_cast<uint32_t*>(smem + G::kOffScale + stage * 2 * G::kScaleBytes) + lane;
+        uint32_t* word = of_k + kTile;
+        bool mine = odd_scale<FMT>(*word);
+        if constexpr (G::kU4) mine = mine || odd_zero(*of_k) || odd_zero(*word);
         if (__any_sync(0xffffffffu, mine)) {
           odd = __any_sync(0xffffffffu, mine && j0 + lane < w.s.len);
           float factor = 1.0f;
-          if (mine) *word = usable_scale<FMT>(*word, factor);
+          if (mine) {
+            uint32_t v = *word;
+            if (odd_scale<FMT>(v)) v = usable_scale<FMT>(v, factor);
+            if constexpr (G::kU4) {  // without a zero-point a token is not a number: its score, or its factor
+              if (odd_zero(*of_k)) *of_k = 0x7fffu;
+              if (odd_zero(v)) v &= 0xffffu, factor = __uint_as_float(0x7fc00000u);
+            }
+            *word = v;
+          }
           factors[lane] = factor;
           __syncwarp();
         }
@@ -354,10 +364,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
         }
         if constexpr (G::kU4) {
           const uint32_t z = __byte_perm(vw.x, vw.y, 0x7632);
-          // a zero-point that is not one (its token is not seen) becomes 0: what is not seen has to stay finite
-          const __half2 zz = __hmin2(__hmax2(*reinterpret_cast<const __half2*>(&z), __float2half2_rn(0.0f)),
-                                     __float2half2_rn(15.0f));
-          const __half2 b = __hadd2(zz, __float2half2_rn(1024.0f));
+          const __half2 b = __hadd2(*reinterpret_cast<const __half2*>(&z), __float2half2_rn(1024.0f));
           vz[n] = *reinterpret_cast<const uint32_t*>(&b);
         }
       }

@@ -227,6 +227,13 @@ __device__ __forceinline__ uint32_t usable_scale(uint32_t word, float& factor) {
   }
 }
 
+// Whether the zero-point of a U4 scale word is none: not a whole number from 0 to 15 (1024 + n, n < 16, is 0x6400 | n).
+__device__ __forceinline__ bool odd_zero(uint32_t word) {
+  const __half z = __ushort_as_half(static_cast<unsigned short>(word >> 16)), big = __float2half_rn(1024.0f);
+  const __half b = __hadd(z, big);
+  return __half_as_ushort(b) - 0x6400u > 15u || !__heq(__hsub(b, big), z);
+}
+
 // 16 bytes from global to shared memory, asynchronously; streamed codes leave L2 first.
 __device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy)

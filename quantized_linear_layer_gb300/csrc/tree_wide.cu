@@ -465,7 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
             uint32_t bias = 0;
             if constexpr (G::kU4) {
               const uint32_t word = *reinterpret_cast<const uint32_t*>(sc + x * kRowsAtOnce * 4);
-              // a zero-point that is not one (its token is not seen) becomes 0: what is not seen has to stay finite
+              // what is no zero-point becomes one: its token counts by its score and its factor, and what is not seen has
+              // to stay finite
               const __half z = __hmin(__hmax(__ushort_as_half(static_cast<unsigned short>(word >> 16)), __float2half(0.0f)),
                                       __float2half(15.0f));
               const __half2 zz = __half2half2(__hadd(z, __float2half(1024.0f)));
@@ -507,13 +508,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           const uint32_t kw = *reinterpret_cast<const uint32_t*>(scales + token * 4);
           uint32_t vw = *reinterpret_cast<const uint32_t*>(scales + (kHalf + token) * 4);
           float factor = 1.0f;
-          if (odd_scale<FMT>(vw)) {
-            vw = usable_scale<FMT>(vw, factor);
-            if (j0 + part * 16 + lane < len) odd_tile[t % kCols] = t + 1;
+          bool odd = odd_scale<FMT>(vw);
+          if (odd) vw = usable_scale<FMT>(vw, factor);
+          if constexpr (G::kU4) {  // without a zero-point a token is not a number: its factor here, its score below
+            if (odd_zero(vw)) odd = true, factor = __uint_as_float(0x7fc00000u);
           }
+          if (odd && j0 + part * 16 + lane < len) odd_tile[t % kCols] = t + 1;
           float sk, sv;
           if constexpr (G::kU4) {
-            sk = __half2float(__ushort_as_half(static_cast<unsigned short>(kw & 0xffffu)));
+            sk = odd_zero(kw) ? __uint_as_float(0x7fc00000u) : __half2float(__ushort_as_half(static_cast<unsigned short>(kw & 0xffffu)));
             sv = __half2float(__ushort_as_half(static_cast<unsigned short>(vw & 0xffffu)));
           } else {
             sk = __uint_as_float(kw);

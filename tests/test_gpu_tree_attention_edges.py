@@ -232,3 +232,28 @@ def test_values_that_are_not_numbers(qlin_gpu, fmt, d, nodes):
             hit[0 if j < 100 else nodes - 1:nodes] = True
             assert torch.equal(out[~hit], clean[~hit]) and not torch.isfinite(out[hit]).any()
             assert ((l2 - lse).abs().double().cpu() <= 2 * bound).all()
+
+
+@pytest.mark.parametrize("d,nodes", SIZES)
+@pytest.mark.parametrize("word", [7.5, -1.0, 16.0, 15.25, 1024.0, float("nan"), float("inf"), -float("inf")])
+def test_zero_points_that_are_none(qlin_gpu, d, nodes, word):
+    """A zero-point that is not a whole number from 0 to 15 makes its token not a number: for the rows that see it,
+    and no other."""
+    p = Problem(qlin_gpu, [(100, nodes), (40, nodes)], 8, 2, d, 32, "u4", torch.float16, "chain", nodes)
+    clean, lse = (x.clone() for x in p.run())
+    p.check()
+    keep = [x.clone() for x in p.t]
+    for which in ((2,), (3,)):
+        for j in (3, 100 + nodes - 1):
+            for x, y in zip(p.t, keep):
+                x.copy_(y)
+            at = _place(p, 0, j)
+            for i in which:
+                p.t[i].view(-1, 2, p.page, 2)[int(p.table[0, j // p.page]), :, j % p.page, 1] = word
+            assert at.any()
+            out, l2 = p.run()
+            hit = torch.zeros(2 * nodes, dtype=torch.bool)
+            hit[0 if j < 100 else nodes - 1:nodes] = True
+            assert torch.equal(out[~hit], clean[~hit]) and torch.isnan(out[hit]).all()
+            assert torch.equal(l2[~hit], lse[~hit])
+            assert torch.isnan(l2[hit]).all() if which == (2,) else torch.equal(l2, lse)
