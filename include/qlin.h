@@ -791,9 +791,12 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * Heads are of D = 64, 128 or 256 elements of F16 or BF16.  Every entry point
  * here only reads lengths, page numbers and places on the device, so all of
  * them can be captured into a graph and replayed while those change.  An
- * index on the device that is out of range (a place, a page number, a
- * sequence's bounds) is not used: the kernel skips it, records an error in
- * the device error word (qlin_get_device_error) and goes on.
+ * index on the device that is out of range is not used: the kernel records an
+ * error in the device error word (qlin_get_device_error) and goes on.  A place
+ * of a write is left out; the tokens of a page whose number is out of range are
+ * zeros, for the read and as keys and values of attention alike; so are rows of
+ * the read that no sequence has; a sequence of attention whose bounds are out of
+ * range is left out, and its rows of out and lse stay as they were.
  *
  * qlin_qk_norm_rope: for every token t and head of q and of k
  *   y = x / sqrt(mean(x^2) + eps) * gamma      (y = x when gamma is NULL)

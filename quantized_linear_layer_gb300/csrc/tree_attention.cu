@@ -146,27 +146,20 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
     const uint64_t policy = tc::l2_policy_evict_first();
     while (!dead && w.next(p)) {
       const int32_t* table = p.table + w.b * p.max_pages;
-      int32_t ahead = -1;  // the page of box `lane` of the 32 boxes from unit `from` on
+      int32_t ahead = kNoPage;  // the page of box `lane` of the 32 boxes from unit `from` on
       int from = 0;
       for (int t = w.tile; t < w.tile + w.tiles; ++t) {
         if (t == w.tile || (t - from) * boxes == 32) {
           from = t;
           const int j = t * kTile + lane * box;
-          ahead = -1;
-          if (j < min(w.s.len, (w.tile + w.tiles) * kTile)) {
-            ahead = table[j >> p.page_shift];
-            if (ahead < 0 || ahead >= p.pages) {
-              record_device_error(p.err, kDevErrBadIndex);
-              ahead = -1;
-            }
-          }
+          ahead = kNoPage;
+          if (j < min(w.s.len, (w.tile + w.tiles) * kTile)) ahead = checked_page(p, table[j >> p.page_shift]);
         }
         if (!tc::mbar_wait_quiet(bar_free + 8 * stage, phase, p.err, 0x50)) dead = true;
         if (__any_sync(0xffffffffu, dead)) {
           dead = true;
           break;
         }
-        // this unit's boxes; those past the end have no page
         const uint32_t codes = base + stage * G::kStage, scales = base + G::kOffScale + stage * 2 * G::kScaleBytes;
         auto row_at = [](int r, int c) { return c / (G::kW / 16) * G::kSubBytes + G::chunk(r, c % (G::kW / 16)); };
         const int at = (t - from) * boxes;

@@ -234,9 +234,10 @@ __device__ __forceinline__ bool odd_zero(uint32_t word) {
   return __half_as_ushort(b) - 0x6400u > 15u || !__heq(__hsub(b, big), z);
 }
 
-// 16 bytes from global to shared memory, asynchronously; streamed codes leave L2 first.
-__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "l"(policy)
+// 16 bytes from global to shared memory, asynchronously, or zeros (bytes = 0: nothing is read); streamed codes leave L2
+// first.
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from, uint32_t bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(to), "l"(from), "r"(bytes), "l"(policy)
                : "memory");
 }
 // Arrives on `bar` (one of its expected arrivals) once this thread's copies so far are there.
@@ -245,8 +246,19 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// A box without a page: behind its sequence's end, where nobody sees its tokens, or with a page number out of range.  Its
+// codes and scales are zeros, as the cache read gives them, so that nothing the stage held before reaches a result.
+constexpr int32_t kNoPage = -1;
+
+// A page number as the table has it, checked.
+__device__ __forceinline__ int32_t checked_page(const Params& p, int32_t page) {
+  if (page >= 0 && page < p.pages) return page;
+  record_device_error(p.err, kDevErrBadIndex);
+  return kNoPage;
+}
+
 // One warp's copies of the scales of TOKENS tokens of a key head, from `first` on, into a stage of a ring.  `ahead` is
-// the page (or -1) of box `lane` of the 32 boxes of `box` tokens that hold the stage's boxes `at` ...
+// the page (or kNoPage) of box `lane` of the 32 boxes of `box` tokens that hold the stage's boxes `at` ...
 template <int TOKENS>
 __device__ __forceinline__ void copy_scales(const Params& p, int head, int first, int box, int32_t ahead, int at,
                                             uint32_t ks_to, uint32_t vs_to, uint64_t policy) {
@@ -255,10 +267,11 @@ __device__ __forceinline__ void copy_scales(const Params& p, int head, int first
   const int lane = threadIdx.x % 32;
   const int token = lane % kLanes * 4;
   const int32_t pg = __shfl_sync(0xffffffffu, ahead, (at + token / box) & 31);
-  if (pg < 0 || lane >= 2 * kLanes) return;
+  if (lane >= 2 * kLanes) return;
   const bool k = lane < kLanes;
   const int64_t row = (static_cast<int64_t>(head) << p.page_shift) + ((first + token) & ((1 << p.page_shift) - 1));
-  copy16((k ? ks_to : vs_to) + token * 4, (k ? p.k_scale : p.v_scale) + pg * p.scale_page_stride + row * 4, policy);
+  copy16((k ? ks_to : vs_to) + token * 4, (k ? p.k_scale : p.v_scale) + max(pg, 0) * p.scale_page_stride + row * 4,
+         pg < 0 ? 0 : 16, policy);
 }
 
 // One warp's copies of the codes of TOKENS tokens, page by page, box by box of BOX tokens; the other arguments are those
@@ -281,17 +294,17 @@ __device__ __forceinline__ void copy_codes(const Params& p, int head, int first,
 #pragma unroll
   for (int b = 0; b < TOKENS / BOX; ++b) {
     const int32_t pg = __shfl_sync(0xffffffffu, ahead, (at + b) & 31);
-    if (pg < 0) continue;
+    const uint32_t bytes = pg < 0 ? 0 : 16;
     const int64_t row = (static_cast<int64_t>(head) << p.page_shift) + ((first + b * BOX) & ((1 << p.page_shift) - 1));
-    const int64_t codes = pg * p.page_stride + row * ROW_BYTES + lane * 16;
+    const int64_t codes = max(pg, 0) * p.page_stride + row * ROW_BYTES + lane * 16;
     const uint8_t* k = p.k + codes;
     const uint8_t* v = p.v + codes;
 #pragma unroll
     for (int x = 0; x < BOX / kRowsAtOnce; ++x) {
       const int y = b * (BOX / kRowsAtOnce) + x;
       const uint32_t at16 = to[y % kPeriod] + y / kPeriod * step;
-      copy16(k_to + at16, k + x * 512, policy);
-      copy16(v_to + at16, v + x * 512, policy);
+      copy16(k_to + at16, k + x * 512, bytes, policy);
+      copy16(v_to + at16, v + x * 512, bytes, policy);
     }
   }
 }

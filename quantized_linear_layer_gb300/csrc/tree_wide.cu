@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
   if (warp == kLoadWarp) {
     // ---------------- loads ----------------
     ring::Filler<kStages> fill;
+    bool zeroed = false;
     const int page = 1 << p.page_shift;
     const int box = min(page, kHalf);
     const int boxes = kHalf / box;
@@ -287,20 +288,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
     while (run.next(p)) {
       const int32_t* table = p.table + run.b * p.max_pages;
       const int end = min(run.s.len, (run.tile + run.tiles) * kTile);
-      int32_t ahead = -1;  // the page of box `lane` of the 32 boxes from half tile `from` on
+      int32_t ahead = kNoPage;  // the page of box `lane` of the 32 boxes from half tile `from` on
+      unsigned bad = 0;  // of them, those whose page is out of range
       int from = 0;
       for (int t = 2 * run.tile; t < 2 * (run.tile + run.tiles); ++t) {
         if (t == 2 * run.tile || (t - from) * boxes == 32) {
           from = t;
           const int j = t * kHalf + lane * box;
-          ahead = -1;
-          if (j < end) {
-            ahead = table[j >> p.page_shift];
-            if (ahead < 0 || ahead >= p.pages) {
-              record_device_error(p.err, kDevErrBadIndex);
-              ahead = -1;
-            }
-          }
+          ahead = kNoPage;
+          if (j < end) ahead = checked_page(p, table[j >> p.page_shift]);
+          bad = __ballot_sync(0xffffffffu, j < end && ahead < 0);
         }
         if (!fill.wait(ops)) continue;
         const uint32_t stage = fill.stage();
@@ -311,15 +308,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
         const int good = __popc(__ballot_sync(0xffffffffu, load));
         if (lane == 0) tc::mbar_arrive_expect_tx(bar, good * box * 2 * G::kRowBytes);
         __syncwarp();
+        const uint32_t raw = base + G::kOffRaw + stage * 2 * G::kRawCode;
         if (load) {
           const int64_t row = static_cast<int64_t>(run.head) * page + ((t * kHalf + lane * box) & (page - 1));
           const int64_t codes = pg * p.page_stride + row * G::kRowBytes;
-          const uint32_t to = base + G::kOffRaw + stage * 2 * G::kRawCode + lane * box * G::kRowBytes;
+          const uint32_t to = raw + lane * box * G::kRowBytes;
+          if (zeroed) tc::fence_proxy_async_smem();  // the stage may hold zeros from below: written by another proxy
           tc::bulk_load_policy(to, p.k + codes, box * G::kRowBytes, bar, policy);
           tc::bulk_load_policy(to + G::kRawCode, p.v + codes, box * G::kRowBytes, bar, policy);
         }
         const uint32_t scales = base + G::kOffScale + stage * 2 * kHalf * 4;
         copy_scales<kHalf>(p, run.head, t * kHalf, box, ahead, (t - from) * boxes, scales, scales + kHalf * 4, policy);
+        if (bad != 0) {
+          for (int b = 0; b < boxes; ++b)
+            if ((bad >> ((t - from) * boxes + b)) & 1) {
+              const uint32_t to = raw + b * box * G::kRowBytes;
+              for (int x = lane * 16; x < box * G::kRowBytes; x += 512) {
+                copy16(to + x, p.k, 0, policy);
+                copy16(to + G::kRawCode + x, p.v, 0, policy);
+              }
+              zeroed = true;
+            }
+        }
         copies_arrive(bar);
         ++fill.filled;
       }

@@ -257,3 +257,40 @@ def test_zero_points_that_are_none(qlin_gpu, d, nodes, word):
             assert torch.equal(out[~hit], clean[~hit]) and torch.isnan(out[hit]).all()
             assert torch.equal(l2[~hit], lse[~hit])
             assert torch.isnan(l2[hit]).all() if which == (2,) else torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,nodes", SIZES)
+@pytest.mark.parametrize("page", [16, 64])
+def test_bad_pages_read_as_zeros(qlin_gpu, fmt, d, nodes, page):
+    """Tokens on a page whose number is out of range are keys and values of zeros, as the read gives them: nothing of
+    other sequences or of earlier calls reaches the result."""
+    q = qlin_gpu
+    p = Problem(q, [(300, nodes), (150, nodes)], 8, 2, d, page, fmt, torch.float16, "tree", nodes)
+    p.run()
+    p.check()
+    keep, bad = p.table.clone(), (p.t[0].shape[0], -1, -(1 << 31))
+    # the oracle's view: one more page, of zeros
+    p.codes, p.scales = (np.concatenate([x, np.zeros_like(x[:, :1])], axis=1) for x in (p.codes, p.scales))
+    first = None
+    for number, at in zip(bad, (1, 150 // page, 300 // page)):
+        for other in range(2):
+            host = keep.clone()
+            host[0, at] = host[0, 0] = p.codes.shape[1] - 1
+            p.table = keep.clone()
+            p.table[0, at] = p.table[0, 0] = number
+            _leave_behind(q, fmt, d)
+            out, _ = p.run()
+            if other == 0:
+                p.table = host
+                p.check(0x2000)
+                first = out.clone()
+                for x in p.t[:2]:    # what the other sequence and the unused pages hold
+                    gone = torch.ones(x.shape[0], dtype=torch.bool)
+                    gone[keep[0, :-(-(300 + nodes) // page)].long()] = False
+                    x[gone] = 0
+            else:
+                assert q.qlin_get_device_error() == 0x2000
+                assert torch.equal(out[:nodes], first[:nodes])
+                for x, y in zip(p.t, p.codes_dev):
+                    x.copy_(torch.from_numpy(y.copy()))
