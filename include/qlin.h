@@ -842,7 +842,9 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  *   out = sum_j p_ij v_j, p = softmax over what node i sees of
  *   scale (q_i . k_j); lse = ln sum_j exp(scale (q_i . k_j))
  * A node that sees nothing gets out = 0 and lse = -infinity.  What a node
- * does not see does not reach its output, whatever its scales hold.  Scales may
+ * does not see does not reach its output, whatever its codes and scales hold.
+ * (E4M3 codes that are NaN, which the library never writes, make NaN of out in
+ * the rows that see their token, in their channel or in all.)  Scales may
  * be zero or negative; one that is not a number makes NaN (a value scale: of
  * out, an infinite one infinities or NaN) in the rows that see its token, and so
  * does a zero-point that is none (qlin_kv_cache_read takes any as it is).  The

@@ -272,6 +272,15 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
         uint32_t* word = of_k + kTile;
         bool mine = odd_scale<FMT>(*word);
         if constexpr (G::kU4) mine = mine || odd_zero(*of_k) || odd_zero(*word);
+        bool nan_codes = false;  // among the values of nodes, or behind the end
+        if constexpr (FMT == QLIN_KV_E4M3) {
+          if (masked && j0 + lane >= w.s.ctx) {
+#pragma unroll 1
+            for (int c = 0; c < G::kRowBytes / 16; ++c)
+              nan_codes |= clear_nan_codes(vs_at + c / (G::kW / 16) * G::kSubBytes + G::chunk(lane, c % (G::kW / 16)));
+          }
+          mine = mine || nan_codes;
+        }
         if (__any_sync(0xffffffffu, mine)) {
           odd = __any_sync(0xffffffffu, mine && j0 + lane < w.s.len);
           float factor = 1.0f;
@@ -282,6 +291,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
               if (odd_zero(*of_k)) *of_k = 0x7fffu;
               if (odd_zero(v)) v &= 0xffffu, factor = __uint_as_float(0x7fc00000u);
             }
+            if (nan_codes) factor = __uint_as_float(0x7fc00000u);
             *word = v;
           }
           factors[lane] = factor;
@@ -428,7 +438,6 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
       else weigh(std::false_type{});
 
       // p . v: the lane's tokens 16 k + 2 r + {0, 1, 8, 9}, contiguous channels of each
-      const bool tail = j0 + kTile > w.s.len;
       auto accumulate = [&](auto shifted) {
         constexpr bool kShifted = decltype(shifted)::value;
 #pragma unroll
@@ -450,13 +459,6 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
               const int tok = 16 * k + 2 * r + (i & 1) + 8 * (i >> 1);
               const int byte = g * kLoad;
               lds<kLoad>(vs_at + h * G::kSubBytes + G::chunk(tok, byte / 16) + byte % 16, wd[i]);
-              if constexpr (FMT == QLIN_KV_E4M3) {
-                // beyond the sequence's end lies anything, E4M3 NaN among it
-                if (tail && j0 + tok >= w.s.len) {
-#pragma unroll
-                  for (int c = 0; c < kLoad / 4; ++c) wd[i][c] = 0u;
-                }
-              }
             }
 #pragma unroll
             for (int c = 0; c < kLoad / 4; ++c) {

@@ -234,6 +234,21 @@ __device__ __forceinline__ bool odd_zero(uint32_t word) {
   return __half_as_ushort(b) - 0x6400u > 15u || !__heq(__hsub(b, big), z);
 }
 
+// One thread's look at 16 bytes of E4M3 codes in shared memory: those that are NaN become 0 there; whether there were any.
+// (A product with a probability of 0 keeps a NaN, so what nobody sees must not hold one.)
+__device__ __forceinline__ bool clear_nan_codes(uint32_t at) {
+  const uint4 u = tc::lds128(at);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t bad[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad[i] = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  if ((bad[0] | bad[1] | bad[2] | bad[3]) == 0) return false;
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0] & ~bad[0]), "r"(w[1] & ~bad[1]), "r"(w[2] & ~bad[2]),
+               "r"(w[3] & ~bad[3])
+               : "memory");
+  return true;
+}
+
 // 16 bytes from global to shared memory, asynchronously, or zeros (bytes = 0: nothing is read); streamed codes leave L2
 // first.
 __device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from, uint32_t bytes, uint64_t policy) {

@@ -461,9 +461,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           const uint32_t from = raw + (v ? G::kRawCode : 0) + (part & 3) * 16 * G::kRowBytes + raw_at;
           const uint8_t* sc = scales + (v ? kHalf * 4 : 0) + ((part & 3) * 16 + row) * 4;
           const uint32_t out = to + part * 16 * 128 + out_at;
-          // beyond the sequence's end lies anything: zeros for the second product
-          const int alive = v ? len - (j0 + part * 16 + row) : 16;  // of this lane's rows, those below it
-          const bool tail = v && j0 + kTile > len;
           uint4 u[G::kBlocks * 16 / kRowsAtOnce];
 #pragma unroll
           for (int x = 0; x < 16 / kRowsAtOnce; ++x)
@@ -496,9 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
                   widen4<FMT>(wd[2 * k], o[0], o[1]);
                   widen4<FMT>(wd[2 * k + 1], o[2], o[3]);
                 }
-                if (tail) {
-                  if (alive <= x * kRowsAtOnce) o[0] = o[1] = o[2] = o[3] = 0u;
-                }
                 sts128((out ^ (k << 4)) + x * kRowsAtOnce * 128 + (b ? second : 0u), o[0], o[1], o[2], o[3]);
               }
             }
@@ -522,6 +516,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_wide_kernel(const 
           if (odd) vw = usable_scale<FMT>(vw, factor);
           if constexpr (G::kU4) {  // without a zero-point a token is not a number: its factor here, its score below
             if (odd_zero(vw)) odd = true, factor = __uint_as_float(0x7fc00000u);
+          }
+          if constexpr (FMT == QLIN_KV_E4M3) {  // among the values of nodes, or behind the end
+            if (j0 + part * 16 + lane >= w.s.ctx) {
+              bool nan_codes = false;
+#pragma unroll 1
+              for (int x = 0; x < G::kRowBytes; x += 16) nan_codes |= clear_nan_codes(raw + G::kRawCode + token * G::kRowBytes + x);
+              if (nan_codes) odd = true, factor = __uint_as_float(0x7fc00000u);
+            }
           }
           if (odd && j0 + part * 16 + lane < len) odd_tile[t % kCols] = t + 1;
           float sk, sv;

@@ -294,3 +294,28 @@ def test_bad_pages_read_as_zeros(qlin_gpu, fmt, d, nodes, page):
                 assert torch.equal(out[:nodes], first[:nodes])
                 for x, y in zip(p.t, p.codes_dev):
                     x.copy_(torch.from_numpy(y.copy()))
+
+
+@pytest.mark.parametrize("d,nodes", SIZES)
+@pytest.mark.parametrize("code", [0x7f, 0xff])
+def test_codes_that_nobody_sees(qlin_gpu, d, nodes, code):
+    """E4M3 codes that are NaN (never written by the library) behind a sequence's end and in a node that no row sees:
+    the same bits.  A row that sees such a node is not a number."""
+    p = Problem(qlin_gpu, [(45, nodes), (10, 2)], 8, 2, d, 16, "e4m3", torch.float16, "tree", nodes)
+    if nodes > 1:
+        _hide(p, 1)
+    gone = ~_live(p) | (_place(p, 0, 46) if nodes > 1 else False)
+    clean, lse = (x.clone() for x in p.run())
+    p.check()
+    for i in range(2):
+        p.t[i][gone[:, None, :].expand(p.t[i].shape[:3]).cuda()] = code
+    out, l2 = p.run()
+    p.check()
+    assert torch.equal(out, clean) and torch.equal(l2, lse)
+    page, off = int(p.table[0, 45 // 16]), 45 % 16
+    p.t[1][page, 0, off, d - 1] = code              # one code of node 0, of the first key head
+    out, l2 = p.run()
+    hit = torch.from_numpy(p.bits[:, 0].copy())
+    hit[nodes:] = False
+    assert torch.isnan(out[hit][:, :4, d - 1]).all() and torch.equal(out[~hit], clean[~hit]) and torch.equal(out[:, 4:], clean[:, 4:])
+    assert torch.equal(l2, lse)
