@@ -319,3 +319,131 @@ def test_codes_that_nobody_sees(qlin_gpu, d, nodes, code):
     hit[nodes:] = False
     assert torch.isnan(out[hit][:, :4, d - 1]).all() and torch.equal(out[~hit], clean[~hit]) and torch.equal(out[:, 4:], clean[:, 4:])
     assert torch.equal(l2, lse)
+
+
+# What the tests of test_gpu_tree_attention reach through one kernel only, through both.
+BOTH = pytest.mark.parametrize("nodes", [3, 9])
+
+
+@BOTH
+def test_a_query_that_is_not_a_number(qlin_gpu, nodes):
+    p = Problem(qlin_gpu, [(45, nodes)], 8, 2, 128, 16, "e4m3", torch.float16, "tree", 4)
+    clean = p.run()[0].clone()
+    for word in (float("nan"), float("inf")):
+        x = p.q.clone()
+        x[1, 5, 77] = word
+        out, lse = p.run(x.cuda())
+        same = torch.ones(nodes, 8, dtype=torch.bool)
+        same[1, 5] = False
+        assert torch.equal(out[same], clean[same]) and torch.isnan(out[1, 5]).all()
+        assert torch.isnan(lse[1, 5]) and torch.isfinite(lse[same]).all()
+
+
+@BOTH
+@pytest.mark.parametrize("d,fmt", [(64, "u4"), (128, "int8"), (128, "e4m3")])
+def test_queries_far_below_one(qlin_gpu, nodes, d, fmt):
+    p = Problem(qlin_gpu, [(200, nodes)], 8, 2, d, 32, fmt, torch.bfloat16, "tree", 4)
+    for i, by in enumerate((2.0 ** -40, 2.0 ** -130, 2.0 ** -20, 0.0, 2.0 ** -8)[:nodes]):
+        p.q[i] *= by
+    p.run()
+    p.check()
+
+
+@BOTH
+def test_strides_and_another_stream(qlin_gpu, nodes):
+    p = Problem(qlin_gpu, [(900, nodes), (30, nodes - 1), (2000, 1)], 8, 2, 128, 64, "e4m3", torch.float16, "tree", 6)
+    first = p.run()[0].clone()
+    p.check()
+    n = p.q.shape[0]
+    joint = torch.randn(n, 14, 128, device="cuda").half()
+    joint[:, 3:11] = p.q.cuda()
+    out = torch.empty(8, n, 128, dtype=torch.float16, device="cuda").transpose(0, 1)
+    side = torch.cuda.Stream()
+    p.run(joint[:, 3:11], out, side, lse=False)
+    assert torch.equal(out, first)
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        p.call.run(side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+
+
+@BOTH
+def test_replay_with_other_lengths(qlin_gpu, nodes):
+    """A captured call replayed while lengths, pages, masks and queries change on the device."""
+    q = qlin_gpu
+    a = Problem(q, [(100, nodes), (900, nodes), (0, nodes)], 8, 2, 128, 16, "u4", torch.float16, "tree", 6)
+    b = Problem(q, [(1301, nodes), (3, 1), (0, 0)], 8, 2, 128, 16, "u4", torch.float16, "random", 7, max_nodes=nodes)
+    tq, pages = 3 * nodes, max(a.t[0].shape[0], b.t[0].shape[0])
+    table = torch.full((3, max(a.table.shape[1], b.table.shape[1])), -1, dtype=torch.int32, device="cuda")
+    x, mask = torch.zeros(tq, 8, 128, dtype=torch.float16, device="cuda"), torch.zeros(tq, 1, dtype=torch.int64, device="cuda")
+    indptr, ctx = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    ten = [torch.zeros(pages, *t.shape[1:], dtype=t.dtype, device="cuda") for t in a.t]
+    cache = q.qlin_kv_cache(*ten, q.QLIN_KV_U4)
+    out, lse = torch.empty_like(x), torch.empty(tq, 8, device="cuda")
+    ws = torch.empty(q.qlin_tree_attention_workspace_bytes(cache, 8, nodes, 3), dtype=torch.uint8, device="cuda")
+    call = q.qlin_tree_attention_prepare(x, cache, table, indptr, ctx, mask, out, ws, nodes, lse=lse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call.run()
+    for p in (a, b, a):
+        n = p.q.shape[0]
+        table[:, :p.table.shape[1]] = p.table.cuda()
+        x[:n], mask[:n] = p.q.cuda(), p.mask
+        indptr.copy_(p.indptr)
+        ctx.copy_(p.ctx)
+        for to, y in zip(ten, p.t):
+            to[:y.shape[0]] = y
+        graph.replay()
+        torch.cuda.synchronize()
+        p.out, p.lse = out[:n].clone(), lse[:n].clone()
+        p.check()
+
+
+@BOTH
+def test_pages_beyond_32_bits(qlin_gpu, nodes):
+    q = qlin_gpu
+    p = Problem(q, [(60, nodes)], 8, 2, 128, 16, "e4m3", torch.float16, "tree", 6, spare=0)
+    pages, gap = p.t[0].shape[0], (1 << 30) + 4096
+    if torch.cuda.mem_get_info()[0] < (2 * pages + 4) * gap:
+        pytest.skip("not enough free memory")
+    near = p.run()[0].clone()
+    p.check()
+    far = []
+    for t in p.t[:2]:
+        buf = torch.empty((pages - 1) * gap + t[0].numel(), dtype=t.dtype, device="cuda")
+        far.append(buf.as_strided(t.shape, (gap, *t.stride()[1:])))
+        far[-1].copy_(t)
+    p.cache = q.qlin_kv_cache(*far, *p.t[2:], q.QLIN_KV_E4M3)
+    out, _ = p.run()
+    p.check()
+    assert torch.equal(out, near)
+
+
+@BOTH
+def test_bounds_that_do_not_fit(qlin_gpu, nodes):
+    """A sequence whose length, rows or nodes are out of range is recorded and left out, its rows as they were."""
+    q = qlin_gpu
+    p = Problem(q, [(100, nodes), (50, nodes), (70, nodes)], 8, 2, 128, 32, "int8", torch.float16, "tree", 6)
+    clean = p.run()[0].clone()
+    p.check()
+    ctx, indptr = p.ctx.clone(), p.indptr.clone()
+    rows = slice(nodes, 2 * nodes)
+    others = torch.ones(3 * nodes, dtype=torch.bool)
+    others[rows] = False
+    for bad in (1 << 20, -1, 0x7fffffff, -(1 << 31)):
+        p.ctx = ctx.clone()
+        p.ctx[1] = bad
+        out, lse = p.run()
+        assert q.qlin_get_device_error() == 0x2000
+        assert torch.equal(out[others], clean[others]) and (out[rows] == 3).all() and (lse[rows] == 3).all()
+    p.ctx = ctx
+    for at, bad in ((3, 3 * nodes + 1), (0, -1), (3, -(1 << 31))):
+        p.indptr = indptr.clone()
+        p.indptr[at] = bad
+        out, _ = p.run()
+        assert q.qlin_get_device_error() == 0x2000
+        assert torch.equal(out[rows], clean[rows])
