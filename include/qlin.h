@@ -796,14 +796,16 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * of a write is left out; the tokens of a page whose number is out of range are
  * zeros, for the read and as keys and values of attention alike; so are rows of
  * the read that no sequence has; a sequence of attention whose bounds are out of
- * range is left out, and its rows of out and lse stay as they were.
+ * range is left out.  Rows of out and lse that belong to no sequence, or to one
+ * left out, stay as they were, and with B = 0 nothing is written.
  *
  * qlin_qk_norm_rope: for every token t and head of q and of k
  *   y = x / sqrt(mean(x^2) + eps) * gamma      (y = x when gamma is NULL)
  *   (a, b) -> (a cos - b sin, b cos + a sin)   with the angle
  *   positions[t] * inv_freq[i] for pair i < rot / 2 (channels from rot on
- *   keep y), in float32 (the angle modulo a full turn exactly, in 64-bit
- *   fixed point), rounded once to dtype.  k (and k_out) may be NULL.  An
+ *   keep y), in float32 (the angle modulo a full turn in 64-bit fixed point:
+ *   within 2^-21 radians below position 2^31 for |inv_freq| <= 1), rounded once
+ *   to dtype.  k (and k_out) may be NULL.  An
  *   output may be its input (same data and strides); other overlaps are not
  *   allowed.
  *
@@ -850,9 +852,13 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * does a zero-point that is none (qlin_kv_cache_read takes any as it is).  The
  * value scales of a row's tokens may lie 2^117 apart (smaller ones than 2^-91
  * counted as that, zeros as 2^-64); beyond, the small one's weight is lost.  Codes
- * enter the products exactly; sums are in float32, and the probabilities are
- * rounded to fp16 before they meet the codes of v.  The result depends on the
- * sequences' lengths and the GPU's number of SMs, not on timing.
+ * enter the products exactly, and so do rows of q, but for elements of a bf16 row
+ * below 2^-13 of its largest, which lose bits, and all below 2^-21; sums are in
+ * float32.  The probabilities, times their value scales, are rounded to 11 bits
+ * before they meet the codes of v, and lose bits below 2^-42 of a row's largest:
+ * an element of out to which only such tokens contribute is not exact.  The
+ * result depends on the sequences' lengths and the GPU's number of SMs, not on
+ * timing.
  *   q, out      [Tq][Hq][D] of dtype; Hq a multiple of the cache's heads
  *   mask        int64 [Tq][mask_words], mask_words = ceil(max_nodes / 64), or NULL
  *   lse         out, float32 [Tq][Hq], or NULL

@@ -15,18 +15,24 @@
 // turns is kept as a 64-bit fraction (worked out once per block in float64);
 // position x fraction modulo 2^64 is then one integer product that drops the
 // whole turns exactly, and what is left converts to a float in [-1/2, 1/2)
-// for sincospif.  An angle of any position below 2^31 is off by less than
-// 2^-21 radians, without a float64 operation per angle (float64 runs at a
-// small fraction of the float32 rate here).
+// for sincospif.  The product is exact, the fraction within 2^-52 of its
+// frequency, so an angle of any position below 2^31 is off by less than 2^-21
+// radians for |inv_freq| <= 1 (and by |inv_freq| times that above), without a
+// float64 operation per angle (float64 runs at a small fraction of the float32
+// rate here).
 //
 // The mean of squares, the norm, the rotation and the scales are float32; a
 // row is rounded once, to its 16-bit output or to its codes.  Integer codes
 // are rounded by adding 1.5 x 2^23 (nearest even, the code in the low bits),
 // which is the float-to-integer conversion at the rate of an addition.
 // Bound: below about a thousand tokens a launch's latency (64 tokens x 48 heads
-// into the cache: 7.5 us); above, HBM and the issue slots together: 8192 tokens x
-// 40 heads of 128 rotated in 39.3 us (4270 GB/s), 6835 x 96 rotated and quantized
-// in 87.4 us (3310 GB/s, about 64 % of the issue slots).
+// into the cache: 4.3 us).  Above, the latency of the rows' loads: neither HBM (half
+// to two thirds of the copy rate) nor the issue slots (56 % rotating, 64 to 70 %
+// quantizing) are full, but the loads ahead begin anew with q, k and v and with
+// every token, whose first row and place are waited for.  8192 tokens x 40 heads of
+// 128 rotated: 40.3 us (4170 GB/s); 5028 x 96, 64 channels of each turned, into the
+// cache: 67 us INT8 (3080 GB/s), 68 E4M3, 78 U4 (2400); k and v of 8192 tokens x 16
+// heads as they are: 16.3 us INT8, 17.6 E4M3, 20.7 U4, part of it in L2.
 #include <algorithm>
 #include <cmath>
 
@@ -40,7 +46,8 @@ constexpr int kThreads = 256;
 // Rows a group takes at once, and blocks that share an SM.  Rotation alone does little per row, so two rows at once and
 // 80 registers; quantizing fills a warp's issue slots by itself, and the shorter code and a fourth block count for
 // more.  Rotation of 8192 tokens x 40 heads of 128: 39.3 us at two rows and three blocks, 45.5 at one and four.
-// Appending 6835 tokens x 96 heads: 92.5 and 90.4 us; 64 tokens x 48 heads: 8.5 and 7.1 us.
+// Appending 5028 tokens x 96 heads, the read of them behind it: 92.5 and 90.4 us; 64 tokens x 48 heads: 8.5 and 7.1 us
+// (a sweep before the quantizer's last step, graph replays).
 __host__ __device__ constexpr int unroll_of(int fmt) { return fmt < 0 ? 2 : 1; }
 __host__ __device__ constexpr int blocks_of(int fmt) { return fmt < 0 ? 3 : 4; }
 constexpr int kFlat = 2;  // rows a group of the plain write takes at once

@@ -10,12 +10,13 @@
 // in tree_common.cuh), so the codes go to the tensor cores as they are and
 // neither product rounds an operand except the probabilities 2^(t - m) (to
 // fp16).  q rows are scaled by a power of two to below 2^15 before they become
-// fp16: exact for fp16, and for bf16 down to 2^-39 of the row's largest.  The
+// fp16: exact for fp16, and for bf16 down to 2^-31 of the row's largest (smaller
+// elements in steps of 2^-39 of it).  The
 // reference m_i follows the running maximum of t lazily: it moves when t
 // exceeds it by more than 2, and the exponent carries an offset of 13, so that
 // the probabilities lie below 2^15 and those down to 2^-27 of the reference are
 // normal fp16 numbers.  Smaller ones matter where the large ones meet codes of
-// 0: when 16 x 16 of them hold any, these go through a second product, times
+// 0: when a unit of 16 x 32 holds any, these go through a second product, times
 // 2^24 against codes times 2^-24 (2^15 for E4M3), both exact in fp16, so that
 // every probability keeps 11 bits down to 2^-51 (2^-42) of the largest.
 //
@@ -41,11 +42,15 @@
 // is permuted such that a lane's operands are contiguous bytes of a row, read
 // without bank conflicts through the swizzle.
 //
-// Bound: up to eight rows per key head, HBM and the latency of the loads: 64
-// ragged sequences of up to 8191 tokens, 8 key heads of 128, E4M3, one node of 32
-// query heads each: 149 us, 4300 GB/s (one copy would take 96 us).  At 16 rows the
-// widening instructions take as long as the loads.  One sequence of 500 tokens,
-// 32 heads: 11 us, two launches' latency.
+// Bound: up to eight rows per key head no unit is full (issue slots 38 %, HBM 5.1
+// TB/s over equal lengths): a unit is one chain of about 700 instructions, ten
+// compute and two loading warps share an SM at 168 registers, and shorter code in
+// either has given a few percent each time.  64 ragged sequences of
+// up to 8191 tokens, 8 key heads of 128, E4M3, one node of 32 query heads each:
+// 141 us, 4540 GB/s (one copy would take 96 us); INT8 152, U4 189 (twice the
+// widening for half the bytes); heads of 256, as many bytes, 163.  Twelve of the 16
+// operand rows are padding there.  At 16 rows the widening takes as long as the loads.
+// One sequence of 500 tokens, 32 heads: 11 us, two launches' latency.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -76,7 +81,7 @@ struct Geo {
   static constexpr int kKLane = kW / 4;                     // bytes of a row a lane takes for q . k
   static constexpr int kVLane = kW / 8;                     // and for p . v
   static constexpr int kNPerSub = kPerSub / 8;              // output tiles of a column block
-  // 168 registers a thread (D = 128) let 12 warps live on an SM, 128 (D = 64) 16, 255 (D = 256) 8
+  // 168 registers a thread (D = 128) let 12 warps live on an SM (ten compute), 128 (D = 64) 16 (14), 255 (D = 256) 8 (6 or 7)
   static constexpr int kBlocksPerSm = D == 256 ? 1 : 2;
   // (six stages of rows of 256 bytes fit beside the merge area: no more than six warps may take turns at them)
   static constexpr int kStages = kRowBytes >= 256 ? 6 : kRowBytes == 128 ? 8 : kRowBytes == 64 ? 12 : 16;

@@ -293,8 +293,8 @@ __device__ __forceinline__ void copy_scales(const Params& p, int head, int first
 // of copy_scales, and row_at(r, c) says where 16-byte chunk c of row r lies (its swizzle repeats after eight rows).  The
 // rows of a box are contiguous in its page, so a lane's chunks are 512 bytes apart and everything but the page's address
 // is known beforehand: the copies of a stage take the warp few instructions (with the box a variable and four copies at
-// once, a decode batch took 163 us instead of 149).  Plain asynchronous copies: with tensor-map copies of these
-// boxes, at the same speed, calls failed when other memory was mapped while they ran.
+// once, a decode batch took 163 us instead of 149).  A thread's copies arrive in order, which the turns at the ring rest on
+// (stage_ring.h); boxes copied through tensor maps, at the same speed, arrive in any.
 template <int TOKENS, int BOX, int ROW_BYTES, class RowAt>
 __device__ __forceinline__ void copy_codes(const Params& p, int head, int first, int32_t ahead, int at, uint32_t k_to,
                                            uint32_t v_to, uint64_t policy, RowAt row_at) {

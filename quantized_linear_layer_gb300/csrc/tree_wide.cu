@@ -30,10 +30,12 @@
 // for about 2900 of them: 768 to 1024 for the products' operands, 1000 for the
 // codes in and out of their widening, 900 for the tokens' scales, which every
 // warp of rows reads; issue slots take 2600 of each scheduler's, products 1024 to
-// 1536, exponentials 1024.  One tree of 26 nodes (104 rows a key head) over 131000 tokens, U4: 140
-// us; 16 sequences x 64 nodes x 64 query heads over up to 8192 tokens, INT8: 340
-// us, 411 TFLOP/s; 32 sequences x 16 nodes over up to 32768, E4M3: 492 us, 2350
-// GB/s.
+// 1536, exponentials 1024.  One tree of 26 nodes (104 rows a key head) over 131001
+// tokens, U4: 139 us; 16 sequences of 33 to 64 nodes (782 in all) x 64 query heads
+// over up to 8192 tokens, INT8: 344 us, 407 TFLOP/s; 32 sequences of 8 to 16 nodes
+// (407) over up to 32768, E4M3: 500 us, 2310 GB/s.  Prompt chunks, 8 sequences of 256
+// nodes x 32 query heads, INT8: 71 us behind no token, 302 behind 4096 (483
+// TFLOP/s), 958 behind 16384 (582).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
