@@ -102,7 +102,8 @@ int turns(int stages, int takers, int late, milliseconds delay) {
     readers.emplace_back([&, w] {
       for (int u = w; u < fills && !wrong; u += takers) {
         const int s = u % stages;
-        full[s].wait((u / stages) & 1, milliseconds(500));
+        for (int tries = 0; tries < 1000 && !wrong && !full[s].wait((u / stages) & 1, milliseconds(20)); ++tries) {
+        }
         if (data[s] != u) wrong = true;
         free[s].arrive();
       }

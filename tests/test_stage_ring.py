@@ -44,5 +44,5 @@ def test_taking_turns(program, stages, takers, late):
 
 def test_more_readers_than_stages(program):
     """Seven readers at six stages: one is a whole round ahead when a copy is late, which the kernels' geometry excludes."""
-    r = subprocess.run([program, "turns", "6", "7", "1", "40"], timeout=60)
+    r = subprocess.run([program, "turns", "6", "7", "1", "300"], timeout=60)
     assert r.returncode == 1
