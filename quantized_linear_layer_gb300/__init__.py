@@ -719,8 +719,8 @@ class qlin_kv_cache:
 
     k, v: [pages][heads][page_size][head_dim] int8 (INT8), float8_e4m3fn or uint8 (E4M3), or
     [..][head_dim / 2] uint8 (U4); k_scale, v_scale: float32 [pages][heads][page_size], or for U4
-    float16 [pages][heads][page_size][2] (scale, zero-point).  Each page is contiguous; the pages of k and
-    v may be any (equal) distance apart, and so may those of the scales."""
+    float16 [pages][heads][page_size][2] (scale, zero-point: a whole number from 0 to 15).  Each page is
+    contiguous; the pages of k and v may be any (equal) distance apart, and so may those of the scales."""
 
     def __init__(self, k, v, k_scale, v_scale, fmt):
         torch = _torch()
