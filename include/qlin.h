@@ -151,6 +151,28 @@ typedef struct {
   int fmt;                    /* qlin_kv_fmt */
 } qlin_kv_cache;
 
+/* The pages of a cache as a serving loop hands them out (all pointers device
+   pointers): which pages each sequence has, and a stack of the free ones.  A
+   page belongs to one sequence at a time. */
+typedef struct {
+  int32_t* block_table;  /* [B][max_pages]: a sequence's pages in the order of its tokens */
+  int64_t max_pages;
+  int32_t* held;         /* [B]: how many it has */
+  int32_t* free_pages;   /* [pages]: free_pages[0 .. *free_count - 1] are free, the last one goes first */
+  int32_t* free_count;   /* [1] */
+  int64_t pages;
+  int64_t page_size;     /* as in qlin_kv_cache */
+} qlin_kv_pages;
+
+/* The scores of qlin_chunk_attention. */
+typedef struct {
+  float scale;
+  float softcap;               /* c > 0: a score s becomes c tanh(s / c); 0: it stays */
+  const float* slopes;         /* [Hq] (device) or NULL: minus slopes[h] |position of the row - token| */
+  int64_t window;              /* w > 0: of the tokens up to its own a row sees the last w; 0: all */
+  const int32_t* prefix_lens;  /* [B] (device) or NULL: the sequence's first tokens, seen by all of its rows */
+} qlin_scores;
+
 /* A checked call of one of the entry points below that have a _prepare form,
    kept by the caller in host memory: qlin_call_run makes the call as often as
    wanted.  It holds the device pointers and sizes it was given (and a plan of
@@ -866,6 +888,81 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  *   workspace   qlin_tree_attention_workspace_bytes(...) bytes, 256-byte
  *               aligned, contents arbitrary; one call at a time may use it
  *
+ * qlin_kv_pages_assign: a step of B sequences, sequence b with ctx_lens[b] tokens
+ * in the cache and new_lens[b] new ones, in at most T rows.  A sequence needs
+ * ceil((ctx_lens[b] + new_lens[b]) / page_size) pages: what it has beyond them goes
+ * back to the stack (lengths of 0: all of them), the last sequence's last page
+ * first; then what it lacks comes from the stack, in the order of the sequences.
+ * A sequence that needs pages is served while those that it and the ones before
+ * it ask for are there, and one that has new tokens while theirs and those before
+ * fit into T; one that is not served keeps the pages it has, gets no rows, and is
+ * asked for again in a later step.  So giving the same lengths twice changes
+ * nothing, and giving new_lens of 0 takes a step back.
+ *   q_indptr   out, int32 [B + 1]: the rows of sequence b are q_indptr[b] ..
+ *              q_indptr[b + 1] - 1, as attention takes them
+ *   positions  out, int64 [T]: ctx_lens[b] + i for row q_indptr[b] + i, or
+ *              ctx_lens[b] + depths[row] where depths (int32 [T]) is given (a
+ *              tree's nodes); 0 for rows behind the last sequence's
+ *   slots      out, int64 [T]: where the row's k and v go (page * page_size +
+ *              offset); -1 for rows behind the last sequence's (the cache write
+ *              leaves them out)
+ * Lengths, page counts or a stack that are out of range are recorded in the
+ * device error word; such a sequence stays as it is and gets no rows.
+ *
+ * qlin_chunk_attention: sequence b has ctx_lens[b] tokens in the cache and, at
+ * places ctx_lens[b] + i, its new ones i < q_indptr[b + 1] - q_indptr[b] <=
+ * max_new, whose queries are the rows q_indptr[b] + i of q: a prompt's chunk, of any
+ * length from one token on.  Row i has the position t = ctx_lens[b] + i and sees
+ * token j when j < prefix_lens[b] (taken between 0 and the sequence's length), or
+ * j <= t and, with a window w, t - j < w.  Heads, out and lse as for
+ * qlin_tree_attention, with the scores
+ *   s_ij = scale (q_i . k_j), then c tanh(s_ij / c) with a softcap c, then minus
+ *   slopes[h] |t - j| with slopes
+ *   q, out      [Tq][Hq][D] of dtype; Hq a multiple of the cache's heads
+ *   lse         out, float32 [Tq][Hq], or NULL
+ *   max_new     1 .. 2^31 - 1, a bound that the call is planned for
+ *   workspace   qlin_chunk_attention_workspace_bytes(...) bytes, 256-byte
+ *               aligned, contents arbitrary; one call at a time may use it
+ *
+ * qlin_verify_drafts: which of the drafted tokens of each sequence stay, and the
+ * token after them.  Node i of sequence b is row q_indptr[b] + i, at most
+ * max_nodes (1 .. 256) of them; node 0 is a token that stands already, node i > 0
+ * the draft tokens[row] behind node parents[row] < i of its sequence (parents NULL:
+ * a chain, i - 1).  target and draft hold rows of V (1 .. 2^20) float32 probabilities, the target's and
+ * the draft's for the token behind each node (entries that are no numbers or below
+ * 0 count as 0, above 1 as 1; a row's sum is about 1).  From node 0 on, the
+ * children of the node reached are tried in the order of their rows, p and q being
+ * its rows: after k rejections there, with c_0 = 0, W_0 = 1,
+ *   r_k = max(p - c_k q, 0), W_k = sum r_k, c_{k+1} = c_k + W_k:
+ *   the child with token x is accepted when accept_u[row] W_k q(x) < r_k(x), which
+ *   makes it the node reached.
+ * draft NULL: the drafts were not drawn (a draft's likeliest tokens); a rejected
+ * token's share is taken from p: r_k = p without the rejected tokens, W_{k+1} = W_k -
+ * p(x), accepted when accept_u[row] W_k < r_k(x).  (So what comes out is distributed
+ * as the target's own tokens are, if the children of a node were drawn from its q
+ * independently.)  The next token is drawn from r_k where no child is accepted:
+ * the lowest j with r_k(0) + .. + r_k(j) > sample_u[b] sum r_k; from p where r_k
+ * is all 0.  Sums are exact, of r_k in steps of 2^-52.
+ *   target, draft  float32 [Tq] rows of V, target_stride / draft_stride elements apart
+ *   parents        int32 [Tq] or NULL;  tokens int64 [Tq]
+ *   accept_u       float32 [Tq], sample_u float32 [B], from [0, 1)
+ *   path           out, int32 [B][max_nodes]: the nodes from 0 on, -1 behind them
+ *   count          out, int32 [B]: how many; 0 for a sequence without nodes
+ *   next_token     out, int64 [B]; -1 for a sequence without nodes or whose row
+ *                  has no weight at all
+ * A node whose parent or token is out of range is not accepted, and recorded in
+ * the device error word.
+ *
+ * qlin_kv_cache_keep: token ctx_lens[b] + path[b][i] of sequence b becomes token
+ * ctx_lens[b] + i, for i < count[b], codes and scales of all heads as they are: what a
+ * verified tree keeps closes the gaps that the others leave.  path[b] ascends and
+ * does not begin below 0; other paths are recorded in the device error word and
+ * their sequences left as they are, as are tokens on a page that is out of range.
+ * (Keys keep the rotation they were written with: a node's position is that of its
+ * depth.)
+ *   path   int32 [B][max_path], count int32 [B], as qlin_verify_drafts gives them
+ *   lens   out, int32 [B]: ctx_lens[b] + count[b], or NULL; not ctx_lens itself
+ *
  * Each call has a _prepare form with the same arguments, which checks them
  * and plans the launches into *call (host memory) without launching anything;
  * qlin_call_run(call, stream) then launches, for decode loops whose buffers
@@ -894,6 +991,25 @@ qlin_status qlin_tree_attention(const qlin_heads* q, const qlin_heads* out, qlin
                                 int64_t mask_words, int64_t max_nodes, float scale, float* lse, void* workspace,
                                 int64_t workspace_bytes, cudaStream_t stream);
 
+qlin_status qlin_kv_pages_assign(const qlin_kv_pages* pages, const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,
+                                 int64_t T, const int32_t* depths, int32_t* q_indptr, int64_t* positions, int64_t* slots,
+                                 cudaStream_t stream);
+/* -1 when an argument is out of range. */
+int64_t qlin_chunk_attention_workspace_bytes(const qlin_kv_cache* cache, int64_t Hq, int64_t max_new, int64_t B);
+qlin_status qlin_chunk_attention(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
+                                 const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                 const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B, int64_t max_new,
+                                 const qlin_scores* scores, float* lse, void* workspace, int64_t workspace_bytes,
+                                 cudaStream_t stream);
+qlin_status qlin_verify_drafts(const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                               int64_t V, int64_t Tq, const int32_t* parents, const int64_t* tokens,
+                               const int32_t* q_indptr, int64_t B, int64_t max_nodes, const float* accept_u,
+                               const float* sample_u, int32_t* path, int32_t* count, int64_t* next_token,
+                               cudaStream_t stream);
+qlin_status qlin_kv_cache_keep(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                               const int32_t* ctx_lens, const int32_t* path, const int32_t* count, int64_t B,
+                               int64_t max_path, int32_t* lens, cudaStream_t stream);
+
 qlin_status qlin_qk_norm_rope_prepare(const qlin_heads* q, const qlin_heads* k, const qlin_heads* q_out,
                                       const qlin_heads* k_out, qlin_dtype dtype, int64_t T, int64_t D,
                                       const qlin_rope* rope, qlin_call* call);
@@ -912,6 +1028,22 @@ qlin_status qlin_tree_attention_prepare(const qlin_heads* q, const qlin_heads* o
                                         const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B,
                                         const int64_t* mask, int64_t mask_words, int64_t max_nodes, float scale,
                                         float* lse, void* workspace, int64_t workspace_bytes, qlin_call* call);
+qlin_status qlin_kv_pages_assign_prepare(const qlin_kv_pages* pages, const int32_t* ctx_lens, const int32_t* new_lens,
+                                         int64_t B, int64_t T, const int32_t* depths, int32_t* q_indptr,
+                                         int64_t* positions, int64_t* slots, qlin_call* call);
+qlin_status qlin_chunk_attention_prepare(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
+                                         const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                         const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B, int64_t max_new,
+                                         const qlin_scores* scores, float* lse, void* workspace,
+                                         int64_t workspace_bytes, qlin_call* call);
+qlin_status qlin_verify_drafts_prepare(const float* target, int64_t target_stride, const float* draft,
+                                       int64_t draft_stride, int64_t V, int64_t Tq, const int32_t* parents,
+                                       const int64_t* tokens, const int32_t* q_indptr, int64_t B, int64_t max_nodes,
+                                       const float* accept_u, const float* sample_u, int32_t* path, int32_t* count,
+                                       int64_t* next_token, qlin_call* call);
+qlin_status qlin_kv_cache_keep_prepare(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                       const int32_t* ctx_lens, const int32_t* path, const int32_t* count, int64_t B,
+                                       int64_t max_path, int32_t* lens, qlin_call* call);
 qlin_status qlin_call_run(const qlin_call* call, cudaStream_t stream);
 
 #ifdef __cplusplus

@@ -35,6 +35,9 @@ __all__ = [
     "qlin_qk_norm_rope", "qlin_qk_norm_rope_prepare", "qlin_qk_norm_rope_cache", "qlin_qk_norm_rope_cache_prepare",
     "qlin_kv_cache_write", "qlin_kv_cache_write_prepare", "qlin_kv_cache_read", "qlin_kv_cache_read_prepare",
     "qlin_tree_attention_workspace_bytes", "qlin_tree_attention", "qlin_tree_attention_prepare",
+    "qlin_kv_pages", "qlin_kv_pages_assign", "qlin_kv_pages_assign_prepare",
+    "qlin_chunk_attention_workspace_bytes", "qlin_chunk_attention", "qlin_chunk_attention_prepare",
+    "qlin_verify_drafts", "qlin_verify_drafts_prepare", "qlin_kv_cache_keep", "qlin_kv_cache_keep_prepare",
 ]
 
 QLIN_F16, QLIN_BF16, QLIN_F32, QLIN_I32 = 0, 1, 2, 3
@@ -111,6 +114,15 @@ _SIGS = {
                              _I64, _P], _I32),
     "qlin_tree_attention_prepare": ([_P, _P, _I32, _I64, _P, _P, _I64, _P, _P, _I64, _P, _I64, _I64, ctypes.c_float, _P,
                                      _P, _I64, _P], _I32),
+    "qlin_kv_pages_assign": ([_P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P], _I32),
+    "qlin_kv_pages_assign_prepare": ([_P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P], _I32),
+    "qlin_chunk_attention_workspace_bytes": ([_P, _I64, _I64, _I64], _I64),
+    "qlin_chunk_attention": ([_P, _P, _I32, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P, _I64, _P], _I32),
+    "qlin_chunk_attention_prepare": ([_P, _P, _I32, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P, _I64, _P], _I32),
+    "qlin_verify_drafts": ([_P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P], _I32),
+    "qlin_verify_drafts_prepare": ([_P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P], _I32),
+    "qlin_kv_cache_keep": ([_P, _P, _I64, _P, _P, _P, _I64, _I64, _P, _P], _I32),
+    "qlin_kv_cache_keep_prepare": ([_P, _P, _I64, _P, _P, _P, _I64, _I64, _P, _P], _I32),
     "qlin_call_run": ([_P, _P], _I32),
 }
 
@@ -936,3 +948,172 @@ def qlin_tree_attention(q, cache, block_table, q_indptr, ctx_lens, mask, out, wo
     a chain); scale defaults to D ** -0.5; lse float32 [Tq][Hq] (optional) gets ln sum exp of the scores."""
     qlin_tree_attention_prepare(q, cache, block_table, q_indptr, ctx_lens, mask, out, workspace, max_nodes, scale,
                                 lse).run(stream)
+
+
+# ---- a serving step: pages and slots, chunk attention, verified drafts -------
+
+
+class _KvPages(ctypes.Structure):
+    """The C struct qlin_kv_pages."""
+    _fields_ = [("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int64), ("held", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64)]
+
+
+class _Scores(ctypes.Structure):
+    """The C struct qlin_scores."""
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("window", ctypes.c_int64), ("prefix_lens", ctypes.c_void_p)]
+
+
+class qlin_kv_pages:
+    """Which pages of a cache the sequences have, and which are free (the C struct of the same name), over
+    caller-allocated int32 tensors that qlin_kv_pages_assign keeps: block_table [B][max_pages], held [B] (pages of
+    each sequence), free_pages [pages] of which the first free_count [1] are free.  A new pool: held 0,
+    free_pages arange(pages), free_count pages."""
+
+    def __init__(self, block_table, held, free_pages, free_count, page_size):
+        torch = _torch()
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B][max_pages]")
+        _need(block_table, torch.int32, name="block_table")
+        self.device, self.seqs = block_table.device, block_table.shape[0]
+        _vector(held, torch.int32, "held", self.seqs, self.device)
+        _vector(free_pages, torch.int32, "free_pages", device=self.device)
+        _vector(free_count, torch.int32, "free_count", 1, self.device)
+        self._keep = (block_table, held, free_pages, free_count)
+        self._c = _KvPages(block_table.data_ptr(), block_table.shape[1], held.data_ptr(), free_pages.data_ptr(),
+                           free_count.data_ptr(), free_pages.numel(), page_size)
+
+
+def qlin_kv_pages_assign_prepare(pages, ctx_lens, new_lens, q_indptr, positions, slots, depths=None):
+    """qlin_kv_pages_assign's arguments checked and its launches planned once (QlinCall.run)."""
+    torch = _torch()
+    b, t, dev = pages.seqs, slots.numel(), pages.device
+    cp = _vector(ctx_lens, torch.int32, "ctx_lens", b, dev)
+    np_ = _vector(new_lens, torch.int32, "new_lens", b, dev)
+    ip = _vector(q_indptr, torch.int32, "q_indptr", b + 1, dev)
+    pp = _vector(positions, torch.int64, "positions", t, dev)
+    sp = _vector(slots, torch.int64, "slots", t, dev)
+    dp = _vector(depths, torch.int32, "depths", t, dev) if depths is not None else None
+    return QlinCall("qlin_kv_pages_assign", (_ref(pages._c), cp, np_, b, t, dp, ip, pp, sp),
+                    (pages, ctx_lens, new_lens, q_indptr, positions, slots, depths), dev)
+
+
+def qlin_kv_pages_assign(pages, ctx_lens, new_lens, q_indptr, positions, slots, depths=None, stream=None):
+    """A step's pages, row bounds, positions and slots from the sequences' lengths (int32 [B]): pages that are no longer
+    needed go back, lacking ones are taken, and q_indptr int32 [B + 1], positions and slots int64 [T] are written, in place.
+    depths int32 [T]: positions are ctx_lens + depths (a tree's nodes).  Sequences that pages or rows run out for get no rows."""
+    qlin_kv_pages_assign_prepare(pages, ctx_lens, new_lens, q_indptr, positions, slots, depths).run(stream)
+
+
+def qlin_chunk_attention_workspace_bytes(cache, heads, max_new, seqs):
+    """Workspace of qlin_chunk_attention for `heads` query heads, at most max_new new tokens per sequence, `seqs` sequences."""
+    n = lib().qlin_chunk_attention_workspace_bytes(_ref(cache._c), heads, max_new, seqs)
+    if n < 0:
+        raise ValueError("no chunk attention for %d heads over %d, %d new tokens, %d sequences" % (heads, cache.heads, max_new, seqs))
+    return n
+
+
+def qlin_chunk_attention_prepare(q, cache, block_table, q_indptr, ctx_lens, out, workspace, max_new, scale=None, softcap=0.0,
+                                 slopes=None, window=0, prefix_lens=None, lse=None):
+    """qlin_chunk_attention's arguments checked and its launches planned once (QlinCall.run)."""
+    torch = _torch()
+    dtype, code = _half_dtype(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [Tq][heads][D]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B][max_pages]")
+    tq, hq, d = q.shape
+    b, max_pages = block_table.shape
+    parts = [_heads(x, dtype, cache.head_dim, n, tq, cache.device) for n, x in (("q", q), ("out", out))]
+    tp = _vector(block_table, torch.int32, "block_table", device=cache.device)
+    ip = _vector(q_indptr, torch.int32, "q_indptr", b + 1, cache.device)
+    cp = _vector(ctx_lens, torch.int32, "ctx_lens", b, cache.device)
+    for name, t, kind, n in (("slopes", slopes, torch.float32, hq), ("prefix_lens", prefix_lens, torch.int32, b)):
+        if t is not None:
+            _vector(t, kind, name, n, cache.device)
+    scores = _Scores(d ** -0.5 if scale is None else scale, softcap, None if slopes is None else slopes.data_ptr(), window,
+                     None if prefix_lens is None else prefix_lens.data_ptr())
+    lp = _vector(lse, torch.float32, "lse", tq * hq, cache.device) if lse is not None else None
+    wp = _vector(workspace, torch.uint8, "workspace", device=cache.device)
+    return QlinCall("qlin_chunk_attention",
+                    (*map(_ref, parts), code, tq, _ref(cache._c), tp, max_pages, ip, cp, b, max_new, _ref(scores), lp, wp,
+                     workspace.numel()),
+                    (parts, scores, q, cache, block_table, q_indptr, ctx_lens, out, workspace, slopes, prefix_lens, lse), cache.device)
+
+
+def qlin_chunk_attention(q, cache, block_table, q_indptr, ctx_lens, out, workspace, max_new, scale=None, softcap=0.0,
+                         slopes=None, window=0, prefix_lens=None, lse=None, stream=None):
+    """Causal attention of every sequence's new tokens (a prompt's chunk, stored in the cache right behind its cached ones).
+
+    q, out [Tq][Hq][D]; sequence b has ctx_lens[b] cached tokens and the rows q_indptr[b] .. q_indptr[b + 1], at most
+    max_new.  A row sees the tokens up to its own (with a window, the last `window` of them) and the sequence's first
+    prefix_lens[b] (int32 [B]).  Scores are scaled (default D ** -0.5), capped to softcap * tanh(s / softcap), and lessened
+    by slopes[h] (float32 [Hq]) times the distance; lse float32 [Tq][Hq] (optional) gets ln sum exp of them."""
+    qlin_chunk_attention_prepare(q, cache, block_table, q_indptr, ctx_lens, out, workspace, max_new, scale, softcap, slopes,
+                                 window, prefix_lens, lse).run(stream)
+
+
+def _rows_of(t, rows, v, name, device):
+    """The row stride of a [rows][V] float32 tensor whose rows are contiguous."""
+    torch = _torch()
+    _need(t, torch.float32, contiguous=False, name=name)
+    if t.dim() != 2 or tuple(t.shape) != (rows, v):
+        raise ValueError("%s has shape %s, (%d, %d) expected" % (name, tuple(t.shape), rows, v))
+    if v > 1 and t.stride(1) != 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    return t.stride(0) if rows > 1 else v
+
+
+def qlin_verify_drafts_prepare(target, draft, parents, tokens, q_indptr, accept_u, sample_u, path, count, next_token):
+    """qlin_verify_drafts' arguments checked and its launches planned once (QlinCall.run)."""
+    torch = _torch()
+    if target.dim() != 2 or path.dim() != 2:
+        raise ValueError("target must be [Tq][V] and path [B][max_nodes]")
+    (tq, v), (b, nodes), dev = target.shape, path.shape, target.device
+    strides = [_rows_of(t, tq, v, n, dev) if t is not None else 0 for n, t in (("target", target), ("draft", draft))]
+    pp = _vector(parents, torch.int32, "parents", tq, dev) if parents is not None else None
+    tp = _vector(tokens, torch.int64, "tokens", tq, dev)
+    ip = _vector(q_indptr, torch.int32, "q_indptr", b + 1, dev)
+    ap = _vector(accept_u, torch.float32, "accept_u", tq, dev)
+    sp = _vector(sample_u, torch.float32, "sample_u", b, dev)
+    op = _vector(path, torch.int32, "path", b * nodes, dev)
+    cp = _vector(count, torch.int32, "count", b, dev)
+    np_ = _vector(next_token, torch.int64, "next_token", b, dev)
+    return QlinCall("qlin_verify_drafts", (_ptr(target), strides[0], _ptr(draft), strides[1], v, tq, pp, tp, ip, b, nodes, ap, sp,
+                                           op, cp, np_),
+                    (target, draft, parents, tokens, q_indptr, accept_u, sample_u, path, count, next_token), dev)
+
+
+def qlin_verify_drafts(target, draft, parents, tokens, q_indptr, accept_u, sample_u, path, count, next_token, stream=None):
+    """Which drafted tokens stay, and the token after them, from given random numbers.
+
+    target, draft float32 [Tq][V]: the target's and the draft's probabilities behind every node (draft None: the drafts
+    were not drawn); node i of sequence b is row q_indptr[b] + i, its parent parents[row] (int32 [Tq]; None: a chain), its
+    token tokens[row] (int64 [Tq]); accept_u float32 [Tq], sample_u float32 [B] from [0, 1).  path int32 [B][max_nodes] gets
+    the nodes that stay from 0 on (-1 behind them), count int32 [B] how many, next_token int64 [B] the token drawn."""
+    qlin_verify_drafts_prepare(target, draft, parents, tokens, q_indptr, accept_u, sample_u, path, count, next_token).run(stream)
+
+
+def qlin_kv_cache_keep_prepare(cache, block_table, ctx_lens, path, count, lens=None):
+    """qlin_kv_cache_keep's arguments checked and its launches planned once (QlinCall.run)."""
+    torch = _torch()
+    if block_table.dim() != 2 or path.dim() != 2:
+        raise ValueError("block_table must be [B][max_pages] and path [B][max_path]")
+    b, max_pages = block_table.shape
+    tp = _vector(block_table, torch.int32, "block_table", device=cache.device)
+    cp = _vector(ctx_lens, torch.int32, "ctx_lens", b, cache.device)
+    pp = _vector(path, torch.int32, "path", b * path.shape[1], cache.device)
+    np_ = _vector(count, torch.int32, "count", b, cache.device)
+    lp = _vector(lens, torch.int32, "lens", b, cache.device) if lens is not None else None
+    return QlinCall("qlin_kv_cache_keep", (_ref(cache._c), tp, max_pages, cp, pp, np_, b, path.shape[1], lp),
+                    (cache, block_table, ctx_lens, path, count, lens), cache.device)
+
+
+def qlin_kv_cache_keep(cache, block_table, ctx_lens, path, count, lens=None, stream=None):
+    """Token ctx_lens[b] + path[b][i] of every sequence moved to place ctx_lens[b] + i, i < count[b] (path int32
+    [B][max_path], ascending); lens int32 [B] (optional, not ctx_lens) gets ctx_lens + count."""
+    qlin_kv_cache_keep_prepare(cache, block_table, ctx_lens, path, count, lens).run(stream)

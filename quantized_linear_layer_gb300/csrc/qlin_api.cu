@@ -3,6 +3,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -808,6 +809,15 @@ qlin_status check_heads(const char* what, const qlin_heads* a, int64_t T, int64_
 
 bool is_head_dim(int64_t d) { return d == 64 || d == 128 || d == 256; }
 
+bool is_page_size(int64_t n) { return n == 16 || n == 32 || n == 64 || n == 128 || n == 256; }
+
+// (null pointers are)
+bool all_aligned(uintptr_t bytes, std::initializer_list<const void*> pointers) {
+  for (const void* p : pointers)
+    if ((reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0) return false;
+  return true;
+}
+
 qlin_status check_cache(const qlin_kv_cache* c) {
   QLIN_REQUIRE(c != nullptr, QLIN_ERR_INVALID_ARG, "null cache");
   QLIN_REQUIRE(c->fmt >= QLIN_KV_INT8 && c->fmt <= QLIN_KV_U4, QLIN_ERR_INVALID_ARG, "cache: unknown format %d", c->fmt);
@@ -1049,6 +1059,126 @@ qlin_status qlin_tree_attention_prepare(const qlin_heads* q, const qlin_heads* o
   return planned(plan, plan_tree_attention(a, plan), "tree_attention");
 }
 
+qlin_status qlin_kv_pages_assign_prepare(const qlin_kv_pages* pages, const int32_t* ctx_lens, const int32_t* new_lens,
+                                         int64_t B, int64_t T, const int32_t* depths, int32_t* q_indptr,
+                                         int64_t* positions, int64_t* slots, qlin_call* call) {
+  Prepared* plan = nullptr;
+  QLIN_CHECK(begin_call(call, &plan));
+  QLIN_REQUIRE(pages != nullptr, QLIN_ERR_INVALID_ARG, "null pages");
+  QLIN_REQUIRE(B >= 0 && B <= 65535 && T >= 0 && T <= kMaxDim, QLIN_ERR_INVALID_ARG, "bad sizes B=%lld T=%lld", (long long)B,
+               (long long)T);
+  QLIN_REQUIRE(is_page_size(pages->page_size), QLIN_ERR_UNSUPPORTED, "page_size=%lld (16, 32, 64, 128 and 256 are built)",
+               (long long)pages->page_size);
+  QLIN_REQUIRE(pages->pages >= 1 && pages->pages <= kMaxDim && pages->max_pages >= 0 && pages->max_pages <= kMaxDim,
+               QLIN_ERR_INVALID_ARG, "pages=%lld or max_pages=%lld out of range", (long long)pages->pages,
+               (long long)pages->max_pages);
+  QLIN_REQUIRE(B == 0 || (pages->block_table && pages->held && ctx_lens && new_lens), QLIN_ERR_INVALID_ARG, "null pointer");
+  QLIN_REQUIRE(pages->free_pages && pages->free_count && q_indptr && (T == 0 || (positions && slots)), QLIN_ERR_INVALID_ARG,
+               "null pointer");
+  QLIN_REQUIRE(all_aligned(4, {pages->block_table, pages->held, pages->free_pages, pages->free_count, ctx_lens, new_lens, depths,
+                               q_indptr}) && all_aligned(8, {positions, slots}),
+               QLIN_ERR_ALIGNMENT, "int32 arrays must be 4-byte aligned, positions and slots 8-byte");
+  QLIN_DEVICE();
+  return planned(plan, plan_kv_pages_assign(*pages, ctx_lens, new_lens, B, T, depths, q_indptr, positions, slots, plan),
+                 "kv_pages_assign");
+}
+
+int64_t qlin_chunk_attention_workspace_bytes(const qlin_kv_cache* cache, int64_t Hq, int64_t max_new, int64_t B) {
+  if (check_cache(cache) != QLIN_OK) return -1;
+  DeviceInfo* info = nullptr;
+  (void)probe_current_device(&info);  // the number of SMs; without a GPU the default is used
+  if (Hq < 1 || Hq > 65535 || Hq % cache->heads != 0 || max_new < 1 || max_new > kMaxDim || B < 0 || B > 65535) return -1;
+  return chunk_attention_workspace_bytes(*cache, Hq, max_new, B);
+}
+
+qlin_status qlin_chunk_attention_prepare(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
+                                         const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                         const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B, int64_t max_new,
+                                         const qlin_scores* scores, float* lse, void* workspace,
+                                         int64_t workspace_bytes, qlin_call* call) {
+  Prepared* plan = nullptr;
+  QLIN_CHECK(begin_call(call, &plan));
+  QLIN_REQUIRE(is_half_dtype(dtype), QLIN_ERR_INVALID_ARG, "dtype must be F16 or BF16");
+  QLIN_REQUIRE(Tq >= 0 && Tq <= kMaxDim && B >= 0 && B <= 65535, QLIN_ERR_INVALID_ARG, "bad sizes Tq=%lld B=%lld",
+               (long long)Tq, (long long)B);
+  QLIN_REQUIRE(max_pages >= 0 && max_pages <= kMaxDim, QLIN_ERR_INVALID_ARG, "max_pages=%lld out of range",
+               (long long)max_pages);
+  QLIN_REQUIRE(max_new >= 1 && max_new <= kMaxDim, QLIN_ERR_INVALID_ARG, "max_new=%lld out of range", (long long)max_new);
+  QLIN_REQUIRE(scores != nullptr, QLIN_ERR_INVALID_ARG, "null scores");
+  QLIN_REQUIRE(scores->scale - scores->scale == 0.0f, QLIN_ERR_INVALID_ARG, "scale must be finite");
+  QLIN_REQUIRE(scores->softcap == 0.0f || (scores->softcap >= 1e-3f && scores->softcap <= 1e6f), QLIN_ERR_INVALID_ARG,
+               "softcap must be 0 or from 1e-3 to 1e6");
+  QLIN_REQUIRE(scores->window >= 0 && scores->window <= kMaxDim, QLIN_ERR_INVALID_ARG, "window=%lld out of range",
+               (long long)scores->window);
+  QLIN_CHECK(check_cache(cache));
+  QLIN_CHECK(check_heads("q", q, Tq, cache->head_dim));
+  QLIN_CHECK(check_heads("out", out, Tq, cache->head_dim));
+  QLIN_CHECK(check_same_heads("out", out, q->heads));
+  QLIN_REQUIRE(q->heads % cache->heads == 0, QLIN_ERR_INVALID_ARG, "%lld query heads over %lld cached heads",
+               (long long)q->heads, (long long)cache->heads);
+  if (Tq == 0 || B == 0) return empty_call(plan);
+  QLIN_REQUIRE(block_table && q_indptr && ctx_lens && workspace, QLIN_ERR_INVALID_ARG, "null pointer");
+  QLIN_REQUIRE(all_aligned(4, {block_table, q_indptr, ctx_lens, lse, scores->slopes, scores->prefix_lens}), QLIN_ERR_ALIGNMENT,
+               "int32 and float arrays must be 4-byte aligned");
+  QLIN_REQUIRE(all_aligned(256, {workspace}), QLIN_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  QLIN_DEVICE();
+  const int64_t need = chunk_attention_workspace_bytes(*cache, q->heads, max_new, B);
+  QLIN_REQUIRE(workspace_bytes >= need, QLIN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed",
+               (long long)workspace_bytes, (long long)need);
+  const ChunkAttentionArgs a = {*q, *out, dtype, Tq, *cache, block_table, max_pages, q_indptr, ctx_lens, B, max_new,
+                                *scores, lse, workspace};
+  return planned(plan, plan_chunk_attention(a, plan), "chunk_attention");
+}
+
+qlin_status qlin_verify_drafts_prepare(const float* target, int64_t target_stride, const float* draft,
+                                       int64_t draft_stride, int64_t V, int64_t Tq, const int32_t* parents,
+                                       const int64_t* tokens, const int32_t* q_indptr, int64_t B, int64_t max_nodes,
+                                       const float* accept_u, const float* sample_u, int32_t* path, int32_t* count,
+                                       int64_t* next_token, qlin_call* call) {
+  Prepared* plan = nullptr;
+  QLIN_CHECK(begin_call(call, &plan));
+  QLIN_REQUIRE(Tq >= 0 && Tq <= kMaxDim && B >= 0 && B <= 65535, QLIN_ERR_INVALID_ARG, "bad sizes Tq=%lld B=%lld",
+               (long long)Tq, (long long)B);
+  QLIN_REQUIRE(V >= 1 && V <= (int64_t(1) << 20), QLIN_ERR_UNSUPPORTED, "V=%lld (1 .. 2^20 are built)", (long long)V);
+  QLIN_REQUIRE(max_nodes >= 1 && max_nodes <= 256, QLIN_ERR_UNSUPPORTED, "max_nodes=%lld (1 .. 256 are built)",
+               (long long)max_nodes);
+  QLIN_REQUIRE(Tq <= 1 || (target_stride >= V && (draft == nullptr || draft_stride >= V)), QLIN_ERR_INVALID_ARG,
+               "row strides below V=%lld", (long long)V);
+  QLIN_REQUIRE(target_stride >= 0 && target_stride <= (int64_t(1) << 40) && draft_stride >= 0 &&
+                   draft_stride <= (int64_t(1) << 40),
+               QLIN_ERR_INVALID_ARG, "row stride out of range");
+  if (B == 0) return empty_call(plan);
+  QLIN_REQUIRE(q_indptr && sample_u && path && count && next_token && (Tq == 0 || (target && tokens && accept_u)),
+               QLIN_ERR_INVALID_ARG, "null pointer");
+  QLIN_REQUIRE(all_aligned(4, {target, draft, parents, q_indptr, accept_u, sample_u, path, count}) &&
+                   all_aligned(8, {tokens, next_token}),
+               QLIN_ERR_ALIGNMENT, "int32 and float arrays must be 4-byte aligned, tokens 8-byte");
+  QLIN_DEVICE();
+  const VerifyDraftsArgs a = {target, target_stride, draft, draft_stride, V, Tq, parents, tokens, q_indptr, B, max_nodes,
+                              accept_u, sample_u, path, count, next_token};
+  return planned(plan, plan_verify_drafts(a, plan), "verify_drafts");
+}
+
+qlin_status qlin_kv_cache_keep_prepare(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                       const int32_t* ctx_lens, const int32_t* path, const int32_t* count, int64_t B,
+                                       int64_t max_path, int32_t* lens, qlin_call* call) {
+  Prepared* plan = nullptr;
+  QLIN_CHECK(begin_call(call, &plan));
+  QLIN_REQUIRE(B >= 0 && B <= 65535, QLIN_ERR_INVALID_ARG, "B=%lld out of range", (long long)B);
+  QLIN_REQUIRE(max_path >= 0 && max_path <= 65535, QLIN_ERR_INVALID_ARG, "max_path=%lld out of range", (long long)max_path);
+  QLIN_REQUIRE(max_pages >= 0 && max_pages <= kMaxDim, QLIN_ERR_INVALID_ARG, "max_pages=%lld out of range",
+               (long long)max_pages);
+  QLIN_CHECK(check_cache(cache));
+  if (B == 0) return empty_call(plan);
+  QLIN_REQUIRE(block_table && ctx_lens && count && (max_path == 0 || path), QLIN_ERR_INVALID_ARG, "null pointer");
+  QLIN_REQUIRE(lens != ctx_lens, QLIN_ERR_INVALID_ARG, "lens must not be ctx_lens");
+  QLIN_REQUIRE(all_aligned(4, {block_table, ctx_lens, path, count, lens}), QLIN_ERR_ALIGNMENT,
+               "int32 arrays must be 4-byte aligned");
+  QLIN_DEVICE();
+  return planned(plan, plan_kv_cache_keep(cache, block_table, max_pages, ctx_lens, path, count, B, max_path, lens, plan),
+                 "kv_cache_keep");
+}
+
 qlin_status qlin_call_run(const qlin_call* call, cudaStream_t stream) {
   QLIN_REQUIRE(call != nullptr, QLIN_ERR_INVALID_ARG, "null call");
   const Prepared& c = *reinterpret_cast<const Prepared*>(call);
@@ -1106,6 +1236,44 @@ qlin_status qlin_kv_cache_write(const qlin_heads* k, const qlin_heads* v, qlin_d
                                 const int64_t* slots, const qlin_kv_cache* cache, cudaStream_t stream) {
   qlin_call call;
   QLIN_CHECK(qlin_kv_cache_write_prepare(k, v, dtype, T, slots, cache, &call));
+  return qlin_call_run(&call, stream);
+}
+
+qlin_status qlin_kv_pages_assign(const qlin_kv_pages* pages, const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,
+                                 int64_t T, const int32_t* depths, int32_t* q_indptr, int64_t* positions, int64_t* slots,
+                                 cudaStream_t stream) {
+  qlin_call call;
+  QLIN_CHECK(qlin_kv_pages_assign_prepare(pages, ctx_lens, new_lens, B, T, depths, q_indptr, positions, slots, &call));
+  return qlin_call_run(&call, stream);
+}
+
+qlin_status qlin_chunk_attention(const qlin_heads* q, const qlin_heads* out, qlin_dtype dtype, int64_t Tq,
+                                 const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                                 const int32_t* q_indptr, const int32_t* ctx_lens, int64_t B, int64_t max_new,
+                                 const qlin_scores* scores, float* lse, void* workspace, int64_t workspace_bytes,
+                                 cudaStream_t stream) {
+  qlin_call call;
+  QLIN_CHECK(qlin_chunk_attention_prepare(q, out, dtype, Tq, cache, block_table, max_pages, q_indptr, ctx_lens, B, max_new,
+                                          scores, lse, workspace, workspace_bytes, &call));
+  return qlin_call_run(&call, stream);
+}
+
+qlin_status qlin_verify_drafts(const float* target, int64_t target_stride, const float* draft, int64_t draft_stride,
+                               int64_t V, int64_t Tq, const int32_t* parents, const int64_t* tokens,
+                               const int32_t* q_indptr, int64_t B, int64_t max_nodes, const float* accept_u,
+                               const float* sample_u, int32_t* path, int32_t* count, int64_t* next_token,
+                               cudaStream_t stream) {
+  qlin_call call;
+  QLIN_CHECK(qlin_verify_drafts_prepare(target, target_stride, draft, draft_stride, V, Tq, parents, tokens, q_indptr, B,
+                                        max_nodes, accept_u, sample_u, path, count, next_token, &call));
+  return qlin_call_run(&call, stream);
+}
+
+qlin_status qlin_kv_cache_keep(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                               const int32_t* ctx_lens, const int32_t* path, const int32_t* count, int64_t B,
+                               int64_t max_path, int32_t* lens, cudaStream_t stream) {
+  qlin_call call;
+  QLIN_CHECK(qlin_kv_cache_keep_prepare(cache, block_table, max_pages, ctx_lens, path, count, B, max_path, lens, &call));
   return qlin_call_run(&call, stream);
 }
 

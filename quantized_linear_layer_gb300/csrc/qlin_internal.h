@@ -202,4 +202,47 @@ struct TreeAttentionArgs {
 int64_t tree_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t Hq, int64_t max_nodes, int64_t B);
 cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out);
 
+// Block tables and slots from lengths.
+cudaError_t plan_kv_pages_assign(const qlin_kv_pages& pages, const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,
+                                 int64_t T, const int32_t* depths, int32_t* q_indptr, int64_t* positions, int64_t* slots,
+                                 Prepared* out);
+cudaError_t plan_kv_cache_keep(const qlin_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                               const int32_t* ctx_lens, const int32_t* path, const int32_t* count, int64_t B,
+                               int64_t max_path, int32_t* lens, Prepared* out);
+
+struct VerifyDraftsArgs {
+  const float* target;
+  int64_t target_stride;
+  const float* draft;
+  int64_t draft_stride;
+  int64_t V, Tq;
+  const int32_t* parents;
+  const int64_t* tokens;
+  const int32_t* q_indptr;
+  int64_t B, max_nodes;
+  const float* accept_u;
+  const float* sample_u;
+  int32_t* path;
+  int32_t* count;
+  int64_t* next_token;
+};
+cudaError_t plan_verify_drafts(const VerifyDraftsArgs& a, Prepared* out);
+
+struct ChunkAttentionArgs {
+  qlin_heads q, out;
+  qlin_dtype dtype;
+  int64_t Tq;
+  qlin_kv_cache cache;
+  const int32_t* block_table;
+  int64_t max_pages;
+  const int32_t* q_indptr;
+  const int32_t* ctx_lens;
+  int64_t B, max_new;
+  qlin_scores scores;
+  float* lse;
+  void* workspace;
+};
+int64_t chunk_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t Hq, int64_t max_new, int64_t B);
+cudaError_t plan_chunk_attention(const ChunkAttentionArgs& a, Prepared* out);
+
 }  // namespace qlin

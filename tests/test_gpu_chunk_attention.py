@@ -1,0 +1,286 @@
+"""Attention of a chunk of new tokens over the paged, quantized cache, against the
+64-bit oracle on the same codes.
+
+Tolerances.  The codes and the rows of q enter exactly.  A score's error e_ij (the
+oracle's chunk_attention says what it adds up) moves p_ij by e_ij and by the error of the
+sum, sum p e, relative.  Rounding a probability to fp16 moves it by 2^-11, and by 2^-34 of
+the row's largest where it becomes subnormal; sums over L tokens in float32 add at most L 2^-24,
+exp, log and the scales a few 2^-22.  So out is within
+  sum p e |v| + (sum p e + 2^-11 + (L + 64) 2^-24) sum p |v| + L 2^-34 max |v|
+plus the final rounding, and lse within sum p e + (L + 64) 2^-24 + 2^-22 |lse|."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as kv
+from oracle import serving as ref
+
+pytestmark = pytest.mark.gpu
+
+KIND = {"int8": torch.int8, "e4m3": torch.uint8, "u4": torch.uint8}
+
+
+class Problem:
+    """Sequences of (ctx, new) over a paged cache whose unused places hold NaN scales and any codes."""
+
+    def __init__(self, q, seqs, hq, hk, d, page, fmt, dtype, seed=0, wide=0.5, softcap=0.0, slopes=None, window=0, prefix=None,
+                 scale=None, spare_rows=0, size=1.5):
+        gen = torch.Generator().manual_seed(seed * 1000 + d + page)
+        self.q_, self.seqs, self.fmt, self.page, self.dtype = q, seqs, fmt, page, dtype
+        per = [-(-(c + n) // page) for c, n in seqs]
+        pages = sum(per) + 2
+        order = torch.randperm(pages, generator=gen).int()
+        self.table = torch.full((len(seqs), max(per, default=0) + 1), -3, dtype=torch.int32)
+        at = 0
+        for b, n in enumerate(per):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        x = torch.randn(2, pages, hk, page, d, generator=gen)
+        x[0, ..., 1] *= 5
+        x *= torch.exp(wide * torch.randn(2, pages, hk, page, 1, generator=gen))
+        self.codes, self.scales = kv.kv_quantize(x.numpy(), fmt)
+        live = np.zeros((pages, page), bool)
+        for b, (c, n) in enumerate(seqs):
+            p = np.arange(c + n)
+            live[self.table[b, p // page].numpy(), p % page] = True
+        dead = self.scales.copy()
+        dead[:, np.broadcast_to(~live[:, None, :], (pages, hk, page))] = np.nan
+        garbage = np.random.default_rng(seed).integers(0, 256, self.codes.shape).astype(self.codes.dtype)
+        self.t = [torch.from_numpy(v.copy()).cuda() for v in (*np.where(live[None, :, None, :, None], self.codes, garbage), *dead)]
+        self.cache = q.qlin_kv_cache(*self.t, {"int8": q.QLIN_KV_INT8, "e4m3": q.QLIN_KV_E4M3, "u4": q.QLIN_KV_U4}[fmt])
+        self.tq = sum(n for _, n in seqs)
+        self.q = (size * torch.randn(self.tq + spare_rows, hq, d, generator=gen)).to(dtype)
+        self.most = max([n for _, n in seqs] + [1])
+        self.scale = d ** -0.5 if scale is None else scale
+        self.how = dict(softcap=softcap, window=window, slopes=slopes, prefix=prefix)
+        self.indptr = torch.tensor([0] + list(np.cumsum([n for _, n in seqs])), dtype=torch.int32)
+        self.ctx = torch.tensor([c for c, _ in seqs], dtype=torch.int32)
+        self.out = torch.full(self.q.shape, 3.0, dtype=dtype, device="cuda")
+        self.lse = torch.full(self.q.shape[:2], 3.0, device="cuda")
+
+    def prepare(self, q_dev=None, out=None, most=None):
+        h, most = self.how, most or self.most
+        n = self.q_.qlin_chunk_attention_workspace_bytes(self.cache, self.q.shape[1], most, len(self.seqs))
+        self.dev = [t.cuda() for t in (self.table, self.indptr, self.ctx)]
+        return self.q_.qlin_chunk_attention_prepare(
+            self.q.cuda() if q_dev is None else q_dev, self.cache, *self.dev, self.out if out is None else out,
+            torch.full((n,), 0xff, dtype=torch.uint8, device="cuda"), most, self.scale, h["softcap"],
+            None if h["slopes"] is None else torch.tensor(h["slopes"], dtype=torch.float32, device="cuda"), h["window"],
+            None if h["prefix"] is None else torch.tensor(h["prefix"], dtype=torch.int32, device="cuda"), self.lse)
+
+    def run(self, **kw):
+        self.prepare(**kw).run()
+        torch.cuda.synchronize()
+        assert self.q_.qlin_get_device_error() == 0
+        return self
+
+    def values(self, b):
+        c, n = self.seqs[b]
+        p = np.arange(c + n)
+        pages = self.table[b, p // self.page].numpy()
+        return [kv.kv_values(self.codes[i][pages, :, p % self.page], self.scales[i][pages, :, p % self.page], self.fmt) for i in range(2)]
+
+    def check(self, only=None, out=None):
+        out, lse = (self.out if out is None else out).double().cpu().numpy(), self.lse.double().cpu().numpy()
+        half = torch.finfo(self.dtype).eps / 2
+        for b, (c, n) in enumerate(self.seqs):
+            if n == 0 or (only is not None and b not in only):
+                continue
+            k, v = self.values(b)
+            a, h = int(self.indptr[b]), self.how
+            prefix = 0 if h["prefix"] is None else min(max(h["prefix"][b], 0), c + n)
+            o, l, w, moved, err = ref.chunk_attention(self.q[a:a + n].double().numpy(), k, v, c, self.scale, h["softcap"], h["slopes"],
+                                                      h["window"], prefix)
+            s = (c + n + 64) * 2.0 ** -24
+            tol = moved + (err[..., None] + 2.0 ** -11 + s) * w + (c + n) * 2.0 ** -34 * np.abs(v).max()
+            tol = tol + half * (np.abs(o) + tol) + 2.0 ** -25
+            bad = ~(np.abs(out[a:a + n] - o) <= tol)
+            assert not bad.any(), (b, c, n, np.argwhere(bad)[:4], np.abs(out[a:a + n] - o).max(), bad.sum())
+            bad = ~(np.abs(lse[a:a + n] - l) <= err + s + 2.0 ** -22 * np.abs(l))
+            assert not bad.any(), (b, c, n, np.argwhere(bad)[:4], np.abs(lse[a:a + n] - l).max())
+        assert (out[self.tq:] == 3).all() and (lse[self.tq:] == 3).all()   # rows behind the last sequence
+        return self
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("hq,hk,d,page", [(1, 1, 64, 16), (4, 4, 128, 32), (8, 2, 128, 64), (10, 2, 64, 128), (8, 1, 256, 16), (3, 3, 256, 256)])
+def test_shapes(qlin_gpu, fmt, dtype, hq, hk, d, page):
+    """Every format, type, group and head size; lengths around a tile's borders, one token and none among them."""
+    seqs = [(0, 1), (0, 130), (127, 1), (128, 65), (5, 0), (300, 257), (255, 3)]
+    Problem(qlin_gpu, seqs, hq, hk, d, page, fmt, dtype, spare_rows=3).run().check()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("how", [dict(softcap=5.0), dict(window=1), dict(window=100), dict(prefix=[0, 129, 600, 7, -5]),
+                                 dict(window=37, prefix=[1, 260, 10 ** 6, 64, 0]), dict(slopes=[0.5, 0.03]),
+                                 dict(softcap=20.0, slopes=[-0.01, 1.0], window=200, prefix=[50, 5, 5, 400, 3])])
+def test_scores(qlin_gpu, fmt, d, how):
+    """Caps, windows, prefixes and biases, alone and together."""
+    seqs = [(0, 140), (200, 70), (10, 300), (515, 33), (129, 1)]
+    dtype = torch.bfloat16 if d == 128 else torch.float16
+    Problem(qlin_gpu, seqs, 2, 1, d, 32, fmt, dtype, seed=d, **how).run().check()
+
+
+@pytest.mark.parametrize("fmt,d,hq,hk", [("int8", 128, 8, 2), ("u4", 64, 4, 4), ("e4m3", 256, 4, 2)])
+def test_longer(qlin_gpu, fmt, d, hq, hk):
+    """Chunks of many tiles, split among blocks, beside single tokens over long contexts."""
+    Problem(qlin_gpu, [(1000, 700), (5003, 1), (0, 1500), (3000, 17)], hq, hk, d, 64, fmt, torch.bfloat16).run().check()
+
+
+def test_few_rows_over_long_contexts(qlin_gpu):
+    for seqs in ([(20000, 1)], [(20000, 3), (1, 1)]):
+        Problem(qlin_gpu, seqs, 4, 2, 128, 64, "int8", torch.float16, slopes=[0.001, 0.0, -0.0001, 0.1]).run().check()
+
+
+@pytest.mark.parametrize("size", [2.0 ** -30, 2.0 ** -9, 2.0 ** 6, 2.0 ** 40])
+def test_rows_of_any_size(qlin_gpu, size):
+    """bf16 rows far beyond fp16's range, with the scale that makes scores of them ordinary ones."""
+    Problem(qlin_gpu, [(100, 140)], 4, 2, 128, 16, "e4m3", torch.bfloat16, size=1.5 * size, scale=0.09 / size).run().check()
+
+
+def test_scores_far_apart(qlin_gpu):
+    """Scores of some hundreds: one token takes all of a row, the reference moves far and often."""
+    Problem(qlin_gpu, [(900, 200)], 4, 2, 128, 16, "int8", torch.float16, scale=2.0, wide=1.0).run().check()
+
+
+def test_strided_rows(qlin_gpu):
+    """q as part of fused q/k/v rows, out as heads-first storage."""
+    p = Problem(qlin_gpu, [(50, 200), (0, 31)], 8, 2, 128, 32, "int8", torch.float16)
+    whole = torch.zeros(p.tq, 12, 128, dtype=torch.float16, device="cuda")
+    whole[:, :8] = p.q.cuda()
+    out = torch.full((8, p.tq, 128), 3.0, dtype=torch.float16, device="cuda").transpose(0, 1)
+    p.run(q_dev=whole[:, :8], out=out).check(out=out)
+
+
+def test_odd_scales(qlin_gpu):
+    """Value and key scales of zero, below zero, very small and very large."""
+    for fmt in ("int8", "e4m3", "u4"):
+        p = Problem(qlin_gpu, [(200, 150)], 4, 2, 128, 16, fmt, torch.bfloat16, window=90, prefix=[20])
+        r = np.random.default_rng(1)
+        for i in range(2):
+            s = p.scales[i][..., 0] if fmt == "u4" else p.scales[i]
+            pick = r.random(s.shape)
+            s[pick < 0.1] *= -1
+            s[(pick > 0.1) & (pick < 0.15)] = 0
+            s[(pick > 0.15) & (pick < 0.2)] *= 2.0 ** -12
+        p.t = [torch.from_numpy(v.copy()).cuda() for v in (*p.codes, *p.scales)]
+        p.cache = qlin_gpu.qlin_kv_cache(*p.t, p.cache.fmt)
+        p.run().check()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_what_is_not_seen_does_not_reach_a_row(qlin_gpu, fmt, which):
+    """Scales (zero-points, E4M3 value codes) that are not numbers: rows that see such a token are NaN, others are not touched."""
+    p = Problem(qlin_gpu, [(130, 200)], 4, 2, 128, 16, fmt, torch.float16, window=60, prefix=[9]).run()
+    clean, clean_lse = p.out.clone(), p.lse.clone()
+    bad = [40, 131, 132, 250, 329]
+    kinds = ["scale"] + (["zero"] if fmt == "u4" else []) + (["code"] if fmt == "e4m3" else [])
+    at, j = 130 + np.arange(200)[:, None], np.array(bad)
+    hit = torch.from_numpy(((j <= at) & (at - j < 60)).any(1)).cuda()
+    for kind in kinds:
+        t = [x.clone() for x in p.t]
+        i = 0 if which == "k" else 1
+        for token in bad:
+            page, off = int(p.table[0, token // 16]), token % 16
+            if kind == "code":
+                t[i][page, :, off, 5] = 0x7f if token % 2 else 0xff
+            elif fmt == "u4":
+                t[2 + i][page, :, off, 0 if kind == "scale" else 1] = float("nan") if kind == "scale" else 7.5
+            else:
+                t[2 + i][page, :, off] = float("nan")
+        p.cache = qlin_gpu.qlin_kv_cache(*t, p.cache.fmt)
+        p.run()
+        assert bool(torch.isnan(p.out[hit]).flatten(1).any(1).all())
+        assert torch.equal(p.out[~hit], clean[~hit]) and torch.equal(p.lse[~hit], clean_lse[~hit])
+
+
+def test_pages_out_of_range_are_zeros(qlin_gpu):
+    """Tokens on a page that is none count as keys and values of zero, and are recorded."""
+    p = Problem(qlin_gpu, [(100, 60), (40, 9)], 4, 2, 128, 16, "int8", torch.float16)
+    page = int(p.table[0, 3])
+    p.codes[:, page] = 0
+    p.table[0, 3] = 10 ** 6
+    p.prepare().run()
+    torch.cuda.synchronize()
+    assert qlin_gpu.qlin_get_device_error() == 0x2000
+    p.table[0, 3] = page
+    p.check()
+
+
+@pytest.mark.parametrize("change", ["ctx", "long", "order", "past", "most"])
+def test_bounds_that_do_not_fit(qlin_gpu, change):
+    """A sequence whose bounds are out of range is recorded and left out; the others are as they were."""
+    p = Problem(qlin_gpu, [(20, 30), (100, 40), (7, 50)], 4, 2, 64, 16, "int8", torch.float16)
+    want, most = [0, 2], p.most
+    if change == "ctx":
+        p.ctx[1] = -1
+    elif change == "long":
+        p.ctx[1] = 16 * p.table.shape[1] - 39
+    elif change == "order":
+        p.indptr[2], want = 10, [0]
+    elif change == "past":
+        p.indptr[3], want = 121, [0, 1]
+    else:
+        most, want = 40, [0, 1]
+    p.prepare(most=most).run()
+    torch.cuda.synchronize()
+    assert qlin_gpu.qlin_get_device_error() == 0x2000
+    p.ctx[1] = 100
+    p.indptr = torch.tensor([0, 30, 70, 120], dtype=torch.int32)
+    p.check(only=want)
+    if change != "order":
+        left = ({0, 1, 2} - set(want)).pop()
+        assert (p.out[p.indptr[left]:p.indptr[left + 1]] == 3).all() and (p.lse[p.indptr[left]:p.indptr[left + 1]] == 3).all()
+
+
+def test_the_same_twice(qlin_gpu):
+    p = Problem(qlin_gpu, [(1000, 300), (77, 1), (0, 513)], 8, 2, 128, 64, "int8", torch.bfloat16)
+    a = p.run().out.clone()
+    for _ in range(3):
+        p.out.fill_(3.0)
+        assert torch.equal(a, p.run().out)
+
+
+def test_replays_with_other_lengths_and_another_stream(qlin_gpu):
+    """A captured call reads lengths, bounds and pages at every replay; a prepared one runs on any stream."""
+    q = qlin_gpu
+    first = Problem(q, [(300, 200), (10, 40), (0, 60)], 4, 2, 128, 16, "int8", torch.float16, seed=1, window=150, prefix=[3, 0, 8])
+    call = first.prepare()
+    dev, side = first.dev, torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call.run(side)
+    torch.cuda.current_stream().wait_stream(side)
+    first.check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.run()
+    for seqs in ([(0, 100), (33, 100), (200, 100)], [(470, 1), (0, 0), (1, 100)]):
+        first.out.fill_(3.0)
+        first.lse.fill_(3.0)
+        first.seqs, first.tq = seqs, sum(n for _, n in seqs)
+        first.indptr = torch.tensor([0] + list(np.cumsum([n for _, n in seqs])), dtype=torch.int32)
+        first.ctx = torch.tensor([c for c, _ in seqs], dtype=torch.int32)
+        # one table for all: the first sequence's pages
+        first.table = first.table[:1].expand(3, -1).contiguous()
+        dev[0].copy_(first.table)
+        dev[1].copy_(first.indptr)
+        dev[2].copy_(first.ctx)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert q.qlin_get_device_error() == 0
+        first.check()
+
+
+def test_as_attention_of_a_chain(qlin_gpu):
+    """Up to 256 new tokens it answers as tree attention of chains does, within both tolerances' roundings."""
+    q = qlin_gpu
+    p = Problem(q, [(500, 100), (64, 7)], 8, 2, 128, 16, "e4m3", torch.float16).run().check()
+    out, lse = torch.zeros_like(p.out), torch.zeros_like(p.lse)
+    ws = torch.empty(q.qlin_tree_attention_workspace_bytes(p.cache, 8, 100, 2), dtype=torch.uint8, device="cuda")
+    q.qlin_tree_attention(p.q.cuda(), p.cache, *p.dev, None, out, ws, 100, scale=p.scale, lse=lse)
+    p.out, p.lse = out, lse
+    p.check()
