@@ -1,137 +1,963 @@
 // Attention of a chunk of new tokens of each sequence over a paged, quantized
-// key / value cache that holds them already: causal, with a prefix that every row sees,
-// a window, capped scores and a bias by distance.
+// key / value cache that holds them already, on the tcgen05 tensor cores: causal, with
+// a prefix that every row sees, a window, capped scores and a bias by distance.
 //
-// One warp per row and query head walks the tokens that the row sees, with a
-// running maximum and sum; a lane holds D / 32 channels.
+// Mathematics: as in tree_attention.cu, with k_j = sk_j n_j and v_j = sv_j u_j
+//   t_ij = log2(e) f(scale sk_j (q_i . n_j)) + log2(sv_j)
+//   o_i  = sum_j 2^(t_ij - m_i) u_j / sum_j 2^(t_ij - m_i) / sv_j
+// f the cap and the bias.  The codes go to the tensor cores as they are; rows of
+// bf16 q that fp16 cannot hold are scaled by a power of two; P = 2^(t - m) is
+// rounded to fp16's 11 bits, the one rounding of an operand (below 2^-33 of the row's
+// largest it becomes 0).  The reference m_i follows the running maximum lazily: P
+// may grow to 2^15 before it moves and the row of O is rescaled.
+// The cap is c tanh(s / c) = c (1 - 2 / (1 + 2^(2 log2(e) s / c))).
+//
+// Work.  The rows of a key head (token, query head of the group) are cut into
+// tiles of 256 (128 for heads of 256), and of the tokens the tiles of 128 that some
+// of these rows see are taken.  All (sequence, key head, row tile, token tile) units in
+// this order are dealt out evenly to one block per SM, on the device, from the
+// lengths; a segment (row tile) cut by a block's border leaves float32 parts
+// that a second kernel joins.  So one long prompt, ragged batches and single
+// tokens over long contexts load the GPU alike, and a captured call stays right when
+// lengths change.
+//
+// A block has 20 warps, whose registers are dealt out anew by role:
+//   0-7    softmax, one thread a row: warps 0-3 the tile's first 128 rows (stream
+//          0), 4-7 the others (stream 1); heads of 256 have one stream and two
+//          threads a row, 64 tokens each
+//   8-15   load codes and scales into registers, a tile ahead, and widen them to fp16
+//          in shared memory, in the tensor core's layout: one widening for 256 rows
+//   16     issues the products (one thread)
+// Per token tile and stream: S = q n^T into the stream's tensor-memory buffer, which the
+// softmax threads turn into P over the same columns; O += P u takes P from there
+// and u as it lies (tokens x channels).  While one stream's softmax runs the tensor
+// cores work for the other.  (One stream: S has two buffers in turn.)
+// Tensor memory: S/P 2 x 128 columns, O 2 x D (1 x 256).
 #include <algorithm>
+#include <cmath>
+#include <type_traits>
 
-#include "kv_common.cuh"
-#include "qlin_internal.h"
-#include "tree_common.cuh"
+#include "chunk_common.cuh"
+#include "stage_ring.h"
 
 namespace qlin {
 namespace chunk {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kLn2 = 0.693147180559945309f;
-constexpr int64_t kMaxLen = 0x7fff0000;
+using namespace tree;  // the widening of codes, scales, pairs of float32
+using chunk::Params;
+using chunk::Sequence;
 
-struct Params {
-  const uint8_t* q;
-  uint8_t* out;
-  int64_t qt, qh, ot, oh;
-  int32_t hq, hk, dtype, fmt;
-  int64_t Tq;
-  kv::CacheView cache;
-  const int32_t* table;
-  int64_t max_pages;
-  const int32_t* q_indptr;
-  const int32_t* ctx_lens;
-  int32_t B, max_new;
-  qlin_scores scores;
-  float* lse;
-  int32_t* err;
+constexpr int kSoftmaxWarps = 8, kWidenWarps = 8;
+constexpr int kMmaWarp = kSoftmaxWarps + kWidenWarps;
+constexpr int kWarps = 20, kThreads = 32 * kWarps;  // whole groups of four warps
+constexpr int kLaunchRegs = 96;                     // of a thread at launch: 61440 in all
+constexpr int kCols = 4;                            // buffers of the tokens' scales: see the widening warps
+constexpr uint32_t kTmemO = 256;
+
+template <int FMT, int D>
+struct Geo {
+  static constexpr bool kU4 = FMT == QLIN_KV_U4;
+  static constexpr int kStreams = D == 256 ? 1 : 2;
+  static constexpr int kSubs = 2 / kStreams;  // threads of a row
+  static constexpr int kSpan = kTile / kSubs;  // tokens of each
+  static constexpr int kMine = D / kSubs;      // channels of q and o of each
+  static constexpr int kRows = 128 * kStreams;
+  static constexpr int kBufs = D == 256 ? 1 : 2;  // of K and of V
+  static constexpr int kRowBytes = kU4 ? D / 2 : D;
+  static constexpr int kBlocks = D / 64;            // 64-channel blocks of 128 rows x 128 bytes
+  static constexpr int kOperand = kBlocks * 16384;  // 128 rows of q, K or V in fp16
+  static constexpr uint32_t kOCols = D;             // tensor memory columns of a stream's O
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kStreams * kOperand;
+  static constexpr int kOffV = kOffK + kBufs * kOperand;
+  static constexpr int kOffCol = kOffV + kBufs * kOperand;             // [kCols][scale sk, log2 sv, 1 / sv, factor][128]
+  static constexpr int kOffPair = kOffCol + kCols * 4 * kTile * 4;     // [tile parity][thread of the row][row]
+  static constexpr int kOffQmax = kOffPair + 2 * kSubs * 128 * 4;      // [thread of the row][row]
+  static constexpr int kOffEnd = kOffQmax + kSubs * 128 * 4;           // [thread of the row][row] l
+  static constexpr int kOffBar = kOffEnd + kSubs * 128 * 4;
+  static constexpr int kBars = 4 * kBufs + 6 + kStreams + 1 + kCols;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;  // tensor memory address, flags
+  static constexpr int kOffScan = (kOffMisc + 32 + 7) / 8 * 8;
+  static constexpr int kOffWalk = (kOffScan + (kWarps + 1) * 8 + 15) / 16 * 16;
+  static constexpr int kSmem = kOffWalk + (kSoftmaxWarps + kWidenWarps + 1) * static_cast<int>(sizeof(Walk<kRows>)) + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kTmemO + kStreams * kOCols <= 512, "tensor memory");
+  static constexpr int kSoftmaxRegs = kStreams == 2 ? 152 : 112, kWidenRegs = kStreams == 2 ? 72 : 112, kOtherRegs = 32;
+  static_assert(kSoftmaxWarps * kSoftmaxRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kWarps * kLaunchRegs, "registers");
 };
 
-template <int D>
-__device__ __forceinline__ void codes_of(const Params& p, const uint8_t* base, const uint8_t* scales, int64_t page, int64_t row, int lane, float* x) {
-  constexpr int kMine = D / 32;
-  const uint8_t* sc = scales + page * p.cache.scale_page_stride + row * 4;
-  const uint8_t* c = base + page * p.cache.page_stride + row * (p.fmt == QLIN_KV_U4 ? D / 2 : D);
-#pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const int i = lane * kMine + k;
-    if (p.fmt == QLIN_KV_U4) {
-      const uint32_t word = *reinterpret_cast<const uint32_t*>(sc);
-      const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(word & 0xffffu)));
-      const float z = tree::odd_zero(word) ? __uint_as_float(0x7fc00000u) : __half2float(__ushort_as_half(static_cast<unsigned short>(word >> 16)));
-      x[k] = (static_cast<float>((c[i / 2] >> (4 * (i & 1))) & 15) - z) * s;
-    } else if (p.fmt == QLIN_KV_INT8) {
-      x[k] = static_cast<float>(reinterpret_cast<const int8_t*>(c)[i]) * *reinterpret_cast<const float*>(sc);
-    } else {
-      x[k] = kv::unpack2<0>(kv::e4m3x2_to_half2(c[i])).x * *reinterpret_cast<const float*>(sc);
+// The rows of a stream of a segment, as its roles need them.
+struct Stream {
+  int32_t first, last;  // positions of its first and last row
+  bool live;            // any row at all
+};
+
+template <int ROWS>
+__device__ __forceinline__ Stream stream_of(const Params& p, const Walk<ROWS>& w, int x) {
+  const int64_t row = static_cast<int64_t>(w.row_tile) * ROWS + x * 128;
+  Stream s;
+  s.live = row < w.s.rows;
+  s.first = w.s.ctx + static_cast<int32_t>(min(row, w.s.rows - 1) / p.group);
+  s.last = w.s.ctx + static_cast<int32_t>(min(row + 127, w.s.rows - 1) / p.group);
+  return s;
+}
+
+// Whether any row of the stream sees any token of the tile that begins at j0.
+__device__ __forceinline__ bool sees(const Params& p, const Stream& s, int32_t prefix, int32_t j0) {
+  return s.live && (j0 < prefix || (j0 <= s.last && (p.window == 0 || j0 + kTile > s.first - p.window + 1)));
+}
+
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+struct WaitOps {  // for stage_ring.h's wait_or_raise
+  volatile uint32_t* flag;
+  __device__ __forceinline__ void raise() { *flag = 1; }
+};
+
+template <int FMT, int D, bool SHAPED>
+__global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __grid_constant__ Params p) {
+  using G = Geo<FMT, D>;
+  constexpr int kRows = G::kRows, kStreams = G::kStreams, kSubs = G::kSubs, kBufs = G::kBufs;
+  using W = Walk<kRows>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - tc::smem_u32(smem_raw));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  const uint32_t bars = base + G::kOffBar;
+  const uint32_t k_full = bars, k_free = k_full + 8 * kBufs;                       // [kBufs]
+  const uint32_t v_full = k_free + 8 * kBufs, v_free = v_full + 8 * kBufs;         // [kBufs]
+  const uint32_t s_full = v_free + 8 * kBufs, p_full = s_full + 16, pv_done = p_full + 16;  // [2]
+  const uint32_t q_full = pv_done + 16;             // [kStreams]
+  const uint32_t all_done = q_full + 8 * kStreams;
+  const uint32_t col_full = all_done + 8;           // [kCols]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
+  volatile uint32_t* ran_out = tmem_slot + 1;  // a wait of some role of the block ran out
+  volatile uint32_t* odd_tile = tmem_slot + 2;  // [kCols]: 1 + the last tile with a factor (usable_scale) that is not 1
+  int64_t* scan = reinterpret_cast<int64_t*>(smem + G::kOffScan);
+  W* walks = reinterpret_cast<W*>(smem + G::kOffWalk);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBufs; ++i) {
+      tc::mbar_init(k_full + 8 * i, kWidenWarps);
+      tc::mbar_init(k_free + 8 * i, 1);
+      tc::mbar_init(v_full + 8 * i, kWidenWarps);
+      tc::mbar_init(v_free + 8 * i, 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(s_full + 8 * i, 1);
+      tc::mbar_init(p_full + 8 * i, kSoftmaxWarps / kStreams);
+      tc::mbar_init(pv_done + 8 * i, 1);
+    }
+    for (int i = 0; i < kStreams; ++i) tc::mbar_init(q_full + 8 * i, kSoftmaxWarps / kStreams);
+    tc::mbar_init(all_done, 1);
+    for (int i = 0; i < kCols; ++i) {
+      tc::mbar_init(col_full + 8 * i, kWidenWarps);
+      odd_tile[i] = 0;
+    }
+    *ran_out = 0;
+    tc::fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const int share = (p.B + kWarps - 1) / kWarps;
+  scan_units<kRows, kWarps>(p, share, scan);
+  const int64_t total = scan[kWarps];
+  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);  // each of these has a unit or more
+  if (threadIdx.x == 0) p.records[blockIdx.x].last = -1;
+  if (blockIdx.x >= blocks) return;
+  W* origin = walks + kSoftmaxWarps + kWidenWarps;
+  begin_run<kRows, kWarps>(p, share, scan, blockIdx.x, blocks, origin);
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // In every role a wait that runs out makes it go on without waiting, so that all loops end and every barrier among
+  // threads is met.
+  bool dead = false;
+  WaitOps ops = {ran_out};
+  auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+    ring::wait_or_raise(ops, dead, [&]() { return tc::mbar_wait_quiet(bar, parity & 1, p.err, site); });
+  };
+  // One lane steps a walk in shared memory.
+  auto next = [&](W& w) {
+    bool more = false;
+    __syncwarp();
+    if (lane == 0) more = w.next(p);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, more, 0) != 0;
+  };
+
+  if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
+  if (warp == kMmaWarp) {
+    // ---------------- products ----------------
+    // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one thread issues.
+    const bool leader = elect_one();
+    const uint32_t idesc_s = tc::idesc_f16(128, kTile, 0);
+    const uint32_t idesc_o = tc::idesc_f16(128, D, 0) | (1u << 16);  // B with n contiguous
+    // a descriptor's address field counts 16 bytes and does not overflow below 256 KB: advancing is an addition
+    const uint64_t q_desc = tc::sw128_kmajor_desc(base + G::kOffQ), k_desc = tc::sw128_kmajor_desc(base + G::kOffK);
+    const uint64_t v_desc = sw128_nmajor_desc(base + G::kOffV, 16384);
+    W& w = walks[kSoftmaxWarps + kWidenWarps];  // (the origin: nobody else reads it once all have their own)
+    uint32_t t = 0, seg = 0;
+    // the product P u of the step before, which is issued behind S of this one
+    struct { uint32_t step, tile; int x; bool on, first, last; } pend = {};
+    bool pending = false;
+    auto second = [&]() {
+      const uint32_t buf = pend.step & 1, vb = pend.tile % kBufs;
+      wait(p_full + 8 * buf, pend.step >> 1, 0x71);
+      if (pend.x == 0) wait(v_full + 8 * vb, pend.tile / kBufs, 0x72);
+      dead = __any_sync(0xffffffffu, dead);
+      tc::tc_fence_after();
+      if (leader) {
+        if (!dead && pend.on) {
+          const uint64_t vd = v_desc + vb * (G::kOperand >> 4);
+          const uint32_t pt = tmem + buf * 128, ot = tmem + kTmemO + pend.x * G::kOCols;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) tc::mma_f16_ta(ot, pt + 8 * k, vd + k * 128, idesc_o, !pend.first || k > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(pv_done + 8 * buf);
+        if (pend.last) tc::mma_commit(v_free + 8 * vb);
+      }
+      __syncwarp();
+    };
+    asm volatile("bar.sync 6, %0;" ::"n"(32 * (kSoftmaxWarps + kWidenWarps + 1)) : "memory");
+    while (next(w)) {
+      const int tiles = w.tiles, tile0 = w.tile, prefix = w.s.prefix;
+      const Tiles seen = w.seen;
+      Stream rows[kStreams];
+      bool begun[kStreams];
+#pragma unroll
+      for (int x = 0; x < kStreams; ++x) rows[x] = stream_of(p, w, x), begun[x] = false;
+      for (int i = 0; i < tiles; ++i, ++t) {
+        const int j0 = seen.at(tile0 + i) * kTile;
+#pragma unroll
+        for (int x = 0; x < kStreams; ++x) {
+          const uint32_t step = t * kStreams + x, buf = step & 1, kb = t % kBufs;
+          const bool on = sees(p, rows[x], prefix, j0);
+          if (i == 0) wait(q_full + 8 * x, seg, 0x73);
+          if (x == 0) wait(k_full + 8 * kb, t / kBufs, 0x74);
+          if (step >= 2) wait(pv_done + 8 * buf, (step - 2) >> 1, 0x75);
+          dead = __any_sync(0xffffffffu, dead);
+          tc::tc_fence_after();
+          if (leader) {
+            if (!dead && on) {
+              const uint64_t qd = q_desc + x * (G::kOperand >> 4), kd = k_desc + kb * (G::kOperand >> 4);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * 1024 + (k & 3) * 2;
+                tc::mma_f16(tmem + buf * 128, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+              }
+            }
+            tc::mma_commit(s_full + 8 * buf);
+            if (x == kStreams - 1) tc::mma_commit(k_free + 8 * kb);
+          }
+          __syncwarp();
+          if (pending) second();
+          pending = true;
+          pend = {step, t, x, on, on && !begun[x], x == kStreams - 1};
+          begun[x] = begun[x] || on;
+        }
+      }
+      ++seg;
+    }
+    if (pending) second();
+    // every product is done before the tensor memory is given back, whatever else ran out
+    if (leader) tc::mma_commit(all_done);
+    __syncwarp();
+    tc::mbar_wait_quiet(all_done, 0, p.err, 0x76);
+    __syncwarp();
+  } else if (warp > kMmaWarp) {
+    // (fills up the group)
+  } else if (warp >= kSoftmaxWarps) {
+    // ---------------- loads and widening ----------------
+    if constexpr (G::kWidenRegs > kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kWidenRegs));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kWidenRegs));
+    const int part = warp - kSoftmaxWarps;  // this warp's 16 tokens of a tile: they lie on one page
+    W& w = walks[warp];
+    if (lane == 0) w = *origin;
+    asm volatile("bar.sync 6, %0;" ::"n"(32 * (kSoftmaxWarps + kWidenWarps + 1)) : "memory");
+    // A lane takes 16 bytes of codes of one row at a time and makes kPieces 16-byte chunks of fp16 of them.  Rows and
+    // chunks are dealt to lanes such that, for each piece, the eight lanes of a quarter warp write to eight different bank
+    // groups, and a lane's row is the same modulo 8 throughout, so that its addresses differ by constants (heads of 256 are
+    // two halves of 128 channels, D2):
+    //   rows of 128 bytes: rows r, r ^ 5 x four chunks, one row's of one 64-channel block, the other's of the other
+    //   rows of 64 bytes, two blocks (U4): rows 0 1 | 6 7 or 2 3 | 4 5 x two chunks of one block | of the other
+    //   rows of 64 or 32 bytes, one block: consecutive rows
+    constexpr int D2 = D == 256 ? 128 : D, kHalves = D / D2;
+    constexpr int kHalfBytes = G::kU4 ? D2 / 2 : D2;  // of a row
+    constexpr int kBlocks2 = D2 / 64;
+    constexpr int kBlockBytes = kHalfBytes / kBlocks2;  // of a row's codes in one 64-channel block
+    constexpr int kPieces = G::kU4 ? 4 : 2;
+    constexpr bool kPairs = kHalfBytes == 128, kFours = G::kU4 && kBlocks2 == 2;
+    constexpr int kRowsAtOnce = kHalfBytes == 32 || kFours ? 16 : 8;
+    constexpr int kLoads = kHalves * 16 / kRowsAtOnce * kBlocks2;  // of 16 bytes, a lane's of K (of V) in a tile
+    int row, c, other = 0;  // of the 16 rows; the 16-byte chunk of the row (of the block); the block this lane takes first
+    if constexpr (kPairs) {
+      row = (lane >> 3) ^ ((lane & 4) ? 5 : 0);
+      c = lane & 3;
+      other = (lane >> 2) & 1;
+    } else if constexpr (kFours) {
+      const int i = (lane >> 1) & 3;
+      row = 8 * (lane >> 4) + ((lane & 8) ? 2 + i : i + (i & 2) * 2);
+      c = lane & 1;
+      other = i >> 1;
+    } else {
+      row = lane / (kHalfBytes / 16);
+      c = lane % (kHalfBytes / 16);
+    }
+    const uint32_t raw_at = static_cast<uint32_t>(row * G::kRowBytes + other * kBlockBytes + c * 16);
+    const uint32_t out_at = static_cast<uint32_t>((part * 16 + row) * 128 + (((c * kPieces) ^ (row & 7)) << 4)) + other * 16384u;
+    const uint32_t second = other ? 0u - 16384u : 16384u;  // from the first block to the second
+    const float to_t = SHAPED && p.softcap > 0.0f ? p.scale * (2.0f * kLog2e / p.softcap) : p.scale * kLog2e;
+
+    // This warp's tokens of a tile: how many of the 16 there are, their row in the page, and the page (not looked at before
+    // it is needed).
+    struct Part {
+      int32_t valid, at, page;
+    };
+    int i = 0, tiles = 0;
+    auto step = [&](Part& a) {
+      if (i == tiles) {
+        if (!next(w)) return false;
+        i = 0;
+        tiles = w.tiles;
+      }
+      const int j = w.seen.at(w.tile + i) * kTile + part * 16;
+      ++i;
+      a.valid = max(0, min(w.s.len - j, 16));
+      a.at = (w.head << p.page_shift) + (j & ((1 << p.page_shift) - 1));
+      a.page = a.valid > 0 ? p.table[w.b * p.max_pages + (j >> p.page_shift)] : 0;
+      return true;
+    };
+    // a page that is none: zeros
+    auto settle = [&](Part& a) {
+      if (a.page >= 0 && a.page < p.pages) return;
+      if (lane == 0) record_device_error(p.err, kDevErrBadIndex);
+      a.page = 0;
+      a.valid = 0;
+    };
+    auto load = [&](const Part& a, const uint8_t* codes, uint4* u) {
+      const uint8_t* from = codes + a.page * p.page_stride + static_cast<int64_t>(a.at) * G::kRowBytes;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int x = 0; x < 16 / kRowsAtOnce; ++x)
+#pragma unroll
+          for (int b = 0; b < kBlocks2; ++b) {
+            uint4& to = u[(h * (16 / kRowsAtOnce) + x) * kBlocks2 + b];
+            to = make_uint4(0u, 0u, 0u, 0u);
+            if (row + x * kRowsAtOnce < a.valid)
+              to = ldg_v4(from + ((raw_at + x * kRowsAtOnce * G::kRowBytes + h * kHalfBytes) ^ (b * kBlockBytes)));
+          }
+    };
+    auto load_scales = [&](const Part& a) {  // lanes 0-15 those of K, 16-31 those of V
+      const uint8_t* from = (lane < 16 ? p.k_scale : p.v_scale) + a.page * p.scale_page_stride + (static_cast<int64_t>(a.at) + (lane & 15)) * 4;
+      return (lane & 15) < a.valid ? __ldg(reinterpret_cast<const uint32_t*>(from)) : 0u;
+    };
+    // `word`: this lane's scale word (of K or of V)
+    auto widen = [&](const uint4* u, uint32_t word, bool v, uint32_t to) {
+      const uint32_t out = to + out_at;
+#pragma unroll
+      for (int x = 0; x < 16 / kRowsAtOnce; ++x) {
+        uint32_t bias = 0;
+        if constexpr (G::kU4) {
+          // what is no zero-point becomes one: its token counts by its score and its factor, and what is not seen has to
+          // stay finite
+          const uint32_t sw = __shfl_sync(0xffffffffu, word, (v ? 16 : 0) + row + x * kRowsAtOnce);
+          const __half z = __hmin(__hmax(__ushort_as_half(static_cast<unsigned short>(sw >> 16)), __float2half(0.0f)),
+                                  __float2half(15.0f));
+          const __half2 zz = __half2half2(__hadd(z, __float2half(1024.0f)));
+          bias = *reinterpret_cast<const uint32_t*>(&zz);
+        }
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+          for (int b = 0; b < kBlocks2; ++b) {
+            const uint4& r4 = u[(h * (16 / kRowsAtOnce) + x) * kBlocks2 + b];
+            const uint32_t wd[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+              uint32_t o[4];
+              if constexpr (G::kU4) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) o[m] = hsub2(((wd[k] >> (4 * m)) & 0x000f000fu) | kMagic, bias);
+              } else {
+                widen4<FMT>(wd[2 * k], o[0], o[1]);
+                widen4<FMT>(wd[2 * k + 1], o[2], o[3]);
+              }
+              sts128((out ^ (k << 4)) + x * kRowsAtOnce * 128 + h * 32768 + (b ? second : 0u), o[0], o[1], o[2], o[3]);
+            }
+          }
+      }
+      tc::fence_proxy_async_smem();
+    };
+
+    Part cur, ahead;
+    uint4 ku[kLoads], vu[kLoads];
+    uint32_t word = 0;
+    bool more = step(cur);
+    if (more) {
+      settle(cur);
+      load(cur, p.k, ku);
+      load(cur, p.v, vu);
+      word = load_scales(cur);
+      more = step(ahead);
+      bool go = true;
+      for (uint32_t t = 0; go; ++t) {
+        const uint32_t buf = t % kBufs;
+        if (t >= kBufs) wait(k_free + 8 * buf, t / kBufs - 1, 0x77);
+        dead = __any_sync(0xffffffffu, dead);
+        widen(ku, word, false, base + G::kOffK + buf * G::kOperand);
+        // The tokens' scales.  Their buffer was last read for tile t - kCols: S of tile t - kBufs is done, and it was issued
+        // after every stream's P of the tile before that one.
+        {
+          static_assert(kCols >= kBufs + 1, "buffers of scales");
+          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 4 * kTile + part * 16 + (lane & 15);
+          if (lane < 16) {
+            float sk;
+            if constexpr (G::kU4)
+              sk = odd_zero(word) ? __uint_as_float(0x7fc00000u) : __half2float(__ushort_as_half(static_cast<unsigned short>(word & 0xffffu)));
+            else
+              sk = __uint_as_float(word);
+            col[0] = sk * to_t;
+          } else {
+            float factor = 1.0f, sv;
+            uint32_t vw = word;
+            bool odd = odd_scale<FMT>(vw);
+            if (odd) vw = usable_scale<FMT>(vw, factor);
+            if constexpr (G::kU4) {  // without a zero-point a token is not a number: its factor here, its score above
+              if (odd_zero(word)) odd = true, factor = __uint_as_float(0x7fc00000u);
+              sv = __half2float(__ushort_as_half(static_cast<unsigned short>(vw & 0xffffu)));
+            } else {
+              sv = __uint_as_float(vw);
+            }
+            if (odd && (lane & 15) < cur.valid) odd_tile[t % kCols] = t + 1;
+            col[kTile] = lg2(sv);
+            col[2 * kTile] = rcp(sv);
+            col[3 * kTile] = factor;
+          }
+          if constexpr (FMT == QLIN_KV_E4M3) {
+            // Value codes that are NaN (which the library never writes) become 0 and their token's factor NaN: a product with
+            // a probability of 0 keeps a NaN, and rows that do not see the token must not get one.
+            uint32_t bad = 0;
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+              bad |= (((vu[k].x & 0x7f7f7f7fu) + 0x01010101u) | ((vu[k].y & 0x7f7f7f7fu) + 0x01010101u) |
+                      ((vu[k].z & 0x7f7f7f7fu) + 0x01010101u) | ((vu[k].w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+            if (__any_sync(0xffffffffu, bad != 0)) {
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < kLoads; ++k) {
+                uint32_t* u = &vu[k].x;
+                uint32_t any = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t m = __vcmpeq4(u[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  any |= m;
+                  u[e] &= ~m;
+                }
+                const int x = k / kBlocks2 % (16 / kRowsAtOnce);
+                if (any != 0) {
+                  reinterpret_cast<float*>(smem + G::kOffCol)[((t % kCols) * 4 + 3) * kTile + part * 16 + row + x * kRowsAtOnce] =
+                      __uint_as_float(0x7fc00000u);
+                  odd_tile[t % kCols] = t + 1;
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(k_full + 8 * buf);
+          tc::mbar_arrive(col_full + 8 * (t % kCols));
+        }
+        go = more;
+        uint32_t word_v = word;
+        if (go) {  // the next tile's keys, and where the one after it lies
+          settle(ahead);
+          load(ahead, p.k, ku);
+          word = load_scales(ahead);
+          cur = ahead;
+          more = step(ahead);
+        }
+        if (t >= kBufs) wait(v_free + 8 * buf, t / kBufs - 1, 0x78);
+        dead = __any_sync(0xffffffffu, dead);
+        widen(vu, word_v, true, base + G::kOffV + buf * G::kOperand);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(v_full + 8 * buf);
+        if (go) load(cur, p.v, vu);
+      }
+    }
+  } else {
+    // ---------------- softmax ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
+    constexpr int kSpan = G::kSpan, kMine = G::kMine;
+    const int quad = warp & 3;
+    const int stream = kStreams == 2 ? warp >> 2 : 0, sub = kStreams == 2 ? 0 : warp >> 2;
+    const int row = quad * 32 + lane;  // of the stream
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t o_at = lanes + kTmemO + stream * G::kOCols + sub * kMine;
+    float* row_max = reinterpret_cast<float*>(smem + G::kOffPair);
+    uint32_t* q_max = reinterpret_cast<uint32_t*>(smem + G::kOffQmax);
+    float* ends = reinterpret_cast<float*>(smem + G::kOffEnd);
+    W& w = walks[warp];
+    if (lane == 0) w = *origin;
+    asm volatile("bar.sync 6, %0;" ::"n"(32 * (kSoftmaxWarps + kWidenWarps + 1)) : "memory");
+    auto sync_rows = [&]() {  // the warps of these rows
+      if constexpr (kSubs > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + quad), "n"(32 * kSubs) : "memory");
+    };
+
+    // What is left to do for a segment once its last product is issued, and what its rows are.
+    struct Segment {
+      int64_t token;    // this row of q and out
+      int32_t head;     // query head
+      int32_t at;       // the row's position (of a row that is none: the last one's)
+      int32_t row_tile;
+      bool live, begins, ends;
+    };
+    auto segment = [&]() {
+      Segment g;
+      const int64_t r = static_cast<int64_t>(w.row_tile) * kRows + stream * 128 + row;
+      g.live = r < w.s.rows;
+      const int32_t node = static_cast<int32_t>(min(r, w.s.rows - 1) / p.group);
+      g.token = w.s.q_row + node;
+      g.head = w.head * p.group + static_cast<int32_t>(min(r, w.s.rows - 1) - static_cast<int64_t>(node) * p.group);
+      g.at = w.s.ctx + node;
+      g.row_tile = w.row_tile;
+      g.begins = w.begins();
+      g.ends = w.ends();
+      if (threadIdx.x == 0 && g.begins && !g.ends) p.records[blockIdx.x] = record_of(w, blocks, total);
+      return g;
+    };
+
+    // q of this thread's part of the row, scaled by a power of two, into shared memory; the factor to undo it
+    auto stage_q = [&](const Segment& g, float& row_scale) {
+      uint4 raw[kMine / 8];
+      uint32_t top = 0;
+      const bool bf16 = p.dtype == QLIN_BF16;
+      const uint8_t* src = p.q + g.token * p.qt + g.head * p.qh + sub * kMine * 2;
+#pragma unroll
+      for (int k = 0; k < kMine / 8; ++k) {
+        raw[k] = g.live ? ldg_v4(src + k * 16) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+        if (bf16) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max((u[e] << 16) & 0x7fffffffu, u[e] & 0x7fff0000u));
+        }
+      }
+      if constexpr (kSubs > 1) {
+        q_max[sub * 128 + row] = top;
+        sync_rows();
+        top = max(top, q_max[(sub ^ 1) * 128 + row]);
+      }
+      // fp16 rows go as they are, and bf16 rows whose largest lies in [2^-4, 2^15): what fp16 drops of those is below
+      // 2^-20 of it; others by a power of two that puts the largest into [2^14, 2^15)
+      int e = 0;
+      if (bf16 && top > 0 && top < 0x7f800000u) {
+        const int x = ilogbf(__uint_as_float(top));
+        if (x < -4 || x > 14) e = x - 14;
+      }
+      row_scale = ldexpf(1.0f, e);
+      const float s1 = ldexpf(1.0f, -(e / 2)), s2 = ldexpf(1.0f, -(e - e / 2));
+#pragma unroll
+      for (int k = 0; k < kMine / 8; ++k) {
+        uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+        if (bf16) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const float2 v = kv::unpack2<1>(u[m]);
+            u[m] = kv::pack2<0>(v.x * s1 * s2, v.y * s1 * s2);
+          }
+        }
+        const int chunk = sub * (kMine / 8) + k;
+        const uint32_t to = base + G::kOffQ + stream * G::kOperand + (chunk >> 3) * 16384 + half_chunk(row, chunk & 7);
+        if constexpr (G::kU4)  // the order in which 4-bit codes are widened: 0 4 1 5 2 6 3 7
+          sts128(to, __byte_perm(u[0], u[2], 0x5410), __byte_perm(u[0], u[2], 0x7632), __byte_perm(u[1], u[3], 0x5410),
+                 __byte_perm(u[1], u[3], 0x7632));
+        else
+          sts128(to, u[0], u[1], u[2], u[3]);
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(q_full + 8 * stream);
+    };
+
+    uint32_t t = 0;
+    bool more = next(w);
+    Segment g = segment();
+    float row_scale;
+    stage_q(g, row_scale);
+    const float cap2 = SHAPED ? p.softcap * kLog2e : 0.0f;
+    while (more) {
+      float ref = kNoRef;
+      uint64_t l2 = pair(0.0f, 0.0f);
+      bool begun = false;
+      const Stream rows = stream_of(p, w, stream);
+      // of this warp's rows
+      const int32_t first = __shfl_sync(0xffffffffu, g.at, 0), last = __shfl_sync(0xffffffffu, g.at, 31);
+      const bool scaled = !__all_sync(0xffffffffu, row_scale == 1.0f);
+      float slope2 = 0.0f;
+      if constexpr (SHAPED) slope2 = p.slopes != nullptr ? -kLog2e * p.slopes[g.head] : 0.0f;
+      // where a moved reference puts the row's largest probability: with more tiles to come, six bits below the
+      // top of fp16, which it may grow by before the row has to be rescaled
+      const float put = w.tiles > 1 ? 9.0f : kOffset;
+      for (int i = 0; i < w.tiles; ++i, ++t) {
+        const uint32_t step = t * kStreams + stream, buf = step & 1;
+        const int j0 = w.seen.at(w.tile + i) * kTile;
+        wait(s_full + 8 * buf, step >> 1, 0x79);
+        if (!sees(p, rows, w.s.prefix, j0)) {  // nothing was multiplied and nothing will be
+          if (lane == 0) tc::mbar_arrive(p_full + 8 * buf);
+          continue;
+        }
+        wait(col_full + 8 * (t % kCols), t / kCols, 0x7a);
+        dead = __any_sync(0xffffffffu, dead);
+        tc::tc_fence_after();
+        const bool odd = odd_tile[t % kCols] == t + 1;
+        const int jc = j0 + sub * kSpan;
+        const bool all = (j0 + kTile - 1 <= first && (p.window == 0 || j0 > last - p.window)) || j0 + kTile <= w.s.prefix;
+        const uint32_t s_at = lanes + buf * 128 + sub * kSpan;
+        const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 4 * kTile + sub * kSpan;
+
+        // t of 32 tokens from column k0 on, from their products
+        auto score = [&](uint32_t (&v)[32], int k0) {
+          if (scaled) {
+            const uint64_t rs = pair(row_scale, row_scale);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rs));
+              v[k] = __float_as_uint(a.x);
+              v[k + 1] = __float_as_uint(a.y);
+            }
+          }
+          if (SHAPED && cap2 > 0.0f) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 sk = *reinterpret_cast<const float4*>(col + k0 + k);
+              const float4 ls = *reinterpret_cast<const float4*>(col + kTile + k0 + k);
+              const float ks[4] = {sk.x, sk.y, sk.z, sk.w}, lv[4] = {ls.x, ls.y, ls.z, ls.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float r = rcp(1.0f + ex2(__uint_as_float(v[k + e]) * ks[e]));
+                v[k + e] = __float_as_uint(fmaf(r, -2.0f * cap2, cap2) + lv[e]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 sk = *reinterpret_cast<const float4*>(col + k0 + k);
+              const float4 ls = *reinterpret_cast<const float4*>(col + kTile + k0 + k);
+              const float2 a = unpair(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y), pair(ls.x, ls.y)));
+              const float2 b =
+                  unpair(fma2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), pair(sk.z, sk.w), pair(ls.z, ls.w)));
+              v[k] = __float_as_uint(a.x);
+              v[k + 1] = __float_as_uint(a.y);
+              v[k + 2] = __float_as_uint(b.x);
+              v[k + 3] = __float_as_uint(b.y);
+            }
+          }
+          if (SHAPED && p.slopes != nullptr) {
+            const float off = static_cast<float>(jc + k0 - g.at);  // exact below 2^24
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              v[k] = __float_as_uint(fmaf(slope2, fabsf(off + static_cast<float>(k)), __uint_as_float(v[k])));
+          }
+          if (!all) {
+            uint32_t bits = low_bits(g.at + 1 - jc - k0);
+            if (p.window > 0) bits &= ~low_bits(g.at - p.window + 1 - jc - k0);
+            bits |= low_bits(w.s.prefix - jc - k0);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((bits >> k) & 1u)) v[k] = 0xff800000u;
+          }
+        };
+        auto largest = [&](const uint32_t (&v)[32], float hi) {
+          float m[4] = {hi, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1])));
+          return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        };
+        // over all threads of the row
+        int rounds = 0;
+        auto of_row = [&](float hi) {
+          if constexpr (kSubs > 1) {
+            float* maxima = row_max + (rounds++ & 1) * kSubs * 128 + row;
+            maxima[sub * 128] = hi;
+            sync_rows();
+            hi = fmaxf(hi, maxima[(sub ^ 1) * 128]);
+          }
+          return hi;
+        };
+        float keep = 1.0f;
+        bool moved = false;
+        auto move = [&](float hi) {  // the reference, where P would grow too large
+          const bool far = hi > ref + (kOffset + kSlack);
+          const float to = far ? hi - put : ref;
+          const float k = ex2(ref - to);
+          ref = to;
+          keep *= k;
+          l2 = mul2(l2, pair(k, k));
+          return __any_sync(0xffffffffu, far);  // (the same in all warps of these rows)
+        };
+
+        uint32_t va[32], vb[32], pk[kSpan / 2];
+        if (!begun) {  // no reference yet: the maximum alone
+          float hi = -INFINITY;
+#pragma unroll
+          for (int k0 = 0; k0 < kSpan; k0 += 32) {
+            tc::tmem_ld_32x32b_x32(s_at + k0, va);
+            tc::tmem_wait_ld(va);
+            score(va, k0);
+            hi = largest(va, hi);
+          }
+          move(of_row(hi));
+        }
+        // P with the reference as it is; where a score lies far above it, once more with a new one
+        while (true) {
+          uint64_t sum = l2;
+          float hi = -INFINITY;
+          const uint64_t nref = pair(-ref, -ref);
+          auto weigh = [&](uint32_t (&v)[32], int k0, auto with_factors) {
+            score(v, k0);
+            hi = largest(v, hi);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 rv = *reinterpret_cast<const float4*>(col + 2 * kTile + k0 + k);
+              const float rr[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+              for (int x = 0; x < 4; x += 2) {
+                const float2 a = unpair(add2(pair(__uint_as_float(v[k + x]), __uint_as_float(v[k + x + 1])), nref));
+                float2 f = make_float2(ex2(a.x), ex2(a.y));
+                sum = fma2(pair(f.x, f.y), pair(rr[x], rr[x + 1]), sum);
+                if constexpr (decltype(with_factors)::value) {  // (what is hidden has no product with a factor that is not a number)
+                  f.x = v[k + x] == 0xff800000u ? 0.0f : f.x * col[3 * kTile + k0 + k + x];
+                  f.y = v[k + x + 1] == 0xff800000u ? 0.0f : f.y * col[3 * kTile + k0 + k + x + 1];
+                }
+                pk[(k0 + k + x) / 2] = kv::pack2<0>(f.x, f.y);
+              }
+            }
+          };
+          auto pass = [&](auto with_factors) {
+            tc::tmem_ld_32x32b_x32(s_at, va);
+#pragma unroll
+            for (int k0 = 0; k0 < kSpan; k0 += 64) {  // the next 32 on their way while these are weighed
+              tc::tmem_wait_ld(va);
+              tc::tmem_ld_32x32b_x32(s_at + k0 + 32, vb);
+              weigh(va, k0, with_factors);
+              tc::tmem_wait_ld(vb);
+              if (k0 + 64 < kSpan) tc::tmem_ld_32x32b_x32(s_at + k0 + 64, va);
+              weigh(vb, k0 + 32, with_factors);
+            }
+          };
+          if (odd) pass(std::true_type{});
+          else pass(std::false_type{});
+          if (!move(of_row(hi))) {
+            l2 = sum;
+            break;
+          }
+          moved = true;
+        }
+        // over the scores, which this row's threads have all read
+#pragma unroll
+        for (int k = 0; k < kSpan / 2; k += 32) tc::tmem_st_32x32b_x32(lanes + buf * 128 + sub * kSpan / 2 + k, pk + k);
+        if (moved && begun) {
+          const uint32_t before = step - kStreams;
+          wait(pv_done + 8 * (before & 1), before >> 1, 0x7b);
+          dead = __any_sync(0xffffffffu, dead);
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < kMine; cc += 16) {
+            uint32_t o[16];
+            tc::tmem_ld_32x32b_x16(o_at + cc, o);
+            tc::tmem_wait_ld(o);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float2 f = unpair(mul2(pair(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), pair(keep, keep)));
+              o[k] = __float_as_uint(f.x);
+              o[k + 1] = __float_as_uint(f.y);
+            }
+            tc::tmem_st_32x32b_x16(o_at + cc, o);
+          }
+        }
+        begun = true;
+        __syncwarp();
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full + 8 * buf);
+      }
+
+      // the next segment's q, then this one's output
+      const Segment done = g;
+      const float2 lp = unpair(l2);
+      float l = lp.x + lp.y;
+      if constexpr (kSubs > 1) ends[sub * 128 + row] = l;
+      more = next(w);
+      if (more) {
+        g = segment();
+        stage_q(g, row_scale);
+      }
+      if constexpr (kSubs > 1) {
+        sync_rows();
+        l = ends[row] + ends[128 + row];  // in one order for both
+      }
+      const uint32_t ended = (t - 1) * kStreams + stream;
+      wait(pv_done + 8 * (ended & 1), ended >> 1, 0x7c);
+      dead = __any_sync(0xffffffffu, dead);
+      tc::tc_fence_after();
+      const bool whole = done.begins && done.ends;
+      const bool none = ref == kNoRef;  // (O then holds anything)
+      const float inv = !whole ? 1.0f : __frcp_rn(l);
+      const float m = none ? -INFINITY : ref + kOffset;
+      const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (done.begins ? 1 : 0)) * p.tile_rows + stream * 128 + row;
+      if (rows.live) {
+#pragma unroll 1
+        for (int cc = 0; cc < kMine; cc += 16) {
+          uint32_t o[16];
+          __syncwarp();
+          tc::tmem_ld_32x32b_x16(o_at + cc, o);
+          tc::tmem_wait_ld(o);
+          float f[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            // 4-bit codes: column k of eight is channel k / 2 + 4 (k % 2)
+            const int ch = G::kU4 ? (k & 8) + ((k & 7) >> 1) + 4 * (k & 1) : k;
+            f[ch] = none ? 0.0f : __uint_as_float(o[k]) * inv;
+          }
+          if (!done.live) continue;
+          const int ch = sub * kMine + cc;
+          if (whole) {
+            uint8_t* out = p.out + done.token * p.ot + done.head * p.oh + ch * 2;
+#pragma unroll
+            for (int k = 0; k < 16; k += 8)
+              *reinterpret_cast<uint4*>(out + k * 2) = p.dtype == QLIN_BF16 ? kv::pack8<1>(f + k) : kv::pack8<0>(f + k);
+          } else {
+            float* out = p.part_o + slot * D + ch;
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(out + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+          }
+        }
+      }
+      if (done.live && sub == 0) {
+        if (!whole) p.part_ml[slot] = make_float2(m, l);
+        else if (p.lse != nullptr) p.lse[done.token * p.hq + done.head] = (lg2(l) + ref) * kLn2;
+      }
+      tc::tc_fence_before();
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
+// Joins the parts of a segment that begins in block `blockIdx.x` of the first kernel and ends in a later one, in the order of
+// the blocks: a warp a row, D / 4 lanes' worth of float4.
 template <int D>
-__global__ void __launch_bounds__(128) chunk_attention_kernel(const __grid_constant__ Params p) {
-  constexpr int kMine = D / 32;
+__global__ void __launch_bounds__(128) chunk_attention_join_kernel(const __grid_constant__ Params p) {
+  constexpr int kLanes = D / 4 < 32 ? D / 4 : 32;
+  constexpr int kWide = D / 4 / kLanes;
   pdl_wait();
   pdl_launch_dependents();
+  const tree::Record rec = p.records[blockIdx.x];
+  if (rec.last < 0) return;
   const int lane = threadIdx.x % 32;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
-  const int64_t row = unit / p.hq;
-  const int h = static_cast<int>(unit - row * p.hq);
-  if (row >= p.Tq) return;
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (p.q_indptr[mid] <= row) lo = mid; else hi = mid;
-  }
-  const int64_t q0 = p.q_indptr[lo], q1 = p.q_indptr[lo + 1], ctx = p.ctx_lens[lo];
-  if (row < q0 || row >= q1) return;
-  const int64_t len = ctx + q1 - q0;
-  if (q0 < 0 || q1 > p.Tq || q1 - q0 > p.max_new || ctx < 0 || len > (p.max_pages << p.cache.page_shift) || len > kMaxLen) {
-    record_device_error(p.err, kDevErrBadIndex);
-    return;
-  }
-  const int64_t at = ctx + row - q0;
-  const int64_t prefix = p.scores.prefix_lens != nullptr ? max(int64_t(0), min(static_cast<int64_t>(p.scores.prefix_lens[lo]), len)) : 0;
-  const int64_t low = p.scores.window > 0 ? max(int64_t(0), at - p.scores.window + 1) : 0;
-  const int head = h / (p.hq / p.hk);
-  float q[kMine], o[kMine] = {};
+  const int count = rec.last - static_cast<int>(blockIdx.x) + 1;
+  const int64_t rows = static_cast<int64_t>(rec.nodes) * p.group;
+  for (int row = blockIdx.y * 4 + threadIdx.x / 32; row < p.tile_rows; row += gridDim.y * 4) {
+    const int64_t at = static_cast<int64_t>(rec.row_tile) * (D == 256 ? 128 : 256) + row;
+    if (at >= rows) return;
+    if (lane >= kLanes) continue;
+    float m = -INFINITY, l = 0.0f;
+    float4 o[kWide];
 #pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const uint16_t u = *reinterpret_cast<const uint16_t*>(p.q + row * p.qt + h * p.qh + (lane * kMine + k) * 2);
-    q[k] = p.dtype == QLIN_BF16 ? kv::unpack2<1>(u).x : kv::unpack2<0>(u).x;
-  }
-  float m = -INFINITY, l = 0.0f;
-  const float slope = p.scores.slopes != nullptr ? p.scores.slopes[h] : 0.0f;
-  for (int64_t j = prefix > 0 ? 0 : low; j < max(prefix, at + 1); ++j) {
-    if (j >= prefix && j < low) j = low;
-    const int32_t page = p.table[lo * p.max_pages + (j >> p.cache.page_shift)];
-    float x[kMine] = {}, y[kMine] = {};
-    if (page >= 0 && page < p.cache.pages) {
-      const int64_t r = (static_cast<int64_t>(head) << p.cache.page_shift) + (j & ((1 << p.cache.page_shift) - 1));
-      codes_of<D>(p, p.cache.k, p.cache.k_scale, page, r, lane, x);
-      codes_of<D>(p, p.cache.v, p.cache.v_scale, page, r, lane, y);
-    } else {
-      record_device_error(p.err, kDevErrBadIndex);
+    for (int i = 0; i < kWide; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const int64_t slot = (2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0)) * p.tile_rows + row;
+      const float2 e = p.part_ml[slot];
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + slot * D) + lane;
+      const float to = fmaxf(m, e.x);
+      const float fa = m == -INFINITY ? 1.0f : ex2(m - to), fb = e.x == -INFINITY ? 1.0f : ex2(e.x - to);
+      m = to;
+      l = l * fa + e.y * fb;
+#pragma unroll
+      for (int x = 0; x < kWide; ++x) {
+        const float4 v = src[x * kLanes];
+        o[x].x = o[x].x * fa + v.x * fb;
+        o[x].y = o[x].y * fa + v.y * fb;
+        o[x].z = o[x].z * fa + v.z * fb;
+        o[x].w = o[x].w * fa + v.w * fb;
+      }
     }
-    float s = 0.0f;
+    const float inv = __frcp_rn(l);
+    const int64_t node = at / p.group;
+    const int head = rec.head * p.group + static_cast<int>(at - node * p.group);
+    const int64_t tok = rec.q_row + node;
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) s += q[k] * x[k];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scores.scale;
-    if (p.scores.softcap > 0.0f) s = p.scores.softcap * tanhf(s / p.scores.softcap);
-    s -= slope * fabsf(static_cast<float>(at - j));
-    const float to = fmaxf(m, s);
-    const float keep = m == -INFINITY ? 0.0f : __expf(m - to), e = __expf(s - to);
-    m = to;
-    l = l * keep + e;
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) o[k] = o[k] * keep + e * y[k];
+    for (int x = 0; x < kWide; ++x) {
+      const float v[4] = {o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv};
+      const uint2 u = p.dtype == QLIN_BF16 ? make_uint2(kv::pack2<1>(v[0], v[1]), kv::pack2<1>(v[2], v[3]))
+                                           : make_uint2(kv::pack2<0>(v[0], v[1]), kv::pack2<0>(v[2], v[3]));
+      *reinterpret_cast<uint2*>(p.out + tok * p.ot + head * p.oh + (lane + x * kLanes) * 8) = u;
+    }
+    if (p.lse != nullptr && lane == 0) p.lse[tok * p.hq + head] = (lg2(l) + (m - kOffset)) * kLn2;
   }
-#pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const uint32_t u = p.dtype == QLIN_BF16 ? kv::pack2<1>(o[k] / l, 0.0f) : kv::pack2<0>(o[k] / l, 0.0f);
-    *reinterpret_cast<uint16_t*>(p.out + row * p.ot + h * p.oh + (lane * kMine + k) * 2) = static_cast<uint16_t>(u);
-  }
-  if (p.lse != nullptr && lane == 0) p.lse[row * p.hq + h] = m + logf(l);
+}
+
+template <int FMT, int D, bool SHAPED>
+cudaError_t plan(const Params& p, Prepared* out) {
+  const void* fn = reinterpret_cast<const void*>(chunk_attention_kernel<FMT, D, SHAPED>);
+  const cudaError_t e = ensure_max_dynamic_smem(fn);
+  if (e != cudaSuccess) return e;
+  const uint32_t blocks = static_cast<uint32_t>(sm_count());
+  out->count = 2;
+  out->launch[0] = {fn, blocks, 1, kThreads, Geo<FMT, D>::kSmem};
+  out->launch[1] = {reinterpret_cast<const void*>(chunk_attention_join_kernel<D>), blocks,
+                    static_cast<uint32_t>((p.tile_rows + 7) / 8), 128, 0};
+  out->set(p);
+  return cudaSuccess;
+}
+
+template <int FMT, int D>
+cudaError_t plan(const Params& p, Prepared* out) {
+  return p.softcap > 0.0f || p.slopes != nullptr ? plan<FMT, D, true>(p, out) : plan<FMT, D, false>(p, out);
+}
+
+template <int FMT>
+cudaError_t plan(const Params& p, int64_t d, Prepared* out) {
+  return d == 64 ? plan<FMT, 64>(p, out) : d == 128 ? plan<FMT, 128>(p, out) : plan<FMT, 256>(p, out);
+}
+
+// Rows of a part in the workspace.
+int64_t part_rows(const qlin_kv_cache& c, int64_t hq, int64_t max_new) {
+  const int64_t group = hq / c.heads;
+  return std::min<int64_t>(c.head_dim == 256 ? 128 : 256, max_new > 256 ? 256 : max_new * group);
 }
 
 }  // namespace
 }  // namespace chunk
 
-int64_t chunk_attention_workspace_bytes(const qlin_kv_cache&, int64_t, int64_t, int64_t) { return 256; }
+int64_t chunk_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t hq, int64_t max_new, int64_t) {
+  const int64_t blocks = sm_count();
+  return blocks * static_cast<int64_t>(sizeof(tree::Record)) + 256 +
+         2 * blocks * chunk::part_rows(cache, hq, max_new) * (cache.head_dim * 4 + static_cast<int64_t>(sizeof(float2)));
+}
 
 cudaError_t plan_chunk_attention(const ChunkAttentionArgs& a, Prepared* out) {
-  using namespace chunk;
-  Params p = {};
+  chunk::Params p = {};
+  const qlin_kv_cache& c = a.cache;
   p.q = static_cast<const uint8_t*>(a.q.data);
   p.out = static_cast<uint8_t*>(a.out.data);
   p.qt = 2 * a.q.token_stride;
@@ -139,27 +965,43 @@ cudaError_t plan_chunk_attention(const ChunkAttentionArgs& a, Prepared* out) {
   p.ot = 2 * a.out.token_stride;
   p.oh = 2 * a.out.head_stride;
   p.hq = static_cast<int32_t>(a.q.heads);
-  p.hk = static_cast<int32_t>(a.cache.heads);
+  p.hk = static_cast<int32_t>(c.heads);
+  p.group = p.hq / p.hk;
   p.dtype = a.dtype;
-  p.fmt = a.cache.fmt;
   p.Tq = a.Tq;
-  p.cache = kv::view_of(a.cache);
+  p.k = static_cast<const uint8_t*>(c.k);
+  p.v = static_cast<const uint8_t*>(c.v);
+  p.page_stride = c.page_stride;
+  p.k_scale = static_cast<const uint8_t*>(c.k_scale);
+  p.v_scale = static_cast<const uint8_t*>(c.v_scale);
+  p.scale_page_stride = c.scale_page_stride;
+  const kv::CacheView view = kv::view_of(c);
+  p.pages = view.pages;
+  p.page_shift = view.page_shift;
   p.table = a.block_table;
   p.max_pages = a.max_pages;
   p.q_indptr = a.q_indptr;
   p.ctx_lens = a.ctx_lens;
   p.B = static_cast<int32_t>(a.B);
-  p.max_new = static_cast<int32_t>(a.max_new);
-  p.scores = a.scores;
+  p.max_nodes = static_cast<int32_t>(a.max_new);
+  p.scale = a.scores.scale;
+  p.softcap = a.scores.softcap;
+  p.slopes = a.scores.slopes;
+  p.window = static_cast<int32_t>(a.scores.window);
+  p.prefix = a.scores.prefix_lens;
   p.lse = a.lse;
+  p.tile_rows = static_cast<int32_t>(chunk::part_rows(c, a.q.heads, a.max_new));
+  const int64_t blocks = sm_count(), rows = 2 * blocks * p.tile_rows;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  ws += rows * c.head_dim * 4;
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  ws += rows * static_cast<int64_t>(sizeof(float2));
+  p.records = reinterpret_cast<tree::Record*>(ws);
   p.err = device_error_word();
-  const void* fn = a.cache.head_dim == 64 ? reinterpret_cast<const void*>(chunk_attention_kernel<64>)
-                   : a.cache.head_dim == 128 ? reinterpret_cast<const void*>(chunk_attention_kernel<128>)
-                                             : reinterpret_cast<const void*>(chunk_attention_kernel<256>);
-  out->count = 1;
-  out->launch[0] = {fn, static_cast<uint32_t>((a.Tq * a.q.heads + 3) / 4), 1, 128, 0};
-  out->set(p);
-  return cudaSuccess;
+  if (c.fmt == QLIN_KV_INT8) return chunk::plan<QLIN_KV_INT8>(p, c.head_dim, out);
+  if (c.fmt == QLIN_KV_E4M3) return chunk::plan<QLIN_KV_E4M3>(p, c.head_dim, out);
+  return chunk::plan<QLIN_KV_U4>(p, c.head_dim, out);
 }
 
 }  // namespace qlin

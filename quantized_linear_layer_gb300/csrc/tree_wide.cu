@@ -94,47 +94,6 @@ struct Geo {
 
 };
 
-// Where 16-byte chunk c (eight channels) of row r of a 64-channel fp16 block lies (128-byte swizzle).
-__device__ __forceinline__ uint32_t half_chunk(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
-
-__device__ __forceinline__ void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// Pairs of float32 in one 64-bit register: two operations per instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
-// True in one thread of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
-  return r != 0;
-}
-
 // Halves below fp16's normal range become 0.
 __device__ __forceinline__ __half2 flush(uint32_t v) {
   uint32_t r;
@@ -148,19 +107,6 @@ __device__ __forceinline__ void split(uint64_t e, uint64_t up, uint32_t& large, 
   const __half2 p16 = flush(kv::pack2<0>(f.x, f.y));
   large = *reinterpret_cast<const uint32_t*>(&p16);
   small = kv::pack2<0>(s.x, s.y) & __heq2_mask(p16, __float2half2_rn(0.0f));
-}
-
-// Shared-memory descriptor of an operand stored k x n with n contiguous, in
-// 128-byte swizzled atoms of 8 k x 64 n: atoms of the next 8 k follow (1024
-// bytes), the next 64 n lie `n_stride` bytes on.
-__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t saddr, uint32_t n_stride) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(n_stride >> 4) << 16;   // leading byte offset
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;      // stride byte offset
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
 }
 
 // Which of the 64 tokens from node `first` on (negative: cached tokens) node
