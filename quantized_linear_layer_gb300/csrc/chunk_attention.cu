@@ -21,13 +21,13 @@
 // tokens over long contexts load the GPU alike, and a captured call stays right when
 // lengths change.
 //
-// A block has 20 warps, whose registers are dealt out anew by role:
+// A block has 16 warps, whose registers are dealt out anew by role:
 //   0-7    softmax, one thread a row: warps 0-3 the tile's first 128 rows (stream
 //          0), 4-7 the others (stream 1); heads of 256 have one stream and two
 //          threads a row, 64 tokens each
-//   8-15   load codes and scales into registers, a tile ahead, and widen them to fp16
+//   8-11   load codes and scales into registers, a tile ahead, and widen them to fp16
 //          in shared memory, in the tensor core's layout: one widening for 256 rows
-//   16     issues the products (one thread)
+//   12     issues the products (one thread)
 // Per token tile and stream: S = q n^T into the stream's tensor-memory buffer, which the
 // softmax threads turn into P over the same columns; O += P u takes P from there
 // and u as it lies (tokens x channels).  While one stream's softmax runs the tensor
@@ -48,10 +48,7 @@ using namespace tree;  // the widening of codes, scales, pairs of float32
 using chunk::Params;
 using chunk::Sequence;
 
-constexpr int kSoftmaxWarps = 8, kWidenWarps = 8;
-constexpr int kMmaWarp = kSoftmaxWarps + kWidenWarps;
-constexpr int kWarps = 20, kThreads = 32 * kWarps;  // whole groups of four warps
-constexpr int kLaunchRegs = 96;                     // of a thread at launch: 61440 in all
+constexpr int kSoftmaxWarps = 8;
 constexpr int kCols = 4;                            // buffers of the tokens' scales: see the widening warps
 constexpr uint32_t kTmemO = 256;
 
@@ -64,6 +61,13 @@ struct Geo {
   static constexpr int kMine = D / kSubs;      // channels of q and o of each
   static constexpr int kRows = 128 * kStreams;
   static constexpr int kBufs = D == 256 ? 1 : 2;  // of K and of V
+  // Warps, whole groups of four, and their registers: what all are launched with is dealt out anew by role.
+  static constexpr int kWidenWarps = 4, kMmaWarp = kSoftmaxWarps + kWidenWarps;
+  static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps;
+  static constexpr int kLaunchRegs = 128;
+  static constexpr int kSoftmaxRegs = D == 256 ? 112 : 160, kWidenRegs = D == 256 ? 232 : 144, kOtherRegs = 48;
+  static_assert(kSoftmaxWarps * kSoftmaxRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kWarps * kLaunchRegs, "registers");
+  static constexpr int kParts = kTile / 16 / kWidenWarps;  // 16 tokens each, of a widening warp
   static constexpr int kRowBytes = kU4 ? D / 2 : D;
   static constexpr int kBlocks = D / 64;            // 64-channel blocks of 128 rows x 128 bytes
   static constexpr int kOperand = kBlocks * 16384;  // 128 rows of q, K or V in fp16
@@ -75,7 +79,9 @@ struct Geo {
   static constexpr int kOffPair = kOffCol + kCols * 4 * kTile * 4;     // [tile parity][thread of the row][row]
   static constexpr int kOffQmax = kOffPair + 2 * kSubs * 128 * 4;      // [thread of the row][row]
   static constexpr int kOffEnd = kOffQmax + kSubs * 128 * 4;           // [thread of the row][row] l
-  static constexpr int kOffBar = kOffEnd + kSubs * 128 * 4;
+  static constexpr int kOffRow = kOffEnd + kSubs * 128 * 4;                          // [segment parity][softmax thread] RowOf
+  static constexpr int kOffWarp = kOffRow + 2 * 32 * kSoftmaxWarps * 16;             // [softmax warp, stream of the products] WarpRows
+  static constexpr int kOffBar = kOffWarp + (kSoftmaxWarps + 2) * 32;
   static constexpr int kBars = 4 * kBufs + 6 + kStreams + 1 + kCols;
   static constexpr int kOffMisc = kOffBar + kBars * 8;  // tensor memory address, flags
   static constexpr int kOffScan = (kOffMisc + 32 + 7) / 8 * 8;
@@ -83,8 +89,6 @@ struct Geo {
   static constexpr int kSmem = kOffWalk + (kSoftmaxWarps + kWidenWarps + 1) * static_cast<int>(sizeof(Walk<kRows>)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kTmemO + kStreams * kOCols <= 512, "tensor memory");
-  static constexpr int kSoftmaxRegs = kStreams == 2 ? 152 : 112, kWidenRegs = kStreams == 2 ? 72 : 112, kOtherRegs = 32;
-  static_assert(kSoftmaxWarps * kSoftmaxRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kWarps * kLaunchRegs, "registers");
 };
 
 // The rows of a stream of a segment, as its roles need them.
@@ -103,9 +107,32 @@ __device__ __forceinline__ Stream stream_of(const Params& p, const Walk<ROWS>& w
   return s;
 }
 
+// What a softmax thread and its warp know of a segment, kept in shared memory: in registers it would take the scores'.
+struct RowOf {
+  int64_t token;  // the row of q and out; -1: none
+  int32_t head;   // query head
+  int32_t flags;  // 1: the segment begins in this block, 2: it ends in it
+};
+struct WarpRows {
+  Stream rows;
+  int32_t first, last;  // positions of the warp's first and last row
+};
+
 // Whether any row of the stream sees any token of the tile that begins at j0.
 __device__ __forceinline__ bool sees(const Params& p, const Stream& s, int32_t prefix, int32_t j0) {
   return s.live && (j0 < prefix || (j0 <= s.last && (p.window == 0 || j0 + kTile > s.first - p.window + 1)));
+}
+
+// Loads that stay where they are written: moved ahead of their use, they would take the registers that the scores need.
+__device__ __forceinline__ float4 lds4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float lds1(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
 }
 
 // Bits 0 .. n - 1.
@@ -117,9 +144,10 @@ struct WaitOps {  // for stage_ring.h's wait_or_raise
 };
 
 template <int FMT, int D, bool SHAPED>
-__global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kernel(const __grid_constant__ Params p) {
   using G = Geo<FMT, D>;
   constexpr int kRows = G::kRows, kStreams = G::kStreams, kSubs = G::kSubs, kBufs = G::kBufs;
+  constexpr int kWidenWarps = G::kWidenWarps, kMmaWarp = G::kMmaWarp, kWarps = G::kWarps;
   using W = Walk<kRows>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -205,43 +233,40 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     // a descriptor's address field counts 16 bytes and does not overflow below 256 KB: advancing is an addition
     const uint64_t q_desc = tc::sw128_kmajor_desc(base + G::kOffQ), k_desc = tc::sw128_kmajor_desc(base + G::kOffK);
     const uint64_t v_desc = sw128_nmajor_desc(base + G::kOffV, 16384);
-    W& w = walks[kSoftmaxWarps + kWidenWarps];  // (the origin: nobody else reads it once all have their own)
+    W& w = *origin;  // (nobody else reads it once all have their own)
+    WarpRows* wr = reinterpret_cast<WarpRows*>(smem + G::kOffWarp) + kSoftmaxWarps;
     uint32_t t = 0, seg = 0;
-    // the product P u of the step before, which is issued behind S of this one
-    struct { uint32_t step, tile; int x; bool on, first, last; } pend = {};
-    bool pending = false;
-    auto second = [&]() {
-      const uint32_t buf = pend.step & 1, vb = pend.tile % kBufs;
-      wait(p_full + 8 * buf, pend.step >> 1, 0x71);
-      if (pend.x == 0) wait(v_full + 8 * vb, pend.tile / kBufs, 0x72);
+    // P u of the step before is issued behind S of this one: whether it has any product, and whether it is its segment's first
+    bool pending = false, pend_on = false, pend_first = false;
+    auto second = [&](uint32_t step) {
+      const uint32_t buf = step & 1, x = step % kStreams, tile = step / kStreams, vb = tile % kBufs;
+      wait(p_full + 8 * buf, step >> 1, 0x71);
+      if (x == 0) wait(v_full + 8 * vb, tile / kBufs, 0x72);
       dead = __any_sync(0xffffffffu, dead);
       tc::tc_fence_after();
       if (leader) {
-        if (!dead && pend.on) {
+        if (!dead && pend_on) {
           const uint64_t vd = v_desc + vb * (G::kOperand >> 4);
-          const uint32_t pt = tmem + buf * 128, ot = tmem + kTmemO + pend.x * G::kOCols;
+          const uint32_t pt = tmem + buf * 128, ot = tmem + kTmemO + x * G::kOCols;
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) tc::mma_f16_ta(ot, pt + 8 * k, vd + k * 128, idesc_o, !pend.first || k > 0 ? 1u : 0u);
+          for (int k = 0; k < kTile / 16; ++k) tc::mma_f16_ta(ot, pt + 8 * k, vd + k * 128, idesc_o, !pend_first || k > 0 ? 1u : 0u);
         }
         tc::mma_commit(pv_done + 8 * buf);
-        if (pend.last) tc::mma_commit(v_free + 8 * vb);
+        if (x == kStreams - 1) tc::mma_commit(v_free + 8 * vb);
       }
       __syncwarp();
     };
     asm volatile("bar.sync 6, %0;" ::"n"(32 * (kSoftmaxWarps + kWidenWarps + 1)) : "memory");
     while (next(w)) {
-      const int tiles = w.tiles, tile0 = w.tile, prefix = w.s.prefix;
-      const Tiles seen = w.seen;
-      Stream rows[kStreams];
-      bool begun[kStreams];
-#pragma unroll
-      for (int x = 0; x < kStreams; ++x) rows[x] = stream_of(p, w, x), begun[x] = false;
-      for (int i = 0; i < tiles; ++i, ++t) {
-        const int j0 = seen.at(tile0 + i) * kTile;
+      if (lane < kStreams) wr[lane].rows = stream_of(p, w, lane);
+      __syncwarp();
+      uint32_t begun = 0;
+      for (int i = 0; i < w.tiles; ++i, ++t) {
+        const int j0 = w.seen.at(w.tile + i) * kTile;
 #pragma unroll
         for (int x = 0; x < kStreams; ++x) {
           const uint32_t step = t * kStreams + x, buf = step & 1, kb = t % kBufs;
-          const bool on = sees(p, rows[x], prefix, j0);
+          const bool on = sees(p, wr[x].rows, w.s.prefix, j0);
           if (i == 0) wait(q_full + 8 * x, seg, 0x73);
           if (x == 0) wait(k_full + 8 * kb, t / kBufs, 0x74);
           if (step >= 2) wait(pv_done + 8 * buf, (step - 2) >> 1, 0x75);
@@ -260,15 +285,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
             if (x == kStreams - 1) tc::mma_commit(k_free + 8 * kb);
           }
           __syncwarp();
-          if (pending) second();
+          if (pending) second(step - 1);
           pending = true;
-          pend = {step, t, x, on, on && !begun[x], x == kStreams - 1};
-          begun[x] = begun[x] || on;
+          pend_on = on;
+          pend_first = on && !((begun >> x) & 1);
+          if (on) begun |= 1u << x;
         }
       }
       ++seg;
     }
-    if (pending) second();
+    if (pending) second(t * kStreams - 1);
     // every product is done before the tensor memory is given back, whatever else ran out
     if (leader) tc::mma_commit(all_done);
     __syncwarp();
@@ -278,9 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     // (fills up the group)
   } else if (warp >= kSoftmaxWarps) {
     // ---------------- loads and widening ----------------
-    if constexpr (G::kWidenRegs > kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kWidenRegs));
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kWidenRegs));
-    const int part = warp - kSoftmaxWarps;  // this warp's 16 tokens of a tile: they lie on one page
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kWidenRegs));
+    constexpr int kParts = G::kParts;
+    const int part0 = (warp - kSoftmaxWarps) * kParts;  // this warp's tokens of a tile: 16 each, which lie on one page
     W& w = walks[warp];
     if (lane == 0) w = *origin;
     asm volatile("bar.sync 6, %0;" ::"n"(32 * (kSoftmaxWarps + kWidenWarps + 1)) : "memory");
@@ -314,59 +340,74 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       c = lane % (kHalfBytes / 16);
     }
     const uint32_t raw_at = static_cast<uint32_t>(row * G::kRowBytes + other * kBlockBytes + c * 16);
-    const uint32_t out_at = static_cast<uint32_t>((part * 16 + row) * 128 + (((c * kPieces) ^ (row & 7)) << 4)) + other * 16384u;
+    const uint32_t out_at = static_cast<uint32_t>((part0 * 16 + row) * 128 + (((c * kPieces) ^ (row & 7)) << 4)) + other * 16384u;
     const uint32_t second = other ? 0u - 16384u : 16384u;  // from the first block to the second
     const float to_t = SHAPED && p.softcap > 0.0f ? p.scale * (2.0f * kLog2e / p.softcap) : p.scale * kLog2e;
 
-    // This warp's tokens of a tile: how many of the 16 there are, their row in the page, and the page (not looked at before
-    // it is needed).
+    // Sixteen tokens of a tile: how many of them there are, their row in the page, and the page (not looked at before it is
+    // needed).
     struct Part {
       int32_t valid, at, page;
     };
     int i = 0, tiles = 0;
-    auto step = [&](Part& a) {
+    auto step = [&](Part (&a)[kParts]) {
       if (i == tiles) {
         if (!next(w)) return false;
         i = 0;
         tiles = w.tiles;
       }
-      const int j = w.seen.at(w.tile + i) * kTile + part * 16;
+      const int j0 = w.seen.at(w.tile + i) * kTile + part0 * 16;
       ++i;
-      a.valid = max(0, min(w.s.len - j, 16));
-      a.at = (w.head << p.page_shift) + (j & ((1 << p.page_shift) - 1));
-      a.page = a.valid > 0 ? p.table[w.b * p.max_pages + (j >> p.page_shift)] : 0;
+#pragma unroll
+      for (int g = 0; g < kParts; ++g) {
+        const int j = j0 + g * 16;
+        a[g].valid = max(0, min(w.s.len - j, 16));
+        a[g].at = (w.head << p.page_shift) + (j & ((1 << p.page_shift) - 1));
+        a[g].page = a[g].valid > 0 ? p.table[w.b * p.max_pages + (j >> p.page_shift)] : 0;
+      }
       return true;
     };
     // a page that is none: zeros
-    auto settle = [&](Part& a) {
-      if (a.page >= 0 && a.page < p.pages) return;
-      if (lane == 0) record_device_error(p.err, kDevErrBadIndex);
-      a.page = 0;
-      a.valid = 0;
+    auto settle = [&](Part (&a)[kParts]) {
+#pragma unroll
+      for (int g = 0; g < kParts; ++g) {
+        if (a[g].page >= 0 && a[g].page < p.pages) continue;
+        if (lane == 0) record_device_error(p.err, kDevErrBadIndex);
+        a[g].page = 0;
+        a[g].valid = 0;
+      }
     };
-    auto load = [&](const Part& a, const uint8_t* codes, uint4* u) {
-      const uint8_t* from = codes + a.page * p.page_stride + static_cast<int64_t>(a.at) * G::kRowBytes;
+    auto load = [&](const Part (&a)[kParts], const uint8_t* codes, uint4 (&u)[kParts][kLoads]) {
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h)
+      for (int g = 0; g < kParts; ++g) {
+        const uint8_t* from = codes + a[g].page * p.page_stride + static_cast<int64_t>(a[g].at) * G::kRowBytes;
 #pragma unroll
-        for (int x = 0; x < 16 / kRowsAtOnce; ++x)
+        for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-          for (int b = 0; b < kBlocks2; ++b) {
-            uint4& to = u[(h * (16 / kRowsAtOnce) + x) * kBlocks2 + b];
-            to = make_uint4(0u, 0u, 0u, 0u);
-            if (row + x * kRowsAtOnce < a.valid)
-              to = ldg_v4(from + ((raw_at + x * kRowsAtOnce * G::kRowBytes + h * kHalfBytes) ^ (b * kBlockBytes)));
-          }
+          for (int x = 0; x < 16 / kRowsAtOnce; ++x)
+#pragma unroll
+            for (int b = 0; b < kBlocks2; ++b) {
+              uint4& to = u[g][(h * (16 / kRowsAtOnce) + x) * kBlocks2 + b];
+              to = make_uint4(0u, 0u, 0u, 0u);
+              if (row + x * kRowsAtOnce < a[g].valid)
+                to = ldg_v4(from + ((raw_at + x * kRowsAtOnce * G::kRowBytes + h * kHalfBytes) ^ (b * kBlockBytes)));
+            }
+      }
     };
-    auto load_scales = [&](const Part& a) {  // lanes 0-15 those of K, 16-31 those of V
-      const uint8_t* from = (lane < 16 ? p.k_scale : p.v_scale) + a.page * p.scale_page_stride + (static_cast<int64_t>(a.at) + (lane & 15)) * 4;
-      return (lane & 15) < a.valid ? __ldg(reinterpret_cast<const uint32_t*>(from)) : 0u;
-    };
-    // `word`: this lane's scale word (of K or of V)
-    auto widen = [&](const uint4* u, uint32_t word, bool v, uint32_t to) {
-      const uint32_t out = to + out_at;
+    auto load_scales = [&](const Part (&a)[kParts], uint32_t (&word)[kParts]) {  // lanes 0-15 those of K, 16-31 those of V
 #pragma unroll
-      for (int x = 0; x < 16 / kRowsAtOnce; ++x) {
+      for (int g = 0; g < kParts; ++g) {
+        const uint8_t* from = (lane < 16 ? p.k_scale : p.v_scale) + a[g].page * p.scale_page_stride + (static_cast<int64_t>(a[g].at) + (lane & 15)) * 4;
+        word[g] = (lane & 15) < a[g].valid ? __ldg(reinterpret_cast<const uint32_t*>(from)) : 0u;
+      }
+    };
+    // `words`: this lane's scale words (of K or of V)
+    auto widen = [&](const uint4 (&us)[kParts][kLoads], const uint32_t (&words)[kParts], bool v, uint32_t to) {
+#pragma unroll
+      for (int gx = 0; gx < kParts * (16 / kRowsAtOnce); ++gx) {
+        const int g = gx / (16 / kRowsAtOnce), x = gx % (16 / kRowsAtOnce);
+        const uint4* u = us[g];
+        const uint32_t word = words[g], out = to + g * 2048 + out_at;
         uint32_t bias = 0;
         if constexpr (G::kU4) {
           // what is no zero-point becomes one: its token counts by its score and its factor, and what is not seen has to
@@ -400,27 +441,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       tc::fence_proxy_async_smem();
     };
 
-    Part cur, ahead;
-    uint4 ku[kLoads], vu[kLoads];
-    uint32_t word = 0;
+    Part cur[kParts], ahead[kParts];
+    uint4 ku[kParts][kLoads], vu[kParts][kLoads];
+    uint32_t words[kParts];
     bool more = step(cur);
     if (more) {
       settle(cur);
       load(cur, p.k, ku);
       load(cur, p.v, vu);
-      word = load_scales(cur);
+      load_scales(cur, words);
       more = step(ahead);
       bool go = true;
       for (uint32_t t = 0; go; ++t) {
         const uint32_t buf = t % kBufs;
         if (t >= kBufs) wait(k_free + 8 * buf, t / kBufs - 1, 0x77);
         dead = __any_sync(0xffffffffu, dead);
-        widen(ku, word, false, base + G::kOffK + buf * G::kOperand);
+        widen(ku, words, false, base + G::kOffK + buf * G::kOperand);
         // The tokens' scales.  Their buffer was last read for tile t - kCols: S of tile t - kBufs is done, and it was issued
         // after every stream's P of the tile before that one.
-        {
-          static_assert(kCols >= kBufs + 1, "buffers of scales");
-          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 4 * kTile + part * 16 + (lane & 15);
+        static_assert(kCols >= kBufs + 1, "buffers of scales");
+#pragma unroll
+        for (int g = 0; g < kParts; ++g) {
+          const uint32_t word = words[g];
+          const int token0 = (part0 + g) * 16;
+          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 4 * kTile + token0 + (lane & 15);
           if (lane < 16) {
             float sk;
             if constexpr (G::kU4)
@@ -439,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
             } else {
               sv = __uint_as_float(vw);
             }
-            if (odd && (lane & 15) < cur.valid) odd_tile[t % kCols] = t + 1;
+            if (odd && (lane & 15) < cur[g].valid) odd_tile[t % kCols] = t + 1;
             col[kTile] = lg2(sv);
             col[2 * kTile] = rcp(sv);
             col[3 * kTile] = factor;
@@ -450,13 +494,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
             uint32_t bad = 0;
 #pragma unroll
             for (int k = 0; k < kLoads; ++k)
-              bad |= (((vu[k].x & 0x7f7f7f7fu) + 0x01010101u) | ((vu[k].y & 0x7f7f7f7fu) + 0x01010101u) |
-                      ((vu[k].z & 0x7f7f7f7fu) + 0x01010101u) | ((vu[k].w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+              bad |= (((vu[g][k].x & 0x7f7f7f7fu) + 0x01010101u) | ((vu[g][k].y & 0x7f7f7f7fu) + 0x01010101u) |
+                      ((vu[g][k].z & 0x7f7f7f7fu) + 0x01010101u) | ((vu[g][k].w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
             if (__any_sync(0xffffffffu, bad != 0)) {
               __syncwarp();
 #pragma unroll
               for (int k = 0; k < kLoads; ++k) {
-                uint32_t* u = &vu[k].x;
+                uint32_t* u = &vu[g][k].x;
                 uint32_t any = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -466,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
                 }
                 const int x = k / kBlocks2 % (16 / kRowsAtOnce);
                 if (any != 0) {
-                  reinterpret_cast<float*>(smem + G::kOffCol)[((t % kCols) * 4 + 3) * kTile + part * 16 + row + x * kRowsAtOnce] =
+                  reinterpret_cast<float*>(smem + G::kOffCol)[((t % kCols) * 4 + 3) * kTile + token0 + row + x * kRowsAtOnce] =
                       __uint_as_float(0x7fc00000u);
                   odd_tile[t % kCols] = t + 1;
                 }
@@ -480,17 +524,20 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
           tc::mbar_arrive(col_full + 8 * (t % kCols));
         }
         go = more;
-        uint32_t word_v = word;
+        uint32_t words_v[kParts];
+#pragma unroll
+        for (int g = 0; g < kParts; ++g) words_v[g] = words[g];
         if (go) {  // the next tile's keys, and where the one after it lies
           settle(ahead);
           load(ahead, p.k, ku);
-          word = load_scales(ahead);
-          cur = ahead;
+          load_scales(ahead, words);
+#pragma unroll
+          for (int g = 0; g < kParts; ++g) cur[g] = ahead[g];
           more = step(ahead);
         }
         if (t >= kBufs) wait(v_free + 8 * buf, t / kBufs - 1, 0x78);
         dead = __any_sync(0xffffffffu, dead);
-        widen(vu, word_v, true, base + G::kOffV + buf * G::kOperand);
+        widen(vu, words_v, true, base + G::kOffV + buf * G::kOperand);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(v_full + 8 * buf);
         if (go) load(cur, p.v, vu);
@@ -498,8 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     }
   } else {
     // ---------------- softmax ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
-    constexpr int kSpan = G::kSpan, kMine = G::kMine;
+    if constexpr (G::kSoftmaxRegs > G::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
+    constexpr int kSpan = G::kSpan, kMine = G::kMine, kChunk = 16;
     const int quad = warp & 3;
     const int stream = kStreams == 2 ? warp >> 2 : 0, sub = kStreams == 2 ? 0 : warp >> 2;
     const int row = quad * 32 + lane;  // of the stream
@@ -515,38 +563,33 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       if constexpr (kSubs > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + quad), "n"(32 * kSubs) : "memory");
     };
 
-    // What is left to do for a segment once its last product is issued, and what its rows are.
-    struct Segment {
-      int64_t token;    // this row of q and out
-      int32_t head;     // query head
-      int32_t at;       // the row's position (of a row that is none: the last one's)
-      int32_t row_tile;
-      bool live, begins, ends;
-    };
-    auto segment = [&]() {
-      Segment g;
+    RowOf* row_of = reinterpret_cast<RowOf*>(smem + G::kOffRow) + threadIdx.x;  // [2 x 256]
+    WarpRows& wr = reinterpret_cast<WarpRows*>(smem + G::kOffWarp)[warp];
+    // The segment that the walk stands at; returns the row's position (of a row that is none: the last one's).
+    auto segment = [&](int parity) {
       const int64_t r = static_cast<int64_t>(w.row_tile) * kRows + stream * 128 + row;
-      g.live = r < w.s.rows;
-      const int32_t node = static_cast<int32_t>(min(r, w.s.rows - 1) / p.group);
-      g.token = w.s.q_row + node;
-      g.head = w.head * p.group + static_cast<int32_t>(min(r, w.s.rows - 1) - static_cast<int64_t>(node) * p.group);
-      g.at = w.s.ctx + node;
-      g.row_tile = w.row_tile;
-      g.begins = w.begins();
-      g.ends = w.ends();
-      if (threadIdx.x == 0 && g.begins && !g.ends) p.records[blockIdx.x] = record_of(w, blocks, total);
-      return g;
+      const int64_t at = min(r, w.s.rows - 1);
+      const int32_t node = static_cast<int32_t>(at / p.group);
+      RowOf o;
+      o.token = r < w.s.rows ? w.s.q_row + node : -1;
+      o.head = w.head * p.group + static_cast<int32_t>(at - static_cast<int64_t>(node) * p.group);
+      o.flags = (w.begins() ? 1 : 0) | (w.ends() ? 2 : 0);
+      row_of[parity * 256] = o;
+      if (threadIdx.x == 0 && o.flags == 1)
+        p.records[blockIdx.x] = record_of(w, min(static_cast<int64_t>(gridDim.x), scan[kWarps]), scan[kWarps]);
+      return w.s.ctx + node;
     };
 
     // q of this thread's part of the row, scaled by a power of two, into shared memory; the factor to undo it
-    auto stage_q = [&](const Segment& g, float& row_scale) {
+    auto stage_q = [&](int parity, float& row_scale) {
+      const RowOf g = row_of[parity * 256];
       uint4 raw[kMine / 8];
       uint32_t top = 0;
       const bool bf16 = p.dtype == QLIN_BF16;
       const uint8_t* src = p.q + g.token * p.qt + g.head * p.qh + sub * kMine * 2;
 #pragma unroll
       for (int k = 0; k < kMine / 8; ++k) {
-        raw[k] = g.live ? ldg_v4(src + k * 16) : make_uint4(0u, 0u, 0u, 0u);
+        raw[k] = g.token >= 0 ? ldg_v4(src + k * 16) : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
         if (bf16) {
 #pragma unroll
@@ -591,29 +634,29 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
     };
 
     uint32_t t = 0;
+    int parity = 0;
     bool more = next(w);
-    Segment g = segment();
+    int32_t at = segment(0);
     float row_scale;
-    stage_q(g, row_scale);
+    stage_q(0, row_scale);
     const float cap2 = SHAPED ? p.softcap * kLog2e : 0.0f;
     while (more) {
       float ref = kNoRef;
       uint64_t l2 = pair(0.0f, 0.0f);
       bool begun = false;
-      const Stream rows = stream_of(p, w, stream);
-      // of this warp's rows
-      const int32_t first = __shfl_sync(0xffffffffu, g.at, 0), last = __shfl_sync(0xffffffffu, g.at, 31);
+      {
+        const int32_t first = __shfl_sync(0xffffffffu, at, 0), last = __shfl_sync(0xffffffffu, at, 31);
+        if (lane == 0) wr = {stream_of(p, w, stream), first, last};
+        __syncwarp();
+      }
       const bool scaled = !__all_sync(0xffffffffu, row_scale == 1.0f);
       float slope2 = 0.0f;
-      if constexpr (SHAPED) slope2 = p.slopes != nullptr ? -kLog2e * p.slopes[g.head] : 0.0f;
-      // where a moved reference puts the row's largest probability: with more tiles to come, six bits below the
-      // top of fp16, which it may grow by before the row has to be rescaled
-      const float put = w.tiles > 1 ? 9.0f : kOffset;
+      if constexpr (SHAPED) slope2 = p.slopes != nullptr ? -kLog2e * p.slopes[row_of[parity * 256].head] : 0.0f;
       for (int i = 0; i < w.tiles; ++i, ++t) {
         const uint32_t step = t * kStreams + stream, buf = step & 1;
         const int j0 = w.seen.at(w.tile + i) * kTile;
         wait(s_full + 8 * buf, step >> 1, 0x79);
-        if (!sees(p, rows, w.s.prefix, j0)) {  // nothing was multiplied and nothing will be
+        if (!sees(p, wr.rows, w.s.prefix, j0)) {  // nothing was multiplied and nothing will be
           if (lane == 0) tc::mbar_arrive(p_full + 8 * buf);
           continue;
         }
@@ -622,16 +665,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
         tc::tc_fence_after();
         const bool odd = odd_tile[t % kCols] == t + 1;
         const int jc = j0 + sub * kSpan;
-        const bool all = (j0 + kTile - 1 <= first && (p.window == 0 || j0 > last - p.window)) || j0 + kTile <= w.s.prefix;
+        const bool all = (j0 + kTile - 1 <= wr.first && (p.window == 0 || j0 > wr.last - p.window)) || j0 + kTile <= w.s.prefix;
         const uint32_t s_at = lanes + buf * 128 + sub * kSpan;
-        const float* col = reinterpret_cast<const float*>(smem + G::kOffCol) + (t % kCols) * 4 * kTile + sub * kSpan;
+        const uint32_t col = base + G::kOffCol + ((t % kCols) * 4 * kTile + sub * kSpan) * 4;
 
-        // t of 32 tokens from column k0 on, from their products
-        auto score = [&](uint32_t (&v)[32], int k0) {
+        // t of kChunk tokens from column k0 on, from their products
+        auto score = [&](uint32_t (&v)[kChunk], int k0) {
           if (scaled) {
             const uint64_t rs = pair(row_scale, row_scale);
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
+            for (int k = 0; k < kChunk; k += 2) {
               const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rs));
               v[k] = __float_as_uint(a.x);
               v[k + 1] = __float_as_uint(a.y);
@@ -639,9 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
           }
           if (SHAPED && cap2 > 0.0f) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 sk = *reinterpret_cast<const float4*>(col + k0 + k);
-              const float4 ls = *reinterpret_cast<const float4*>(col + kTile + k0 + k);
+            for (int k = 0; k < kChunk; k += 4) {
+              const float4 sk = lds4(col + 4 * (k0 + k));
+              const float4 ls = lds4(col + 4 * (kTile + k0 + k));
               const float ks[4] = {sk.x, sk.y, sk.z, sk.w}, lv[4] = {ls.x, ls.y, ls.z, ls.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -651,9 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 sk = *reinterpret_cast<const float4*>(col + k0 + k);
-              const float4 ls = *reinterpret_cast<const float4*>(col + kTile + k0 + k);
+            for (int k = 0; k < kChunk; k += 4) {
+              const float4 sk = lds4(col + 4 * (k0 + k));
+              const float4 ls = lds4(col + 4 * (kTile + k0 + k));
               const float2 a = unpair(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y), pair(ls.x, ls.y)));
               const float2 b =
                   unpair(fma2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), pair(sk.z, sk.w), pair(ls.z, ls.w)));
@@ -664,24 +707,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
             }
           }
           if (SHAPED && p.slopes != nullptr) {
-            const float off = static_cast<float>(jc + k0 - g.at);  // exact below 2^24
+            const float off = static_cast<float>(jc + k0 - at);  // exact below 2^24
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
+            for (int k = 0; k < kChunk; ++k)
               v[k] = __float_as_uint(fmaf(slope2, fabsf(off + static_cast<float>(k)), __uint_as_float(v[k])));
           }
           if (!all) {
-            uint32_t bits = low_bits(g.at + 1 - jc - k0);
-            if (p.window > 0) bits &= ~low_bits(g.at - p.window + 1 - jc - k0);
+            uint32_t bits = low_bits(at + 1 - jc - k0);
+            if (p.window > 0) bits &= ~low_bits(at - p.window + 1 - jc - k0);
             bits |= low_bits(w.s.prefix - jc - k0);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
+            for (int k = 0; k < kChunk; ++k)
               if (!((bits >> k) & 1u)) v[k] = 0xff800000u;
           }
         };
-        auto largest = [&](const uint32_t (&v)[32], float hi) {
+        auto largest = [&](const uint32_t (&v)[kChunk], float hi) {
           float m[4] = {hi, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
+          for (int k = 0; k < kChunk; k += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1])));
           return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
@@ -701,7 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
         bool moved = false;
         auto move = [&](float hi) {  // the reference, where P would grow too large
           const bool far = hi > ref + (kOffset + kSlack);
-          const float to = far ? hi - put : ref;
+          // with more tiles to come, a moved reference puts the row's largest probability six bits below the top of fp16,
+          // which it may grow by before the row has to be rescaled
+          const float to = far ? hi - (w.tiles > 1 ? 9.0f : kOffset) : ref;
           const float k = ex2(ref - to);
           ref = to;
           keep *= k;
@@ -709,12 +754,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
           return __any_sync(0xffffffffu, far);  // (the same in all warps of these rows)
         };
 
-        uint32_t va[32], vb[32], pk[kSpan / 2];
+        uint32_t va[kChunk], vb[kChunk], pk[kSpan / 2];
         if (!begun) {  // no reference yet: the maximum alone
           float hi = -INFINITY;
 #pragma unroll
-          for (int k0 = 0; k0 < kSpan; k0 += 32) {
-            tc::tmem_ld_32x32b_x32(s_at + k0, va);
+          for (int k0 = 0; k0 < kSpan; k0 += kChunk) {
+            tc::tmem_ld_32x32b_x16(s_at + k0, va);
             tc::tmem_wait_ld(va);
             score(va, k0);
             hi = largest(va, hi);
@@ -726,12 +771,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
           uint64_t sum = l2;
           float hi = -INFINITY;
           const uint64_t nref = pair(-ref, -ref);
-          auto weigh = [&](uint32_t (&v)[32], int k0, auto with_factors) {
+          auto weigh = [&](uint32_t (&v)[kChunk], int k0, auto with_factors) {
             score(v, k0);
             hi = largest(v, hi);
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 rv = *reinterpret_cast<const float4*>(col + 2 * kTile + k0 + k);
+            for (int k = 0; k < kChunk; k += 4) {
+              const float4 rv = lds4(col + 4 * (2 * kTile + k0 + k));
               const float rr[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
               for (int x = 0; x < 4; x += 2) {
@@ -739,23 +784,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
                 float2 f = make_float2(ex2(a.x), ex2(a.y));
                 sum = fma2(pair(f.x, f.y), pair(rr[x], rr[x + 1]), sum);
                 if constexpr (decltype(with_factors)::value) {  // (what is hidden has no product with a factor that is not a number)
-                  f.x = v[k + x] == 0xff800000u ? 0.0f : f.x * col[3 * kTile + k0 + k + x];
-                  f.y = v[k + x + 1] == 0xff800000u ? 0.0f : f.y * col[3 * kTile + k0 + k + x + 1];
+                  f.x = v[k + x] == 0xff800000u ? 0.0f : f.x * lds1(col + 4 * (3 * kTile + k0 + k + x));
+                  f.y = v[k + x + 1] == 0xff800000u ? 0.0f : f.y * lds1(col + 4 * (3 * kTile + k0 + k + x + 1));
                 }
                 pk[(k0 + k + x) / 2] = kv::pack2<0>(f.x, f.y);
               }
             }
           };
           auto pass = [&](auto with_factors) {
-            tc::tmem_ld_32x32b_x32(s_at, va);
+            tc::tmem_ld_32x32b_x16(s_at, va);
 #pragma unroll
-            for (int k0 = 0; k0 < kSpan; k0 += 64) {  // the next 32 on their way while these are weighed
+            for (int k0 = 0; k0 < kSpan; k0 += 2 * kChunk) {  // the next ones on their way while these are weighed
               tc::tmem_wait_ld(va);
-              tc::tmem_ld_32x32b_x32(s_at + k0 + 32, vb);
+              tc::tmem_ld_32x32b_x16(s_at + k0 + kChunk, vb);
               weigh(va, k0, with_factors);
               tc::tmem_wait_ld(vb);
-              if (k0 + 64 < kSpan) tc::tmem_ld_32x32b_x32(s_at + k0 + 64, va);
-              weigh(vb, k0 + 32, with_factors);
+              if (k0 + 2 * kChunk < kSpan) tc::tmem_ld_32x32b_x16(s_at + k0 + 2 * kChunk, va);
+              weigh(vb, k0 + kChunk, with_factors);
             }
           };
           if (odd) pass(std::true_type{});
@@ -797,14 +842,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       }
 
       // the next segment's q, then this one's output
-      const Segment done = g;
+      const bool live = wr.rows.live;
       const float2 lp = unpair(l2);
       float l = lp.x + lp.y;
       if constexpr (kSubs > 1) ends[sub * 128 + row] = l;
       more = next(w);
       if (more) {
-        g = segment();
-        stage_q(g, row_scale);
+        at = segment(parity ^ 1);
+        stage_q(parity ^ 1, row_scale);
       }
       if constexpr (kSubs > 1) {
         sync_rows();
@@ -814,12 +859,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
       wait(pv_done + 8 * (ended & 1), ended >> 1, 0x7c);
       dead = __any_sync(0xffffffffu, dead);
       tc::tc_fence_after();
-      const bool whole = done.begins && done.ends;
+      const RowOf done = row_of[parity * 256];
+      parity ^= 1;
+      const bool whole = done.flags == 3;
       const bool none = ref == kNoRef;  // (O then holds anything)
       const float inv = !whole ? 1.0f : __frcp_rn(l);
       const float m = none ? -INFINITY : ref + kOffset;
-      const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (done.begins ? 1 : 0)) * p.tile_rows + stream * 128 + row;
-      if (rows.live) {
+      const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (done.flags & 1)) * p.tile_rows + stream * 128 + row;
+      if (live) {
 #pragma unroll 1
         for (int cc = 0; cc < kMine; cc += 16) {
           uint32_t o[16];
@@ -833,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
             const int ch = G::kU4 ? (k & 8) + ((k & 7) >> 1) + 4 * (k & 1) : k;
             f[ch] = none ? 0.0f : __uint_as_float(o[k]) * inv;
           }
-          if (!done.live) continue;
+          if (done.token < 0) continue;
           const int ch = sub * kMine + cc;
           if (whole) {
             uint8_t* out = p.out + done.token * p.ot + done.head * p.oh + ch * 2;
@@ -847,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attention_kernel(const __gr
           }
         }
       }
-      if (done.live && sub == 0) {
+      if (done.token >= 0 && sub == 0) {
         if (!whole) p.part_ml[slot] = make_float2(m, l);
         else if (p.lse != nullptr) p.lse[done.token * p.hq + done.head] = (lg2(l) + ref) * kLn2;
       }
@@ -923,7 +970,7 @@ cudaError_t plan(const Params& p, Prepared* out) {
   if (e != cudaSuccess) return e;
   const uint32_t blocks = static_cast<uint32_t>(sm_count());
   out->count = 2;
-  out->launch[0] = {fn, blocks, 1, kThreads, Geo<FMT, D>::kSmem};
+  out->launch[0] = {fn, blocks, 1, Geo<FMT, D>::kThreads, Geo<FMT, D>::kSmem};
   out->launch[1] = {reinterpret_cast<const void*>(chunk_attention_join_kernel<D>), blocks,
                     static_cast<uint32_t>((p.tile_rows + 7) / 8), 128, 0};
   out->set(p);
