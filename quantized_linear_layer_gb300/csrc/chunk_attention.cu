@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           const uint64_t vd = v_desc + vb * (G::kOperand >> 4);
           const uint32_t pt = tmem + buf * 128, ot = tmem + kTmemO + x * G::kOCols;
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) tc::mma_f16_ta(ot, pt + 8 * k, vd + k * 128, idesc_o, !pend_first || k > 0 ? 1u : 0u);
+          for (int k = 0; k < kTile / 16; ++k)  // P of 64 tokens lies over the first half of their scores
+            tc::mma_f16_ta(ot, pt + 64 * (k >> 2) + 8 * (k & 3), vd + k * 128, idesc_o, !pend_first || k > 0 ? 1u : 0u);
         }
         tc::mma_commit(pv_done + 8 * buf);
         if (x == kStreams - 1) tc::mma_commit(v_free + 8 * vb);
@@ -547,7 +548,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
     // ---------------- softmax ----------------
     if constexpr (G::kSoftmaxRegs > G::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
-    constexpr int kSpan = G::kSpan, kMine = G::kMine, kChunk = 16;
+    constexpr int kSpan = G::kSpan, kMine = G::kMine;
+    constexpr int kStep = 64;  // tokens weighed at a time
     const int quad = warp & 3;
     const int stream = kStreams == 2 ? warp >> 2 : 0, sub = kStreams == 2 ? 0 : warp >> 2;
     const int row = quad * 32 + lane;  // of the stream
@@ -669,12 +671,12 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         const uint32_t s_at = lanes + buf * 128 + sub * kSpan;
         const uint32_t col = base + G::kOffCol + ((t % kCols) * 4 * kTile + sub * kSpan) * 4;
 
-        // t of kChunk tokens from column k0 on, from their products
-        auto score = [&](uint32_t (&v)[kChunk], int k0) {
+        // t of kStep tokens from column k0 on, from their products
+        auto score = [&](uint32_t (&v)[kStep], int k0) {
           if (scaled) {
             const uint64_t rs = pair(row_scale, row_scale);
 #pragma unroll
-            for (int k = 0; k < kChunk; k += 2) {
+            for (int k = 0; k < kStep; k += 2) {
               const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rs));
               v[k] = __float_as_uint(a.x);
               v[k + 1] = __float_as_uint(a.y);
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           }
           if (SHAPED && cap2 > 0.0f) {
 #pragma unroll
-            for (int k = 0; k < kChunk; k += 4) {
+            for (int k = 0; k < kStep; k += 4) {
               const float4 sk = lds4(col + 4 * (k0 + k));
               const float4 ls = lds4(col + 4 * (kTile + k0 + k));
               const float ks[4] = {sk.x, sk.y, sk.z, sk.w}, lv[4] = {ls.x, ls.y, ls.z, ls.w};
@@ -694,7 +696,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < kChunk; k += 4) {
+            for (int k = 0; k < kStep; k += 4) {
               const float4 sk = lds4(col + 4 * (k0 + k));
               const float4 ls = lds4(col + 4 * (kTile + k0 + k));
               const float2 a = unpair(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y), pair(ls.x, ls.y)));
@@ -709,112 +711,89 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           if (SHAPED && p.slopes != nullptr) {
             const float off = static_cast<float>(jc + k0 - at);  // exact below 2^24
 #pragma unroll
-            for (int k = 0; k < kChunk; ++k)
+            for (int k = 0; k < kStep; ++k)
               v[k] = __float_as_uint(fmaf(slope2, fabsf(off + static_cast<float>(k)), __uint_as_float(v[k])));
           }
           if (!all) {
-            uint32_t bits = low_bits(at + 1 - jc - k0);
-            if (p.window > 0) bits &= ~low_bits(at - p.window + 1 - jc - k0);
-            bits |= low_bits(w.s.prefix - jc - k0);
 #pragma unroll
-            for (int k = 0; k < kChunk; ++k)
-              if (!((bits >> k) & 1u)) v[k] = 0xff800000u;
+            for (int k1 = 0; k1 < kStep; k1 += 32) {
+              const int c = jc + k0 + k1;
+              uint32_t bits = low_bits(at + 1 - c);
+              if (p.window > 0) bits &= ~low_bits(at - p.window + 1 - c);
+              bits |= low_bits(w.s.prefix - c);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((bits >> k) & 1u)) v[k1 + k] = 0xff800000u;
+            }
           }
         };
-        auto largest = [&](const uint32_t (&v)[kChunk], float hi) {
-          float m[4] = {hi, -INFINITY, -INFINITY, -INFINITY};
+        float keep = 1.0f;
+#pragma unroll 1
+        for (int k0 = 0; k0 < kSpan; k0 += kStep) {
+          uint32_t v[kStep];
+          tc::tmem_ld_32x32b_x32(s_at + k0, v);
+          tc::tmem_ld_32x32b_x32(s_at + k0 + 32, v + 32);
+          tc::tmem_wait_ld(v);
+          score(v, k0);
+          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < kChunk; k += 8)
+          for (int k = 0; k < kStep; k += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1])));
-          return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-        };
-        // over all threads of the row
-        int rounds = 0;
-        auto of_row = [&](float hi) {
-          if constexpr (kSubs > 1) {
-            float* maxima = row_max + (rounds++ & 1) * kSubs * 128 + row;
+          float hi = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+          if constexpr (kSubs > 1) {  // over both threads of the row; and both have their scores: P may go over them
+            float* maxima = row_max + (t & 1) * kSubs * 128 + row;
             maxima[sub * 128] = hi;
             sync_rows();
             hi = fmaxf(hi, maxima[(sub ^ 1) * 128]);
           }
-          return hi;
-        };
-        float keep = 1.0f;
-        bool moved = false;
-        auto move = [&](float hi) {  // the reference, where P would grow too large
-          const bool far = hi > ref + (kOffset + kSlack);
-          // with more tiles to come, a moved reference puts the row's largest probability six bits below the top of fp16,
-          // which it may grow by before the row has to be rescaled
-          const float to = far ? hi - (w.tiles > 1 ? 9.0f : kOffset) : ref;
-          const float k = ex2(ref - to);
-          ref = to;
-          keep *= k;
-          l2 = mul2(l2, pair(k, k));
-          return __any_sync(0xffffffffu, far);  // (the same in all warps of these rows)
-        };
-
-        uint32_t va[kChunk], vb[kChunk], pk[kSpan / 2];
-        if (!begun) {  // no reference yet: the maximum alone
-          float hi = -INFINITY;
+          if (__any_sync(0xffffffffu, hi > ref + (kOffset + kSlack))) {  // (the same in all warps of these rows)
+            // The reference moves, by a whole number of powers of two, so that the row's probabilities of this tile that are
+            // written already can be scaled in fp16.  With more tiles to come its largest one goes six bits below the top of
+            // fp16, which it may grow by before the row has to be rescaled.
+            const float to = hi > ref + (kOffset + kSlack) ? ceilf(hi) - (w.tiles > 1 ? 9.0f : kOffset) : ref;
+            const float f = ex2(ref - to);
+            ref = to;
+            keep *= f;
+            l2 = mul2(l2, pair(f, f));
+            const __half2 h = __float2half2_rn(f);
+#pragma unroll 1
+            for (int c = 0; c < k0; c += kStep) {
+#pragma unroll 1
+              for (int x = 0; x < kStep / 2; x += 16) {
+                uint32_t o[16];
+                tc::tmem_ld_32x32b_x16(s_at + c + x, o);
+                tc::tmem_wait_ld(o);
 #pragma unroll
-          for (int k0 = 0; k0 < kSpan; k0 += kChunk) {
-            tc::tmem_ld_32x32b_x16(s_at + k0, va);
-            tc::tmem_wait_ld(va);
-            score(va, k0);
-            hi = largest(va, hi);
+                for (int k = 0; k < 16; ++k) o[k] = hmul2(o[k], *reinterpret_cast<const uint32_t*>(&h));
+                tc::tmem_st_32x32b_x16(s_at + c + x, o);
+              }
+            }
           }
-          move(of_row(hi));
-        }
-        // P with the reference as it is; where a score lies far above it, once more with a new one
-        while (true) {
-          uint64_t sum = l2;
-          float hi = -INFINITY;
           const uint64_t nref = pair(-ref, -ref);
-          auto weigh = [&](uint32_t (&v)[kChunk], int k0, auto with_factors) {
-            score(v, k0);
-            hi = largest(v, hi);
+          auto weigh = [&](auto with_factors) {
 #pragma unroll
-            for (int k = 0; k < kChunk; k += 4) {
+            for (int k = 0; k < kStep; k += 4) {
               const float4 rv = lds4(col + 4 * (2 * kTile + k0 + k));
               const float rr[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
               for (int x = 0; x < 4; x += 2) {
                 const float2 a = unpair(add2(pair(__uint_as_float(v[k + x]), __uint_as_float(v[k + x + 1])), nref));
                 float2 f = make_float2(ex2(a.x), ex2(a.y));
-                sum = fma2(pair(f.x, f.y), pair(rr[x], rr[x + 1]), sum);
+                l2 = fma2(pair(f.x, f.y), pair(rr[x], rr[x + 1]), l2);
                 if constexpr (decltype(with_factors)::value) {  // (what is hidden has no product with a factor that is not a number)
                   f.x = v[k + x] == 0xff800000u ? 0.0f : f.x * lds1(col + 4 * (3 * kTile + k0 + k + x));
                   f.y = v[k + x + 1] == 0xff800000u ? 0.0f : f.y * lds1(col + 4 * (3 * kTile + k0 + k + x + 1));
                 }
-                pk[(k0 + k + x) / 2] = kv::pack2<0>(f.x, f.y);
+                v[(k + x) / 2] = kv::pack2<0>(f.x, f.y);
               }
             }
           };
-          auto pass = [&](auto with_factors) {
-            tc::tmem_ld_32x32b_x16(s_at, va);
-#pragma unroll
-            for (int k0 = 0; k0 < kSpan; k0 += 2 * kChunk) {  // the next ones on their way while these are weighed
-              tc::tmem_wait_ld(va);
-              tc::tmem_ld_32x32b_x16(s_at + k0 + kChunk, vb);
-              weigh(va, k0, with_factors);
-              tc::tmem_wait_ld(vb);
-              if (k0 + 2 * kChunk < kSpan) tc::tmem_ld_32x32b_x16(s_at + k0 + 2 * kChunk, va);
-              weigh(vb, k0 + kChunk, with_factors);
-            }
-          };
-          if (odd) pass(std::true_type{});
-          else pass(std::false_type{});
-          if (!move(of_row(hi))) {
-            l2 = sum;
-            break;
-          }
-          moved = true;
+          if (odd) weigh(std::true_type{});
+          else weigh(std::false_type{});
+          tc::tmem_st_32x32b_x32(s_at + k0, v);  // over the first half of its scores
         }
-        // over the scores, which this row's threads have all read
-#pragma unroll
-        for (int k = 0; k < kSpan / 2; k += 32) tc::tmem_st_32x32b_x32(lanes + buf * 128 + sub * kSpan / 2 + k, pk + k);
-        if (moved && begun) {
+        if (__any_sync(0xffffffffu, keep != 1.0f) && begun) {  // (NaN too)
           const uint32_t before = step - kStreams;
           wait(pv_done + 8 * (before & 1), before >> 1, 0x7b);
           dead = __any_sync(0xffffffffu, dead);
