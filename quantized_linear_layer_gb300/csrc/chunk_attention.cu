@@ -57,7 +57,7 @@ struct Geo {
   static constexpr bool kU4 = FMT == QLIN_KV_U4;
   static constexpr int kStreams = D == 256 ? 1 : 2;
   static constexpr int kSubs = 2 / kStreams;  // threads of a row
-  static constexpr int kSpan = kTile / kSubs;  // tokens of each
+  static constexpr int kHalves = kStreams;     // a thread takes a tile's scores 64 at a time
   static constexpr int kMine = D / kSubs;      // channels of q and o of each
   static constexpr int kRows = 128 * kStreams;
   static constexpr int kBufs = D == 256 ? 1 : 2;  // of K and of V
@@ -65,7 +65,7 @@ struct Geo {
   static constexpr int kWidenWarps = 4, kMmaWarp = kSoftmaxWarps + kWidenWarps;
   static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps;
   static constexpr int kLaunchRegs = 128;
-  static constexpr int kSoftmaxRegs = D == 256 ? 112 : 160, kWidenRegs = D == 256 ? 232 : 144, kOtherRegs = 48;
+  static constexpr int kSoftmaxRegs = D == 256 ? 104 : 120, kWidenRegs = D == 256 ? 232 : 200, kOtherRegs = 64;
   static_assert(kSoftmaxWarps * kSoftmaxRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kWarps * kLaunchRegs, "registers");
   static constexpr int kParts = kTile / 16 / kWidenWarps;  // 16 tokens each, of a widening warp
   static constexpr int kRowBytes = kU4 ? D / 2 : D;
@@ -80,9 +80,8 @@ struct Geo {
   static constexpr int kOffQmax = kOffPair + 2 * kSubs * 128 * 4;      // [thread of the row][row]
   static constexpr int kOffEnd = kOffQmax + kSubs * 128 * 4;           // [thread of the row][row] l
   static constexpr int kOffRow = kOffEnd + kSubs * 128 * 4;                          // [segment parity][softmax thread] RowOf
-  static constexpr int kOffWarp = kOffRow + 2 * 32 * kSoftmaxWarps * 16;             // [softmax warp, stream of the products] WarpRows
-  static constexpr int kOffBar = kOffWarp + (kSoftmaxWarps + 2) * 32;
-  static constexpr int kBars = 4 * kBufs + 6 + kStreams + 1 + kCols;
+  static constexpr int kOffBar = kOffRow + 2 * 32 * kSoftmaxWarps * 16;
+  static constexpr int kBars = 4 * kBufs + 2 + 4 + 4 + kStreams + 1 + kCols;
   static constexpr int kOffMisc = kOffBar + kBars * 8;  // tensor memory address, flags
   static constexpr int kOffScan = (kOffMisc + 32 + 7) / 8 * 8;
   static constexpr int kOffWalk = (kOffScan + (kWarps + 1) * 8 + 15) / 16 * 16;
@@ -91,37 +90,36 @@ struct Geo {
   static_assert(kTmemO + kStreams * kOCols <= 512, "tensor memory");
 };
 
-// The rows of a stream of a segment, as its roles need them.
-struct Stream {
-  int32_t first, last;  // positions of its first and last row
-  bool live;            // any row at all
+// Tokens that are of the prefix, or from `low` to `high`.
+struct Range {
+  int32_t prefix, low, high;
 };
 
+// The first tokens of the spans of `width` that some row of positions first .. last sees a token of (none if there is no row).
+__device__ __forceinline__ Range some_seen(const Params& p, const Sequence& s, int32_t first, int32_t last, int32_t width, bool live) {
+  return {live ? s.prefix : 0, p.window > 0 ? first - p.window + 2 - width : INT32_MIN, live ? last : -1};
+}
+// The first tokens of the spans of `width` that all these rows see all of.
+__device__ __forceinline__ Range all_seen(const Params& p, const Sequence& s, int32_t first, int32_t last, int32_t width) {
+  return {s.prefix - width + 1, p.window > 0 ? last - p.window + 1 : INT32_MIN, first - width + 1};
+}
+__device__ __forceinline__ bool within(const Range& r, int32_t j) { return j < r.prefix || (j >= r.low && j <= r.high); }
+
+// That of a stream (its 128 rows of a row tile) for a tile.
 template <int ROWS>
-__device__ __forceinline__ Stream stream_of(const Params& p, const Walk<ROWS>& w, int x) {
+__device__ __forceinline__ Range stream_sees(const Params& p, const Walk<ROWS>& w, int x) {
   const int64_t row = static_cast<int64_t>(w.row_tile) * ROWS + x * 128;
-  Stream s;
-  s.live = row < w.s.rows;
-  s.first = w.s.ctx + static_cast<int32_t>(min(row, w.s.rows - 1) / p.group);
-  s.last = w.s.ctx + static_cast<int32_t>(min(row + 127, w.s.rows - 1) / p.group);
-  return s;
+  const int32_t first = w.s.ctx + token_of(p, min(row, w.s.rows - 1)), last = w.s.ctx + token_of(p, min(row + 127, w.s.rows - 1));
+  return some_seen(p, w.s, first, last, kTile, row < w.s.rows);
 }
 
-// What a softmax thread and its warp know of a segment, kept in shared memory: in registers it would take the scores'.
+// What a softmax thread knows of a segment until it writes its row, kept in shared memory: in registers it would take the
+// scores'.
 struct RowOf {
   int64_t token;  // the row of q and out; -1: none
   int32_t head;   // query head
   int32_t flags;  // 1: the segment begins in this block, 2: it ends in it
 };
-struct WarpRows {
-  Stream rows;
-  int32_t first, last;  // positions of the warp's first and last row
-};
-
-// Whether any row of the stream sees any token of the tile that begins at j0.
-__device__ __forceinline__ bool sees(const Params& p, const Stream& s, int32_t prefix, int32_t j0) {
-  return s.live && (j0 < prefix || (j0 <= s.last && (p.window == 0 || j0 + kTile > s.first - p.window + 1)));
-}
 
 // Loads that stay where they are written: moved ahead of their use, they would take the registers that the scores need.
 __device__ __forceinline__ float4 lds4(uint32_t at) {
@@ -137,6 +135,19 @@ __device__ __forceinline__ float lds1(uint32_t at) {
 
 // Bits 0 .. n - 1.
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// tc::mbar_wait_quiet in fewer instructions: the loops of all roles have to stay in the instruction cache together.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, int32_t* err, int site) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  uint32_t tries = 0;
+#pragma unroll 1
+  do {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+  } while ((++tries & 255) != 0 || clock64() - t0 <= tc::kWaitTimeoutCycles);
+  record_device_error(err, kDevErrTimeoutBase + site);
+  return false;
+}
 
 struct WaitOps {  // for stage_ring.h's wait_or_raise
   volatile uint32_t* flag;
@@ -157,8 +168,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
   const uint32_t bars = base + G::kOffBar;
   const uint32_t k_full = bars, k_free = k_full + 8 * kBufs;                       // [kBufs]
   const uint32_t v_full = k_free + 8 * kBufs, v_free = v_full + 8 * kBufs;         // [kBufs]
-  const uint32_t s_full = v_free + 8 * kBufs, p_full = s_full + 16, pv_done = p_full + 16;  // [2]
-  const uint32_t q_full = pv_done + 16;             // [kStreams]
+  // two streams: S of stream x, P and P u of its half h at 2 x + h; one stream: of two buffers in turn
+  const uint32_t s_full = v_free + 8 * kBufs, p_full = s_full + 16, pv_done = p_full + 32;  // [2], [4], [4]
+  const uint32_t q_full = pv_done + 32;  // [kStreams]
   const uint32_t all_done = q_full + 8 * kStreams;
   const uint32_t col_full = all_done + 8;           // [kCols]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
@@ -174,8 +186,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
       tc::mbar_init(v_full + 8 * i, kWidenWarps);
       tc::mbar_init(v_free + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(s_full + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(s_full + 8 * i, 1);
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(p_full + 8 * i, kSoftmaxWarps / kStreams);
       tc::mbar_init(pv_done + 8 * i, 1);
     }
@@ -212,7 +224,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
   bool dead = false;
   WaitOps ops = {ran_out};
   auto wait = [&](uint32_t bar, uint32_t parity, int site) {
-    ring::wait_or_raise(ops, dead, [&]() { return tc::mbar_wait_quiet(bar, parity & 1, p.err, site); });
+    ring::wait_or_raise(ops, dead, [&]() { return wait_on(bar, parity & 1, p.err, site); });
   };
   // One lane steps a walk in shared memory.
   auto next = [&](W& w) {
@@ -234,68 +246,95 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
     const uint64_t q_desc = tc::sw128_kmajor_desc(base + G::kOffQ), k_desc = tc::sw128_kmajor_desc(base + G::kOffK);
     const uint64_t v_desc = sw128_nmajor_desc(base + G::kOffV, 16384);
     W& w = *origin;  // (nobody else reads it once all have their own)
-    WarpRows* wr = reinterpret_cast<WarpRows*>(smem + G::kOffWarp) + kSoftmaxWarps;
-    uint32_t t = 0, seg = 0;
-    // P u of the step before is issued behind S of this one: whether it has any product, and whether it is its segment's first
-    bool pending = false, pend_on = false, pend_first = false;
-    auto second = [&](uint32_t step) {
-      const uint32_t buf = step & 1, x = step % kStreams, tile = step / kStreams, vb = tile % kBufs;
-      wait(p_full + 8 * buf, step >> 1, 0x71);
-      if (x == 0) wait(v_full + 8 * vb, tile / kBufs, 0x72);
-      dead = __any_sync(0xffffffffu, dead);
-      tc::tc_fence_after();
-      if (leader) {
-        if (!dead && pend_on) {
-          const uint64_t vd = v_desc + vb * (G::kOperand >> 4);
-          const uint32_t pt = tmem + buf * 128, ot = tmem + kTmemO + x * G::kOCols;
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)  // P of 64 tokens lies over the first half of their scores
-            tc::mma_f16_ta(ot, pt + 64 * (k >> 2) + 8 * (k & 3), vd + k * 128, idesc_o, !pend_first || k > 0 ? 1u : 0u);
-        }
-        tc::mma_commit(pv_done + 8 * buf);
-        if (x == kStreams - 1) tc::mma_commit(v_free + 8 * vb);
-      }
-      __syncwarp();
-    };
     asm volatile("bar.sync 6, %0;" ::"n"(32 * (kSoftmaxWarps + kWidenWarps + 1)) : "memory");
-    while (next(w)) {
-      if (lane < kStreams) wr[lane].rows = stream_of(p, w, lane);
-      __syncwarp();
-      uint32_t begun = 0;
-      for (int i = 0; i < w.tiles; ++i, ++t) {
-        const int j0 = w.seen.at(w.tile + i) * kTile;
+    // Steps (tile, stream), in this order.  Two streams: P u of the stream's tile before (the first 64 tokens as soon as their P
+    // is there), then S of this one, over P's columns.  One stream: S of this tile, then P u of the one before, which the
+    // softmax threads have turned into P meanwhile.
+    uint32_t step = 0, seg = 0;
+    uint32_t on = 0, begun = 0, firsts = 0;  // of the streams' last tiles: whether they have products; whether P u begins O
+    int left = 0, i = 0, prefix_tiles = 0, next_tile = 0;
+    Range seen0 = {}, seen1 = {};  // of the streams
+    auto second = [&](uint32_t x, uint32_t t) {
+      const uint32_t vb = t % kBufs;
+#pragma unroll 1
+      for (uint32_t h = 0; h < static_cast<uint32_t>(G::kHalves); ++h) {
+        const uint32_t bar = kStreams == 2 ? 2 * x + h : t & 1, phase = kStreams == 2 ? t : t >> 1;
+        wait(p_full + 8 * bar, phase, 0x71);
+        if (x == 0 && h == 0) wait(v_full + 8 * vb, t / kBufs, 0x72);
+        dead = __any_sync(0xffffffffu, dead);
+        tc::tc_fence_after();
+        if (leader) {
+          if (!dead && ((on >> x) & 1)) {
+            constexpr int kProducts = kTile / 16 / G::kHalves;
+            const uint64_t vd = v_desc + vb * (G::kOperand >> 4) + h * (kProducts * 128);
+            const uint32_t pt = tmem + (kStreams == 2 ? x : t & 1) * 128 + h * 64, ot = tmem + kTmemO + x * G::kOCols;
+            const uint32_t keep = h > 0 || !((firsts >> x) & 1) ? 1u : 0u;
 #pragma unroll
-        for (int x = 0; x < kStreams; ++x) {
-          const uint32_t step = t * kStreams + x, buf = step & 1, kb = t % kBufs;
-          const bool on = sees(p, wr[x].rows, w.s.prefix, j0);
-          if (i == 0) wait(q_full + 8 * x, seg, 0x73);
-          if (x == 0) wait(k_full + 8 * kb, t / kBufs, 0x74);
-          if (step >= 2) wait(pv_done + 8 * buf, (step - 2) >> 1, 0x75);
-          dead = __any_sync(0xffffffffu, dead);
-          tc::tc_fence_after();
-          if (leader) {
-            if (!dead && on) {
-              const uint64_t qd = q_desc + x * (G::kOperand >> 4), kd = k_desc + kb * (G::kOperand >> 4);
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * 1024 + (k & 3) * 2;
-                tc::mma_f16(tmem + buf * 128, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
-              }
-            }
-            tc::mma_commit(s_full + 8 * buf);
-            if (x == kStreams - 1) tc::mma_commit(k_free + 8 * kb);
+            for (int k = 0; k < kProducts; ++k)  // P of 32 tokens lies over the first half of their scores
+              tc::mma_f16_ta(ot, pt + 32 * (k >> 1) + 8 * (k & 1), vd + k * 128, idesc_o, k > 0 ? 1u : keep);
           }
-          __syncwarp();
-          if (pending) second(step - 1);
-          pending = true;
-          pend_on = on;
-          pend_first = on && !((begun >> x) & 1);
-          if (on) begun |= 1u << x;
+          tc::mma_commit(pv_done + 8 * bar);
+          if (x == kStreams - 1 && h == G::kHalves - 1) tc::mma_commit(v_free + 8 * vb);
+        }
+        __syncwarp();
+      }
+    };
+    bool more = true;
+#pragma unroll 1
+    while (true) {
+      const uint32_t x = step % kStreams, t = step / kStreams, kb = t % kBufs;
+      if (x == 0) {
+        if (left == 0 && more) {
+          more = next(w);
+          if (more) {
+            left = w.tiles;
+            i = w.tile;
+            prefix_tiles = w.seen.head;
+            next_tile = w.seen.next - w.seen.head;
+            seen0 = stream_sees(p, w, 0);
+            if (kStreams == 2) seen1 = stream_sees(p, w, 1);
+            begun = 0;
+            ++seg;
+          }
         }
       }
-      ++seg;
+      if (kStreams == 2 && t > 0) second(x, t - 1);
+      if (left > 0) {
+        if (!((begun >> (8 + x)) & 1)) {
+          wait(q_full + 8 * x, seg - 1, 0x73);
+          begun |= 256u << x;  // this segment's q is there
+        }
+        if (x == 0) wait(k_full + 8 * kb, t / kBufs, 0x74);
+        if (kStreams == 2 ? t > 0 : t > 1) wait(pv_done + 8 * (kStreams == 2 ? 2 * x + 1 : t & 1), kStreams == 2 ? t - 1 : (t - 2) >> 1, 0x75);
+        const int j0 = (i < prefix_tiles ? i : next_tile + i) * kTile;
+        const bool here = x == 0 ? within(seen0, j0) : within(seen1, j0);
+        dead = __any_sync(0xffffffffu, dead);
+        tc::tc_fence_after();
+        if (leader) {
+          if (!dead && here) {
+            const uint64_t qd = q_desc + x * (G::kOperand >> 4), kd = k_desc + kb * (G::kOperand >> 4);
+            const uint32_t st = tmem + (kStreams == 2 ? x : t & 1) * 128;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * 1024 + (k & 3) * 2;
+              tc::mma_f16(st, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+            }
+          }
+          tc::mma_commit(s_full + 8 * (kStreams == 2 ? x : t & 1));
+          if (x == kStreams - 1) tc::mma_commit(k_free + 8 * kb);
+        }
+        __syncwarp();
+        if (kStreams == 1 && t > 0) second(0, t - 1);
+        on = (on & ~(1u << x)) | (here ? 1u << x : 0u);
+        firsts = (firsts & ~(1u << x)) | ((begun >> x) & 1 ? 0u : 1u << x);
+        if (here) begun |= 1u << x;
+        if (x == kStreams - 1) --left, ++i;
+      } else {
+        if (kStreams == 1 && t > 0) second(0, t - 1);
+        if (x == kStreams - 1) break;
+      }
+      ++step;
     }
-    if (pending) second(t * kStreams - 1);
     // every product is done before the tensor memory is given back, whatever else ran out
     if (leader) tc::mma_commit(all_done);
     __syncwarp();
@@ -305,7 +344,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
     // (fills up the group)
   } else if (warp >= kSoftmaxWarps) {
     // ---------------- loads and widening ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kWidenRegs));
+    if constexpr (G::kWidenRegs > G::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kWidenRegs));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kWidenRegs));
     constexpr int kParts = G::kParts;
     const int part0 = (warp - kSoftmaxWarps) * kParts;  // this warp's tokens of a tile: 16 each, which lie on one page
     W& w = walks[warp];
@@ -444,23 +484,21 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
 
     Part cur[kParts], ahead[kParts];
     uint4 ku[kParts][kLoads], vu[kParts][kLoads];
-    uint32_t words[kParts];
-    bool more = step(cur);
-    if (more) {
-      settle(cur);
-      load(cur, p.k, ku);
-      load(cur, p.v, vu);
-      load_scales(cur, words);
-      more = step(ahead);
-      bool go = true;
-      for (uint32_t t = 0; go; ++t) {
-        const uint32_t buf = t % kBufs;
+    uint32_t words[kParts] = {};
+    // Per turn: the keys of tile t, then its values; in between and behind, the loads of tile t + 1, whose page numbers came
+    // with the turn before, and the page numbers of tile t + 2.
+    uint32_t t = 0;
+    bool have = false, found = false;  // tile t is loaded; the one behind it is `ahead`
+#pragma unroll 1
+    while (true) {
+      const uint32_t buf = t % kBufs;
+      if (have) {
         if (t >= kBufs) wait(k_free + 8 * buf, t / kBufs - 1, 0x77);
         dead = __any_sync(0xffffffffu, dead);
         widen(ku, words, false, base + G::kOffK + buf * G::kOperand);
         // The tokens' scales.  Their buffer was last read for tile t - kCols: S of tile t - kBufs is done, and it was issued
-        // after every stream's P of the tile before that one.
-        static_assert(kCols >= kBufs + 1, "buffers of scales");
+        // after every stream's P of the last but one before it.
+        static_assert(kCols >= kBufs + 2, "buffers of scales");
 #pragma unroll
         for (int g = 0; g < kParts; ++g) {
           const uint32_t word = words[g];
@@ -524,32 +562,37 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           tc::mbar_arrive(k_full + 8 * buf);
           tc::mbar_arrive(col_full + 8 * (t % kCols));
         }
-        go = more;
-        uint32_t words_v[kParts];
+      }
+      uint32_t words_v[kParts];
 #pragma unroll
-        for (int g = 0; g < kParts; ++g) words_v[g] = words[g];
-        if (go) {  // the next tile's keys, and where the one after it lies
-          settle(ahead);
-          load(ahead, p.k, ku);
-          load_scales(ahead, words);
+      for (int g = 0; g < kParts; ++g) words_v[g] = words[g];
+      const bool go = found;
+      if (go) {
+        settle(ahead);
+        load(ahead, p.k, ku);
+        load_scales(ahead, words);
 #pragma unroll
-          for (int g = 0; g < kParts; ++g) cur[g] = ahead[g];
-          more = step(ahead);
-        }
+        for (int g = 0; g < kParts; ++g) cur[g] = ahead[g];
+      }
+      found = step(ahead);
+      if (have) {
         if (t >= kBufs) wait(v_free + 8 * buf, t / kBufs - 1, 0x78);
         dead = __any_sync(0xffffffffu, dead);
         widen(vu, words_v, true, base + G::kOffV + buf * G::kOperand);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(v_full + 8 * buf);
-        if (go) load(cur, p.v, vu);
+        ++t;
       }
+      if (go) load(cur, p.v, vu);
+      have = go;
+      if (!go && !found) break;
     }
   } else {
     // ---------------- softmax ----------------
     if constexpr (G::kSoftmaxRegs > G::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
-    constexpr int kSpan = G::kSpan, kMine = G::kMine;
-    constexpr int kStep = 64;  // tokens weighed at a time
+    constexpr int kMine = G::kMine;
+    constexpr int kStep = 32;  // tokens weighed at a time
     const int quad = warp & 3;
     const int stream = kStreams == 2 ? warp >> 2 : 0, sub = kStreams == 2 ? 0 : warp >> 2;
     const int row = quad * 32 + lane;  // of the stream
@@ -566,12 +609,11 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
     };
 
     RowOf* row_of = reinterpret_cast<RowOf*>(smem + G::kOffRow) + threadIdx.x;  // [2 x 256]
-    WarpRows& wr = reinterpret_cast<WarpRows*>(smem + G::kOffWarp)[warp];
     // The segment that the walk stands at; returns the row's position (of a row that is none: the last one's).
     auto segment = [&](int parity) {
       const int64_t r = static_cast<int64_t>(w.row_tile) * kRows + stream * 128 + row;
       const int64_t at = min(r, w.s.rows - 1);
-      const int32_t node = static_cast<int32_t>(at / p.group);
+      const int32_t node = token_of(p, at);
       RowOf o;
       o.token = r < w.s.rows ? w.s.q_row + node : -1;
       o.head = w.head * p.group + static_cast<int32_t>(at - static_cast<int64_t>(node) * p.group);
@@ -636,43 +678,106 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
     };
 
     uint32_t t = 0;
-    int parity = 0;
-    bool more = next(w);
-    int32_t at = segment(0);
-    float row_scale;
-    stage_q(0, row_scale);
+    int parity = 0;  // of the segment
+    int32_t at = 0;
+    float row_scale = 1.0f, ref = 0.0f, l = 0.0f;
+    bool live = false, done_any = false;
     const float cap2 = SHAPED ? p.softcap * kLog2e : 0.0f;
-    while (more) {
-      float ref = kNoRef;
+    while (true) {
+      // the next segment's q, then the output of the one before it
+      const bool more = next(w);
+      if (more) {
+        at = segment(parity);
+        stage_q(parity, row_scale);
+      }
+      if (done_any) {
+        if constexpr (kSubs > 1) {
+          sync_rows();
+          l = ends[row] + ends[128 + row];  // in one order for both
+        }
+        wait(pv_done + 8 * (kStreams == 2 ? 2 * stream + 1 : (t - 1) & 1), kStreams == 2 ? t - 1 : (t - 1) >> 1, 0x7c);
+        dead = __any_sync(0xffffffffu, dead);
+        tc::tc_fence_after();
+        const RowOf done = row_of[(parity ^ 1) * 256];
+        const bool whole = done.flags == 3;
+        const bool none = ref == kNoRef;  // (O then holds anything)
+        const float inv = !whole ? 1.0f : __frcp_rn(l);
+        const float m = none ? -INFINITY : ref + kOffset;
+        const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (done.flags & 1)) * p.tile_rows + stream * 128 + row;
+        if (live) {
+#pragma unroll 1
+          for (int cc = 0; cc < kMine; cc += 16) {
+            uint32_t o[16];
+            __syncwarp();
+            tc::tmem_ld_32x32b_x16(o_at + cc, o);
+            tc::tmem_wait_ld(o);
+            float f[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              // 4-bit codes: column k of eight is channel k / 2 + 4 (k % 2)
+              const int ch = G::kU4 ? (k & 8) + ((k & 7) >> 1) + 4 * (k & 1) : k;
+              f[ch] = none ? 0.0f : __uint_as_float(o[k]) * inv;
+            }
+            if (done.token < 0) continue;
+            const int ch = sub * kMine + cc;
+            if (whole) {
+              uint8_t* out = p.out + done.token * p.ot + done.head * p.oh + ch * 2;
+#pragma unroll
+              for (int k = 0; k < 16; k += 8)
+                *reinterpret_cast<uint4*>(out + k * 2) = p.dtype == QLIN_BF16 ? kv::pack8<1>(f + k) : kv::pack8<0>(f + k);
+            } else {
+              float* out = p.part_o + slot * D + ch;
+#pragma unroll
+              for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(out + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+            }
+          }
+        }
+        if (done.token >= 0 && sub == 0) {
+          if (!whole) p.part_ml[slot] = make_float2(m, l);
+          else if (p.lse != nullptr) p.lse[done.token * p.hq + done.head] = (lg2(l) + ref) * kLn2;
+        }
+        tc::tc_fence_before();
+      }
+      if (!more) break;
+      done_any = true;
+      ref = kNoRef;
       uint64_t l2 = pair(0.0f, 0.0f);
       bool begun = false;
-      {
-        const int32_t first = __shfl_sync(0xffffffffu, at, 0), last = __shfl_sync(0xffffffffu, at, 31);
-        if (lane == 0) wr = {stream_of(p, w, stream), first, last};
-        __syncwarp();
-      }
+      const Range some = stream_sees(p, w, stream);
+      const Range all = all_seen(p, w.s, __shfl_sync(0xffffffffu, at, 0), __shfl_sync(0xffffffffu, at, 31), 64);
+      const int prefix = w.s.prefix, prefix_tiles = w.seen.head, next_tile = w.seen.next - w.seen.head;
+      int i = w.tile;
+      const int i_end = w.tile + w.tiles;
       const bool scaled = !__all_sync(0xffffffffu, row_scale == 1.0f);
       float slope2 = 0.0f;
       if constexpr (SHAPED) slope2 = p.slopes != nullptr ? -kLog2e * p.slopes[row_of[parity * 256].head] : 0.0f;
-      for (int i = 0; i < w.tiles; ++i, ++t) {
-        const uint32_t step = t * kStreams + stream, buf = step & 1;
-        const int j0 = w.seen.at(w.tile + i) * kTile;
-        wait(s_full + 8 * buf, step >> 1, 0x79);
-        if (!sees(p, wr.rows, w.s.prefix, j0)) {  // nothing was multiplied and nothing will be
-          if (lane == 0) tc::mbar_arrive(p_full + 8 * buf);
+#pragma unroll 1
+      for (; i < i_end; ++i, ++t) {
+        const int j0 = (i < prefix_tiles ? i : next_tile + i) * kTile;
+        wait(s_full + 8 * (kStreams == 2 ? stream : t & 1), kStreams == 2 ? t : t >> 1, 0x79);
+        if (!within(some, j0)) {  // nothing was multiplied and nothing will be
+          if (lane == 0) {
+            tc::mbar_arrive(p_full + 8 * (kStreams == 2 ? 2 * stream : t & 1));
+            if (kStreams == 2) tc::mbar_arrive(p_full + 8 * (2 * stream + 1));
+          }
           continue;
         }
         wait(col_full + 8 * (t % kCols), t / kCols, 0x7a);
         dead = __any_sync(0xffffffffu, dead);
         tc::tc_fence_after();
         const bool odd = odd_tile[t % kCols] == t + 1;
-        const int jc = j0 + sub * kSpan;
-        const bool all = (j0 + kTile - 1 <= wr.first && (p.window == 0 || j0 > wr.last - p.window)) || j0 + kTile <= w.s.prefix;
-        const uint32_t s_at = lanes + buf * 128 + sub * kSpan;
-        const uint32_t col = base + G::kOffCol + ((t % kCols) * 4 * kTile + sub * kSpan) * 4;
+#pragma unroll 1
+        for (int h = 0; h < G::kHalves; ++h) {
+        const int part = kSubs > 1 ? sub : h;  // of the tile's two times 64 tokens
+        const uint32_t s_at = lanes + (kStreams == 2 ? stream : t & 1) * 128 + part * 64;
+        float keep = 1.0f;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 64; c0 += kStep) {
+        const int jc = j0 + part * 64 + c0;
+        const uint32_t col = base + G::kOffCol + ((t % kCols) * 4 * kTile + part * 64 + c0) * 4;
 
-        // t of kStep tokens from column k0 on, from their products
-        auto score = [&](uint32_t (&v)[kStep], int k0) {
+        // t of these tokens from their products
+        auto score = [&](uint32_t (&v)[kStep]) {
           if (scaled) {
             const uint64_t rs = pair(row_scale, row_scale);
 #pragma unroll
@@ -685,8 +790,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           if (SHAPED && cap2 > 0.0f) {
 #pragma unroll
             for (int k = 0; k < kStep; k += 4) {
-              const float4 sk = lds4(col + 4 * (k0 + k));
-              const float4 ls = lds4(col + 4 * (kTile + k0 + k));
+              const float4 sk = lds4(col + 4 * k);
+              const float4 ls = lds4(col + 4 * (kTile + k));
               const float ks[4] = {sk.x, sk.y, sk.z, sk.w}, lv[4] = {ls.x, ls.y, ls.z, ls.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -697,8 +802,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           } else {
 #pragma unroll
             for (int k = 0; k < kStep; k += 4) {
-              const float4 sk = lds4(col + 4 * (k0 + k));
-              const float4 ls = lds4(col + 4 * (kTile + k0 + k));
+              const float4 sk = lds4(col + 4 * k);
+              const float4 ls = lds4(col + 4 * (kTile + k));
               const float2 a = unpair(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y), pair(ls.x, ls.y)));
               const float2 b =
                   unpair(fma2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), pair(sk.z, sk.w), pair(ls.z, ls.w)));
@@ -709,32 +814,29 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
             }
           }
           if (SHAPED && p.slopes != nullptr) {
-            const float off = static_cast<float>(jc + k0 - at);  // exact below 2^24
+            const float off = static_cast<float>(jc - at);  // exact below 2^24
 #pragma unroll
             for (int k = 0; k < kStep; ++k)
               v[k] = __float_as_uint(fmaf(slope2, fabsf(off + static_cast<float>(k)), __uint_as_float(v[k])));
           }
-          if (!all) {
+          if (!within(all, jc)) {
 #pragma unroll
             for (int k1 = 0; k1 < kStep; k1 += 32) {
-              const int c = jc + k0 + k1;
+              const int c = jc + k1;
               uint32_t bits = low_bits(at + 1 - c);
               if (p.window > 0) bits &= ~low_bits(at - p.window + 1 - c);
-              bits |= low_bits(w.s.prefix - c);
+              bits |= low_bits(prefix - c);
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (!((bits >> k) & 1u)) v[k1 + k] = 0xff800000u;
             }
           }
         };
-        float keep = 1.0f;
-#pragma unroll 1
-        for (int k0 = 0; k0 < kSpan; k0 += kStep) {
+        {
           uint32_t v[kStep];
-          tc::tmem_ld_32x32b_x32(s_at + k0, v);
-          tc::tmem_ld_32x32b_x32(s_at + k0 + 32, v + 32);
+          tc::tmem_ld_32x32b_x32(s_at + c0, v);
           tc::tmem_wait_ld(v);
-          score(v, k0);
+          score(v);
           float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int k = 0; k < kStep; k += 8)
@@ -742,39 +844,38 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
             for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1])));
           float hi = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
           if constexpr (kSubs > 1) {  // over both threads of the row; and both have their scores: P may go over them
-            float* maxima = row_max + (t & 1) * kSubs * 128 + row;
+            float* maxima = row_max + (c0 / kStep & 1) * kSubs * 128 + row;
             maxima[sub * 128] = hi;
             sync_rows();
             hi = fmaxf(hi, maxima[(sub ^ 1) * 128]);
           }
           if (__any_sync(0xffffffffu, hi > ref + (kOffset + kSlack))) {  // (the same in all warps of these rows)
-            // The reference moves, by a whole number of powers of two, so that the row's probabilities of this tile that are
-            // written already can be scaled in fp16.  With more tiles to come its largest one goes six bits below the top of
-            // fp16, which it may grow by before the row has to be rescaled.
-            const float to = hi > ref + (kOffset + kSlack) ? ceilf(hi) - (w.tiles > 1 ? 9.0f : kOffset) : ref;
-            const float f = ex2(ref - to);
+            // The reference moves, by a whole number of powers of two, so that the row's probabilities that wait for the products
+            // already can be scaled in fp16.  With more to come its largest one goes six bits below the top of fp16, which it may
+            // grow by before the row has to be rescaled.
+            const float to = hi > ref + (kOffset + kSlack) ? ceilf(hi) - 9.0f : ref;
+            const float before = ref, f = ex2(ref - to);
             ref = to;
             keep *= f;
             l2 = mul2(l2, pair(f, f));
-            const __half2 h = __float2half2_rn(f);
-#pragma unroll 1
-            for (int c = 0; c < k0; c += kStep) {
-#pragma unroll 1
-              for (int x = 0; x < kStep / 2; x += 16) {
-                uint32_t o[16];
-                tc::tmem_ld_32x32b_x16(s_at + c + x, o);
-                tc::tmem_wait_ld(o);
+            if (c0 > 0) {
+              // in two steps: down to 2^-39 of P may be left, and fp16 ends at 2^-24
+              const float e = fmaxf(before - to, -48.0f), e1 = floorf(0.5f * e);
+              const __half2 f1 = __float2half2_rn(ex2(e1)), f2 = __float2half2_rn(ex2(e - e1));
+              uint32_t o[16];
+              tc::tmem_wait_st();
+              tc::tmem_ld_32x32b_x16(s_at, o);
+              tc::tmem_wait_ld(o);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = hmul2(o[k], *reinterpret_cast<const uint32_t*>(&h));
-                tc::tmem_st_32x32b_x16(s_at + c + x, o);
-              }
+              for (int k = 0; k < 16; ++k) o[k] = hmul2(hmul2(o[k], *reinterpret_cast<const uint32_t*>(&f1)), *reinterpret_cast<const uint32_t*>(&f2));
+              tc::tmem_st_32x32b_x16(s_at, o);
             }
           }
           const uint64_t nref = pair(-ref, -ref);
           auto weigh = [&](auto with_factors) {
 #pragma unroll
             for (int k = 0; k < kStep; k += 4) {
-              const float4 rv = lds4(col + 4 * (2 * kTile + k0 + k));
+              const float4 rv = lds4(col + 4 * (2 * kTile + k));
               const float rr[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
               for (int x = 0; x < 4; x += 2) {
@@ -782,8 +883,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
                 float2 f = make_float2(ex2(a.x), ex2(a.y));
                 l2 = fma2(pair(f.x, f.y), pair(rr[x], rr[x + 1]), l2);
                 if constexpr (decltype(with_factors)::value) {  // (what is hidden has no product with a factor that is not a number)
-                  f.x = v[k + x] == 0xff800000u ? 0.0f : f.x * lds1(col + 4 * (3 * kTile + k0 + k + x));
-                  f.y = v[k + x + 1] == 0xff800000u ? 0.0f : f.y * lds1(col + 4 * (3 * kTile + k0 + k + x + 1));
+                  f.x = v[k + x] == 0xff800000u ? 0.0f : f.x * lds1(col + 4 * (3 * kTile + k + x));
+                  f.y = v[k + x + 1] == 0xff800000u ? 0.0f : f.y * lds1(col + 4 * (3 * kTile + k + x + 1));
                 }
                 v[(k + x) / 2] = kv::pack2<0>(f.x, f.y);
               }
@@ -791,11 +892,13 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           };
           if (odd) weigh(std::true_type{});
           else weigh(std::false_type{});
-          tc::tmem_st_32x32b_x32(s_at + k0, v);  // over the first half of its scores
+          tc::tmem_st_32x32b_x16(s_at + c0, v);  // over the first half of their scores
+        }
         }
         if (__any_sync(0xffffffffu, keep != 1.0f) && begun) {  // (NaN too)
-          const uint32_t before = step - kStreams;
-          wait(pv_done + 8 * (before & 1), before >> 1, 0x7b);
+          // P u of what came before: of the tile before, with two streams, it is (S went over its P); of this one's first half
+          if (kStreams == 1) wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x7b);
+          else if (h == 1) wait(pv_done + 8 * (2 * stream), t, 0x7b);
           dead = __any_sync(0xffffffffu, dead);
           tc::tc_fence_after();
 #pragma unroll 1
@@ -817,67 +920,15 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full + 8 * buf);
-      }
-
-      // the next segment's q, then this one's output
-      const bool live = wr.rows.live;
-      const float2 lp = unpair(l2);
-      float l = lp.x + lp.y;
-      if constexpr (kSubs > 1) ends[sub * 128 + row] = l;
-      more = next(w);
-      if (more) {
-        at = segment(parity ^ 1);
-        stage_q(parity ^ 1, row_scale);
-      }
-      if constexpr (kSubs > 1) {
-        sync_rows();
-        l = ends[row] + ends[128 + row];  // in one order for both
-      }
-      const uint32_t ended = (t - 1) * kStreams + stream;
-      wait(pv_done + 8 * (ended & 1), ended >> 1, 0x7c);
-      dead = __any_sync(0xffffffffu, dead);
-      tc::tc_fence_after();
-      const RowOf done = row_of[parity * 256];
-      parity ^= 1;
-      const bool whole = done.flags == 3;
-      const bool none = ref == kNoRef;  // (O then holds anything)
-      const float inv = !whole ? 1.0f : __frcp_rn(l);
-      const float m = none ? -INFINITY : ref + kOffset;
-      const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (done.flags & 1)) * p.tile_rows + stream * 128 + row;
-      if (live) {
-#pragma unroll 1
-        for (int cc = 0; cc < kMine; cc += 16) {
-          uint32_t o[16];
-          __syncwarp();
-          tc::tmem_ld_32x32b_x16(o_at + cc, o);
-          tc::tmem_wait_ld(o);
-          float f[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            // 4-bit codes: column k of eight is channel k / 2 + 4 (k % 2)
-            const int ch = G::kU4 ? (k & 8) + ((k & 7) >> 1) + 4 * (k & 1) : k;
-            f[ch] = none ? 0.0f : __uint_as_float(o[k]) * inv;
-          }
-          if (done.token < 0) continue;
-          const int ch = sub * kMine + cc;
-          if (whole) {
-            uint8_t* out = p.out + done.token * p.ot + done.head * p.oh + ch * 2;
-#pragma unroll
-            for (int k = 0; k < 16; k += 8)
-              *reinterpret_cast<uint4*>(out + k * 2) = p.dtype == QLIN_BF16 ? kv::pack8<1>(f + k) : kv::pack8<0>(f + k);
-          } else {
-            float* out = p.part_o + slot * D + ch;
-#pragma unroll
-            for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(out + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
-          }
+        if (lane == 0) tc::mbar_arrive(p_full + 8 * (kStreams == 2 ? 2 * stream + h : t & 1));
         }
       }
-      if (done.token >= 0 && sub == 0) {
-        if (!whole) p.part_ml[slot] = make_float2(m, l);
-        else if (p.lse != nullptr) p.lse[done.token * p.hq + done.head] = (lg2(l) + ref) * kLn2;
-      }
-      tc::tc_fence_before();
+
+      const float2 lp = unpair(l2);
+      l = lp.x + lp.y;
+      if constexpr (kSubs > 1) ends[sub * 128 + row] = l;
+      live = some.high >= 0;
+      parity ^= 1;
     }
   }
   tc::tc_fence_before();
@@ -1013,7 +1064,7 @@ cudaError_t plan_chunk_attention(const ChunkAttentionArgs& a, Prepared* out) {
   p.scale = a.scores.scale;
   p.softcap = a.scores.softcap;
   p.slopes = a.scores.slopes;
-  p.window = static_cast<int32_t>(a.scores.window);
+  p.window = a.scores.window >= tree::kMaxLen ? 0 : static_cast<int32_t>(a.scores.window);  // no sequence is longer
   p.prefix = a.scores.prefix_lens;
   p.lse = a.lse;
   p.tile_rows = static_cast<int32_t>(chunk::part_rows(c, a.q.heads, a.max_new));

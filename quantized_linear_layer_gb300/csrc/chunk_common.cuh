@@ -42,6 +42,11 @@ __device__ __forceinline__ Sequence sequence(const Params& p, int b) {
   return s;
 }
 
+// The new token that a row of a key head belongs to (rows lie below 2^32: a row of q has 128 bytes or more).
+__device__ __forceinline__ int32_t token_of(const Params& p, int64_t row) {
+  return static_cast<int32_t>(static_cast<uint32_t>(row) / static_cast<uint32_t>(p.group));
+}
+
 // The token tiles that some row of a tile of rows sees: those of the prefix, 0 .. head - 1, and those of the
 // window, next .. next + (count - head) - 1.
 struct Tiles {
@@ -67,7 +72,7 @@ __device__ __forceinline__ int32_t row_tiles(const Sequence& s) {
 template <int ROWS>
 __device__ __forceinline__ Tiles tiles_of_row_tile(const Params& p, const Sequence& s, int32_t row_tile) {
   const int64_t first = static_cast<int64_t>(row_tile) * ROWS, last = min(first + ROWS, s.rows) - 1;
-  return tiles_of(p, s, static_cast<int32_t>(first / p.group), static_cast<int32_t>(last / p.group));
+  return tiles_of(p, s, token_of(p, first), token_of(p, last));
 }
 
 // Token tiles of all row tiles of one key head of a sequence, by a whole warp.
