@@ -75,15 +75,15 @@ struct Geo {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kStreams * kOperand;
   static constexpr int kOffV = kOffK + kBufs * kOperand;
-  static constexpr int kOffCol = kOffV + kBufs * kOperand;             // [kCols][scale sk, log2 sv, 1 / sv, factor][128]
-  static constexpr int kOffPair = kOffCol + kCols * 4 * kTile * 4;     // [tile parity][thread of the row][row]
+  static constexpr int kOffCol = kOffV + kBufs * kOperand;             // [kCols][scale sk, sv][128]
+  static constexpr int kOffPair = kOffCol + kCols * 2 * kTile * 4;     // [tile parity][thread of the row][row]
   static constexpr int kOffQmax = kOffPair + 2 * kSubs * 128 * 4;      // [thread of the row][row]
   static constexpr int kOffEnd = kOffQmax + kSubs * 128 * 4;           // [thread of the row][row] l
   static constexpr int kOffRow = kOffEnd + kSubs * 128 * 4;                          // [segment parity][softmax thread] RowOf
   static constexpr int kOffBar = kOffRow + 2 * 32 * kSoftmaxWarps * 16;
   static constexpr int kBars = 4 * kBufs + 2 + 4 + 4 + kStreams + 1 + kCols;
-  static constexpr int kOffMisc = kOffBar + kBars * 8;  // tensor memory address, flags
-  static constexpr int kOffScan = (kOffMisc + 32 + 7) / 8 * 8;
+  static constexpr int kOffMisc = (kOffBar + kBars * 8 + 15) / 16 * 16;  // tensor memory address, flags, exponents
+  static constexpr int kOffScan = kOffMisc + 32 + kCols * 16;
   static constexpr int kOffWalk = (kOffScan + (kWarps + 1) * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffWalk + (kSoftmaxWarps + kWidenWarps + 1) * static_cast<int>(sizeof(Walk<kRows>)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -125,11 +125,6 @@ struct RowOf {
 __device__ __forceinline__ float4 lds4(uint32_t at) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ float lds1(uint32_t at) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
   return v;
 }
 
@@ -175,7 +170,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
   const uint32_t col_full = all_done + 8;           // [kCols]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
   volatile uint32_t* ran_out = tmem_slot + 1;  // a wait of some role of the block ran out
-  volatile uint32_t* odd_tile = tmem_slot + 2;  // [kCols]: 1 + the last tile with a factor (usable_scale) that is not 1
+  volatile uint32_t* odd_tile = tmem_slot + 2;  // [kCols]: 1 + the last tile with a value scale that is not finite
+  int32_t* top_exp = reinterpret_cast<int32_t*>(smem + G::kOffMisc + 32);  // [kCols][widening warp]: all its |sv| are below 2^this
   int64_t* scan = reinterpret_cast<int64_t*>(smem + G::kOffScan);
   W* walks = reinterpret_cast<W*>(smem + G::kOffWalk);
 
@@ -451,8 +447,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         const uint32_t word = words[g], out = to + g * 2048 + out_at;
         uint32_t bias = 0;
         if constexpr (G::kU4) {
-          // what is no zero-point becomes one: its token counts by its score and its factor, and what is not seen has to
-          // stay finite
+          // what is no zero-point becomes one: its token counts by its scales, and what is not seen has to stay finite
           const uint32_t sw = __shfl_sync(0xffffffffu, word, (v ? 16 : 0) + row + x * kRowsAtOnce);
           const __half z = __hmin(__hmax(__ushort_as_half(static_cast<unsigned short>(sw >> 16)), __float2half(0.0f)),
                                   __float2half(15.0f));
@@ -499,36 +494,27 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         // The tokens' scales.  Their buffer was last read for tile t - kCols: S of tile t - kBufs is done, and it was issued
         // after every stream's P of the last but one before it.
         static_assert(kCols >= kBufs + 2, "buffers of scales");
+        int32_t top = -64;
 #pragma unroll
         for (int g = 0; g < kParts; ++g) {
           const uint32_t word = words[g];
           const int token0 = (part0 + g) * 16;
-          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 4 * kTile + token0 + (lane & 15);
+          float* col = reinterpret_cast<float*>(smem + G::kOffCol) + (t % kCols) * 2 * kTile + token0 + (lane & 15);
+          float sc;
+          if constexpr (G::kU4)  // without a zero-point a token is not a number
+            sc = odd_zero(word) ? __uint_as_float(0x7fc00000u) : __half2float(__ushort_as_half(static_cast<unsigned short>(word & 0xffffu)));
+          else
+            sc = __uint_as_float(word);
+          const uint32_t e = (__float_as_uint(sc) >> 23) & 0xffu;
           if (lane < 16) {
-            float sk;
-            if constexpr (G::kU4)
-              sk = odd_zero(word) ? __uint_as_float(0x7fc00000u) : __half2float(__ushort_as_half(static_cast<unsigned short>(word & 0xffffu)));
-            else
-              sk = __uint_as_float(word);
-            col[0] = sk * to_t;
+            col[0] = sc * to_t;
           } else {
-            float factor = 1.0f, sv;
-            uint32_t vw = word;
-            bool odd = odd_scale<FMT>(vw);
-            if (odd) vw = usable_scale<FMT>(vw, factor);
-            if constexpr (G::kU4) {  // without a zero-point a token is not a number: its factor here, its score above
-              if (odd_zero(word)) odd = true, factor = __uint_as_float(0x7fc00000u);
-              sv = __half2float(__ushort_as_half(static_cast<unsigned short>(vw & 0xffffu)));
-            } else {
-              sv = __uint_as_float(vw);
-            }
-            if (odd && (lane & 15) < cur[g].valid) odd_tile[t % kCols] = t + 1;
-            col[kTile] = lg2(sv);
-            col[2 * kTile] = rcp(sv);
-            col[3 * kTile] = factor;
+            col[kTile] = sc;
+            if (e == 255) odd_tile[t % kCols] = t + 1;
+            else top = max(top, static_cast<int32_t>(e) - 126);
           }
           if constexpr (FMT == QLIN_KV_E4M3) {
-            // Value codes that are NaN (which the library never writes) become 0 and their token's factor NaN: a product with
+            // Value codes that are NaN (which the library never writes) become 0 and their token's scale NaN: a product with
             // a probability of 0 keeps a NaN, and rows that do not see the token must not get one.
             uint32_t bad = 0;
 #pragma unroll
@@ -549,7 +535,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
                 }
                 const int x = k / kBlocks2 % (16 / kRowsAtOnce);
                 if (any != 0) {
-                  reinterpret_cast<float*>(smem + G::kOffCol)[((t % kCols) * 4 + 3) * kTile + token0 + row + x * kRowsAtOnce] =
+                  reinterpret_cast<float*>(smem + G::kOffCol)[((t % kCols) * 2 + 1) * kTile + token0 + row + x * kRowsAtOnce] =
                       __uint_as_float(0x7fc00000u);
                   odd_tile[t % kCols] = t + 1;
                 }
@@ -557,8 +543,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
             }
           }
         }
-        __syncwarp();
+        top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) {
+          top_exp[(t % kCols) * 4 + warp - kSoftmaxWarps] = top;
           tc::mbar_arrive(k_full + 8 * buf);
           tc::mbar_arrive(col_full + 8 * (t % kCols));
         }
@@ -766,6 +753,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         dead = __any_sync(0xffffffffu, dead);
         tc::tc_fence_after();
         const bool odd = odd_tile[t % kCols] == t + 1;
+        const int4 te = *reinterpret_cast<const int4*>(top_exp + (t % kCols) * 4);
+        const float top = static_cast<float>(max(max(te.x, te.y), max(te.z, te.w)));
 #pragma unroll 1
         for (int h = 0; h < G::kHalves; ++h) {
         const int part = kSubs > 1 ? sub : h;  // of the tile's two times 64 tokens
@@ -774,7 +763,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
 #pragma unroll 1
         for (int c0 = 0; c0 < 64; c0 += kStep) {
         const int jc = j0 + part * 64 + c0;
-        const uint32_t col = base + G::kOffCol + ((t % kCols) * 4 * kTile + part * 64 + c0) * 4;
+        const uint32_t col = base + G::kOffCol + ((t % kCols) * 2 * kTile + part * 64 + c0) * 4;
 
         // t of these tokens from their products
         auto score = [&](uint32_t (&v)[kStep]) {
@@ -791,22 +780,19 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
 #pragma unroll
             for (int k = 0; k < kStep; k += 4) {
               const float4 sk = lds4(col + 4 * k);
-              const float4 ls = lds4(col + 4 * (kTile + k));
-              const float ks[4] = {sk.x, sk.y, sk.z, sk.w}, lv[4] = {ls.x, ls.y, ls.z, ls.w};
+              const float ks[4] = {sk.x, sk.y, sk.z, sk.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float r = rcp(1.0f + ex2(__uint_as_float(v[k + e]) * ks[e]));
-                v[k + e] = __float_as_uint(fmaf(r, -2.0f * cap2, cap2) + lv[e]);
+                v[k + e] = __float_as_uint(fmaf(r, -2.0f * cap2, cap2));
               }
             }
           } else {
 #pragma unroll
             for (int k = 0; k < kStep; k += 4) {
               const float4 sk = lds4(col + 4 * k);
-              const float4 ls = lds4(col + 4 * (kTile + k));
-              const float2 a = unpair(fma2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y), pair(ls.x, ls.y)));
-              const float2 b =
-                  unpair(fma2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), pair(sk.z, sk.w), pair(ls.z, ls.w)));
+              const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y)));
+              const float2 b = unpair(mul2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), pair(sk.z, sk.w)));
               v[k] = __float_as_uint(a.x);
               v[k + 1] = __float_as_uint(a.y);
               v[k + 2] = __float_as_uint(b.x);
@@ -842,7 +828,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           for (int k = 0; k < kStep; k += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1])));
-          float hi = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+          float hi = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) + top;  // no product with a value scale is above 2^this
           if constexpr (kSubs > 1) {  // over both threads of the row; and both have their scores: P may go over them
             float* maxima = row_max + (c0 / kStep & 1) * kSubs * 128 + row;
             maxima[sub * 128] = hi;
@@ -872,19 +858,20 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
             }
           }
           const uint64_t nref = pair(-ref, -ref);
-          auto weigh = [&](auto with_factors) {
+          auto weigh = [&](auto with_odd) {
 #pragma unroll
             for (int k = 0; k < kStep; k += 4) {
-              const float4 rv = lds4(col + 4 * (2 * kTile + k));
-              const float rr[4] = {rv.x, rv.y, rv.z, rv.w};
+              const float4 sv = lds4(col + 4 * (kTile + k));
+              const float ss[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
               for (int x = 0; x < 4; x += 2) {
                 const float2 a = unpair(add2(pair(__uint_as_float(v[k + x]), __uint_as_float(v[k + x + 1])), nref));
-                float2 f = make_float2(ex2(a.x), ex2(a.y));
-                l2 = fma2(pair(f.x, f.y), pair(rr[x], rr[x + 1]), l2);
-                if constexpr (decltype(with_factors)::value) {  // (what is hidden has no product with a factor that is not a number)
-                  f.x = v[k + x] == 0xff800000u ? 0.0f : f.x * lds1(col + 4 * (3 * kTile + k + x));
-                  f.y = v[k + x + 1] == 0xff800000u ? 0.0f : f.y * lds1(col + 4 * (3 * kTile + k + x + 1));
+                const uint64_t e = pair(ex2(a.x), ex2(a.y));
+                l2 = add2(l2, e);
+                float2 f = unpair(mul2(e, pair(ss[x], ss[x + 1])));
+                if constexpr (decltype(with_odd)::value) {  // (what is hidden has no product with a scale that is not a number)
+                  if (v[k + x] == 0xff800000u) f.x = 0.0f;
+                  if (v[k + x + 1] == 0xff800000u) f.y = 0.0f;
                 }
                 v[(k + x) / 2] = kv::pack2<0>(f.x, f.y);
               }
