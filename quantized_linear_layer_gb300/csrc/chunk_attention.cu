@@ -63,7 +63,7 @@ struct Geo {
   static constexpr int kBufs = D == 256 ? 1 : 2;  // of K and of V
   // Warps, whole groups of four, and their registers: what all are launched with is dealt out anew by role.
   static constexpr int kWidenWarps = 4, kMmaWarp = kSoftmaxWarps + kWidenWarps;
-  static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps;
+  static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps, kActive = 32 * (kMmaWarp + kStreams);
   static constexpr int kLaunchRegs = 128;
   static constexpr int kSoftmaxRegs = D == 256 ? 104 : 120, kWidenRegs = D == 256 ? 232 : 200, kOtherRegs = 64;
   static_assert(kSoftmaxWarps * kSoftmaxRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kWarps * kLaunchRegs, "registers");
@@ -78,14 +78,14 @@ struct Geo {
   static constexpr int kOffCol = kOffV + kBufs * kOperand;             // [kCols][scale sk, sv][128]
   static constexpr int kOffPair = kOffCol + kCols * 2 * kTile * 4;     // [tile parity][thread of the row][row]
   static constexpr int kOffQmax = kOffPair + 2 * kSubs * 128 * 4;      // [thread of the row][row]
-  static constexpr int kOffEnd = kOffQmax + kSubs * 128 * 4;           // [thread of the row][row] l
-  static constexpr int kOffRow = kOffEnd + kSubs * 128 * 4;                          // [segment parity][softmax thread] RowOf
+  static constexpr int kOffEnd = kOffQmax + kSubs * 128 * 4;           // [segment parity][thread of the row][row] l
+  static constexpr int kOffRow = kOffEnd + 2 * kSubs * 128 * 4;  // [segment parity][softmax thread] RowOf
   static constexpr int kOffBar = kOffRow + 2 * 32 * kSoftmaxWarps * 16;
-  static constexpr int kBars = 4 * kBufs + 2 + 4 + 4 + kStreams + 1 + kCols;
+  static constexpr int kBars = 4 * kBufs + 3 * 4 + kStreams + 1 + kCols;
   static constexpr int kOffMisc = (kOffBar + kBars * 8 + 15) / 16 * 16;  // tensor memory address, flags, exponents
   static constexpr int kOffScan = kOffMisc + 32 + kCols * 16;
   static constexpr int kOffWalk = (kOffScan + (kWarps + 1) * 8 + 15) / 16 * 16;
-  static constexpr int kSmem = kOffWalk + (kSoftmaxWarps + kWidenWarps + 1) * static_cast<int>(sizeof(Walk<kRows>)) + 1024;
+  static constexpr int kSmem = kOffWalk + (kMmaWarp + kStreams + 1) * static_cast<int>(sizeof(Walk<kRows>)) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kTmemO + kStreams * kOCols <= 512, "tensor memory");
 };
@@ -163,11 +163,11 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
   const uint32_t bars = base + G::kOffBar;
   const uint32_t k_full = bars, k_free = k_full + 8 * kBufs;                       // [kBufs]
   const uint32_t v_full = k_free + 8 * kBufs, v_free = v_full + 8 * kBufs;         // [kBufs]
-  // two streams: S of stream x, P and P u of its half h at 2 x + h; one stream: of two buffers in turn
-  const uint32_t s_full = v_free + 8 * kBufs, p_full = s_full + 16, pv_done = p_full + 32;  // [2], [4], [4]
+  // two streams: S, P and P u of stream x and half h of the tokens at 2 x + h; one stream: of two buffers in turn
+  const uint32_t s_full = v_free + 8 * kBufs, p_full = s_full + 32, pv_done = p_full + 32;  // [4] each
   const uint32_t q_full = pv_done + 32;  // [kStreams]
   const uint32_t all_done = q_full + 8 * kStreams;
-  const uint32_t col_full = all_done + 8;           // [kCols]
+  const uint32_t col_full = all_done + 8;  // [kCols]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::kOffMisc);
   volatile uint32_t* ran_out = tmem_slot + 1;  // a wait of some role of the block ran out
   volatile uint32_t* odd_tile = tmem_slot + 2;  // [kCols]: 1 + the last tile with a value scale that is not finite
@@ -178,17 +178,17 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBufs; ++i) {
       tc::mbar_init(k_full + 8 * i, kWidenWarps);
-      tc::mbar_init(k_free + 8 * i, 1);
+      tc::mbar_init(k_free + 8 * i, kStreams);
       tc::mbar_init(v_full + 8 * i, kWidenWarps);
-      tc::mbar_init(v_free + 8 * i, 1);
+      tc::mbar_init(v_free + 8 * i, kStreams);
     }
-    for (int i = 0; i < 2; ++i) tc::mbar_init(s_full + 8 * i, 1);
     for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(s_full + 8 * i, 1);
       tc::mbar_init(p_full + 8 * i, kSoftmaxWarps / kStreams);
       tc::mbar_init(pv_done + 8 * i, 1);
     }
     for (int i = 0; i < kStreams; ++i) tc::mbar_init(q_full + 8 * i, kSoftmaxWarps / kStreams);
-    tc::mbar_init(all_done, 1);
+    tc::mbar_init(all_done, kStreams);
     for (int i = 0; i < kCols; ++i) {
       tc::mbar_init(col_full + 8 * i, kWidenWarps);
       odd_tile[i] = 0;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
   const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);  // each of these has a unit or more
   if (threadIdx.x == 0) p.records[blockIdx.x].last = -1;
   if (blockIdx.x >= blocks) return;
-  W* origin = walks + kSoftmaxWarps + kWidenWarps;
+  W* origin = walks + kMmaWarp + kStreams;
   begin_run<kRows, kWarps>(p, share, scan, blockIdx.x, blocks, origin);
   if (warp == kMmaWarp) {
     tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
@@ -232,111 +232,110 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
   };
 
   if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kOtherRegs));
-  if (warp == kMmaWarp) {
-    // ---------------- products ----------------
+  if (warp >= kMmaWarp && warp < kMmaWarp + kStreams) {
+    // ---------------- products: a warp for each stream ----------------
     // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers; one thread issues.
     const bool leader = elect_one();
-    const uint32_t idesc_s = tc::idesc_f16(128, kTile, 0);
+    const uint32_t x = warp - kMmaWarp;
+    const uint32_t idesc_s = tc::idesc_f16(128, kTile / G::kHalves, 0);
     const uint32_t idesc_o = tc::idesc_f16(128, D, 0) | (1u << 16);  // B with n contiguous
     // a descriptor's address field counts 16 bytes and does not overflow below 256 KB: advancing is an addition
-    const uint64_t q_desc = tc::sw128_kmajor_desc(base + G::kOffQ), k_desc = tc::sw128_kmajor_desc(base + G::kOffK);
+    const uint64_t q_desc = tc::sw128_kmajor_desc(base + G::kOffQ + x * G::kOperand), k_desc = tc::sw128_kmajor_desc(base + G::kOffK);
     const uint64_t v_desc = sw128_nmajor_desc(base + G::kOffV, 16384);
-    W& w = *origin;  // (nobody else reads it once all have their own)
-    asm volatile("bar.sync 6, %0;" ::"n"(32 * (kSoftmaxWarps + kWidenWarps + 1)) : "memory");
-    // Steps (tile, stream), in this order.  Two streams: P u of the stream's tile before (the first 64 tokens as soon as their P
-    // is there), then S of this one, over P's columns.  One stream: S of this tile, then P u of the one before, which the
-    // softmax threads have turned into P meanwhile.
-    uint32_t step = 0, seg = 0;
-    uint32_t on = 0, begun = 0, firsts = 0;  // of the streams' last tiles: whether they have products; whether P u begins O
+    W& w = walks[warp];
+    if (lane == 0) w = *origin;
+    asm volatile("bar.sync 15, %0;" ::"n"(G::kActive) : "memory");
+    uint32_t t = 0, seg = 0;
     int left = 0, i = 0, prefix_tiles = 0, next_tile = 0;
-    Range seen0 = {}, seen1 = {};  // of the streams
-    auto second = [&](uint32_t x, uint32_t t) {
-      const uint32_t vb = t % kBufs;
-#pragma unroll 1
-      for (uint32_t h = 0; h < static_cast<uint32_t>(G::kHalves); ++h) {
-        const uint32_t bar = kStreams == 2 ? 2 * x + h : t & 1, phase = kStreams == 2 ? t : t >> 1;
-        wait(p_full + 8 * bar, phase, 0x71);
-        if (x == 0 && h == 0) wait(v_full + 8 * vb, t / kBufs, 0x72);
-        dead = __any_sync(0xffffffffu, dead);
-        tc::tc_fence_after();
-        if (leader) {
-          if (!dead && ((on >> x) & 1)) {
-            constexpr int kProducts = kTile / 16 / G::kHalves;
-            const uint64_t vd = v_desc + vb * (G::kOperand >> 4) + h * (kProducts * 128);
-            const uint32_t pt = tmem + (kStreams == 2 ? x : t & 1) * 128 + h * 64, ot = tmem + kTmemO + x * G::kOCols;
-            const uint32_t keep = h > 0 || !((firsts >> x) & 1) ? 1u : 0u;
-#pragma unroll
-            for (int k = 0; k < kProducts; ++k)  // P of 32 tokens lies over the first half of their scores
-              tc::mma_f16_ta(ot, pt + 32 * (k >> 1) + 8 * (k & 1), vd + k * 128, idesc_o, k > 0 ? 1u : keep);
-          }
-          tc::mma_commit(pv_done + 8 * bar);
-          if (x == kStreams - 1 && h == G::kHalves - 1) tc::mma_commit(v_free + 8 * vb);
-        }
-        __syncwarp();
-      }
-    };
-    bool more = true;
+    Range seen = {};
+    bool begun = false;
+    bool on = false, first = false;  // whether the tile before has products; whether its P u begins O
+    // Two streams: for each half of the tokens, P u of the tile before and S of this one, over P's columns: the softmax threads
+    // have the other half meanwhile.  One stream: S of this tile, then P u of the one before, which the softmax threads have
+    // turned into P meanwhile.
 #pragma unroll 1
     while (true) {
-      const uint32_t x = step % kStreams, t = step / kStreams, kb = t % kBufs;
-      if (x == 0) {
-        if (left == 0 && more) {
-          more = next(w);
-          if (more) {
-            left = w.tiles;
-            i = w.tile;
-            prefix_tiles = w.seen.head;
-            next_tile = w.seen.next - w.seen.head;
-            seen0 = stream_sees(p, w, 0);
-            if (kStreams == 2) seen1 = stream_sees(p, w, 1);
-            begun = 0;
-            ++seg;
-          }
+      bool more = left > 0, fresh = false;
+      if (!more) {
+        more = fresh = next(w);
+        if (more) {
+          left = w.tiles;
+          i = w.tile;
+          prefix_tiles = w.seen.head;
+          next_tile = w.seen.next - w.seen.head;
+          seen = stream_sees(p, w, x);
         }
       }
-      if (kStreams == 2 && t > 0) second(x, t - 1);
-      if (left > 0) {
-        if (!((begun >> (8 + x)) & 1)) {
-          wait(q_full + 8 * x, seg - 1, 0x73);
-          begun |= 256u << x;  // this segment's q is there
-        }
-        if (x == 0) wait(k_full + 8 * kb, t / kBufs, 0x74);
-        if (kStreams == 2 ? t > 0 : t > 1) wait(pv_done + 8 * (kStreams == 2 ? 2 * x + 1 : t & 1), kStreams == 2 ? t - 1 : (t - 2) >> 1, 0x75);
-        const int j0 = (i < prefix_tiles ? i : next_tile + i) * kTile;
-        const bool here = x == 0 ? within(seen0, j0) : within(seen1, j0);
-        dead = __any_sync(0xffffffffu, dead);
-        tc::tc_fence_after();
-        if (leader) {
-          if (!dead && here) {
-            const uint64_t qd = q_desc + x * (G::kOperand >> 4), kd = k_desc + kb * (G::kOperand >> 4);
-            const uint32_t st = tmem + (kStreams == 2 ? x : t & 1) * 128;
+      const uint32_t kb = t % kBufs, vb = (t - 1) % kBufs;
+      const bool here = more && within(seen, (i < prefix_tiles ? i : next_tile + i) * kTile);
+#pragma unroll 1
+      for (uint32_t h = 0; h < static_cast<uint32_t>(G::kHalves); ++h) {
+        auto weighted = [&]() {  // P u of tile t - 1
+          const uint32_t bar = kStreams == 2 ? 2 * x + h : (t - 1) & 1;
+          wait(p_full + 8 * bar, kStreams == 2 ? t - 1 : (t - 1) >> 1, 0x71);
+          if (h == 0) wait(v_full + 8 * vb, (t - 1) / kBufs, 0x72);
+          dead = __any_sync(0xffffffffu, dead);
+          tc::tc_fence_after();
+          if (leader) {
+            if (!dead && on) {
+              constexpr int kProducts = kTile / 16 / G::kHalves;
+              const uint64_t vd = v_desc + vb * (G::kOperand >> 4) + h * (kProducts * 128);
+              const uint32_t pt = tmem + (kStreams == 2 ? x : (t - 1) & 1) * 128 + h * 64, ot = tmem + kTmemO + x * G::kOCols;
+              const uint32_t keep = h > 0 || !first ? 1u : 0u;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * 1024 + (k & 3) * 2;
-              tc::mma_f16(st, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+              for (int k = 0; k < kProducts; ++k)  // P of 32 tokens lies over the first half of their scores
+                tc::mma_f16_ta(ot, pt + 32 * (k >> 1) + 8 * (k & 1), vd + k * 128, idesc_o, k > 0 ? 1u : keep);
             }
+            tc::mma_commit(pv_done + 8 * bar);
+            if (h == G::kHalves - 1) tc::mma_commit(v_free + 8 * vb);
           }
-          tc::mma_commit(s_full + 8 * (kStreams == 2 ? x : t & 1));
-          if (x == kStreams - 1) tc::mma_commit(k_free + 8 * kb);
+          __syncwarp();
+        };
+        if (kStreams == 2 && t > 0) weighted();
+        if (more) {
+          const uint32_t bar = kStreams == 2 ? 2 * x + h : t & 1;
+          if (h == 0) {
+            if (fresh) wait(q_full + 8 * x, seg, 0x73);
+            wait(k_full + 8 * kb, t / kBufs, 0x74);
+          }
+          if (t >= (kStreams == 2 ? 1 : 2)) wait(pv_done + 8 * bar, kStreams == 2 ? t - 1 : (t - 2) >> 1, 0x75);
+          dead = __any_sync(0xffffffffu, dead);
+          tc::tc_fence_after();
+          if (leader) {
+            if (!dead && here) {
+              const uint64_t kd = k_desc + kb * (G::kOperand >> 4) + h * 512;  // 64 rows of 128 bytes
+              const uint32_t st = tmem + (kStreams == 2 ? x : t & 1) * 128 + h * 64;
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * 1024 + (k & 3) * 2;
+                tc::mma_f16(st, q_desc + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+              }
+            }
+            tc::mma_commit(s_full + 8 * bar);
+            if (h == G::kHalves - 1) tc::mma_commit(k_free + 8 * kb);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (kStreams == 1 && t > 0) second(0, t - 1);
-        on = (on & ~(1u << x)) | (here ? 1u << x : 0u);
-        firsts = (firsts & ~(1u << x)) | ((begun >> x) & 1 ? 0u : 1u << x);
-        if (here) begun |= 1u << x;
-        if (x == kStreams - 1) --left, ++i;
-      } else {
-        if (kStreams == 1 && t > 0) second(0, t - 1);
-        if (x == kStreams - 1) break;
+        if (kStreams == 1 && t > 0) weighted();
       }
-      ++step;
+      if (!more) break;
+      if (fresh) {
+        ++seg;
+        begun = false;
+      }
+      on = here;
+      first = !begun;
+      begun = begun || here;
+      ++t;
+      --left;
+      ++i;
     }
     // every product is done before the tensor memory is given back, whatever else ran out
     if (leader) tc::mma_commit(all_done);
     __syncwarp();
     tc::mbar_wait_quiet(all_done, 0, p.err, 0x76);
     __syncwarp();
-  } else if (warp > kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // (fills up the group)
   } else if (warp >= kSoftmaxWarps) {
     // ---------------- loads and widening ----------------
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
     const int part0 = (warp - kSoftmaxWarps) * kParts;  // this warp's tokens of a tile: 16 each, which lie on one page
     W& w = walks[warp];
     if (lane == 0) w = *origin;
-    asm volatile("bar.sync 6, %0;" ::"n"(32 * (kSoftmaxWarps + kWidenWarps + 1)) : "memory");
+    asm volatile("bar.sync 15, %0;" ::"n"(G::kActive) : "memory");
     // A lane takes 16 bytes of codes of one row at a time and makes kPieces 16-byte chunks of fp16 of them.  Rows and
     // chunks are dealt to lanes such that, for each piece, the eight lanes of a quarter warp write to eight different bank
     // groups, and a lane's row is the same modulo 8 throughout, so that its addresses differ by constants (heads of 256 are
@@ -544,6 +543,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           }
         }
         top = __reduce_max_sync(0xffffffffu, top);
+        __syncwarp();  // (what all lanes wrote is there for those who see the arrival)
         if (lane == 0) {
           top_exp[(t % kCols) * 4 + warp - kSoftmaxWarps] = top;
           tc::mbar_arrive(k_full + 8 * buf);
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
     float* ends = reinterpret_cast<float*>(smem + G::kOffEnd);
     W& w = walks[warp];
     if (lane == 0) w = *origin;
-    asm volatile("bar.sync 6, %0;" ::"n"(32 * (kSoftmaxWarps + kWidenWarps + 1)) : "memory");
+    asm volatile("bar.sync 15, %0;" ::"n"(G::kActive) : "memory");
     auto sync_rows = [&]() {  // the warps of these rows
       if constexpr (kSubs > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + quad), "n"(32 * kSubs) : "memory");
     };
@@ -680,7 +680,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
       if (done_any) {
         if constexpr (kSubs > 1) {
           sync_rows();
-          l = ends[row] + ends[128 + row];  // in one order for both
+          const float* both = ends + (parity ^ 1) * 256 + row;
+          l = both[0] + both[128];  // in one order for both
         }
         wait(pv_done + 8 * (kStreams == 2 ? 2 * stream + 1 : (t - 1) & 1), kStreams == 2 ? t - 1 : (t - 1) >> 1, 0x7c);
         dead = __any_sync(0xffffffffu, dead);
@@ -741,22 +742,25 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
 #pragma unroll 1
       for (; i < i_end; ++i, ++t) {
         const int j0 = (i < prefix_tiles ? i : next_tile + i) * kTile;
-        wait(s_full + 8 * (kStreams == 2 ? stream : t & 1), kStreams == 2 ? t : t >> 1, 0x79);
-        if (!within(some, j0)) {  // nothing was multiplied and nothing will be
-          if (lane == 0) {
-            tc::mbar_arrive(p_full + 8 * (kStreams == 2 ? 2 * stream : t & 1));
-            if (kStreams == 2) tc::mbar_arrive(p_full + 8 * (2 * stream + 1));
-          }
-          continue;
+        const bool here = within(some, j0);  // otherwise nothing is multiplied
+        bool odd = false;
+        float top = 0.0f;
+        if (here) {
+          wait(col_full + 8 * (t % kCols), t / kCols, 0x7a);
+          odd = odd_tile[t % kCols] == t + 1;
+          const int4 te = *reinterpret_cast<const int4*>(top_exp + (t % kCols) * 4);
+          top = static_cast<float>(max(max(te.x, te.y), max(te.z, te.w)));
         }
-        wait(col_full + 8 * (t % kCols), t / kCols, 0x7a);
-        dead = __any_sync(0xffffffffu, dead);
-        tc::tc_fence_after();
-        const bool odd = odd_tile[t % kCols] == t + 1;
-        const int4 te = *reinterpret_cast<const int4*>(top_exp + (t % kCols) * 4);
-        const float top = static_cast<float>(max(max(te.x, te.y), max(te.z, te.w)));
 #pragma unroll 1
         for (int h = 0; h < G::kHalves; ++h) {
+        const uint32_t bar = kStreams == 2 ? 2 * stream + h : t & 1;
+        wait(s_full + 8 * bar, kStreams == 2 ? t : t >> 1, 0x79);
+        if (!here) {
+          if (lane == 0) tc::mbar_arrive(p_full + 8 * bar);
+          continue;
+        }
+        dead = __any_sync(0xffffffffu, dead);
+        tc::tc_fence_after();
         const int part = kSubs > 1 ? sub : h;  // of the tile's two times 64 tokens
         const uint32_t s_at = lanes + (kStreams == 2 ? stream : t & 1) * 128 + part * 64;
         float keep = 1.0f;
@@ -883,9 +887,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         }
         }
         if (__any_sync(0xffffffffu, keep != 1.0f) && begun) {  // (NaN too)
-          // P u of what came before: of the tile before, with two streams, it is (S went over its P); of this one's first half
+          // all P u of what came before
           if (kStreams == 1) wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x7b);
-          else if (h == 1) wait(pv_done + 8 * (2 * stream), t, 0x7b);
+          else wait(pv_done + 8 * (2 * stream + (h ^ 1)), h == 0 ? t - 1 : t, 0x7b);
           dead = __any_sync(0xffffffffu, dead);
           tc::tc_fence_after();
 #pragma unroll 1
@@ -907,13 +911,13 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full + 8 * (kStreams == 2 ? 2 * stream + h : t & 1));
+        if (lane == 0) tc::mbar_arrive(p_full + 8 * bar);
         }
       }
 
       const float2 lp = unpair(l2);
       l = lp.x + lp.y;
-      if constexpr (kSubs > 1) ends[sub * 128 + row] = l;
+      if constexpr (kSubs > 1) ends[parity * 256 + sub * 128 + row] = l;
       live = some.high >= 0;
       parity ^= 1;
     }
