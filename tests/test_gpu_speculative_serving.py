@@ -1,0 +1,150 @@
+"""The serving operators run together, as examples/speculative_serving.py does: pages
+and slots from lengths, prompts in chunks, trees of drafts, verification, kept paths;
+each pass checked on what the passes before it left.
+
+Tolerances.  Attention: as in test_gpu_chunk_attention.py (prompts) and
+test_gpu_tree_attention.py (trees), for the q and the codes that the pass itself
+wrote.  Pages, places, paths, tokens, moved codes: equal."""
+
+import importlib.util
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from conftest import ROOT
+from oracle import attention as ref
+from oracle import serving
+
+pytestmark = pytest.mark.gpu
+
+
+def _example():
+    spec = importlib.util.spec_from_file_location("speculative_serving", os.path.join(ROOT, "examples", "speculative_serving.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def _rows(cache, b, n):
+    """Codes and scales of a sequence's first n tokens, and what they stand for."""
+    at = torch.arange(n, device="cuda")
+    page, off = cache.table[b, at // cache.page].long(), at % cache.page
+    raw = [t[page, :, off].cpu().numpy() for t in cache.tensors]
+    return raw, [ref.kv_values(raw[i], raw[2 + i], cache.fmt) for i in range(2)]
+
+
+def _state(cache):
+    return serving.Pages(cache.table.tolist(), cache.held.tolist(), cache.free[:int(cache.count)].tolist(), cache.page, cache.table.shape[1])
+
+
+def _check_pages(p, cache, state, ctx, new, depths=None):
+    bounds, positions, slots = state.assign(ctx, new, p.slots.numel(), depths)
+    assert p.indptr.tolist() == bounds and p.positions.tolist() == positions and p.slots.tolist() == slots
+    assert cache.held.tolist() == state.held and cache.free[:int(cache.count)].tolist() == state.free
+    for b, n in enumerate(state.held):
+        assert cache.table[b, :n].tolist() == state.table[b][:n]
+
+
+def _close(got, o, w, moved, err, length, top):
+    s = (length + 64) * 2.0 ** -24
+    tol = moved + (err[..., None] + 2.0 ** -11 + s) * w + length * 2.0 ** -34 * top
+    tol = tol + 2.0 ** -11 * (np.abs(o) + tol) + 2.0 ** -25
+    assert (np.abs(got - o) <= tol).all(), np.nanmax(np.abs(got - o) / tol)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+def test_prompts_drafts_and_kept_paths(qlin_gpu, fmt):
+    ex = _example()
+    seqs, vocab, d, page, chunk = 3, 512, 64, 16, 90
+    model = ex.Model(vocab, 256, 8, 2, d)
+    cache = ex.Cache(seqs, 240, 40, 2, d, fmt, page)
+    gen = torch.Generator().manual_seed(4)
+    prefill = ex.Prefill(model, cache, chunk, window=50, prefix_lens=torch.tensor([4, 0, 100], **ex.I32))
+    lens = [0] * seqs
+    for new in ([90, 33, 1], [40, 0, 77]):  # prompts of different lengths, one of them done early
+        state = _state(cache)
+        tokens = [torch.randint(vocab, (n,), generator=gen).cuda() for n in new]
+        prefill.run(tokens, torch.rand(seqs, generator=gen).cuda())
+        torch.cuda.synchronize()
+        assert qlin_gpu.qlin_get_device_error() == 0
+        _check_pages(prefill, cache, state, lens, new)
+        q, got = prefill.q.double().cpu().numpy(), prefill.att.double().cpu().numpy()
+        a = 0
+        for b, n in enumerate(new):
+            if n > 0:
+                _, (k, v) = _rows(cache, b, lens[b] + n)
+                o, _, w, moved, err = serving.chunk_attention(q[a:a + n], k, v, lens[b], d ** -0.5, window=50,
+                                                              prefix=min([4, 0, 100][b], lens[b] + n))
+                _close(got[a:a + n], o, w, moved, err, lens[b] + n, np.abs(v).max())
+            a += n
+        lens = [x + n for x, n in zip(lens, new)]
+        assert cache.ctx.tolist() == lens
+
+    parents = [-1, 0, 0, 0, 1, 1, 2, 4, 4, 6, 7]
+    n, depth = len(parents), ex.tree_words(parents, 1)[1].tolist()
+    seen = ((ex.tree_words(parents, 1)[0].numpy()[:, :1] >> np.arange(n)) & 1).astype(bool)
+    step = ex.Speculate(model, cache, parents)
+    longest = 0
+    for turn in range(4):
+        state, last = _state(cache), cache.last.tolist()
+        accept, sample = torch.rand(seqs * n, generator=gen), torch.rand(seqs, generator=gen)
+        if turn == 2:
+            accept.zero_()  # every draft that the target gives any weight
+        if step.graph is None:
+            step.capture()
+            assert cache.ctx.tolist() == lens and cache.last.tolist() == last
+        # the step's state before the kept paths move: the same launches without the last three
+        pages_before = [t.clone() for t in (cache.table, cache.held, cache.free, cache.count)]
+        step.accept.copy_(accept)
+        step.sample.copy_(sample)
+        step.draft()
+        probs = model.probabilities(step.hidden())
+        torch.cuda.synchronize()
+        before = [_rows(cache, b, lens[b] + n) for b in range(seqs)]
+        for t, old in zip((cache.table, cache.held, cache.free, cache.count), pages_before):
+            t.copy_(old)
+        step.run(accept, sample)
+        torch.cuda.synchronize()
+        assert qlin_gpu.qlin_get_device_error() == 0
+        _check_pages(step, cache, state, lens, [n] * seqs, depth * seqs)
+        assert torch.equal(step.probs, probs)
+        q, got = step.q.double().cpu().numpy(), step.att.double().cpu().numpy()
+        for b in range(seqs):
+            at = slice(b * n, (b + 1) * n)
+            raw, (k, v) = before[b]
+            bits = np.ones((n, lens[b] + n), bool)
+            bits[:, lens[b]:] = seen
+            o, _, w, spread = ref.tree_attention(q[at], k, v, bits, d ** -0.5)
+            tol = (2.0 ** -11 + 2 * d * 2.0 ** -24 * spread + (lens[b] + n + 64) * 2.0 ** -24)[..., None] * w
+            assert (np.abs(got[at] - o) <= tol + 2.0 ** -11 * np.abs(o) + 2.0 ** -24).all()
+            toks = step.tokens[at].tolist()
+            assert toks[0] == last[b]
+            path, token = serving.verify(step.probs[at].cpu().numpy(), None, parents, toks, accept[at].numpy(), float(sample[b]))
+            assert step.path[b].tolist() == path + [-1] * (n - len(path)) and int(step.kept[b]) == len(path)
+            assert int(cache.last[b]) == token
+            after, _ = _rows(cache, b, lens[b] + len(path))
+            for x, y in zip(raw, after):
+                assert np.array_equal(y[:lens[b]], x[:lens[b]]) and np.array_equal(y[lens[b]:], x[lens[b]:][path])
+            longest = max(longest, len(path))
+            lens[b] += len(path)
+        assert cache.ctx.tolist() == lens
+    assert longest > 1  # (accept of 0 takes a draft of any weight)
+
+    # all pages go back
+    cache.ctx.zero_()
+    step.new.zero_()
+    step.assign.run()
+    torch.cuda.synchronize()
+    assert int(cache.count) == 40 and sorted(cache.free.tolist()) == list(range(40)) and not cache.held.any()
+    assert qlin_gpu.qlin_get_device_error() == 0
+
+
+def test_the_command_runs(qlin_gpu):
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "speculative_serving.py"), "--hidden", "512", "--heads", "8",
+                        "--kv-heads", "2", "--vocab", "1024", "--seqs", "2", "--prompt", "300", "--chunk", "128", "--steps", "2"],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "pages free" in r.stdout, r.stdout + r.stderr
