@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
             for (int k1 = 0; k1 < kStep; k1 += 32) {
               const int c = jc + k1;
               uint32_t bits = low_bits(at + 1 - c);
-              if (p.window > 0) bits &= ~low_bits(at - p.window + 1 - c);
+              if (p.window > 0) bits &= ~low_bits(max(at + 1 - c, 0) - p.window);  // (without overflow)
               bits |= low_bits(prefix - c);
 #pragma unroll
               for (int k = 0; k < 32; ++k)
@@ -1014,18 +1014,43 @@ int64_t part_rows(const qlin_kv_cache& c, int64_t hq, int64_t max_new) {
   return std::min<int64_t>(c.head_dim == 256 ? 128 : 256, max_new > 256 ? 256 : max_new * group);
 }
 
+// Up to 16 rows per key head the kernel of few rows answers plain scores: it has no tile of 256 rows to fill.  64 single tokens
+// behind 1000 (32 query heads on 8 of 128, INT8) take 51 us there and 122 us here, 4 tokens behind 16000 27 and 47; with 32
+// rows the two are within a third of each other, with 128 it is 55 and 48 us.
+bool few_rows(const qlin_kv_cache& c, int64_t hq, int64_t max_new) { return max_new * (hq / c.heads) <= 16; }
+
 }  // namespace
 }  // namespace chunk
 
-int64_t chunk_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t hq, int64_t max_new, int64_t) {
+int64_t chunk_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t hq, int64_t max_new, int64_t B) {
   const int64_t blocks = sm_count();
-  return blocks * static_cast<int64_t>(sizeof(tree::Record)) + 256 +
-         2 * blocks * chunk::part_rows(cache, hq, max_new) * (cache.head_dim * 4 + static_cast<int64_t>(sizeof(float2)));
+  const int64_t own = blocks * static_cast<int64_t>(sizeof(tree::Record)) + 256 +
+                      2 * blocks * chunk::part_rows(cache, hq, max_new) * (cache.head_dim * 4 + static_cast<int64_t>(sizeof(float2)));
+  return chunk::few_rows(cache, hq, max_new) ? std::max(own, tree_attention_workspace_bytes(cache, hq, max_new, B)) : own;
 }
 
 cudaError_t plan_chunk_attention(const ChunkAttentionArgs& a, Prepared* out) {
   chunk::Params p = {};
   const qlin_kv_cache& c = a.cache;
+  const bool plain = a.scores.softcap == 0.0f && a.scores.slopes == nullptr && a.scores.window == 0 && a.scores.prefix_lens == nullptr;
+  if (plain && chunk::few_rows(c, a.q.heads, a.max_new)) {
+    TreeAttentionArgs t = {};
+    t.q = a.q;
+    t.out = a.out;
+    t.dtype = a.dtype;
+    t.Tq = a.Tq;
+    t.cache = c;
+    t.block_table = a.block_table;
+    t.max_pages = a.max_pages;
+    t.q_indptr = a.q_indptr;
+    t.ctx_lens = a.ctx_lens;
+    t.B = a.B;
+    t.max_nodes = a.max_new;
+    t.scale = a.scores.scale;
+    t.lse = a.lse;
+    t.workspace = a.workspace;
+    return plan_tree_attention(t, out);
+  }
   p.q = static_cast<const uint8_t*>(a.q.data);
   p.out = static_cast<uint8_t*>(a.out.data);
   p.qt = 2 * a.q.token_stride;

@@ -86,6 +86,29 @@ __device__ __forceinline__ int64_t units_of_head(const Params& p, const Sequence
   return sum;
 }
 
+// Units of sequence b (none from `end` on), each lane its own: short ones are counted by their lanes side by side, so that a
+// batch of many sequences costs few turns, long ones by the whole warp.
+template <int ROWS>
+__device__ __forceinline__ int64_t units_of(const Params& p, int b, int end) {
+  constexpr int kShort = 4;  // row tiles
+  const int lane = threadIdx.x % 32;
+  int n = 0;
+  int64_t sum = 0;
+  if (b < end) {
+    const Sequence s = sequence(p, b);
+    n = row_tiles<ROWS>(s);
+    if (n <= kShort)
+      for (int r = 0; r < n; ++r) sum += tiles_of_row_tile<ROWS>(p, s, r).count;
+  }
+  __syncwarp();
+  for (unsigned longer = __ballot_sync(0xffffffffu, n > kShort); longer != 0; longer &= longer - 1) {
+    const int of = __ffs(longer) - 1;
+    const int64_t v = units_of_head<ROWS>(p, sequence(p, b - lane + of));
+    if (lane == of) sum = v;
+  }
+  return sum * p.hk;
+}
+
 // Walks a block's run of units (token tiles of row tiles of key heads of sequences, in this order), one segment (row
 // tile) at a time.
 template <int ROWS>
@@ -126,7 +149,10 @@ template <int ROWS, int WARPS>
 __device__ __forceinline__ void scan_units(const Params& p, int share, int64_t* scan) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int64_t sum = 0;
-  for (int b = warp * share; b < min(p.B, (warp + 1) * share); ++b) sum += units_of_head<ROWS>(p, sequence(p, b)) * p.hk;
+  const int end = min(p.B, (warp + 1) * share);
+  for (int b0 = warp * share; b0 < end; b0 += 32) sum += units_of<ROWS>(p, b0 + lane, end);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) scan[warp + 1] = sum;
   if (threadIdx.x == 0) scan[0] = 0;
   __syncthreads();
@@ -142,13 +168,24 @@ __device__ __forceinline__ void begin_run(const Params& p, int share, const int6
   const int64_t total = scan[WARPS], at = total * block / blocks;
   if (scan[warp] <= at && at < scan[warp + 1]) {
     int64_t rest = at - scan[warp];
-    for (int b = warp * share; b < min(p.B, (warp + 1) * share); ++b) {
-      const Sequence s = sequence(p, b);
-      const int64_t of_head = units_of_head<ROWS>(p, s);
-      if (rest >= of_head * p.hk) {
-        rest -= of_head * p.hk;
+    const int b_end = min(p.B, (warp + 1) * share);
+    for (int b0 = warp * share; b0 < b_end; b0 += 32) {
+      const int64_t units = units_of<ROWS>(p, b0 + lane, b_end);
+      int64_t sums = units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, sums, o);
+        if (lane >= o) sums += x;
+      }
+      const unsigned holds = __ballot_sync(0xffffffffu, sums > rest);
+      if (holds == 0) {
+        rest -= __shfl_sync(0xffffffffu, sums, 31);
         continue;
       }
+      const int of = __ffs(holds) - 1, b = b0 + of;
+      rest -= __shfl_sync(0xffffffffu, sums - units, of);
+      const int64_t of_head = __shfl_sync(0xffffffffu, units, of) / p.hk;
+      const Sequence s = sequence(p, b);
       const int head = static_cast<int>(rest / of_head);
       rest -= head * of_head;
       const int n = row_tiles<ROWS>(s);

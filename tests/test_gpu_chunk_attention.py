@@ -284,3 +284,92 @@ def test_as_attention_of_a_chain(qlin_gpu):
     q.qlin_tree_attention(p.q.cuda(), p.cache, *p.dev, None, out, ws, 100, scale=p.scale, lse=lse)
     p.out, p.lse = out, lse
     p.check()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("hq,hk,d,most", [(8, 8, 128, 1), (8, 2, 128, 4), (32, 2, 64, 1), (10, 2, 256, 3), (10, 2, 256, 4), (3, 1, 64, 6)])
+def test_few_rows(qlin_gpu, fmt, hq, hk, d, most):
+    """Single tokens and a few of them, as a decode step has them, on both sides of 16 rows per key head."""
+    seqs = [(0, 1), (700, most), (16, 0), (127, 1), (128, most), (2100, 1), (5, most)]
+    for dtype in (torch.float16, torch.bfloat16):
+        Problem(qlin_gpu, seqs, hq, hk, d, 16, fmt, dtype, spare_rows=2).run().check()
+    # a call planned for more, and one with a window that takes everything
+    Problem(qlin_gpu, seqs, hq, hk, d, 16, fmt, torch.float16, spare_rows=2).run(most=300).check()
+    Problem(qlin_gpu, seqs, hq, hk, d, 16, fmt, torch.float16, spare_rows=2, window=2 ** 31 - 1).run().check()
+
+
+@pytest.mark.parametrize("seqs,new", [(200, 1), (200, 9), (33, 70), (1, 1)])
+def test_many_sequences(qlin_gpu, seqs, new):
+    """Batches whose sequences a block counts side by side, long and short ones in turn; also those with none at all."""
+    r = np.random.default_rng(seqs + new)
+    which = [(int(r.integers(0, 400)), int(r.integers(0, new + 1)) if b % 17 else 260) for b in range(seqs)]
+    Problem(qlin_gpu, which, 8, 2, 64, 32, "int8", torch.float16, window=0 if new > 1 else 300, spare_rows=1).run().check()
+
+
+def test_no_new_tokens(qlin_gpu):
+    p = Problem(qlin_gpu, [(100, 3), (40, 5)], 4, 2, 128, 16, "int8", torch.float16, window=50)
+    p.indptr = torch.zeros(3, dtype=torch.int32)
+    p.run()
+    assert (p.out == 3).all() and (p.lse == 3).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "u4"])
+def test_scales_of_the_scores(qlin_gpu, fmt):
+    """Zero and negative scales; the widest window; a prefix of everything; a row far behind the first of a long chunk."""
+    for scale in (0.0, -0.05):
+        Problem(qlin_gpu, [(100, 140)], 4, 2, 128, 16, fmt, torch.bfloat16, scale=scale, softcap=3.0).run().check()
+    Problem(qlin_gpu, [(1, 700)], 4, 2, 64, 16, fmt, torch.float16, window=2 ** 31 - 65537, prefix=[701]).run().check()
+
+
+@pytest.mark.parametrize("d,most", [(128, 1), (256, 60), (64, 300)])
+def test_two_calls_on_two_streams(qlin_gpu, d, most):
+    """Calls with workspaces of their own run side by side; a captured and a plain one of the same data too."""
+    q = qlin_gpu
+    a = Problem(q, [(900, most), (30, 1)], 8, 2, d, 16, "int8", torch.float16, seed=1)
+    b = Problem(q, [(5, 1), (1500, most)], 8, 2, d, 16, "e4m3", torch.bfloat16, seed=2)
+    calls, streams = [a.prepare(), b.prepare()], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls[0].run()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        calls[1].run(streams[1])
+    torch.cuda.synchronize()
+    assert q.qlin_get_device_error() == 0
+    a.check()
+    b.check()
+
+
+def test_rows_of_infinity(qlin_gpu):
+    """A row of q with an infinity or a NaN reaches no other row."""
+    for dtype in (torch.float16, torch.bfloat16):
+        p = Problem(qlin_gpu, [(60, 150)], 4, 2, 128, 16, "int8", dtype).run()
+        clean, clean_lse = p.out.clone(), p.lse.clone()
+        p.q[7, 1, 5], p.q[80, 3, 0], p.q[149, 0, 127] = float("inf"), float("nan"), -float("inf")
+        p.run()
+        hit = torch.zeros(p.q.shape[:2], dtype=torch.bool)
+        hit[7, 1] = hit[80, 3] = hit[149, 0] = True
+        assert torch.equal(p.out[~hit.cuda()], clean[~hit.cuda()]) and torch.equal(p.lse[~hit.cuda()], clean_lse[~hit.cuda()])
+        assert not torch.isfinite(p.out[hit.cuda()]).all()
+
+
+def test_a_cache_beyond_32_bits(qlin_gpu):
+    """Pages whose bytes and scales lie beyond 2^32 bytes, at the end of a large cache."""
+    q, hk, d, page, n = qlin_gpu, 2, 128, 64, 70
+    pages = (2 ** 32 + 2 ** 28) // (hk * page * d)
+    kv_ = [torch.zeros(pages, hk, page, d, dtype=torch.int8, device="cuda") for _ in range(2)]
+    sc = [torch.zeros(pages, hk, page, device="cuda") for _ in range(2)]
+    p = Problem(q, [(300, n), (17, 1)], 8, hk, d, page, "int8", torch.float16)
+    some = p.t[0].shape[0]
+    first = pages - some
+    for big, small in zip((*kv_, *sc), p.t):
+        big[first:] = small
+    p.cache = q.qlin_kv_cache(*kv_, *sc, q.QLIN_KV_INT8)
+    near = p.table.clone()
+    p.table = torch.where(near >= 0, near + first, near)
+    p.run()
+    p.table = near
+    p.check()
