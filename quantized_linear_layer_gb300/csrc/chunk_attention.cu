@@ -65,7 +65,7 @@ struct Geo {
   static constexpr int kWidenWarps = 4, kMmaWarp = kSoftmaxWarps + kWidenWarps;
   static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps, kActive = 32 * (kMmaWarp + kStreams);
   static constexpr int kLaunchRegs = 128;
-  static constexpr int kSoftmaxRegs = D == 256 ? 104 : 120, kWidenRegs = D == 256 ? 232 : 200, kOtherRegs = 64;
+  static constexpr int kSoftmaxRegs = D == 256 ? 104 : 136, kWidenRegs = D == 256 ? 232 : 168, kOtherRegs = 64;
   static_assert(kSoftmaxWarps * kSoftmaxRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kWarps * kLaunchRegs, "registers");
   static constexpr int kParts = kTile / 16 / kWidenWarps;  // 16 tokens each, of a widening warp
   static constexpr int kRowBytes = kU4 ? D / 2 : D;
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
     if constexpr (G::kSoftmaxRegs > G::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kSoftmaxRegs));
     constexpr int kMine = G::kMine;
-    constexpr int kStep = 32;  // tokens weighed at a time
+    constexpr int kStep = kSubs > 1 ? 32 : 64;  // tokens weighed at a time
     const int quad = warp & 3;
     const int stream = kStreams == 2 ? warp >> 2 : 0, sub = kStreams == 2 ? 0 : warp >> 2;
     const int row = quad * 32 + lane;  // of the stream
@@ -753,165 +753,167 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         }
 #pragma unroll 1
         for (int h = 0; h < G::kHalves; ++h) {
-        const uint32_t bar = kStreams == 2 ? 2 * stream + h : t & 1;
-        wait(s_full + 8 * bar, kStreams == 2 ? t : t >> 1, 0x79);
-        if (!here) {
-          if (lane == 0) tc::mbar_arrive(p_full + 8 * bar);
-          continue;
-        }
-        dead = __any_sync(0xffffffffu, dead);
-        tc::tc_fence_after();
-        const int part = kSubs > 1 ? sub : h;  // of the tile's two times 64 tokens
-        const uint32_t s_at = lanes + (kStreams == 2 ? stream : t & 1) * 128 + part * 64;
-        float keep = 1.0f;
-#pragma unroll 1
-        for (int c0 = 0; c0 < 64; c0 += kStep) {
-        const int jc = j0 + part * 64 + c0;
-        const uint32_t col = base + G::kOffCol + ((t % kCols) * 2 * kTile + part * 64 + c0) * 4;
-
-        // t of these tokens from their products
-        auto score = [&](uint32_t (&v)[kStep]) {
-          if (scaled) {
-            const uint64_t rs = pair(row_scale, row_scale);
-#pragma unroll
-            for (int k = 0; k < kStep; k += 2) {
-              const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rs));
-              v[k] = __float_as_uint(a.x);
-              v[k + 1] = __float_as_uint(a.y);
-            }
+          const uint32_t bar = kStreams == 2 ? 2 * stream + h : t & 1;
+          wait(s_full + 8 * bar, kStreams == 2 ? t : t >> 1, 0x79);
+          if (!here) {
+            if (lane == 0) tc::mbar_arrive(p_full + 8 * bar);
+            continue;
           }
-          if (SHAPED && cap2 > 0.0f) {
-#pragma unroll
-            for (int k = 0; k < kStep; k += 4) {
-              const float4 sk = lds4(col + 4 * k);
-              const float ks[4] = {sk.x, sk.y, sk.z, sk.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float r = rcp(1.0f + ex2(__uint_as_float(v[k + e]) * ks[e]));
-                v[k + e] = __float_as_uint(fmaf(r, -2.0f * cap2, cap2));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < kStep; k += 4) {
-              const float4 sk = lds4(col + 4 * k);
-              const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y)));
-              const float2 b = unpair(mul2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), pair(sk.z, sk.w)));
-              v[k] = __float_as_uint(a.x);
-              v[k + 1] = __float_as_uint(a.y);
-              v[k + 2] = __float_as_uint(b.x);
-              v[k + 3] = __float_as_uint(b.y);
-            }
-          }
-          if (SHAPED && p.slopes != nullptr) {
-            const float off = static_cast<float>(jc - at);  // exact below 2^24
-#pragma unroll
-            for (int k = 0; k < kStep; ++k)
-              v[k] = __float_as_uint(fmaf(slope2, fabsf(off + static_cast<float>(k)), __uint_as_float(v[k])));
-          }
-          if (!within(all, jc)) {
-#pragma unroll
-            for (int k1 = 0; k1 < kStep; k1 += 32) {
-              const int c = jc + k1;
-              uint32_t bits = low_bits(at + 1 - c);
-              if (p.window > 0) bits &= ~low_bits(max(at + 1 - c, 0) - p.window);  // (without overflow)
-              bits |= low_bits(prefix - c);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((bits >> k) & 1u)) v[k1 + k] = 0xff800000u;
-            }
-          }
-        };
-        {
-          uint32_t v[kStep];
-          tc::tmem_ld_32x32b_x32(s_at + c0, v);
-          tc::tmem_wait_ld(v);
-          score(v);
-          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int k = 0; k < kStep; k += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1])));
-          float hi = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) + top;  // no product with a value scale is above 2^this
-          if constexpr (kSubs > 1) {  // over both threads of the row; and both have their scores: P may go over them
-            float* maxima = row_max + (c0 / kStep & 1) * kSubs * 128 + row;
-            maxima[sub * 128] = hi;
-            sync_rows();
-            hi = fmaxf(hi, maxima[(sub ^ 1) * 128]);
-          }
-          if (__any_sync(0xffffffffu, hi > ref + (kOffset + kSlack))) {  // (the same in all warps of these rows)
-            // The reference moves, by a whole number of powers of two, so that the row's probabilities that wait for the products
-            // already can be scaled in fp16.  With more to come its largest one goes six bits below the top of fp16, which it may
-            // grow by before the row has to be rescaled.
-            const float to = hi > ref + (kOffset + kSlack) ? ceilf(hi) - 9.0f : ref;
-            const float before = ref, f = ex2(ref - to);
-            ref = to;
-            keep *= f;
-            l2 = mul2(l2, pair(f, f));
-            if (c0 > 0) {
-              // in two steps: down to 2^-39 of P may be left, and fp16 ends at 2^-24
-              const float e = fmaxf(before - to, -48.0f), e1 = floorf(0.5f * e);
-              const __half2 f1 = __float2half2_rn(ex2(e1)), f2 = __float2half2_rn(ex2(e - e1));
-              uint32_t o[16];
-              tc::tmem_wait_st();
-              tc::tmem_ld_32x32b_x16(s_at, o);
-              tc::tmem_wait_ld(o);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = hmul2(hmul2(o[k], *reinterpret_cast<const uint32_t*>(&f1)), *reinterpret_cast<const uint32_t*>(&f2));
-              tc::tmem_st_32x32b_x16(s_at, o);
-            }
-          }
-          const uint64_t nref = pair(-ref, -ref);
-          auto weigh = [&](auto with_odd) {
-#pragma unroll
-            for (int k = 0; k < kStep; k += 4) {
-              const float4 sv = lds4(col + 4 * (kTile + k));
-              const float ss[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-              for (int x = 0; x < 4; x += 2) {
-                const float2 a = unpair(add2(pair(__uint_as_float(v[k + x]), __uint_as_float(v[k + x + 1])), nref));
-                const uint64_t e = pair(ex2(a.x), ex2(a.y));
-                l2 = add2(l2, e);
-                float2 f = unpair(mul2(e, pair(ss[x], ss[x + 1])));
-                if constexpr (decltype(with_odd)::value) {  // (what is hidden has no product with a scale that is not a number)
-                  if (v[k + x] == 0xff800000u) f.x = 0.0f;
-                  if (v[k + x + 1] == 0xff800000u) f.y = 0.0f;
-                }
-                v[(k + x) / 2] = kv::pack2<0>(f.x, f.y);
-              }
-            }
-          };
-          if (odd) weigh(std::true_type{});
-          else weigh(std::false_type{});
-          tc::tmem_st_32x32b_x16(s_at + c0, v);  // over the first half of their scores
-        }
-        }
-        if (__any_sync(0xffffffffu, keep != 1.0f) && begun) {  // (NaN too)
-          // all P u of what came before
-          if (kStreams == 1) wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x7b);
-          else wait(pv_done + 8 * (2 * stream + (h ^ 1)), h == 0 ? t - 1 : t, 0x7b);
           dead = __any_sync(0xffffffffu, dead);
           tc::tc_fence_after();
+          const int part = kSubs > 1 ? sub : h;  // of the tile's two times 64 tokens
+          const uint32_t s_at = lanes + (kStreams == 2 ? stream : t & 1) * 128 + part * 64;
+          float keep = 1.0f;
 #pragma unroll 1
-          for (int cc = 0; cc < kMine; cc += 16) {
-            uint32_t o[16];
-            tc::tmem_ld_32x32b_x16(o_at + cc, o);
-            tc::tmem_wait_ld(o);
+          for (int c0 = 0; c0 < 64; c0 += kStep) {
+            const int jc = j0 + part * 64 + c0;
+            const uint32_t col = base + G::kOffCol + ((t % kCols) * 2 * kTile + part * 64 + c0) * 4;
+
+            // t of these tokens from their products
+            auto score = [&](uint32_t (&v)[kStep]) {
+              if (scaled) {
+                const uint64_t rs = pair(row_scale, row_scale);
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float2 f = unpair(mul2(pair(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), pair(keep, keep)));
-              o[k] = __float_as_uint(f.x);
-              o[k + 1] = __float_as_uint(f.y);
+                for (int k = 0; k < kStep; k += 2) {
+                  const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), rs));
+                  v[k] = __float_as_uint(a.x);
+                  v[k + 1] = __float_as_uint(a.y);
+                }
+              }
+              if (SHAPED && cap2 > 0.0f) {
+#pragma unroll
+                for (int k = 0; k < kStep; k += 4) {
+                  const float4 sk = lds4(col + 4 * k);
+                  const float ks[4] = {sk.x, sk.y, sk.z, sk.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const float r = rcp(1.0f + ex2(__uint_as_float(v[k + e]) * ks[e]));
+                    v[k + e] = __float_as_uint(fmaf(r, -2.0f * cap2, cap2));
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < kStep; k += 4) {
+                  const float4 sk = lds4(col + 4 * k);
+                  const float2 a = unpair(mul2(pair(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), pair(sk.x, sk.y)));
+                  const float2 b = unpair(mul2(pair(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), pair(sk.z, sk.w)));
+                  v[k] = __float_as_uint(a.x);
+                  v[k + 1] = __float_as_uint(a.y);
+                  v[k + 2] = __float_as_uint(b.x);
+                  v[k + 3] = __float_as_uint(b.y);
+                }
+              }
+              if (SHAPED && p.slopes != nullptr) {
+                const float off = static_cast<float>(jc - at);  // exact below 2^24
+#pragma unroll
+                for (int k = 0; k < kStep; ++k)
+                  v[k] = __float_as_uint(fmaf(slope2, fabsf(off + static_cast<float>(k)), __uint_as_float(v[k])));
+              }
+              if (!within(all, jc)) {
+#pragma unroll
+                for (int k1 = 0; k1 < kStep; k1 += 32) {
+                  const int c = jc + k1;
+                  uint32_t bits = low_bits(at + 1 - c);
+                  if (p.window > 0) bits &= ~low_bits(max(at + 1 - c, 0) - p.window);  // (without overflow)
+                  bits |= low_bits(prefix - c);
+#pragma unroll
+                  for (int k = 0; k < 32; ++k)
+                    if (!((bits >> k) & 1u)) v[k1 + k] = 0xff800000u;
+                }
+              }
+            };
+            {
+              uint32_t v[kStep];
+#pragma unroll
+              for (int k = 0; k < kStep; k += 32) tc::tmem_ld_32x32b_x32(s_at + c0 + k, v + k);
+              tc::tmem_wait_ld(v);
+              score(v);
+              float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int k = 0; k < kStep; k += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fmaxf(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1])));
+              float hi = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) + top;  // no product with a value scale is above 2^this
+              if constexpr (kSubs > 1) {  // over both threads of the row; and both have their scores: P may go over them
+                float* maxima = row_max + (c0 / kStep & 1) * kSubs * 128 + row;
+                maxima[sub * 128] = hi;
+                sync_rows();
+                hi = fmaxf(hi, maxima[(sub ^ 1) * 128]);
+              }
+              if (__any_sync(0xffffffffu, hi > ref + (kOffset + kSlack))) {  // (the same in all warps of these rows)
+                // The reference moves, by a whole number of powers of two, so that the row's probabilities that wait for the products
+                // already can be scaled in fp16.  With more to come its largest one goes six bits below the top of fp16, which it may
+                // grow by before the row has to be rescaled.
+                const float to = hi > ref + (kOffset + kSlack) ? ceilf(hi) - 9.0f : ref;
+                const float before = ref, f = ex2(ref - to);
+                ref = to;
+                keep *= f;
+                l2 = mul2(l2, pair(f, f));
+                if (c0 > 0) {
+                  // in two steps: down to 2^-39 of P may be left, and fp16 ends at 2^-24
+                  const float e = fmaxf(before - to, -48.0f), e1 = floorf(0.5f * e);
+                  const __half2 f1 = __float2half2_rn(ex2(e1)), f2 = __float2half2_rn(ex2(e - e1));
+                  uint32_t o[16];
+                  tc::tmem_wait_st();
+                  tc::tmem_ld_32x32b_x16(s_at, o);
+                  tc::tmem_wait_ld(o);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) o[k] = hmul2(hmul2(o[k], *reinterpret_cast<const uint32_t*>(&f1)), *reinterpret_cast<const uint32_t*>(&f2));
+                  tc::tmem_st_32x32b_x16(s_at, o);
+                }
+              }
+              const uint64_t nref = pair(-ref, -ref);
+              auto weigh = [&](auto with_odd) {
+#pragma unroll
+                for (int k = 0; k < kStep; k += 4) {
+                  const float4 sv = lds4(col + 4 * (kTile + k));
+                  const float ss[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+                  for (int x = 0; x < 4; x += 2) {
+                    const float2 a = unpair(add2(pair(__uint_as_float(v[k + x]), __uint_as_float(v[k + x + 1])), nref));
+                    const uint64_t e = pair(ex2(a.x), ex2(a.y));
+                    l2 = add2(l2, e);
+                    float2 f = unpair(mul2(e, pair(ss[x], ss[x + 1])));
+                    if constexpr (decltype(with_odd)::value) {  // (what is hidden has no product with a scale that is not a number)
+                      if (v[k + x] == 0xff800000u) f.x = 0.0f;
+                      if (v[k + x + 1] == 0xff800000u) f.y = 0.0f;
+                    }
+                    v[(k + x) / 2] = kv::pack2<0>(f.x, f.y);
+                  }
+                }
+              };
+              if (odd) weigh(std::true_type{});
+              else weigh(std::false_type{});
+#pragma unroll
+              for (int k = 0; k < kStep; k += 32) tc::tmem_st_32x32b_x16(s_at + c0 + k, v + k / 2);  // over the first half of their scores
             }
-            tc::tmem_st_32x32b_x16(o_at + cc, o);
           }
-        }
-        begun = true;
-        __syncwarp();
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full + 8 * bar);
+          if (__any_sync(0xffffffffu, keep != 1.0f) && begun) {  // (NaN too)
+            // all P u of what came before
+            if (kStreams == 1) wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1, 0x7b);
+            else wait(pv_done + 8 * (2 * stream + (h ^ 1)), h == 0 ? t - 1 : t, 0x7b);
+            dead = __any_sync(0xffffffffu, dead);
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < kMine; cc += 16) {
+              uint32_t o[16];
+              tc::tmem_ld_32x32b_x16(o_at + cc, o);
+              tc::tmem_wait_ld(o);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float2 f = unpair(mul2(pair(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), pair(keep, keep)));
+                o[k] = __float_as_uint(f.x);
+                o[k + 1] = __float_as_uint(f.y);
+              }
+              tc::tmem_st_32x32b_x16(o_at + cc, o);
+            }
+          }
+          begun = true;
+          __syncwarp();
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(p_full + 8 * bar);
         }
       }
 
