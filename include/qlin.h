@@ -923,6 +923,13 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  *   max_new     1 .. 2^31 - 1, a bound that the call is planned for
  *   workspace   qlin_chunk_attention_workspace_bytes(...) bytes, 256-byte
  *               aligned, contents arbitrary; one call at a time may use it
+ * Scores, sums and out are held in float32; a cap adds up to 2^-20 of itself
+ * to a score's error.  A probability times its value's scale is rounded to 11
+ * bits; it keeps them down to 2^-23 of the largest such product of its row (of the largest
+ * value scale of the row's 128 tokens, seen or not, where that is more) and is
+ * lost below 2^-33.  Scales of 0 and below it are as good as others.  A key or a value
+ * that is not a number (its scale, its zero-point, an E4M3 code) makes the rows
+ * that see its token not numbers, and no others.
  *
  * qlin_verify_drafts: which of the drafted tokens of each sequence stay, and the
  * token after them.  Node i of sequence b is row q_indptr[b] + i, at most

@@ -25,6 +25,8 @@ Operations (sizes as flags):
   norm_rope_cache  qlin_qk_norm_rope_cache, T new tokens, heads --hq / --hk of 128, cache of --fmt
   tree_attention   qlin_tree_attention, T sequences of --ctx cached tokens and --nodes new ones (a chain), heads
                --hq / --hk of 128, cache of --fmt
+  chunk_attention  qlin_chunk_attention, T sequences of --ctx cached tokens and --nodes new ones, else as tree_attention
+  verify_drafts  qlin_verify_drafts, T sequences of a chain of --nodes nodes, rows of --K probabilities
   fp8_quant    qlin_quant_fp8, X [T][K] fp16, per-row E4M3
   fp8_gemm     qlin_fp8_gemm, A [T][K] and B [N][K] E4M3 (made by the quantizer), bias, bf16 out
 
@@ -219,11 +221,22 @@ def _setup(args, q, torch):
         out = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
         return lambda i: q.qlin_fp8_gemm(qa, ws[i % copies][0], sa, ws[i % copies][1], out, bias=bias)
 
-    if args.op in ("norm_rope_cache", "tree_attention"):
+    if args.op == "verify_drafts":
+        rows = T * args.nodes
+        target, draft = (torch.softmax(3 * torch.randn((rows, K), device="cuda", generator=g), -1) for _ in range(2))
+        tokens = torch.multinomial(draft, 1, generator=g).view(T, args.nodes).roll(1, 1).reshape(-1).contiguous()
+        u = torch.rand(rows + T, device="cuda", generator=g)
+        path = torch.empty((T, args.nodes), dtype=torch.int32, device="cuda")
+        count, after = torch.empty(T, dtype=torch.int32, device="cuda"), torch.empty(T, dtype=torch.int64, device="cuda")
+        starts = torch.arange(T + 1, dtype=torch.int32, device="cuda") * args.nodes
+        call = q.qlin_verify_drafts_prepare(target, draft, None, tokens, starts, u[:rows], u[rows:].clone(), path, count, after)
+        return lambda i: call.run()
+
+    if args.op in ("norm_rope_cache", "tree_attention", "chunk_attention"):
         d, page, u4 = 128, 64, args.fmt == "u4"
         fmt = {"int8": q.QLIN_KV_INT8, "e4m3": q.QLIN_KV_E4M3, "u4": q.QLIN_KV_U4}[args.fmt]
         nodes, seqs = (1, 1) if args.op == "norm_rope_cache" else (args.nodes, T)
-        per = -(-(args.ctx + nodes) // page) if args.op == "tree_attention" else -(-T // page)
+        per = -(-(args.ctx + nodes) // page) if args.op != "norm_rope_cache" else -(-T // page)
         kv = [torch.empty((seqs * per, args.hk, page, d // 2 if u4 else d), dtype=torch.int8 if args.fmt == "int8" else torch.uint8,
                           device="cuda").random_(0, 100, generator=g) for _ in range(2)]
         scales = [torch.rand((seqs * per, args.hk, page), device="cuda", generator=g) * 0.02 + 0.01 for _ in range(2)]
@@ -242,10 +255,13 @@ def _setup(args, q, torch):
         else:
             table = torch.randperm(seqs * per, device="cuda", generator=g).int().view(seqs, per)
             starts = torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * nodes
-            work = torch.empty(q.qlin_tree_attention_workspace_bytes(cache, args.hq, nodes, seqs), dtype=torch.uint8, device="cuda")
-            call = q.qlin_tree_attention_prepare(x[:, :args.hq], cache, table, starts,
-                                                 torch.full((seqs,), args.ctx, dtype=torch.int32, device="cuda"), None, out,
-                                                 work, nodes)
+            ctx = torch.full((seqs,), args.ctx, dtype=torch.int32, device="cuda")
+            if args.op == "chunk_attention":
+                work = torch.empty(q.qlin_chunk_attention_workspace_bytes(cache, args.hq, nodes, seqs), dtype=torch.uint8, device="cuda")
+                call = q.qlin_chunk_attention_prepare(x[:, :args.hq], cache, table, starts, ctx, out, work, nodes)
+            else:
+                work = torch.empty(q.qlin_tree_attention_workspace_bytes(cache, args.hq, nodes, seqs), dtype=torch.uint8, device="cuda")
+                call = q.qlin_tree_attention_prepare(x[:, :args.hq], cache, table, starts, ctx, None, out, work, nodes)
         return lambda i: call.run()
 
     raise ValueError(args.op)
@@ -257,7 +273,7 @@ def main(argv=None):
                                    "nvfp4_quant", "nvfp4_gemm",
                                    "fp8_quant", "fp8_gemm", "rmsnorm_nvfp4", "rmsnorm_int8", "mxfp8_quant",
                                    "mxfp4_quant", "mxfp8_gemm", "mxfp4_gemm", "hadamard", "w4a16_act_order", "norm_rope_cache",
-                                   "tree_attention"])
+                                   "tree_attention", "chunk_attention", "verify_drafts"])
     ap.add_argument("--n", type=int, default=256, help="Hadamard group size")
     ap.add_argument("--kind", type=int, default=0, help="Hadamard kind: 0 Sylvester, 1 regular")
     ap.add_argument("--T", type=int, default=1)

@@ -27,12 +27,26 @@
 //          threads a row, 64 tokens each
 //   8-11   load codes and scales into registers, a tile ahead, and widen them to fp16
 //          in shared memory, in the tensor core's layout: one widening for 256 rows
-//   12     issues the products (one thread)
+//   12-13  issue the products of a stream each (one thread)
 // Per token tile and stream: S = q n^T into the stream's tensor-memory buffer, which the
 // softmax threads turn into P over the same columns; O += P u takes P from there
-// and u as it lies (tokens x channels).  While one stream's softmax runs the tensor
-// cores work for the other.  (One stream: S has two buffers in turn.)
+// and u as it lies (tokens x channels).  A tile's 64 first and 64 last tokens are
+// handed over separately: while the softmax has one half, P u of the other and
+// then S of the next tile's go through the tensor cores, so that its threads find their
+// next scores there (S of 64 tokens costs 54 of the 64 cycles that 128 take, but
+// waiting for whole tiles took longer: 3559 -> 3118 us in the case below).  One
+// stream: S has two buffers in turn.
 // Tensor memory: S/P 2 x 128 columns, O 2 x D (1 x 256).
+//
+// Bound: the instructions of the softmax and of the widening, and what they wait
+// for one another; neither DRAM nor the tensor cores.  8192 tokens behind 16384 (32 query heads on
+// 8 of 128, INT8): 2863 us, 960 TFLOP/s, half of what a large product reaches; a
+// tile of 256 rows x 128 tokens takes about 5000 cycles, of which the
+// products are 2750 (2048 with whole tiles), the exponentials 1024, and issue slots are
+// used in 0.53 of the cycles (0.36 tensor, 0.18 exponentials busy).  What has been
+// measured: 32 scores at a time instead of 64 3103 us (a step's maximum and vote cost the
+// same); 16 softmax warps 3937; one warp for both streams' products 3559; values'
+// scales in the exponent 3669.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -6,7 +6,10 @@
 // whole path, kBatch tokens at a time: it loads all of a batch before it stores
 // any of it.  A path ascends, so path[i] >= i: what a batch stores, at places below
 // its end, no later batch reads, and within a thread no other one interferes.
-// Bound: latency for few sequences, memory for many.
+// Bound: latency for few sequences (lengths, path, page, bytes: one conversation's path
+// and the read of what it kept take 7.0 us together), memory for many: 192 sequences that
+// keep up to 9 of 64 tokens, 32 heads of 128, and that read take 17.8 us for 42 MB
+// (6.3 us).
 #include <algorithm>
 
 #include "kv_common.cuh"

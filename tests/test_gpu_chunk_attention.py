@@ -298,6 +298,27 @@ def test_few_rows(qlin_gpu, fmt, hq, hk, d, most):
     Problem(qlin_gpu, seqs, hq, hk, d, 16, fmt, torch.float16, spare_rows=2, window=2 ** 31 - 1).run().check()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_what_few_rows_do_not_see(qlin_gpu, fmt, which):
+    """As above for calls of few rows: a token that is no number reaches the rows from its own on."""
+    p = Problem(qlin_gpu, [(130, 5)], 4, 2, 128, 16, fmt, torch.float16).run()
+    clean, clean_lse = p.out.clone(), p.lse.clone()
+    for kind in ["scale"] + (["zero"] if fmt == "u4" else []) + (["code"] if fmt == "e4m3" else []):
+        t = [x.clone() for x in p.t]
+        i, (page, off) = 0 if which == "k" else 1, (int(p.table[0, 132 // 16]), 132 % 16)
+        if kind == "code":
+            t[i][page, :, off, 5] = 0x7f
+        elif fmt == "u4":
+            t[2 + i][page, :, off, 0 if kind == "scale" else 1] = float("nan") if kind == "scale" else 7.5
+        else:
+            t[2 + i][page, :, off] = float("nan")
+        p.cache = qlin_gpu.qlin_kv_cache(*t, p.cache.fmt)
+        p.run()
+        assert bool(torch.isnan(p.out[2:]).flatten(1).any(1).all()), kind
+        assert torch.equal(p.out[:2], clean[:2]) and torch.equal(p.lse[:2], clean_lse[:2]), kind
+
+
 @pytest.mark.parametrize("seqs,new", [(200, 1), (200, 9), (33, 70), (1, 1)])
 def test_many_sequences(qlin_gpu, seqs, new):
     """Batches whose sequences a block counts side by side, long and short ones in turn; also those with none at all."""
