@@ -100,6 +100,17 @@ def test_large(qlin_gpu, drawn):
     p.check(*out)
 
 
+@pytest.mark.parametrize("drawn,fan", [(True, 1), (True, 3), (False, 3)])
+@pytest.mark.parametrize("seqs,v", [(19, 40001), (20, 40001), (76, 9000), (77, 9000), (90, 70003)])
+def test_batches(qlin_gpu, seqs, v, drawn, fan):
+    """Numbers of sequences around those at which fewer blocks take each of them."""
+    p = Problem([1 + (b * 7) % 5 for b in range(seqs)], v, fan, drawn, agree=0.3)
+    out = p.outputs()
+    qlin_gpu.qlin_verify_drafts(*p.args(), *out)
+    p.check(*out)
+    assert qlin_gpu.qlin_get_device_error() == 0
+
+
 @pytest.mark.parametrize("offset,pad", [(1, 0), (2, 3), (4, 4), (0, 1), (3, 1)])
 def test_strides_and_alignments(qlin_gpu, offset, pad):
     for v in (31, 4100):
