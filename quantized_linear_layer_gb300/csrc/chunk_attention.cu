@@ -1030,9 +1030,9 @@ int64_t part_rows(const qlin_kv_cache& c, int64_t hq, int64_t max_new) {
   return std::min<int64_t>(c.head_dim == 256 ? 128 : 256, max_new > 256 ? 256 : max_new * group);
 }
 
-// Up to 16 rows per key head the kernel of few rows answers plain scores: it has no tile of 256 rows to fill.  64 single tokens
-// behind 1000 (32 query heads on 8 of 128, INT8) take 51 us there and 122 us here, 4 tokens behind 16000 27 and 47; with 32
-// rows the two are within a third of each other, with 128 it is 55 and 48 us.
+// Up to 16 rows per key head the kernel of few rows answers: it has no tile of 256 rows to fill.  64 single tokens
+// behind 1000 (32 query heads on 8 of 128, INT8) take 51 us there and 122 us here (61 with a cap), 4 tokens behind 16000 27 and 47;
+// with 32 rows the two are within a third of each other, with 128 it is 55 and 48 us.
 bool few_rows(const qlin_kv_cache& c, int64_t hq, int64_t max_new) { return max_new * (hq / c.heads) <= 16; }
 
 }  // namespace
@@ -1048,8 +1048,8 @@ int64_t chunk_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t hq, 
 cudaError_t plan_chunk_attention(const ChunkAttentionArgs& a, Prepared* out) {
   chunk::Params p = {};
   const qlin_kv_cache& c = a.cache;
-  const bool plain = a.scores.softcap == 0.0f && a.scores.slopes == nullptr && a.scores.window == 0 && a.scores.prefix_lens == nullptr;
-  if (plain && chunk::few_rows(c, a.q.heads, a.max_new)) {
+  if (chunk::few_rows(c, a.q.heads, a.max_new)) {
+    const bool plain = a.scores.softcap == 0.0f && a.scores.slopes == nullptr && a.scores.window == 0 && a.scores.prefix_lens == nullptr;
     TreeAttentionArgs t = {};
     t.q = a.q;
     t.out = a.out;
@@ -1065,7 +1065,7 @@ cudaError_t plan_chunk_attention(const ChunkAttentionArgs& a, Prepared* out) {
     t.scale = a.scores.scale;
     t.lse = a.lse;
     t.workspace = a.workspace;
-    return plan_tree_attention(t, out);
+    return plain ? plan_tree_attention(t, out) : plan_chain_attention(t, a.scores, out);
   }
   p.q = static_cast<const uint8_t*>(a.q.data);
   p.out = static_cast<uint8_t*>(a.out.data);

@@ -9,12 +9,7 @@ namespace chunk {
 
 constexpr int kTile = 128;  // tokens
 
-struct Params : tree::Params {  // (max_nodes: the most new tokens of a sequence)
-  float softcap;          // 0: none
-  const float* slopes;    // or null
-  int32_t window;         // 0: none
-  const int32_t* prefix;  // or null
-};
+using Params = tree::ScoredParams;  // (max_nodes: the most new tokens of a sequence)
 
 // A sequence's bounds as far as they can be used: rows = 0 when they cannot.
 struct Sequence {

@@ -201,6 +201,8 @@ struct TreeAttentionArgs {
 };
 int64_t tree_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t Hq, int64_t max_nodes, int64_t B);
 cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out);
+// Chains (no mask) of up to 16 rows per key head whose scores have another form.
+cudaError_t plan_chain_attention(const TreeAttentionArgs& a, const qlin_scores& scores, Prepared* out);
 
 // Block tables and slots from lengths.
 cudaError_t plan_kv_pages_assign(const qlin_kv_pages& pages, const int32_t* ctx_lens, const int32_t* new_lens, int64_t B,

@@ -51,6 +51,13 @@
 // widening for half the bytes); heads of 256, as many bytes, 163.  Twelve of the 16
 // operand rows are padding there.  At 16 rows the widening takes as long as the loads.
 // One sequence of 500 tokens, 32 heads: 11 us, two launches' latency.
+//
+// Chains whose scores have another form (ScoredParams: a cap, a bias by distance, a window, a
+// prefix) are a variant of their own: a cap's exponential and reciprocal and the bias
+// are a few instructions for each score, and of the tokens only the tiles that some
+// row sees are units.  64 single tokens behind 1000, INT8, 32 heads on 8 of 128:
+// 51 us plain, 61 capped, 50 with a window of 512; 4 x 4 behind 16000 with that
+// window 22 (49 without).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -110,9 +117,11 @@ struct Geo {
   }
 };
 
-template <int FMT, int D>
+// P: Params, or ScoredParams (chains whose scores have another form).
+template <int FMT, int D, class P>
 __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPerSm)
-    tree_attention_kernel(const __grid_constant__ Params p) {
+    tree_attention_kernel(const __grid_constant__ P p) {
+  constexpr bool kScored = std::is_same<P, ScoredParams>::value;
   using G = Geo<FMT, D>;
   constexpr int kWarps = G::kWarps, kThreads = G::kThreads;
   extern __shared__ uint8_t smem_raw[];
@@ -154,11 +163,14 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
       int32_t ahead = kNoPage;  // the page of box `lane` of the 32 boxes from unit `from` on
       int from = 0;
       for (int t = w.tile; t < w.tile + w.tiles; ++t) {
-        if (t == w.tile || (t - from) * boxes == 32) {
+        if (t == w.tile || (t - from) * boxes == 32 || (kScored && t == w.s.prefix_tiles)) {
           from = t;
-          const int j = t * kTile + lane * box;
+          const int first = w.s.template token_tile<P>(t);
+          // (up to where the tiles are those of consecutive tokens)
+          const int past = kScored && t < w.s.prefix_tiles ? min(w.tile + w.tiles, w.s.prefix_tiles) : w.tile + w.tiles;
+          const int j = first * kTile + lane * box;
           ahead = kNoPage;
-          if (j < min(w.s.len, (w.tile + w.tiles) * kTile)) ahead = checked_page(p, table[j >> p.page_shift]);
+          if (j < min(w.s.len, (first + past - t) * kTile)) ahead = checked_page(p, table[j >> p.page_shift]);
         }
         if (!tc::mbar_wait_quiet(bar_free + 8 * stage, phase, p.err, 0x50)) dead = true;
         if (__any_sync(0xffffffffu, dead)) {
@@ -168,11 +180,12 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
         const uint32_t codes = base + stage * G::kStage, scales = base + G::kOffScale + stage * 2 * G::kScaleBytes;
         auto row_at = [](int r, int c) { return c / (G::kW / 16) * G::kSubBytes + G::chunk(r, c % (G::kW / 16)); };
         const int at = (t - from) * boxes;
-        copy_scales<kTile>(p, w.head, t * kTile, box, ahead, at, scales, scales + G::kScaleBytes, policy);
+        const int j0 = w.s.template token_tile<P>(t) * kTile;
+        copy_scales<kTile>(p, w.head, j0, box, ahead, at, scales, scales + G::kScaleBytes, policy);
         if (box == kTile)
-          copy_codes<kTile, kTile, G::kRowBytes>(p, w.head, t * kTile, ahead, at, codes, codes + G::kCodeBytes, policy, row_at);
+          copy_codes<kTile, kTile, G::kRowBytes>(p, w.head, j0, ahead, at, codes, codes + G::kCodeBytes, policy, row_at);
         else
-          copy_codes<kTile, 16, G::kRowBytes>(p, w.head, t * kTile, ahead, at, codes, codes + G::kCodeBytes, policy, row_at);
+          copy_codes<kTile, 16, G::kRowBytes>(p, w.head, j0, ahead, at, codes, codes + G::kCodeBytes, policy, row_at);
         copies_arrive(bar_full + 8 * stage);
         if (++stage == G::kStages) {
           stage = 0;
@@ -199,7 +212,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
     if (!__shfl_sync(0xffffffffu, more, 0)) break;
     // q of this lane's rows g and g + 8, as fp16 operands scaled by a power of two
     uint32_t qa[D / 16][4];
-    float row_scale[2];
+    float row_scale[2], slope2[2] = {0.0f, 0.0f};
     int32_t row_node[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -207,6 +220,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
       const int node = row / p.group;
       const bool live = node < w.s.nodes;
       row_node[i] = live ? node : -1;
+      if constexpr (kScored) {
+        if (p.slopes != nullptr && live) slope2[i] = -kLog2e * p.slopes[w.head * p.group + row - node * p.group];
+      }
       const uint8_t* src = p.q + (w.s.q_row + node) * p.qt + (w.head * p.group + row - node * p.group) * p.qh;
       uint32_t raw[D / 8];  // this lane's D / 4 channels: kPerSub / 4 contiguous ones of each column block
       uint32_t top = 0;
@@ -263,11 +279,13 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
       const uint32_t stage = u % G::kStages;
       if (!dead) dead = !tc::mbar_wait_quiet(bar_full + 8 * stage, (u / G::kStages) & 1, p.err, 0x51);
       dead = __any_sync(0xffffffffu, dead);
-      const int j0 = (w.tile + static_cast<int>(u - unit0)) * kTile;  // the unit's first token
+      const int j0 = w.s.template token_tile<P>(w.tile + static_cast<int>(u - unit0)) * kTile;  // the unit's first token
       const uint32_t ks_at = base + stage * G::kStage;
       const uint32_t vs_at = ks_at + G::kCodeBytes;
       const uint8_t* sc = smem + G::kOffScale + stage * 2 * G::kScaleBytes;
-      const bool masked = j0 + kTile > w.s.ctx;
+      bool masked = j0 + kTile > w.s.ctx;
+      if constexpr (kScored)
+        masked = j0 + kTile > w.s.prefix && (masked || (p.window > 0 && w.s.ctx + w.s.nodes - 1 - j0 >= p.window));
 
       // odd value scales of the unit (it is this warp's alone until it is given free), those behind the end among them
       float* factors = reinterpret_cast<float*>(smem + G::kOffFactor) + warp * kTile;
@@ -277,9 +295,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
         uint32_t* word = of_k + kTile;
         bool mine = odd_scale<FMT>(*word);
         if constexpr (G::kU4) mine = mine || odd_zero(*of_k) || odd_zero(*word);
-        bool nan_codes = false;  // among the values of nodes, or behind the end
+        bool nan_codes = false;  // among the values of tokens that some row does not see, or behind the end
         if constexpr (FMT == QLIN_KV_E4M3) {
-          if (masked && j0 + lane >= w.s.ctx) {
+          if (masked && (kScored || j0 + lane >= w.s.ctx)) {
 #pragma unroll 1
             for (int c = 0; c < G::kRowBytes / 16; ++c)
               nan_codes |= clear_nan_codes(vs_at + c / (G::kW / 16) * G::kSubBytes + G::chunk(lane, c % (G::kW / 16)));
@@ -367,8 +385,21 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
           }
           const float lsv = lg2(sv);
           rsv[2 * n + i] = rcp(sv);
-          s[n][i] = fmaf(s[n][i] * row_scale[0], sk, lsv);
-          s[n][2 + i] = fmaf(s[n][2 + i] * row_scale[1], sk, lsv);
+          if constexpr (kScored) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float t = s[n][2 * x + i] * row_scale[x] * sk;
+              if (p.softcap > 0.0f) {  // c tanh(s / c) = c (1 - 2 / (1 + e^(2 s / c)))
+                const float cap2 = p.softcap * kLog2e;
+                t = fmaf(rcp(1.0f + ex2(t * __fdividef(2.0f, p.softcap))), -2.0f * cap2, cap2);
+              }
+              if (p.slopes != nullptr) t = fmaf(slope2[x], fabsf(static_cast<float>(w.s.ctx + row_node[x] - j0 - tok - i)), t);
+              s[n][2 * x + i] = t + lsv;
+            }
+          } else {
+            s[n][i] = fmaf(s[n][i] * row_scale[0], sk, lsv);
+            s[n][2 + i] = fmaf(s[n][2 + i] * row_scale[1], sk, lsv);
+          }
         }
         if constexpr (G::kU4) {
           const uint32_t z = __byte_perm(vw.x, vw.y, 0x7632);
@@ -384,10 +415,13 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
             const int j = j0 + 8 * n + 2 * r + (i & 1) - w.s.ctx;  // the node that the token is
             const int node = row_node[i >> 1];
             bool seen = j < 0;
-            if (!seen && j < w.s.nodes && node >= 0)
+            if constexpr (kScored) {
+              seen = node >= 0 && j < w.s.nodes && (j + w.s.ctx < w.s.prefix || (j <= node && (p.window == 0 || node - j < p.window)));
+            } else if (!seen && j < w.s.nodes && node >= 0) {
               seen = p.mask == nullptr
                          ? j <= node
                          : ((p.mask[(w.s.q_row + node) * p.mask_words + (j >> 6)] >> (j & 63)) & 1) != 0;
+            }
             if (!seen) s[n][i] = -INFINITY;
           }
         }
@@ -585,10 +619,10 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
 
 int grid_blocks(int64_t head_dim) { return sm_count() * (head_dim == 256 ? 1 : 2); }
 
-template <int FMT, int D>
-cudaError_t plan(const Params& p, Prepared* out) {
+template <int FMT, int D, class P>
+cudaError_t plan(const P& p, Prepared* out) {
   using G = Geo<FMT, D>;
-  const void* fn = reinterpret_cast<const void*>(tree_attention_kernel<FMT, D>);
+  const void* fn = reinterpret_cast<const void*>(tree_attention_kernel<FMT, D, P>);
   const cudaError_t e = ensure_max_dynamic_smem(fn);
   if (e != cudaSuccess) return e;
   const uint32_t blocks = static_cast<uint32_t>(grid_blocks(D));
@@ -600,8 +634,8 @@ cudaError_t plan(const Params& p, Prepared* out) {
   return cudaSuccess;
 }
 
-template <int FMT>
-cudaError_t plan(const Params& p, int64_t d, Prepared* out) {
+template <int FMT, class P>
+cudaError_t plan(const P& p, int64_t d, Prepared* out) {
   if (d == 64) return plan<FMT, 64>(p, out);
   if (d == 128) return plan<FMT, 128>(p, out);
   return plan<FMT, 256>(p, out);
@@ -643,10 +677,10 @@ int64_t tree_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t hq, i
          2 * s.blocks * s.rows * (cache.head_dim * 4 + static_cast<int64_t>(sizeof(float2)));
 }
 
-cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out) {
-  Params p = {};
+namespace {
+
+void fill(Params& p, const TreeAttentionArgs& a, const Shape& shape) {
   const qlin_kv_cache& c = a.cache;
-  const Shape shape = shape_of(c, a.q.heads, a.max_nodes);
   p.q = static_cast<const uint8_t*>(a.q.data);
   p.out = static_cast<uint8_t*>(a.out.data);
   p.qt = 2 * a.q.token_stride;
@@ -685,10 +719,33 @@ cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out) {
   ws += 2 * shape.blocks * shape.rows * static_cast<int64_t>(sizeof(float2));
   p.records = reinterpret_cast<Record*>(ws);
   p.err = device_error_word();
-  if (shape.wide) return plan_wide(p, c.fmt, c.head_dim, out);
+}
+
+template <class P>
+cudaError_t plan(const P& p, const qlin_kv_cache& c, Prepared* out) {
   if (c.fmt == QLIN_KV_INT8) return plan<QLIN_KV_INT8>(p, c.head_dim, out);
   if (c.fmt == QLIN_KV_E4M3) return plan<QLIN_KV_E4M3>(p, c.head_dim, out);
   return plan<QLIN_KV_U4>(p, c.head_dim, out);
+}
+
+}  // namespace
+
+cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out) {
+  const qlin_kv_cache& c = a.cache;
+  const Shape shape = shape_of(c, a.q.heads, a.max_nodes);
+  Params p = {};
+  fill(p, a, shape);
+  return shape.wide ? plan_wide(p, c.fmt, c.head_dim, out) : plan(p, c, out);
+}
+
+cudaError_t plan_chain_attention(const TreeAttentionArgs& a, const qlin_scores& scores, Prepared* out) {
+  ScoredParams p = {};
+  fill(p, a, shape_of(a.cache, a.q.heads, a.max_nodes));
+  p.softcap = scores.softcap;
+  p.slopes = scores.slopes;
+  p.window = scores.window >= kMaxLen ? 0 : static_cast<int32_t>(scores.window);  // no sequence is longer
+  p.prefix = scores.prefix_lens;
+  return plan(p, a.cache, out);
 }
 
 }  // namespace qlin

@@ -4,6 +4,8 @@
 // described in tree_attention.cu.
 #pragma once
 
+#include <type_traits>
+
 #include <cmath>
 
 #include "kv_common.cuh"
@@ -57,6 +59,14 @@ struct Params {
   int32_t* err;
 };
 
+// With scores in another form, for chains: see qlin_scores.
+struct ScoredParams : Params {
+  float softcap;          // 0: none
+  const float* slopes;    // or null
+  int32_t window;         // 0: none
+  const int32_t* prefix;  // or null
+};
+
 // The longest sequence, nodes included: far enough below 2^31 that the token numbers the kernels form past a sequence's
 // end (whole tiles, and the loading warps' 32 boxes of up to 64 tokens) stay in an int32.
 constexpr int64_t kMaxLen = 0x7fff0000;
@@ -66,11 +76,18 @@ struct Sequence {
   int64_t q_row;
   int32_t nodes, ctx, len;
   int32_t row_tiles, token_tiles;
+  // with scores in another form: the prefix, and the token tiles that some row sees, those of the prefix and, `skipped` tiles
+  // further on, those of the window
+  int32_t prefix, prefix_tiles, skipped;
+  template <class P>
+  __device__ __forceinline__ int32_t token_tile(int32_t i) const {
+    return std::is_same<P, ScoredParams>::value && i >= prefix_tiles ? i + skipped : i;
+  }
 };
 
 // In row tiles of ROWS and token tiles of TILE.
-template <int ROWS, int TILE>
-__device__ __forceinline__ Sequence sequence(const Params& p, int b) {
+template <int ROWS, int TILE, class P>
+__device__ __forceinline__ Sequence sequence(const P& p, int b) {
   Sequence s;
   const int32_t q0 = p.q_indptr[b], q1 = p.q_indptr[b + 1];
   s.q_row = q0;
@@ -87,6 +104,13 @@ __device__ __forceinline__ Sequence sequence(const Params& p, int b) {
   s.row_tiles = (s.nodes * p.group + ROWS - 1) / ROWS;
   s.token_tiles = (s.len + TILE - 1) / TILE;
   if (s.nodes == 0) s.row_tiles = 0;
+  if constexpr (std::is_same<P, ScoredParams>::value) {
+    s.prefix = p.prefix != nullptr && s.nodes > 0 ? max(0, min(p.prefix[b], s.len)) : 0;
+    s.prefix_tiles = (s.prefix + TILE - 1) / TILE;
+    const int32_t low = p.window > 0 ? max(0, s.ctx - p.window + 1) : 0;  // of the first row
+    s.skipped = max(low / TILE - s.prefix_tiles, 0);
+    s.token_tiles -= s.skipped;
+  }
   return s;
 }
 
@@ -104,7 +128,8 @@ struct Walk {
   // the segment's part that is this block's
   int32_t head, row_tile, tile, tiles;
 
-  __device__ __forceinline__ bool next(const Params& p) {
+  template <class P>
+  __device__ __forceinline__ bool next(const P& p) {
     if (at >= end) return false;
     int64_t n = units(p, s);
     while (at - first >= n) {
@@ -380,8 +405,8 @@ __device__ __forceinline__ void copy_codes(const Params& p, int head, int first,
 
 // The units before each thread's share of the sequences, into scan[THREADS + 1]
 // (share b .. b + share - 1 of thread b / share), by all threads of the block.
-template <int ROWS, int TILE, int THREADS>
-__device__ __forceinline__ void scan_units(const Params& p, int share, int64_t* scan) {
+template <int ROWS, int TILE, int THREADS, class P>
+__device__ __forceinline__ void scan_units(const P& p, int share, int64_t* scan) {
   int64_t sum = 0;
   for (int b = threadIdx.x * share; b < min(p.B, static_cast<int>(threadIdx.x + 1) * share); ++b)
     sum += units(p, sequence<ROWS, TILE>(p, b));
@@ -407,8 +432,8 @@ __device__ __forceinline__ void scan_units(const Params& p, int share, int64_t* 
 }
 
 // The run of units of block `block` of `blocks`.
-template <int ROWS, int TILE, int THREADS>
-__device__ __forceinline__ Walk<ROWS, TILE> begin_run(const Params& p, int share, const int64_t* scan, int64_t block,
+template <int ROWS, int TILE, int THREADS, class P>
+__device__ __forceinline__ Walk<ROWS, TILE> begin_run(const P& p, int share, const int64_t* scan, int64_t block,
                                                       int64_t blocks) {
   Walk<ROWS, TILE> run;
   const int64_t total = scan[THREADS];

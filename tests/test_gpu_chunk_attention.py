@@ -299,6 +299,48 @@ def test_few_rows(qlin_gpu, fmt, hq, hk, d, most):
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("hq,hk,d,most,page", [(4, 4, 128, 1, 64), (8, 2, 64, 4, 16), (5, 1, 256, 3, 128), (2, 1, 128, 8, 32)])
+@pytest.mark.parametrize("how", [dict(softcap=5.0), dict(window=1), dict(window=100), dict(window=33, prefix=[1, 260, 10 ** 6, 64, 0, 30, 95]),
+                                 dict(prefix=[0, 2100, 3, 7, -5, 1, 96]), dict(slopes=True), dict(window=64, prefix=[0, 64, 128, 0, 32, 0, 128]),
+                                 dict(softcap=20.0, slopes=True, window=700, prefix=[50, 5, 5, 400, 3, 0, 1000])])
+def test_scores_of_few_rows(qlin_gpu, fmt, hq, hk, d, most, page, how):
+    """Caps, windows, prefixes and biases of a decode step's rows; windows that leave whole tiles out, behind a prefix and without."""
+    seqs = [(0, most), (2100, most), (127, 1), (600, most), (16, 0), (31, 1), (999, most)]
+    how = dict(how, slopes=[0.3 * (-0.5) ** h for h in range(hq)]) if how.get("slopes") else how
+    for dtype in (torch.float16, torch.bfloat16):
+        Problem(qlin_gpu, seqs, hq, hk, d, page, fmt, dtype, seed=most, spare_rows=1, **how).run().check()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_what_a_window_of_few_rows_hides(qlin_gpu, fmt, which):
+    """Tokens that are no numbers on either side of a window's edge, in a tile that rows see part of; pages of whole tiles
+    that nobody sees are not looked at."""
+    p = Problem(qlin_gpu, [(300, 4)], 4, 2, 128, 16, fmt, torch.float16, window=60, prefix=[9]).run()
+    clean, clean_lse = p.out.clone(), p.lse.clone()
+    at, bad = 300 + np.arange(4)[:, None], np.array([20, 241, 242, 302])
+    for kind in ["scale"] + (["zero"] if fmt == "u4" else []) + (["code"] if fmt == "e4m3" else []):
+        for token in bad.tolist():
+            t = [x.clone() for x in p.t]
+            i, (page, off) = 0 if which == "k" else 1, (int(p.table[0, token // 16]), token % 16)
+            if kind == "code":
+                t[i][page, :, off, 5] = 0x7f
+            elif fmt == "u4":
+                t[2 + i][page, :, off, 0 if kind == "scale" else 1] = float("nan") if kind == "scale" else 7.5
+            else:
+                t[2 + i][page, :, off] = float("nan")
+            p.cache = qlin_gpu.qlin_kv_cache(*t, p.cache.fmt)
+            p.run()
+            hit = torch.from_numpy(((token <= at) & (at - token < 60))[:, 0]).cuda()
+            assert bool(torch.isnan(p.out[hit]).flatten(1).any(1).all()), (kind, token)
+            assert torch.equal(p.out[~hit], clean[~hit]) and torch.equal(p.lse[~hit], clean_lse[~hit]), (kind, token)
+    p.cache = qlin_gpu.qlin_kv_cache(*p.t, p.cache.fmt)
+    p.table[0, 3:14] = -7   # tokens 48 .. 223
+    p.run()
+    assert torch.equal(p.out, clean) and torch.equal(p.lse, clean_lse)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
 @pytest.mark.parametrize("which", ["k", "v"])
 def test_what_few_rows_do_not_see(qlin_gpu, fmt, which):
     """As above for calls of few rows: a token that is no number reaches the rows from its own on."""
