@@ -1030,10 +1030,15 @@ int64_t part_rows(const qlin_kv_cache& c, int64_t hq, int64_t max_new) {
   return std::min<int64_t>(c.head_dim == 256 ? 128 : 256, max_new > 256 ? 256 : max_new * group);
 }
 
-// Up to 16 rows per key head the kernel of few rows answers: it has no tile of 256 rows to fill.  64 single tokens
-// behind 1000 (32 query heads on 8 of 128, INT8) take 51 us there and 122 us here (61 with a cap), 4 tokens behind 16000 27 and 47;
-// with 32 rows the two are within a third of each other, with 128 it is 55 and 48 us.
-bool few_rows(const qlin_kv_cache& c, int64_t hq, int64_t max_new) { return max_new * (hq / c.heads) <= 16; }
+// Calls of few rows per key head go to tree attention's kernels, which have no tile of 256 rows to fill: up to 16 in any form,
+// plain ones up to 64 (heads of 256 have no such kernel there).  INT8, 32 heads on 8 of 128, there / here: 64 single tokens
+// behind 1000 51 / 122 us (61 with a cap), 4 x 4 tokens behind 16000 49 / 91; of 32 rows 95 / 123 and 77 / 91, of 64 101 / 124
+// and 84 / 92, of 128 125 / 140 and 97 / 97.
+constexpr int64_t kFewRows = 16, kFewPlainRows = 64;
+int64_t rows_of(const qlin_kv_cache& c, int64_t hq, int64_t max_new) { return max_new * (hq / c.heads); }
+bool few_rows(const qlin_kv_cache& c, int64_t rows, bool plain) {
+  return rows <= kFewRows || (plain && c.head_dim <= 128 && rows <= kFewPlainRows);
+}
 
 }  // namespace
 }  // namespace chunk
@@ -1042,14 +1047,15 @@ int64_t chunk_attention_workspace_bytes(const qlin_kv_cache& cache, int64_t hq, 
   const int64_t blocks = sm_count();
   const int64_t own = blocks * static_cast<int64_t>(sizeof(tree::Record)) + 256 +
                       2 * blocks * chunk::part_rows(cache, hq, max_new) * (cache.head_dim * 4 + static_cast<int64_t>(sizeof(float2)));
-  return chunk::few_rows(cache, hq, max_new) ? std::max(own, tree_attention_workspace_bytes(cache, hq, max_new, B)) : own;
+  const bool other = chunk::few_rows(cache, chunk::rows_of(cache, hq, max_new), true);
+  return other ? std::max(own, tree_attention_workspace_bytes(cache, hq, max_new, B)) : own;
 }
 
 cudaError_t plan_chunk_attention(const ChunkAttentionArgs& a, Prepared* out) {
   chunk::Params p = {};
   const qlin_kv_cache& c = a.cache;
-  if (chunk::few_rows(c, a.q.heads, a.max_new)) {
-    const bool plain = a.scores.softcap == 0.0f && a.scores.slopes == nullptr && a.scores.window == 0 && a.scores.prefix_lens == nullptr;
+  const bool plain = a.scores.softcap == 0.0f && a.scores.slopes == nullptr && a.scores.window == 0 && a.scores.prefix_lens == nullptr;
+  if (chunk::few_rows(c, chunk::rows_of(c, a.q.heads, a.max_new), plain)) {
     TreeAttentionArgs t = {};
     t.q = a.q;
     t.out = a.out;

@@ -287,9 +287,10 @@ def test_as_attention_of_a_chain(qlin_gpu):
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
-@pytest.mark.parametrize("hq,hk,d,most", [(8, 8, 128, 1), (8, 2, 128, 4), (32, 2, 64, 1), (10, 2, 256, 3), (10, 2, 256, 4), (3, 1, 64, 6)])
+@pytest.mark.parametrize("hq,hk,d,most", [(8, 8, 128, 1), (8, 2, 128, 4), (32, 2, 64, 1), (10, 2, 256, 3), (10, 2, 256, 4), (3, 1, 64, 6), (8, 2, 128, 9),
+                                            (8, 8, 64, 64), (8, 8, 128, 65)])
 def test_few_rows(qlin_gpu, fmt, hq, hk, d, most):
-    """Single tokens and a few of them, as a decode step has them, on both sides of 16 rows per key head."""
+    """Single tokens and a few of them, as a decode step has them, on both sides of 16 and of 64 rows per key head."""
     seqs = [(0, 1), (700, most), (16, 0), (127, 1), (128, most), (2100, 1), (5, most)]
     for dtype in (torch.float16, torch.bfloat16):
         Problem(qlin_gpu, seqs, hq, hk, d, 16, fmt, dtype, spare_rows=2).run().check()
