@@ -90,7 +90,7 @@ struct Geo {
   static constexpr int kOffK = kOffQ + kStreams * kOperand;
   static constexpr int kOffV = kOffK + kBufs * kOperand;
   static constexpr int kOffCol = kOffV + kBufs * kOperand;             // [kCols][scale sk, sv][128]
-  static constexpr int kOffPair = kOffCol + kCols * 2 * kTile * 4;     // [tile parity][thread of the row][row]
+  static constexpr int kOffPair = kOffCol + kCols * 2 * kTile * 4;     // [32 tokens, in turn][thread of the row][row]
   static constexpr int kOffQmax = kOffPair + 2 * kSubs * 128 * 4;      // [thread of the row][row]
   static constexpr int kOffEnd = kOffQmax + kSubs * 128 * 4;           // [segment parity][thread of the row][row] l
   static constexpr int kOffRow = kOffEnd + 2 * kSubs * 128 * 4;  // [segment parity][softmax thread] RowOf
