@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) kv_keep_kernel(const __grid_constant
   const int64_t ctx = p.ctx[b];
   const int count = p.count[b];
   const int32_t* path = p.path + b * p.max_path;
-  bool bad = count < 0 || count > p.max_path || ctx < 0;
+  bool bad = count < 0 || count > p.max_path || ctx < 0 || ctx + count > INT32_MAX;  // (lengths are int32)
   if (!bad) {
     for (int i = threadIdx.x; i < count; i += kThreads)
       bad |= path[i] < i || (i > 0 && path[i] <= path[i - 1]) || ((ctx + path[i]) >> p.cache.page_shift) >= p.max_pages;

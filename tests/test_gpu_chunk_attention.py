@@ -437,3 +437,34 @@ def test_a_cache_beyond_32_bits(qlin_gpu):
     p.run()
     p.table = near
     p.check()
+
+
+@pytest.mark.parametrize("d,n", [(128, 1), (64, 5), (256, 30), (128, 200)])
+def test_the_longest_sequence(qlin_gpu, d, n):
+    """A window and a prefix at the end of a sequence of 2^31 - 2^16 tokens, which seven pages hold in turn: the same as
+    those tokens alone; one token more is recorded."""
+    q, page, window, prefix, length = qlin_gpu, 256, 300, 5, 0x7fff0000
+    p = Problem(q, [(prefix + window - 1, n)], 2, 1, d, page, "int8", torch.float16, window=window, prefix=[prefix])
+    ctx = length - n
+    # the same tokens, each where the long sequence has it: seven pages, filled from the short one's
+    j = np.concatenate([np.arange(prefix), ctx - window + 1 + np.arange(window - 1 + n)])
+    at = np.arange(prefix + window - 1 + n)
+    src = p.table[0, at // page].numpy(), at % page
+    t = []
+    for x in (*p.codes, *p.scales):
+        y = np.zeros((7,) + x.shape[1:], x.dtype)
+        y[(j // page) % 7, :, j % page] = x[src[0], :, src[1]]
+        t.append(torch.from_numpy(y).cuda())
+    assert len(set(zip((j // page % 7).tolist(), (j % page).tolist()))) == len(j)
+    p.cache = q.qlin_kv_cache(*t, q.QLIN_KV_INT8)
+    short, seqs = p.table, p.seqs
+    p.table = (torch.arange(-(-(length + 1) // page), dtype=torch.int32) % 7)[None]
+    p.ctx = torch.tensor([ctx], dtype=torch.int32)
+    p.run()
+    p.table, p.seqs = short, seqs
+    p.check()
+    p.ctx[0] = ctx + 1
+    p.table = (torch.arange(-(-(length + 1) // page), dtype=torch.int32) % 7)[None]
+    p.prepare().run()
+    torch.cuda.synchronize()
+    assert q.qlin_get_device_error() == 0x2000

@@ -86,6 +86,21 @@ def test_refused_on_the_device(qlin_gpu, bad):
     assert lens.tolist() == [12 if bad == "page" else ctx[0], 22]
 
 
+def test_lengths_that_pass_31_bits(qlin_gpu):
+    """A length that an int32 does not hold is recorded and its sequence left; the longest that it holds is not."""
+    q, page = qlin_gpu, 256
+    t, cache = _cache(q, "e4m3", 3, 2, page, 64)
+    table = (torch.arange(2 ** 31 // page, dtype=torch.int32) % 3)[None].repeat(2, 1)
+    top = 2 ** 31 - 1
+    ctx, paths = [top - 1, top - 6], [[0, 1], [0, 2, 3]]
+    want = _moved(t, table, page, ctx, [[], paths[1]])
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q.qlin_kv_cache_keep(cache, table.cuda(), torch.tensor(ctx, dtype=torch.int32, device="cuda"),
+                         torch.tensor([[0, 1, 0], paths[1]], dtype=torch.int32, device="cuda"),
+                         torch.tensor([2, 3], dtype=torch.int32, device="cuda"), lens)
+    assert q.qlin_get_device_error() == 0x2000 and lens.tolist() == [top - 1, top - 3] and _same(t, want)
+
+
 def test_pages_apart_streams_and_replays(qlin_gpu):
     """Pages with others between them; a prepared call on another stream and replayed with other paths."""
     q, page = qlin_gpu, 32
