@@ -79,7 +79,10 @@ struct Geo {
   static constexpr int kWidenWarps = 4, kMmaWarp = kSoftmaxWarps + kWidenWarps;
   static constexpr int kWarps = kMmaWarp + 4, kThreads = 32 * kWarps, kActive = 32 * (kMmaWarp + kStreams);
   static constexpr int kLaunchRegs = 128;
-  static constexpr int kSoftmaxRegs = D == 256 ? 104 : 136, kWidenRegs = D == 256 ? 232 : 168, kOtherRegs = 64;
+  // (No role spills at these.  Sixteen bytes of one role's cost 5 % of the time: 72 registers for the products instead of 64 took
+  // 4 prompts of 2048 tokens behind 8192 with E4M3 codes from 1140 to 1096 us; INT8 codes and heads of 128 spill at 72, not at 64.)
+  static constexpr int kSoftmaxRegs = D == 256 ? 104 : 136, kWidenRegs = D == 256 ? 232 : 168;
+  static constexpr int kOtherRegs = FMT == QLIN_KV_INT8 && D == 128 ? 64 : 72;
   static_assert(kSoftmaxWarps * kSoftmaxRegs + kWidenWarps * kWidenRegs + 4 * kOtherRegs <= kWarps * kLaunchRegs, "registers");
   static constexpr int kParts = kTile / 16 / kWidenWarps;  // 16 tokens each, of a widening warp
   static constexpr int kRowBytes = kU4 ? D / 2 : D;
