@@ -773,6 +773,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
           const uint32_t bar = kStreams == 2 ? 2 * stream + h : t & 1;
           wait(s_full + 8 * bar, kStreams == 2 ? t : t >> 1, 0x79);
           if (!here) {
+            // Not before all lanes have seen this phase: one that still waits would take a phase two later for it and wait for good.
+            __syncwarp();
             if (lane == 0) tc::mbar_arrive(p_full + 8 * bar);
             continue;
           }

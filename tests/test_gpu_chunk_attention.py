@@ -468,3 +468,21 @@ def test_the_longest_sequence(qlin_gpu, d, n):
     p.prepare().run()
     torch.cuda.synchronize()
     assert q.qlin_get_device_error() == 0x2000
+
+
+@pytest.mark.parametrize("fmt,seqs,slopes", [("e4m3", [(700, 257), (311, 130), (64, 200)], None), ("int8", [(6000, 9)], [0.2, 0.1, 0.3, 0.4]),
+                                             ("u4", [(900, 33), (5, 70), (2000, 40)], None)])
+def test_streams_without_rows(qlin_gpu, fmt, seqs, slopes):
+    """Tiles of which one of the two halves of rows has none, or none that sees the tile, over and over: no wait runs out and
+    every pass gives the same."""
+    p = Problem(qlin_gpu, seqs, 4, 1, 128, 16, fmt, torch.float16, slopes=slopes)
+    call = p.prepare()
+    call.run()
+    torch.cuda.synchronize()
+    p.check()
+    want = p.out.clone()
+    for _ in range(20):
+        for _ in range(50):
+            call.run()
+        torch.cuda.synchronize()
+        assert qlin_gpu.qlin_get_device_error() == 0 and torch.equal(p.out, want)
