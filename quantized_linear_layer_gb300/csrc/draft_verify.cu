@@ -102,6 +102,7 @@ struct Shared {
   uint64_t total;
   uint64_t c;               // the pass asked for
   int32_t at, rejected, done;
+  int32_t plain;            // nothing was left of the row at `at`: it is taken as it is
   int32_t holder;           // the warp whose part holds the drawn place, and what lies before it
   uint64_t base;
   uint64_t piece[kWarps];   // sums of the pieces of that part
@@ -249,7 +250,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(kThreads, 2) d
   const int64_t span = (p.V + kParts * 128 - 1) / (kParts * 128) * 128;  // of a warp
   const int64_t begin = (static_cast<int64_t>(rank) * kWarps + warp) * span, end = min(begin + span, p.V);
   bool have = false;   // the sums at hand are those of (at, c)
-  bool plain = false;  // nothing was left: p as it is
+  bool plain = false;  // s.plain
   while (true) {
     if (t == 0) {
       bool ask = false;
@@ -276,7 +277,11 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(kThreads, 2) d
           ask = true;
         }
       }
-      s.done = !ask && have;
+      // Nothing left where the walk ends (not before: a child behind the rejected one may be tried still, and most nodes behind it
+      // are no children of this one): one more sum, of the row as it is.
+      const bool again = !ask && have && w == 0 && !plain && (c != 0 || rejected > 0);
+      s.plain = plain || again;
+      s.done = !ask && have && !again;
       s.at = at;
       s.c = c;
       s.rejected = rejected;
@@ -284,6 +289,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(kThreads, 2) d
     }
     __syncthreads();
     if (s.done) break;
+    plain = s.plain != 0;
     // sums of what is left of the row
     const float* prow = p.target + (q0 + s.at) * p.target_stride;
     const uint64_t cc = plain ? 0 : s.c;
@@ -318,12 +324,6 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(kThreads, 2) d
     w = s.total;
     left = static_cast<double>(w) * 0x1p-52;
     ++pass;
-    // nothing left of a node that has no more children to try (child is thread 0's): its row as it is
-    const bool again = __syncthreads_or(t == 0 && w == 0 && child >= n && !plain && (s.c != 0 || s.rejected > 0));
-    if (again) {
-      plain = true;
-      have = false;
-    }
   }
 
   // the drawn place

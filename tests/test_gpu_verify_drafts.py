@@ -157,6 +157,54 @@ def test_rows_without_weight(qlin_gpu):
     assert out[1].tolist() == [1, 2, 1] and out[2].tolist() == [3, 0, -1] and q.qlin_get_device_error() == 0
 
 
+@pytest.mark.parametrize("v", [8, 4099])
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("parents", [[-1, 0, 1], [-1, 0, 1, 2, 3, 4], [-1, 0, 0, 0], [-1, 0, 0, 1, 1, 2, 0], [-1, 0, 1, 1, 3], [-1, 0, 0, 2, 2, 1, 3]])
+def test_nothing_left_before_the_last_node(qlin_gpu, parents, drawn, v):
+    """A rejection after which nothing is left draws from p, whatever nodes follow: the rest of the chain, siblings, others' children."""
+    n = len(parents)
+    at = [(3 * i + 1) % v for i in range(n)]             # each row has one token
+    for first in range(1, n):                            # the first node that cannot be, its drafts' row as the target's
+        p = Problem([n, 1, n], v, 2, drawn)
+        rows = torch.zeros(n, v)
+        rows[torch.arange(n), at] = 1.0 if drawn else 0.5
+        p.target = torch.cat([rows, rows[:1], rows]).cuda()
+        p.draft = p.target.clone() if drawn else None
+        up = [max(x, 0) for x in parents]
+        own = torch.tensor([0] + [at[up[i]] if i < first or not drawn else (at[up[i]] + 1) % v for i in range(1, n)])
+        p.tokens = torch.cat([own, own[:1], own])
+        p.accept = torch.tensor([0.0 if i < first else 0.9 for i in range(n)]).repeat(3)[:2 * n + 1]
+        p.accept[n:] = torch.cat([torch.zeros(1), p.accept[:n]])
+        p.parents = parents + [-1] + parents
+        out = p.outputs()
+        qlin_gpu.qlin_verify_drafts(*p.args(), *out)
+        p.check(*out)
+        assert (out[2] >= 0).all() and qlin_gpu.qlin_get_device_error() == 0
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("v", [3, 6, 700])
+def test_rows_of_eighths(qlin_gpu, v, drawn):
+    """Rows of few whole eighths, alike more often than not, trees of any shape: everything is exact in the oracle too, and
+    nothing left, ties and tokens twice among siblings are common."""
+    r = np.random.default_rng(v)
+    for turn in range(8):
+        nodes = [int(x) for x in r.integers(0, 9, 60)]
+        p = Problem(nodes, v, 2, drawn, seed=turn)
+        rows = lambda: r.multinomial(8, np.r_[0.5, 0.3, 0.2, np.zeros(v - 3)], sum(nodes)) / 8
+        target = rows()
+        draft = np.where(r.random((sum(nodes), 1)) < 0.6, target, rows())
+        p.target = torch.from_numpy(target).float().cuda()
+        p.draft = torch.from_numpy(draft).float().cuda() if drawn else None
+        p.parents = [-1 if i == 0 else int(r.integers(max(0, i - 4), i)) for n in nodes for i in range(n)]
+        p.tokens = torch.from_numpy(r.integers(0, 3, sum(nodes)))
+        p.accept = torch.from_numpy(r.integers(0, 8, sum(nodes)) / 8).float()
+        out = p.outputs()
+        qlin_gpu.qlin_verify_drafts(*p.args(), *out)
+        p.check(*out)
+    assert qlin_gpu.qlin_get_device_error() == 0
+
+
 def test_bad_indexes(qlin_gpu):
     """A parent or a token out of range: the node is not accepted, and it is recorded; bounds out of range: no nodes."""
     q = qlin_gpu
