@@ -705,7 +705,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         tc::tc_fence_after();
         const RowOf done = row_of[(parity ^ 1) * 256];
         const bool whole = done.flags == 3;
-        const bool none = ref == kNoRef;  // (O then holds anything)
+        // No score above -infinity: l is 0, or NaN where a score is none (maxima drop it), and O holds anything.
+        const bool none = ref == kNoRef;
         const float inv = !whole ? 1.0f : __frcp_rn(l);
         const float m = none ? -INFINITY : ref + kOffset;
         const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (done.flags & 1)) * p.tile_rows + stream * 128 + row;
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
             for (int k = 0; k < 16; ++k) {
               // 4-bit codes: column k of eight is channel k / 2 + 4 (k % 2)
               const int ch = G::kU4 ? (k & 8) + ((k & 7) >> 1) + 4 * (k & 1) : k;
-              f[ch] = none ? 0.0f : __uint_as_float(o[k]) * inv;
+              f[ch] = none ? l : __uint_as_float(o[k]) * inv;
             }
             if (done.token < 0) continue;
             const int ch = sub * kMine + cc;

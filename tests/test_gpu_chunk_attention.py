@@ -486,3 +486,42 @@ def test_streams_without_rows(qlin_gpu, fmt, seqs, slopes):
             call.run()
         torch.cuda.synchronize()
         assert qlin_gpu.qlin_get_device_error() == 0 and torch.equal(p.out, want)
+
+
+# Batches of which every segment is one block's (many sequences of one tile, or several tiles a block), and such as are cut
+# between blocks; of rows beyond those that the kernel of few rows takes, and of its own.
+CUTS = [([(0, 100)], 100), ([(0, 70)] * 3 + [(3, 66)], 70), ([(0, 40), (20, 65)] * 150, 65), ([(700, 300)], 300), ([(0, 4), (200, 3)], 4)]
+
+
+def _with_key(p, token, value):
+    """The cache with another scale of sequence 0's key `token`, all heads."""
+    t = [x.clone() for x in p.t]
+    page, off = int(p.table[0, token // p.page]), token % p.page
+    if p.fmt == "u4":
+        t[2][page, :, off, 0] = value
+    else:
+        t[2][page, :, off] = value
+    return p.q_.qlin_kv_cache(*t, p.cache.fmt)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("seqs,most", CUTS)
+def test_rows_that_are_no_numbers(qlin_gpu, fmt, d, seqs, most):
+    """A row whose only scores are NaN is NaN, out and lse, whoever has its segment: from its q, from a key that it sees alone."""
+    for window, hit_of in ((0, "q"), (0, "key"), (1, "key")):
+        p = Problem(qlin_gpu, seqs, 4, 2, d, 16, fmt, torch.float16, window=window).run()
+        clean, clean_lse = p.out.clone(), p.lse.clone()
+        c, n = seqs[0]
+        hit = torch.zeros(p.q.shape[:2], dtype=torch.bool)
+        if hit_of == "q":
+            p.q[0, 0, 3] = p.q[n - 1, 1, d - 1] = p.q[n // 2, 3, 0] = p.q[p.tq - 1, 2, 1] = float("nan")
+            hit[0, 0] = hit[n - 1, 1] = hit[n // 2, 3] = hit[p.tq - 1, 2] = True
+        else:
+            token = c + (n // 2 if window else 0)        # (without a window and a context: all that row 0 sees)
+            p.cache = _with_key(p, token, float("nan"))
+            hit[token - c:token - c + 1 if window else n] = True
+        p.run()
+        hit = hit.cuda()
+        assert bool(torch.isnan(p.out[hit]).all()) and bool(torch.isnan(p.lse[hit]).all())
+        assert torch.equal(p.out[~hit], clean[~hit]) and torch.equal(p.lse[~hit], clean_lse[~hit])
