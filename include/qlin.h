@@ -930,7 +930,8 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * lost below 2^-33.  Scales of 0 and below it are as good as others.  A key or a value
  * that is not a number (its scale, its zero-point, an E4M3 code) makes the rows
  * that see its token not numbers, and no others; a row of q that holds a NaN is
- * not a number either.
+ * not a number either.  A row whose scores are all -infinity gets out = 0 and lse =
+ * -infinity.
  *
  * qlin_verify_drafts: which of the drafted tokens of each sequence stay, and the
  * token after them.  Node i of sequence b is row q_indptr[b] + i, at most

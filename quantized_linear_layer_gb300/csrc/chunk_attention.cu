@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(128) chunk_attention_join_kernel(const __grid_
         o[x].w = o[x].w * fa + v.w * fb;
       }
     }
-    const float inv = __frcp_rn(l);
+    const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
     const int64_t node = at / p.group;
     const int head = rec.head * p.group + static_cast<int>(at - node * p.group);
     const int64_t tok = rec.q_row + node;

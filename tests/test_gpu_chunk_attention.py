@@ -493,14 +493,16 @@ def test_streams_without_rows(qlin_gpu, fmt, seqs, slopes):
 CUTS = [([(0, 100)], 100), ([(0, 70)] * 3 + [(3, 66)], 70), ([(0, 40), (20, 65)] * 150, 65), ([(700, 300)], 300), ([(0, 4), (200, 3)], 4)]
 
 
-def _with_key(p, token, value):
-    """The cache with another scale of sequence 0's key `token`, all heads."""
+def _with_key(p, token, value, code=None):
+    """The cache with another scale (and code) of sequence 0's key `token`, all heads."""
     t = [x.clone() for x in p.t]
     page, off = int(p.table[0, token // p.page]), token % p.page
     if p.fmt == "u4":
         t[2][page, :, off, 0] = value
     else:
         t[2][page, :, off] = value
+    if code is not None:
+        t[0][page, :, off] = code
     return p.q_.qlin_kv_cache(*t, p.cache.fmt)
 
 
@@ -524,4 +526,22 @@ def test_rows_that_are_no_numbers(qlin_gpu, fmt, d, seqs, most):
         p.run()
         hit = hit.cuda()
         assert bool(torch.isnan(p.out[hit]).all()) and bool(torch.isnan(p.lse[hit]).all())
+        assert torch.equal(p.out[~hit], clean[~hit]) and torch.equal(p.lse[~hit], clean_lse[~hit])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("seqs,most", CUTS)
+def test_rows_of_minus_infinity(qlin_gpu, d, seqs, most):
+    """A row whose only score is -infinity: 0 and -infinity, whoever has its segment."""
+    p = Problem(qlin_gpu, seqs, 4, 2, d, 16, "int8", torch.float16, window=1)
+    p.q.abs_()
+    p.run()
+    clean, clean_lse = p.out.clone(), p.lse.clone()
+    c, n = seqs[0]
+    for row in (0, n // 2, n - 1):
+        p.cache = _with_key(p, c + row, float("inf"), -7)
+        p.run()
+        hit = torch.zeros(len(p.q), dtype=torch.bool, device="cuda")
+        hit[row] = True
+        assert not p.out[hit].any() and bool((p.lse[hit] == -float("inf")).all())
         assert torch.equal(p.out[~hit], clean[~hit]) and torch.equal(p.lse[~hit], clean_lse[~hit])
