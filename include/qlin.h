@@ -970,7 +970,8 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * (Keys keep the rotation they were written with: a node's position is that of its
  * depth.)
  *   path   int32 [B][max_path], count int32 [B], as qlin_verify_drafts gives them
- *   lens   out, int32 [B]: ctx_lens[b] + count[b], or NULL; not ctx_lens itself
+ *   lens   out, int32 [B]: ctx_lens[b] + count[b], or NULL; it must not overlap
+ *          ctx_lens, count, path or block_table
  *
  * Each call has a _prepare form with the same arguments, which checks them
  * and plans the launches into *call (host memory) without launching anything;

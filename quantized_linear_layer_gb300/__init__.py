@@ -1115,5 +1115,5 @@ def qlin_kv_cache_keep_prepare(cache, block_table, ctx_lens, path, count, lens=N
 
 def qlin_kv_cache_keep(cache, block_table, ctx_lens, path, count, lens=None, stream=None):
     """Token ctx_lens[b] + path[b][i] of every sequence moved to place ctx_lens[b] + i, i < count[b] (path int32
-    [B][max_path], ascending); lens int32 [B] (optional, not ctx_lens) gets ctx_lens + count."""
+    [B][max_path], ascending); lens int32 [B] (optional, apart from the others) gets ctx_lens + count."""
     qlin_kv_cache_keep_prepare(cache, block_table, ctx_lens, path, count, lens).run(stream)

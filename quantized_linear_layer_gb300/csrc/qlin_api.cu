@@ -818,6 +818,12 @@ bool all_aligned(uintptr_t bytes, std::initializer_list<const void*> pointers) {
   return true;
 }
 
+// Whether two arrays of 4-byte elements share memory (a null pointer's has none).
+bool overlap4(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + 4 * static_cast<uint64_t>(nb) && y < x + 4 * static_cast<uint64_t>(na);
+}
+
 qlin_status check_cache(const qlin_kv_cache* c) {
   QLIN_REQUIRE(c != nullptr, QLIN_ERR_INVALID_ARG, "null cache");
   QLIN_REQUIRE(c->fmt >= QLIN_KV_INT8 && c->fmt <= QLIN_KV_U4, QLIN_ERR_INVALID_ARG, "cache: unknown format %d", c->fmt);
@@ -1171,9 +1177,12 @@ qlin_status qlin_kv_cache_keep_prepare(const qlin_kv_cache* cache, const int32_t
   QLIN_CHECK(check_cache(cache));
   if (B == 0) return empty_call(plan);
   QLIN_REQUIRE(block_table && ctx_lens && count && (max_path == 0 || path), QLIN_ERR_INVALID_ARG, "null pointer");
-  QLIN_REQUIRE(lens != ctx_lens, QLIN_ERR_INVALID_ARG, "lens must not be ctx_lens");
   QLIN_REQUIRE(all_aligned(4, {block_table, ctx_lens, path, count, lens}), QLIN_ERR_ALIGNMENT,
                "int32 arrays must be 4-byte aligned");
+  // One of a sequence's blocks writes its length while others still read what they go by.
+  QLIN_REQUIRE(!overlap4(lens, B, ctx_lens, B) && !overlap4(lens, B, count, B) && !overlap4(lens, B, path, B * max_path) &&
+                   !overlap4(lens, B, block_table, B * max_pages),
+               QLIN_ERR_INVALID_ARG, "lens must not overlap ctx_lens, count, path or block_table");
   QLIN_DEVICE();
   return planned(plan, plan_kv_cache_keep(cache, block_table, max_pages, ctx_lens, path, count, B, max_path, lens, plan),
                  "kv_cache_keep");

@@ -96,6 +96,23 @@ def test_verify_and_keep_refusals(L):
     assert keep(c=cache(page_size=48)) == UNSUPPORTED and keep(b=0, table=None) == OK
 
 
+def test_keep_refuses_lengths_over_what_it_reads(L):
+    """lens may share no byte with what the blocks of a sequence still read when one of them writes it."""
+    call = ctypes.cast((ctypes.c_uint64 * 112)(), P)
+    at = dict(table=1024, ctx=2048, path=4096, count=8192)          # 4 sequences: 48, 16, 80 and 16 bytes
+
+    def keep(lens, **change):
+        a = changed(at, change)
+        return L.qlin_kv_cache_keep_prepare(ptr(cache()), P(a["table"]), 3, P(a["ctx"]), P(a["path"]), P(a["count"]), 4, 5,
+                                            None if lens is None else P(lens), call)
+    for name, size in (("table", 48), ("ctx", 16), ("path", 80), ("count", 16)):
+        for lens in (at[name] - 12, at[name], at[name] + 4, at[name] + size - 4):
+            assert keep(lens) == INVALID, (name, lens)
+        for lens in (at[name] - 16, at[name] + size):
+            assert keep(lens) != INVALID, (name, lens)
+    assert keep(None) != INVALID
+
+
 def test_prepared_refusals(L):
     c = (ctypes.c_uint64 * 112)()
     at = ctypes.cast(c, P)
