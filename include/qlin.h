@@ -906,8 +906,10 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  *   slots      out, int64 [T]: where the row's k and v go (page * page_size +
  *              offset); -1 for rows behind the last sequence's (the cache write
  *              leaves them out)
- * Lengths, page counts or a stack that are out of range are recorded in the
- * device error word; such a sequence stays as it is and gets no rows.
+ * Lengths and page counts that are out of range are recorded in the device error
+ * word; such a sequence stays as it is and gets no rows.  So is a stack whose
+ * count is out of range, or goes out of it by what is given back; then no sequence
+ * and no page changes, and there are no rows.
  *
  * qlin_chunk_attention: sequence b has ctx_lens[b] tokens in the cache and, at
  * places ctx_lens[b] + i, its new ones i < q_indptr[b + 1] - q_indptr[b] <=

@@ -140,9 +140,12 @@ __global__ void __launch_bounds__(kThreads) kv_pages_kernel(const __grid_constan
     given += total.a;
   }
   int64_t top = *p.free_count;
-  if (top < 0 || top + given > p.pages) {  // no stack of this many pages
+  if (top < 0 || top + given > p.pages) {  // no stack of this many pages: nothing moves, nobody gets rows
     if (t == 0) record_device_error(p.err, kDevErrBadIndex);
-    top = top < 0 ? 0 : min(top, static_cast<int64_t>(p.pages));
+    for (int64_t b = t; b <= p.B; b += kThreads) p.indptr[b] = 0;
+    if (p.rows_inside)
+      for (int64_t row = t; row < p.T; row += kThreads) write_row(p, row, -1, 0);
+    return;
   }
 
   // back to the stack
@@ -156,14 +159,13 @@ __global__ void __launch_bounds__(kThreads) kv_pages_kernel(const __grid_constan
       __syncthreads();
       for (int64_t i = t; i < total.a; i += kThreads) {
         const int x = last_at(begin, kThreads, i);
-        const int64_t to = top + given - 1 - (before + i);
-        if (to < p.pages) p.free_pages[to] = p.table[(b0 + x) * p.max_pages + at_of[x] + i - begin[x]];
+        p.free_pages[top + given - 1 - (before + i)] = p.table[(b0 + x) * p.max_pages + at_of[x] + i - begin[x]];
       }
       before += total.a;
       __syncthreads();
     }
   }
-  top = min(top + given, static_cast<int64_t>(p.pages));
+  top += given;
   __syncthreads();  // (and the stack's new pages are there for all threads)
 
   // from the stack; what the sequences before asked for counts whether they got it or not

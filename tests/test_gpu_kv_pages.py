@@ -114,6 +114,29 @@ def test_stack_out_of_range(qlin_gpu):
         assert whole[:2].tolist() == [77, 77] and whole[10:].tolist() == [77, 77]
 
 
+@pytest.mark.parametrize("seqs,rows", [(1, 0), (3, 40), (1500, 40), (3, 3000)])
+@pytest.mark.parametrize("count", [-3, -2 ** 31, 0, 2 ** 31 - 1, "one too many", "one too many free"])
+def test_a_stack_out_of_range_moves_nothing(qlin_gpu, seqs, rows, count):
+    """Pages that would go back, be taken or be kept all stay where they are, and there are no rows."""
+    q, most, pages = qlin_gpu, 4, seqs * 4
+    gives = seqs * 2
+    bad = {"one too many": pages - gives + 1, "one too many free": pages + 1}.get(count, count)
+    held = [3] * seqs
+    table = torch.arange(seqs * most, dtype=torch.int32, device="cuda").view(seqs, most)
+    state = [table, _ints(held), _ints(list(range(pages))), _ints([bad])]
+    before = [x.clone() for x in state]
+    pool = q.qlin_kv_pages(*state, 16)
+    indptr, positions, slots = _ints([9] * (seqs + 1)), _ints([9] * rows, torch.int64), _ints([9] * rows, torch.int64)
+    ctx, new = [0 if b < gives // 2 else 40 for b in range(seqs)], [1] * seqs
+    q.qlin_kv_pages_assign(pool, _ints(ctx), _ints(new), indptr, positions, slots)
+    if count == 0:    # (an empty stack is one)
+        assert q.qlin_get_device_error() == 0 and state[3].item() == gives and state[1].tolist() == [1] * seqs
+        return
+    assert q.qlin_get_device_error() == 0x2000
+    assert all(torch.equal(x, y) for x, y in zip(state, before))
+    assert not indptr.any() and not positions.any() and bool((slots == -1).all())
+
+
 def test_page_numbers_out_of_range(qlin_gpu):
     """A table that holds a page that is none gives no slot there."""
     q = qlin_gpu
