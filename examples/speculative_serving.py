@@ -115,19 +115,22 @@ class Prefill(Pass):
         self.attend = qlin.qlin_chunk_attention_prepare(self.q, cache.handle, cache.table, self.indptr, cache.ctx, self.att,
                                                         torch.empty(size, dtype=torch.uint8, device="cuda"), chunk, **scores)
         # the token behind a prompt: a tree of one node, from which nothing is kept
-        self.none, self.nodes = torch.zeros(seqs, **I64), torch.arange(seqs + 1, **I32)
-        self.path, self.kept = torch.zeros(seqs, 1, **I32), torch.zeros(seqs, **I32)
+        self.none, self.nodes = torch.zeros(seqs, **I64), torch.zeros(seqs + 1, **I32)
+        self.path, self.kept, self.next = torch.zeros(seqs, 1, **I32), torch.zeros(seqs, **I32), torch.zeros(seqs, **I64)
 
     def run(self, tokens, sample):
-        """`tokens`: a list of int64 tensors; the next token of each sequence is drawn with `sample` [seqs]."""
+        """`tokens`: a list of int64 tensors; the next token of each sequence that has any is drawn with `sample` [seqs]."""
         self.new.copy_(torch.tensor([t.numel() for t in tokens]))
         flat = torch.cat(tokens)
         self.tokens[:flat.numel()] = flat
         h = self.hidden()
-        ends = (self.indptr[1:].long() - 1).clamp(min=0)
+        # a node for each sequence with rows, at the last of them; the others have none and keep the token that they have
+        some = self.indptr[1:] > self.indptr[:-1]
+        self.nodes[1:] = some.cumsum(0)
+        ends = (self.indptr[1:].long() - 1).clamp(min=0)[(~some).long().argsort(stable=True)]
         probs = self.model.probabilities(h[ends])
-        qlin.qlin_verify_drafts(probs, None, None, self.none, self.nodes, torch.zeros_like(sample), sample, self.path, self.kept,
-                                self.cache.last)
+        qlin.qlin_verify_drafts(probs, None, None, self.none, self.nodes, torch.zeros_like(sample), sample, self.path, self.kept, self.next)
+        self.cache.last.copy_(torch.where(self.kept > 0, self.next, self.cache.last))
         self.cache.ctx += self.new
 
 

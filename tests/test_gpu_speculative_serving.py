@@ -141,6 +141,53 @@ def test_prompts_drafts_and_kept_paths(qlin_gpu, fmt):
     assert qlin_gpu.qlin_get_device_error() == 0
 
 
+class _Spy:
+    """A model's probabilities, and the rows that they were asked for."""
+
+    def __init__(self, model):
+        self.inner, self.calls = model.probabilities, []
+        model.probabilities = self
+
+    def __call__(self, h):
+        probs = self.inner(h)
+        self.calls.append((h.clone(), probs.clone()))
+        return probs
+
+    def of(self, row):
+        """The last call's probabilities for a row equal to `row`."""
+        h, probs = self.calls[-1]
+        same = (h == row).all(1).nonzero()[:, 0]
+        assert len(same)
+        return probs[int(same[0])]
+
+
+def _small(ex, seqs, pages, room=240, page=16):
+    model = ex.Model(300, 256, 8, 2, 64)
+    return model, ex.Cache(seqs, room, pages, 2, 64, "int8", page)
+
+
+def test_prompts_of_some_sequences(qlin_gpu):
+    """A sequence with tokens in a pass gets the one drawn behind its own; the others keep what they have."""
+    ex = _example()
+    model, cache = _small(ex, 4, 40)
+    spy, gen = _Spy(model), torch.Generator().manual_seed(9)
+    prefill = ex.Prefill(model, cache, 30)
+    last, lens = [7, 8, 9, 10], [0] * 4
+    cache.last.copy_(torch.tensor(last))
+    for new in ([5, 0, 3, 0], [0, 30, 0, 1], [0, 0, 0, 2], [1, 1, 1, 1], [0, 0, 17, 0], [0, 0, 0, 0]):
+        sample = torch.rand(4, generator=gen)
+        prefill.run([torch.randint(300, (n,), generator=gen).cuda() for n in new], sample.cuda())
+        torch.cuda.synchronize()
+        h = model.embedding[prefill.tokens] + prefill.y
+        for b, n in enumerate(new):
+            if n > 0:
+                probs = spy.of(h[int(prefill.indptr[b + 1]) - 1]).cpu().numpy()
+                last[b] = serving.verify(probs[None], None, [-1], [0], [0.0], float(sample[b]))[1]
+            lens[b] += n
+        assert cache.last.tolist() == last and cache.ctx.tolist() == lens
+    assert qlin_gpu.qlin_get_device_error() == 0
+
+
 def test_the_command_runs(qlin_gpu):
     import subprocess
     import sys
