@@ -86,7 +86,7 @@ class Pass:
         self.new = torch.zeros(seqs, **I32)
         self.indptr = torch.zeros(seqs + 1, **I32)
         self.positions, self.slots = torch.zeros(rows, **I64), torch.zeros(rows, **I64)
-        self.tokens = torch.zeros(rows, **I64)
+        self.tokens, self.at = torch.zeros(rows, **I64), torch.arange(rows, **I32)
         self.qkv = [torch.zeros(rows, n, m.head_dim, **f16) for n in (m.heads, m.kv_heads, m.kv_heads)]
         self.q, self.att = (torch.zeros(rows, m.heads, m.head_dim, **f16) for _ in range(2))
         self.y = torch.zeros(rows, m.embedding.shape[1], **f16)
@@ -94,9 +94,16 @@ class Pass:
         self.rotate = qlin.qlin_qk_norm_rope_cache_prepare(*self.qkv, self.q, self.positions, m.inv_freq, self.slots, cache.handle,
                                                            m.q_gamma, m.k_gamma)
 
+    def rows(self):
+        """The sequence of each row, and which of its new tokens it is: a sequence that pages or rows ran out for has no rows, and
+        those behind it move up.  (Rows behind the last sequence's: of any.)"""
+        seq = torch.searchsorted(self.indptr[1:], self.at, right=True).clamp(max=self.new.numel() - 1)
+        return seq, self.at - self.indptr[seq]
+
     def hidden(self):
         """Pages, places and the block's output for the rows' tokens (rows behind the last sequence's mean nothing)."""
         self.assign.run()
+        self.place()
         x = self.model.embedding[self.tokens]
         qlin.qlin_w4a16_gemm_grouped(x, *map(list, zip(*self.model.w_qkv)), [t.view(t.shape[0], -1) for t in self.qkv])
         self.rotate.run()
@@ -114,24 +121,34 @@ class Prefill(Pass):
         size = qlin.qlin_chunk_attention_workspace_bytes(cache.handle, model.heads, chunk, seqs)
         self.attend = qlin.qlin_chunk_attention_prepare(self.q, cache.handle, cache.table, self.indptr, cache.ctx, self.att,
                                                         torch.empty(size, dtype=torch.uint8, device="cuda"), chunk, **scores)
+        self.given, self.starts = torch.zeros(seqs * chunk, **I64), torch.zeros(seqs, **I64)
         # the token behind a prompt: a tree of one node, from which nothing is kept
         self.none, self.nodes = torch.zeros(seqs, **I64), torch.zeros(seqs + 1, **I32)
         self.path, self.kept, self.next = torch.zeros(seqs, 1, **I32), torch.zeros(seqs, **I32), torch.zeros(seqs, **I64)
 
+    def place(self):
+        seq, i = self.rows()
+        self.tokens.copy_(self.given[(self.starts[seq] + i).clamp(max=self.given.numel() - 1)])
+
     def run(self, tokens, sample):
-        """`tokens`: a list of int64 tensors; the next token of each sequence that has any is drawn with `sample` [seqs]."""
-        self.new.copy_(torch.tensor([t.numel() for t in tokens]))
+        """`tokens`: a list of int64 tensors; the next token of each sequence that has any is drawn with `sample` [seqs].  Returns how
+        many of them each sequence took, on the device: all, or none where pages or rows ran out (they can be given again)."""
+        sizes = torch.tensor([t.numel() for t in tokens])
+        self.new.copy_(sizes)
+        self.starts.copy_(sizes.cumsum(0) - sizes)
         flat = torch.cat(tokens)
-        self.tokens[:flat.numel()] = flat
+        self.given[:flat.numel()] = flat
         h = self.hidden()
         # a node for each sequence with rows, at the last of them; the others have none and keep the token that they have
-        some = self.indptr[1:] > self.indptr[:-1]
+        taken = self.indptr[1:] - self.indptr[:-1]
+        some = taken > 0
         self.nodes[1:] = some.cumsum(0)
         ends = (self.indptr[1:].long() - 1).clamp(min=0)[(~some).long().argsort(stable=True)]
         probs = self.model.probabilities(h[ends])
         qlin.qlin_verify_drafts(probs, None, None, self.none, self.nodes, torch.zeros_like(sample), sample, self.path, self.kept, self.next)
         self.cache.last.copy_(torch.where(self.kept > 0, self.next, self.cache.last))
-        self.cache.ctx += self.new
+        self.cache.ctx += taken
+        return taken
 
 
 class Speculate(Pass):
@@ -144,27 +161,36 @@ class Speculate(Pass):
         self.seqs, self.n = seqs, n
         self.levels = [(p, torch.tensor([i for i, x in enumerate(parents) if x == p], **I64)) for p in sorted(set(parents[1:]))]
         self.new.fill_(n)
+        # (a sequence with rows has n of them, so these are the same rows whoever has none)
         self.parent = torch.tensor([max(p, 0) for p in parents], **I32).repeat(seqs)
         self.mask = words.repeat(seqs, 1).cuda()
+        self.tree = torch.zeros(seqs, n, **I64)
         self.accept, self.sample = torch.zeros(seqs * n, device="cuda"), torch.zeros(seqs, device="cuda")
+        self.accept_rows = torch.zeros(seqs * n, device="cuda")
         self.path, self.kept = torch.zeros(seqs, n, **I32), torch.zeros(seqs, **I32)
         self.next, self.after = torch.zeros(seqs, **I64), torch.zeros(seqs, **I32)
         self.probs = torch.zeros(seqs * n, model.vocab, device="cuda")
         size = qlin.qlin_tree_attention_workspace_bytes(cache.handle, model.heads, n, seqs)
         self.attend = qlin.qlin_tree_attention_prepare(self.q, cache.handle, cache.table, self.indptr, cache.ctx, self.mask, self.att,
                                                        torch.empty(size, dtype=torch.uint8, device="cuda"), n)
-        self.verify = qlin.qlin_verify_drafts_prepare(self.probs, None, self.parent, self.tokens, self.indptr, self.accept, self.sample,
+        self.verify = qlin.qlin_verify_drafts_prepare(self.probs, None, self.parent, self.tokens, self.indptr, self.accept_rows, self.sample,
                                                       self.path, self.kept, self.next)
         self.keep = qlin.qlin_kv_cache_keep_prepare(cache.handle, cache.table, cache.ctx, self.path, self.kept, self.after)
         self.graph = None
 
     def draft(self):
         """Level by level, a node's children are the likeliest tokens behind it."""
-        tree = self.tokens.view(self.seqs, self.n)
+        tree = self.tree
         tree[:, 0] = self.cache.last
         for p, children in self.levels:
             likely = self.model.logits(self.model.embedding[tree[:, p]]).topk(children.numel()).indices
             tree.index_copy_(1, children, likely)
+
+    def place(self):
+        seq, i = self.rows()
+        i = i.clamp(max=self.n - 1)
+        self.tokens.copy_(self.tree[seq, i])
+        self.accept_rows.copy_(self.accept.view(self.seqs, self.n)[seq, i])
 
     def launch(self):
         self.draft()
@@ -172,7 +198,7 @@ class Speculate(Pass):
         self.verify.run()
         self.keep.run()
         self.cache.ctx.copy_(self.after)
-        self.cache.last.copy_(self.next)
+        self.cache.last.copy_(torch.where(self.kept > 0, self.next, self.cache.last))  # (none kept: no pages, tried again)
 
     def capture(self):
         """Captures the step (on copies of the state, which a first run moves on)."""
@@ -190,7 +216,8 @@ class Speculate(Pass):
             self.launch()
 
     def run(self, accept, sample):
-        """One step with these random numbers; returns the kept nodes and how many, [seqs][n] and [seqs], on the device."""
+        """One step with these random numbers, [seqs][n] and [seqs]; returns the kept nodes and how many (none where pages ran out), as
+        many, on the device."""
         self.accept.copy_(accept)
         self.sample.copy_(sample)
         if self.graph is None:
@@ -237,6 +264,8 @@ def main():
     for at in range(0, a.prompt, a.chunk):
         part = prompts[:, at:at + a.chunk]
         timed("prompt, %d tokens behind %d, %d sequences" % (part.shape[1], at, a.seqs), lambda: prefill.run(list(part), rand(a.seqs)))
+    if int(cache.ctx.min()) < a.prompt:
+        raise RuntimeError("too few pages for the prompts")
     step = Speculate(model, cache, parents)
     step.capture()
     kept = 0

@@ -188,6 +188,72 @@ def test_prompts_of_some_sequences(qlin_gpu):
     assert qlin_gpu.qlin_get_device_error() == 0
 
 
+def test_prompts_that_pages_run_out_for(qlin_gpu):
+    """A refused prompt changes nothing of its sequence and can be given again; one served behind it has its own tokens."""
+    ex = _example()
+    model, cache = _small(ex, 3, 4)
+    spy, gen = _Spy(model), torch.Generator().manual_seed(3)
+    prefill = ex.Prefill(model, cache, 60)
+    last, lens = [7, 8, 9], [0] * 3
+    cache.last.copy_(torch.tensor(last))
+    for new, ended, want in (([30, 0, 3], None, [30, 0, 3]), ([0, 60, 5], None, [0, 0, 5]), ([0, 60, 0], None, [0, 0, 0]),
+                             ([2, 60, 8], None, [2, 0, 8]), ([0, 60, 0], 0, [0, 0, 0]), ([0, 48, 0], None, [0, 48, 0]),
+                             ([1, 0, 0], None, [0, 0, 0])):
+        if ended is not None:
+            cache.ctx[ended] = lens[ended] = 0
+        sample = torch.rand(3, generator=gen)
+        tokens = [torch.randint(300, (n,), generator=gen).cuda() for n in new]
+        prefill.run(tokens, sample.cuda())
+        torch.cuda.synchronize()
+        assert (prefill.indptr[1:] - prefill.indptr[:-1]).tolist() == want
+        h = model.embedding[prefill.tokens] + prefill.y
+        for b, n in enumerate(want):
+            if n > 0:
+                a, e = int(prefill.indptr[b]), int(prefill.indptr[b + 1])
+                assert torch.equal(prefill.tokens[a:e], tokens[b]) and prefill.positions[a:e].tolist() == list(range(lens[b], lens[b] + n))
+                last[b] = serving.verify(spy.of(h[e - 1]).cpu().numpy()[None], None, [-1], [0], [0.0], float(sample[b]))[1]
+            lens[b] += n
+        assert cache.last.tolist() == last and cache.ctx.tolist() == lens
+    assert qlin_gpu.qlin_get_device_error() == 0
+
+
+def test_trees_that_pages_run_out_for(qlin_gpu):
+    """A refused sequence keeps its length and its token, is taken up with them when pages come back, and the sequences behind it
+    are verified with their own tokens and numbers."""
+    ex = _example()
+    model, cache = _small(ex, 3, 6)
+    gen = torch.Generator().manual_seed(6)
+    ex.Prefill(model, cache, 30).run([torch.randint(300, (n,), generator=gen).cuda() for n in (30, 16, 17)], torch.rand(3, generator=gen).cuda())
+    parents = [-1, 0, 0, 0, 1, 1, 2, 4, 4, 6, 7]
+    n = len(parents)
+    step = ex.Speculate(model, cache, parents)
+    lens, last, refused = [30, 16, 17], cache.last.tolist(), 0
+    for turn in range(6):
+        if turn == 3:       # the first sequence ends
+            cache.ctx[0] = step.new[0] = lens[0] = 0
+        state = _state(cache)
+        accept, sample = torch.rand(3 * n, generator=gen), torch.rand(3, generator=gen)
+        if turn % 2:
+            accept.zero_()
+        step.run(accept, sample)
+        torch.cuda.synchronize()
+        bounds, _, _ = state.assign(lens, step.new.tolist(), 3 * n, ex.tree_words(parents, 1)[1].tolist() * 3)
+        assert step.indptr.tolist() == bounds
+        for b in range(3):
+            a, e = bounds[b:b + 2]
+            if a == e:
+                assert int(step.kept[b]) == 0
+                refused += turn < 3 and b == 1
+                continue
+            toks = step.tokens[a:e].tolist()
+            assert toks[0] == last[b]
+            path, last[b] = serving.verify(step.probs[a:e].cpu().numpy(), None, parents, toks, accept[b * n:b * n + n].numpy(), float(sample[b]))
+            assert step.path[b].tolist() == path + [-1] * (n - len(path)) and int(step.kept[b]) == len(path)
+            lens[b] += len(path)
+        assert cache.ctx.tolist() == lens and cache.last.tolist() == last
+    assert refused > 0 and lens[1] > 16 and qlin_gpu.qlin_get_device_error() == 0
+
+
 def test_the_command_runs(qlin_gpu):
     import subprocess
     import sys
