@@ -897,7 +897,10 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * it ask for are there, and one that has new tokens while theirs and those before
  * fit into T; one that is not served keeps the pages it has, gets no rows, and is
  * asked for again in a later step.  So giving the same lengths twice changes
- * nothing, and giving new_lens of 0 takes a step back.
+ * nothing, and giving new_lens of 0 takes a step back.  Rows of sequences behind one
+ * that is not served move up: what a caller has for each row (tokens, masks,
+ * parents, random numbers, depths) is taken up by q_indptr, depths by that of a
+ * first call without them, where they differ from sequence to sequence.
  *   q_indptr   out, int32 [B + 1]: the rows of sequence b are q_indptr[b] ..
  *              q_indptr[b + 1] - 1, as attention takes them
  *   positions  out, int64 [T]: ctx_lens[b] + i for row q_indptr[b] + i, or

@@ -1003,7 +1003,8 @@ def qlin_kv_pages_assign_prepare(pages, ctx_lens, new_lens, q_indptr, positions,
 def qlin_kv_pages_assign(pages, ctx_lens, new_lens, q_indptr, positions, slots, depths=None, stream=None):
     """A step's pages, row bounds, positions and slots from the sequences' lengths (int32 [B]): pages that are no longer
     needed go back, lacking ones are taken, and q_indptr int32 [B + 1], positions and slots int64 [T] are written, in place.
-    depths int32 [T]: positions are ctx_lens + depths (a tree's nodes).  Sequences that pages or rows run out for get no rows."""
+    depths int32 [T]: positions are ctx_lens + depths (a tree's nodes).  Sequences that pages or rows run out for get no rows, and
+    those behind them move up: depths that differ by sequence are packed by the q_indptr of a first call without them."""
     qlin_kv_pages_assign_prepare(pages, ctx_lens, new_lens, q_indptr, positions, slots, depths).run(stream)
 
 

@@ -76,6 +76,33 @@ def test_a_step_taken_back(qlin_gpu):
         assert all(torch.equal(a, b) for a, b in zip(before, (pool.free, pool.count, pool.held)))
 
 
+@pytest.mark.parametrize("seqs,rows", [(7, 40), (300, 1500), (1200, 5000)])
+def test_depths_of_trees_that_differ(qlin_gpu, seqs, rows):
+    """Sequences run out of pages or rows: depths packed by a first call's row bounds are those of their own sequences' nodes."""
+    r = random.Random(rows)
+    page = 16
+    pool = Pool(qlin_gpu, seqs, seqs * 2, page, 5)
+    refused = 0
+    for turn in range(4):
+        ctx = [r.randint(0, 3 * page) if turn else 0 for _ in range(seqs)]
+        new = [r.randint(0, 2 * page - 4) if r.random() < 0.3 else r.randint(0, 4) for _ in range(seqs)]
+        trees = [[r.randint(0, 9) for _ in range(n)] for n in new]
+        indptr, _, slots = [t.clone() for t in pool.step(ctx, new, rows)]
+        first = torch.tensor([0] + new).cumsum(0).cuda()
+        flat = _ints([x for t in trees for x in t] + [0] * rows)
+        at = torch.arange(rows, dtype=torch.int32, device="cuda")
+        seq = torch.searchsorted(indptr[1:], at, right=True).clamp(max=seqs - 1)
+        depths = flat[(first[seq] + at - indptr[seq]).clamp(max=flat.numel() - 1)]
+        again, positions, slots2 = pool.step(ctx, new, rows, depths.tolist())
+        assert torch.equal(indptr, again) and torch.equal(slots, slots2)
+        bounds, positions = indptr.tolist(), positions.tolist()
+        for b, (c, n) in enumerate(zip(ctx, new)):
+            a, e = bounds[b:b + 2]
+            assert positions[a:e] == [c + x for x in trees[b]][:e - a] and e - a in (0, n)
+            refused += e - a < n
+    assert refused > 0 and qlin_gpu.qlin_get_device_error() == 0
+
+
 def test_long_prompt(qlin_gpu):
     """One sequence takes 8192 pages and gives them back."""
     pool = Pool(qlin_gpu, 2, 8200, 16, 8192)
