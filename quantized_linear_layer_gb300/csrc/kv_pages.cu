@@ -3,8 +3,9 @@
 //
 // Sequence b needs need = ceil((ctx + new) / page) pages and holds `held`.  It
 // gives back give = max(held - need, 0) and asks for take = max(need - held, 0)
-// of the stack of free pages.  All three of (give, take, new) are summed along
-// the sequences by one block, 1024 sequences at a time; what moves is then dealt
+// of the stack of free pages.  One block sums along the sequences, 1024 at a time:
+// what they give; what they ask for and add, which says who is served; and what of
+// that the served ones get.  What moves is then dealt
 // out evenly to the threads (a thread finds its sequence in the sums by
 // bisection), so one long prompt and a thousand short ones cost alike.  The
 // last sequence's last page goes on the stack first, so a step that is taken
@@ -47,7 +48,7 @@ struct Params {
 };
 
 struct Sums {
-  int64_t a, b, c;
+  int64_t a, b;
 };
 
 // Inclusive sums over the block's threads, and the block's totals; `part` has kWarps + 1 entries.
@@ -55,9 +56,8 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* part, Sums& total) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t a = __shfl_up_sync(0xffffffffu, v.a, o), b = __shfl_up_sync(0xffffffffu, v.b, o),
-                  c = __shfl_up_sync(0xffffffffu, v.c, o);
-    if (lane >= o) v.a += a, v.b += b, v.c += c;
+    const int64_t a = __shfl_up_sync(0xffffffffu, v.a, o), b = __shfl_up_sync(0xffffffffu, v.b, o);
+    if (lane >= o) v.a += a, v.b += b;
   }
   __syncthreads();  // the last use of `part` is over
   if (lane == 31) part[warp] = v;
@@ -66,15 +66,14 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* part, Sums& total) {
     Sums s = part[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t a = __shfl_up_sync(0xffffffffu, s.a, o), b = __shfl_up_sync(0xffffffffu, s.b, o),
-                    c = __shfl_up_sync(0xffffffffu, s.c, o);
-      if (lane >= o) s.a += a, s.b += b, s.c += c;
+      const int64_t a = __shfl_up_sync(0xffffffffu, s.a, o), b = __shfl_up_sync(0xffffffffu, s.b, o);
+      if (lane >= o) s.a += a, s.b += b;
     }
     part[lane] = s;
   }
   __syncthreads();
   total = part[kWarps - 1];
-  if (warp > 0) v.a += part[warp - 1].a, v.b += part[warp - 1].b, v.c += part[warp - 1].c;
+  if (warp > 0) v.a += part[warp - 1].a, v.b += part[warp - 1].b;
   return v;
 }
 
@@ -136,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) kv_pages_kernel(const __grid_constan
   int64_t given = 0;  // by all sequences
   Sums total;
   for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
-    block_scan({request(p, b0 + t).give(), 0, 0}, part, total);
+    block_scan({request(p, b0 + t).give(), 0}, part, total);
     given += total.a;
   }
   int64_t top = *p.free_count;
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) kv_pages_kernel(const __grid_constan
     int64_t before = 0;
     for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
       const Request r = request(p, b0 + t);
-      const Sums s = block_scan({r.give(), 0, 0}, part, total);
+      const Sums s = block_scan({r.give(), 0}, part, total);
       begin[t] = s.a - r.give();
       at_of[t] = r.need;
       __syncthreads();
@@ -173,12 +172,12 @@ __global__ void __launch_bounds__(kThreads) kv_pages_kernel(const __grid_constan
   for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
     const int64_t b = b0 + t;
     const Request r = request(p, b);
-    const Sums ask = block_scan({r.take(), r.add, 0}, part, total);
+    const Sums ask = block_scan({r.take(), r.add}, part, total);
     const bool fits = (r.take() == 0 || asked_pages + ask.a <= top) && (r.add == 0 || asked_rows + ask.b <= p.T);
     asked_pages += total.a;
     asked_rows += total.b;
     const int64_t take = fits ? r.take() : 0, add = fits ? r.add : 0;
-    const Sums got = block_scan({take, add, 0}, part, total);
+    const Sums got = block_scan({take, add}, part, total);
     if (b < p.B) {
       if (r.valid) p.held[b] = static_cast<int32_t>(fits ? r.need : min(r.held, r.need));
       p.indptr[b + 1] = static_cast<int32_t>(rows + got.b);
