@@ -929,7 +929,7 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  *   workspace   qlin_chunk_attention_workspace_bytes(...) bytes, 256-byte
  *               aligned, contents arbitrary; one call at a time may use it
  * Scores, sums and out are held in float32; a cap adds up to 2^-20 of itself
- * to a score's error.  A probability times its value's scale is rounded to 11
+ * to a score's error, caps above 256 no more than 2^-18 of the score.  A probability times its value's scale is rounded to 11
  * bits; it keeps them down to 2^-23 of the largest such product of its row (of the largest
  * value scale of the row's 128 tokens, seen or not, where that is more) and is
  * lost below 2^-33.  Scales of 0 and below it are as good as others.  A key or a value

@@ -49,7 +49,7 @@ def chunk_attention(q, k, v, ctx, scale, softcap=0.0, slopes=None, window=0, pre
     """One sequence.  q [n][Hq][D], k, v [ctx + n][Hk][D] float64.
 
     Returns out, lse, and three bounds' parts: weight = sum p |v|; and with e_ij the error that float32 may make in a
-    score (D roundings of its products' magnitudes, 2^-20 of the cap, 2^-22 of the score and of the bias),
+    score (D roundings of its products' magnitudes, 2^-20 of the cap, of caps above 256 at most 2^-18 of the capped score, 2^-22 of the score and of the bias),
     sum p e |v| and sum p e."""
     n, hq, d = q.shape
     group, length = hq // k.shape[1], k.shape[0]
@@ -66,7 +66,7 @@ def chunk_attention(q, k, v, ctx, scale, softcap=0.0, slopes=None, window=0, pre
         e = d * 2.0 ** -24 * (np.abs(q[:, h]) @ np.abs(kk).T) * abs(scale) + 2.0 ** -22 * np.abs(s)
         if softcap:
             s = softcap * np.tanh(s / softcap)
-            e = e + 2.0 ** -20 * softcap
+            e = e + (2.0 ** -20 * softcap if softcap <= 256 else np.minimum(2.0 ** -20 * softcap, 2.0 ** -18 * np.abs(s)))
         if slopes is not None:
             bias = slopes[h] * np.abs(at - j)
             s, e = s - bias, e + 2.0 ** -22 * np.abs(bias)

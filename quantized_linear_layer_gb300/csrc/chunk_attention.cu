@@ -10,7 +10,8 @@
 // rounded to fp16's 11 bits, the one rounding of an operand (below 2^-33 of the row's
 // largest it becomes 0).  The reference m_i follows the running maximum lazily: P
 // may grow to 2^15 before it moves and the row of O is rescaled.
-// The cap is c tanh(s / c) = c (1 - 2 / (1 + 2^(2 log2(e) s / c))).
+// The cap is c tanh(s / c) = c (1 - 2 / (1 + 2^(2 log2(e) s / c))); caps above 256, for which that
+// loses small scores, have a variant of the kernel with tanh's power series.
 //
 // Work.  The rows of a key head (token, query head of the group) are cut into
 // tiles of 256 (128 for heads of 256), and of the tokens the tiles of 128 that some
@@ -161,12 +162,15 @@ __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, int32_t* 
   return false;
 }
 
+// Forms of the scores: plain ones (with a window and a prefix or without); a cap or a bias; a cap that large_capped() takes.
+enum { kPlainScores, kShaped, kLargeCap };
+
 struct WaitOps {  // for stage_ring.h's wait_or_raise
   volatile uint32_t* flag;
   __device__ __forceinline__ void raise() { *flag = 1; }
 };
 
-template <int FMT, int D, bool SHAPED>
+template <int FMT, int D, int SHAPED>
 __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kernel(const __grid_constant__ Params p) {
   using G = Geo<FMT, D>;
   constexpr int kRows = G::kRows, kStreams = G::kStreams, kSubs = G::kSubs, kBufs = G::kBufs;
@@ -807,8 +811,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
                   const float ks[4] = {sk.x, sk.y, sk.z, sk.w};
 #pragma unroll
                   for (int e = 0; e < 4; ++e) {
-                    const float r = rcp(1.0f + ex2(__uint_as_float(v[k + e]) * ks[e]));
-                    v[k + e] = __float_as_uint(fmaf(r, -2.0f * cap2, cap2));
+                    const float x = __uint_as_float(v[k + e]) * ks[e];
+                    v[k + e] = __float_as_uint(SHAPED == kLargeCap ? large_capped(x, cap2) : capped(x, cap2));
                   }
                 }
               } else {
@@ -1006,7 +1010,7 @@ __global__ void __launch_bounds__(128) chunk_attention_join_kernel(const __grid_
   }
 }
 
-template <int FMT, int D, bool SHAPED>
+template <int FMT, int D, int SHAPED>
 cudaError_t plan(const Params& p, Prepared* out) {
   const void* fn = reinterpret_cast<const void*>(chunk_attention_kernel<FMT, D, SHAPED>);
   const cudaError_t e = ensure_max_dynamic_smem(fn);
@@ -1022,7 +1026,8 @@ cudaError_t plan(const Params& p, Prepared* out) {
 
 template <int FMT, int D>
 cudaError_t plan(const Params& p, Prepared* out) {
-  return p.softcap > 0.0f || p.slopes != nullptr ? plan<FMT, D, true>(p, out) : plan<FMT, D, false>(p, out);
+  if (p.softcap > kPlainCap) return plan<FMT, D, kLargeCap>(p, out);
+  return p.softcap > 0.0f || p.slopes != nullptr ? plan<FMT, D, kShaped>(p, out) : plan<FMT, D, kPlainScores>(p, out);
 }
 
 template <int FMT>

@@ -117,11 +117,11 @@ struct Geo {
   }
 };
 
-// P: Params, or ScoredParams (chains whose scores have another form).
+// P: Params, or ScoredParams or LargeCapParams (chains whose scores have another form).
 template <int FMT, int D, class P>
 __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPerSm)
     tree_attention_kernel(const __grid_constant__ P p) {
-  constexpr bool kScored = std::is_same<P, ScoredParams>::value;
+  constexpr bool kScored = kIsScored<P>;
   using G = Geo<FMT, D>;
   constexpr int kWarps = G::kWarps, kThreads = G::kThreads;
   extern __shared__ uint8_t smem_raw[];
@@ -389,9 +389,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               float t = s[n][2 * x + i] * row_scale[x] * sk;
-              if (p.softcap > 0.0f) {  // c tanh(s / c) = c (1 - 2 / (1 + e^(2 s / c)))
-                const float cap2 = p.softcap * kLog2e;
-                t = fmaf(rcp(1.0f + ex2(t * __fdividef(2.0f, p.softcap))), -2.0f * cap2, cap2);
+              if (p.softcap > 0.0f) {
+                const float cap2 = p.softcap * kLog2e, at = t * __fdividef(2.0f, p.softcap);
+                t = std::is_same<P, LargeCapParams>::value ? large_capped(at, cap2) : capped(at, cap2);
               }
               if (p.slopes != nullptr) t = fmaf(slope2[x], fabsf(static_cast<float>(w.s.ctx + row_node[x] - j0 - tok - i)), t);
               s[n][2 * x + i] = t + lsv;
@@ -739,13 +739,13 @@ cudaError_t plan_tree_attention(const TreeAttentionArgs& a, Prepared* out) {
 }
 
 cudaError_t plan_chain_attention(const TreeAttentionArgs& a, const qlin_scores& scores, Prepared* out) {
-  ScoredParams p = {};
+  LargeCapParams p = {};
   fill(p, a, shape_of(a.cache, a.q.heads, a.max_nodes));
   p.softcap = scores.softcap;
   p.slopes = scores.slopes;
   p.window = scores.window >= kMaxLen ? 0 : static_cast<int32_t>(scores.window);  // no sequence is longer
   p.prefix = scores.prefix_lens;
-  return plan(p, a.cache, out);
+  return p.softcap > kPlainCap ? plan(p, a.cache, out) : plan(static_cast<const ScoredParams&>(p), a.cache, out);
 }
 
 }  // namespace qlin

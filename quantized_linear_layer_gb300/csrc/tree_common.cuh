@@ -66,6 +66,10 @@ struct ScoredParams : Params {
   int32_t window;         // 0: none
   const int32_t* prefix;  // or null
 };
+// And with a cap that large_capped() takes.
+struct LargeCapParams : ScoredParams {};
+template <class P>
+constexpr bool kIsScored = std::is_base_of<ScoredParams, P>::value;
 
 // The longest sequence, nodes included: far enough below 2^31 that the token numbers the kernels form past a sequence's
 // end (whole tiles, and the loading warps' 32 boxes of up to 64 tokens) stay in an int32.
@@ -81,7 +85,7 @@ struct Sequence {
   int32_t prefix, prefix_tiles, skipped;
   template <class P>
   __device__ __forceinline__ int32_t token_tile(int32_t i) const {
-    return std::is_same<P, ScoredParams>::value && i >= prefix_tiles ? i + skipped : i;
+    return kIsScored<P> && i >= prefix_tiles ? i + skipped : i;
   }
 };
 
@@ -104,7 +108,7 @@ __device__ __forceinline__ Sequence sequence(const P& p, int b) {
   s.row_tiles = (s.nodes * p.group + ROWS - 1) / ROWS;
   s.token_tiles = (s.len + TILE - 1) / TILE;
   if (s.nodes == 0) s.row_tiles = 0;
-  if constexpr (std::is_same<P, ScoredParams>::value) {
+  if constexpr (kIsScored<P>) {
     s.prefix = p.prefix != nullptr && s.nodes > 0 ? max(0, min(p.prefix[b], s.len)) : 0;
     s.prefix_tiles = (s.prefix + TILE - 1) / TILE;
     const int32_t low = p.window > 0 ? max(0, s.ctx - p.window + 1) : 0;  // of the first row
@@ -164,6 +168,24 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Caps up to this one are taken by capped(), larger ones by large_capped().
+constexpr float kPlainCap = 256.0f;
+
+// log2(e) c tanh(s / c), of x = 2 log2(e) s / c and cap2 = log2(e) c: c (1 - 2 / (1 + 2^x)).  Small scores are a difference of
+// numbers near c there, off by up to 2^-20 of it: 2^-12 at the largest cap that is taken like this.
+__device__ __forceinline__ float capped(float x, float cap2) { return fmaf(rcp(1.0f + ex2(x)), -2.0f * cap2, cap2); }
+
+// The same for any cap: below c / 4 by the power series of tanh (its next term is 2^-32 of the score), above it the
+// difference is off by 2^-18 of the score at most.
+__device__ __forceinline__ float large_capped(float x, float cap2) {
+  const float y = x * (0.5f * kLn2), z = y * y;
+  float t = fmaf(z, -1382.0f / 155925.0f, 62.0f / 2835.0f);
+  t = fmaf(z, t, -17.0f / 315.0f);
+  t = fmaf(z, t, 2.0f / 15.0f);
+  t = fmaf(z, t, -1.0f / 3.0f);
+  return z < 0.0625f ? cap2 * fmaf(y * z, t, y) : capped(x, cap2);
 }
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {

@@ -545,3 +545,17 @@ def test_rows_of_minus_infinity(qlin_gpu, d, seqs, most):
         hit[row] = True
         assert not p.out[hit].any() and bool((p.lse[hit] == -float("inf")).all())
         assert torch.equal(p.out[~hit], clean[~hit]) and torch.equal(p.lse[~hit], clean_lse[~hit])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cap", [256.0, 257.0, 1e3, 3e4, 1e6])
+def test_large_caps(qlin_gpu, fmt, d, cap):
+    """Caps far above the scores leave them as they are, to float32's own precision; scores around the cap, and beyond it.  Tiles of
+    rows, and few rows."""
+    for scale in (None, 0.2 * cap * d ** -0.5, 2 * cap * d ** -0.5):
+        if scale is not None and cap > 1e3:
+            continue      # (float32 products of that size say nothing)
+        for seqs in ([(0, 140), (200, 70), (515, 33)], [(300, 3), (0, 2)]):
+            Problem(qlin_gpu, seqs, 2, 1, d, 32, fmt, torch.float16, seed=d, softcap=cap, scale=scale,
+                    slopes=[0.5, 0.03] if d == 64 else None, wide=0.2, size=0.5).run().check()
