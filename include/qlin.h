@@ -931,8 +931,8 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * Scores, sums and out are held in float32; a cap adds up to 2^-20 of itself
  * to a score's error, caps above 256 no more than 2^-18 of the score.  A probability times its value's scale is rounded to 11
  * bits; it keeps them down to 2^-23 of the largest such product of its row (of the largest
- * value scale of the row's 128 tokens, seen or not, where that is more) and is
- * lost below 2^-33.  Scales of 0 and below it are as good as others.  A key or a value
+ * value scale among the row's 128 tokens, those included that only others of the
+ * sequence's rows see, where that is more) and is lost below 2^-33.  Scales of 0 and below it are as good as others.  A key or a value
  * that is not a number (its scale, its zero-point, an E4M3 code) makes the rows
  * that see its token not numbers, and no others; a row of q that holds a NaN is
  * not a number either.  A row whose scores are all -infinity gets out = 0 and lse =

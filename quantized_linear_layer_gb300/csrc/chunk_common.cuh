@@ -113,6 +113,9 @@ struct Walk {
   int32_t tile;     // of this segment, the block's first unit
   int32_t tiles;    // and how many
   Tiles seen;
+  // Of these tiles' tokens no row sees the `gap` ones from `hidden` on (in whole sixteens), and those from `high` on.
+  int32_t hidden, high;
+  uint32_t gap;
   Sequence s;
   int32_t next_tile, next_row_tile;  // where the run goes on
 
@@ -129,6 +132,11 @@ struct Walk {
       }
     }
     seen = tiles_of_row_tile<ROWS>(p, s, row_tile);
+    const int64_t row0 = static_cast<int64_t>(row_tile) * ROWS;
+    hidden = (s.prefix + 15) & ~15;
+    const int32_t low = p.window > 0 ? s.ctx + token_of(p, row0) - p.window + 1 : 0;
+    gap = max((low & ~15) - hidden, 0);
+    high = max(s.ctx + token_of(p, min(row0 + ROWS, s.rows) - 1) + 1, s.prefix);
     tiles = static_cast<int32_t>(min(static_cast<int64_t>(seen.count - tile), end - at));
     at += tiles;
     next_tile = 0;

@@ -559,3 +559,45 @@ def test_large_caps(qlin_gpu, fmt, d, cap):
         for seqs in ([(0, 140), (200, 70), (515, 33)], [(300, 3), (0, 2)]):
             Problem(qlin_gpu, seqs, 2, 1, d, 32, fmt, torch.float16, seed=d, softcap=cap, scale=scale,
                     slopes=[0.5, 0.03] if d == 64 else None, wide=0.2, size=0.5).run().check()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "u4"])
+@pytest.mark.parametrize("d,n", [(64, 200), (128, 200), (256, 200), (128, 4)])
+@pytest.mark.parametrize("page", [16, 64])
+def test_what_every_window_has_left(qlin_gpu, fmt, d, n, page):
+    """Tokens between a prefix and the first row's window, on pages that may hold anything by now: scales of any size change
+    nothing, and page numbers that are none are not looked at (in a tile of which rows see a part)."""
+    seqs = [(200, n), (300, n)]
+    p = Problem(qlin_gpu, seqs, 4, 2, d, page, fmt, torch.bfloat16, window=60, prefix=[9, 0]).run().check()
+    clean, clean_lse = p.out.clone(), p.lse.clone()
+    left = [(b, j // page) for b, (c, _) in enumerate(seqs) for j in range(0, c - 59 - page + 1, page) if j >= p.how["prefix"][b]]
+    assert len(left) >= 4
+    for scale in ([6e4, -6e4] if fmt == "u4" else [2.0 ** 40, 3e38, -3e38]):
+        t = [x.clone() for x in p.t]
+        for b, i in left:
+            x = t[3][int(p.table[b, i])]
+            (x[..., 0] if fmt == "u4" else x).fill_(scale)
+        p.cache = qlin_gpu.qlin_kv_cache(*t, p.cache.fmt)
+        p.run().check()
+        assert torch.equal(p.out, clean) and torch.equal(p.lse, clean_lse)
+    if n > 16:           # (the kernel of few rows looks at all pages of a tile)
+        for b, i in left:
+            p.table[b, i] = -5
+        p.prepare().run()
+        torch.cuda.synchronize()
+        assert torch.equal(p.out, clean) and qlin_gpu.qlin_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("up", [6, 12, 18])
+def test_large_scales_that_only_later_rows_see(qlin_gpu, fmt, d, up):
+    """A value scale 2^up above the others': rows before its token keep theirs down to 2^-34 of the largest value of the tile."""
+    p = Problem(qlin_gpu, [(130, 200)], 4, 2, d, 16, fmt, torch.bfloat16)
+    for token in (230, 231, 300):
+        page, off = int(p.table[0, token // 16]), token % 16
+        p.scales[1][page, :, off] *= 2.0 ** up
+    t = [x.clone() for x in p.t]
+    t[3] = torch.from_numpy(p.scales[1].copy()).cuda()
+    p.cache = qlin_gpu.qlin_kv_cache(*t, p.cache.fmt)
+    p.run().check()
