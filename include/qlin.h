@@ -934,7 +934,8 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * value scale among the row's 128 tokens, those included that only others of the
  * sequence's rows see, where that is more) and is lost below 2^-33.  Scales of 0 and below it are as good as others.  A key or a value
  * that is not a number (its scale, its zero-point, an E4M3 code) makes the rows
- * that see its token not numbers, and no others; a row of q that holds a NaN is
+ * that see its token not numbers, and no others; pages of which no row sees a token
+ * (a window has left them) are not looked at; a row of q that holds a NaN is
  * not a number either.  A row whose scores are all -infinity gets out = 0 and lse =
  * -infinity.
  *

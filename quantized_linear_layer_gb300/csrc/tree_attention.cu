@@ -170,7 +170,10 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, Geo<FMT, D>::kBlocksPer
           const int past = kScored && t < w.s.prefix_tiles ? min(w.tile + w.tiles, w.s.prefix_tiles) : w.tile + w.tiles;
           const int j = first * kTile + lane * box;
           ahead = kNoPage;
-          if (j < min(w.s.len, (first + past - t) * kTile)) ahead = checked_page(p, table[j >> p.page_shift]);
+          bool seen = j < min(w.s.len, (first + past - t) * kTile);
+          if constexpr (kScored)  // a box that every window has left has no page: its number may be none by now
+            seen = seen && (j < w.s.prefix || p.window == 0 || j + box > w.s.ctx - p.window + 1);
+          if (seen) ahead = checked_page(p, table[j >> p.page_shift]);
         }
         if (!tc::mbar_wait_quiet(bar_free + 8 * stage, phase, p.err, 0x50)) dead = true;
         if (__any_sync(0xffffffffu, dead)) {

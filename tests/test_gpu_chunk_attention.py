@@ -580,12 +580,11 @@ def test_what_every_window_has_left(qlin_gpu, fmt, d, n, page):
         p.cache = qlin_gpu.qlin_kv_cache(*t, p.cache.fmt)
         p.run().check()
         assert torch.equal(p.out, clean) and torch.equal(p.lse, clean_lse)
-    if n > 16:           # (the kernel of few rows looks at all pages of a tile)
-        for b, i in left:
-            p.table[b, i] = -5
-        p.prepare().run()
-        torch.cuda.synchronize()
-        assert torch.equal(p.out, clean) and qlin_gpu.qlin_get_device_error() == 0
+    for b, i in left:
+        p.table[b, i] = -5
+    p.prepare().run()
+    torch.cuda.synchronize()
+    assert torch.equal(p.out, clean) and qlin_gpu.qlin_get_device_error() == 0
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
