@@ -134,7 +134,7 @@ struct Walk {
     seen = tiles_of_row_tile<ROWS>(p, s, row_tile);
     const int64_t row0 = static_cast<int64_t>(row_tile) * ROWS;
     hidden = (s.prefix + 15) & ~15;
-    const int32_t low = p.window > 0 ? s.ctx + token_of(p, row0) - p.window + 1 : 0;
+    const int32_t low = p.window > 0 ? max(0, s.ctx + token_of(p, row0) - p.window + 1) : 0;
     gap = max((low & ~15) - hidden, 0);
     high = max(s.ctx + token_of(p, min(row0 + ROWS, s.rows) - 1) + 1, s.prefix);
     tiles = static_cast<int32_t>(min(static_cast<int64_t>(seen.count - tile), end - at));
