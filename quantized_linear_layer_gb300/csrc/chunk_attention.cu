@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::kThreads, 1) chunk_attention_kern
         const int j = j0 + g * 16;
         // What no row of the segment sees (a window has left it, and its page may be another's by now) is taken as zeros: its value
         // scale, whatever it is, would count in the bound of the tile's.
-        a[g].valid = static_cast<uint32_t>(j - w.hidden) < w.gap ? 0 : min(w.high - j, 16);
+        a[g].valid = max(0, static_cast<uint32_t>(j - w.hidden) < w.gap ? 0 : min(w.high - j, 16));
         a[g].at = (w.head << p.page_shift) + (j & ((1 << p.page_shift) - 1));
         a[g].page = a[g].valid > 0 ? p.table[w.b * p.max_pages + (j >> p.page_shift)] : 0;
       }
