@@ -41,7 +41,7 @@
 //
 // Bound: the instructions of the softmax and of the widening, and what they wait
 // for one another; neither DRAM nor the tensor cores.  8192 tokens behind 16384 (32 query heads on
-// 8 of 128, INT8): 2847 us, 965 TFLOP/s, half of what a large product reaches; a
+// 8 of 128, INT8): 2861 us, 961 TFLOP/s, half of what a large product reaches; a
 // tile of 256 rows x 128 tokens takes about 5000 cycles, of which the
 // products are 2750 (2048 with whole tiles), the exponentials 1024, and issue slots are
 // used in 0.53 of the cycles (0.36 tensor, 0.18 exponentials busy).  What has been

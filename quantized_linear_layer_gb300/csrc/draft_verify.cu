@@ -25,11 +25,12 @@
 // part holds the drawn place looks it up there (its part comes from L2), a piece
 // to a warp.
 //
-// Bound: DRAM while rows are summed (sequences of 128256 tokens with a rejection
-// move 6.9 TB/s then), a chain of dependent reads before and behind: lengths, nodes,
-// their probabilities, the walk, the sums' exchange, the look-up, 8 us together.
-// 64 chains of 128256 tokens take 25.7 us (66 MB at most: 9 us), one of 32000
-// 8.6 us, 32 trees of 50257 12.8 us.
+// Bound: memory while rows are summed (64 sequences of 128256 tokens with a rejection
+// each: 66 MB in some 11 us; repeated, 51 MB of it come from DRAM and the rest from L2),
+// a chain of dependent reads before and behind: lengths, nodes, their
+// probabilities, the walk, the sums' exchange, the look-up, 8 us together.
+// 64 chains of 128256 tokens take 25.6 us (66 MB at most: 9.9 us at the copy rate),
+// one of 32000 8.6 us, 32 trees of 50257 12.6 us.
 #include <algorithm>
 
 #include "kv_common.cuh"

@@ -12,8 +12,8 @@
 // back leaves the stack as it was.
 //
 // Bound: latency, a chain of dependent reads, scans and barriers of one block: a
-// decode step of 64 sequences takes 5.3 us, 600 sequences of 24 tokens each that
-// need some 900 pages (0.7 MB written: 0.1 us) 10.4.  Few rows are written by the
+// decode step of 64 sequences takes 4.8 us, 600 sequences of 24 tokens each that
+// need some 900 pages (0.7 MB written: 0.1 us) 9.8.  Few rows are written by the
 // block that works out the sums (one launch); more go to a second kernel over
 // the whole GPU.
 #include <algorithm>
