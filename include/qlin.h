@@ -819,7 +819,8 @@ qlin_status qlin_rmsnorm_quant_nvfp4(const void* x, qlin_dtype x_dtype, int64_t 
  * zeros, for the read and as keys and values of attention alike; so are rows of
  * the read that no sequence has; a sequence of attention whose bounds are out of
  * range is left out.  Rows of out and lse that belong to no sequence, or to one
- * left out, stay as they were, and with B = 0 nothing is written.
+ * left out, stay as they were, and with B = 0 nothing is written.  Where nothing
+ * else is said, what a call writes shares no memory with its other arrays.
  *
  * qlin_qk_norm_rope: for every token t and head of q and of k
  *   y = x / sqrt(mean(x^2) + eps) * gamma      (y = x when gamma is NULL)
